@@ -1,0 +1,349 @@
+"""Thin Python binding over include/glr.h: the operators of a gated recurrent block.
+
+* ``glr_scan`` / ``glr_scan_backward`` / ``glr_step``: the gated linear recurrence over a sequence
+  (the diagonal recurrence with a decay that the token chooses), its gradients, one token;
+* ``glr_join`` / ``glr_join_backward``: gate, norm, residual scale and add, and the next block's
+  norm, with their gradients;
+* ``glr_ckpt_pack`` / ``glr_ckpt_unpack``: activations kept in 8 bits, also written by
+  ``glr_join(ckpt=True)`` and read by ``glr_join_backward(ckpt=...)``.
+
+Like ``dlr.py`` this module passes pointers, sizes and the current torch CUDA stream, and turns
+non-zero status codes into exceptions; there is no CPU fallback. Activations are float32,
+bfloat16 or float16 with contiguous channels and otherwise any strides (so ``x``, ``r`` and ``i``
+may be columns of one projection's output); parameters and states are contiguous float32. Memory
+allocated here for a call on ``stream`` belongs to that stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import struct
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import dlr as _dlr
+
+TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+NORM = {"rms": 0, "layer": 1}
+ACT = {"silu": 0, "sigmoid": 1, "none": 2}
+STATE_STEPS = 64  # GLR_STATE_STEPS
+CKPT_GROUP = 32   # GLR_CKPT_GROUP
+
+_lib = None
+# the argument structs of glr.h, every field 8 bytes wide
+_SCAN = struct.Struct("4qd19q").pack
+_SCAN_BACK = struct.Struct("4qd30q").pack
+_STEP = struct.Struct("3qd16q").pack
+_JOIN = struct.Struct("5qd22q").pack
+_JOIN_BACK = struct.Struct("5qd36q").pack
+_NONE3 = (0, 0, 0)
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        lib = _dlr._load()
+        P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        for name in ("glr_scan", "glr_scan_backward", "glr_step", "glr_join", "glr_join_backward"):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = [ctypes.c_char_p, P], i32
+        for name, n in (("glr_scan_workspace_size", 3), ("glr_scan_backward_workspace_size", 3),
+                        ("glr_join_backward_workspace_size", 2)):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = [i64] * n, sz
+        lib.glr_states.argtypes, lib.glr_states.restype = [i64], i64
+        lib.glr_ckpt_pack.argtypes = [i64, i64, i64, P, i64, P, P, P]
+        lib.glr_ckpt_pack.restype = i32
+        lib.glr_ckpt_unpack.argtypes = [i64, i64, i64, P, P, P, i64, P]
+        lib.glr_ckpt_unpack.restype = i32
+        lib.glr_abi_version.restype = i32
+        _lib = lib
+    return _lib
+
+
+def _ok(fn: str, status: int):
+    if status:
+        raise _dlr.DLRError(fn, status)
+
+
+def _stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on(stream):
+    """Allocations for a call on ``stream`` come from that stream's memory."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _act_type(t) -> int:
+    if not t.is_cuda or t.dtype not in TYPE:
+        raise TypeError("expected float32, bfloat16 or float16 CUDA tensors")
+    return TYPE[t.dtype]
+
+
+def _view3(t, like, what: str):
+    """(pointer, stride_b, stride_t) of an activation [B, L, H] shaped as ``like``."""
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{what}: expected {like.dtype} on {like.device}")
+    if t.shape != like.shape:
+        raise ValueError(f"{what}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    sb, st, sh = t.stride()
+    if sh != 1 and t.shape[2] > 1:
+        raise ValueError(f"{what}: channels must be contiguous")
+    return t.data_ptr(), sb, st
+
+
+def _view2(t, like, what: str):
+    """The same for rows [M, H]: (pointer, 0, stride_t)."""
+    if t is None:
+        return _NONE3
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{what}: expected {like.dtype} on {like.device}")
+    if t.shape != like.shape:
+        raise ValueError(f"{what}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    st, sh = t.stride()
+    if sh != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what}: channels must be contiguous")
+    return t.data_ptr(), 0, st
+
+
+def _f32(t, shape, like, what: str) -> int:
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.device != like.device or not t.is_contiguous():
+        raise TypeError(f"{what}: expected a contiguous float32 tensor on {like.device}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _bytes(t, shape, like, what: str) -> int:
+    if t is None:
+        return 0
+    if t.dtype not in (torch.uint8, torch.bool) or t.device != like.device or \
+            not t.is_contiguous():
+        raise TypeError(f"{what}: expected a contiguous bool or uint8 tensor on {like.device}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _workspace(workspace, need: int, like):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace.dtype != torch.uint8 or workspace.device != like.device or \
+            not workspace.is_contiguous():
+        raise TypeError("workspace: expected a contiguous uint8 tensor on the same device")
+    return workspace
+
+
+def glr_scan_workspace_size(B: int, L: int, H: int) -> int:
+    """Bytes of device workspace glr_scan needs (0 for sizes out of range)."""
+    return int(_load().glr_scan_workspace_size(B, L, H))
+
+
+def glr_scan_backward_workspace_size(B: int, L: int, H: int) -> int:
+    """Bytes of device workspace glr_scan_backward needs (0 for sizes out of range)."""
+    return int(_load().glr_scan_backward_workspace_size(B, L, H))
+
+
+def glr_join_backward_workspace_size(M: int, H: int) -> int:
+    """Bytes of device workspace glr_join_backward needs (0 for sizes out of range)."""
+    return int(_load().glr_join_backward_workspace_size(M, H))
+
+
+def glr_scan(x, r, i, p, scale: float = 8.0, h0=None, reset=None, save_states: bool = False,
+             out=None, workspace=None, stream=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with
+    a_t = exp(-scale softplus(p) sigmoid(r_t)) over x, r, i [B, L, H]; p [H]; h0 [B, H] the state
+    before the first step (None: zero); reset [B, L] (bool or uint8, None: none) marks steps that
+    begin a new sequence. Returns (y [B, L, H], h_last [B, H]) and, with ``save_states``, the
+    float32 states [B, ceil(L / 64), H] that glr_scan_backward takes."""
+    lib, kind = _load(), _act_type(x)
+    if x.dim() != 3:
+        raise ValueError("x: expected [B, L, H]")
+    B, L, H = x.shape
+    with _on(stream):
+        y = torch.empty((B, L, H), dtype=x.dtype, device=x.device) if out is None else out
+        h_last = torch.empty((B, H), dtype=torch.float32, device=x.device)
+        states = torch.empty((B, (L + STATE_STEPS - 1) // STATE_STEPS, H), dtype=torch.float32,
+                             device=x.device) if save_states else None
+        ws = _workspace(workspace, lib.glr_scan_workspace_size(B, L, H), x)
+    args = _SCAN(kind, B, L, H, scale, *_view3(x, x, "x"), *_view3(r, x, "r"), *_view3(i, x, "i"),
+                 _f32(p, (H,), x, "p"), _f32(h0, (B, H), x, "h0"),
+                 _bytes(reset, (B, L), x, "reset"), *_view3(y, x, "out"), h_last.data_ptr(),
+                 0 if states is None else states.data_ptr(), ws.data_ptr(), ws.numel())
+    _ok("glr_scan", lib.glr_scan(args, _stream(stream, x.device)))
+    return (y, h_last, states) if save_states else (y, h_last)
+
+
+def glr_scan_backward(x, r, i, p, dy, states, scale: float = 8.0, h0=None, reset=None,
+                      dh_last=None, out=None, workspace=None, stream=None):
+    """Gradients of glr_scan for the gradients dy [B, L, H] of y and dh_last [B, H] (None: zero)
+    of h_last; the other arguments as the forward call had them, ``states`` as it returned them.
+    ``out``: (dx, dr, di) to write, e.g. the columns of one buffer. Returns (dx, dr, di, dp, dh0),
+    dh0 None when h0 is."""
+    lib, kind = _load(), _act_type(x)
+    if x.dim() != 3:
+        raise ValueError("x: expected [B, L, H]")
+    B, L, H = x.shape
+    n = (L + STATE_STEPS - 1) // STATE_STEPS
+    with _on(stream):
+        dx, dr, di = out if out is not None else (
+            torch.empty((B, L, H), dtype=x.dtype, device=x.device) for _ in range(3))
+        dp = torch.empty((H,), dtype=torch.float32, device=x.device)
+        dh0 = None if h0 is None else torch.empty_like(h0)
+        ws = _workspace(workspace, lib.glr_scan_backward_workspace_size(B, L, H), x)
+    args = _SCAN_BACK(kind, B, L, H, scale, *_view3(x, x, "x"), *_view3(r, x, "r"),
+                      *_view3(i, x, "i"), *_view3(dy, x, "dy"), _f32(p, (H,), x, "p"),
+                      _f32(h0, (B, H), x, "h0"), _bytes(reset, (B, L), x, "reset"),
+                      _f32(states, (B, n, H), x, "states"),
+                      _f32(dh_last, (B, H), x, "dh_last"), *_view3(dx, x, "dx"),
+                      *_view3(dr, x, "dr"), *_view3(di, x, "di"), dp.data_ptr(),
+                      0 if dh0 is None else dh0.data_ptr(), ws.data_ptr(), ws.numel())
+    _ok("glr_scan_backward", lib.glr_scan_backward(args, _stream(stream, x.device)))
+    return dx, dr, di, dp, dh0
+
+
+def glr_step(x, r, i, p, h, scale: float = 8.0, reset=None, h_out=None, out=None, stream=None):
+    """One token of the gated linear recurrence: x, r, i [B, H], the state h [B, H] (float32),
+    which becomes the next one in place unless ``h_out`` is given; reset [B] (bool or uint8)
+    marks sequences that begin with this token. Returns y [B, H]."""
+    lib, kind = _load(), _act_type(x)
+    if x.dim() != 2:
+        raise ValueError("x: expected [B, H]")
+    B, H = x.shape
+    if out is None:
+        with _on(stream):
+            out = torch.empty((B, H), dtype=x.dtype, device=x.device)
+    if h_out is None:
+        h_out = h
+    xp, _, xs = _view2(x, x, "x")
+    rp, _, rs = _view2(r, x, "r")
+    ip, _, is_ = _view2(i, x, "i")
+    yp, _, ys = _view2(out, x, "out")
+    args = _STEP(kind, B, H, scale, xp, xs, 0, rp, rs, 0, ip, is_, 0, _f32(p, (H,), x, "p"),
+                 _f32(h, (B, H), x, "h"), _bytes(reset, (B,), x, "reset"), yp, ys, 0,
+                 _f32(h_out, (B, H), x, "h_out"))
+    _ok("glr_step", lib.glr_step(args, _stream(stream, x.device)))
+    return out
+
+
+class Ckpt8(NamedTuple):
+    """An activation [M, H] in 8 bits: e4m3 codes [M, H] and, per group of 32 channels, the
+    exponent of its power-of-two scale plus 127 [M, ceil(H / 32)] (both uint8)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _new_ckpt(M, H, device) -> Ckpt8:
+    return Ckpt8(torch.empty((M, H), dtype=torch.uint8, device=device),
+                 torch.empty((M, (H + CKPT_GROUP - 1) // CKPT_GROUP), dtype=torch.uint8,
+                             device=device))
+
+
+def _ckpt_ptrs(c: Optional[Ckpt8], M, H, like, what: str):
+    if c is None:
+        return 0, 0
+    return (_bytes(c[0], (M, H), like, what + " codes"),
+            _bytes(c[1], (M, (H + CKPT_GROUP - 1) // CKPT_GROUP), like, what + " scales"))
+
+
+def glr_ckpt_pack(t, stream=None) -> Ckpt8:
+    """t [M, H] (contiguous channels) as an 8-bit checkpoint."""
+    lib, kind = _load(), _act_type(t)
+    if t.dim() != 2:
+        raise ValueError("t: expected [M, H]")
+    M, H = t.shape
+    p, _, st = _view2(t, t, "t")
+    with _on(stream):
+        c = _new_ckpt(M, H, t.device)
+    _ok("glr_ckpt_pack", lib.glr_ckpt_pack(kind, M, H, p, st, c.codes.data_ptr(),
+                                           c.scales.data_ptr(), _stream(stream, t.device)))
+    return c
+
+
+def glr_ckpt_unpack(c: Ckpt8, dtype=torch.float32, out=None, stream=None):
+    """The values [M, H] that an 8-bit checkpoint stands for, in ``dtype`` (or into ``out``)."""
+    lib = _load()
+    codes, scales = c
+    if not codes.is_cuda or codes.dim() != 2:
+        raise TypeError("codes: expected a CUDA tensor [M, H]")
+    M, H = codes.shape
+    if out is None:
+        with _on(stream):
+            out = torch.empty((M, H), dtype=dtype, device=codes.device)
+    kind = _act_type(out)
+    if out.shape != codes.shape:
+        raise ValueError("out: expected the shape of the codes")
+    cp, sp = _ckpt_ptrs(c, M, H, codes, "c")
+    p, _, st = _view2(out, out, "out")
+    _ok("glr_ckpt_unpack", lib.glr_ckpt_unpack(kind, M, H, cp, sp, p, st,
+                                               _stream(stream, codes.device)))
+    return out
+
+
+def glr_join(x, h, g, w, alpha, v, norm: str = "rms", act: str = "silu", eps: float = 1e-6,
+             ckpt: bool = False, out=None, stream=None):
+    """The end of a block and the norm that begins the next: y = x + alpha w norm(h act(g)),
+    n = v norm(y), for rows x, h, g [M, H]; w, v [H] and alpha [1] float32. ``norm``: "rms" or
+    "layer" (the mean taken off); ``act``: "silu", "sigmoid" or "none" (g None). v None: no next
+    norm (n is None). h None: only n = v norm(x) (w, alpha, g None; y is None). ``out``: (y, n) to
+    write; y may be x, and n may be h or g. Returns (y, n) and, with ``ckpt``, h and g as 8-bit
+    checkpoints (Ckpt8 or None each) for glr_join_backward."""
+    lib, kind = _load(), _act_type(x)
+    if x.dim() != 2:
+        raise ValueError("x: expected rows [M, H]")
+    M, H = x.shape
+    if act == "none" and g is not None:
+        raise ValueError('g: must be None with act="none"')
+    if h is None and (g is not None or w is not None or alpha is not None or ckpt):
+        raise ValueError("g, w, alpha and ckpt need h")
+    with _on(stream):
+        y, n = out if out is not None else (
+            None if h is None else torch.empty((M, H), dtype=x.dtype, device=x.device),
+            None if v is None else torch.empty((M, H), dtype=x.dtype, device=x.device))
+        hc = _new_ckpt(M, H, x.device) if ckpt else None
+        gc = _new_ckpt(M, H, x.device) if ckpt and g is not None else None
+    args = _JOIN(kind, M, H, NORM[norm], ACT[act], eps, *_view2(x, x, "x"), *_view2(h, x, "h"),
+                 *_view2(g, x, "g"), _f32(w, (H,), x, "w"), _f32(alpha, (1,), x, "alpha"),
+                 _f32(v, (H,), x, "v"), *_view2(y, x, "y"), *_view2(n, x, "n"),
+                 *_ckpt_ptrs(hc, M, H, x, "h"), *_ckpt_ptrs(gc, M, H, x, "g"))
+    _ok("glr_join", lib.glr_join(args, _stream(stream, x.device)))
+    return (y, n, (hc, gc)) if ckpt else (y, n)
+
+
+def glr_join_backward(dy, dn, x, h, g, w, alpha, v, norm: str = "rms", act: str = "silu",
+                      eps: float = 1e-6, ckpt=None, out=None, workspace=None, stream=None):
+    """Gradients of glr_join for the gradients dy (None: zero) of y and dn of n (given exactly
+    when v is), the rest as the forward call had it. With ``ckpt`` (what glr_join returned) h and
+    g come from their 8-bit checkpoints and are None here: the gradients are those at the values
+    kept. ``out``: (dx, dh, dg) to write (those that exist); dx may be dy. Returns
+    (dx, dh, dg, dw, dalpha, dv), None for what the call does not have."""
+    lib, kind = _load(), _act_type(x)
+    if x.dim() != 2:
+        raise ValueError("x: expected rows [M, H]")
+    M, H = x.shape
+    block, gated = w is not None, w is not None and act != "none"
+    hc, gc = ckpt if ckpt is not None else (None, None)
+    with _on(stream):
+        dx, dh, dg = out if out is not None else (
+            torch.empty((M, H), dtype=x.dtype, device=x.device) if on else None
+            for on in (True, block, gated))
+        dw, dalpha = (torch.empty((k,), dtype=torch.float32, device=x.device) if block else None
+                      for k in (H, 1))
+        dv = torch.empty((H,), dtype=torch.float32, device=x.device) if v is not None else None
+        ws = _workspace(workspace, lib.glr_join_backward_workspace_size(M, H), x)
+    args = _JOIN_BACK(kind, M, H, NORM[norm], ACT[act], eps, *_view2(dy, x, "dy"),
+                      *_view2(dn, x, "dn"), *_view2(x, x, "x"), *_view2(h, x, "h"),
+                      *_view2(g, x, "g"), *_ckpt_ptrs(hc, M, H, x, "h"),
+                      *_ckpt_ptrs(gc, M, H, x, "g"), _f32(w, (H,), x, "w"),
+                      _f32(alpha, (1,), x, "alpha"), _f32(v, (H,), x, "v"), *_view2(dx, x, "dx"),
+                      *_view2(dh, x, "dh"), *_view2(dg, x, "dg"),
+                      0 if dw is None else dw.data_ptr(), 0 if dalpha is None else dalpha.data_ptr(),
+                      0 if dv is None else dv.data_ptr(), ws.data_ptr(), ws.numel())
+    _ok("glr_join_backward", lib.glr_join_backward(args, _stream(stream, x.device)))
+    return dx, dh, dg, dw, dalpha, dv
