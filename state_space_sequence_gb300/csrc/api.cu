@@ -85,6 +85,13 @@ dlr_status status_from_cuda(cudaError_t e) {
   t_last_cuda_error_msg = cudaGetErrorString(e);
   return DLR_ERR_CUDA;
 }
+
+// Device address of the status word on the current device (kernels with bounded waits write it).
+int* device_status_word() {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_dlr_device_status) != cudaSuccess) return nullptr;
+  return static_cast<int*>(p);
+}
 }  // namespace dlr
 
 namespace {
@@ -92,12 +99,7 @@ namespace {
 constexpr int64_t kMaxL = (int64_t(1) << 24) - 1;
 constexpr int64_t kMaxGrid = 2147483647;
 
-// Device address of the status word on the current device (kernels with bounded waits write it).
-int* status_word() {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_dlr_device_status) != cudaSuccess) return nullptr;
-  return static_cast<int*>(p);
-}
+int* status_word() { return dlr::device_status_word(); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -27,6 +27,12 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
+// VEC neighbouring elements, read or written at once.
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) pack {
+  T v[VEC];
+};
+
 // An array [B, L, H] with contiguous channels (strides in elements).
 template <typename T>
 struct view {
@@ -82,23 +88,22 @@ __device__ __forceinline__ void decay(float z, float& w, float& a) {
   q = fmaf(q, f, 0.240226498f);
   q = fmaf(q, f, 0.693147188f);
   q *= f;
-  w = fmaf(s, q, s - 1.0f);
+  w = -fmaf(-s, q, 1.0f - s);  // -0 where a = 1
   a = fmaf(s, q, s);
 }
 
 // One step's gates. kz = -c softplus(p) log2(e).
 struct gate {
   float sr, si;  // sigmoid(r), sigmoid(i)
-  float a;       // the decay
+  float w, a;    // the decay less 1, and the decay
   float m, rm;   // sqrt(1 - a^2) and its reciprocal (a finite number where m is 0)
 };
 __device__ __forceinline__ gate make_gate(float r, float i, float kz) {
   gate g;
   g.sr = sigmoid(r);
   g.si = sigmoid(i);
-  float w;
-  decay(kz * g.sr, w, g.a);
-  const float v = -w * (2.0f + w);
+  decay(kz * g.sr, g.w, g.a);
+  const float v = -g.w * (2.0f + g.w);
   g.rm = rsqrt_approx(max_nan(v, 1e-36f));
   g.m = v * g.rm;
   return g;

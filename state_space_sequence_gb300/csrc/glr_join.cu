@@ -19,10 +19,6 @@ constexpr int kMaxThreads = 1024;
 constexpr int kParts = 1024;  // most partial sums of a channel in the gradients
 
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) pack {
-  T v[VEC];
-};
-template <typename T, int VEC>
 __device__ __forceinline__ void load(const T* p, float* out) {
   const pack<T, VEC> k = *reinterpret_cast<const pack<T, VEC>*>(p);
 #pragma unroll
