@@ -12,7 +12,7 @@ dlr_status status_from_cuda(cudaError_t e);
 namespace glr {
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H);
 size_t scan_backward_workspace_bytes(int64_t B, int64_t L, int64_t H);
-int64_t scan_blocks(int64_t B, int64_t L, int64_t H);
+int64_t scan_tiles(int64_t B, int64_t L, int64_t H);
 cudaError_t launch_scan(const glr_scan_args& a, cudaStream_t s);
 cudaError_t launch_scan_backward(const glr_scan_backward_args& a, cudaStream_t s);
 cudaError_t launch_step(const glr_step_args& a, cudaStream_t s);
@@ -110,7 +110,7 @@ dlr_status scan_sizes(int64_t type, int64_t B, int64_t L, int64_t H, double c) {
   if (!(c >= 0.0) || !std::isfinite((float)c)) return DLR_ERR_INVALID_ARG;
   if (B > kMaxGrid || L > kMaxGrid || H > kMaxH) return DLR_ERR_UNSUPPORTED;
   // B * L * H < 2^86 could overflow: bound the rows first
-  if (B * ((L + 63) / 64 + 1) > kMaxGrid || dlr::glr::scan_blocks(B, L, H) > kMaxGrid)
+  if (B * ((L + 63) / 64 + 1) > kMaxGrid || dlr::glr::scan_tiles(B, L, H) > kMaxGrid)
     return DLR_ERR_UNSUPPORTED;
   return DLR_OK;
 }

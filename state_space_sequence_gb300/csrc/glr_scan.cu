@@ -6,13 +6,16 @@
 // run backwards in time with G_t = dy_t + abar_{t+1} G_{t+1}: a stretch maps the gradient that
 // enters behind it to the one that leaves before it by G -> A G + C with the same A.
 //
-// Each direction is one launch that reads every input once. A block takes a tile of GLR_STATE_STEPS steps
-// of 32 VEC channels, each warp S of the steps with its gates in registers; the warps' maps meet in
-// shared memory, the tiles of a row in a chain through global memory: a tile publishes its map, looks
-// back over the maps of the tiles before it to the nearest one whose end value is there, and
-// publishes its own end value. End values are always formed in the same order (each from the one before
-// it), so the results do not depend on which of them a tile found. A tile that begins a sequence
-// knows its end from its own steps.
+// Each direction is one launch that reads every input once from memory. Blocks stay on the GPU and
+// take tiles (some steps of a group of channels) in turn; while a block works on one tile, the next
+// one's inputs come into shared memory by asynchronous copies. Each warp takes S of a tile's steps,
+// its gates in registers; the warps' maps meet in shared memory, the tiles of a row in a chain
+// through global memory: a tile publishes its map, looks back over the maps of the tiles before it
+// to the nearest one whose end value is there, and publishes its own end value. End values are
+// always formed in the same order (each from the one before it), so the results do not depend on
+// which of them a tile found. A tile that begins a sequence knows its end from its own steps.
+#include <algorithm>
+
 #include "glr_common.cuh"
 
 namespace dlr {
@@ -24,13 +27,11 @@ int* device_status_word();
 namespace glr {
 namespace {
 
-constexpr int kTile = GLR_STATE_STEPS;  // steps of a tile: it begins at a kept state
-constexpr int kHead = 64;               // words of the chain's workspace before its flags
+constexpr int kHead = 64;  // words of the chain's workspace before its flags
 
 // Flags of a tile: nothing yet, its map is there, its end value is there.
 constexpr uint32_t kHasMap = 1, kHasEnd = 2;
 constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;  // a longer wait is a fault
-constexpr int kLook = 32;  // tiles looked back over, one for each lane
 
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
   uint32_t v;
@@ -63,27 +64,22 @@ struct Job {
 };
 
 struct Tile {
-  int64_t b, chain;
-  int group, tile;
+  int b, group, tile;  // tile < 0: none left
 };
 
 // Tiles are handed out by a counter, the first tile of every chain before the second of any. A
-// block waits for tiles handed out before its own only, and their blocks are running or done,
-// whatever order the GPU starts blocks in.
-template <bool kChain, typename J>
-__device__ __forceinline__ Tile take_tile(const J& q, bool backwards, uint32_t* shared) {
-  int64_t k = blockIdx.x;
-  if (kChain) {
-    if (threadIdx.x == 0) *shared = atomicAdd(q.head, 1u);
-    __syncthreads();
-    k = *shared;
-  }
-  Tile at;
-  at.tile = (int)(k / q.chains);
+// block takes its tiles in the order it got them and waits for tiles handed out earlier only, so
+// the earliest unfinished one waits for nothing, whatever order the GPU runs blocks in.
+template <typename J>
+__device__ __forceinline__ Tile tile_of(const J& q, uint32_t k, bool backwards) {
+  const uint32_t chains = (uint32_t)q.chains;
+  Tile at{0, 0, -1};
+  if (k >= chains * (uint32_t)q.tiles) return at;
+  at.tile = (int)(k / chains);
+  const uint32_t chain = k % chains;
   if (backwards) at.tile = q.tiles - 1 - at.tile;
-  at.chain = k % q.chains;
-  at.group = (int)(at.chain % q.groups);
-  at.b = at.chain / q.groups;
+  at.group = (int)(chain % (uint32_t)q.groups);
+  at.b = (int)(chain / (uint32_t)q.groups);
   return at;
 }
 
@@ -94,19 +90,23 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t what) {
   if ((threadIdx.x & 31) == 0) store_release(flag, what);
 }
 
-// Called by one warp. Waits until one of the `back` <= 32 tiles before this one (lane l looks l + 1
-// tiles back, `step` flags from one to the next) has its end value and all those between have
-// their maps. Returns how far back it is, or 0 when the wait ran out.
+// Called by one warp. Waits until one of the `back` tiles before this one has its end value and all
+// those between have their maps; each lane looks at one tile at a time (`step` flags from one to
+// the next). Returns how far back it is, or 0 when the wait ran out. The first tile of a chain always
+// comes to its end value by itself.
 __device__ __forceinline__ int look_back(const uint32_t* flag, int back, int step) {
   const int lane = threadIdx.x & 31;
   uint64_t t0 = 0;
-  for (;;) {
-    const uint32_t f = lane < back ? load_acquire(flag - (int64_t)step * (lane + 1)) : 0u;
+  for (int first = 0;;) {
+    const int k = first + lane + 1;
+    const uint32_t f = k <= back ? load_acquire(flag - (int64_t)step * k) : 0u;
     const uint32_t ends = __ballot_sync(0xffffffffu, f == kHasEnd);
     const uint32_t none = __ballot_sync(0xffffffffu, f == 0u);
-    if (ends) {
-      const int l = __ffs(ends) - 1;
-      if (!(none & ((1u << l) - 1u))) return l + 1;
+    const int l = ends ? __ffs(ends) - 1 : 32;
+    if (!(none & (l == 32 ? 0xffffffffu : (1u << l) - 1u))) {
+      if (l < 32) return first + l + 1;
+      first += 32;  // 32 maps and no end among them
+      continue;
     }
     const uint64_t t = timer_ns();
     if (t0 == 0) t0 = t;
@@ -117,47 +117,47 @@ __device__ __forceinline__ int look_back(const uint32_t* flag, int back, int ste
 // Called by one warp: the value s that enters the tile, and `end`, the one that leaves it, from
 // the tile's map (A, e); `cut`: the map does not depend on what enters. row: the lane's first
 // element of in and maps, dir = 1 forwards, -1 backwards. The first tile of the chain has its s.
-template <bool kChain, int VEC, typename J>
-__device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, int dir, bool on,
-                                      const float (&A)[VEC], const float (&e)[VEC], bool cut,
-                                      float (&s)[VEC], float (&end)[VEC]) {
+template <int VEC, typename J>
+__device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, int dir,
+                                      const bool (&on)[VEC], const float (&A)[VEC],
+                                      const float (&e)[VEC], bool cut, float (&s)[VEC],
+                                      float (&end)[VEC]) {
   const int done = dir > 0 ? at.tile : q.tiles - 1 - at.tile;  // tiles of the chain before this
   const bool last = done == q.tiles - 1;
   const int64_t dH = dir * q.H;
-  uint32_t* flag = q.head + kHead + at.chain * q.tiles + at.tile;
-  if (kChain && done > 0) {
+  uint32_t* flag = q.head + kHead + ((int64_t)at.b * q.groups + at.group) * q.tiles + at.tile;
+  if (done > 0) {
     if (!last) {
-      if (on)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          if (cut)
-            q.in[row + dH + v] = e[v];
-          else
-            q.maps[row + v] = make_float2(A[v], e[v]);
-        }
+      for (int v = 0; v < VEC; ++v) {
+        if (!on[v]) continue;
+        if (cut)
+          q.in[row + dH + v] = e[v];
+        else
+          q.maps[row + v] = make_float2(A[v], e[v]);
+      }
       publish(flag, cut ? kHasEnd : kHasMap);
     }
-    const int far = look_back(flag, min(done, kLook), dir);
+    const int far = look_back(flag, done, dir);
     if (far == 0 && (threadIdx.x & 31) == 0) report_status(q.status, DLR_ERR_TIMEOUT);
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
-      s[v] = on && far ? __ldcg(&q.in[row - (far - 1) * dH + v]) : 0.0f;
+      s[v] = on[v] && far ? __ldcg(&q.in[row - (far - 1) * dH + v]) : 0.0f;
+#pragma unroll 4
     for (int k = far - 1; k >= 1; --k)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float2 m = on ? __ldcg(&q.maps[row - k * dH + v]) : make_float2(0.0f, 0.0f);
+        const float2 m = on[v] ? __ldcg(&q.maps[row - k * dH + v]) : make_float2(0.0f, 0.0f);
         s[v] = fmaf(m.x, s[v], m.y);
       }
   }
 #pragma unroll
   for (int v = 0; v < VEC; ++v) end[v] = cut ? e[v] : fmaf(A[v], s[v], e[v]);
-  if (last) return;
-  if (!(kChain && done > 0 && cut)) {
-    if (on)
+  if (last || (done > 0 && cut)) return;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) q.in[row + dH + v] = end[v];
-    if (kChain) publish(flag, kHasEnd);
-  }
+  for (int v = 0; v < VEC; ++v)
+    if (on[v]) q.in[row + dH + v] = end[v];
+  publish(flag, kHasEnd);
 }
 
 // bits of the n steps from t on that begin a sequence
@@ -177,260 +177,418 @@ __device__ __forceinline__ float kept_rest(float k) {  // 1 - a^2
   return fmaf(-k, fmaf(2.0f, s, k), 1.0f - s);
 }
 
-// S steps of VEC channels of an activation; steps from n on are left as they are
-template <typename T, int VEC, int S>
-__device__ __forceinline__ void load_steps(pack<T, VEC> (&out)[S], const T* p, int64_t st, int n) {
-#pragma unroll
-  for (int j = 0; j < S; ++j)
-    if (j < n) out[j] = *reinterpret_cast<const pack<T, VEC>*>(p + j * st);
+// How a tile's inputs come into shared memory: by asynchronous copies of 16 bytes where every row
+// begins on a 16-byte boundary and H is a whole number of them, of 4 bytes where the same holds for 4,
+// else (16-bit types with odd strides) by loads of single elements.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  const int n = on ? kBytes : 0;  // nothing is read and zeros are written where off
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int VEC, int W, bool kChain>
-__global__ void __launch_bounds__(W * 32, 16 / W)
-scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict__ h_last) {
-  constexpr int S = kTile / W;
-  __shared__ float2 map_s[W][32 * VEC];
-  __shared__ float in_s[32 * VEC];
-  __shared__ uint32_t cut_s[W], ticket_s;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Tile at = take_tile<kChain>(q, false, &ticket_s);
-  const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
-  const bool on = h < q.H && DLR_IN(at.b, q.B);
-  const int64_t t0 = (int64_t)at.tile * kTile + warp * S;
-  const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
-
-  pack<T, VEC> xr[S] = {}, rr[S] = {}, ir[S] = {};
-  if (on) {
-    load_steps(rr, q.r.row(at.b, t0) + h, q.r.st, n);
-    load_steps(ir, q.i.row(at.b, t0) + h, q.i.st, n);
-    load_steps(xr, q.x.row(at.b, t0) + h, q.x.st, n);
+// `steps` rows of C channels of v into dst [steps][C]; rows past the end and channels past H are zero
+template <typename T, int C, int kBytes, int kThreads>
+__device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b, int64_t t0,
+                                      int64_t h0, int steps, int64_t L, int64_t H) {
+  constexpr int per = kBytes / (int)sizeof(T), cols = C / per;
+  const int col = threadIdx.x % cols * per;
+  const bool in = h0 + col < H;
+  const T* src = v.row(b, t0) + h0 + col;
+  if constexpr (kBytes == 2) {
+#pragma unroll 4
+    for (int j = threadIdx.x / cols; j < steps; j += kThreads / cols)
+      dst[j * C + col] = in && t0 + j < L ? src[j * v.st] : from_f<T>(0.0f);
+  } else {
+    const int64_t dp = (kThreads / cols) * v.st;
+    const T* p = src + (threadIdx.x / cols) * v.st;
+#pragma unroll 4
+    for (int j = threadIdx.x / cols; j < steps; j += kThreads / cols, p += dp) {
+      const bool on = in && t0 + j < L;
+      copy_async<kBytes>(dst + j * C + col, on ? p : v.p, on);
+    }
   }
-  float kz[VEC];
+}
+
+// VEC neighbouring values to memory: at once, or one by one where they are not aligned
+template <typename T, int VEC, bool kOne>
+__device__ __forceinline__ void put(T* p, const float (&f)[VEC], bool (&on)[VEC]) {
+  if constexpr (kOne) {
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) kz[v] = on ? -q.c * softplus(q.p[h + v]) * kLog2e : 0.0f;
-  const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
-  float a[S][VEC], b[S][VEC], A[VEC], e[VEC];
+    for (int v = 0; v < VEC; ++v)
+      if (on[v]) p[v] = from_f<T>(f[v]);
+  } else {
+    pack<T, VEC> o;
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f;
-#pragma unroll
-  for (int j = 0; j < S; ++j)
+    for (int v = 0; v < VEC; ++v) o.v[v] = from_f<T>(f[v]);
+    if (on[0]) *reinterpret_cast<pack<T, VEC>*>(p) = o;
+  }
+}
+
+// channels of a lane: a warp's row of a tile is 128 bytes
+template <typename T>
+constexpr int kVec = 4 / (int)sizeof(T);
+
+constexpr int kScanSteps = 16;                       // of a warp
+constexpr int kScanWarps = 8;
+constexpr int kScanTile = kScanSteps * kScanWarps;   // steps
+constexpr int kScanBlocks = 2;                       // blocks that an SM holds
+
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kScanWarps * 32, kScanBlocks)
+scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
+            float* __restrict__ states) {
+  constexpr int VEC = kVec<T>, W = kScanWarps, S = kScanSteps, C = 32 * VEC, threads = W * 32;
+  constexpr bool kOne = kBytes == 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  T* const buf = reinterpret_cast<T*>(smem);  // [2][r i x][kScanTile][C]
+  __shared__ float2 map_s[W][C];
+  __shared__ float in_s[C];
+  __shared__ uint32_t cut_s[W];
+  __shared__ Tile tile_s[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) tile_s[0] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) : blockIdx.x, false);
+  __syncthreads();
+  auto fetch = [&](const Tile& at, int k) {
+    if (at.tile >= 0) {
+      T* d = buf + k * 3 * kScanTile * C;
+      const int64_t t0 = (int64_t)at.tile * kScanTile, c0 = (int64_t)at.group * C;
+      const int steps = (int)min((int64_t)kScanTile, q.L - t0);
+      stage<T, C, kBytes, threads>(d, q.r, at.b, t0, c0, steps, q.L, q.H);
+      stage<T, C, kBytes, threads>(d + kScanTile * C, q.i, at.b, t0, c0, steps, q.L, q.H);
+      stage<T, C, kBytes, threads>(d + 2 * kScanTile * C, q.x, at.b, t0, c0, steps, q.L, q.H);
+    }
+    copies_end();
+  };
+  fetch(tile_s[0], 0);
+  for (int turn = 0;; turn ^= 1) {
+    const Tile at = tile_s[turn];
+    if (at.tile < 0) return;
+    uint32_t ticket = 0;
+    if (threadIdx.x == 0) {
+      ticket = q.tiles > 1 ? atomicAdd(q.head, 1u) : 0xffffffffu;
+      tile_s[turn ^ 1] = tile_of(q, ticket, false);
+    }
+    copies_wait();
+    __syncthreads();
+    fetch(tile_s[turn ^ 1], turn ^ 1);
+
+    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+    const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
+    const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
+    const T* mine = buf + turn * 3 * kScanTile * C + warp * S * C + lane * VEC;
+    bool on[VEC];
+    float kz[VEC], a[S][VEC], b[S][VEC], A[VEC], e[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const gate g = make_gate(to_f(rr[j].v[v]), to_f(ir[j].v[v]), kz[v]);
-      a[j][v] = g.a;
-      b[j][v] = g.m * g.si * to_f(xr[j].v[v]);
-      if (n < S && j >= n) a[j][v] = 1.0f, b[j][v] = 0.0f;
-      e[v] = (cut >> j) & 1u ? b[j][v] : fmaf(a[j][v], e[v], b[j][v]);
-      A[v] *= a[j][v];
+      on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+      kz[v] = on[v] ? -q.c * softplus(q.p[h + v]) * kLog2e : 0.0f;
+      A[v] = 1.0f, e[v] = 0.0f;
+    }
+    const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      const pack<T, VEC> r = *reinterpret_cast<const pack<T, VEC>*>(mine + j * C);
+      const pack<T, VEC> i = *reinterpret_cast<const pack<T, VEC>*>(mine + (kScanTile + j) * C);
+      const pack<T, VEC> x = *reinterpret_cast<const pack<T, VEC>*>(mine + (2 * kScanTile + j) * C);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const gate g = make_gate(to_f(r.v[v]), to_f(i.v[v]), kz[v]);
+        a[j][v] = g.a;
+        b[j][v] = g.m * g.si * to_f(x.v[v]);
+      }
+    }
+    const bool plain = n == S && cut == 0;  // the same for all of the warp
+    if (plain) {
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          e[v] = fmaf(a[j][v], e[v], b[j][v]);
+          A[v] *= a[j][v];
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          if (j >= n) a[j][v] = 1.0f, b[j][v] = 0.0f;
+          e[v] = (cut >> j) & 1u ? b[j][v] : fmaf(a[j][v], e[v], b[j][v]);
+          A[v] *= a[j][v];
+        }
     }
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
-  if (lane == 0) cut_s[warp] = cut;
-  __syncthreads();
+    for (int v = 0; v < VEC; ++v) map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
+    if (lane == 0) cut_s[warp] = cut;
+    __syncthreads();
 
-  if (warp == 0) {
-    float s[VEC], end[VEC];
-    bool any = false;
-    const int64_t row = (at.b * q.tiles + at.tile) * q.H + h;
+    if (warp == 0) {
+      float s[VEC], end[VEC];
+      bool any = false;
+      const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.H + h;
 #pragma unroll
-    for (int w = 1; w < W; ++w)
+      for (int w = 1; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const float2 m = map_s[w][lane * VEC + v];
+          e[v] = cut_s[w] ? m.y : fmaf(m.x, e[v], m.y);
+          A[v] *= m.x;
+        }
+#pragma unroll
+      for (int w = 0; w < W; ++w) any |= cut_s[w] != 0;
+      if (at.tile == 0)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
+      chain(q, at, row, 1, on, A, e, any, s, end);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        if (at.tile == q.tiles - 1 && h_last && on[v]) h_last[at.b * q.H + h + v] = end[v];
+        in_s[lane * VEC + v] = s[v];
+      }
+    }
+    __syncthreads();
+
+    float s[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) s[v] = in_s[lane * VEC + v];
+    for (int w = 0; w < warp; ++w)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const float2 m = map_s[w][lane * VEC + v];
-        e[v] = cut_s[w] ? m.y : fmaf(m.x, e[v], m.y);
-        A[v] *= m.x;
+        s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
       }
+    if (states && t0 % GLR_STATE_STEPS == 0 && n > 0)
 #pragma unroll
-    for (int w = 0; w < W; ++w) any |= cut_s[w] != 0;
-    if (at.tile == 0)
+      for (int v = 0; v < VEC; ++v)
+        if (on[v])
+          states[(at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t0 / GLR_STATE_STEPS) * q.H + h + v] =
+              s[v];
+    T* yp = y.row(at.b, t0) + h;
+    if (plain) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        s[v] = h0 && on ? h0[at.b * q.H + h + v] : 0.0f;
-        if (on) q.in[row + v] = s[v];
+      for (int j = 0; j < S; ++j) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = fmaf(a[j][v], s[v], b[j][v]);
+        put<T, VEC, kOne>(yp, s, on);
+        yp += y.st;
       }
-    chain<kChain>(q, at, row, 1, on, A, e, any, s, end);
-    if (at.tile == q.tiles - 1 && h_last && on)
+    } else {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) h_last[at.b * q.H + h + v] = end[v];
+      for (int j = 0; j < S; ++j) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) in_s[lane * VEC + v] = s[v];
-  }
-  __syncthreads();
-
-  float s[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) s[v] = in_s[lane * VEC + v];
-  for (int w = 0; w < warp; ++w)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float2 m = map_s[w][lane * VEC + v];
-      s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
+        for (int v = 0; v < VEC; ++v)
+          s[v] = (cut >> j) & 1u ? b[j][v] : fmaf(a[j][v], s[v], b[j][v]);
+        if (j < n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp, s, on);
+        yp += y.st;
+      }
     }
-  T* yp = y.row(at.b, t0) + h;
-#pragma unroll
-  for (int j = 0; j < S; ++j) {
-    pack<T, VEC> o;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      s[v] = (cut >> j) & 1u ? b[j][v] : fmaf(a[j][v], s[v], b[j][v]);
-      o.v[v] = from_f<T>(s[v]);
-    }
-    if (on && j < n && DLR_IN(t0 + j, q.L)) *reinterpret_cast<pack<T, VEC>*>(yp + j * y.st) = o;
   }
 }
 
-template <typename T, int VEC, int W, bool kChain>
-__global__ void __launch_bounds__(W * 32, 16 / W)
+constexpr int kBackSteps = 16;
+constexpr int kBackWarps = 4;
+constexpr int kBackTile = kBackSteps * kBackWarps;
+constexpr int kBackBlocks = 3;
+static_assert(kBackTile == GLR_STATE_STEPS, "a tile begins at a kept state");
+
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kBackWarps * 32, kBackBlocks)
 back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
             const float* __restrict__ dh_last, view<T> dx, view<T> dr, view<T> di,
             float* __restrict__ dh0, float* __restrict__ part) {
-  constexpr int S = kTile / W;
-  __shared__ float2 map_s[W][32 * VEC];  // (A, e) of each warp's steps
-  __shared__ float back_s[W][32 * VEC];  // and C; at the end the warps' sums for dp
-  __shared__ float in_s[32 * VEC];
-  __shared__ uint32_t cut_s[W], ticket_s;
+  constexpr int VEC = kVec<T>, W = kBackWarps, S = kBackSteps, C = 32 * VEC, threads = W * 32;
+  constexpr int kArray = kBackTile * C;
+  constexpr bool kOne = kBytes == 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  T* const buf = reinterpret_cast<T*>(smem);  // [2][r i x dy][kBackTile][C]
+  __shared__ float2 map_s[W][C];  // (A, e) of each warp's steps
+  __shared__ float back_s[W][C];  // and C; at the end of a tile the warps' sums for dp
+  __shared__ float in_s[C];
+  __shared__ uint32_t cut_s[W];
+  __shared__ Tile tile_s[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Tile at = take_tile<kChain>(q, true, &ticket_s);
-  const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
-  const bool on = h < q.H && DLR_IN(at.b, q.B);
-  const int64_t t0 = (int64_t)at.tile * kTile + warp * S;
-  const int64_t row = (at.b * q.tiles + at.tile) * q.H + h;
-  const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
 
-  pack<T, VEC> xr[S] = {}, rr[S] = {}, ir[S] = {}, gr[S] = {};
-  if (on) {
-    load_steps(rr, q.r.row(at.b, t0) + h, q.r.st, n);
-    load_steps(ir, q.i.row(at.b, t0) + h, q.i.st, n);
-    load_steps(xr, q.x.row(at.b, t0) + h, q.x.st, n);
-    load_steps(gr, dy.row(at.b, t0) + h, dy.st, n);
-  }
-  float k[VEC], s[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    k[v] = on ? q.c * softplus(q.p[h + v]) : 0.0f;
-    s[v] = on ? states[row + v] : 0.0f;
-  }
-  const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
-  // the decay (see kept_decay), and b, in whose place the state before the step comes later
-  float ka[S][VEC], hb[S][VEC], A[VEC], e[VEC], C[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f, C[v] = 0.0f;
-#pragma unroll
-  for (int j = 0; j < S; ++j)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const gate g = make_gate(to_f(rr[j].v[v]), to_f(ir[j].v[v]), -k[v] * kLog2e);
-      ka[j][v] = keep_decay(g);
-      hb[j][v] = g.m * g.si * to_f(xr[j].v[v]);
-      if (n < S && j >= n) ka[j][v] = -0.0f, hb[j][v] = 0.0f;
-      const float a = kept_decay(ka[j][v]);
-      e[v] = (cut >> j) & 1u ? hb[j][v] : fmaf(a, e[v], hb[j][v]);
-      A[v] *= a;
-    }
-#pragma unroll
-  for (int j = S - 1; j >= 0; --j)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float G = to_f(gr[j].v[v]) + C[v];
-      C[v] = (cut >> j) & 1u ? 0.0f : kept_decay(ka[j][v]) * G;
-    }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
-    back_s[warp][lane * VEC + v] = C[v];
-  }
-  if (lane == 0) cut_s[warp] = cut;
+  if (threadIdx.x == 0) tile_s[0] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) : blockIdx.x, true);
   __syncthreads();
+  auto fetch = [&](const Tile& at, int k) {
+    if (at.tile >= 0) {
+      T* d = buf + k * 4 * kArray;
+      const int64_t t0 = (int64_t)at.tile * kBackTile, c0 = (int64_t)at.group * C;
+      const int steps = (int)min((int64_t)kBackTile, q.L - t0);
+      stage<T, C, kBytes, threads>(d, q.r, at.b, t0, c0, steps, q.L, q.H);
+      stage<T, C, kBytes, threads>(d + kArray, q.i, at.b, t0, c0, steps, q.L, q.H);
+      stage<T, C, kBytes, threads>(d + 2 * kArray, q.x, at.b, t0, c0, steps, q.L, q.H);
+      stage<T, C, kBytes, threads>(d + 3 * kArray, dy, at.b, t0, c0, steps, q.L, q.H);
+    }
+    copies_end();
+  };
+  fetch(tile_s[0], 0);
+  for (int turn = 0;; turn ^= 1) {
+    const Tile at = tile_s[turn];
+    if (at.tile < 0) return;
+    if (threadIdx.x == 0)
+      tile_s[turn ^ 1] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) : 0xffffffffu, true);
+    copies_wait();
+    __syncthreads();
+    fetch(tile_s[turn ^ 1], turn ^ 1);
 
-  if (warp == 0) {
-    float tA[VEC], tC[VEC], in[VEC], end[VEC];
-    bool any = false;
+    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+    const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
+    const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.H + h;
+    const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
+    const T* mine = buf + turn * 4 * kArray + warp * S * C + lane * VEC;
+    auto raw = [&](int array, int j) {
+      return *reinterpret_cast<const pack<T, VEC>*>(mine + array * kArray + j * C);
+    };
+    bool on[VEC];
+    float k[VEC], s[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) tA[v] = 1.0f, tC[v] = 0.0f;
+    for (int v = 0; v < VEC; ++v) {
+      on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+      k[v] = on[v] ? q.c * softplus(q.p[h + v]) : 0.0f;
+      s[v] = on[v] ? states[row + v] : 0.0f;
+    }
+    const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
+    // the decay (see kept_decay), and b, in whose place the state before the step comes later
+    float ka[S][VEC], hb[S][VEC], A[VEC], e[VEC], G[VEC];
 #pragma unroll
-    for (int w = W - 1; w >= 0; --w) {
+    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f, G[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      const pack<T, VEC> r = raw(0, j), i = raw(1, j), x = raw(2, j);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const gate g = make_gate(to_f(r.v[v]), to_f(i.v[v]), -k[v] * kLog2e);
+        ka[j][v] = keep_decay(g);
+        hb[j][v] = g.m * g.si * to_f(x.v[v]);
+        if (n < S && j >= n) ka[j][v] = -0.0f, hb[j][v] = 0.0f;
+        const float a = kept_decay(ka[j][v]);
+        e[v] = (cut >> j) & 1u ? hb[j][v] : fmaf(a, e[v], hb[j][v]);
+        A[v] *= a;
+      }
+    }
+#pragma unroll
+    for (int j = S - 1; j >= 0; --j) {
+      const pack<T, VEC> g = raw(3, j);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float t = (n < S && j >= n ? 0.0f : to_f(g.v[v])) + G[v];
+        G[v] = (cut >> j) & 1u ? 0.0f : kept_decay(ka[j][v]) * t;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
+      back_s[warp][lane * VEC + v] = G[v];
+    }
+    if (lane == 0) cut_s[warp] = cut;
+    __syncthreads();
+
+    if (warp == 0) {
+      float tA[VEC], tC[VEC], in[VEC], end[VEC];
+      bool any = false;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) tA[v] = 1.0f, tC[v] = 0.0f;
+#pragma unroll
+      for (int w = W - 1; w >= 0; --w) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const float m = map_s[w][lane * VEC + v].x, c = back_s[w][lane * VEC + v];
+          tC[v] = cut_s[w] ? c : fmaf(m, tC[v], c);
+          tA[v] *= m;
+        }
+        any |= cut_s[w] != 0;
+      }
+      if (at.tile == q.tiles - 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          in[v] = dh_last && on[v] ? dh_last[at.b * q.H + h + v] : 0.0f;
+      chain(q, at, row, -1, on, tA, tC, any, in, end);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        if (at.tile == 0 && dh0 && on[v]) dh0[at.b * q.H + h + v] = end[v];
+        in_s[lane * VEC + v] = in[v];
+      }
+    }
+    // the states before the steps, while the first warp looks along the chain
+    for (int w = 0; w < warp; ++w)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float2 m = map_s[w][lane * VEC + v];
+        s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
+      }
+#pragma unroll
+    for (int j = 0; j < S; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float b = hb[j][v];
+        if ((cut >> j) & 1u) s[v] = 0.0f;
+        hb[j][v] = s[v];
+        s[v] = fmaf(kept_decay(ka[j][v]), s[v], b);
+      }
+    __syncthreads();
+
+    float sum[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) G[v] = in_s[lane * VEC + v], sum[v] = 0.0f;
+    for (int w = W - 1; w > warp; --w)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const float m = map_s[w][lane * VEC + v].x, c = back_s[w][lane * VEC + v];
-        tC[v] = cut_s[w] ? c : fmaf(m, tC[v], c);
-        tA[v] *= m;
+        G[v] = cut_s[w] ? c : fmaf(m, G[v], c);
       }
-      any |= cut_s[w] != 0;
+    T* xp = dx.row(at.b, t0) + h;
+    T* rp = dr.row(at.b, t0) + h;
+    T* ip = di.row(at.b, t0) + h;
+#pragma unroll
+    for (int j = S - 1; j >= 0; --j) {
+      if (j >= n) continue;
+      const pack<T, VEC> r = raw(0, j), i = raw(1, j), x = raw(2, j), g = raw(3, j);
+      float ox[VEC], orr[VEC], oi[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float sr = sigmoid(to_f(r.v[v])), si = sigmoid(to_f(i.v[v]));
+        const float a = kept_decay(ka[j][v]), u = kept_rest(ka[j][v]);
+        const float rm = rsqrt_approx(max_nan(u, 1e-36f));
+        const float t = to_f(g.v[v]) + G[v], sx = si * to_f(x.v[v]);
+        const float E = t * a * (hb[j][v] - a * rm * sx) * sr, tm = t * (u * rm);
+        sum[v] += E;
+        ox[v] = tm * si;
+        oi[v] = tm * sx * (1.0f - si);
+        orr[v] = -k[v] * E * (1.0f - sr);
+        G[v] = (cut >> j) & 1u ? 0.0f : a * t;
+      }
+      if (DLR_IN(t0 + j, q.L)) {
+        put<T, VEC, kOne>(xp + j * dx.st, ox, on);
+        put<T, VEC, kOne>(rp + j * dr.st, orr, on);
+        put<T, VEC, kOne>(ip + j * di.st, oi, on);
+      }
     }
-    if (at.tile == q.tiles - 1)
+    __syncthreads();  // back_s has been read
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) in[v] = dh_last && on ? dh_last[at.b * q.H + h + v] : 0.0f;
-    chain<kChain>(q, at, row, -1, on, tA, tC, any, in, end);
-    if (at.tile == 0 && dh0 && on)
+    for (int v = 0; v < VEC; ++v) back_s[warp][lane * VEC + v] = sum[v];
+    __syncthreads();
+    if (warp == 0)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) dh0[at.b * q.H + h + v] = end[v];
+      for (int v = 0; v < VEC; ++v) {
+        float t = 0.0f;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) in_s[lane * VEC + v] = in[v];
+        for (int w = 0; w < W; ++w) t += back_s[w][lane * VEC + v];
+        if (on[v]) part[row + v] = t;
+      }
   }
-  // the states before the steps, while the first warp looks along the chain
-  for (int w = 0; w < warp; ++w)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float2 m = map_s[w][lane * VEC + v];
-      s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
-    }
-#pragma unroll
-  for (int j = 0; j < S; ++j)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float b = hb[j][v];
-      if ((cut >> j) & 1u) s[v] = 0.0f;
-      hb[j][v] = s[v];
-      s[v] = fmaf(kept_decay(ka[j][v]), s[v], b);
-    }
-  __syncthreads();
-
-  float sum[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) C[v] = in_s[lane * VEC + v], sum[v] = 0.0f;
-  for (int w = W - 1; w > warp; --w)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float m = map_s[w][lane * VEC + v].x, c = back_s[w][lane * VEC + v];
-      C[v] = cut_s[w] ? c : fmaf(m, C[v], c);
-    }
-  T* xp = dx.row(at.b, t0) + h;
-  T* rp = dr.row(at.b, t0) + h;
-  T* ip = di.row(at.b, t0) + h;
-#pragma unroll
-  for (int j = S - 1; j >= 0; --j) {
-    pack<T, VEC> ox, orr, oi;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float sr = sigmoid(to_f(rr[j].v[v])), si = sigmoid(to_f(ir[j].v[v]));
-      const float a = kept_decay(ka[j][v]), u = kept_rest(ka[j][v]);
-      const float rm = rsqrt_approx(max_nan(u, 1e-36f));
-      const float G = to_f(gr[j].v[v]) + C[v], sx = si * to_f(xr[j].v[v]);
-      const float E = G * a * (hb[j][v] - a * rm * sx) * sr, Gm = G * (u * rm);
-      if (j < n) sum[v] += E;
-      ox.v[v] = from_f<T>(Gm * si);
-      oi.v[v] = from_f<T>(Gm * sx * (1.0f - si));
-      orr.v[v] = from_f<T>(-k[v] * E * (1.0f - sr));
-      C[v] = (cut >> j) & 1u ? 0.0f : a * G;
-    }
-    if (on && j < n && DLR_IN(t0 + j, q.L)) {
-      *reinterpret_cast<pack<T, VEC>*>(xp + j * dx.st) = ox;
-      *reinterpret_cast<pack<T, VEC>*>(rp + j * dr.st) = orr;
-      *reinterpret_cast<pack<T, VEC>*>(ip + j * di.st) = oi;
-    }
-  }
-  __syncthreads();  // back_s has been read
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) back_s[warp][lane * VEC + v] = sum[v];
-  __syncthreads();
-  if (warp == 0 && on)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      float t = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) t += back_s[w][lane * VEC + v];
-      part[row + v] = t;
-    }
 }
 
 // dp = -c sigmoid(p) times the sum of a channel's parts, in a fixed order: a warp for each 32
@@ -484,77 +642,78 @@ view<T> out_view(const glr_out& v) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Bytes of the parts of a workspace: the chain's counter and flags, the maps, the entering values
-// and (backwards) the parts of dp. Flags are counted for the narrowest groups, of 32 channels.
+// Bytes of the parts of a workspace for tiles of `steps` steps: the chain's counter and flags (for
+// the narrowest groups, of 32 channels), the maps and the entering values.
 struct Space {
+  int64_t tiles;
   size_t head, maps, in;
-  Space(int64_t B, int64_t L, int64_t H) {
-    const size_t rows = (size_t)B * (size_t)glr_states(L);
+  Space(int64_t B, int64_t L, int64_t H, int64_t steps) : tiles(L < 1 ? 0 : (L - 1) / steps + 1) {
+    const size_t rows = (size_t)B * (size_t)tiles;
     head = align256(4 * (kHead + rows * (size_t)((H + 31) / 32)));
     maps = align256(sizeof(float2) * rows * (size_t)H);
     in = align256(sizeof(float) * rows * (size_t)H);
   }
 };
 
-// Two neighbouring 16-bit channels to a lane when every row begins on a 4-byte boundary and H is
-// even: a warp then reads 128 bytes of a row at once, where single channels make 64.
+// the widest access of `n` bytes that a view's rows allow
 template <typename V>
-bool in_pairs(const V& v) {
-  return ((reinterpret_cast<uintptr_t>(v.data) | (uintptr_t)(v.stride_b * 2) |
-           (uintptr_t)(v.stride_t * 2)) & 3u) == 0;
+bool wide(const V& v, int64_t size, uintptr_t n) {
+  return ((reinterpret_cast<uintptr_t>(v.data) | (uintptr_t)(v.stride_b * size) |
+           (uintptr_t)(v.stride_t * size)) & (n - 1)) == 0;
 }
 
-template <typename T, int VEC, typename A>
-Job<T> make_job(const A& a, float* in, const Space& sp) {
+template <typename T, typename A>
+Job<T> make_job(const A& a, const Space& sp) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const int64_t groups = (a.H + 32 * VEC - 1) / (32 * VEC);
-  return {in_view<T>(a.x), in_view<T>(a.r), in_view<T>(a.i), a.p, a.reset, in,
-          reinterpret_cast<float2*>(ws + sp.head), reinterpret_cast<uint32_t*>(ws),
-          device_status_word(), a.B, a.L, a.H, a.B * groups, (int)groups, (int)glr_states(a.L),
-          (float)a.c};
-}
-template <typename T>
-cudaError_t clear_chain(const Job<T>& q, cudaStream_t s) {
-  return cudaMemsetAsync(q.head, 0, 4 * (size_t)(kHead + q.chains * q.tiles), s);
+  const int64_t groups = (a.H + 32 * kVec<T> - 1) / (32 * kVec<T>);
+  return {in_view<T>(a.x), in_view<T>(a.r), in_view<T>(a.i), a.p, a.reset,
+          reinterpret_cast<float*>(ws + sp.head + sp.maps), reinterpret_cast<float2*>(ws + sp.head),
+          reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, a.B * groups,
+          (int)groups, (int)sp.tiles, (float)a.c};
 }
 
-template <typename T, int VEC, int W>
-cudaError_t scan_v(const glr_scan_args& a, cudaStream_t s) {
-  const Space sp(a.B, a.L, a.H);
-  float* in = a.states ? a.states
-                       : reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.head +
-                                                  sp.maps);
-  const Job<T> q = make_job<T, VEC>(a, in, sp);
-  const unsigned blocks = (unsigned)(q.chains * q.tiles);
-  if (q.tiles == 1) {
-    scan_kernel<T, VEC, W, false><<<blocks, W * 32, 0, s>>>(q, out_view<T>(a.y), a.h0, a.h_last);
-  } else {
-    const cudaError_t e = clear_chain(q, s);
-    if (e != cudaSuccess) return e;
-    scan_kernel<T, VEC, W, true><<<blocks, W * 32, 0, s>>>(q, out_view<T>(a.y), a.h0, a.h_last);
-  }
+// Blocks for `tiles` tiles: what the GPU holds at once at most. A chain of one tile needs no
+// counter and takes a block for each.
+template <typename T>
+cudaError_t prepare_chain(const Job<T>& q, int per_sm, unsigned* blocks, cudaStream_t s) {
+  const int64_t all = q.chains * q.tiles;
+  *blocks = (unsigned)all;
+  if (q.tiles == 1) return cudaSuccess;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  *blocks = (unsigned)std::min<int64_t>(all, (int64_t)sms * per_sm);
+  return cudaMemsetAsync(q.head, 0, 4 * (size_t)(kHead + all), s);
+}
+
+template <typename T, int kBytes>
+cudaError_t scan_w(const glr_scan_args& a, cudaStream_t s) {
+  constexpr size_t smem = 2 * 3 * kScanTile * 128;
+  const Job<T> q = make_job<T>(a, Space(a.B, a.L, a.H, kScanTile));
+  unsigned blocks;
+  cudaError_t e = prepare_chain(q, kScanBlocks, &blocks, s);
+  if (e == cudaSuccess) e = max_smem_once<scan_kernel<T, kBytes>>(smem);
+  if (e != cudaSuccess) return e;
+  scan_kernel<T, kBytes><<<blocks, kScanWarps * 32, smem, s>>>(q, out_view<T>(a.y), a.h0, a.h_last,
+                                                               a.states);
   return cudaGetLastError();
 }
 
-template <typename T, int VEC, int W>
-cudaError_t back_v(const glr_scan_backward_args& a, cudaStream_t s) {
-  const Space sp(a.B, a.L, a.H);
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  float* in = reinterpret_cast<float*>(ws + sp.head + sp.maps);
-  float* part = reinterpret_cast<float*>(ws + sp.head + sp.maps + sp.in);
-  const Job<T> q = make_job<T, VEC>(a, in, sp);
-  const unsigned blocks = (unsigned)(q.chains * q.tiles);
-  auto launch = [&](auto kernel) {
-    kernel<<<blocks, W * 32, 0, s>>>(q, in_view<T>(a.dy), a.states, a.dh_last, out_view<T>(a.dx),
-                                     out_view<T>(a.dr), out_view<T>(a.di), a.dh0, part);
-  };
-  if (q.tiles == 1) {
-    launch(back_kernel<T, VEC, W, false>);
-  } else {
-    const cudaError_t e = clear_chain(q, s);
-    if (e != cudaSuccess) return e;
-    launch(back_kernel<T, VEC, W, true>);
-  }
+template <typename T, int kBytes>
+cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
+  constexpr size_t smem = 2 * 4 * kBackTile * 128;
+  const Space sp(a.B, a.L, a.H, kBackTile);
+  const Job<T> q = make_job<T>(a, sp);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.head + sp.maps +
+                                         sp.in);
+  unsigned blocks;
+  cudaError_t e = prepare_chain(q, kBackBlocks, &blocks, s);
+  if (e == cudaSuccess) e = max_smem_once<back_kernel<T, kBytes>>(smem);
+  if (e != cudaSuccess) return e;
+  back_kernel<T, kBytes><<<blocks, kBackWarps * 32, smem, s>>>(
+      q, in_view<T>(a.dy), a.states, a.dh_last, out_view<T>(a.dx), out_view<T>(a.dr),
+      out_view<T>(a.di), a.dh0, part);
   back_sum<<<(unsigned)((a.H + 31) / 32), 256, 0, s>>>(part, a.B * q.tiles, a.H, a.p, (float)a.c,
                                                        a.dp);
   return cudaGetLastError();
@@ -562,18 +721,25 @@ cudaError_t back_v(const glr_scan_backward_args& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t scan_t(const glr_scan_args& a, cudaStream_t s) {
-  if constexpr (sizeof(T) == 2)
-    if (a.H % 2 == 0 && in_pairs(a.x) && in_pairs(a.r) && in_pairs(a.i) && in_pairs(a.y))
-      return scan_v<T, 2, 4>(a, s);
-  return scan_v<T, 1, 4>(a, s);
+  const int64_t z = sizeof(T);
+  auto all = [&](int64_t n) {
+    return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
+           wide(a.y, z, n);
+  };
+  if (all(16)) return scan_w<T, 16>(a, s);
+  if (sizeof(T) == 4 || all(4)) return scan_w<T, 4>(a, s);
+  if constexpr (sizeof(T) == 2) return scan_w<T, 2>(a, s);
 }
 template <typename T>
 cudaError_t back_t(const glr_scan_backward_args& a, cudaStream_t s) {
-  if constexpr (sizeof(T) == 2)
-    if (a.H % 2 == 0 && in_pairs(a.x) && in_pairs(a.r) && in_pairs(a.i) && in_pairs(a.dy) &&
-        in_pairs(a.dx) && in_pairs(a.dr) && in_pairs(a.di))
-      return back_v<T, 2, 8>(a, s);
-  return back_v<T, 1, 8>(a, s);
+  const int64_t z = sizeof(T);
+  auto all = [&](int64_t n) {
+    return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
+           wide(a.dy, z, n) && wide(a.dx, z, n) && wide(a.dr, z, n) && wide(a.di, z, n);
+  };
+  if (all(16)) return back_w<T, 16>(a, s);
+  if (sizeof(T) == 4 || all(4)) return back_w<T, 4>(a, s);
+  if constexpr (sizeof(T) == 2) return back_w<T, 2>(a, s);
 }
 
 template <typename T>
@@ -588,15 +754,15 @@ cudaError_t step_t(const glr_step_args& a, cudaStream_t s) {
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H) {
-  const Space sp(B, L, H);
+  const Space sp(B, L, H, kScanTile);
   return sp.head + sp.maps + sp.in;
 }
 size_t scan_backward_workspace_bytes(int64_t B, int64_t L, int64_t H) {
-  const Space sp(B, L, H);
+  const Space sp(B, L, H, kBackTile);
   return sp.head + sp.maps + 2 * sp.in;
 }
-// blocks of the largest grid that a call of this size launches
-int64_t scan_blocks(int64_t B, int64_t L, int64_t H) {
+// tiles (which a 32-bit counter hands out) of the finest cut that a call of this size takes
+int64_t scan_tiles(int64_t B, int64_t L, int64_t H) {
   return B * glr_states(L) * ((H + 31) / 32);
 }
 
