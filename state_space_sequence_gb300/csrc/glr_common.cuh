@@ -70,42 +70,57 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-kLog2
 // softplus(v) = log(1 + e^v); above 20 it is v to float precision
 __device__ __forceinline__ float softplus(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
 
-// a - 1 and a for a = 2^z, z <= 0. With n = rint(z), f = z - n and q = 2^f - 1 (a polynomial with
-// q(0) = 0, so its relative error of 2e-8 holds down to z = 0), a - 1 = 2^n q + (2^n - 1). a - 1
-// therefore keeps its digits where a is next to 1, and so does 1 - a^2 = -(a - 1)(2 + (a - 1)): with
-// a alone its rounding to 2^-24 would be 6e-5 of 1 - a^2 at a memory of 1000 steps. The
-// coefficients are a least-maximum fit of (2^f - 1) / f on |f| <= 1/2. Below z = -126 a is held
-// at 2^-126.
-__device__ __forceinline__ void decay(float z, float& w, float& a) {
-  z = max_nan(z, -126.0f);
-  const float t = z + 12582912.0f;  // 1.5 * 2^23: n in the low bits
-  const float f = z - (t - 12582912.0f);
-  const float s = __int_as_float((__float_as_int(t) << 23) + 0x3f800000);  // 2^n
-  float q = 0.000154035120f;
-  q = fmaf(q, f, 0.00133907355f);
-  q = fmaf(q, f, 0.00961823750f);
-  q = fmaf(q, f, 0.0555035743f);
-  q = fmaf(q, f, 0.240226498f);
-  q = fmaf(q, f, 0.693147188f);
-  q *= f;
-  w = -fmaf(-s, q, 1.0f - s);  // -0 where a = 1
-  a = fmaf(s, q, s);
+// Two elements at a time: one instruction works on both halves.
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 t = mul2(v, two(-kLog2e));
+  const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), two(1.0f));
+  return make_float2(rcp(d.x), rcp(d.y));
 }
 
-// One step's gates. kz = -c softplus(p) log2(e).
-struct gate {
-  float sr, si;  // sigmoid(r), sigmoid(i)
-  float w, a;    // the decay less 1, and the decay
-  float m, rm;   // sqrt(1 - a^2) and its reciprocal (a finite number where m is 0)
+// 1 - a and a for a = 2^z, z <= 0. With n = rint(z), f = z - n and q = 1 - 2^f (a polynomial with
+// q(0) = 0, so its relative error of 2e-8 holds down to z = 0), 1 - a = 2^n q + (1 - 2^n). 1 - a
+// therefore keeps its digits where a is next to 1, and so does 1 - a^2 = (1 - a)(1 + a): from a
+// alone its rounding to 2^-24 would be 6e-5 of 1 - a^2 at a memory of 1000 steps. The coefficients are
+// a least-maximum fit of (1 - 2^f) / f on |f| <= 1/2. Below z = -126 a is held at 2^-126.
+__device__ __forceinline__ void decay2(float2 z, float2& rest, float2& a) {
+  z = make_float2(max_nan(z.x, -126.0f), max_nan(z.y, -126.0f));
+  const float2 t = add2(z, two(12582912.0f));  // 1.5 * 2^23: n in the low bits
+  const float2 f = fma2(add2(t, two(-12582912.0f)), two(-1.0f), z);
+  const float2 s = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                               __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));  // 2^n
+  float2 q = two(-0.000154035120f);
+  q = fma2(q, f, two(-0.00133907355f));
+  q = fma2(q, f, two(-0.00961823750f));
+  q = fma2(q, f, two(-0.0555035743f));
+  q = fma2(q, f, two(-0.240226498f));
+  q = fma2(q, f, two(-0.693147188f));
+  q = mul2(q, f);
+  rest = fma2(s, q, fma2(s, two(-1.0f), two(1.0f)));
+  a = mul2(s, fma2(q, two(-1.0f), two(1.0f)));
+}
+
+// Two elements' gates. kz = -c softplus(p) log2(e).
+struct gate2 {
+  float2 sr, si;    // sigmoid(r), sigmoid(i)
+  float2 rest, a;   // the decay from 1, and the decay
+  float2 m;         // sqrt(1 - a^2)
 };
-__device__ __forceinline__ gate make_gate(float r, float i, float kz) {
-  gate g;
-  g.sr = sigmoid(r);
-  g.si = sigmoid(i);
-  decay(kz * g.sr, g.w, g.a);
-  const float v = -g.w * (2.0f + g.w);
-  g.rm = rsqrt_approx(max_nan(v, 1e-36f));
-  g.m = v * g.rm;
+// 1 / sqrt(u), a finite number where u is 0
+__device__ __forceinline__ float2 rsqrt2(float2 u) {
+  return make_float2(rsqrt_approx(max_nan(u.x, 1e-36f)), rsqrt_approx(max_nan(u.y, 1e-36f)));
+}
+__device__ __forceinline__ gate2 make_gate2(float2 r, float2 i, float2 kz) {
+  gate2 g;
+  g.sr = sigmoid2(r);
+  g.si = sigmoid2(i);
+  decay2(mul2(kz, g.sr), g.rest, g.a);
+  const float2 u = mul2(g.rest, add2(g.a, two(1.0f)));
+  g.m = mul2(u, rsqrt2(u));
   return g;
 }
 

@@ -167,14 +167,46 @@ __device__ __forceinline__ uint32_t cuts(const uint8_t* reset, int64_t first, in
   return __ballot_sync(0xffffffffu, lane < n && reset[first + lane] != 0);
 }
 
-// A decay in one register with its digits both next to 1 and next to 0: a - 1 (negative, with -0 for
+// A decay in one register with its digits both next to 1 and next to 0: a - 1 (negative; -0 for
 // a = 1) where a > 1/2, else a.
-__device__ __forceinline__ float keep_decay(const gate& g) { return g.a > 0.5f ? g.w : g.a; }
-__device__ __forceinline__ float sign_one(float k) { return signbit(k) ? 1.0f : 0.0f; }
-__device__ __forceinline__ float kept_decay(float k) { return k + sign_one(k); }
-__device__ __forceinline__ float kept_rest(float k) {  // 1 - a^2
-  const float s = sign_one(k);
-  return fmaf(-k, fmaf(2.0f, s, k), 1.0f - s);
+__device__ __forceinline__ float2 keep_decay(const gate2& g) {
+  return make_float2(g.a.x > 0.5f ? -g.rest.x : g.a.x, g.a.y > 0.5f ? -g.rest.y : g.a.y);
+}
+__device__ __forceinline__ float2 sign_ones(float2 k) {
+  return make_float2(__float_as_int(k.x) < 0 ? 1.0f : 0.0f, __float_as_int(k.y) < 0 ? 1.0f : 0.0f);
+}
+__device__ __forceinline__ float2 kept_decay(float2 k) { return add2(k, sign_ones(k)); }
+
+// A warp's S steps of VEC channels a lane are S VEC / 2 pairs: the two channels of a step, or, with one
+// channel to a lane, two steps. half(): step j of channel v.
+template <int VEC, int N>
+__device__ __forceinline__ float& half(float2 (&p)[N], int j, int v) {
+  if constexpr (VEC == 2) return v ? p[j].y : p[j].x;
+  return j & 1 ? p[j / 2].y : p[j / 2].x;
+}
+__device__ __forceinline__ float2 floats(pack<__nv_bfloat16, 2> k) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&k);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 floats(pack<__half, 2> k) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&k));
+}
+// pair m of the rows [.][C] at p
+template <typename T, int VEC, int C>
+__device__ __forceinline__ float2 get2(const T* p, int m) {
+  if constexpr (VEC == 2) return floats(*reinterpret_cast<const pack<T, 2>*>(p + m * C));
+  else return make_float2(p[2 * m * C], p[(2 * m + 1) * C]);
+}
+
+// s through the step j: abar s + b
+template <int VEC, int N>
+__device__ __forceinline__ void advance(float (&s)[VEC], float2 (&a)[N], float2 (&b)[N], int j) {
+  if constexpr (VEC == 2) {
+    const float2 t = fma2(a[j], make_float2(s[0], s[1]), b[j]);
+    s[0] = t.x, s[1] = t.y;
+  } else {
+    s[0] = fmaf(half<VEC>(a, j, 0), s[0], half<VEC>(b, j, 0));
+  }
 }
 
 // How a tile's inputs come into shared memory: by asynchronous copies of 16 bytes where every row
@@ -250,6 +282,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, kScanBlocks)
 scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
             float* __restrict__ states) {
   constexpr int VEC = kVec<T>, W = kScanWarps, S = kScanSteps, C = 32 * VEC, threads = W * 32;
+  constexpr int NP = S * VEC / 2;
   constexpr bool kOne = kBytes == 2;
   extern __shared__ __align__(16) uint8_t smem[];
   T* const buf = reinterpret_cast<T*>(smem);  // [2][r i x][kScanTile][C]
@@ -290,44 +323,48 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
     const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
     const T* mine = buf + turn * 3 * kScanTile * C + warp * S * C + lane * VEC;
     bool on[VEC];
-    float kz[VEC], a[S][VEC], b[S][VEC], A[VEC], e[VEC];
+    float kz[VEC], A[VEC], e[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       on[v] = h + v < q.H && DLR_IN(at.b, q.B);
       kz[v] = on[v] ? -q.c * softplus(q.p[h + v]) * kLog2e : 0.0f;
       A[v] = 1.0f, e[v] = 0.0f;
     }
-    const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
+    const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);  // as n, the same for all of the warp
+    float2 a[NP], b[NP];
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const pack<T, VEC> r = *reinterpret_cast<const pack<T, VEC>*>(mine + j * C);
-      const pack<T, VEC> i = *reinterpret_cast<const pack<T, VEC>*>(mine + (kScanTile + j) * C);
-      const pack<T, VEC> x = *reinterpret_cast<const pack<T, VEC>*>(mine + (2 * kScanTile + j) * C);
+    for (int m = 0; m < NP; ++m) {
+      const gate2 g = make_gate2(get2<T, VEC, C>(mine, m), get2<T, VEC, C>(mine + kScanTile * C, m),
+                                 make_float2(kz[0], kz[VEC - 1]));
+      a[m] = g.a;
+      b[m] = mul2(g.m, mul2(g.si, get2<T, VEC, C>(mine + 2 * kScanTile * C, m)));
+    }
+    if (n < S) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const gate g = make_gate(to_f(r.v[v]), to_f(i.v[v]), kz[v]);
-        a[j][v] = g.a;
-        b[j][v] = g.m * g.si * to_f(x.v[v]);
+      for (int j = 0; j < S; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          if (j >= n) half<VEC>(a, j, v) = 1.0f, half<VEC>(b, j, v) = 0.0f;
+    }
+#pragma unroll
+    for (int m = 0; m < NP; ++m) {
+      if constexpr (VEC == 2) {
+        A[0] *= a[m].x, A[1] *= a[m].y;
+      } else {
+        A[0] *= a[m].x * a[m].y;
       }
     }
-    const bool plain = n == S && cut == 0;  // the same for all of the warp
-    if (plain) {
+    if (cut == 0) {
 #pragma unroll
-      for (int j = 0; j < S; ++j)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          e[v] = fmaf(a[j][v], e[v], b[j][v]);
-          A[v] *= a[j][v];
-        }
+      for (int j = 0; j < S; ++j) advance<VEC>(e, a, b, j);
     } else {
 #pragma unroll
-      for (int j = 0; j < S; ++j)
+      for (int j = 0; j < S; ++j) {
+        advance<VEC>(e, a, b, j);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          if (j >= n) a[j][v] = 1.0f, b[j][v] = 0.0f;
-          e[v] = (cut >> j) & 1u ? b[j][v] : fmaf(a[j][v], e[v], b[j][v]);
-          A[v] *= a[j][v];
-        }
+        for (int v = 0; v < VEC; ++v)
+          if ((cut >> j) & 1u) e[v] = half<VEC>(b, j, v);
+      }
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
@@ -376,20 +413,20 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
           states[(at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t0 / GLR_STATE_STEPS) * q.H + h + v] =
               s[v];
     T* yp = y.row(at.b, t0) + h;
-    if (plain) {
+    if (n == S && cut == 0) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) s[v] = fmaf(a[j][v], s[v], b[j][v]);
+        advance<VEC>(s, a, b, j);
         put<T, VEC, kOne>(yp, s, on);
         yp += y.st;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
+        advance<VEC>(s, a, b, j);
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          s[v] = (cut >> j) & 1u ? b[j][v] : fmaf(a[j][v], s[v], b[j][v]);
+          if ((cut >> j) & 1u) s[v] = half<VEC>(b, j, v);
         if (j < n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp, s, on);
         yp += y.st;
       }
@@ -397,10 +434,10 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
   }
 }
 
-constexpr int kBackSteps = 16;
-constexpr int kBackWarps = 4;
+constexpr int kBackSteps = 8;
+constexpr int kBackWarps = 8;
 constexpr int kBackTile = kBackSteps * kBackWarps;
-constexpr int kBackBlocks = 3;
+constexpr int kBackBlocks = 2;
 static_assert(kBackTile == GLR_STATE_STEPS, "a tile begins at a kept state");
 
 template <typename T, int kBytes>
@@ -409,6 +446,7 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
             const float* __restrict__ dh_last, view<T> dx, view<T> dr, view<T> di,
             float* __restrict__ dh0, float* __restrict__ part) {
   constexpr int VEC = kVec<T>, W = kBackWarps, S = kBackSteps, C = 32 * VEC, threads = W * 32;
+  constexpr int NP = S * VEC / 2;
   constexpr int kArray = kBackTile * C;
   constexpr bool kOne = kBytes == 2;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -449,9 +487,7 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
     const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.H + h;
     const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
     const T* mine = buf + turn * 4 * kArray + warp * S * C + lane * VEC;
-    auto raw = [&](int array, int j) {
-      return *reinterpret_cast<const pack<T, VEC>*>(mine + array * kArray + j * C);
-    };
+    auto raw = [&](int array, int m) { return get2<T, VEC, C>(mine + array * kArray, m); };
     bool on[VEC];
     float k[VEC], s[VEC];
 #pragma unroll
@@ -461,32 +497,46 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
       s[v] = on[v] ? states[row + v] : 0.0f;
     }
     const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
-    // the decay (see kept_decay), and b, in whose place the state before the step comes later
-    float ka[S][VEC], hb[S][VEC], A[VEC], e[VEC], G[VEC];
+    const float2 k2 = make_float2(k[0], k[VEC - 1]), kz = mul2(k2, two(-kLog2e));
+    // the decay (see keep_decay), and b, in whose place the state before the step comes later
+    float2 ka[NP], hb[NP];
+    float A[VEC], e[VEC], G[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f, G[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const pack<T, VEC> r = raw(0, j), i = raw(1, j), x = raw(2, j);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const gate g = make_gate(to_f(r.v[v]), to_f(i.v[v]), -k[v] * kLog2e);
-        ka[j][v] = keep_decay(g);
-        hb[j][v] = g.m * g.si * to_f(x.v[v]);
-        if (n < S && j >= n) ka[j][v] = -0.0f, hb[j][v] = 0.0f;
-        const float a = kept_decay(ka[j][v]);
-        e[v] = (cut >> j) & 1u ? hb[j][v] : fmaf(a, e[v], hb[j][v]);
-        A[v] *= a;
-      }
+    for (int m = 0; m < NP; ++m) {
+      const gate2 g = make_gate2(raw(0, m), raw(1, m), kz);
+      ka[m] = keep_decay(g);
+      hb[m] = mul2(g.m, mul2(g.si, raw(2, m)));
     }
+    if (n < S) {
 #pragma unroll
-    for (int j = S - 1; j >= 0; --j) {
-      const pack<T, VEC> g = raw(3, j);
+      for (int j = 0; j < S; ++j)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float t = (n < S && j >= n ? 0.0f : to_f(g.v[v])) + G[v];
-        G[v] = (cut >> j) & 1u ? 0.0f : kept_decay(ka[j][v]) * t;
+        for (int v = 0; v < VEC; ++v)
+          if (j >= n) half<VEC>(ka, j, v) = -0.0f, half<VEC>(hb, j, v) = 0.0f;
+    }
+    // the warp's maps in both directions
+    {
+      float2 a[NP], t[NP];
+#pragma unroll
+      for (int m = 0; m < NP; ++m) a[m] = kept_decay(ka[m]), t[m] = raw(3, m);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f, G[v] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        advance<VEC>(e, a, hb, j);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          A[v] *= half<VEC>(a, j, v);
+          if ((cut >> j) & 1u) e[v] = half<VEC>(hb, j, v);
+        }
       }
+#pragma unroll
+      for (int j = S - 1; j >= 0; --j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const float d = j < n ? half<VEC>(t, j, v) : 0.0f;
+          G[v] = (cut >> j) & 1u ? 0.0f : half<VEC>(a, j, v) * (d + G[v]);
+        }
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -529,15 +579,23 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
         const float2 m = map_s[w][lane * VEC + v];
         s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
       }
+    {
+      float2 a[NP];
 #pragma unroll
-    for (int j = 0; j < S; ++j)
+      for (int m = 0; m < NP; ++m) a[m] = kept_decay(ka[m]);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float b = hb[j][v];
-        if ((cut >> j) & 1u) s[v] = 0.0f;
-        hb[j][v] = s[v];
-        s[v] = fmaf(kept_decay(ka[j][v]), s[v], b);
+      for (int j = 0; j < S; ++j) {
+        float before[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          if ((cut >> j) & 1u) s[v] = 0.0f;
+          before[v] = s[v];
+        }
+        advance<VEC>(s, a, hb, j);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) half<VEC>(hb, j, v) = before[v];
       }
+    }
     __syncthreads();
 
     float sum[VEC];
@@ -553,27 +611,57 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
     T* rp = dr.row(at.b, t0) + h;
     T* ip = di.row(at.b, t0) + h;
 #pragma unroll
-    for (int j = S - 1; j >= 0; --j) {
+    for (int m = NP - 1; m >= 0; --m) {
+      constexpr int per = VEC == 2 ? 1 : 2;  // steps of a pair
+      const int j = m * per;
       if (j >= n) continue;
-      const pack<T, VEC> r = raw(0, j), i = raw(1, j), x = raw(2, j), g = raw(3, j);
-      float ox[VEC], orr[VEC], oi[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float sr = sigmoid(to_f(r.v[v])), si = sigmoid(to_f(i.v[v]));
-        const float a = kept_decay(ka[j][v]), u = kept_rest(ka[j][v]);
-        const float rm = rsqrt_approx(max_nan(u, 1e-36f));
-        const float t = to_f(g.v[v]) + G[v], sx = si * to_f(x.v[v]);
-        const float E = t * a * (hb[j][v] - a * rm * sx) * sr, tm = t * (u * rm);
-        sum[v] += E;
-        ox[v] = tm * si;
-        oi[v] = tm * sx * (1.0f - si);
-        orr[v] = -k[v] * E * (1.0f - sr);
-        G[v] = (cut >> j) & 1u ? 0.0f : a * t;
+      const float2 sr = sigmoid2(raw(0, m)), si = sigmoid2(raw(1, m));
+      // 1 - a^2 from what is kept: 1 - a^2, or -k (2 + k) with k = a - 1
+      const float2 neg = sign_ones(ka[m]), a = add2(ka[m], neg);
+      const float2 u = fma2(mul2(ka[m], two(-1.0f)), fma2(neg, two(2.0f), ka[m]),
+                            fma2(neg, two(-1.0f), two(1.0f)));
+      const float2 rm = rsqrt2(u), sx = mul2(si, raw(2, m)), dyv = raw(3, m);
+      float2 t;  // G of the two
+      if constexpr (VEC == 2) {
+        t = add2(dyv, make_float2(G[0], G[1]));
+        const float2 next = mul2(a, t);
+        G[0] = (cut >> j) & 1u ? 0.0f : next.x;
+        G[1] = (cut >> j) & 1u ? 0.0f : next.y;
+      } else {
+        t.y = G[0];
+        if (j + 1 < n) {
+          t.y += dyv.y;
+          G[0] = (cut >> (j + 1)) & 1u ? 0.0f : a.y * t.y;
+        }
+        t.x = dyv.x + G[0];
+        G[0] = (cut >> j) & 1u ? 0.0f : a.x * t.x;
       }
-      if (DLR_IN(t0 + j, q.L)) {
-        put<T, VEC, kOne>(xp + j * dx.st, ox, on);
-        put<T, VEC, kOne>(rp + j * dr.st, orr, on);
-        put<T, VEC, kOne>(ip + j * di.st, oi, on);
+      const float2 arm = mul2(mul2(a, rm), two(-1.0f));
+      const float2 E = mul2(mul2(mul2(t, a), sr), fma2(arm, sx, hb[m]));
+      const float2 tm = mul2(t, mul2(u, rm));
+      const float2 ox = mul2(tm, si);
+      const float2 oi = mul2(mul2(tm, sx), fma2(si, two(-1.0f), two(1.0f)));
+      const float2 orr = mul2(mul2(k2, E), fma2(sr, two(1.0f), two(-1.0f)));
+      if constexpr (VEC == 2) {
+        sum[0] += E.x, sum[1] += E.y;
+      } else {
+        sum[0] += E.x;
+        if (j + 1 < n) sum[0] += E.y;
+      }
+#pragma unroll
+      for (int d = 0; d < per; ++d) {
+        float px[VEC], pr[VEC], pi[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          px[v] = d + v ? ox.y : ox.x;
+          pr[v] = d + v ? orr.y : orr.x;
+          pi[v] = d + v ? oi.y : oi.x;
+        }
+        if (j + d < n && DLR_IN(t0 + j + d, q.L)) {
+          put<T, VEC, kOne>(xp + (j + d) * dx.st, px, on);
+          put<T, VEC, kOne>(rp + (j + d) * dr.st, pr, on);
+          put<T, VEC, kOne>(ip + (j + d) * di.st, pi, on);
+        }
       }
     }
     __syncthreads();  // back_s has been read
@@ -623,9 +711,9 @@ step_kernel(view<const T> x, view<const T> r, view<const T> i, const float* __re
   if (k >= B * H) return;
   const int64_t b = k / H, ch = k % H;
   const float kz = -c * softplus(p[ch]) * kLog2e;
-  const gate g = make_gate(to_f(r.row(b, 0)[ch]), to_f(i.row(b, 0)[ch]), kz);
-  const float bt = g.m * g.si * to_f(x.row(b, 0)[ch]);
-  const float s = reset && reset[b] ? bt : fmaf(g.a, h[k], bt);
+  const gate2 g = make_gate2(two(to_f(r.row(b, 0)[ch])), two(to_f(i.row(b, 0)[ch])), two(kz));
+  const float bt = g.m.x * g.si.x * to_f(x.row(b, 0)[ch]);
+  const float s = reset && reset[b] ? bt : fmaf(g.a.x, h[k], bt);
   if (!DLR_IN(k, B * H)) return;
   h_out[k] = s;
   y.row(b, 0)[ch] = from_f<T>(s);
