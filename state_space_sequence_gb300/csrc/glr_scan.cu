@@ -27,19 +27,49 @@ int* device_status_word();
 namespace glr {
 namespace {
 
-constexpr int kHead = 64;  // words of the chain's workspace before its flags
+constexpr int kHead = 64;  // words of the chain's workspace before the maps; the first counts tickets
 
-// Flags of a tile: nothing yet, its map is there, its end value is there.
-constexpr uint32_t kHasMap = 1, kHasEnd = 2;
+// Every word of the chain's workspace begins with these bits, a NaN that no arithmetic makes: a float
+// that reads otherwise has been published. One 32-bit store publishes one float, so readers need
+// neither flags nor fences; with flags, the two fences of a tile (to the L2 and back each)
+// and the flag's own way made a tile's turn on the chain 4 us long instead of some 1.2 us.
+constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;  // a longer wait is a fault
 
-__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+__device__ __forceinline__ bool empty(float v) { return __float_as_uint(v) == kEmpty; }
+__device__ __forceinline__ float full(float v) {  // any NaN but that one
+  return empty(v) ? __uint_as_float(0x7fffffffu) : v;
 }
-__device__ __forceinline__ void store_release(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+// N neighbouring floats (each a store or load of its own to other threads)
+template <int N>
+__device__ __forceinline__ void post(float* p, const float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "one access");
+  if constexpr (N == 1)
+    asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(full(v[0])) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(full(v[0])),
+                 "f"(full(v[1]))
+                 : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(full(v[0])),
+                 "f"(full(v[1])), "f"(full(v[2])), "f"(full(v[3]))
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void look(const float* p, float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "one access");
+  if constexpr (N == 1)
+    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v[0]) : "l"(p) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v[0]), "=f"(v[1])
+                 : "l"(p)
+                 : "memory");
+  else
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "l"(p)
+                 : "memory");
 }
 __device__ __forceinline__ uint64_t timer_ns() {
   uint64_t t;
@@ -47,18 +77,18 @@ __device__ __forceinline__ uint64_t timer_ns() {
   return t;
 }
 
-// What the two directions share. head: a ticket counter, then the flags [chains, tiles], all zero
-// at the launch. A chain is the row of tiles of one batch entry and group of 32 VEC channels.
+// What the two directions share. A chain is the row of tiles of one batch entry and group of 32 VEC
+// channels. The channels of `in` and `maps` are padded to whole groups.
 template <typename T>
 struct Job {
   view<const T> x, r, i;
   const float* p;
   const uint8_t* reset;
-  float* in;     // [B, tiles, H]: the value that enters each tile
-  float2* maps;  // [B, tiles, H]: each tile's map
+  float* in;    // [B, tiles, HP]: the value that enters each tile but the chain's first
+  float* maps;  // [B, tiles, HP, 2]: each tile's map (A, e)
   uint32_t* head;
   int* status;
-  int64_t B, L, H, chains;
+  int64_t B, L, H, HP, chains;
   int groups, tiles;
   float c;
 };
@@ -83,81 +113,90 @@ __device__ __forceinline__ Tile tile_of(const J& q, uint32_t k, bool backwards) 
   return at;
 }
 
-// Called by one warp whose lanes have stored what the flag announces.
-__device__ __forceinline__ void publish(uint32_t* flag, uint32_t what) {
-  __threadfence();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) store_release(flag, what);
-}
-
-// Called by one warp. Waits until one of the `back` tiles before this one has its end value and all
-// those between have their maps; each lane looks at one tile at a time (`step` flags from one to
-// the next). Returns how far back it is, or 0 when the wait ran out. The first tile of a chain always
-// comes to its end value by itself.
-__device__ __forceinline__ int look_back(const uint32_t* flag, int back, int step) {
-  const int lane = threadIdx.x & 31;
-  uint64_t t0 = 0;
-  for (int first = 0;;) {
-    const int k = first + lane + 1;
-    const uint32_t f = k <= back ? load_acquire(flag - (int64_t)step * k) : 0u;
-    const uint32_t ends = __ballot_sync(0xffffffffu, f == kHasEnd);
-    const uint32_t none = __ballot_sync(0xffffffffu, f == 0u);
-    const int l = ends ? __ffs(ends) - 1 : 32;
-    if (!(none & (l == 32 ? 0xffffffffu : (1u << l) - 1u))) {
-      if (l < 32) return first + l + 1;
-      first += 32;  // 32 maps and no end among them
-      continue;
-    }
-    const uint64_t t = timer_ns();
-    if (t0 == 0) t0 = t;
-    if (__any_sync(0xffffffffu, t - t0 > kWaitNs)) return 0;
-  }
-}
-
 // Called by one warp: the value s that enters the tile, and `end`, the one that leaves it, from
 // the tile's map (A, e); `cut`: the map does not depend on what enters. row: the lane's first
-// element of in and maps, dir = 1 forwards, -1 backwards. The first tile of the chain has its s.
+// element of `in`; dir = 1 forwards, -1 backwards. The first tile of the chain has its s.
+//
+// It looks at four tiles at a time for the nearest one whose end value is there, all maps between
+// being there too; the first tile of a chain always comes to its end value by itself.
 template <int VEC, typename J>
 __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, int dir,
-                                      const bool (&on)[VEC], const float (&A)[VEC],
-                                      const float (&e)[VEC], bool cut, float (&s)[VEC],
-                                      float (&end)[VEC]) {
+                                      const float (&A)[VEC], const float (&e)[VEC], bool cut,
+                                      float (&s)[VEC], float (&end)[VEC]) {
+  constexpr int U = 4;
   const int done = dir > 0 ? at.tile : q.tiles - 1 - at.tile;  // tiles of the chain before this
   const bool last = done == q.tiles - 1;
-  const int64_t dH = dir * q.H;
-  uint32_t* flag = q.head + kHead + ((int64_t)at.b * q.groups + at.group) * q.tiles + at.tile;
+  const int64_t step = dir * q.HP;
   if (done > 0) {
-    if (!last) {
+    if (!last && cut) {
+      post(q.in + row + step, e);
+    } else if (!last) {
+      float m[2 * VEC];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        if (!on[v]) continue;
-        if (cut)
-          q.in[row + dH + v] = e[v];
-        else
-          q.maps[row + v] = make_float2(A[v], e[v]);
-      }
-      publish(flag, cut ? kHasEnd : kHasMap);
+      for (int v = 0; v < VEC; ++v) m[2 * v] = A[v], m[2 * v + 1] = e[v];
+      post(q.maps + 2 * row, m);
     }
-    const int far = look_back(flag, done, dir);
-    if (far == 0 && (threadIdx.x & 31) == 0) report_status(q.status, DLR_ERR_TIMEOUT);
+    const float* in = q.in + row;               // what enters this tile: the end of the one before
+    const float* maps = q.maps + 2 * (row - step);  // of the one before
+    float ends[U][VEC], m[U][2 * VEC];
+    uint64_t t0 = 0;
+    int far = 0;  // tiles back whose maps come into it
+    for (bool found = false; !found;) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      s[v] = on[v] && far ? __ldcg(&q.in[row - (far - 1) * dH + v]) : 0.0f;
-#pragma unroll 4
-    for (int k = far - 1; k >= 1; --k)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float2 m = on[v] ? __ldcg(&q.maps[row - k * dH + v]) : make_float2(0.0f, 0.0f);
-        s[v] = fmaf(m.x, s[v], m.y);
+      for (int u = 0; u < U; ++u) {
+        if (far + u >= done) continue;
+        look(in - (far + u) * step, ends[u]);
+        look(maps - 2 * (far + u) * step, m[u]);
       }
+      int more = 0;  // of these, maps that are there before the first end
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (found || more < u || far + u >= done) continue;
+        bool no_end = false, no_map = false;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          no_end |= empty(ends[u][v]);
+          no_map |= empty(m[u][2 * v]) || empty(m[u][2 * v + 1]);
+        }
+        if (!__any_sync(0xffffffffu, no_end)) {
+          found = true;
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) s[v] = ends[u][v];
+        } else if (!__any_sync(0xffffffffu, no_map)) {
+          more = u + 1;
+        }
+      }
+      if (found && far == 0) {  // the maps are at hand
+#pragma unroll
+        for (int u = U - 2; u >= 0; --u)
+          if (u < more)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s[v] = fmaf(m[u][2 * v], s[v], m[u][2 * v + 1]);
+        break;
+      }
+      far += more;
+      if (found || more == U) continue;
+      const uint64_t t = timer_ns();
+      if (t0 == 0) t0 = t;
+      if (__any_sync(0xffffffffu, t - t0 > kWaitNs)) {
+        if ((threadIdx.x & 31) == 0) report_status(q.status, DLR_ERR_TIMEOUT);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = 0.0f;
+        far = 0;
+        break;
+      }
+    }
+#pragma unroll 8
+    for (int k = far - 1; k >= 0; --k) {
+      float t[2 * VEC];
+      look(maps - 2 * k * step, t);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) s[v] = fmaf(t[2 * v], s[v], t[2 * v + 1]);
+    }
   }
 #pragma unroll
   for (int v = 0; v < VEC; ++v) end[v] = cut ? e[v] : fmaf(A[v], s[v], e[v]);
-  if (last || (done > 0 && cut)) return;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v)
-    if (on[v]) q.in[row + dH + v] = end[v];
-  publish(flag, kHasEnd);
+  if (!last && !(done > 0 && cut)) post(q.in + row + step, end);
 }
 
 // bits of the n steps from t on that begin a sequence
@@ -230,27 +269,39 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// `steps` rows of C channels of v into dst [steps][C]; rows past the end and channels past H are zero
-template <typename T, int C, int kBytes, int kThreads>
+// kSteps rows of C channels of v into dst [kSteps][C], by kThreads threads; rows past the end and channels
+// past H are zero
+template <typename T, int C, int kSteps, int kBytes, int kThreads>
 __device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b, int64_t t0,
-                                      int64_t h0, int steps, int64_t L, int64_t H) {
-  constexpr int per = kBytes / (int)sizeof(T), cols = C / per;
-  const int col = threadIdx.x % cols * per;
-  const bool in = h0 + col < H;
-  const T* src = v.row(b, t0) + h0 + col;
-  if constexpr (kBytes == 2) {
-#pragma unroll 4
-    for (int j = threadIdx.x / cols; j < steps; j += kThreads / cols)
-      dst[j * C + col] = in && t0 + j < L ? src[j * v.st] : from_f<T>(0.0f);
-  } else {
-    const int64_t dp = (kThreads / cols) * v.st;
-    const T* p = src + (threadIdx.x / cols) * v.st;
-#pragma unroll 4
-    for (int j = threadIdx.x / cols; j < steps; j += kThreads / cols, p += dp) {
-      const bool on = in && t0 + j < L;
-      copy_async<kBytes>(dst + j * C + col, on ? p : v.p, on);
-    }
+                                      int64_t h0, int64_t L, int64_t H) {
+  constexpr int per = kBytes / (int)sizeof(T), cols = C / per, rows = kThreads / cols;
+  static_assert(kSteps % rows == 0, "whole rounds");
+  const int col = threadIdx.x % cols * per, first = threadIdx.x / cols;
+  const T* p = v.row(b, t0 + first) + h0 + col;
+  const int64_t dp = rows * v.st;
+  dst += first * C + col;
+  if (kBytes != 2 && t0 + kSteps <= L && h0 + C <= H) {
+#pragma unroll
+    for (int j = 0; j < kSteps; j += rows, p += dp) copy_async<kBytes>(dst + j * C, p, true);
+    return;
   }
+  const bool in = h0 + col < H;
+#pragma unroll 4
+  for (int j = 0; j < kSteps; j += rows, p += dp) {
+    const bool on = in && t0 + first + j < L;
+    if constexpr (kBytes == 2)
+      dst[j * C] = on ? *p : from_f<T>(0.0f);
+    else
+      copy_async<kBytes>(dst + j * C, on ? p : v.p, on);
+  }
+}
+
+// Named barriers: a warp that only arrives does not wait.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // VEC neighbouring values to memory: at once, or one by one where they are not aligned
@@ -272,165 +323,228 @@ __device__ __forceinline__ void put(T* p, const float (&f)[VEC], bool (&on)[VEC]
 template <typename T>
 constexpr int kVec = 4 / (int)sizeof(T);
 
-constexpr int kScanSteps = 16;                       // of a warp
-constexpr int kScanWarps = 8;
+constexpr int kScanSteps = 8;                        // of a warp
+constexpr int kScanWarps = 16;                       // that compute; one more keeps the chain
 constexpr int kScanTile = kScanSteps * kScanWarps;   // steps
-constexpr int kScanBlocks = 2;                       // blocks that an SM holds
+constexpr int kScanThreads = 32 * (kScanWarps + 1);
+constexpr int kRing = 8;                             // tiles whose places a block remembers
 
+// Named barriers of a block, two of each kind for even and odd tiles: the maps of a tile are in shared
+// memory (the computing warps arrive, the chain's warp waits); the values that enter its
+// warps are there (the other way round); and one for the computing warps alone.
+constexpr int kMapsBar = 1, kEnterBar = 3, kWarpsBar = 5;
+
+template <typename T>
+struct ScanShared {
+  static constexpr int C = 32 * kVec<T>;
+  T buf[2][3][kScanTile][C];        // r, i, x of two tiles
+  float2 map[3][kScanWarps][C];     // (A, e) of each warp's steps
+  float enter[2][kScanWarps][C];    // the state that enters them
+  float kz[kRing][C];
+  uint32_t cut[3][kScanWarps];
+  Tile tile[kRing];
+};
+
+// The last warp keeps the chain; the others compute, one tile ahead of it: they have the gates of
+// tile k + 1 done before they need the state that enters tile k, so a tile's way along the chain (some
+// 1.5 us of stores and loads through L2) passes while they work.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kScanWarps * 32, kScanBlocks)
+__global__ void __launch_bounds__(kScanThreads, 1)
 scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
             float* __restrict__ states) {
-  constexpr int VEC = kVec<T>, W = kScanWarps, S = kScanSteps, C = 32 * VEC, threads = W * 32;
-  constexpr int NP = S * VEC / 2;
+  constexpr int VEC = kVec<T>, W = kScanWarps, S = kScanSteps, C = 32 * VEC, NP = S * VEC / 2;
+  constexpr int kWork = 32 * W;
   constexpr bool kOne = kBytes == 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  T* const buf = reinterpret_cast<T*>(smem);  // [2][r i x][kScanTile][C]
-  __shared__ float2 map_s[W][C];
-  __shared__ float in_s[C];
-  __shared__ uint32_t cut_s[W];
-  __shared__ Tile tile_s[2];
+  ScanShared<T>& sh = *reinterpret_cast<ScanShared<T>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  if (threadIdx.x == 0) tile_s[0] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) : blockIdx.x, false);
-  __syncthreads();
-  auto fetch = [&](const Tile& at, int k) {
+  // the chain's warp: the place and the decay parameters of the block's k-th tile
+  auto take = [&](int k) {
+    uint32_t t = 0;
+    if (lane == 0)
+      t = q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : k == 0 ? blockIdx.x : 0xffffffffu;
+    const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), false);
+    if (lane == 0) sh.tile[k % kRing] = at;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
+      sh.kz[k % kRing][lane * VEC + v] =
+          at.tile >= 0 && h < q.H ? -q.c * softplus(q.p[h]) * kLog2e : 0.0f;
+    }
+  };
+  if (warp == W) {
+    for (int k = 0; k < 3; ++k) take(k);
+    __syncthreads();
+    for (int k = 0;; ++k) {
+      const Tile at = sh.tile[k % kRing];
+      if (at.tile < 0) return;
+      take(k + 3);
+      bar_sync(kMapsBar + (k & 1), kScanThreads);
+      const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+      const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.HP + h;
+      const uint32_t cut = __ballot_sync(0xffffffffu, lane < W && sh.cut[k % 3][lane] != 0);
+      bool on[VEC];
+      float A[VEC], e[VEC], s[VEC], end[VEC];
+      float2 m[W][VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+        A[v] = 1.0f, e[v] = 0.0f;
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) m[w][v] = sh.map[k % 3][w][lane * VEC + v];
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          e[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, e[v], m[w][v].y);
+          A[v] *= m[w][v].x;
+        }
+      if (at.tile == 0)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
+      chain(q, at, row, 1, A, e, cut != 0, s, end);
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          sh.enter[k & 1][w][lane * VEC + v] = s[v];
+          const int64_t t = (int64_t)at.tile * kScanTile + w * S;
+          if (w * S % GLR_STATE_STEPS == 0 && states && t < q.L && on[v])
+            states[(at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t / GLR_STATE_STEPS) * q.H + h + v] =
+                s[v];
+          s[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, s[v], m[w][v].y);
+        }
+      if (at.tile == q.tiles - 1 && h_last)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          if (on[v]) h_last[at.b * q.H + h + v] = end[v];
+      bar_arrive(kEnterBar + (k & 1), kScanThreads);
+    }
+  }
+
+  auto fetch = [&](int k) {
+    const Tile at = sh.tile[k % kRing];
     if (at.tile >= 0) {
-      T* d = buf + k * 3 * kScanTile * C;
       const int64_t t0 = (int64_t)at.tile * kScanTile, c0 = (int64_t)at.group * C;
-      const int steps = (int)min((int64_t)kScanTile, q.L - t0);
-      stage<T, C, kBytes, threads>(d, q.r, at.b, t0, c0, steps, q.L, q.H);
-      stage<T, C, kBytes, threads>(d + kScanTile * C, q.i, at.b, t0, c0, steps, q.L, q.H);
-      stage<T, C, kBytes, threads>(d + 2 * kScanTile * C, q.x, at.b, t0, c0, steps, q.L, q.H);
+      auto& d = sh.buf[k & 1];
+      stage<T, C, kScanTile, kBytes, kWork>(&d[0][0][0], q.r, at.b, t0, c0, q.L, q.H);
+      stage<T, C, kScanTile, kBytes, kWork>(&d[1][0][0], q.i, at.b, t0, c0, q.L, q.H);
+      stage<T, C, kScanTile, kBytes, kWork>(&d[2][0][0], q.x, at.b, t0, c0, q.L, q.H);
     }
     copies_end();
   };
-  fetch(tile_s[0], 0);
-  for (int turn = 0;; turn ^= 1) {
-    const Tile at = tile_s[turn];
-    if (at.tile < 0) return;
-    uint32_t ticket = 0;
-    if (threadIdx.x == 0) {
-      ticket = q.tiles > 1 ? atomicAdd(q.head, 1u) : 0xffffffffu;
-      tile_s[turn ^ 1] = tile_of(q, ticket, false);
-    }
-    copies_wait();
-    __syncthreads();
-    fetch(tile_s[turn ^ 1], turn ^ 1);
-
-    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
-    const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
-    const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
-    const T* mine = buf + turn * 3 * kScanTile * C + warp * S * C + lane * VEC;
-    bool on[VEC];
-    float kz[VEC], A[VEC], e[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      on[v] = h + v < q.H && DLR_IN(at.b, q.B);
-      kz[v] = on[v] ? -q.c * softplus(q.p[h + v]) * kLog2e : 0.0f;
-      A[v] = 1.0f, e[v] = 0.0f;
-    }
-    const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);  // as n, the same for all of the warp
+  struct Part {  // what a warp has of a tile: its steps, how many there are, which begin a sequence
     float2 a[NP], b[NP];
+    int n;
+    uint32_t cut;
+  };
+  auto gates = [&](int k, Part& z) {
+    const Tile at = sh.tile[k % kRing];
+    if (at.tile < 0) return;
+    const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
+    z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
+    z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
+    const float2 kz = make_float2(sh.kz[k % kRing][lane * VEC], sh.kz[k % kRing][lane * VEC + VEC - 1]);
+    const T* r = &sh.buf[k & 1][0][warp * S][lane * VEC];
 #pragma unroll
     for (int m = 0; m < NP; ++m) {
-      const gate2 g = make_gate2(get2<T, VEC, C>(mine, m), get2<T, VEC, C>(mine + kScanTile * C, m),
-                                 make_float2(kz[0], kz[VEC - 1]));
-      a[m] = g.a;
-      b[m] = mul2(g.m, mul2(g.si, get2<T, VEC, C>(mine + 2 * kScanTile * C, m)));
+      const gate2 g = make_gate2(get2<T, VEC, C>(r, m), get2<T, VEC, C>(r + kScanTile * C, m), kz);
+      z.a[m] = g.a;
+      z.b[m] = mul2(g.m, mul2(g.si, get2<T, VEC, C>(r + 2 * kScanTile * C, m)));
     }
-    if (n < S) {
+    if (z.n < S) {
 #pragma unroll
       for (int j = 0; j < S; ++j)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          if (j >= n) half<VEC>(a, j, v) = 1.0f, half<VEC>(b, j, v) = 0.0f;
+          if (j >= z.n) half<VEC>(z.a, j, v) = 1.0f, half<VEC>(z.b, j, v) = 0.0f;
     }
+    float A[VEC], e[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f;
 #pragma unroll
     for (int m = 0; m < NP; ++m) {
       if constexpr (VEC == 2) {
-        A[0] *= a[m].x, A[1] *= a[m].y;
+        const float2 t = mul2(make_float2(A[0], A[1]), z.a[m]);
+        A[0] = t.x, A[1] = t.y;
       } else {
-        A[0] *= a[m].x * a[m].y;
+        A[0] *= z.a[m].x * z.a[m].y;
       }
     }
-    if (cut == 0) {
+    if (z.cut == 0) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) advance<VEC>(e, a, b, j);
+      for (int j = 0; j < S; ++j) advance<VEC>(e, z.a, z.b, j);
     } else {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        advance<VEC>(e, a, b, j);
+        advance<VEC>(e, z.a, z.b, j);
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          if ((cut >> j) & 1u) e[v] = half<VEC>(b, j, v);
+          if ((z.cut >> j) & 1u) e[v] = half<VEC>(z.b, j, v);
       }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
-    if (lane == 0) cut_s[warp] = cut;
-    __syncthreads();
-
-    if (warp == 0) {
-      float s[VEC], end[VEC];
-      bool any = false;
-      const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.H + h;
-#pragma unroll
-      for (int w = 1; w < W; ++w)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          const float2 m = map_s[w][lane * VEC + v];
-          e[v] = cut_s[w] ? m.y : fmaf(m.x, e[v], m.y);
-          A[v] *= m.x;
-        }
-#pragma unroll
-      for (int w = 0; w < W; ++w) any |= cut_s[w] != 0;
-      if (at.tile == 0)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
-      chain(q, at, row, 1, on, A, e, any, s, end);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        if (at.tile == q.tiles - 1 && h_last && on[v]) h_last[at.b * q.H + h + v] = end[v];
-        in_s[lane * VEC + v] = s[v];
-      }
-    }
-    __syncthreads();
-
+    for (int v = 0; v < VEC; ++v) sh.map[k % 3][warp][lane * VEC + v] = make_float2(A[v], e[v]);
+    if (lane == 0) sh.cut[k % 3][warp] = z.cut;
+    bar_arrive(kMapsBar + (k & 1), kScanThreads);
+  };
+  auto finish = [&](int k, Part& z) {
+    const Tile at = sh.tile[k % kRing];
+    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+    const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
+    bool on[VEC];
     float s[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) s[v] = in_s[lane * VEC + v];
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float2 m = map_s[w][lane * VEC + v];
-        s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
-      }
-    if (states && t0 % GLR_STATE_STEPS == 0 && n > 0)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v)
-        if (on[v])
-          states[(at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t0 / GLR_STATE_STEPS) * q.H + h + v] =
-              s[v];
+    for (int v = 0; v < VEC; ++v) {
+      on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+      s[v] = sh.enter[k & 1][warp][lane * VEC + v];
+    }
     T* yp = y.row(at.b, t0) + h;
-    if (n == S && cut == 0) {
+    if (z.n == S && z.cut == 0) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        advance<VEC>(s, a, b, j);
+        advance<VEC>(s, z.a, z.b, j);
         put<T, VEC, kOne>(yp, s, on);
         yp += y.st;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        advance<VEC>(s, a, b, j);
+        advance<VEC>(s, z.a, z.b, j);
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          if ((cut >> j) & 1u) s[v] = half<VEC>(b, j, v);
-        if (j < n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp, s, on);
+          if ((z.cut >> j) & 1u) s[v] = half<VEC>(z.b, j, v);
+        if (j < z.n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp, s, on);
         yp += y.st;
       }
     }
+  };
+  // tile k's gates are in `now`; true when it was the last
+  auto turn = [&](int k, Part& now, Part& next) {
+    gates(k + 1, next);
+    copies_wait();
+    bar_sync(kEnterBar + (k & 1), kScanThreads);
+    fetch(k + 3);
+    finish(k, now);
+    return sh.tile[(k + 1) % kRing].tile < 0;
+  };
+  Part z0, z1;
+  __syncthreads();
+  fetch(0);
+  fetch(1);
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  bar_sync(kWarpsBar, kWork);
+  gates(0, z0);
+  copies_wait();
+  bar_sync(kWarpsBar, kWork);
+  fetch(2);
+  for (int k = 0;; k += 2) {
+    if (turn(k, z0, z1)) return;
+    if (turn(k + 1, z1, z0)) return;
   }
 }
 
@@ -458,17 +572,16 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
   __shared__ Tile tile_s[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  if (threadIdx.x == 0) tile_s[0] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) : blockIdx.x, true);
+  if (threadIdx.x == 0) tile_s[0] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : blockIdx.x, true);
   __syncthreads();
   auto fetch = [&](const Tile& at, int k) {
     if (at.tile >= 0) {
       T* d = buf + k * 4 * kArray;
       const int64_t t0 = (int64_t)at.tile * kBackTile, c0 = (int64_t)at.group * C;
-      const int steps = (int)min((int64_t)kBackTile, q.L - t0);
-      stage<T, C, kBytes, threads>(d, q.r, at.b, t0, c0, steps, q.L, q.H);
-      stage<T, C, kBytes, threads>(d + kArray, q.i, at.b, t0, c0, steps, q.L, q.H);
-      stage<T, C, kBytes, threads>(d + 2 * kArray, q.x, at.b, t0, c0, steps, q.L, q.H);
-      stage<T, C, kBytes, threads>(d + 3 * kArray, dy, at.b, t0, c0, steps, q.L, q.H);
+      stage<T, C, kBackTile, kBytes, threads>(d, q.r, at.b, t0, c0, q.L, q.H);
+      stage<T, C, kBackTile, kBytes, threads>(d + kArray, q.i, at.b, t0, c0, q.L, q.H);
+      stage<T, C, kBackTile, kBytes, threads>(d + 2 * kArray, q.x, at.b, t0, c0, q.L, q.H);
+      stage<T, C, kBackTile, kBytes, threads>(d + 3 * kArray, dy, at.b, t0, c0, q.L, q.H);
     }
     copies_end();
   };
@@ -477,7 +590,7 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
     const Tile at = tile_s[turn];
     if (at.tile < 0) return;
     if (threadIdx.x == 0)
-      tile_s[turn ^ 1] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) : 0xffffffffu, true);
+      tile_s[turn ^ 1] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : 0xffffffffu, true);
     copies_wait();
     __syncthreads();
     fetch(tile_s[turn ^ 1], turn ^ 1);
@@ -565,7 +678,7 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           in[v] = dh_last && on[v] ? dh_last[at.b * q.H + h + v] : 0.0f;
-      chain(q, at, row, -1, on, tA, tC, any, in, end);
+      chain(q, at, ((int64_t)at.b * q.tiles + at.tile) * q.HP + h, -1, tA, tC, any, in, end);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         if (at.tile == 0 && dh0 && on[v]) dh0[at.b * q.H + h + v] = end[v];
@@ -728,18 +841,15 @@ view<T> out_view(const glr_out& v) {
   return {static_cast<T*>(v.data), v.stride_b, v.stride_t};
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Bytes of the parts of a workspace for tiles of `steps` steps: the chain's counter and flags (for
-// the narrowest groups, of 32 channels), the maps and the entering values.
+// Bytes of the parts of a workspace for tiles of `steps` steps, laid out one behind the other: the
+// head, the maps, the entering values.
 struct Space {
-  int64_t tiles;
+  int64_t tiles, HP;
   size_t head, maps, in;
-  Space(int64_t B, int64_t L, int64_t H, int64_t steps) : tiles(L < 1 ? 0 : (L - 1) / steps + 1) {
-    const size_t rows = (size_t)B * (size_t)tiles;
-    head = align256(4 * (kHead + rows * (size_t)((H + 31) / 32)));
-    maps = align256(sizeof(float2) * rows * (size_t)H);
-    in = align256(sizeof(float) * rows * (size_t)H);
+  Space(int64_t B, int64_t L, int64_t H, int64_t steps)
+      : tiles(L < 1 ? 0 : (L - 1) / steps + 1), HP((H + 63) / 64 * 64), head(4 * kHead) {
+    in = sizeof(float) * (size_t)B * (size_t)tiles * (size_t)HP;
+    maps = 2 * in;
   }
 };
 
@@ -755,15 +865,16 @@ Job<T> make_job(const A& a, const Space& sp) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int64_t groups = (a.H + 32 * kVec<T> - 1) / (32 * kVec<T>);
   return {in_view<T>(a.x), in_view<T>(a.r), in_view<T>(a.i), a.p, a.reset,
-          reinterpret_cast<float*>(ws + sp.head + sp.maps), reinterpret_cast<float2*>(ws + sp.head),
-          reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, a.B * groups,
+          reinterpret_cast<float*>(ws + sp.head + sp.maps), reinterpret_cast<float*>(ws + sp.head),
+          reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, sp.HP, a.B * groups,
           (int)groups, (int)sp.tiles, (float)a.c};
 }
 
 // Blocks for `tiles` tiles: what the GPU holds at once at most. A chain of one tile needs no
 // counter and takes a block for each.
 template <typename T>
-cudaError_t prepare_chain(const Job<T>& q, int per_sm, unsigned* blocks, cudaStream_t s) {
+cudaError_t prepare_chain(const Job<T>& q, const Space& sp, int per_sm, unsigned* blocks,
+                          cudaStream_t s) {
   const int64_t all = q.chains * q.tiles;
   *blocks = (unsigned)all;
   if (q.tiles == 1) return cudaSuccess;
@@ -772,19 +883,20 @@ cudaError_t prepare_chain(const Job<T>& q, int per_sm, unsigned* blocks, cudaStr
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   *blocks = (unsigned)std::min<int64_t>(all, (int64_t)sms * per_sm);
-  return cudaMemsetAsync(q.head, 0, 4 * (size_t)(kHead + all), s);
+  return cudaMemsetAsync(q.head, 0xff, sp.head + sp.maps + sp.in, s);
 }
 
 template <typename T, int kBytes>
 cudaError_t scan_w(const glr_scan_args& a, cudaStream_t s) {
-  constexpr size_t smem = 2 * 3 * kScanTile * 128;
-  const Job<T> q = make_job<T>(a, Space(a.B, a.L, a.H, kScanTile));
+  constexpr size_t smem = sizeof(ScanShared<T>);
+  const Space sp(a.B, a.L, a.H, kScanTile);
+  const Job<T> q = make_job<T>(a, sp);
   unsigned blocks;
-  cudaError_t e = prepare_chain(q, kScanBlocks, &blocks, s);
+  cudaError_t e = prepare_chain(q, sp, 1, &blocks, s);
   if (e == cudaSuccess) e = max_smem_once<scan_kernel<T, kBytes>>(smem);
   if (e != cudaSuccess) return e;
-  scan_kernel<T, kBytes><<<blocks, kScanWarps * 32, smem, s>>>(q, out_view<T>(a.y), a.h0, a.h_last,
-                                                               a.states);
+  scan_kernel<T, kBytes><<<blocks, kScanThreads, smem, s>>>(q, out_view<T>(a.y), a.h0, a.h_last,
+                                                            a.states);
   return cudaGetLastError();
 }
 
@@ -796,7 +908,7 @@ cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.head + sp.maps +
                                          sp.in);
   unsigned blocks;
-  cudaError_t e = prepare_chain(q, kBackBlocks, &blocks, s);
+  cudaError_t e = prepare_chain(q, sp, kBackBlocks, &blocks, s);
   if (e == cudaSuccess) e = max_smem_once<back_kernel<T, kBytes>>(smem);
   if (e != cudaSuccess) return e;
   back_kernel<T, kBytes><<<blocks, kBackWarps * 32, smem, s>>>(
@@ -847,7 +959,7 @@ size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H) {
 }
 size_t scan_backward_workspace_bytes(int64_t B, int64_t L, int64_t H) {
   const Space sp(B, L, H, kBackTile);
-  return sp.head + sp.maps + 2 * sp.in;
+  return sp.head + sp.maps + 2 * sp.in;  // and the parts of dp
 }
 // tiles (which a 32-bit counter hands out) of the finest cut that a call of this size takes
 int64_t scan_tiles(int64_t B, int64_t L, int64_t H) {
