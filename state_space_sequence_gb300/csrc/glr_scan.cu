@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "glr_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace dlr {
 // source file number of the bounds-checked build's failing sites
@@ -324,14 +325,14 @@ template <typename T>
 constexpr int kVec = 4 / (int)sizeof(T);
 
 constexpr int kScanSteps = 8;                        // of a warp
-constexpr int kScanWarps = 16;                       // that compute; one more keeps the chain
+constexpr int kScanWarps = 14;                       // that compute; two more serve them
 constexpr int kScanTile = kScanSteps * kScanWarps;   // steps
-constexpr int kScanThreads = 32 * (kScanWarps + 1);
+constexpr int kScanThreads = 32 * (kScanWarps + 2);
 constexpr int kRing = 8;                             // tiles whose places a block remembers
 
 // Named barriers of a block, two of each kind for even and odd tiles: the maps of a tile are in shared
 // memory (the computing warps arrive, the chain's warp waits); the values that enter its
-// warps are there (the other way round); and one for the computing warps alone.
+// warps are there (the chain's warp arrives, all others wait); and two for the beginning.
 constexpr int kMapsBar = 1, kEnterBar = 3, kWarpsBar = 5;
 
 template <typename T>
@@ -343,47 +344,95 @@ struct ScanShared {
   float kz[kRing][C];
   uint32_t cut[3][kScanWarps];
   Tile tile[kRing];
+  uint64_t here[2];                 // barriers of the buffers' copies
 };
 
-// The last warp keeps the chain; the others compute, one tile ahead of it: they have the gates of
-// tile k + 1 done before they need the state that enters tile k, so a tile's way along the chain (some
-// 1.5 us of stores and loads through L2) passes while they work.
+// The supplying warp's part of a block: it takes the tiles and, where rows allow 16-byte copies, has
+// their inputs copied (a bulk copy for each row of 128 bytes); the rows and channels that a tile has
+// past the ends are not written.
+template <typename T, int kTile, int kArrays>
+__device__ __forceinline__ void bulk_tile(T (&dst)[kArrays][kTile][32 * kVec<T>], uint64_t* here,
+                                          const view<const T> (&v)[kArrays], const Tile& at,
+                                          int64_t L, int64_t H) {
+  constexpr int C = 32 * kVec<T>;
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = (int64_t)at.tile * kTile, c0 = (int64_t)at.group * C;
+  const int rows = (int)min((int64_t)kTile, L - t0);
+  const uint32_t bytes = (uint32_t)min((int64_t)C, H - c0) * (uint32_t)sizeof(T);
+  if (lane == 0) tc::mbar_arrive_expect_tx(here, bytes * rows * kArrays);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < kArrays; ++k) {
+    const T* p = v[k].row(at.b, t0 + lane) + c0;
+    const int64_t dp = 32 * v[k].st;
+    for (int j = lane; j < rows; j += 32, p += dp) tc::bulk_load(&dst[k][j][0], p, bytes, here);
+  }
+}
+
+// One warp keeps the chain and one supplies the tiles; the others compute, one tile ahead of the
+// chain: they have the gates of tile k + 1 done before they need the state that enters tile k, so a
+// tile's way along the chain (stores and loads through L2) passes while they work.
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(kScanThreads, 1)
 scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
             float* __restrict__ states) {
   constexpr int VEC = kVec<T>, W = kScanWarps, S = kScanSteps, C = 32 * VEC, NP = S * VEC / 2;
   constexpr int kWork = 32 * W;
-  constexpr bool kOne = kBytes == 2;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr bool kOne = kBytes == 2, kBulk = false;
+  extern __shared__ __align__(128) uint8_t smem[];
   ScanShared<T>& sh = *reinterpret_cast<ScanShared<T>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  // the chain's warp: the place and the decay parameters of the block's k-th tile
-  auto take = [&](int k) {
-    uint32_t t = 0;
-    if (lane == 0)
-      t = q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : k == 0 ? blockIdx.x : 0xffffffffu;
-    const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), false);
-    if (lane == 0) sh.tile[k % kRing] = at;
+  if (warp == W + 1) {
+    auto take = [&](int k) {  // the place and the decay parameters of the block's k-th tile
+      uint32_t t = 0;
+      if (lane == 0)
+        t = q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : k == 0 ? blockIdx.x : 0xffffffffu;
+      const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), false);
+      if (lane == 0) sh.tile[k % kRing] = at;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
-      sh.kz[k % kRing][lane * VEC + v] =
-          at.tile >= 0 && h < q.H ? -q.c * softplus(q.p[h]) * kLog2e : 0.0f;
+      for (int v = 0; v < VEC; ++v) {
+        const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
+        sh.kz[k % kRing][lane * VEC + v] =
+            at.tile >= 0 && h < q.H ? -q.c * softplus(q.p[h]) * kLog2e : 0.0f;
+      }
+      __syncwarp();
+    };
+    auto copy = [&](int k) {
+      if constexpr (kBulk) {
+        const Tile at = sh.tile[k % kRing];
+        const view<const T> in[3] = {q.r, q.i, q.x};
+        if (at.tile >= 0)
+          bulk_tile<T, kScanTile, 3>(sh.buf[k & 1], &sh.here[k & 1], in, at, q.L, q.H);
+      }
+    };
+    if (lane == 0) {
+      tc::mbar_init(&sh.here[0], 1);
+      tc::mbar_init(&sh.here[1], 1);
+      tc::mbar_fence_init();
     }
-  };
-  if (warp == W) {
     for (int k = 0; k < 3; ++k) take(k);
+    copy(0);
+    copy(1);
+    __syncthreads();
+    bar_sync(kWarpsBar, kWork + 32);
+    copy(2);
+    for (int k = 0; sh.tile[k % kRing].tile >= 0; ++k) {
+      take(k + 3);
+      bar_sync(kEnterBar + (k & 1), kScanThreads);
+      copy(k + 3);
+    }
+    return;
+  }
+  if (warp == W) {
     __syncthreads();
     for (int k = 0;; ++k) {
+      bar_sync(kMapsBar + (k & 1), kWork + 32);
       const Tile at = sh.tile[k % kRing];
       if (at.tile < 0) return;
-      take(k + 3);
-      bar_sync(kMapsBar + (k & 1), kScanThreads);
       const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
       const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.HP + h;
-      const uint32_t cut = __ballot_sync(0xffffffffu, lane < W && sh.cut[k % 3][lane] != 0);
+      const uint32_t cut = __ballot_sync(0xffffffffu, lane < W && sh.cut[k % 3][lane % W] != 0);
       bool on[VEC];
       float A[VEC], e[VEC], s[VEC], end[VEC];
       float2 m[W][VEC];
@@ -407,35 +456,44 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
       chain(q, at, row, 1, A, e, cut != 0, s, end);
+      float enter[W][VEC];
 #pragma unroll
       for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-          sh.enter[k & 1][w][lane * VEC + v] = s[v];
-          const int64_t t = (int64_t)at.tile * kScanTile + w * S;
-          if (w * S % GLR_STATE_STEPS == 0 && states && t < q.L && on[v])
-            states[(at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t / GLR_STATE_STEPS) * q.H + h + v] =
-                s[v];
+          sh.enter[k & 1][w][lane * VEC + v] = enter[w][v] = s[v];
           s[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, s[v], m[w][v].y);
+        }
+      bar_arrive(kEnterBar + (k & 1), kScanThreads);
+      if (states)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int64_t t = (int64_t)at.tile * kScanTile + w * S;
+          if (t % GLR_STATE_STEPS != 0 || t >= q.L) continue;
+          const int64_t to = (at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t / GLR_STATE_STEPS) * q.H;
+#pragma unroll
+          for (int v = 0; v < VEC; ++v)
+            if (on[v]) states[to + h + v] = enter[w][v];
         }
       if (at.tile == q.tiles - 1 && h_last)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           if (on[v]) h_last[at.b * q.H + h + v] = end[v];
-      bar_arrive(kEnterBar + (k & 1), kScanThreads);
     }
   }
 
   auto fetch = [&](int k) {
-    const Tile at = sh.tile[k % kRing];
-    if (at.tile >= 0) {
-      const int64_t t0 = (int64_t)at.tile * kScanTile, c0 = (int64_t)at.group * C;
-      auto& d = sh.buf[k & 1];
-      stage<T, C, kScanTile, kBytes, kWork>(&d[0][0][0], q.r, at.b, t0, c0, q.L, q.H);
-      stage<T, C, kScanTile, kBytes, kWork>(&d[1][0][0], q.i, at.b, t0, c0, q.L, q.H);
-      stage<T, C, kScanTile, kBytes, kWork>(&d[2][0][0], q.x, at.b, t0, c0, q.L, q.H);
+    if constexpr (!kBulk) {
+      const Tile at = sh.tile[k % kRing];
+      if (at.tile >= 0) {
+        const int64_t t0 = (int64_t)at.tile * kScanTile, c0 = (int64_t)at.group * C;
+        auto& d = sh.buf[k & 1];
+        stage<T, C, kScanTile, kBytes, kWork>(&d[0][0][0], q.r, at.b, t0, c0, q.L, q.H);
+        stage<T, C, kScanTile, kBytes, kWork>(&d[1][0][0], q.i, at.b, t0, c0, q.L, q.H);
+        stage<T, C, kScanTile, kBytes, kWork>(&d[2][0][0], q.x, at.b, t0, c0, q.L, q.H);
+      }
+      copies_end();
     }
-    copies_end();
   };
   struct Part {  // what a warp has of a tile: its steps, how many there are, which begin a sequence
     float2 a[NP], b[NP];
@@ -444,12 +502,17 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
   };
   auto gates = [&](int k, Part& z) {
     const Tile at = sh.tile[k % kRing];
-    if (at.tile < 0) return;
+    if (at.tile < 0) {
+      bar_arrive(kMapsBar + (k & 1), kWork + 32);
+      return;
+    }
     const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
     z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
     const float2 kz = make_float2(sh.kz[k % kRing][lane * VEC], sh.kz[k % kRing][lane * VEC + VEC - 1]);
     const T* r = &sh.buf[k & 1][0][warp * S][lane * VEC];
+    if (kBulk && !tc::mbar_wait_sleep(&sh.here[k & 1], (k >> 1) & 1) && lane == 0)
+      report_status(q.status, DLR_ERR_TIMEOUT);
 #pragma unroll
     for (int m = 0; m < NP; ++m) {
       const gate2 g = make_gate2(get2<T, VEC, C>(r, m), get2<T, VEC, C>(r + kScanTile * C, m), kz);
@@ -490,7 +553,7 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
 #pragma unroll
     for (int v = 0; v < VEC; ++v) sh.map[k % 3][warp][lane * VEC + v] = make_float2(A[v], e[v]);
     if (lane == 0) sh.cut[k % 3][warp] = z.cut;
-    bar_arrive(kMapsBar + (k & 1), kScanThreads);
+    bar_arrive(kMapsBar + (k & 1), kWork + 32);
   };
   auto finish = [&](int k, Part& z) {
     const Tile at = sh.tile[k % kRing];
@@ -526,7 +589,7 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
   // tile k's gates are in `now`; true when it was the last
   auto turn = [&](int k, Part& now, Part& next) {
     gates(k + 1, next);
-    copies_wait();
+    if (!kBulk) copies_wait();
     bar_sync(kEnterBar + (k & 1), kScanThreads);
     fetch(k + 3);
     finish(k, now);
@@ -535,12 +598,14 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
   Part z0, z1;
   __syncthreads();
   fetch(0);
+  if (!kBulk) {
+    copies_wait();
+    bar_sync(kWarpsBar + 1, kWork);
+  }
   fetch(1);
-  asm volatile("cp.async.wait_group 1;" ::: "memory");
-  bar_sync(kWarpsBar, kWork);
   gates(0, z0);
-  copies_wait();
-  bar_sync(kWarpsBar, kWork);
+  if (!kBulk) copies_wait();
+  bar_sync(kWarpsBar, kWork + 32);
   fetch(2);
   for (int k = 0;; k += 2) {
     if (turn(k, z0, z1)) return;
