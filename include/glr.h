@@ -50,7 +50,7 @@ typedef struct {
 } glr_out;
 
 /* Steps between the states that glr_scan keeps for its gradients. */
-#define GLR_STATE_STEPS 64
+#define GLR_STATE_STEPS 8
 
 /*
  * glr_scan -- the gated linear recurrence over x [B, L, H] with the recurrence gate r and the

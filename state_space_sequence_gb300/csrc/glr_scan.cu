@@ -15,6 +15,7 @@
 // always formed in the same order (each from the one before it), so the results do not depend on
 // which of them a tile found. A tile that begins a sequence knows its end from its own steps.
 #include <algorithm>
+#include <type_traits>
 
 #include "glr_common.cuh"
 #include "tc_ptx.cuh"
@@ -91,7 +92,20 @@ struct Job {
   int* status;
   int64_t B, L, H, HP, chains;
   int groups, tiles;
+  int most;  // tiles that a block takes at most
   float c;
+
+  // the k-th tile of this block; called by one thread
+  __device__ __forceinline__ uint32_t ticket(int k) const {
+    if (tiles == 1) return k == 0 ? blockIdx.x : 0xffffffffu;
+    return k < most ? atomicAdd(head, 1u) + 1u : 0xffffffffu;
+  }
+};
+
+// Descriptions of arrays [B, L, H] for the tensor copies.
+template <int N>
+struct Maps {
+  CUtensorMap map[N];
 };
 
 struct Tile {
@@ -209,8 +223,8 @@ __device__ __forceinline__ uint32_t cuts(const uint8_t* reset, int64_t first, in
 
 // A decay in one register with its digits both next to 1 and next to 0: a - 1 (negative; -0 for
 // a = 1) where a > 1/2, else a.
-__device__ __forceinline__ float2 keep_decay(const gate2& g) {
-  return make_float2(g.a.x > 0.5f ? -g.rest.x : g.a.x, g.a.y > 0.5f ? -g.rest.y : g.a.y);
+__device__ __forceinline__ float2 keep_decay(float2 a, float2 rest) {
+  return make_float2(a.x > 0.5f ? -rest.x : a.x, a.y > 0.5f ? -rest.y : a.y);
 }
 __device__ __forceinline__ float2 sign_ones(float2 k) {
   return make_float2(__float_as_int(k.x) < 0 ? 1.0f : 0.0f, __float_as_int(k.y) < 0 ? 1.0f : 0.0f);
@@ -249,19 +263,18 @@ __device__ __forceinline__ void advance(float (&s)[VEC], float2 (&a)[N], float2 
   }
 }
 
-// How a tile's inputs come into shared memory: by asynchronous copies of 16 bytes where every row
-// begins on a 16-byte boundary and H is a whole number of them, of 4 bytes where the same holds for 4,
-// else (16-bit types with odd strides) by loads of single elements.
-template <int kBytes>
+// How a tile's inputs come into shared memory and its outputs leave it. Where every row begins on a
+// 16-byte boundary and H is a whole number of 16 bytes (kTma) one thread has a whole tile moved by a tensor
+// copy, which also fills what a tile has past the ends with zeros and leaves it out on the way back.
+// Else the computing warps copy 4 bytes at a time where rows begin on 4-byte boundaries, single elements
+// where not even that holds (16-bit types with odd strides), and store for themselves.
+constexpr int kTma = 16;
+
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  const int n = on ? kBytes : 0;  // nothing is read and zeros are written where off
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n)
-                 : "memory");
+  const int n = on ? 4 : 0;  // nothing is read and zeros are written where off
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n)
+               : "memory");
 }
 __device__ __forceinline__ void copies_end() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -283,7 +296,7 @@ __device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b,
   dst += first * C + col;
   if (kBytes != 2 && t0 + kSteps <= L && h0 + C <= H) {
 #pragma unroll
-    for (int j = 0; j < kSteps; j += rows, p += dp) copy_async<kBytes>(dst + j * C, p, true);
+    for (int j = 0; j < kSteps; j += rows, p += dp) copy_async(dst + j * C, p, true);
     return;
   }
   const bool in = h0 + col < H;
@@ -293,7 +306,7 @@ __device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b,
     if constexpr (kBytes == 2)
       dst[j * C] = on ? *p : from_f<T>(0.0f);
     else
-      copy_async<kBytes>(dst + j * C, on ? p : v.p, on);
+      copy_async(dst + j * C, on ? p : v.p, on);
   }
 }
 
@@ -339,6 +352,7 @@ template <typename T>
 struct ScanShared {
   static constexpr int C = 32 * kVec<T>;
   T buf[2][3][kScanTile][C];        // r, i, x of two tiles
+  T out[kScanTile][C];
   float2 map[3][kScanWarps][C];     // (A, e) of each warp's steps
   float enter[2][kScanWarps][C];    // the state that enters them
   float kz[kRing][C];
@@ -347,47 +361,24 @@ struct ScanShared {
   uint64_t here[2];                 // barriers of the buffers' copies
 };
 
-// The supplying warp's part of a block: it takes the tiles and, where rows allow 16-byte copies, has
-// their inputs copied (a bulk copy for each row of 128 bytes); the rows and channels that a tile has
-// past the ends are not written.
-template <typename T, int kTile, int kArrays>
-__device__ __forceinline__ void bulk_tile(T (&dst)[kArrays][kTile][32 * kVec<T>], uint64_t* here,
-                                          const view<const T> (&v)[kArrays], const Tile& at,
-                                          int64_t L, int64_t H) {
-  constexpr int C = 32 * kVec<T>;
-  const int lane = threadIdx.x & 31;
-  const int64_t t0 = (int64_t)at.tile * kTile, c0 = (int64_t)at.group * C;
-  const int rows = (int)min((int64_t)kTile, L - t0);
-  const uint32_t bytes = (uint32_t)min((int64_t)C, H - c0) * (uint32_t)sizeof(T);
-  if (lane == 0) tc::mbar_arrive_expect_tx(here, bytes * rows * kArrays);
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < kArrays; ++k) {
-    const T* p = v[k].row(at.b, t0 + lane) + c0;
-    const int64_t dp = 32 * v[k].st;
-    for (int j = lane; j < rows; j += 32, p += dp) tc::bulk_load(&dst[k][j][0], p, bytes, here);
-  }
-}
-
 // One warp keeps the chain and one supplies the tiles; the others compute, one tile ahead of the
 // chain: they have the gates of tile k + 1 done before they need the state that enters tile k, so a
 // tile's way along the chain (stores and loads through L2) passes while they work.
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(kScanThreads, 1)
-scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
+scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant__ Maps<1> out,
+            view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
             float* __restrict__ states) {
   constexpr int VEC = kVec<T>, W = kScanWarps, S = kScanSteps, C = 32 * VEC, NP = S * VEC / 2;
   constexpr int kWork = 32 * W;
-  constexpr bool kOne = kBytes == 2, kBulk = false;
+  constexpr bool kOne = kBytes == 2, kBulk = kBytes == kTma;
   extern __shared__ __align__(128) uint8_t smem[];
   ScanShared<T>& sh = *reinterpret_cast<ScanShared<T>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   if (warp == W + 1) {
     auto take = [&](int k) {  // the place and the decay parameters of the block's k-th tile
-      uint32_t t = 0;
-      if (lane == 0)
-        t = q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : k == 0 ? blockIdx.x : 0xffffffffu;
+      const uint32_t t = lane == 0 ? q.ticket(k) : 0u;
       const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), false);
       if (lane == 0) sh.tile[k % kRing] = at;
 #pragma unroll
@@ -399,12 +390,13 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
       __syncwarp();
     };
     auto copy = [&](int k) {
-      if constexpr (kBulk) {
-        const Tile at = sh.tile[k % kRing];
-        const view<const T> in[3] = {q.r, q.i, q.x};
-        if (at.tile >= 0)
-          bulk_tile<T, kScanTile, 3>(sh.buf[k & 1], &sh.here[k & 1], in, at, q.L, q.H);
-      }
+      const Tile at = sh.tile[k % kRing];
+      if (!kBulk || at.tile < 0 || lane != 0) return;
+      tc::mbar_arrive_expect_tx(&sh.here[k & 1], sizeof(sh.buf[0]));
+#pragma unroll
+      for (int a = 0; a < 3; ++a)
+        tc::tma_load_3d(&sh.buf[k & 1][a][0][0], &in.map[a], at.group * C, at.tile * kScanTile, at.b,
+                        &sh.here[k & 1]);
     };
     if (lane == 0) {
       tc::mbar_init(&sh.here[0], 1);
@@ -456,25 +448,14 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
       chain(q, at, row, 1, A, e, cut != 0, s, end);
-      float enter[W][VEC];
 #pragma unroll
       for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-          sh.enter[k & 1][w][lane * VEC + v] = enter[w][v] = s[v];
+          sh.enter[k & 1][w][lane * VEC + v] = s[v];
           s[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, s[v], m[w][v].y);
         }
       bar_arrive(kEnterBar + (k & 1), kScanThreads);
-      if (states)
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const int64_t t = (int64_t)at.tile * kScanTile + w * S;
-          if (t % GLR_STATE_STEPS != 0 || t >= q.L) continue;
-          const int64_t to = (at.b * ((q.L - 1) / GLR_STATE_STEPS + 1) + t / GLR_STATE_STEPS) * q.H;
-#pragma unroll
-          for (int v = 0; v < VEC; ++v)
-            if (on[v]) states[to + h + v] = enter[w][v];
-        }
       if (at.tile == q.tiles - 1 && h_last)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
@@ -566,13 +547,25 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
       on[v] = h + v < q.H && DLR_IN(at.b, q.B);
       s[v] = sh.enter[k & 1][warp][lane * VEC + v];
     }
-    T* yp = y.row(at.b, t0) + h;
-    if (z.n == S && z.cut == 0) {
+    if (states && z.n > 0) {
+      float* to = states + (at.b * ((q.L - 1) / S + 1) + t0 / S) * q.H + h;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+        if (on[v]) to[v] = s[v];
+    }
+    T* yp = kBulk ? &sh.out[warp * S][lane * VEC] : y.row(at.b, t0) + h;
+    const int64_t st = kBulk ? C : y.st;
+    if (kBulk) {
+      if (lane == 0) tc::bulk_wait_group_read0();  // the last tile's have left
+      __syncwarp();
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) on[v] = true;
+    }
+    if (z.cut == 0 && (kBulk || z.n == S)) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
         advance<VEC>(s, z.a, z.b, j);
-        put<T, VEC, kOne>(yp, s, on);
-        yp += y.st;
+        put<T, VEC, kOne>(yp + j * st, s, on);
       }
     } else {
 #pragma unroll
@@ -581,8 +574,15 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           if ((z.cut >> j) & 1u) s[v] = half<VEC>(z.b, j, v);
-        if (j < z.n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp, s, on);
-        yp += y.st;
+        if (j < z.n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp + j * st, s, on);
+      }
+    }
+    if (kBulk && z.n > 0) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::tma_store_3d(&out.map[0], &sh.out[warp * S][0], at.group * C, (int)t0, at.b);
+        tc::bulk_commit_group();
       }
     }
   };
@@ -593,7 +593,9 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
     bar_sync(kEnterBar + (k & 1), kScanThreads);
     fetch(k + 3);
     finish(k, now);
-    return sh.tile[(k + 1) % kRing].tile < 0;
+    const bool last = sh.tile[(k + 1) % kRing].tile < 0;
+    if (kBulk && last && lane == 0) tc::bulk_wait_group0();
+    return last;
   };
   Part z0, z1;
   __syncthreads();
@@ -606,6 +608,7 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
   gates(0, z0);
   if (!kBulk) copies_wait();
   bar_sync(kWarpsBar, kWork + 32);
+  if (sh.tile[0].tile < 0) return;
   fetch(2);
   for (int k = 0;; k += 2) {
     if (turn(k, z0, z1)) return;
@@ -614,217 +617,318 @@ scan_kernel(Job<T> q, view<T> y, const float* __restrict__ h0, float* __restrict
 }
 
 constexpr int kBackSteps = 8;
-constexpr int kBackWarps = 8;
+constexpr int kBackWarps = 14;
 constexpr int kBackTile = kBackSteps * kBackWarps;
-constexpr int kBackBlocks = 2;
-static_assert(kBackTile == GLR_STATE_STEPS, "a tile begins at a kept state");
+constexpr int kBackThreads = 32 * (kBackWarps + 2);
+static_assert(kBackSteps == GLR_STATE_STEPS && kScanSteps == GLR_STATE_STEPS,
+              "the forward pass keeps the state that enters a warp's steps");
 
+template <typename T>
+struct BackShared {
+  static constexpr int C = 32 * kVec<T>;
+  T rd[4][2][kBackTile][C];         // r, dy of four tiles; r's place takes dr
+  T ix[2][2][kBackTile][C];         // i, x of two; they take di, dx
+  float2 map[3][kBackWarps][C];     // (A, C) of each warp's steps
+  float enter[2][kBackWarps][C];    // the gradient that enters behind them
+  float sum[2][kBackWarps][C];      // their parts of dp
+  float k[kRing][C];                // c softplus(p)
+  uint32_t cut[3][kBackWarps];
+  Tile tile[kRing];
+  uint64_t rd_here[4], ix_here[2];  // barriers of the buffers' copies
+};
+
+// As scan_kernel, backwards. One tile ahead of the chain the computing warps need r and dy only (a
+// tile's map is made of the decays and dy), which come three tiles ahead; i and x come one ahead.
+// With what enters known, a warp first goes back over its steps for G, then forwards from the
+// kept state, so that each step's state is at hand when its gradients are formed: nothing is
+// computed twice but sigmoid(r), and only the decays and G stay in registers.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kBackWarps * 32, kBackBlocks)
-back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
-            const float* __restrict__ dh_last, view<T> dx, view<T> dr, view<T> di,
-            float* __restrict__ dh0, float* __restrict__ part) {
-  constexpr int VEC = kVec<T>, W = kBackWarps, S = kBackSteps, C = 32 * VEC, threads = W * 32;
-  constexpr int NP = S * VEC / 2;
-  constexpr int kArray = kBackTile * C;
-  constexpr bool kOne = kBytes == 2;
-  extern __shared__ __align__(16) uint8_t smem[];
-  T* const buf = reinterpret_cast<T*>(smem);  // [2][r i x dy][kBackTile][C]
-  __shared__ float2 map_s[W][C];  // (A, e) of each warp's steps
-  __shared__ float back_s[W][C];  // and C; at the end of a tile the warps' sums for dp
-  __shared__ float in_s[C];
-  __shared__ uint32_t cut_s[W];
-  __shared__ Tile tile_s[2];
+__global__ void __launch_bounds__(kBackThreads, 1)
+back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant__ Maps<3> out,
+            view<const T> dy, const float* __restrict__ states, const float* __restrict__ dh_last,
+            view<T> dx, view<T> dr, view<T> di, float* __restrict__ dh0, float* __restrict__ part) {
+  constexpr int VEC = kVec<T>, W = kBackWarps, S = kBackSteps, C = 32 * VEC, NP = S * VEC / 2;
+  constexpr int kWork = 32 * W;
+  constexpr bool kOne = kBytes == 2, kBulk = kBytes == kTma;
+  extern __shared__ __align__(128) uint8_t smem[];
+  BackShared<T>& sh = *reinterpret_cast<BackShared<T>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  if (threadIdx.x == 0) tile_s[0] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : blockIdx.x, true);
-  __syncthreads();
-  auto fetch = [&](const Tile& at, int k) {
-    if (at.tile >= 0) {
-      T* d = buf + k * 4 * kArray;
-      const int64_t t0 = (int64_t)at.tile * kBackTile, c0 = (int64_t)at.group * C;
-      stage<T, C, kBackTile, kBytes, threads>(d, q.r, at.b, t0, c0, q.L, q.H);
-      stage<T, C, kBackTile, kBytes, threads>(d + kArray, q.i, at.b, t0, c0, q.L, q.H);
-      stage<T, C, kBackTile, kBytes, threads>(d + 2 * kArray, q.x, at.b, t0, c0, q.L, q.H);
-      stage<T, C, kBackTile, kBytes, threads>(d + 3 * kArray, dy, at.b, t0, c0, q.L, q.H);
-    }
-    copies_end();
-  };
-  fetch(tile_s[0], 0);
-  for (int turn = 0;; turn ^= 1) {
-    const Tile at = tile_s[turn];
-    if (at.tile < 0) return;
-    if (threadIdx.x == 0)
-      tile_s[turn ^ 1] = tile_of(q, q.tiles > 1 ? atomicAdd(q.head, 1u) + 1u : 0xffffffffu, true);
-    copies_wait();
-    __syncthreads();
-    fetch(tile_s[turn ^ 1], turn ^ 1);
-
-    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
-    const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
-    const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.H + h;
-    const int n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
-    const T* mine = buf + turn * 4 * kArray + warp * S * C + lane * VEC;
-    auto raw = [&](int array, int m) { return get2<T, VEC, C>(mine + array * kArray, m); };
-    bool on[VEC];
-    float k[VEC], s[VEC];
+  if (warp == W + 1) {
+    auto take = [&](int k) {  // the place and the decay parameters of the block's k-th tile
+      const uint32_t t = lane == 0 ? q.ticket(k) : 0u;
+      const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), true);
+      if (lane == 0) sh.tile[k % kRing] = at;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      on[v] = h + v < q.H && DLR_IN(at.b, q.B);
-      k[v] = on[v] ? q.c * softplus(q.p[h + v]) : 0.0f;
-      s[v] = on[v] ? states[row + v] : 0.0f;
+      for (int v = 0; v < VEC; ++v) {
+        const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
+        sh.k[k % kRing][lane * VEC + v] = at.tile >= 0 && h < q.H ? q.c * softplus(q.p[h]) : 0.0f;
+      }
+      __syncwarp();
+    };
+    auto copy = [&](T* dst, uint64_t* here, int first, int k) {
+      const Tile at = sh.tile[k % kRing];
+      if (!kBulk || at.tile < 0 || lane != 0) return;
+      tc::mbar_arrive_expect_tx(here, 2 * kBackTile * 128);
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+        tc::tma_load_3d(dst + a * kBackTile * C, &in.map[first + a], at.group * C, at.tile * kBackTile, at.b,
+                        here);
+    };
+    auto copy_rd = [&](int k) { copy(&sh.rd[k & 3][0][0][0], &sh.rd_here[k & 3], 0, k); };
+    auto copy_ix = [&](int k) { copy(&sh.ix[k & 1][0][0][0], &sh.ix_here[k & 1], 2, k); };
+    // the parts of dp of the block's k-th tile
+    auto sums = [&](int k) {
+      const Tile at = sh.tile[k % kRing];
+      const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) t += sh.sum[k & 1][w][lane * VEC + v];
+        if (h + v < q.H && DLR_IN(at.b, q.B))
+          part[((int64_t)at.b * q.tiles + at.tile) * q.H + h + v] = t;
+      }
+    };
+    if (lane == 0) {
+      for (int k = 0; k < 4; ++k) tc::mbar_init(&sh.rd_here[k], 1);
+      for (int k = 0; k < 2; ++k) tc::mbar_init(&sh.ix_here[k], 1);
+      tc::mbar_fence_init();
     }
-    const uint32_t cut = cuts(q.reset, at.b * q.L + t0, n);
-    const float2 k2 = make_float2(k[0], k[VEC - 1]), kz = mul2(k2, two(-kLog2e));
-    // the decay (see keep_decay), and b, in whose place the state before the step comes later
-    float2 ka[NP], hb[NP];
-    float A[VEC], e[VEC], G[VEC];
+    for (int k = 0; k < 3; ++k) {
+      take(k);
+      copy_rd(k);
+    }
+    copy_ix(0);
+    __syncthreads();
+    int k = 0;
+    for (; sh.tile[k % kRing].tile >= 0; ++k) {
+      take(k + 3);
+      bar_sync(kEnterBar + (k & 1), kBackThreads);  // all warps are done with tile k - 1
+      copy_rd(k + 3);
+      copy_ix(k + 1);
+      if (k > 0) sums(k - 1);
+    }
+    bar_sync(kWarpsBar, kWork + 32);
+    if (k > 0) sums(k - 1);
+    return;
+  }
+  if (warp == W) {
+    __syncthreads();
+    for (int k = 0;; ++k) {
+      bar_sync(kMapsBar + (k & 1), kWork + 32);
+      const Tile at = sh.tile[k % kRing];
+      if (at.tile < 0) return;
+      const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+      const int64_t row = ((int64_t)at.b * q.tiles + at.tile) * q.HP + h;
+      const uint32_t cut = __ballot_sync(0xffffffffu, lane < W && sh.cut[k % 3][lane % W] != 0);
+      bool on[VEC];
+      float A[VEC], e[VEC], s[VEC], end[VEC];
+      float2 m[W][VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+        A[v] = 1.0f, e[v] = 0.0f;
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) m[w][v] = sh.map[k % 3][w][lane * VEC + v];
+#pragma unroll
+      for (int w = W - 1; w >= 0; --w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          e[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, e[v], m[w][v].y);
+          A[v] *= m[w][v].x;
+        }
+      if (at.tile == q.tiles - 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          s[v] = dh_last && on[v] ? dh_last[at.b * q.H + h + v] : 0.0f;
+      chain(q, at, row, -1, A, e, cut != 0, s, end);
+#pragma unroll
+      for (int w = W - 1; w >= 0; --w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          sh.enter[k & 1][w][lane * VEC + v] = s[v];
+          s[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, s[v], m[w][v].y);
+        }
+      bar_arrive(kEnterBar + (k & 1), kBackThreads);
+      if (at.tile == 0 && dh0)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          if (on[v]) dh0[at.b * q.H + h + v] = end[v];
+    }
+  }
+
+  auto fetch = [&](T* dst, const view<const T>& v0, const view<const T>& v1, int k) {
+    if constexpr (!kBulk) {
+      const Tile at = sh.tile[k % kRing];
+      if (at.tile < 0) return;
+      const int64_t t0 = (int64_t)at.tile * kBackTile, c0 = (int64_t)at.group * C;
+      stage<T, C, kBackTile, kBytes, kWork>(dst, v0, at.b, t0, c0, q.L, q.H);
+      stage<T, C, kBackTile, kBytes, kWork>(dst + kBackTile * C, v1, at.b, t0, c0, q.L, q.H);
+    }
+  };
+  auto fetch_rd = [&](int k) { fetch(&sh.rd[k & 3][0][0][0], q.r, dy, k); };
+  auto fetch_ix = [&](int k) { fetch(&sh.ix[k & 1][0][0][0], q.i, q.x, k); };
+  auto wait = [&](uint64_t* here, int parity) {
+    if (kBulk && !tc::mbar_wait_sleep(here, parity) && lane == 0)
+      report_status(q.status, DLR_ERR_TIMEOUT);
+  };
+  struct Part {  // what a warp has of a tile: its decays, its steps, which begin a sequence
+    float2 ka[NP];
+    int n;
+    uint32_t cut;
+  };
+  auto decays = [&](int k, Part& z) {
+    const Tile at = sh.tile[k % kRing];
+    if (at.tile < 0) {
+      bar_arrive(kMapsBar + (k & 1), kWork + 32);
+      return;
+    }
+    const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
+    z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
+    z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
+    const float2 kz = mul2(make_float2(sh.k[k % kRing][lane * VEC], sh.k[k % kRing][lane * VEC + VEC - 1]),
+                           two(-kLog2e));
+    const T* r = &sh.rd[k & 3][0][warp * S][lane * VEC];
+    wait(&sh.rd_here[k & 3], (k >> 2) & 1);
+    float2 a[NP];
 #pragma unroll
     for (int m = 0; m < NP; ++m) {
-      const gate2 g = make_gate2(raw(0, m), raw(1, m), kz);
-      ka[m] = keep_decay(g);
-      hb[m] = mul2(g.m, mul2(g.si, raw(2, m)));
+      float2 rest;
+      decay2(mul2(kz, sigmoid2(get2<T, VEC, C>(r, m))), rest, a[m]);
+      z.ka[m] = keep_decay(a[m], rest);
     }
-    if (n < S) {
+    if (z.n < S) {  // steps past the end pass the gradient through; their dy is zero
 #pragma unroll
       for (int j = 0; j < S; ++j)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          if (j >= n) half<VEC>(ka, j, v) = -0.0f, half<VEC>(hb, j, v) = 0.0f;
+          if (j >= z.n) half<VEC>(a, j, v) = 1.0f, half<VEC>(z.ka, j, v) = -0.0f;
     }
-    // the warp's maps in both directions
-    {
-      float2 a[NP], t[NP];
+    float A[VEC], G[VEC];
 #pragma unroll
-      for (int m = 0; m < NP; ++m) a[m] = kept_decay(ka[m]), t[m] = raw(3, m);
+    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, G[v] = 0.0f;
+    float2 d[NP];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) A[v] = 1.0f, e[v] = 0.0f, G[v] = 0.0f;
+    for (int m = 0; m < NP; ++m) d[m] = get2<T, VEC, C>(r + kBackTile * C, m);
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        advance<VEC>(e, a, hb, j);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          A[v] *= half<VEC>(a, j, v);
-          if ((cut >> j) & 1u) e[v] = half<VEC>(hb, j, v);
-        }
+    for (int j = S - 1; j >= 0; --j) {
+      if constexpr (VEC == 2) {
+        const float2 t = mul2(a[j], add2(d[j], make_float2(G[0], G[1])));
+        G[0] = t.x, G[1] = t.y;
+      } else {
+        G[0] = half<VEC>(a, j, 0) * (half<VEC>(d, j, 0) + G[0]);
       }
-#pragma unroll
-      for (int j = S - 1; j >= 0; --j)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          const float d = j < n ? half<VEC>(t, j, v) : 0.0f;
-          G[v] = (cut >> j) & 1u ? 0.0f : half<VEC>(a, j, v) * (d + G[v]);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      map_s[warp][lane * VEC + v] = make_float2(A[v], e[v]);
-      back_s[warp][lane * VEC + v] = G[v];
-    }
-    if (lane == 0) cut_s[warp] = cut;
-    __syncthreads();
-
-    if (warp == 0) {
-      float tA[VEC], tC[VEC], in[VEC], end[VEC];
-      bool any = false;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) tA[v] = 1.0f, tC[v] = 0.0f;
-#pragma unroll
-      for (int w = W - 1; w >= 0; --w) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          const float m = map_s[w][lane * VEC + v].x, c = back_s[w][lane * VEC + v];
-          tC[v] = cut_s[w] ? c : fmaf(m, tC[v], c);
-          tA[v] *= m;
-        }
-        any |= cut_s[w] != 0;
-      }
-      if (at.tile == q.tiles - 1)
+      if (z.cut)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          in[v] = dh_last && on[v] ? dh_last[at.b * q.H + h + v] : 0.0f;
-      chain(q, at, ((int64_t)at.b * q.tiles + at.tile) * q.HP + h, -1, tA, tC, any, in, end);
+          if ((z.cut >> j) & 1u) G[v] = 0.0f;
+    }
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        if (at.tile == 0 && dh0 && on[v]) dh0[at.b * q.H + h + v] = end[v];
-        in_s[lane * VEC + v] = in[v];
+    for (int m = 0; m < NP; ++m) {
+      if constexpr (VEC == 2) {
+        const float2 t = mul2(make_float2(A[0], A[1]), a[m]);
+        A[0] = t.x, A[1] = t.y;
+      } else {
+        A[0] *= a[m].x * a[m].y;
       }
     }
-    // the states before the steps, while the first warp looks along the chain
-    for (int w = 0; w < warp; ++w)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float2 m = map_s[w][lane * VEC + v];
-        s[v] = cut_s[w] ? m.y : fmaf(m.x, s[v], m.y);
-      }
-    {
-      float2 a[NP];
+    for (int v = 0; v < VEC; ++v) sh.map[k % 3][warp][lane * VEC + v] = make_float2(A[v], G[v]);
+    if (lane == 0) sh.cut[k % 3][warp] = z.cut;
+    bar_arrive(kMapsBar + (k & 1), kWork + 32);
+  };
+  // the state that enters the warp's steps of a tile
+  auto kept = [&](int k, float (&s)[VEC]) {
+    const Tile at = sh.tile[k % kRing];
+    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+    const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
 #pragma unroll
-      for (int m = 0; m < NP; ++m) a[m] = kept_decay(ka[m]);
+    for (int v = 0; v < VEC; ++v)
+      s[v] = t0 < q.L && h + v < q.H && DLR_IN(at.b, q.B)
+                 ? states[(at.b * ((q.L - 1) / S + 1) + t0 / S) * q.H + h + v]
+                 : 0.0f;
+  };
+  // plain (a constant in each call): all S steps are there and none begins a sequence
+  auto finish = [&](int k, Part& z, float (&s)[VEC], const bool plain) {
+    const Tile at = sh.tile[k % kRing];
+    const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
+    const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
+    bool on[VEC];
+    float G[VEC], sum[VEC];
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        float before[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          if ((cut >> j) & 1u) s[v] = 0.0f;
-          before[v] = s[v];
-        }
-        advance<VEC>(s, a, hb, j);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) half<VEC>(hb, j, v) = before[v];
-      }
+    for (int v = 0; v < VEC; ++v) {
+      on[v] = kBulk || (h + v < q.H && DLR_IN(at.b, q.B));
+      G[v] = sh.enter[k & 1][warp][lane * VEC + v];
+      sum[v] = 0.0f;
     }
-    __syncthreads();
-
-    float sum[VEC];
+    const float2 k2 = make_float2(sh.k[k % kRing][lane * VEC], sh.k[k % kRing][lane * VEC + VEC - 1]);
+    T* r = &sh.rd[k & 3][0][warp * S][lane * VEC];
+    T* i = &sh.ix[k & 1][0][warp * S][lane * VEC];
+    T* x = i + kBackTile * C;
+    float2 t[NP];  // G of each step
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) G[v] = in_s[lane * VEC + v], sum[v] = 0.0f;
-    for (int w = W - 1; w > warp; --w)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float m = map_s[w][lane * VEC + v].x, c = back_s[w][lane * VEC + v];
-        G[v] = cut_s[w] ? c : fmaf(m, G[v], c);
-      }
-    T* xp = dx.row(at.b, t0) + h;
-    T* rp = dr.row(at.b, t0) + h;
-    T* ip = di.row(at.b, t0) + h;
+    for (int m = 0; m < NP; ++m) t[m] = get2<T, VEC, C>(r + kBackTile * C, m);
 #pragma unroll
     for (int m = NP - 1; m >= 0; --m) {
+      float2 a = kept_decay(z.ka[m]);
+      if constexpr (VEC == 2) {
+        t[m] = add2(t[m], make_float2(G[0], G[1]));
+        const float2 g = mul2(a, t[m]);
+        G[0] = g.x, G[1] = g.y;
+        if (!plain && (z.cut >> m) & 1u) G[0] = G[1] = 0.0f;
+      } else {
+        t[m].y += G[0];
+        G[0] = a.y * t[m].y;
+        if (!plain && (z.cut >> (2 * m + 1)) & 1u) G[0] = 0.0f;
+        t[m].x += G[0];
+        G[0] = a.x * t[m].x;
+        if (!plain && (z.cut >> (2 * m)) & 1u) G[0] = 0.0f;
+      }
+    }
+    wait(&sh.ix_here[k & 1], (k >> 1) & 1);
+#pragma unroll
+    for (int m = 0; m < NP; ++m) {
       constexpr int per = VEC == 2 ? 1 : 2;  // steps of a pair
       const int j = m * per;
-      if (j >= n) continue;
-      const float2 sr = sigmoid2(raw(0, m)), si = sigmoid2(raw(1, m));
-      // 1 - a^2 from what is kept: 1 - a^2, or -k (2 + k) with k = a - 1
-      const float2 neg = sign_ones(ka[m]), a = add2(ka[m], neg);
-      const float2 u = fma2(mul2(ka[m], two(-1.0f)), fma2(neg, two(2.0f), ka[m]),
+      const float2 sr = sigmoid2(get2<T, VEC, C>(r, m)), si = sigmoid2(get2<T, VEC, C>(i, m));
+      const float2 sx = mul2(si, get2<T, VEC, C>(x, m));
+      // 1 - a^2 from what is kept: 1 - k^2, or -k (2 + k) where k = a - 1
+      const float2 neg = sign_ones(z.ka[m]), a = add2(z.ka[m], neg);
+      const float2 u = fma2(mul2(z.ka[m], two(-1.0f)), fma2(neg, two(2.0f), z.ka[m]),
                             fma2(neg, two(-1.0f), two(1.0f)));
-      const float2 rm = rsqrt2(u), sx = mul2(si, raw(2, m)), dyv = raw(3, m);
-      float2 t;  // G of the two
+      const float2 rm = rsqrt2(u), mm = mul2(u, rm), b = mul2(mm, sx);
+      float2 before;  // the state before the step
       if constexpr (VEC == 2) {
-        t = add2(dyv, make_float2(G[0], G[1]));
-        const float2 next = mul2(a, t);
-        G[0] = (cut >> j) & 1u ? 0.0f : next.x;
-        G[1] = (cut >> j) & 1u ? 0.0f : next.y;
+        if (!plain && (z.cut >> m) & 1u) s[0] = s[1] = 0.0f;
+        before = make_float2(s[0], s[1]);
+        const float2 n = fma2(a, before, b);
+        s[0] = n.x, s[1] = n.y;
       } else {
-        t.y = G[0];
-        if (j + 1 < n) {
-          t.y += dyv.y;
-          G[0] = (cut >> (j + 1)) & 1u ? 0.0f : a.y * t.y;
-        }
-        t.x = dyv.x + G[0];
-        G[0] = (cut >> j) & 1u ? 0.0f : a.x * t.x;
+        if (!plain && (z.cut >> j) & 1u) s[0] = 0.0f;
+        before.x = s[0];
+        s[0] = fmaf(a.x, s[0], b.x);
+        if (!plain && (z.cut >> (j + 1)) & 1u) s[0] = 0.0f;
+        before.y = s[0];
+        s[0] = fmaf(a.y, s[0], b.y);
       }
-      const float2 arm = mul2(mul2(a, rm), two(-1.0f));
-      const float2 E = mul2(mul2(mul2(t, a), sr), fma2(arm, sx, hb[m]));
-      const float2 tm = mul2(t, mul2(u, rm));
+      const float2 arm = mul2(mul2(a, two(-1.0f)), rm);
+      const float2 E = mul2(mul2(mul2(t[m], a), sr), fma2(arm, sx, before));
+      const float2 tm = mul2(t[m], mm);
       const float2 ox = mul2(tm, si);
       const float2 oi = mul2(mul2(tm, sx), fma2(si, two(-1.0f), two(1.0f)));
-      const float2 orr = mul2(mul2(k2, E), fma2(sr, two(1.0f), two(-1.0f)));
+      const float2 orr = mul2(mul2(k2, E), add2(sr, two(-1.0f)));
       if constexpr (VEC == 2) {
-        sum[0] += E.x, sum[1] += E.y;
+        if (plain || j < z.n) {
+          const float2 n = add2(make_float2(sum[0], sum[1]), E);
+          sum[0] = n.x, sum[1] = n.y;
+        }
       } else {
-        sum[0] += E.x;
-        if (j + 1 < n) sum[0] += E.y;
+        if (plain || j < z.n) sum[0] += E.x;
+        if (plain || j + 1 < z.n) sum[0] += E.y;
       }
 #pragma unroll
       for (int d = 0; d < per; ++d) {
@@ -835,26 +939,68 @@ back_kernel(Job<T> q, view<const T> dy, const float* __restrict__ states,
           pr[v] = d + v ? orr.y : orr.x;
           pi[v] = d + v ? oi.y : oi.x;
         }
-        if (j + d < n && DLR_IN(t0 + j + d, q.L)) {
-          put<T, VEC, kOne>(xp + (j + d) * dx.st, px, on);
-          put<T, VEC, kOne>(rp + (j + d) * dr.st, pr, on);
-          put<T, VEC, kOne>(ip + (j + d) * di.st, pi, on);
+        if constexpr (kBulk) {
+          put<T, VEC, kOne>(x + (j + d) * C, px, on);
+          put<T, VEC, kOne>(r + (j + d) * C, pr, on);
+          put<T, VEC, kOne>(i + (j + d) * C, pi, on);
+        } else if (j + d < z.n && DLR_IN(t0 + j + d, q.L)) {
+          put<T, VEC, kOne>(dx.row(at.b, t0 + j + d) + h, px, on);
+          put<T, VEC, kOne>(dr.row(at.b, t0 + j + d) + h, pr, on);
+          put<T, VEC, kOne>(di.row(at.b, t0 + j + d) + h, pi, on);
         }
       }
     }
-    __syncthreads();  // back_s has been read
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) back_s[warp][lane * VEC + v] = sum[v];
-    __syncthreads();
-    if (warp == 0)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        float t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) t += back_s[w][lane * VEC + v];
-        if (on[v]) part[row + v] = t;
+    for (int v = 0; v < VEC; ++v) sh.sum[k & 1][warp][lane * VEC + v] = sum[v];
+    if (kBulk && z.n > 0) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::tma_store_3d(&out.map[0], &sh.ix[k & 1][1][warp * S][0], at.group * C, (int)t0, at.b);
+        tc::tma_store_3d(&out.map[1], &sh.rd[k & 3][0][warp * S][0], at.group * C, (int)t0, at.b);
+        tc::tma_store_3d(&out.map[2], &sh.ix[k & 1][0][warp * S][0], at.group * C, (int)t0, at.b);
+        tc::bulk_commit_group();
       }
+    }
+  };
+  // tile k's decays are in `now`; true when it was the last
+  auto turn = [&](int k, Part& now, Part& next) {
+    float s[VEC];
+    kept(k, s);
+    decays(k + 1, next);
+    if (kBulk) {
+      if (lane == 0) tc::bulk_wait_group_read0();  // the outputs of tile k - 1 have left
+      __syncwarp();
+    } else {
+      copies_wait();
+    }
+    bar_sync(kEnterBar + (k & 1), kBackThreads);
+    fetch_rd(k + 3);
+    fetch_ix(k + 1);
+    if (!kBulk) copies_end();
+    if (now.n == S && now.cut == 0)
+      finish(k, now, s, true);
+    else
+      finish(k, now, s, false);
+    return sh.tile[(k + 1) % kRing].tile < 0;
+  };
+  Part z0, z1;
+  __syncthreads();
+  for (int k = 0; k < 3; ++k) fetch_rd(k);
+  fetch_ix(0);
+  if (!kBulk) {
+    copies_end();
+    copies_wait();
+    bar_sync(kWarpsBar + 1, kWork);
   }
+  decays(0, z0);
+  const bool any = sh.tile[0].tile >= 0;  // read now: its place in the ring is used again
+  for (int k = 0; any; k += 2) {
+    if (turn(k, z0, z1)) break;
+    if (turn(k + 1, z1, z0)) break;
+  }
+  bar_sync(kWarpsBar, kWork + 32);  // the supplying warp has the last tile's sums to add
+  if (kBulk && lane == 0) tc::bulk_wait_group0();
 }
 
 // dp = -c sigmoid(p) times the sum of a channel's parts, in a fixed order: a warp for each 32
@@ -918,7 +1064,32 @@ struct Space {
   }
 };
 
-// the widest access of `n` bytes that a view's rows allow
+// A tensor map over an array [B, L, H] whose boxes are `rows` rows of 128 bytes.
+template <typename T, typename V>
+bool describe(CUtensorMap* m, const V& v, int64_t B, int64_t L, int64_t H, int rows) {
+  auto fn = tc::tensor_map_encoder();
+  if (!fn) return false;
+  const CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t dims[3] = {(cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
+  // the stride of a dimension of one is never used
+  const cuuint64_t st = (cuuint64_t)(L > 1 ? v.stride_t : H) * sizeof(T);
+  const cuuint64_t strides[2] = {st, B > 1 ? (cuuint64_t)v.stride_b * sizeof(T) : st};
+  const cuuint32_t box[3] = {128 / sizeof(T), (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
+  return fn(m, type, 3, const_cast<void*>(static_cast<const void*>(v.data)), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// whether it can be: strides that are positive, a multiple of 16 bytes and below 2^40 of them
+template <typename V>
+bool can_describe(const V& v, int64_t size, int64_t B, int64_t L) {
+  auto ok = [&](int64_t s) { return s > 0 && s * size % 16 == 0 && s * size < (int64_t(1) << 40); };
+  return (reinterpret_cast<uintptr_t>(v.data) & 15u) == 0 && (L <= 1 || ok(v.stride_t)) &&
+         (B <= 1 || ok(v.stride_b));
+}
+
+// whether accesses of `n` bytes fit a view's rows
 template <typename V>
 bool wide(const V& v, int64_t size, uintptr_t n) {
   return ((reinterpret_cast<uintptr_t>(v.data) | (uintptr_t)(v.stride_b * size) |
@@ -932,14 +1103,13 @@ Job<T> make_job(const A& a, const Space& sp) {
   return {in_view<T>(a.x), in_view<T>(a.r), in_view<T>(a.i), a.p, a.reset,
           reinterpret_cast<float*>(ws + sp.head + sp.maps), reinterpret_cast<float*>(ws + sp.head),
           reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, sp.HP, a.B * groups,
-          (int)groups, (int)sp.tiles, (float)a.c};
+          (int)groups, (int)sp.tiles, 1, (float)a.c};
 }
 
-// Blocks for `tiles` tiles: what the GPU holds at once at most. A chain of one tile needs no
-// counter and takes a block for each.
+// Blocks for all tiles, one to an SM at most; the chain's workspace becomes empty. A chain of one tile
+// needs neither that nor the counter: each has a block.
 template <typename T>
-cudaError_t prepare_chain(const Job<T>& q, const Space& sp, int per_sm, unsigned* blocks,
-                          cudaStream_t s) {
+cudaError_t prepare_chain(Job<T>& q, const Space& sp, unsigned* blocks, cudaStream_t s) {
   const int64_t all = q.chains * q.tiles;
   *blocks = (unsigned)all;
   if (q.tiles == 1) return cudaSuccess;
@@ -947,7 +1117,8 @@ cudaError_t prepare_chain(const Job<T>& q, const Space& sp, int per_sm, unsigned
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  *blocks = (unsigned)std::min<int64_t>(all, (int64_t)sms * per_sm);
+  *blocks = (unsigned)std::min<int64_t>(all, sms);
+  q.most = (int)((all - 1) / *blocks + 1);  // all blocks get as many, however early they come
   return cudaMemsetAsync(q.head, 0xff, sp.head + sp.maps + sp.in, s);
 }
 
@@ -955,29 +1126,46 @@ template <typename T, int kBytes>
 cudaError_t scan_w(const glr_scan_args& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(ScanShared<T>);
   const Space sp(a.B, a.L, a.H, kScanTile);
-  const Job<T> q = make_job<T>(a, sp);
+  Job<T> q = make_job<T>(a, sp);
   unsigned blocks;
-  cudaError_t e = prepare_chain(q, sp, 1, &blocks, s);
+  cudaError_t e = prepare_chain(q, sp, &blocks, s);
   if (e == cudaSuccess) e = max_smem_once<scan_kernel<T, kBytes>>(smem);
   if (e != cudaSuccess) return e;
-  scan_kernel<T, kBytes><<<blocks, kScanThreads, smem, s>>>(q, out_view<T>(a.y), a.h0, a.h_last,
-                                                            a.states);
+  Maps<3> in{};
+  Maps<1> out{};
+  if (kBytes == kTma && !(describe<T>(&in.map[0], a.r, a.B, a.L, a.H, kScanTile) &&
+                          describe<T>(&in.map[1], a.i, a.B, a.L, a.H, kScanTile) &&
+                          describe<T>(&in.map[2], a.x, a.B, a.L, a.H, kScanTile) &&
+                          describe<T>(&out.map[0], a.y, a.B, a.L, a.H, kScanSteps)))
+    return cudaErrorInvalidValue;
+  scan_kernel<T, kBytes><<<blocks, kScanThreads, smem, s>>>(q, in, out, out_view<T>(a.y), a.h0,
+                                                            a.h_last, a.states);
   return cudaGetLastError();
 }
 
 template <typename T, int kBytes>
 cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
-  constexpr size_t smem = 2 * 4 * kBackTile * 128;
+  constexpr size_t smem = sizeof(BackShared<T>);
   const Space sp(a.B, a.L, a.H, kBackTile);
-  const Job<T> q = make_job<T>(a, sp);
+  Job<T> q = make_job<T>(a, sp);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.head + sp.maps +
                                          sp.in);
   unsigned blocks;
-  cudaError_t e = prepare_chain(q, sp, kBackBlocks, &blocks, s);
+  cudaError_t e = prepare_chain(q, sp, &blocks, s);
   if (e == cudaSuccess) e = max_smem_once<back_kernel<T, kBytes>>(smem);
   if (e != cudaSuccess) return e;
-  back_kernel<T, kBytes><<<blocks, kBackWarps * 32, smem, s>>>(
-      q, in_view<T>(a.dy), a.states, a.dh_last, out_view<T>(a.dx), out_view<T>(a.dr),
+  Maps<4> in{};
+  Maps<3> out{};
+  if (kBytes == kTma && !(describe<T>(&in.map[0], a.r, a.B, a.L, a.H, kBackTile) &&
+                          describe<T>(&in.map[1], a.dy, a.B, a.L, a.H, kBackTile) &&
+                          describe<T>(&in.map[2], a.i, a.B, a.L, a.H, kBackTile) &&
+                          describe<T>(&in.map[3], a.x, a.B, a.L, a.H, kBackTile) &&
+                          describe<T>(&out.map[0], a.dx, a.B, a.L, a.H, kBackSteps) &&
+                          describe<T>(&out.map[1], a.dr, a.B, a.L, a.H, kBackSteps) &&
+                          describe<T>(&out.map[2], a.di, a.B, a.L, a.H, kBackSteps)))
+    return cudaErrorInvalidValue;
+  back_kernel<T, kBytes><<<blocks, kBackThreads, smem, s>>>(
+      q, in, out, in_view<T>(a.dy), a.states, a.dh_last, out_view<T>(a.dx), out_view<T>(a.dr),
       out_view<T>(a.di), a.dh0, part);
   back_sum<<<(unsigned)((a.H + 31) / 32), 256, 0, s>>>(part, a.B * q.tiles, a.H, a.p, (float)a.c,
                                                        a.dp);
@@ -987,24 +1175,25 @@ cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
 template <typename T>
 cudaError_t scan_t(const glr_scan_args& a, cudaStream_t s) {
   const int64_t z = sizeof(T);
-  auto all = [&](int64_t n) {
-    return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
-           wide(a.y, z, n);
-  };
-  if (all(16)) return scan_w<T, 16>(a, s);
-  if (sizeof(T) == 4 || all(4)) return scan_w<T, 4>(a, s);
-  if constexpr (sizeof(T) == 2) return scan_w<T, 2>(a, s);
+  auto tma = [&](const auto& v) { return can_describe(v, z, a.B, a.L); };
+  if (a.H * z % 16 == 0 && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.y)) return scan_w<T, kTma>(a, s);
+  if constexpr (sizeof(T) == 2)
+    if (a.H % 2 || !wide(a.x, 2, 4) || !wide(a.r, 2, 4) || !wide(a.i, 2, 4) || !wide(a.y, 2, 4))
+      return scan_w<T, 2>(a, s);
+  return scan_w<T, 4>(a, s);
 }
 template <typename T>
 cudaError_t back_t(const glr_scan_backward_args& a, cudaStream_t s) {
   const int64_t z = sizeof(T);
-  auto all = [&](int64_t n) {
-    return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
-           wide(a.dy, z, n) && wide(a.dx, z, n) && wide(a.dr, z, n) && wide(a.di, z, n);
-  };
-  if (all(16)) return back_w<T, 16>(a, s);
-  if (sizeof(T) == 4 || all(4)) return back_w<T, 4>(a, s);
-  if constexpr (sizeof(T) == 2) return back_w<T, 2>(a, s);
+  auto tma = [&](const auto& v) { return can_describe(v, z, a.B, a.L); };
+  if (a.H * z % 16 == 0 && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.dy) && tma(a.dx) && tma(a.dr) &&
+      tma(a.di))
+    return back_w<T, kTma>(a, s);
+  if constexpr (sizeof(T) == 2)
+    if (a.H % 2 || !wide(a.x, 2, 4) || !wide(a.r, 2, 4) || !wide(a.i, 2, 4) || !wide(a.dy, 2, 4) ||
+        !wide(a.dx, 2, 4) || !wide(a.dr, 2, 4) || !wide(a.di, 2, 4))
+      return back_w<T, 2>(a, s);
+  return back_w<T, 4>(a, s);
 }
 
 template <typename T>
@@ -1026,9 +1215,9 @@ size_t scan_backward_workspace_bytes(int64_t B, int64_t L, int64_t H) {
   const Space sp(B, L, H, kBackTile);
   return sp.head + sp.maps + 2 * sp.in;  // and the parts of dp
 }
-// tiles (which a 32-bit counter hands out) of the finest cut that a call of this size takes
+// tiles, which a 32-bit counter hands out, of the finest cut that a call of this size takes
 int64_t scan_tiles(int64_t B, int64_t L, int64_t H) {
-  return B * glr_states(L) * ((H + 31) / 32);
+  return B * ((L + kScanTile - 1) / kScanTile) * ((H + 31) / 32);
 }
 
 cudaError_t launch_scan(const glr_scan_args& a, cudaStream_t s) {

@@ -27,7 +27,7 @@ from . import dlr as _dlr
 TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 NORM = {"rms": 0, "layer": 1}
 ACT = {"silu": 0, "sigmoid": 1, "none": 2}
-STATE_STEPS = 64  # GLR_STATE_STEPS
+STATE_STEPS = 8  # GLR_STATE_STEPS
 CKPT_GROUP = 32   # GLR_CKPT_GROUP
 
 _lib = None
@@ -161,7 +161,7 @@ def glr_scan(x, r, i, p, scale: float = 8.0, h0=None, reset=None, save_states: b
     a_t = exp(-scale softplus(p) sigmoid(r_t)) over x, r, i [B, L, H]; p [H]; h0 [B, H] the state
     before the first step (None: zero); reset [B, L] (bool or uint8, None: none) marks steps that
     begin a new sequence. Returns (y [B, L, H], h_last [B, H]) and, with ``save_states``, the
-    float32 states [B, ceil(L / 64), H] that glr_scan_backward takes."""
+    float32 states [B, ceil(L / 8), H] that glr_scan_backward takes."""
     lib, kind = _load(), _act_type(x)
     if x.dim() != 3:
         raise ValueError("x: expected [B, L, H]")

@@ -34,7 +34,7 @@ def test_every_declared_function_is_exported(lib):
 
 
 def test_sizes(lib):
-    assert [lib.glr_states(n) for n in (0, 1, 64, 65, 4096)] == [0, 1, 1, 2, 64]
+    assert [lib.glr_states(n) for n in (0, 1, 8, 9, 4096)] == [0, 1, 1, 2, 512]
     assert lib.glr_scan_workspace_size(0, 10, 10) == 0
     assert lib.glr_scan_workspace_size(1, 10, 0) == 0
     assert lib.glr_scan_workspace_size(1, 1 << 31, 1) == 0
