@@ -39,5 +39,14 @@ __device__ __forceinline__ float decode(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
 
+// Two at a time: the first in the low byte.
+__device__ __forceinline__ uint32_t encode2(float2 q) {
+  const uint32_t c = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  return (isinf(q.x) ? 0x7fu : c & 0xffu) | (isinf(q.y) ? 0x7f00u : c & 0xff00u);
+}
+__device__ __forceinline__ float2 decode2(uint32_t codes) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
+}
+
 }  // namespace glr
 }  // namespace dlr
