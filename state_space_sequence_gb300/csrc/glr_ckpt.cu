@@ -19,8 +19,8 @@ pack_kernel(Rows<const T> t, int64_t M, int H, uint8_t* __restrict__ codes,
   const int64_t row = group / groups;
   const int c = (int)(group % groups) * GLR_CKPT_GROUP + (int)(k % GLR_CKPT_GROUP);
   const bool on = row < M && c < H;
-  pack<T, VEC> v{};
-  if (on) v = *reinterpret_cast<const pack<T, VEC>*>(t.at(row, c));
+  words<T, VEC> v;
+  if (on) v.get(t.at(row, c));
   keep<T, VEC>(v, on, codes + row * H + c, scales + group);
 }
 template <typename T, int VEC>
@@ -34,7 +34,9 @@ unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sca
   const int c = (int)(group % groups) * GLR_CKPT_GROUP + (int)(k % GLR_CKPT_GROUP);
   if (row >= M || c >= H) return;
   float v[VEC];
-  kept<VEC>(*reinterpret_cast<const pack<uint8_t, VEC>*>(codes + row * H + c), scales[group], v);
+  words<uint8_t, VEC> item;
+  item.get(codes + row * H + c);
+  kept<VEC>(item, scales[group], v);
   store<T, VEC>(t.at(row, c), v);
 }
 

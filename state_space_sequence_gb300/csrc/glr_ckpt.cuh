@@ -50,19 +50,16 @@ __device__ __forceinline__ float2 decode2(uint32_t codes) {
 
 // The largest bit pattern of |t| in an item; patterns of floats of one sign are in their order.
 template <typename T, int VEC>
-__device__ __forceinline__ uint32_t top_bits(const pack<T, VEC>& t) {
+__device__ __forceinline__ uint32_t top_bits(const words<T, VEC>& t) {
   if constexpr (sizeof(T) == 4) {
     uint32_t m = 0;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) m = max(m, __float_as_uint(t.v[v]) & 0x7fffffffu);
+    for (int v = 0; v < VEC; ++v) m = max(m, t.w[v] & 0x7fffffffu);
     return m;
-  } else if constexpr (VEC == 1) {
-    return *reinterpret_cast<const uint16_t*>(&t) & 0x7fffu;
   } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&t);
-    uint32_t m = w[0] & 0x7fff7fffu;
+    uint32_t m = t.w[0] & 0x7fff7fffu;
 #pragma unroll
-    for (int v = 1; v < VEC / 2; ++v) m = __vmaxu2(m, w[v] & 0x7fff7fffu);
+    for (int v = 1; v < VEC / 2; ++v) m = __vmaxu2(m, t.w[v] & 0x7fff7fffu);
     return max(m & 0xffffu, m >> 16);
   }
 }
@@ -75,16 +72,18 @@ __device__ __forceinline__ float from_bits(uint32_t bits) {
 
 // VEC codes and their group's scale. A group is 32 / VEC neighbouring lanes; whole warps call it.
 template <typename T, int VEC>
-__device__ __forceinline__ void keep(const pack<T, VEC>& t, bool on, uint8_t* codes, uint8_t* scale) {
+__device__ __forceinline__ void keep(const words<T, VEC>& t, bool on, uint8_t* codes, uint8_t* scale) {
   uint32_t top = top_bits<T, VEC>(t);
 #pragma unroll
   for (int o = 16 / VEC; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float f[VEC];
+  t.to(f);
   float amax = from_bits<T>(top);
   const bool finite = amax <= 3.40282347e38f;
   if (__any_sync(0xffffffffu, !finite)) {  // once more, over what is finite
     amax = 0.0f;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) amax = fmaxf(amax, finite_abs(to_f(t.v[v])));
+    for (int v = 0; v < VEC; ++v) amax = fmaxf(amax, finite_abs(f[v]));
 #pragma unroll
     for (int o = 16 / VEC; o >= 1; o >>= 1)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -93,13 +92,13 @@ __device__ __forceinline__ void keep(const pack<T, VEC>& t, bool on, uint8_t* co
   const int b = scale_byte(amax);
   const float inv = inverse_scale_of(b);
   if constexpr (VEC == 1) {
-    *codes = (uint8_t)encode(to_f(t.v[0]) * inv);
+    *codes = (uint8_t)encode(f[0] * inv);
   } else {
     uint32_t w[VEC / 4];
 #pragma unroll
     for (int v = 0; v < VEC; v += 4) {
-      const float2 p = mul2(make_float2(to_f(t.v[v]), to_f(t.v[v + 1])), two(inv));
-      const float2 q = mul2(make_float2(to_f(t.v[v + 2]), to_f(t.v[v + 3])), two(inv));
+      const float2 p = mul2(make_float2(f[v], f[v + 1]), two(inv));
+      const float2 q = mul2(make_float2(f[v + 2], f[v + 3]), two(inv));
       if (finite)
         w[v / 4] = (uint32_t)__nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3) |
                    (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) << 16;
@@ -112,16 +111,15 @@ __device__ __forceinline__ void keep(const pack<T, VEC>& t, bool on, uint8_t* co
   if ((threadIdx.x & (32 / VEC - 1)) == 0) *scale = (uint8_t)b;
 }
 template <int VEC>
-__device__ __forceinline__ void kept(const pack<uint8_t, VEC>& k, int scale, float* out) {
+__device__ __forceinline__ void kept(const words<uint8_t, VEC>& k, int scale, float* out) {
   const float s = scale_of(scale);
   if constexpr (VEC == 1) {
-    out[0] = decode(k.v[0]) * s;
+    out[0] = decode(k.w[0]) * s;
   } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&k);
 #pragma unroll
     for (int v = 0; v < VEC; v += 4) {
-      const float2 p = mul2(decode2(w[v / 4] & 0xffffu), two(s));
-      const float2 q = mul2(decode2(w[v / 4] >> 16), two(s));
+      const float2 p = mul2(decode2(k.w[v / 4] & 0xffffu), two(s));
+      const float2 q = mul2(decode2(k.w[v / 4] >> 16), two(s));
       out[v] = p.x, out[v + 1] = p.y, out[v + 2] = q.x, out[v + 3] = q.y;
     }
   }

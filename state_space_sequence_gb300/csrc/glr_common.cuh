@@ -13,6 +13,11 @@
 namespace dlr {
 namespace glr {
 
+template <typename T>
+constexpr bool is_half = false;
+template <>
+inline constexpr bool is_half<__half> = true;
+
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -27,10 +32,81 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// VEC neighbouring elements, read or written at once.
+// Two 16-bit values of a word as floats and back, the first in the low half.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (sizeof(T) == 2 && !is_half<T>)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  if constexpr (is_half<T>) {
+    const __half2 p = __float22half2_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  } else {
+    const __nv_bfloat162 p = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+// An item of memory by one access of its size, in words.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) pack {
-  T v[VEC];
+struct words {
+  static constexpr int kBytes = VEC * (int)sizeof(T), kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords] = {};
+  __device__ __forceinline__ void get(const void* p) {
+    if constexpr (kBytes == 16) {
+      const uint4 t = *static_cast<const uint4*>(p);
+      w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 t = *static_cast<const uint2*>(p);
+      w[0] = t.x, w[1] = t.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *static_cast<const uint32_t*>(p);
+    } else if constexpr (kBytes == 2) {
+      w[0] = *static_cast<const uint16_t*>(p);
+    } else {
+      w[0] = *static_cast<const uint8_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void put(void* p) const {
+    if constexpr (kBytes == 16)
+      *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 8)
+      *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (kBytes == 4)
+      *static_cast<uint32_t*>(p) = w[0];
+    else if constexpr (kBytes == 2)
+      *static_cast<uint16_t*>(p) = (uint16_t)w[0];
+    else
+      *static_cast<uint8_t*>(p) = (uint8_t)w[0];
+  }
+  __device__ __forceinline__ void to(float* out) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) out[v] = __uint_as_float(w[v]);
+    } else if constexpr (VEC == 1) {
+      out[0] = unpack2<T>(w[0]).x;
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; v += 2) {
+        const float2 t = unpack2<T>(w[v / 2]);
+        out[v] = t.x, out[v + 1] = t.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void from(const float* in) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) w[v] = __float_as_uint(in[v]);
+    } else if constexpr (VEC == 1) {
+      w[0] = pack2<T>(make_float2(in[0], 0.0f));
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; v += 2) w[v / 2] = pack2<T>(make_float2(in[v], in[v + 1]));
+    }
+  }
 };
 
 // An array [B, L, H] with contiguous channels (strides in elements).

@@ -19,16 +19,15 @@ constexpr int kStages = 2;  // rows in shared memory: the one at work and the ne
 
 template <typename T, int VEC>
 __device__ __forceinline__ void load(const T* p, float* out) {
-  const pack<T, VEC> k = *reinterpret_cast<const pack<T, VEC>*>(p);
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) out[v] = to_f(k.v[v]);
+  words<T, VEC> k;
+  k.get(p);
+  k.to(out);
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void store(T* p, const float* in) {
-  pack<T, VEC> k;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) k.v[v] = from_f<T>(in[v]);
-  *reinterpret_cast<pack<T, VEC>*>(p) = k;
+  words<T, VEC> k;
+  k.from(in);
+  k.put(p);
 }
 __device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
 
@@ -147,7 +146,9 @@ template <typename T, int VEC, int NV, bool kDirect>
 struct Staged {
   static constexpr int kBytes = VEC * (int)sizeof(T);
   static constexpr bool kAsync = kBytes == 16 || kBytes == 8 || kBytes == 4;
-  using item = pack<T, VEC>;
+  struct alignas(kBytes) item {
+    uint8_t bytes[kBytes];
+  };
   static __device__ __forceinline__ int slot(int j) { return j * (int)blockDim.x + (int)threadIdx.x; }
   static __device__ __forceinline__ int items() { return NV * (int)blockDim.x; }
   // zeros for an item that is not there
@@ -167,24 +168,26 @@ struct Staged {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(p), "r"(n)
                      : "memory");
     } else {
-      item z{};
-      if (on) z = *reinterpret_cast<const item*>(src);
-      s[slot(j)] = z;
+      words<T, VEC> z;
+      if (on) z.get(src);
+      z.put(s + slot(j));
     }
   }
-  static __device__ __forceinline__ item one(const item* s, int j, const T* src, bool on) {
-    if constexpr (kDirect) return on ? *reinterpret_cast<const item*>(src) : item{};
-    else return s[slot(j)];
+  static __device__ __forceinline__ words<T, VEC> one(const item* s, int j, const T* src, bool on) {
+    words<T, VEC> k;
+    if constexpr (!kDirect)
+      k.get(s + slot(j));
+    else if (on)
+      k.get(src);
+    return k;
   }
   static __device__ __forceinline__ void get(const item* s, const Items<VEC, NV>& it, const Rows<const T>& r,
                                              int64_t row,
                                              float2 (&out)[Items<VEC, NV>::P]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const item k = one(s, j, r.at(row, it.channel(j)), it.on(j));
       float t[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) t[v] = to_f(k.v[v]);
+      one(s, j, r.at(row, it.channel(j)), it.on(j)).to(t);
       Items<VEC, NV>::place(j, t, out);
     }
   }

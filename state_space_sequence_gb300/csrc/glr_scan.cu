@@ -238,17 +238,10 @@ __device__ __forceinline__ float& half(float2 (&p)[N], int j, int v) {
   if constexpr (VEC == 2) return v ? p[j].y : p[j].x;
   return j & 1 ? p[j / 2].y : p[j / 2].x;
 }
-__device__ __forceinline__ float2 floats(pack<__nv_bfloat16, 2> k) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&k);
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ float2 floats(pack<__half, 2> k) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&k));
-}
 // pair m of the rows [.][C] at p
 template <typename T, int VEC, int C>
 __device__ __forceinline__ float2 get2(const T* p, int m) {
-  if constexpr (VEC == 2) return floats(*reinterpret_cast<const pack<T, 2>*>(p + m * C));
+  if constexpr (VEC == 2) return unpack2<T>(*reinterpret_cast<const uint32_t*>(p + m * C));
   else return make_float2(p[2 * m * C], p[(2 * m + 1) * C]);
 }
 
@@ -326,10 +319,9 @@ __device__ __forceinline__ void put(T* p, const float (&f)[VEC], bool (&on)[VEC]
     for (int v = 0; v < VEC; ++v)
       if (on[v]) p[v] = from_f<T>(f[v]);
   } else {
-    pack<T, VEC> o;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) o.v[v] = from_f<T>(f[v]);
-    if (on[0]) *reinterpret_cast<pack<T, VEC>*>(p) = o;
+    words<T, VEC> o;
+    o.from(f);
+    if (on[0]) o.put(p);
   }
 }
 
