@@ -28,14 +28,11 @@ join_kernel(JoinArgs a, Rows<const T> x, Rows<const T> h, Rows<const T> g, Rows<
   const float alpha = h.p ? *a.alpha : 0.0f, inv_h = 1.0f / (float)a.H;
   int64_t row = blockIdx.x;
   auto fetch = [&](int64_t r, int k) {
-    if (r < a.M)
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = it.channel(j);
-        St::fetch(sm + (k * 3) * per, j, x.at(r, c), x.p, it.on(j));
-        if (h.p) St::fetch(sm + (k * 3 + 1) * per, j, h.at(r, c), h.p, it.on(j));
-        if (g.p) St::fetch(sm + (k * 3 + 2) * per, j, g.at(r, c), g.p, it.on(j));
-      }
+    if (r < a.M) {
+      St::fetch_row(sm + (k * 3) * per, it, x.at(r, 0));
+      if (h.p) St::fetch_row(sm + (k * 3 + 1) * per, it, h.at(r, 0));
+      if (g.p) St::fetch_row(sm + (k * 3 + 2) * per, it, g.at(r, 0));
+    }
     stage_end();
   };
   fetch(row, 0);
@@ -105,7 +102,7 @@ cudaError_t join_n(const glr_join_args& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 // 16 channels to a thread while the row's threads then fill an SM evenly; single channels (rows that
-// allow no 16-byte access) 8 to a thread while the row is short, so that more threads share it.
+// allow no 16-byte access) 6 to a thread while the row is short, so that more threads share it.
 template <typename T>
 cudaError_t join_t(const glr_join_args& a, cudaStream_t s) {
   constexpr int W = 16 / sizeof(T);
@@ -118,7 +115,7 @@ cudaError_t join_t(const glr_join_args& a, cudaStream_t s) {
     if (a.H <= 16 * 512) return join_n<T, W, 16 / W, 512, 512>(a, s);
     return join_n<T, W, 16 / W, 1024, 1024>(a, s);
   }
-  if (a.H <= 8 * 128) return join_n<T, 1, 8, 128, 768>(a, s);
+  if (a.H <= 6 * 128) return join_n<T, 1, 6, 128, 768>(a, s);
   if (a.H <= 16 * 256) return join_n<T, 1, 16, 256, 512>(a, s);
   return join_n<T, 1, 16, 1024, 1024>(a, s);
 }

@@ -88,19 +88,26 @@ struct Items {
   static __device__ __forceinline__ constexpr int second(int p) { return VEC > 1 ? p * 2 / VEC : 2 * p + 1; }
   // float32 parameters of the channels; 0 past the end
   __device__ __forceinline__ void params(const float* w, float2 (&out)[P]) const {
+    if (all()) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float t[VEC] = {};
-      if (on(j)) {
-        if constexpr (VEC == 8) {
-          load<float, 4>(w + channel(j), t);
-          load<float, 4>(w + channel(j) + 4, t + 4);
-        } else {
-          load<float, VEC>(w + channel(j), t);
-        }
-      }
-      place(j, t, out);
+      for (int j = 0; j < NV; ++j) param<true>(w, j, out);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) param<false>(w, j, out);
     }
+  }
+  template <bool kAll>
+  __device__ __forceinline__ void param(const float* w, int j, float2 (&out)[P]) const {
+    float t[VEC] = {};
+    if (kAll || on(j)) {
+      if constexpr (VEC == 8) {
+        load<float, 4>(w + channel(j), t);
+        load<float, 4>(w + channel(j) + 4, t + 4);
+      } else {
+        load<float, VEC>(w + channel(j), t);
+      }
+    }
+    place(j, t, out);
   }
   static __device__ __forceinline__ void place(int j, const float* t, float2 (&out)[P]) {
     if constexpr (VEC > 1) {
@@ -129,13 +136,21 @@ struct Items {
   }
   template <typename T>
   __device__ __forceinline__ void put(const Rows<T>& r, int64_t row, const float2 (&in)[P]) const {
+    T* p = r.at(row, 0);
+    if (all()) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!on(j) || !DLR_IN(channel(j) + VEC - 1, H)) continue;
-      float t[VEC];
-      pick(j, in, t);
-      store<T, VEC>(r.at(row, channel(j)), t);
+      for (int j = 0; j < NV; ++j) put_one<true>(p, j, in);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) put_one<false>(p, j, in);
     }
+  }
+  template <bool kAll, typename T>
+  __device__ __forceinline__ void put_one(T* p, int j, const float2 (&in)[P]) const {
+    if (!(kAll || on(j)) || !DLR_IN_FILE(channel(j) + VEC - 1, H, 17)) return;
+    float t[VEC];
+    pick(j, in, t);
+    store<T, VEC>(p + channel(j), t);
   }
 };
 
@@ -171,6 +186,16 @@ struct Staged {
       words<T, VEC> z;
       if (on) z.get(src);
       z.put(s + slot(j));
+    }
+  }
+  // the items of a row that begins at p
+  static __device__ __forceinline__ void fetch_row(item* s, const Items<VEC, NV>& it, const T* p) {
+    if (it.all()) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) fetch(s, j, p + it.channel(j), p, true);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) fetch(s, j, p + it.channel(j), p, it.on(j));
     }
   }
   static __device__ __forceinline__ words<T, VEC> one(const item* s, int j, const T* src, bool on) {

@@ -12,6 +12,23 @@ namespace dlr {
 namespace glr {
 namespace {
 
+// s[0] over the row and, for a layer norm, s[1] the sum of q
+template <int P>
+__device__ __forceinline__ void both_sums(bool layer, const float2 (&q)[P], float (&s)[2], float* buf,
+                                          int& turn) {
+  if (layer) {
+    float2 t = two(0.0f);
+#pragma unroll
+    for (int p = 0; p < P; ++p) t = add2(t, q[p]);
+    s[1] = sum2(t);
+    row_sum<2>(s, buf, turn);
+  } else {
+    float one[1] = {s[0]};
+    row_sum<1>(one, buf, turn);
+    s[0] = one[0];
+  }
+}
+
 // part: [parts, 2, H] sums of D uhat and of dn yhat, then [parts] sums of w D uhat
 template <typename T, int VEC, int NV, bool kKept, bool kDirect, int kThreads, int kResident>
 __global__ void __launch_bounds__(kThreads, kResident / kThreads)
@@ -36,23 +53,22 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
   auto codes_at = [&](int k, int array) { return reinterpret_cast<typename Sc::item*>(at(k, array)); };
   int scale_h[NV] = {}, scale_g[NV] = {};  // of the next row
   auto fetch = [&](int64_t r, int k) {
-    if (r < a.M)
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool on = it.on(j);
-      const int c = it.channel(j);
-      St::fetch(at(k, 0), j, x.at(r, c), x.p, on);
-      if (dy.p) St::fetch(at(k, 1), j, dy.at(r, c), dy.p, on);
-      if (dn.p) St::fetch(at(k, 2), j, dn.at(r, c), dn.p, on);
+    if (r < a.M) {
+      St::fetch_row(at(k, 0), it, x.at(r, 0));
+      if (dy.p) St::fetch_row(at(k, 1), it, dy.at(r, 0));
+      if (dn.p) St::fetch_row(at(k, 2), it, dn.at(r, 0));
       if constexpr (kKept) {
-        Sc::fetch(codes_at(k, 3), j, ck.hc + r * a.H + c, ck.hc, on);
-        if (gated) Sc::fetch(codes_at(k, 4), j, ck.gc + r * a.H + c, ck.gc, on);
-        const int64_t s = r * groups + c / GLR_CKPT_GROUP;
-        scale_h[j] = on ? ck.hs[s] : 0;
-        if (gated) scale_g[j] = on ? ck.gs[s] : 0;
+        Sc::fetch_row(codes_at(k, 3), it, ck.hc + r * a.H);
+        if (gated) Sc::fetch_row(codes_at(k, 4), it, ck.gc + r * a.H);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int64_t s = r * groups + it.channel(j) / GLR_CKPT_GROUP;
+          scale_h[j] = it.on(j) ? ck.hs[s] : 0;
+          if (gated) scale_g[j] = it.on(j) ? ck.gs[s] : 0;
+        }
       } else {
-        if (block) St::fetch(at(k, 3), j, h.at(r, c), h.p, on);
-        if (gated) St::fetch(at(k, 4), j, g.at(r, c), g.p, on);
+        if (block) St::fetch_row(at(k, 3), it, h.at(r, 0));
+        if (gated) St::fetch_row(at(k, 4), it, g.at(r, 0));
       }
     }
     stage_end();
@@ -99,7 +115,7 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
     float2 d[P];
     if (dn.p) {
       const float ry = centre<VEC, NV>(it, z, layer, inv_h, a.eps, buf, turn);
-      float2 q[P], v[P], s0 = two(0.0f), s1 = two(0.0f);
+      float2 q[P], v[P], s0 = two(0.0f);
       St::get(at(k, 2), it, dn, row, q);
       it.params(a.v, v);
 #pragma unroll
@@ -108,10 +124,9 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
         sv[p] = fma2(q[p], z[p], sv[p]);
         q[p] = mul2(q[p], v[p]);
         s0 = fma2(q[p], z[p], s0);
-        s1 = add2(s1, q[p]);
       }
-      float s[2] = {sum2(s0), sum2(s1)};
-      row_sum<2>(s, buf, turn);
+      float s[2] = {sum2(s0), 0.0f};
+      both_sums(layer, q, s, buf, turn);
       // what cancels does so before it is scaled
       const float2 m = two(-s[0] * inv_h), mean = two(layer ? -s[1] * inv_h : 0.0f);
 #pragma unroll
@@ -131,17 +146,16 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
     if (!block) continue;
     it.params(a.w, w);
     if (layer) it.clear(d);
-    float2 s0 = two(0.0f), s1 = two(0.0f);
+    float2 s0 = two(0.0f);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       u[p] = mul2(u[p], two(ru));  // uhat
       sw[p] = fma2(d[p], u[p], sw[p]);
       d[p] = mul2(d[p], w[p]);
       s0 = fma2(d[p], u[p], s0);
-      s1 = add2(s1, d[p]);
     }
-    float s[2] = {sum2(s0), sum2(s1)};
-    row_sum<2>(s, buf, turn);
+    float s[2] = {sum2(s0), 0.0f};
+    both_sums(layer, d, s, buf, turn);
     if (threadIdx.x == 0) sa += (double)s[0];
     // alpha stands outside, so that dalpha's sum needs no division
     const float ar = alpha * ru;
@@ -270,7 +284,7 @@ cudaError_t back_t(const glr_join_backward_args& a, cudaStream_t s) {
     if (a.H <= 16 * 512) return back_n<T, W, 16 / W, kKept, 512, 512>(a, s);
     return back_n<T, W, 16 / W, kKept, 1024, 1024>(a, s);
   }
-  if (a.H <= 8 * 128) return back_n<T, 1, 8, kKept, 128, 640>(a, s);
+  if (a.H <= 6 * 128) return back_n<T, 1, 6, kKept, 128, 640>(a, s);
   if (a.H <= 16 * 256) return back_n<T, 1, 16, kKept, 256, 512>(a, s);
   return back_n<T, 1, 16, kKept, 1024, 1024>(a, s);
 }
