@@ -62,7 +62,7 @@ typedef struct {
  * new sequence: nothing before it, not even an infinity or a NaN, reaches it.
  * states (NULL: not kept): float32 [B, glr_states(L), H], the state before each run of
  * GLR_STATE_STEPS steps, for glr_scan_backward.
- * workspace: glr_scan_workspace_size(B, L, H) bytes, 16-byte aligned.
+ * workspace: glr_scan_workspace_size(B, L, H) bytes, 16-byte aligned (0 for short rows: none).
  * L = 0 copies h0 (or zero) to h_last. B, H >= 1; B and L < 2^31, H < 2^24.
  * Results do not depend on the order in which the GPU runs the blocks.
  */

@@ -116,7 +116,7 @@ dlr_status scan_sizes(int64_t type, int64_t B, int64_t L, int64_t H, double c) {
 }
 
 dlr_status bad_workspace(const void* ws, uint64_t bytes, size_t need) {
-  return !ws || !aligned(ws, 16) || bytes < need ? DLR_ERR_WORKSPACE : DLR_OK;
+  return need && (!ws || !aligned(ws, 16) || bytes < need) ? DLR_ERR_WORKSPACE : DLR_OK;
 }
 
 }  // namespace
@@ -157,7 +157,8 @@ dlr_status glr_scan(const glr_scan_args* args, dlr_stream_t stream) {
                      strided(a.i, a.type, a.B, a.L, a.H), flat(a.p, 4 * a.H), flat(a.h0, bh),
                      flat(a.reset, a.B * a.L)};
   const Area out[] = {strided(a.y, a.type, a.B, a.L, a.H), flat(a.h_last, bh),
-                      flat(a.states, bh * glr_states(a.L)), flat(a.workspace, (int64_t)need)};
+                      flat(a.states, bh * glr_states(a.L)),
+                      flat(need ? a.workspace : nullptr, (int64_t)need)};
   if (!distinct(out[0]) || meet(in, out)) return DLR_ERR_INVALID_ARG;
   return dlr::status_from_cuda(dlr::glr::launch_scan(a, s));
 }

@@ -257,17 +257,23 @@ __device__ __forceinline__ void advance(float (&s)[VEC], float2 (&a)[N], float2 
 }
 
 // How a tile's inputs come into shared memory and its outputs leave it. Where every row begins on a
-// 16-byte boundary and H is a whole number of 16 bytes (kTma) one thread has a whole tile moved by a tensor
-// copy, which also fills what a tile has past the ends with zeros and leaves it out on the way back.
-// Else the computing warps copy 4 bytes at a time where rows begin on 4-byte boundaries, single elements
-// where not even that holds (16-bit types with odd strides), and store for themselves.
-constexpr int kTma = 16;
+// 16-byte boundary and H is a whole number of 16 bytes, one thread has a whole tile moved by a tensor
+// copy (kTma), which also fills what a tile has past the ends with zeros and leaves it out on the way
+// back. Else, and where every block has but one tile, the computing warps copy pieces of 16, 4 or 2 bytes, the
+// widest that the rows allow, and store for themselves: a tensor copy's description costs the host
+// 1.1 us an array, and with one tile to a block its copies run beside nothing.
+constexpr int kTma = 128;
 
+template <int kBytes>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  const int n = on ? 4 : 0;  // nothing is read and zeros are written where off
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n)
-               : "memory");
+  const int n = on ? kBytes : 0;  // nothing is read and zeros are written where off
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_end() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -289,7 +295,7 @@ __device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b,
   dst += first * C + col;
   if (kBytes != 2 && t0 + kSteps <= L && h0 + C <= H) {
 #pragma unroll
-    for (int j = 0; j < kSteps; j += rows, p += dp) copy_async(dst + j * C, p, true);
+    for (int j = 0; j < kSteps; j += rows, p += dp) copy_async<kBytes>(dst + j * C, p, true);
     return;
   }
   const bool in = h0 + col < H;
@@ -299,7 +305,7 @@ __device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b,
     if constexpr (kBytes == 2)
       dst[j * C] = on ? *p : from_f<T>(0.0f);
     else
-      copy_async(dst + j * C, on ? p : v.p, on);
+      copy_async<kBytes>(dst + j * C, on ? p : v.p, on);
   }
 }
 
@@ -1164,28 +1170,46 @@ cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// whether every block of a call has one tile at most
+template <typename T>
+bool one_each(int64_t B, int64_t L, int64_t H, int64_t steps) {
+  int dev = 0, sms = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+         B * ((L - 1) / steps + 1) * ((H - 1) / (32 * kVec<T>) + 1) <= sms;
+}
+
 template <typename T>
 cudaError_t scan_t(const glr_scan_args& a, cudaStream_t s) {
   const int64_t z = sizeof(T);
   auto tma = [&](const auto& v) { return can_describe(v, z, a.B, a.L); };
-  if (a.H * z % 16 == 0 && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.y)) return scan_w<T, kTma>(a, s);
-  if constexpr (sizeof(T) == 2)
-    if (a.H % 2 || !wide(a.x, 2, 4) || !wide(a.r, 2, 4) || !wide(a.i, 2, 4) || !wide(a.y, 2, 4))
-      return scan_w<T, 2>(a, s);
-  return scan_w<T, 4>(a, s);
+  auto all = [&](int64_t n) {
+    return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
+           wide(a.y, z, n);
+  };
+  if (all(16) && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.y) &&
+      !one_each<T>(a.B, a.L, a.H, kScanTile))
+    return scan_w<T, kTma>(a, s);
+  if (all(16)) return scan_w<T, 16>(a, s);
+  if (all(4)) return scan_w<T, 4>(a, s);
+  if constexpr (sizeof(T) == 2) return scan_w<T, 2>(a, s);
+  return cudaErrorInvalidValue;  // not reached: float rows begin on 4-byte boundaries
 }
 template <typename T>
 cudaError_t back_t(const glr_scan_backward_args& a, cudaStream_t s) {
   const int64_t z = sizeof(T);
   auto tma = [&](const auto& v) { return can_describe(v, z, a.B, a.L); };
-  if (a.H * z % 16 == 0 && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.dy) && tma(a.dx) && tma(a.dr) &&
-      tma(a.di))
+  auto all = [&](int64_t n) {
+    return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
+           wide(a.dy, z, n) && wide(a.dx, z, n) && wide(a.dr, z, n) && wide(a.di, z, n);
+  };
+  if (all(16) && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.dy) && tma(a.dx) && tma(a.dr) &&
+      tma(a.di) && !one_each<T>(a.B, a.L, a.H, kBackTile))
     return back_w<T, kTma>(a, s);
-  if constexpr (sizeof(T) == 2)
-    if (a.H % 2 || !wide(a.x, 2, 4) || !wide(a.r, 2, 4) || !wide(a.i, 2, 4) || !wide(a.dy, 2, 4) ||
-        !wide(a.dx, 2, 4) || !wide(a.dr, 2, 4) || !wide(a.di, 2, 4))
-      return back_w<T, 2>(a, s);
-  return back_w<T, 4>(a, s);
+  if (all(16)) return back_w<T, 16>(a, s);
+  if (all(4)) return back_w<T, 4>(a, s);
+  if constexpr (sizeof(T) == 2) return back_w<T, 2>(a, s);
+  return cudaErrorInvalidValue;  // not reached, as above
 }
 
 template <typename T>
@@ -1201,7 +1225,7 @@ cudaError_t step_t(const glr_step_args& a, cudaStream_t s) {
 
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H) {
   const Space sp(B, L, H, kScanTile);
-  return sp.head + sp.maps + sp.in;
+  return sp.tiles <= 1 ? 0 : sp.head + sp.maps + sp.in;
 }
 size_t scan_backward_workspace_bytes(int64_t B, int64_t L, int64_t H) {
   const Space sp(B, L, H, kBackTile);

@@ -67,81 +67,99 @@ def _ok(fn: str, status: int):
         raise _dlr.DLRError(fn, status)
 
 
-def _stream(stream, device):
+def _stream(stream, dev: int):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _on(stream):
     """Allocations for a call on ``stream`` come from that stream's memory."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _act_type(t) -> int:
-    if not t.is_cuda or t.dtype not in TYPE:
+    kind = TYPE.get(t.dtype)
+    if kind is None or not t.is_cuda:
         raise TypeError("expected float32, bfloat16 or float16 CUDA tensors")
-    return TYPE[t.dtype]
+    return kind
 
 
-def _view3(t, like, what: str):
-    """(pointer, stride_b, stride_t) of an activation [B, L, H] shaped as ``like``."""
+def _wrong(t, like, shape, what: str):
+    """Says what is wrong with a tensor that a check below turned down."""
     if t.dtype != like.dtype or t.device != like.device:
         raise TypeError(f"{what}: expected {like.dtype} on {like.device}")
-    if t.shape != like.shape:
-        raise ValueError(f"{what}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{what}: channels must be contiguous")
+
+
+def _view3(t, like, dtype, dev, shape, what: str):
+    """(pointer, stride_b, stride_t) of an activation [B, L, H]."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _wrong(t, like, shape, what)
     sb, st, sh = t.stride()
-    if sh != 1 and t.shape[2] > 1:
-        raise ValueError(f"{what}: channels must be contiguous")
+    if sh != 1 and shape[2] > 1:
+        _wrong(t, like, shape, what)
     return t.data_ptr(), sb, st
 
 
-def _view2(t, like, what: str):
-    """The same for rows [M, H]: (pointer, 0, stride_t)."""
+def _view2(t, like, dtype, dev, shape, what: str):
+    """The same for rows [M, H]: (pointer, 0, stride_t); nothing for None."""
     if t is None:
         return _NONE3
-    if t.dtype != like.dtype or t.device != like.device:
-        raise TypeError(f"{what}: expected {like.dtype} on {like.device}")
-    if t.shape != like.shape:
-        raise ValueError(f"{what}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _wrong(t, like, shape, what)
     st, sh = t.stride()
-    if sh != 1 and t.shape[1] > 1:
-        raise ValueError(f"{what}: channels must be contiguous")
+    if sh != 1 and shape[1] > 1:
+        _wrong(t, like, shape, what)
     return t.data_ptr(), 0, st
 
 
-def _f32(t, shape, like, what: str) -> int:
+def _f32(t, shape, dev, what: str) -> int:
     if t is None:
         return 0
-    if t.dtype != torch.float32 or t.device != like.device or not t.is_contiguous():
-        raise TypeError(f"{what}: expected a contiguous float32 tensor on {like.device}")
+    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
+        raise TypeError(f"{what}: expected a contiguous float32 tensor on cuda:{dev}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _bytes(t, shape, like, what: str) -> int:
+def _bytes(t, shape, dev, what: str) -> int:
     if t is None:
         return 0
-    if t.dtype not in (torch.uint8, torch.bool) or t.device != like.device or \
+    if t.dtype not in (torch.uint8, torch.bool) or t.get_device() != dev or \
             not t.is_contiguous():
-        raise TypeError(f"{what}: expected a contiguous bool or uint8 tensor on {like.device}")
+        raise TypeError(f"{what}: expected a contiguous bool or uint8 tensor on cuda:{dev}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _workspace(workspace, need: int, like):
+class _NoSpace:
+    """Stands for a workspace of no bytes."""
+    data_ptr = staticmethod(lambda: 0)
+    numel = staticmethod(lambda: 0)
+
+
+_NO_SPACE = _NoSpace()
+
+
+def _workspace(workspace, need: int, x):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    if workspace.dtype != torch.uint8 or workspace.device != like.device or \
+        return torch.empty(need, dtype=torch.uint8, device=x.device) if need else _NO_SPACE
+    if workspace.dtype != torch.uint8 or workspace.device != x.device or \
             not workspace.is_contiguous():
         raise TypeError("workspace: expected a contiguous uint8 tensor on the same device")
     return workspace
 
 
 def glr_scan_workspace_size(B: int, L: int, H: int) -> int:
-    """Bytes of device workspace glr_scan needs (0 for sizes out of range)."""
+    """Bytes of device workspace glr_scan needs (0: none, or sizes out of range)."""
     return int(_load().glr_scan_workspace_size(B, L, H))
 
 
@@ -165,18 +183,21 @@ def glr_scan(x, r, i, p, scale: float = 8.0, h0=None, reset=None, save_states: b
     lib, kind = _load(), _act_type(x)
     if x.dim() != 3:
         raise ValueError("x: expected [B, L, H]")
-    B, L, H = x.shape
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    B, L, H = shape
     with _on(stream):
-        y = torch.empty((B, L, H), dtype=x.dtype, device=x.device) if out is None else out
+        y = torch.empty_like(x) if out is None else out
         h_last = torch.empty((B, H), dtype=torch.float32, device=x.device)
         states = torch.empty((B, (L + STATE_STEPS - 1) // STATE_STEPS, H), dtype=torch.float32,
                              device=x.device) if save_states else None
         ws = _workspace(workspace, lib.glr_scan_workspace_size(B, L, H), x)
-    args = _SCAN(kind, B, L, H, scale, *_view3(x, x, "x"), *_view3(r, x, "r"), *_view3(i, x, "i"),
-                 _f32(p, (H,), x, "p"), _f32(h0, (B, H), x, "h0"),
-                 _bytes(reset, (B, L), x, "reset"), *_view3(y, x, "out"), h_last.data_ptr(),
-                 0 if states is None else states.data_ptr(), ws.data_ptr(), ws.numel())
-    _ok("glr_scan", lib.glr_scan(args, _stream(stream, x.device)))
+    args = _SCAN(kind, B, L, H, scale, *_view3(x, x, dtype, dev, shape, "x"),
+                 *_view3(r, x, dtype, dev, shape, "r"), *_view3(i, x, dtype, dev, shape, "i"),
+                 _f32(p, (H,), dev, "p"), _f32(h0, (B, H), dev, "h0"),
+                 _bytes(reset, (B, L), dev, "reset"), *_view3(y, x, dtype, dev, shape, "out"),
+                 h_last.data_ptr(), 0 if states is None else states.data_ptr(), ws.data_ptr(),
+                 ws.numel())
+    _ok("glr_scan", lib.glr_scan(args, _stream(stream, dev)))
     return (y, h_last, states) if save_states else (y, h_last)
 
 
@@ -189,22 +210,27 @@ def glr_scan_backward(x, r, i, p, dy, states, scale: float = 8.0, h0=None, reset
     lib, kind = _load(), _act_type(x)
     if x.dim() != 3:
         raise ValueError("x: expected [B, L, H]")
-    B, L, H = x.shape
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    B, L, H = shape
     n = (L + STATE_STEPS - 1) // STATE_STEPS
     with _on(stream):
-        dx, dr, di = out if out is not None else (
-            torch.empty((B, L, H), dtype=x.dtype, device=x.device) for _ in range(3))
+        dx, dr, di = out if out is not None else (torch.empty_like(x), torch.empty_like(x),
+                                                  torch.empty_like(x))
         dp = torch.empty((H,), dtype=torch.float32, device=x.device)
         dh0 = None if h0 is None else torch.empty_like(h0)
         ws = _workspace(workspace, lib.glr_scan_backward_workspace_size(B, L, H), x)
-    args = _SCAN_BACK(kind, B, L, H, scale, *_view3(x, x, "x"), *_view3(r, x, "r"),
-                      *_view3(i, x, "i"), *_view3(dy, x, "dy"), _f32(p, (H,), x, "p"),
-                      _f32(h0, (B, H), x, "h0"), _bytes(reset, (B, L), x, "reset"),
-                      _f32(states, (B, n, H), x, "states"),
-                      _f32(dh_last, (B, H), x, "dh_last"), *_view3(dx, x, "dx"),
-                      *_view3(dr, x, "dr"), *_view3(di, x, "di"), dp.data_ptr(),
+    args = _SCAN_BACK(kind, B, L, H, scale, *_view3(x, x, dtype, dev, shape, "x"),
+                      *_view3(r, x, dtype, dev, shape, "r"),
+                      *_view3(i, x, dtype, dev, shape, "i"),
+                      *_view3(dy, x, dtype, dev, shape, "dy"), _f32(p, (H,), dev, "p"),
+                      _f32(h0, (B, H), dev, "h0"), _bytes(reset, (B, L), dev, "reset"),
+                      _f32(states, (B, n, H), dev, "states"),
+                      _f32(dh_last, (B, H), dev, "dh_last"),
+                      *_view3(dx, x, dtype, dev, shape, "dx"),
+                      *_view3(dr, x, dtype, dev, shape, "dr"),
+                      *_view3(di, x, dtype, dev, shape, "di"), dp.data_ptr(),
                       0 if dh0 is None else dh0.data_ptr(), ws.data_ptr(), ws.numel())
-    _ok("glr_scan_backward", lib.glr_scan_backward(args, _stream(stream, x.device)))
+    _ok("glr_scan_backward", lib.glr_scan_backward(args, _stream(stream, dev)))
     return dx, dr, di, dp, dh0
 
 
@@ -215,20 +241,21 @@ def glr_step(x, r, i, p, h, scale: float = 8.0, reset=None, h_out=None, out=None
     lib, kind = _load(), _act_type(x)
     if x.dim() != 2:
         raise ValueError("x: expected [B, H]")
-    B, H = x.shape
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    B, H = shape
     if out is None:
         with _on(stream):
-            out = torch.empty((B, H), dtype=x.dtype, device=x.device)
+            out = torch.empty_like(x)
     if h_out is None:
         h_out = h
-    xp, _, xs = _view2(x, x, "x")
-    rp, _, rs = _view2(r, x, "r")
-    ip, _, is_ = _view2(i, x, "i")
-    yp, _, ys = _view2(out, x, "out")
-    args = _STEP(kind, B, H, scale, xp, xs, 0, rp, rs, 0, ip, is_, 0, _f32(p, (H,), x, "p"),
-                 _f32(h, (B, H), x, "h"), _bytes(reset, (B,), x, "reset"), yp, ys, 0,
-                 _f32(h_out, (B, H), x, "h_out"))
-    _ok("glr_step", lib.glr_step(args, _stream(stream, x.device)))
+    xp, _, xs = _view2(x, x, dtype, dev, shape, "x")
+    rp, _, rs = _view2(r, x, dtype, dev, shape, "r")
+    ip, _, is_ = _view2(i, x, dtype, dev, shape, "i")
+    yp, _, ys = _view2(out, x, dtype, dev, shape, "out")
+    args = _STEP(kind, B, H, scale, xp, xs, 0, rp, rs, 0, ip, is_, 0, _f32(p, (H,), dev, "p"),
+                 _f32(h, shape, dev, "h"), _bytes(reset, (B,), dev, "reset"), yp, ys, 0,
+                 _f32(h_out, shape, dev, "h_out"))
+    _ok("glr_step", lib.glr_step(args, _stream(stream, dev)))
     return out
 
 
@@ -245,11 +272,11 @@ def _new_ckpt(M, H, device) -> Ckpt8:
                              device=device))
 
 
-def _ckpt_ptrs(c: Optional[Ckpt8], M, H, like, what: str):
+def _ckpt_ptrs(c: Optional[Ckpt8], M, H, dev, what: str):
     if c is None:
         return 0, 0
-    return (_bytes(c[0], (M, H), like, what + " codes"),
-            _bytes(c[1], (M, (H + CKPT_GROUP - 1) // CKPT_GROUP), like, what + " scales"))
+    return (_bytes(c[0], (M, H), dev, what + " codes"),
+            _bytes(c[1], (M, (H + CKPT_GROUP - 1) // CKPT_GROUP), dev, what + " scales"))
 
 
 def glr_ckpt_pack(t, stream=None) -> Ckpt8:
@@ -257,32 +284,31 @@ def glr_ckpt_pack(t, stream=None) -> Ckpt8:
     lib, kind = _load(), _act_type(t)
     if t.dim() != 2:
         raise ValueError("t: expected [M, H]")
+    dev = t.get_device()
     M, H = t.shape
-    p, _, st = _view2(t, t, "t")
+    p, _, st = _view2(t, t, t.dtype, dev, t.shape, "t")
     with _on(stream):
         c = _new_ckpt(M, H, t.device)
-    _ok("glr_ckpt_pack", lib.glr_ckpt_pack(kind, M, H, p, st, c.codes.data_ptr(),
-                                           c.scales.data_ptr(), _stream(stream, t.device)))
+    _ok("glr_ckpt_pack", lib.glr_ckpt_pack(kind, M, H, p, st, c[0].data_ptr(), c[1].data_ptr(),
+                                           _stream(stream, dev)))
     return c
 
 
 def glr_ckpt_unpack(c: Ckpt8, dtype=torch.float32, out=None, stream=None):
     """The values [M, H] that an 8-bit checkpoint stands for, in ``dtype`` (or into ``out``)."""
     lib = _load()
-    codes, scales = c
+    codes = c[0]
     if not codes.is_cuda or codes.dim() != 2:
         raise TypeError("codes: expected a CUDA tensor [M, H]")
+    dev = codes.get_device()
     M, H = codes.shape
     if out is None:
         with _on(stream):
             out = torch.empty((M, H), dtype=dtype, device=codes.device)
     kind = _act_type(out)
-    if out.shape != codes.shape:
-        raise ValueError("out: expected the shape of the codes")
-    cp, sp = _ckpt_ptrs(c, M, H, codes, "c")
-    p, _, st = _view2(out, out, "out")
-    _ok("glr_ckpt_unpack", lib.glr_ckpt_unpack(kind, M, H, cp, sp, p, st,
-                                               _stream(stream, codes.device)))
+    cp, sp = _ckpt_ptrs(c, M, H, dev, "c")
+    p, _, st = _view2(out, out, out.dtype, dev, codes.shape, "out")
+    _ok("glr_ckpt_unpack", lib.glr_ckpt_unpack(kind, M, H, cp, sp, p, st, _stream(stream, dev)))
     return out
 
 
@@ -297,22 +323,28 @@ def glr_join(x, h, g, w, alpha, v, norm: str = "rms", act: str = "silu", eps: fl
     lib, kind = _load(), _act_type(x)
     if x.dim() != 2:
         raise ValueError("x: expected rows [M, H]")
-    M, H = x.shape
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    M, H = shape
     if act == "none" and g is not None:
         raise ValueError('g: must be None with act="none"')
     if h is None and (g is not None or w is not None or alpha is not None or ckpt):
         raise ValueError("g, w, alpha and ckpt need h")
+    hc = gc = None
     with _on(stream):
-        y, n = out if out is not None else (
-            None if h is None else torch.empty((M, H), dtype=x.dtype, device=x.device),
-            None if v is None else torch.empty((M, H), dtype=x.dtype, device=x.device))
-        hc = _new_ckpt(M, H, x.device) if ckpt else None
-        gc = _new_ckpt(M, H, x.device) if ckpt and g is not None else None
-    args = _JOIN(kind, M, H, NORM[norm], ACT[act], eps, *_view2(x, x, "x"), *_view2(h, x, "h"),
-                 *_view2(g, x, "g"), _f32(w, (H,), x, "w"), _f32(alpha, (1,), x, "alpha"),
-                 _f32(v, (H,), x, "v"), *_view2(y, x, "y"), *_view2(n, x, "n"),
-                 *_ckpt_ptrs(hc, M, H, x, "h"), *_ckpt_ptrs(gc, M, H, x, "g"))
-    _ok("glr_join", lib.glr_join(args, _stream(stream, x.device)))
+        if out is not None:
+            y, n = out
+        else:
+            y = None if h is None else torch.empty_like(x)
+            n = None if v is None else torch.empty_like(x)
+        if ckpt:
+            hc = _new_ckpt(M, H, x.device)
+            gc = None if g is None else _new_ckpt(M, H, x.device)
+    args = _JOIN(kind, M, H, NORM[norm], ACT[act], eps, *_view2(x, x, dtype, dev, shape, "x"),
+                 *_view2(h, x, dtype, dev, shape, "h"), *_view2(g, x, dtype, dev, shape, "g"),
+                 _f32(w, (H,), dev, "w"), _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"),
+                 *_view2(y, x, dtype, dev, shape, "y"), *_view2(n, x, dtype, dev, shape, "n"),
+                 *_ckpt_ptrs(hc, M, H, dev, "h"), *_ckpt_ptrs(gc, M, H, dev, "g"))
+    _ok("glr_join", lib.glr_join(args, _stream(stream, dev)))
     return (y, n, (hc, gc)) if ckpt else (y, n)
 
 
@@ -326,24 +358,35 @@ def glr_join_backward(dy, dn, x, h, g, w, alpha, v, norm: str = "rms", act: str 
     lib, kind = _load(), _act_type(x)
     if x.dim() != 2:
         raise ValueError("x: expected rows [M, H]")
-    M, H = x.shape
-    block, gated = w is not None, w is not None and act != "none"
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    M, H = shape
+    block = w is not None
     hc, gc = ckpt if ckpt is not None else (None, None)
+    dw = dalpha = dv = None
     with _on(stream):
-        dx, dh, dg = out if out is not None else (
-            torch.empty((M, H), dtype=x.dtype, device=x.device) if on else None
-            for on in (True, block, gated))
-        dw, dalpha = (torch.empty((k,), dtype=torch.float32, device=x.device) if block else None
-                      for k in (H, 1))
-        dv = torch.empty((H,), dtype=torch.float32, device=x.device) if v is not None else None
+        if out is not None:
+            dx, dh, dg = out
+        else:
+            dx = torch.empty_like(x)
+            dh = torch.empty_like(x) if block else None
+            dg = torch.empty_like(x) if block and act != "none" else None
+        if block:
+            dw = torch.empty_like(w)
+            dalpha = torch.empty((1,), dtype=torch.float32, device=x.device)
+        if v is not None:
+            dv = torch.empty_like(v)
         ws = _workspace(workspace, lib.glr_join_backward_workspace_size(M, H), x)
-    args = _JOIN_BACK(kind, M, H, NORM[norm], ACT[act], eps, *_view2(dy, x, "dy"),
-                      *_view2(dn, x, "dn"), *_view2(x, x, "x"), *_view2(h, x, "h"),
-                      *_view2(g, x, "g"), *_ckpt_ptrs(hc, M, H, x, "h"),
-                      *_ckpt_ptrs(gc, M, H, x, "g"), _f32(w, (H,), x, "w"),
-                      _f32(alpha, (1,), x, "alpha"), _f32(v, (H,), x, "v"), *_view2(dx, x, "dx"),
-                      *_view2(dh, x, "dh"), *_view2(dg, x, "dg"),
-                      0 if dw is None else dw.data_ptr(), 0 if dalpha is None else dalpha.data_ptr(),
-                      0 if dv is None else dv.data_ptr(), ws.data_ptr(), ws.numel())
-    _ok("glr_join_backward", lib.glr_join_backward(args, _stream(stream, x.device)))
+    args = _JOIN_BACK(kind, M, H, NORM[norm], ACT[act], eps,
+                      *_view2(dy, x, dtype, dev, shape, "dy"),
+                      *_view2(dn, x, dtype, dev, shape, "dn"),
+                      *_view2(x, x, dtype, dev, shape, "x"), *_view2(h, x, dtype, dev, shape, "h"),
+                      *_view2(g, x, dtype, dev, shape, "g"), *_ckpt_ptrs(hc, M, H, dev, "h"),
+                      *_ckpt_ptrs(gc, M, H, dev, "g"), _f32(w, (H,), dev, "w"),
+                      _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"),
+                      *_view2(dx, x, dtype, dev, shape, "dx"),
+                      *_view2(dh, x, dtype, dev, shape, "dh"),
+                      *_view2(dg, x, dtype, dev, shape, "dg"), _f32(dw, (H,), dev, "dw"),
+                      0 if dalpha is None else dalpha.data_ptr(), _f32(dv, (H,), dev, "dv"),
+                      ws.data_ptr(), ws.numel())
+    _ok("glr_join_backward", lib.glr_join_backward(args, _stream(stream, dev)))
     return dx, dh, dg, dw, dalpha, dv

@@ -38,7 +38,8 @@ def test_sizes(lib):
     assert lib.glr_scan_workspace_size(0, 10, 10) == 0
     assert lib.glr_scan_workspace_size(1, 10, 0) == 0
     assert lib.glr_scan_workspace_size(1, 1 << 31, 1) == 0
-    assert lib.glr_scan_workspace_size(2, 100, 64) > 0
+    assert lib.glr_scan_workspace_size(2, 200, 64) > 0
+    assert lib.glr_scan_workspace_size(2, 8, 64) == 0           # a row that one block takes
     assert lib.glr_scan_backward_workspace_size(2, 100, 64) > 0
     assert lib.glr_join_backward_workspace_size(5, 16385) == 0
     assert lib.glr_join_backward_workspace_size(5, 1024) > 0
@@ -48,8 +49,8 @@ def test_sizes(lib):
 A = [k << 40 for k in range(1, 20)]
 
 
-def scan(type=1, B=2, L=100, H=64, c=8.0, x=(A[0], 6400, 64), r=(A[1], 6400, 64), i=(A[2], 6400, 64),
-         p=A[3], h0=0, reset=0, y=(A[4], 6400, 64), h_last=A[5], states=A[6], ws=A[7],
+def scan(type=1, B=2, L=200, H=64, c=8.0, x=(A[0], 12800, 64), r=(A[1], 12800, 64),
+         i=(A[2], 12800, 64), p=A[3], h0=0, reset=0, y=(A[4], 12800, 64), h_last=A[5], states=A[6], ws=A[7],
          n=1 << 30):
     return struct.pack("4qd19q", type, B, L, H, c, *x, *r, *i, p, h0, reset, *y, h_last, states,
                        ws, n)
@@ -58,14 +59,14 @@ def scan(type=1, B=2, L=100, H=64, c=8.0, x=(A[0], 6400, 64), r=(A[1], 6400, 64)
 @pytest.mark.parametrize("status,change", [
     (INVALID, {"type": 3}), (INVALID, {"B": 0}), (INVALID, {"L": -1}), (INVALID, {"H": 0}),
     (INVALID, {"c": -1.0}), (INVALID, {"c": float("nan")}), (INVALID, {"c": 1e300}),
-    (INVALID, {"x": (0, 6400, 64)}), (INVALID, {"x": (A[0] + 1, 6400, 64)}),
+    (INVALID, {"x": (0, 12800, 64)}), (INVALID, {"x": (A[0] + 1, 12800, 64)}),
     (INVALID, {"r": (A[1], -1, 64)}), (INVALID, {"p": 0}), (INVALID, {"p": A[3] + 2}),
-    (INVALID, {"h0": A[8] + 1}), (INVALID, {"y": (A[4], 6400, 63)}),   # its rows meet
-    (INVALID, {"y": (A[4], 64, 64)}), (INVALID, {"y": (A[0], 6400, 64)}),
-    (INVALID, {"y": (A[0] + 64, 6400, 64)}), (INVALID, {"h_last": A[6]}),
+    (INVALID, {"h0": A[8] + 1}), (INVALID, {"y": (A[4], 12800, 63)}),   # its rows meet
+    (INVALID, {"y": (A[4], 64, 64)}), (INVALID, {"y": (A[0], 12800, 64)}),
+    (INVALID, {"y": (A[0] + 64, 12800, 64)}), (INVALID, {"h_last": A[6]}),
     (INVALID, {"states": A[7]}), (INVALID, {"h0": A[5]}),
     # columns of one buffer that meet: 64 wide, 63 apart
-    (INVALID, {"x": (A[0], 12800, 128), "y": (A[0] + 2 * 63, 12800, 128)}),
+    (INVALID, {"x": (A[0], 25600, 128), "y": (A[0] + 2 * 63, 25600, 128)}),
     (UNSUPPORTED, {"L": 1 << 31}), (UNSUPPORTED, {"H": (1 << 24) + 1}),
     (UNSUPPORTED, {"B": 1 << 30}),
     (WORKSPACE, {"ws": 0}), (WORKSPACE, {"ws": A[7] + 8}), (WORKSPACE, {"n": 16}),

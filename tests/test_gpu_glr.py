@@ -564,7 +564,7 @@ def test_refusals():
         glr.glr_scan(x, r, i, p, out=torch.empty(1, L, H, dtype=x.dtype,
                                                  device="cuda").expand(B, L, H))
     with pytest.raises(dlr.DLRError):
-        glr.glr_scan(x, r, i, p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        glr.glr_scan(*(t.repeat(1, 20, 1) for t in (x, r, i)), p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     w, al = torch.ones(H, device="cuda"), torch.ones(1, device="cuda")
     a = [t.reshape(B * L, H) for t in (x, r, i)]
     with pytest.raises(KeyError):
