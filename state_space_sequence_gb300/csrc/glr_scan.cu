@@ -87,7 +87,7 @@ struct Job {
   const float* p;
   const uint8_t* reset;
   float* in;    // [B, tiles, HP]: the value that enters each tile but the chain's first
-  float* maps;  // [B, tiles, HP, 2]: each tile's map (A, e)
+  float* maps;  // [B, tiles, HP / VEC, 2, VEC]: each tile's map, VEC of A and VEC of e
   uint32_t* head;
   int* status;
   int64_t B, L, H, HP, chains;
@@ -128,91 +128,168 @@ __device__ __forceinline__ Tile tile_of(const J& q, uint32_t k, bool backwards) 
   return at;
 }
 
+// s through a map (A, e): A s + e
+template <int VEC>
+__device__ __forceinline__ void through(const float (&A)[VEC], const float (&e)[VEC], float (&s)[VEC]) {
+  if constexpr (VEC == 2) {
+    const float2 t = fma2(make_float2(A[0], A[1]), make_float2(s[0], s[1]), make_float2(e[0], e[1]));
+    s[0] = t.x, s[1] = t.y;
+  } else {
+    s[0] = fmaf(A[0], s[0], e[0]);
+  }
+}
+template <int N>
+__device__ __forceinline__ bool any_empty(const float (&v)[N]) {
+  bool is = false;
+#pragma unroll
+  for (int k = 0; k < N; ++k) is |= empty(v[k]);
+  return __any_sync(0xffffffffu, is);
+}
+
+// The limit of a chain's waits.
+struct Patience {
+  uint64_t t0 = 0;
+  bool gone = false;
+  __device__ __forceinline__ bool ends() {  // called by whole warps
+    const uint64_t t = timer_ns();
+    if (t0 == 0) t0 = t;
+    gone = __any_sync(0xffffffffu, t - t0 > kWaitNs);
+    return gone;
+  }
+};
+
 // Called by one warp: the value s that enters the tile, and `end`, the one that leaves it, from
 // the tile's map (A, e); `cut`: the map does not depend on what enters. row: the lane's first
 // element of `in`; dir = 1 forwards, -1 backwards. The first tile of the chain has its s.
 //
-// It looks at four tiles at a time for the nearest one whose end value is there, all maps between
-// being there too; the first tile of a chain always comes to its end value by itself.
+// Each lane looks at one of the 32 tiles before this one, at the group's first channel, for the
+// nearest whose end value is there with all maps between there too; the first tile of a chain always
+// comes to its end value by itself. With the same loads comes the end value of the tile just before
+// for the lane's own channels, which many chains side by side mostly find; else that end value
+// and the maps are read then.
 template <int VEC, typename J>
 __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, int dir,
                                       const float (&A)[VEC], const float (&e)[VEC], bool cut,
                                       float (&s)[VEC], float (&end)[VEC]) {
   constexpr int U = 4;
+  const int lane = threadIdx.x & 31;
   const int done = dir > 0 ? at.tile : q.tiles - 1 - at.tile;  // tiles of the chain before this
   const bool last = done == q.tiles - 1;
   const int64_t step = dir * q.HP;
   if (done > 0) {
-    if (!last && cut) {
-      post(q.in + row + step, e);
-    } else if (!last) {
-      float m[2 * VEC];
+    float m[2 * VEC];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) m[2 * v] = A[v], m[2 * v + 1] = e[v];
-      post(q.maps + 2 * row, m);
-    }
-    const float* in = q.in + row;               // what enters this tile: the end of the one before
+    for (int v = 0; v < VEC; ++v) m[v] = A[v], m[VEC + v] = e[v];
+    if (!last && cut) post(q.in + row + step, e);
+    if (!last && !cut) post(q.maps + 2 * row, m);
+    const float* in = q.in + row;                   // what enters this tile: the end of the one before
     const float* maps = q.maps + 2 * (row - step);  // of the one before
-    float ends[U][VEC], m[U][2 * VEC];
-    uint64_t t0 = 0;
-    int far = 0;  // tiles back whose maps come into it
+    Patience wait;
+    int far = 0;           // maps between the nearest end and this tile
+    bool at_hand = false;  // none, and s has been read
     for (bool found = false; !found;) {
+      const int k = far + lane;
+      float has_end[1] = {0.0f}, has_map[1] = {0.0f};
+      if (k < done) {
+        look(in - lane * VEC - k * step, has_end);
+        look(maps - 2 * (lane * VEC + k * step), has_map);
+      }
+      if (far == 0) look(in, s);
+      const uint32_t ends = __ballot_sync(0xffffffffu, k < done && !empty(has_end[0]));
+      const uint32_t there = __ballot_sync(0xffffffffu, k < done && !empty(has_map[0]));
+      const int l = ends ? __ffs(ends) - 1 : 32;
+      const uint32_t before = l == 32 ? 0xffffffffu : (1u << l) - 1u;
+      if ((there & before) != before) {
+        if (wait.ends()) break;
+        continue;
+      }
+      far += l;
+      found = l < 32;
+      if (far == 0) at_hand = !any_empty(s);
+    }
+    // the end value with the first maps, then the others
+    for (int k = far - 1; !at_hand; k -= U) {
+      float t[U][2 * VEC], first[VEC];
+      bool is;
+      do {
+        is = false;
+        if (k == far - 1) look(in - far * step, first);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k >= u) look(maps - 2 * (k - u) * step, t[u]);
+        if (k == far - 1)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) is |= empty(first[v]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k >= u)
+#pragma unroll
+            for (int v = 0; v < 2 * VEC; ++v) is |= empty(t[u][v]);
+      } while (__any_sync(0xffffffffu, is) && !wait.ends());
+      if (k == far - 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = first[v];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (far + u >= done) continue;
-        look(in - (far + u) * step, ends[u]);
-        look(maps - 2 * (far + u) * step, m[u]);
+        if (k < u) continue;
+        float a[VEC], b[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) a[v] = t[u][v], b[v] = t[u][VEC + v];
+        through<VEC>(a, b, s);
       }
-      int more = 0;  // of these, maps that are there before the first end
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (found || more < u || far + u >= done) continue;
-        bool no_end = false, no_map = false;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          no_end |= empty(ends[u][v]);
-          no_map |= empty(m[u][2 * v]) || empty(m[u][2 * v + 1]);
-        }
-        if (!__any_sync(0xffffffffu, no_end)) {
-          found = true;
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) s[v] = ends[u][v];
-        } else if (!__any_sync(0xffffffffu, no_map)) {
-          more = u + 1;
-        }
-      }
-      if (found && far == 0) {  // the maps are at hand
-#pragma unroll
-        for (int u = U - 2; u >= 0; --u)
-          if (u < more)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s[v] = fmaf(m[u][2 * v], s[v], m[u][2 * v + 1]);
-        break;
-      }
-      far += more;
-      if (found || more == U) continue;
-      const uint64_t t = timer_ns();
-      if (t0 == 0) t0 = t;
-      if (__any_sync(0xffffffffu, t - t0 > kWaitNs)) {
-        if ((threadIdx.x & 31) == 0) report_status(q.status, DLR_ERR_TIMEOUT);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) s[v] = 0.0f;
-        far = 0;
-        break;
-      }
+      at_hand = k < U;
     }
-#pragma unroll 8
-    for (int k = far - 1; k >= 0; --k) {
-      float t[2 * VEC];
-      look(maps - 2 * k * step, t);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) s[v] = fmaf(t[2 * v], s[v], t[2 * v + 1]);
-    }
+    if (wait.gone && lane == 0) report_status(q.status, DLR_ERR_TIMEOUT);
   }
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) end[v] = cut ? e[v] : fmaf(A[v], s[v], e[v]);
+  for (int v = 0; v < VEC; ++v) end[v] = s[v];
+  through<VEC>(A, e, end);
+  if (cut)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) end[v] = e[v];
   if (!last && !(done > 0 && cut)) post(q.in + row + step, end);
 }
+
+// The warps' maps of a tile, (A, e) of all its channels each, folded in shared memory's order by the
+// chain's warp: the tile's map, and the value that enters each warp's steps.
+template <int W, int VEC>
+struct Fold {
+  float A[W][VEC], e[W][VEC];
+  uint32_t cut;
+  template <int C>
+  __device__ __forceinline__ void read(const float (&map)[W][2][C], uint32_t cuts) {
+    const int lane = threadIdx.x & 31;
+    cut = cuts;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        A[w][v] = map[w][0][lane * VEC + v];
+        e[w][v] = map[w][1][lane * VEC + v];
+      }
+  }
+  __device__ __forceinline__ void advance(int w, float (&s)[VEC]) const {
+    through<VEC>(A[w], e[w], s);
+    if (cut && (cut >> w) & 1u)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) s[v] = e[w][v];
+  }
+  // the whole tile's map, from the first warp on or from the last
+  __device__ __forceinline__ void all(bool backwards, float (&a)[VEC], float (&b)[VEC]) const {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) a[v] = 1.0f, b[v] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      advance(backwards ? W - 1 - k : k, b);
+      if constexpr (VEC == 2) {
+        const float2 t = mul2(make_float2(a[0], a[1]), make_float2(A[k][0], A[k][1]));
+        a[0] = t.x, a[1] = t.y;
+      } else {
+        a[0] *= A[k][0];
+      }
+    }
+  }
+};
 
 // bits of the n steps from t on that begin a sequence
 __device__ __forceinline__ uint32_t cuts(const uint8_t* reset, int64_t first, int n) {
@@ -351,7 +428,7 @@ struct ScanShared {
   static constexpr int C = 32 * kVec<T>;
   T buf[2][3][kScanTile][C];        // r, i, x of two tiles
   T out[kScanTile][C];
-  float2 map[3][kScanWarps][C];     // (A, e) of each warp's steps
+  float map[3][kScanWarps][2][C];   // A and e of each warp's steps
   float enter[2][kScanWarps][C];    // the state that enters them
   float kz[kRing][C];
   uint32_t cut[3][kScanWarps];
@@ -375,17 +452,20 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   if (warp == W + 1) {
-    auto take = [&](int k) {  // the place and the decay parameters of the block's k-th tile
+    auto take = [&](int k) {  // the place of the block's k-th tile
       const uint32_t t = lane == 0 ? q.ticket(k) : 0u;
       const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), false);
       if (lane == 0) sh.tile[k % kRing] = at;
+      __syncwarp();
+    };
+    auto params = [&](int k) {  // and its decay parameters
+      const Tile at = sh.tile[k % kRing];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
         sh.kz[k % kRing][lane * VEC + v] =
             at.tile >= 0 && h < q.H ? -q.c * softplus(q.p[h]) * kLog2e : 0.0f;
       }
-      __syncwarp();
     };
     auto copy = [&](int k) {
       const Tile at = sh.tile[k % kRing];
@@ -401,14 +481,17 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       tc::mbar_init(&sh.here[1], 1);
       tc::mbar_fence_init();
     }
-    for (int k = 0; k < 3; ++k) take(k);
-    copy(0);
-    copy(1);
+    for (int k = 0; k < 3; ++k) {
+      take(k);
+      if (k < 2) copy(k);
+      params(k);
+    }
     __syncthreads();
     bar_sync(kWarpsBar, kWork + 32);
     copy(2);
     for (int k = 0; sh.tile[k % kRing].tile >= 0; ++k) {
       take(k + 3);
+      params(k + 3);
       bar_sync(kEnterBar + (k & 1), kScanThreads);
       copy(k + 3);
     }
@@ -425,34 +508,21 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       const uint32_t cut = __ballot_sync(0xffffffffu, lane < W && sh.cut[k % 3][lane % W] != 0);
       bool on[VEC];
       float A[VEC], e[VEC], s[VEC], end[VEC];
-      float2 m[W][VEC];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        on[v] = h + v < q.H && DLR_IN(at.b, q.B);
-        A[v] = 1.0f, e[v] = 0.0f;
-      }
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) m[w][v] = sh.map[k % 3][w][lane * VEC + v];
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          e[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, e[v], m[w][v].y);
-          A[v] *= m[w][v].x;
-        }
+      for (int v = 0; v < VEC; ++v) on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+      Fold<W, VEC> fold;
+      fold.read(sh.map[k % 3], cut);
+      fold.all(false, A, e);
       if (at.tile == 0)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
       chain(q, at, row, 1, A, e, cut != 0, s, end);
 #pragma unroll
-      for (int w = 0; w < W; ++w)
+      for (int w = 0; w < W; ++w) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          sh.enter[k & 1][w][lane * VEC + v] = s[v];
-          s[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, s[v], m[w][v].y);
-        }
+        for (int v = 0; v < VEC; ++v) sh.enter[k & 1][w][lane * VEC + v] = s[v];
+        fold.advance(w, s);
+      }
       bar_arrive(kEnterBar + (k & 1), kScanThreads);
       if (at.tile == q.tiles - 1 && h_last)
 #pragma unroll
@@ -530,7 +600,10 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh.map[k % 3][warp][lane * VEC + v] = make_float2(A[v], e[v]);
+    for (int v = 0; v < VEC; ++v) {
+      sh.map[k % 3][warp][0][lane * VEC + v] = A[v];
+      sh.map[k % 3][warp][1][lane * VEC + v] = e[v];
+    }
     if (lane == 0) sh.cut[k % 3][warp] = z.cut;
     bar_arrive(kMapsBar + (k & 1), kWork + 32);
   };
@@ -626,7 +699,7 @@ struct BackShared {
   static constexpr int C = 32 * kVec<T>;
   T rd[4][2][kBackTile][C];         // r, dy of four tiles; r's place takes dr
   T ix[2][2][kBackTile][C];         // i, x of two; they take di, dx
-  float2 map[3][kBackWarps][C];     // (A, C) of each warp's steps
+  float map[3][kBackWarps][2][C];   // A and C of each warp's steps
   float enter[2][kBackWarps][C];    // the gradient that enters behind them
   float sum[2][kBackWarps][C];      // their parts of dp
   float k[kRing][C];                // c softplus(p)
@@ -653,16 +726,19 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   if (warp == W + 1) {
-    auto take = [&](int k) {  // the place and the decay parameters of the block's k-th tile
+    auto take = [&](int k) {  // the place of the block's k-th tile
       const uint32_t t = lane == 0 ? q.ticket(k) : 0u;
       const Tile at = tile_of(q, __shfl_sync(0xffffffffu, t, 0), true);
       if (lane == 0) sh.tile[k % kRing] = at;
+      __syncwarp();
+    };
+    auto params = [&](int k) {  // and its decay parameters
+      const Tile at = sh.tile[k % kRing];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
         sh.k[k % kRing][lane * VEC + v] = at.tile >= 0 && h < q.H ? q.c * softplus(q.p[h]) : 0.0f;
       }
-      __syncwarp();
     };
     auto copy = [&](T* dst, uint64_t* here, int first, int k) {
       const Tile at = sh.tile[k % kRing];
@@ -696,12 +772,14 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
     for (int k = 0; k < 3; ++k) {
       take(k);
       copy_rd(k);
+      if (k == 0) copy_ix(0);
+      params(k);
     }
-    copy_ix(0);
     __syncthreads();
     int k = 0;
     for (; sh.tile[k % kRing].tile >= 0; ++k) {
       take(k + 3);
+      params(k + 3);
       bar_sync(kEnterBar + (k & 1), kBackThreads);  // all warps are done with tile k - 1
       copy_rd(k + 3);
       copy_ix(k + 1);
@@ -722,35 +800,22 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       const uint32_t cut = __ballot_sync(0xffffffffu, lane < W && sh.cut[k % 3][lane % W] != 0);
       bool on[VEC];
       float A[VEC], e[VEC], s[VEC], end[VEC];
-      float2 m[W][VEC];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        on[v] = h + v < q.H && DLR_IN(at.b, q.B);
-        A[v] = 1.0f, e[v] = 0.0f;
-      }
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) m[w][v] = sh.map[k % 3][w][lane * VEC + v];
-#pragma unroll
-      for (int w = W - 1; w >= 0; --w)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          e[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, e[v], m[w][v].y);
-          A[v] *= m[w][v].x;
-        }
+      for (int v = 0; v < VEC; ++v) on[v] = h + v < q.H && DLR_IN(at.b, q.B);
+      Fold<W, VEC> fold;
+      fold.read(sh.map[k % 3], cut);
+      fold.all(true, A, e);
       if (at.tile == q.tiles - 1)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           s[v] = dh_last && on[v] ? dh_last[at.b * q.H + h + v] : 0.0f;
       chain(q, at, row, -1, A, e, cut != 0, s, end);
 #pragma unroll
-      for (int w = W - 1; w >= 0; --w)
+      for (int w = W - 1; w >= 0; --w) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          sh.enter[k & 1][w][lane * VEC + v] = s[v];
-          s[v] = (cut >> w) & 1u ? m[w][v].y : fmaf(m[w][v].x, s[v], m[w][v].y);
-        }
+        for (int v = 0; v < VEC; ++v) sh.enter[k & 1][w][lane * VEC + v] = s[v];
+        fold.advance(w, s);
+      }
       bar_arrive(kEnterBar + (k & 1), kBackThreads);
       if (at.tile == 0 && dh0)
 #pragma unroll
@@ -835,7 +900,10 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh.map[k % 3][warp][lane * VEC + v] = make_float2(A[v], G[v]);
+    for (int v = 0; v < VEC; ++v) {
+      sh.map[k % 3][warp][0][lane * VEC + v] = A[v];
+      sh.map[k % 3][warp][1][lane * VEC + v] = G[v];
+    }
     if (lane == 0) sh.cut[k % 3][warp] = z.cut;
     bar_arrive(kMapsBar + (k & 1), kWork + 32);
   };
