@@ -171,7 +171,7 @@ template <int VEC, typename J>
 __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, int dir,
                                       const float (&A)[VEC], const float (&e)[VEC], bool cut,
                                       float (&s)[VEC], float (&end)[VEC]) {
-  constexpr int U = 4;
+  constexpr int U = VEC == 1 ? 8 : 4;  // 90 against 94 us at B1 L65536 H256 f32; 8 pairs cost registers
   const int lane = threadIdx.x & 31;
   const int done = dir > 0 ? at.tile : q.tiles - 1 - at.tile;  // tiles of the chain before this
   const bool last = done == q.tiles - 1;
@@ -216,7 +216,7 @@ __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, i
         if (k == far - 1) look(in - far * step, first);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (k >= u) look(maps - 2 * (k - u) * step, t[u]);
+          look(maps - 2 * max(k - u, 0) * step, t[u]);
         if (k == far - 1)
 #pragma unroll
           for (int v = 0; v < VEC; ++v) is |= empty(first[v]);

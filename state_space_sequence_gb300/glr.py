@@ -107,6 +107,12 @@ def _view3(t, like, dtype, dev, shape, what: str):
     return t.data_ptr(), sb, st
 
 
+def _strides3(t):
+    """The same of a tensor that is known to fit."""
+    sb, st, _ = t.stride()
+    return t.data_ptr(), sb, st
+
+
 def _view2(t, like, dtype, dev, shape, what: str):
     """The same for rows [M, H]: (pointer, 0, stride_t); nothing for None."""
     if t is None:
@@ -117,6 +123,14 @@ def _view2(t, like, dtype, dev, shape, what: str):
     if sh != 1 and shape[1] > 1:
         _wrong(t, like, shape, what)
     return t.data_ptr(), 0, st
+
+
+def _new2(x, H: int, wanted: bool):
+    """A tensor of rows for a result, and its (pointer, 0, stride_t); nothing when not wanted."""
+    if not wanted:
+        return None, _NONE3
+    t = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return t, (t.data_ptr(), 0, H)
 
 
 def _f32(t, shape, dev, what: str) -> int:
@@ -186,19 +200,21 @@ def glr_scan(x, r, i, p, scale: float = 8.0, h0=None, reset=None, save_states: b
     shape, dtype, dev = x.shape, x.dtype, x.get_device()
     B, L, H = shape
     with _on(stream):
-        y = torch.empty_like(x) if out is None else out
+        y = _strides3(out := torch.empty_like(x)) if out is None else \
+            _view3(out, x, dtype, dev, shape, "out")
         h_last = torch.empty((B, H), dtype=torch.float32, device=x.device)
         states = torch.empty((B, (L + STATE_STEPS - 1) // STATE_STEPS, H), dtype=torch.float32,
                              device=x.device) if save_states else None
         ws = _workspace(workspace, lib.glr_scan_workspace_size(B, L, H), x)
-    args = _SCAN(kind, B, L, H, scale, *_view3(x, x, dtype, dev, shape, "x"),
-                 *_view3(r, x, dtype, dev, shape, "r"), *_view3(i, x, dtype, dev, shape, "i"),
+    xv = _view3(x, x, dtype, dev, shape, "x")
+    args = _SCAN(kind, B, L, H, scale, *xv, *_view3(r, x, dtype, dev, shape, "r"),
+                 *_view3(i, x, dtype, dev, shape, "i"),
                  _f32(p, (H,), dev, "p"), _f32(h0, (B, H), dev, "h0"),
-                 _bytes(reset, (B, L), dev, "reset"), *_view3(y, x, dtype, dev, shape, "out"),
+                 _bytes(reset, (B, L), dev, "reset"), *y,
                  h_last.data_ptr(), 0 if states is None else states.data_ptr(), ws.data_ptr(),
                  ws.numel())
     _ok("glr_scan", lib.glr_scan(args, _stream(stream, dev)))
-    return (y, h_last, states) if save_states else (y, h_last)
+    return (out, h_last, states) if save_states else (out, h_last)
 
 
 def glr_scan_backward(x, r, i, p, dy, states, scale: float = 8.0, h0=None, reset=None,
@@ -214,8 +230,13 @@ def glr_scan_backward(x, r, i, p, dy, states, scale: float = 8.0, h0=None, reset
     B, L, H = shape
     n = (L + STATE_STEPS - 1) // STATE_STEPS
     with _on(stream):
-        dx, dr, di = out if out is not None else (torch.empty_like(x), torch.empty_like(x),
-                                                  torch.empty_like(x))
+        if out is None:
+            dx, dr, di = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+            outs = *_strides3(dx), *_strides3(dr), *_strides3(di)
+        else:
+            dx, dr, di = out
+            outs = (*_view3(dx, x, dtype, dev, shape, "dx"), *_view3(dr, x, dtype, dev, shape, "dr"),
+                    *_view3(di, x, dtype, dev, shape, "di"))
         dp = torch.empty((H,), dtype=torch.float32, device=x.device)
         dh0 = None if h0 is None else torch.empty_like(h0)
         ws = _workspace(workspace, lib.glr_scan_backward_workspace_size(B, L, H), x)
@@ -225,10 +246,7 @@ def glr_scan_backward(x, r, i, p, dy, states, scale: float = 8.0, h0=None, reset
                       *_view3(dy, x, dtype, dev, shape, "dy"), _f32(p, (H,), dev, "p"),
                       _f32(h0, (B, H), dev, "h0"), _bytes(reset, (B, L), dev, "reset"),
                       _f32(states, (B, n, H), dev, "states"),
-                      _f32(dh_last, (B, H), dev, "dh_last"),
-                      *_view3(dx, x, dtype, dev, shape, "dx"),
-                      *_view3(dr, x, dtype, dev, shape, "dr"),
-                      *_view3(di, x, dtype, dev, shape, "di"), dp.data_ptr(),
+                      _f32(dh_last, (B, H), dev, "dh_last"), *outs, dp.data_ptr(),
                       0 if dh0 is None else dh0.data_ptr(), ws.data_ptr(), ws.numel())
     _ok("glr_scan_backward", lib.glr_scan_backward(args, _stream(stream, dev)))
     return dx, dr, di, dp, dh0
@@ -245,16 +263,17 @@ def glr_step(x, r, i, p, h, scale: float = 8.0, reset=None, h_out=None, out=None
     B, H = shape
     if out is None:
         with _on(stream):
-            out = torch.empty_like(x)
-    if h_out is None:
-        h_out = h
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        yp, ys = out.data_ptr(), H
+    else:
+        yp, _, ys = _view2(out, x, dtype, dev, shape, "out")
+    hp = _f32(h, shape, dev, "h")
+    op = hp if h_out is None else _f32(h_out, shape, dev, "h_out")
     xp, _, xs = _view2(x, x, dtype, dev, shape, "x")
     rp, _, rs = _view2(r, x, dtype, dev, shape, "r")
     ip, _, is_ = _view2(i, x, dtype, dev, shape, "i")
-    yp, _, ys = _view2(out, x, dtype, dev, shape, "out")
     args = _STEP(kind, B, H, scale, xp, xs, 0, rp, rs, 0, ip, is_, 0, _f32(p, (H,), dev, "p"),
-                 _f32(h, shape, dev, "h"), _bytes(reset, (B,), dev, "reset"), yp, ys, 0,
-                 _f32(h_out, shape, dev, "h_out"))
+                 hp, _bytes(reset, (B,), dev, "reset"), yp, ys, 0, op)
     _ok("glr_step", lib.glr_step(args, _stream(stream, dev)))
     return out
 
@@ -333,17 +352,18 @@ def glr_join(x, h, g, w, alpha, v, norm: str = "rms", act: str = "silu", eps: fl
     with _on(stream):
         if out is not None:
             y, n = out
+            yv, nv = _view2(y, x, dtype, dev, shape, "y"), _view2(n, x, dtype, dev, shape, "n")
         else:
-            y = None if h is None else torch.empty_like(x)
-            n = None if v is None else torch.empty_like(x)
+            y, yv = _new2(x, H, h is not None)
+            n, nv = _new2(x, H, v is not None)
         if ckpt:
             hc = _new_ckpt(M, H, x.device)
             gc = None if g is None else _new_ckpt(M, H, x.device)
     args = _JOIN(kind, M, H, NORM[norm], ACT[act], eps, *_view2(x, x, dtype, dev, shape, "x"),
                  *_view2(h, x, dtype, dev, shape, "h"), *_view2(g, x, dtype, dev, shape, "g"),
                  _f32(w, (H,), dev, "w"), _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"),
-                 *_view2(y, x, dtype, dev, shape, "y"), *_view2(n, x, dtype, dev, shape, "n"),
-                 *_ckpt_ptrs(hc, M, H, dev, "h"), *_ckpt_ptrs(gc, M, H, dev, "g"))
+                 *yv, *nv, *_ckpt_ptrs(hc, M, H, dev, "h"),
+                 *_ckpt_ptrs(gc, M, H, dev, "g"))
     _ok("glr_join", lib.glr_join(args, _stream(stream, dev)))
     return (y, n, (hc, gc)) if ckpt else (y, n)
 
@@ -366,10 +386,13 @@ def glr_join_backward(dy, dn, x, h, g, w, alpha, v, norm: str = "rms", act: str 
     with _on(stream):
         if out is not None:
             dx, dh, dg = out
+            outs = (*_view2(dx, x, dtype, dev, shape, "dx"), *_view2(dh, x, dtype, dev, shape, "dh"),
+                    *_view2(dg, x, dtype, dev, shape, "dg"))
         else:
-            dx = torch.empty_like(x)
-            dh = torch.empty_like(x) if block else None
-            dg = torch.empty_like(x) if block and act != "none" else None
+            dx, xv = _new2(x, H, True)
+            dh, hv = _new2(x, H, block)
+            dg, gv = _new2(x, H, block and act != "none")
+            outs = *xv, *hv, *gv
         if block:
             dw = torch.empty_like(w)
             dalpha = torch.empty((1,), dtype=torch.float32, device=x.device)
@@ -382,10 +405,8 @@ def glr_join_backward(dy, dn, x, h, g, w, alpha, v, norm: str = "rms", act: str 
                       *_view2(x, x, dtype, dev, shape, "x"), *_view2(h, x, dtype, dev, shape, "h"),
                       *_view2(g, x, dtype, dev, shape, "g"), *_ckpt_ptrs(hc, M, H, dev, "h"),
                       *_ckpt_ptrs(gc, M, H, dev, "g"), _f32(w, (H,), dev, "w"),
-                      _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"),
-                      *_view2(dx, x, dtype, dev, shape, "dx"),
-                      *_view2(dh, x, dtype, dev, shape, "dh"),
-                      *_view2(dg, x, dtype, dev, shape, "dg"), _f32(dw, (H,), dev, "dw"),
+                      _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"), *outs,
+                      _f32(dw, (H,), dev, "dw"),
                       0 if dalpha is None else dalpha.data_ptr(), _f32(dv, (H,), dev, "dv"),
                       ws.data_ptr(), ws.numel())
     _ok("glr_join_backward", lib.glr_join_backward(args, _stream(stream, dev)))
