@@ -18,7 +18,7 @@ pack_kernel(Rows<const T> t, int64_t M, int H, uint8_t* __restrict__ codes,
   const int64_t group = k / GLR_CKPT_GROUP;
   const int64_t row = group / groups;
   const int c = (int)(group % groups) * GLR_CKPT_GROUP + (int)(k % GLR_CKPT_GROUP);
-  const bool on = row < M && c < H;
+  const bool on = row < M && c < H && DLR_IN(row * H + c + VEC - 1, M * H);
   words<T, VEC> v;
   if (on) v.get(t.at(row, c));
   keep<T, VEC>(v, on, codes + row * H + c, scales + group);
@@ -32,7 +32,7 @@ unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sca
   const int64_t group = k / GLR_CKPT_GROUP;
   const int64_t row = group / groups;
   const int c = (int)(group % groups) * GLR_CKPT_GROUP + (int)(k % GLR_CKPT_GROUP);
-  if (row >= M || c >= H) return;
+  if (row >= M || c >= H || !DLR_IN(row * H + c + VEC - 1, M * H)) return;
   float v[VEC];
   words<uint8_t, VEC> item;
   item.get(codes + row * H + c);

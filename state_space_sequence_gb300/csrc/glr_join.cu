@@ -47,7 +47,8 @@ join_kernel(JoinArgs a, Rows<const T> x, Rows<const T> h, Rows<const T> g, Rows<
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const int c = it.channel(j);
-          keep<T, VEC>(St::one(sm + (k * 3 + array) * per, j, r.at(row, c), it.on(j)), it.on(j),
+          const bool on = it.on(j) && DLR_IN(row * a.H + c + VEC - 1, a.M * a.H);
+          keep<T, VEC>(St::one(sm + (k * 3 + array) * per, j, r.at(row, c), on), on,
                        codes + row * a.H + c, scales + row * groups + c / GLR_CKPT_GROUP);
         }
       };

@@ -192,7 +192,7 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
   const int64_t parts = gridDim.x, me = blockIdx.x;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (!it.on(j)) continue;
+    if (!it.on(j) || !DLR_IN((me * 2 + 1) * a.H + it.channel(j) + VEC - 1, parts * 2 * a.H)) continue;
     float t[VEC];
     it.pick(j, sw, t);
     store<float, VEC == 8 ? 4 : VEC>(part + (me * 2) * a.H + it.channel(j), t);

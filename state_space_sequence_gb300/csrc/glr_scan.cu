@@ -180,8 +180,9 @@ __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, i
     float m[2 * VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) m[v] = A[v], m[VEC + v] = e[v];
-    if (!last && cut) post(q.in + row + step, e);
-    if (!last && !cut) post(q.maps + 2 * row, m);
+    const int64_t all = q.B * q.tiles * q.HP;
+    if (!last && cut && DLR_IN(row + step + VEC - 1, all)) post(q.in + row + step, e);
+    if (!last && !cut && DLR_IN(row + VEC - 1, all)) post(q.maps + 2 * row, m);
     const float* in = q.in + row;                   // what enters this tile: the end of the one before
     const float* maps = q.maps + 2 * (row - step);  // of the one before
     Patience wait;
@@ -247,7 +248,8 @@ __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, i
   if (cut)
 #pragma unroll
     for (int v = 0; v < VEC; ++v) end[v] = e[v];
-  if (!last && !(done > 0 && cut)) post(q.in + row + step, end);
+  if (!last && !(done > 0 && cut) && DLR_IN(row + step, q.B * q.tiles * q.HP))
+    post(q.in + row + step, end);
 }
 
 // The warps' maps of a tile, (A, e) of all its channels each, folded in shared memory's order by the
@@ -619,10 +621,11 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       s[v] = sh.enter[k & 1][warp][lane * VEC + v];
     }
     if (states && z.n > 0) {
-      float* to = states + (at.b * ((q.L - 1) / S + 1) + t0 / S) * q.H + h;
+      const int64_t runs = (q.L - 1) / S + 1;
+      float* to = states + (at.b * runs + t0 / S) * q.H + h;
 #pragma unroll
       for (int v = 0; v < VEC; ++v)
-        if (on[v]) to[v] = s[v];
+        if (on[v] && DLR_IN((at.b * runs + t0 / S) * q.H + h + v, q.B * runs * q.H)) to[v] = s[v];
     }
     T* yp = kBulk ? &sh.out[warp * S][lane * VEC] : y.row(at.b, t0) + h;
     const int64_t st = kBulk ? C : y.st;
@@ -760,8 +763,8 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
         float t = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) t += sh.sum[k & 1][w][lane * VEC + v];
-        if (h + v < q.H && DLR_IN(at.b, q.B))
-          part[((int64_t)at.b * q.tiles + at.tile) * q.H + h + v] = t;
+        const int64_t to = ((int64_t)at.b * q.tiles + at.tile) * q.H + h + v;
+        if (h + v < q.H && DLR_IN(to, q.B * q.tiles * q.H)) part[to] = t;
       }
     };
     if (lane == 0) {
@@ -913,10 +916,10 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
     const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      s[v] = t0 < q.L && h + v < q.H && DLR_IN(at.b, q.B)
-                 ? states[(at.b * ((q.L - 1) / S + 1) + t0 / S) * q.H + h + v]
-                 : 0.0f;
+    for (int v = 0; v < VEC; ++v) {
+      const int64_t runs = (q.L - 1) / S + 1, from = (at.b * runs + t0 / S) * q.H + h + v;
+      s[v] = t0 < q.L && h + v < q.H && DLR_IN(from, q.B * runs * q.H) ? states[from] : 0.0f;
+    }
   };
   // plain (a constant in each call): all S steps are there and none begins a sequence
   auto finish = [&](int k, Part& z, float (&s)[VEC], const bool plain) {
