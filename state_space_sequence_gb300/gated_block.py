@@ -99,13 +99,20 @@ def step(par: Params, y, n, h, reset=None):
 
 def main() -> None:
     torch.manual_seed(0)
-    B, L, H, V, lr = 16, 192, 128, 32, 0.03
+    B, L, H, V, lr = 16, 192, 128, 32, 3e-3
     dtype = torch.bfloat16
     blocks = [make_params(H, dtype, seed=k) for k in range(2)]
     embed = torch.randn(V, H, device="cuda")
     first = torch.ones(H, device="cuda")
-    moments = [[torch.zeros_like(t, dtype=torch.float32) for t in b] for b in blocks]
-    moment_e = torch.zeros_like(embed)
+    weights = [[t.float() for t in b] for b in blocks] + [[embed]]  # the masters, in float32
+    moments = [[(torch.zeros_like(t), torch.zeros_like(t)) for t in b] for b in weights]
+
+    def adam(k, ws, ms, grads):
+        for t, (m, v), g in zip(ws, ms, grads):
+            g = g.float()
+            m.lerp_(g, 0.1)
+            v.lerp_(g * g, 0.02)
+            t.sub_(lr * (m / (1 - 0.9 ** (k + 1))) / ((v / (1 - 0.98 ** (k + 1))).sqrt() + 1e-8))
 
     def batch():
         tok = torch.randint(2, V, (B, L), device="cuda")
@@ -132,14 +139,14 @@ def main() -> None:
             saved.append(s)
         return n, saved
 
-    for k in range(161):
+    for k in range(241):
         tok, reset, want = batch()
         n, saved = run(tok, reset)
         logits = n.float() @ embed.t()
         prob = torch.softmax(logits, -1)
         count = B * L
         loss = -torch.log(prob.gather(-1, want[..., None]) + 1e-9).mean()
-        if k % 40 == 0:
+        if k % 60 == 0:
             print(f"step {k:3d}  loss {loss.item():.4f}")
         d = prob
         d.scatter_add_(-1, want[..., None], torch.full_like(d[..., :1], -1.0))
@@ -148,14 +155,9 @@ def main() -> None:
         dn, dy = (d @ embed).to(dtype), torch.zeros_like(n)
         for j in (1, 0):
             dy, dn, grads = backward(blocks[j], saved[j], dy, dn)
-            new = []
-            for t, g, m in zip(blocks[j], grads, moments[j]):  # momentum on normalised gradients
-                g = g.float()
-                m.mul_(0.9).add_(g / (g.norm() + 1e-12) * t.float().norm().clamp(min=1.0))
-                new.append((t.float() - lr * m).to(t.dtype))
-            blocks[j] = Params(*new)
-        moment_e.mul_(0.9).add_(de / (de.norm() + 1e-12) * embed.norm())
-        embed.sub_(lr * moment_e)
+            adam(k, weights[j], moments[j], grads)
+            blocks[j] = Params(*(w.to(t.dtype) for w, t in zip(weights[j], blocks[j])))
+        adam(k, weights[2], moments[2], [de])
 
     # the same rows token by token: a state a block, reset where a document begins
     tok, reset, _ = batch()

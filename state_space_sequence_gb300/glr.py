@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import struct
 from typing import NamedTuple, Optional
 
@@ -97,14 +98,16 @@ def _wrong(t, like, shape, what: str):
     raise ValueError(f"{what}: channels must be contiguous")
 
 
-def _view3(t, like, dtype, dev, shape, what: str):
-    """(pointer, stride_b, stride_t) of an activation [B, L, H]."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _wrong(t, like, shape, what)
-    sb, st, sh = t.stride()
-    if sh != 1 and shape[2] > 1:
-        _wrong(t, like, shape, what)
-    return t.data_ptr(), sb, st
+def _views3(ts, like, dtype, dev, shape, what):
+    """(pointer, stride_b, stride_t) of activations [B, L, H], one after the other."""
+    out, H = [], shape[2]
+    for t in ts:
+        sb, st, sh = t.stride() if t.dtype is dtype and t.shape == shape and \
+            t.get_device() == dev else (0, 0, -1)
+        if sh != 1 and (H > 1 or sh < 0):
+            _wrong(t, like, shape, what[len(out) // 3])
+        out += (t.data_ptr(), sb, st)
+    return out
 
 
 def _strides3(t):
@@ -113,16 +116,19 @@ def _strides3(t):
     return t.data_ptr(), sb, st
 
 
-def _view2(t, like, dtype, dev, shape, what: str):
-    """The same for rows [M, H]: (pointer, 0, stride_t); nothing for None."""
-    if t is None:
-        return _NONE3
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _wrong(t, like, shape, what)
-    st, sh = t.stride()
-    if sh != 1 and shape[1] > 1:
-        _wrong(t, like, shape, what)
-    return t.data_ptr(), 0, st
+def _views2(ts, like, dtype, dev, shape, what):
+    """The same for rows [M, H]: (pointer, 0, stride_t), nothing for None."""
+    out, H = [], shape[1]
+    for t in ts:
+        if t is None:
+            out += _NONE3
+            continue
+        st, sh = t.stride() if t.dtype is dtype and t.shape == shape and \
+            t.get_device() == dev else (0, -1)
+        if sh != 1 and (H > 1 or sh < 0):
+            _wrong(t, like, shape, what[len(out) // 3])
+        out += (t.data_ptr(), 0, st)
+    return out
 
 
 def _new2(x, H: int, wanted: bool):
@@ -172,16 +178,20 @@ def _workspace(workspace, need: int, x):
     return workspace
 
 
+# The sizes are pure functions of their arguments; asking the library costs 0.5 us a call.
+@functools.lru_cache(maxsize=1024)
 def glr_scan_workspace_size(B: int, L: int, H: int) -> int:
     """Bytes of device workspace glr_scan needs (0: none, or sizes out of range)."""
     return int(_load().glr_scan_workspace_size(B, L, H))
 
 
+@functools.lru_cache(maxsize=1024)
 def glr_scan_backward_workspace_size(B: int, L: int, H: int) -> int:
     """Bytes of device workspace glr_scan_backward needs (0 for sizes out of range)."""
     return int(_load().glr_scan_backward_workspace_size(B, L, H))
 
 
+@functools.lru_cache(maxsize=1024)
 def glr_join_backward_workspace_size(M: int, H: int) -> int:
     """Bytes of device workspace glr_join_backward needs (0 for sizes out of range)."""
     return int(_load().glr_join_backward_workspace_size(M, H))
@@ -199,18 +209,19 @@ def glr_scan(x, r, i, p, scale: float = 8.0, h0=None, reset=None, save_states: b
         raise ValueError("x: expected [B, L, H]")
     shape, dtype, dev = x.shape, x.dtype, x.get_device()
     B, L, H = shape
+    views = _views3((x, r, i), x, dtype, dev, shape, ("x", "r", "i"))
     with _on(stream):
-        y = _strides3(out := torch.empty_like(x)) if out is None else \
-            _view3(out, x, dtype, dev, shape, "out")
+        if out is None:
+            out = torch.empty_like(x)
+            y = _strides3(out)
+        else:
+            y = _views3((out,), x, dtype, dev, shape, ("out",))
         h_last = torch.empty((B, H), dtype=torch.float32, device=x.device)
         states = torch.empty((B, (L + STATE_STEPS - 1) // STATE_STEPS, H), dtype=torch.float32,
                              device=x.device) if save_states else None
-        ws = _workspace(workspace, lib.glr_scan_workspace_size(B, L, H), x)
-    xv = _view3(x, x, dtype, dev, shape, "x")
-    args = _SCAN(kind, B, L, H, scale, *xv, *_view3(r, x, dtype, dev, shape, "r"),
-                 *_view3(i, x, dtype, dev, shape, "i"),
-                 _f32(p, (H,), dev, "p"), _f32(h0, (B, H), dev, "h0"),
-                 _bytes(reset, (B, L), dev, "reset"), *y,
+        ws = _workspace(workspace, glr_scan_workspace_size(B, L, H), x)
+    args = _SCAN(kind, B, L, H, scale, *views, _f32(p, (H,), dev, "p"),
+                 _f32(h0, (B, H), dev, "h0"), _bytes(reset, (B, L), dev, "reset"), *y,
                  h_last.data_ptr(), 0 if states is None else states.data_ptr(), ws.data_ptr(),
                  ws.numel())
     _ok("glr_scan", lib.glr_scan(args, _stream(stream, dev)))
@@ -229,21 +240,18 @@ def glr_scan_backward(x, r, i, p, dy, states, scale: float = 8.0, h0=None, reset
     shape, dtype, dev = x.shape, x.dtype, x.get_device()
     B, L, H = shape
     n = (L + STATE_STEPS - 1) // STATE_STEPS
+    views = _views3((x, r, i, dy), x, dtype, dev, shape, ("x", "r", "i", "dy"))
     with _on(stream):
         if out is None:
             dx, dr, di = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
             outs = *_strides3(dx), *_strides3(dr), *_strides3(di)
         else:
             dx, dr, di = out
-            outs = (*_view3(dx, x, dtype, dev, shape, "dx"), *_view3(dr, x, dtype, dev, shape, "dr"),
-                    *_view3(di, x, dtype, dev, shape, "di"))
+            outs = _views3(out, x, dtype, dev, shape, ("dx", "dr", "di"))
         dp = torch.empty((H,), dtype=torch.float32, device=x.device)
         dh0 = None if h0 is None else torch.empty_like(h0)
-        ws = _workspace(workspace, lib.glr_scan_backward_workspace_size(B, L, H), x)
-    args = _SCAN_BACK(kind, B, L, H, scale, *_view3(x, x, dtype, dev, shape, "x"),
-                      *_view3(r, x, dtype, dev, shape, "r"),
-                      *_view3(i, x, dtype, dev, shape, "i"),
-                      *_view3(dy, x, dtype, dev, shape, "dy"), _f32(p, (H,), dev, "p"),
+        ws = _workspace(workspace, glr_scan_backward_workspace_size(B, L, H), x)
+    args = _SCAN_BACK(kind, B, L, H, scale, *views, _f32(p, (H,), dev, "p"),
                       _f32(h0, (B, H), dev, "h0"), _bytes(reset, (B, L), dev, "reset"),
                       _f32(states, (B, n, H), dev, "states"),
                       _f32(dh_last, (B, H), dev, "dh_last"), *outs, dp.data_ptr(),
@@ -264,14 +272,12 @@ def glr_step(x, r, i, p, h, scale: float = 8.0, reset=None, h_out=None, out=None
     if out is None:
         with _on(stream):
             out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        yp, ys = out.data_ptr(), H
+        yp, _, ys = out.data_ptr(), 0, H
     else:
-        yp, _, ys = _view2(out, x, dtype, dev, shape, "out")
+        yp, _, ys = _views2((out,), x, dtype, dev, shape, ("out",))
+    xp, _, xs, rp, _, rs, ip, _, is_ = _views2((x, r, i), x, dtype, dev, shape, ("x", "r", "i"))
     hp = _f32(h, shape, dev, "h")
     op = hp if h_out is None else _f32(h_out, shape, dev, "h_out")
-    xp, _, xs = _view2(x, x, dtype, dev, shape, "x")
-    rp, _, rs = _view2(r, x, dtype, dev, shape, "r")
-    ip, _, is_ = _view2(i, x, dtype, dev, shape, "i")
     args = _STEP(kind, B, H, scale, xp, xs, 0, rp, rs, 0, ip, is_, 0, _f32(p, (H,), dev, "p"),
                  hp, _bytes(reset, (B,), dev, "reset"), yp, ys, 0, op)
     _ok("glr_step", lib.glr_step(args, _stream(stream, dev)))
@@ -305,7 +311,7 @@ def glr_ckpt_pack(t, stream=None) -> Ckpt8:
         raise ValueError("t: expected [M, H]")
     dev = t.get_device()
     M, H = t.shape
-    p, _, st = _view2(t, t, t.dtype, dev, t.shape, "t")
+    p, _, st = _views2((t,), t, t.dtype, dev, t.shape, ("t",))
     with _on(stream):
         c = _new_ckpt(M, H, t.device)
     _ok("glr_ckpt_pack", lib.glr_ckpt_pack(kind, M, H, p, st, c[0].data_ptr(), c[1].data_ptr(),
@@ -326,7 +332,7 @@ def glr_ckpt_unpack(c: Ckpt8, dtype=torch.float32, out=None, stream=None):
             out = torch.empty((M, H), dtype=dtype, device=codes.device)
     kind = _act_type(out)
     cp, sp = _ckpt_ptrs(c, M, H, dev, "c")
-    p, _, st = _view2(out, out, out.dtype, dev, codes.shape, "out")
+    p, _, st = _views2((out,), out, out.dtype, dev, codes.shape, ("out",))
     _ok("glr_ckpt_unpack", lib.glr_ckpt_unpack(kind, M, H, cp, sp, p, st, _stream(stream, dev)))
     return out
 
@@ -348,22 +354,21 @@ def glr_join(x, h, g, w, alpha, v, norm: str = "rms", act: str = "silu", eps: fl
         raise ValueError('g: must be None with act="none"')
     if h is None and (g is not None or w is not None or alpha is not None or ckpt):
         raise ValueError("g, w, alpha and ckpt need h")
+    views = _views2((x, h, g), x, dtype, dev, shape, ("x", "h", "g"))
     hc = gc = None
     with _on(stream):
         if out is not None:
             y, n = out
-            yv, nv = _view2(y, x, dtype, dev, shape, "y"), _view2(n, x, dtype, dev, shape, "n")
+            yv, nv = _views2(out, x, dtype, dev, shape, ("y", "n")), ()
         else:
             y, yv = _new2(x, H, h is not None)
             n, nv = _new2(x, H, v is not None)
         if ckpt:
             hc = _new_ckpt(M, H, x.device)
             gc = None if g is None else _new_ckpt(M, H, x.device)
-    args = _JOIN(kind, M, H, NORM[norm], ACT[act], eps, *_view2(x, x, dtype, dev, shape, "x"),
-                 *_view2(h, x, dtype, dev, shape, "h"), *_view2(g, x, dtype, dev, shape, "g"),
-                 _f32(w, (H,), dev, "w"), _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"),
-                 *yv, *nv, *_ckpt_ptrs(hc, M, H, dev, "h"),
-                 *_ckpt_ptrs(gc, M, H, dev, "g"))
+    args = _JOIN(kind, M, H, NORM[norm], ACT[act], eps, *views, _f32(w, (H,), dev, "w"),
+                 _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"), *yv, *nv,
+                 *_ckpt_ptrs(hc, M, H, dev, "h"), *_ckpt_ptrs(gc, M, H, dev, "g"))
     _ok("glr_join", lib.glr_join(args, _stream(stream, dev)))
     return (y, n, (hc, gc)) if ckpt else (y, n)
 
@@ -383,31 +388,27 @@ def glr_join_backward(dy, dn, x, h, g, w, alpha, v, norm: str = "rms", act: str 
     block = w is not None
     hc, gc = ckpt if ckpt is not None else (None, None)
     dw = dalpha = dv = None
+    views = _views2((dy, dn, x, h, g), x, dtype, dev, shape, ("dy", "dn", "x", "h", "g"))
     with _on(stream):
         if out is not None:
             dx, dh, dg = out
-            outs = (*_view2(dx, x, dtype, dev, shape, "dx"), *_view2(dh, x, dtype, dev, shape, "dh"),
-                    *_view2(dg, x, dtype, dev, shape, "dg"))
+            outs = _views2(out, x, dtype, dev, shape, ("dx", "dh", "dg"))
         else:
             dx, xv = _new2(x, H, True)
             dh, hv = _new2(x, H, block)
             dg, gv = _new2(x, H, block and act != "none")
             outs = *xv, *hv, *gv
         if block:
-            dw = torch.empty_like(w)
+            dw = torch.empty((H,), dtype=torch.float32, device=x.device)
             dalpha = torch.empty((1,), dtype=torch.float32, device=x.device)
         if v is not None:
-            dv = torch.empty_like(v)
-        ws = _workspace(workspace, lib.glr_join_backward_workspace_size(M, H), x)
-    args = _JOIN_BACK(kind, M, H, NORM[norm], ACT[act], eps,
-                      *_view2(dy, x, dtype, dev, shape, "dy"),
-                      *_view2(dn, x, dtype, dev, shape, "dn"),
-                      *_view2(x, x, dtype, dev, shape, "x"), *_view2(h, x, dtype, dev, shape, "h"),
-                      *_view2(g, x, dtype, dev, shape, "g"), *_ckpt_ptrs(hc, M, H, dev, "h"),
-                      *_ckpt_ptrs(gc, M, H, dev, "g"), _f32(w, (H,), dev, "w"),
-                      _f32(alpha, (1,), dev, "alpha"), _f32(v, (H,), dev, "v"), *outs,
-                      _f32(dw, (H,), dev, "dw"),
-                      0 if dalpha is None else dalpha.data_ptr(), _f32(dv, (H,), dev, "dv"),
-                      ws.data_ptr(), ws.numel())
+            dv = torch.empty((H,), dtype=torch.float32, device=x.device)
+        ws = _workspace(workspace, glr_join_backward_workspace_size(M, H), x)
+    args = _JOIN_BACK(kind, M, H, NORM[norm], ACT[act], eps, *views,
+                      *_ckpt_ptrs(hc, M, H, dev, "h"), *_ckpt_ptrs(gc, M, H, dev, "g"),
+                      _f32(w, (H,), dev, "w"), _f32(alpha, (1,), dev, "alpha"),
+                      _f32(v, (H,), dev, "v"), *outs, 0 if dw is None else dw.data_ptr(),
+                      0 if dalpha is None else dalpha.data_ptr(),
+                      0 if dv is None else dv.data_ptr(), ws.data_ptr(), ws.numel())
     _ok("glr_join_backward", lib.glr_join_backward(args, _stream(stream, dev)))
     return dx, dh, dg, dw, dalpha, dv
