@@ -117,6 +117,7 @@ dlr_status glr_scan_backward(const glr_scan_backward_args* args, dlr_stream_t st
 /*
  * glr_step -- glr_scan for one token (L = 1; stride_t unused): y [B, H] and the state h_out from
  * the state h (float32 [B, H] both; h_out may be h). reset: bytes [B] or NULL. One launch.
+ * B <= 262140.
  */
 typedef struct {
   int64_t type, B, H;

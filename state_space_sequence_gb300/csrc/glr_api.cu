@@ -211,6 +211,7 @@ dlr_status glr_step(const glr_step_args* args, dlr_stream_t stream) {
   const glr_step_args& a = *args;
   dlr_status st = scan_sizes(a.type, a.B, 1, a.H, a.c);
   if (st != DLR_OK) return st;
+  if (a.B > 4 * 65535) return DLR_ERR_UNSUPPORTED;  // four batch entries to a row of blocks
   if (bad_view(a.x, a.type) || bad_view(a.r, a.type) || bad_view(a.i, a.type) ||
       bad_view(a.y, a.type) || bad_f32(a.p) || bad_f32(a.h) || bad_f32(a.h_out))
     return DLR_ERR_INVALID_ARG;
