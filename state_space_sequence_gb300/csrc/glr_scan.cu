@@ -88,10 +88,13 @@ struct Job {
   const uint8_t* reset;
   float* in;    // [B, tiles, HP]: the value that enters each tile but the chain's first
   float* maps;  // [B, tiles, HP / VEC, 2, VEC]: each tile's map, VEC of A and VEC of e
+  float* run_in;    // [B, runs, HP]: with runs, the value that enters each but the first
+  float* run_maps;  // [B, runs, HP / VEC, 2, VEC]: and its map
   uint32_t* head;
   int* status;
   int64_t B, L, H, HP, chains;
   int groups, tiles;
+  int runs;  // runs of a chain (0: none)
   int most;  // tiles that a block takes at most
   float c;
 
@@ -293,6 +296,147 @@ struct Fold {
   }
 };
 
+// As chain(), for few chains, of which many tiles are at work at a time, in runs of kRun tiles: the last tile of a
+// run publishes the map of the whole run, and later the value that enters the next run. A tile takes the value
+// that enters its own run, looking back over runs, through the maps of its run's tiles before it. A map that does
+// not depend on what enters has kCut for its A.
+constexpr uint32_t kCut = 0xfffffffeu;
+constexpr int kRun = 8;
+template <int VEC>
+__device__ __forceinline__ void through_cut(const float (&m)[2 * VEC], float (&s)[VEC]) {
+  float a[VEC], b[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) a[v] = m[v], b[v] = m[VEC + v];
+  through<VEC>(a, b, s);
+  if (__float_as_uint(m[0]) == kCut)  // the same for all channels
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) s[v] = m[VEC + v];
+}
+template <int VEC, typename J>
+__device__ __forceinline__ void chain_runs(const J& q, const Tile& at, int64_t row, int dir,
+                                           const float (&A)[VEC], const float (&e)[VEC], bool cut,
+                                           float (&s)[VEC], float (&end)[VEC]) {
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 31;
+  const int done = dir > 0 ? at.tile : q.tiles - 1 - at.tile;  // tiles of the chain before this
+  const bool last = done == q.tiles - 1;
+  const int run = done / kRun, j = done % kRun;
+  const bool closes = j == kRun - 1 && !last;
+  const int64_t step = dir * q.HP, all = q.B * q.tiles * q.HP;
+  // runs in the chain's order: their maps, and the values that enter them
+  const int64_t h = row - ((int64_t)at.b * q.tiles + at.tile) * q.HP;
+  const int64_t mine = ((int64_t)at.b * q.runs + run) * q.HP + h;
+  float m[2 * VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) m[v] = cut ? __uint_as_float(kCut) : A[v], m[VEC + v] = e[v];
+  if (!last && !closes && DLR_IN(row + VEC - 1, all)) post(q.maps + 2 * row, m);
+  Patience wait;
+  // the maps of the run's tiles before this one, the first of them first
+  float t[kRun - 1][2 * VEC];
+  const float* from = q.maps + 2 * (row - j * step);
+  uint32_t top;
+  do {
+    top = 0;
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u)
+      if (u < j) {
+        look(from + 2 * u * step, t[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u)
+      if (u < j)
+#pragma unroll
+        for (int v = 0; v < 2 * VEC; ++v) top = max(top, __float_as_uint(t[u][v]));
+  } while (__any_sync(0xffffffffu, top == kEmpty) && !wait.ends());
+  float whole[2 * VEC];
+  if (closes) {
+    float a[VEC], b[VEC];
+    bool any = cut;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) a[v] = 1.0f, b[v] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u)
+      if (u < j) {
+        through_cut<VEC>(t[u], b);
+        any |= __float_as_uint(t[u][0]) == kCut;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) a[v] *= t[u][v];
+      }
+    through_cut<VEC>(m, b);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      whole[v] = any ? __uint_as_float(kCut) : a[v] * m[v];
+      whole[VEC + v] = b[v];
+    }
+    if (DLR_IN(mine + VEC - 1, q.B * q.runs * q.HP)) post(q.run_maps + 2 * mine, whole);
+  }
+  if (run > 0) {
+    const float* in = q.run_in + mine;                    // the value that enters this run
+    const float* maps = q.run_maps + 2 * (mine - q.HP);   // the run before
+    int far = 0;
+    bool at_hand = false;
+    for (bool found = false; !found;) {
+      const int k = far + lane;
+      float has_in[1] = {0.0f}, has_map[1] = {0.0f};
+      if (k < run) {
+        look(in - lane * VEC - k * q.HP, has_in);
+        look(maps - 2 * (lane * VEC + k * q.HP), has_map);
+      }
+      if (far == 0) look(in, s);
+      const uint32_t ins = __ballot_sync(0xffffffffu, k < run && !empty(has_in[0]));
+      const uint32_t there = __ballot_sync(0xffffffffu, k < run && !empty(has_map[0]));
+      const int l = ins ? __ffs(ins) - 1 : 32;
+      const uint32_t before = l == 32 ? 0xffffffffu : (1u << l) - 1u;
+      if ((there & before) != before) {
+        if (wait.ends()) break;
+        continue;
+      }
+      far += l;
+      found = l < 32;
+      if (far == 0) at_hand = !any_empty(s);
+    }
+    for (int k = far - 1; !at_hand; k -= U) {
+      float g[U][2 * VEC], first[VEC];
+      do {
+        top = 0;
+        if (k == far - 1) {
+          look(in - far * q.HP, first);
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) top = max(top, __float_as_uint(first[v]));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) look(maps - 2 * max(k - u, 0) * q.HP, g[u]);
+        if (k >= 0)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int v = 0; v < 2 * VEC; ++v) top = max(top, __float_as_uint(g[u][v]));
+      } while (__any_sync(0xffffffffu, top == kEmpty) && !wait.ends());
+      if (k == far - 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = first[v];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k >= u) through_cut<VEC>(g[u], s);
+      at_hand = k < U;
+    }
+  }
+  if (closes) {
+    float next[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) next[v] = s[v];
+    through_cut<VEC>(whole, next);
+    if (DLR_IN(mine + q.HP + VEC - 1, q.B * q.runs * q.HP)) post(q.run_in + mine + q.HP, next);
+  }
+#pragma unroll
+  for (int u = 0; u < kRun - 1; ++u)
+    if (u < j) through_cut<VEC>(t[u], s);
+  if (wait.gone && lane == 0) report_status(q.status, DLR_ERR_TIMEOUT);
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) end[v] = s[v];
+  through_cut<VEC>(m, end);
+}
+
 // bits of the n steps from t on that begin a sequence
 __device__ __forceinline__ uint32_t cuts(const uint8_t* reset, int64_t first, int n) {
   if (!reset) return 0u;
@@ -436,7 +580,7 @@ struct ScanShared {
 // One warp keeps the chain and one supplies the tiles; the others compute, one tile ahead of the
 // chain: they have the gates of tile k + 1 done before they need the state that enters tile k, so a
 // tile's way along the chain (stores and loads through L2) passes while they work.
-template <typename T, int kBytes>
+template <typename T, int kBytes, bool kRuns>
 __global__ void __launch_bounds__(kScanThreads, 1)
 scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant__ Maps<1> out,
             view<T> y, const float* __restrict__ h0, float* __restrict__ h_last,
@@ -510,10 +654,13 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       Fold<W, VEC> fold;
       fold.read(sh.map[k % 3], cut);
       fold.all(false, A, e);
-      if (at.tile == 0)
+      if (at.tile < (kRuns ? kRun : 1))  // what enters the first tile, or the first run
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = h0 && on[v] ? h0[at.b * q.H + h + v] : 0.0f;
-      chain(q, at, row, 1, A, e, cut != 0, s, end);
+      if constexpr (kRuns)
+        chain_runs(q, at, row, 1, A, e, cut != 0, s, end);
+      else
+        chain(q, at, row, 1, A, e, cut != 0, s, end);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
 #pragma unroll
@@ -711,7 +858,7 @@ struct BackShared {
 // With what enters known, a warp first goes back over its steps for G, then forwards from the
 // kept state, so that each step's state is at hand when its gradients are formed: nothing is
 // computed twice but sigmoid(r), and only the decays and G stay in registers.
-template <typename T, int kBytes>
+template <typename T, int kBytes, bool kRuns>
 __global__ void __launch_bounds__(kBackThreads, 1)
 back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant__ Maps<3> out,
             view<const T> dy, const float* __restrict__ states, const float* __restrict__ dh_last,
@@ -803,11 +950,14 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       Fold<W, VEC> fold;
       fold.read(sh.map[k % 3], cut);
       fold.all(true, A, e);
-      if (at.tile == q.tiles - 1)
+      if (q.tiles - 1 - at.tile < (kRuns ? kRun : 1))
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           s[v] = dh_last && on[v] ? dh_last[at.b * q.H + h + v] : 0.0f;
-      chain(q, at, row, -1, A, e, cut != 0, s, end);
+      if constexpr (kRuns)
+        chain_runs(q, at, row, -1, A, e, cut != 0, s, end);
+      else
+        chain(q, at, row, -1, A, e, cut != 0, s, end);
 #pragma unroll
       for (int w = W - 1; w >= 0; --w) {
 #pragma unroll
@@ -1152,15 +1302,17 @@ view<T> out_view(const glr_out& v) {
 }
 
 // Bytes of the parts of a workspace for tiles of `steps` steps, laid out one behind the other: the
-// head, the maps, the entering values.
+// head, the maps, the entering values, and those of the runs.
 struct Space {
   int64_t tiles, HP;
-  size_t head, maps, in;
+  size_t head, maps, in, runs;
   Space(int64_t B, int64_t L, int64_t H, int64_t steps)
       : tiles(L < 1 ? 0 : (L - 1) / steps + 1), HP((H + 63) / 64 * 64), head(4 * kHead) {
     in = sizeof(float) * (size_t)B * (size_t)tiles * (size_t)HP;
     maps = 2 * in;
+    runs = 3 * sizeof(float) * (size_t)B * (size_t)((tiles + kRun - 1) / kRun) * (size_t)HP;
   }
+  size_t all() const { return head + maps + in + runs; }
 };
 
 // A tensor map over an array [B, L, H] whose boxes are `rows` rows of 128 bytes.
@@ -1201,8 +1353,8 @@ Job<T> make_job(const A& a, const Space& sp) {
   const int64_t groups = (a.H + 32 * kVec<T> - 1) / (32 * kVec<T>);
   return {in_view<T>(a.x), in_view<T>(a.r), in_view<T>(a.i), a.p, a.reset,
           reinterpret_cast<float*>(ws + sp.head + sp.maps), reinterpret_cast<float*>(ws + sp.head),
-          reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, sp.HP, a.B * groups,
-          (int)groups, (int)sp.tiles, 1, (float)a.c};
+          nullptr, nullptr, reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, sp.HP, a.B * groups,
+          (int)groups, (int)sp.tiles, 0, 1, (float)a.c};
 }
 
 // Blocks for all tiles, one to an SM at most; the chain's workspace becomes empty. A chain of one tile
@@ -1218,7 +1370,13 @@ cudaError_t prepare_chain(Job<T>& q, const Space& sp, unsigned* blocks, cudaStre
   if (e != cudaSuccess) return e;
   *blocks = (unsigned)std::min<int64_t>(all, sms);
   q.most = (int)((all - 1) / *blocks + 1);  // all blocks get as many, however early they come
-  return cudaMemsetAsync(q.head, 0xff, sp.head + sp.maps + sp.in, s);
+  // Runs, where many tiles of a chain are at work at a time. B1 L65536, us with and without runs: float32
+  // H64 (2 chains) 28 and 41, H128 (4) 63 and 57, H256 (8) 115 and 89; bfloat16 H64 (1) 21 and 65, H256
+  // (4) 68 and 89, but B2 H256 (8) 128 and 112.
+  if (*blocks / q.chains * kVec<T> >= 64) q.runs = (q.tiles - 1) / kRun + 1;
+  q.run_in = q.in + sp.in / sizeof(float);
+  q.run_maps = q.run_in + q.B * q.runs * q.HP;
+  return cudaMemsetAsync(q.head, 0xff, q.runs ? sp.all() : sp.head + sp.maps + sp.in, s);
 }
 
 template <typename T, int kBytes>
@@ -1228,7 +1386,6 @@ cudaError_t scan_w(const glr_scan_args& a, cudaStream_t s) {
   Job<T> q = make_job<T>(a, sp);
   unsigned blocks;
   cudaError_t e = prepare_chain(q, sp, &blocks, s);
-  if (e == cudaSuccess) e = max_smem_once<scan_kernel<T, kBytes>>(smem);
   if (e != cudaSuccess) return e;
   Maps<3> in{};
   Maps<1> out{};
@@ -1237,9 +1394,16 @@ cudaError_t scan_w(const glr_scan_args& a, cudaStream_t s) {
                           describe<T>(&in.map[2], a.x, a.B, a.L, a.H, kScanTile) &&
                           describe<T>(&out.map[0], a.y, a.B, a.L, a.H, kScanSteps)))
     return cudaErrorInvalidValue;
-  scan_kernel<T, kBytes><<<blocks, kScanThreads, smem, s>>>(q, in, out, out_view<T>(a.y), a.h0,
-                                                            a.h_last, a.states);
-  return cudaGetLastError();
+  auto launch = [&](auto kernel, cudaError_t ready) {
+    if (ready != cudaSuccess) return ready;
+    kernel<<<blocks, kScanThreads, smem, s>>>(q, in, out, out_view<T>(a.y), a.h0, a.h_last,
+                                              a.states);
+    return cudaGetLastError();
+  };
+  return q.runs ? launch(scan_kernel<T, kBytes, true>,
+                         max_smem_once<scan_kernel<T, kBytes, true>>(smem))
+                : launch(scan_kernel<T, kBytes, false>,
+                         max_smem_once<scan_kernel<T, kBytes, false>>(smem));
 }
 
 template <typename T, int kBytes>
@@ -1247,11 +1411,9 @@ cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(BackShared<T>);
   const Space sp(a.B, a.L, a.H, kBackTile);
   Job<T> q = make_job<T>(a, sp);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.head + sp.maps +
-                                         sp.in);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.all());
   unsigned blocks;
   cudaError_t e = prepare_chain(q, sp, &blocks, s);
-  if (e == cudaSuccess) e = max_smem_once<back_kernel<T, kBytes>>(smem);
   if (e != cudaSuccess) return e;
   Maps<4> in{};
   Maps<3> out{};
@@ -1263,9 +1425,18 @@ cudaError_t back_w(const glr_scan_backward_args& a, cudaStream_t s) {
                           describe<T>(&out.map[1], a.dr, a.B, a.L, a.H, kBackSteps) &&
                           describe<T>(&out.map[2], a.di, a.B, a.L, a.H, kBackSteps)))
     return cudaErrorInvalidValue;
-  back_kernel<T, kBytes><<<blocks, kBackThreads, smem, s>>>(
-      q, in, out, in_view<T>(a.dy), a.states, a.dh_last, out_view<T>(a.dx), out_view<T>(a.dr),
-      out_view<T>(a.di), a.dh0, part);
+  auto launch = [&](auto kernel, cudaError_t ready) {
+    if (ready == cudaSuccess)
+      kernel<<<blocks, kBackThreads, smem, s>>>(q, in, out, in_view<T>(a.dy), a.states, a.dh_last,
+                                                out_view<T>(a.dx), out_view<T>(a.dr),
+                                                out_view<T>(a.di), a.dh0, part);
+    return ready;
+  };
+  e = q.runs ? launch(back_kernel<T, kBytes, true>,
+                      max_smem_once<back_kernel<T, kBytes, true>>(smem))
+             : launch(back_kernel<T, kBytes, false>,
+                      max_smem_once<back_kernel<T, kBytes, false>>(smem));
+  if (e != cudaSuccess) return e;
   back_sum<<<(unsigned)((a.H + 31) / 32), 256, 0, s>>>(part, a.B * q.tiles, a.H, a.p, (float)a.c,
                                                        a.dp);
   return cudaGetLastError();
@@ -1325,11 +1496,11 @@ cudaError_t step_t(const glr_step_args& a, cudaStream_t s) {
 
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H) {
   const Space sp(B, L, H, kScanTile);
-  return sp.tiles <= 1 ? 0 : sp.head + sp.maps + sp.in;
+  return sp.tiles <= 1 ? 0 : sp.all();
 }
 size_t scan_backward_workspace_bytes(int64_t B, int64_t L, int64_t H) {
   const Space sp(B, L, H, kBackTile);
-  return sp.head + sp.maps + 2 * sp.in;  // and the parts of dp
+  return sp.all() + sp.in;  // and the parts of dp
 }
 // tiles, which a 32-bit counter hands out, of the finest cut that a call of this size takes
 int64_t scan_tiles(int64_t B, int64_t L, int64_t H) {

@@ -73,6 +73,8 @@ SCAN_CASES = [
     (2, 1025, 258, "columns", False, 0), (5, 321, 17, "apart", True, 1),
     (1, 5000, 8, "apart", True, 3), (1, 70001, 3, "apart", False, 0),
     (4, 4000, 640, "columns", True, 9),  # more tiles to a block than it remembers places for
+    # few chains with many tiles at work: runs of tiles, ended by resets and by the row's end
+    (1, 40000, 32, "apart", True, 0), (1, 9000, 64, "columns", True, 40), (2, 21000, 20, "apart", False, 3),
 ]
 
 
@@ -477,7 +479,11 @@ def test_join_gradient_against_differences():
 
 
 def test_results_do_not_depend_on_the_run_or_the_workspace():
-    B, L, H = 3, 3000, 192
+    for B, L, H in ((3, 3000, 192), (1, 30000, 64)):
+        check_repeats(B, L, H)
+
+
+def check_repeats(B, L, H):
     x, r, i, dy = arrays("apart", 4, 1, B, L, H, torch.bfloat16)
     p, reset = decay_param(H), resets(3, B, L, 4)
     need = max(glr.glr_scan_workspace_size(B, L, H), glr.glr_scan_backward_workspace_size(B, L, H),
