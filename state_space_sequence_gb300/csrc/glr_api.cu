@@ -250,7 +250,8 @@ dlr_status glr_join(const glr_join_args* args, dlr_stream_t stream) {
   if (next ? bad_view(a.n, a.type) || bad_f32(a.v) : a.n.data != nullptr)
     return DLR_ERR_INVALID_ARG;
   const bool keep = a.hc || a.hs || a.gc || a.gs;
-  if (keep && (!block || !a.hc || !a.hs || gated != (a.gc != nullptr) || gated != (a.gs != nullptr)))
+  if (keep && (!block || !a.hc || !a.hs || gated != (a.gc != nullptr) ||
+               gated != (a.gs != nullptr)))
     return DLR_ERR_INVALID_ARG;
   const int64_t nc = a.M * a.H, ns = a.M * ((a.H + GLR_CKPT_GROUP - 1) / GLR_CKPT_GROUP);
   auto rows = [&](const auto& v) { return strided(v, a.type, 1, a.M, a.H); };

@@ -16,8 +16,8 @@ __device__ __forceinline__ float finite_abs(float t) {
   return a <= 3.40282347e38f ? a : 0.0f;
 }
 
-// s + 127 for the least s with amax <= 448 * 2^s. amax = m 2^E with 1 <= m < 2 and 448 = 1.75 * 2^8,
-// so s = E - 8, or E - 7 where m > 1.75; below -127 it is held there.
+// s + 127 for the least s with amax <= 448 * 2^s. amax = m 2^E with 1 <= m < 2 and 448 = 1.75 *
+// 2^8, so s = E - 8, or E - 7 where m > 1.75; below -127 it is held there.
 __device__ __forceinline__ int scale_byte(float amax) {
   const int bits = __float_as_int(amax);
   const int b = (bits >> 23) - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
@@ -45,7 +45,8 @@ __device__ __forceinline__ uint32_t encode2(float2 q) {
   return (isinf(q.x) ? 0x7fu : c & 0xffu) | (isinf(q.y) ? 0x7f00u : c & 0xff00u);
 }
 __device__ __forceinline__ float2 decode2(uint32_t codes) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
+  return __half22float2(
+      __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
 }
 
 // The largest bit pattern of |t| in an item; patterns of floats of one sign are in their order.
@@ -72,7 +73,8 @@ __device__ __forceinline__ float from_bits(uint32_t bits) {
 
 // VEC codes and their group's scale. A group is 32 / VEC neighbouring lanes; whole warps call it.
 template <typename T, int VEC>
-__device__ __forceinline__ void keep(const words<T, VEC>& t, bool on, uint8_t* codes, uint8_t* scale) {
+__device__ __forceinline__ void keep(const words<T, VEC>& t, bool on, uint8_t* codes,
+                                     uint8_t* scale) {
   uint32_t top = top_bits<T, VEC>(t);
 #pragma unroll
   for (int o = 16 / VEC; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));

@@ -161,8 +161,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 // 1 - a and a for a = 2^z, z <= 0. With n = rint(z), f = z - n and q = 1 - 2^f (a polynomial with
 // q(0) = 0, so its relative error of 2e-8 holds down to z = 0), 1 - a = 2^n q + (1 - 2^n). 1 - a
 // therefore keeps its digits where a is next to 1, and so does 1 - a^2 = (1 - a)(1 + a): from a
-// alone its rounding to 2^-24 would be 6e-5 of 1 - a^2 at a memory of 1000 steps. The coefficients are
-// a least-maximum fit of (1 - 2^f) / f on |f| <= 1/2. Below z = -126 a is held at 2^-126.
+// alone its rounding to 2^-24 would be 6e-5 of 1 - a^2 at a memory of 1000 steps. The coefficients
+// are a least-maximum fit of (1 - 2^f) / f on |f| <= 1/2. Below z = -126 a is held at 2^-126.
 __device__ __forceinline__ void decay2(float2 z, float2& rest, float2& a) {
   z = make_float2(max_nan(z.x, -126.0f), max_nan(z.y, -126.0f));
   const float2 t = add2(z, two(12582912.0f));  // 1.5 * 2^23: n in the low bits

@@ -1,11 +1,11 @@
-// glr_join.cuh -- what the kernels over rows share (glr_join and its gradients): a row of H channels
-// belongs to a block of R threads (a multiple of 32) and stays in their registers. Item (j, v) of
-// thread t is channel (j R + t) VEC + v. VEC elements make a 16-byte access when H, the strides and the
-// pointers allow it, else VEC = 1. Every sum over a row is taken from registers, in two passes
-// where a mean has to come off first, and each activation is read once and written once. Blocks
-// stay on the GPU and go from row to row; while a row's sums go around its warps, the next row's
-// inputs come into shared memory by asynchronous copies, each thread its own items, so that no
-// barrier waits for them. One row to a block keeps every row's address in uniform registers.
+// glr_join.cuh -- what the kernels over rows share (glr_join and its gradients): a row of H
+// channels belongs to a block of R threads (a multiple of 32) and stays in their registers. Item
+// (j, v) of thread t is channel (j R + t) VEC + v. VEC elements make a 16-byte access when H, the
+// strides and the pointers allow it, else VEC = 1. Every sum over a row is taken from registers, in
+// two passes where a mean has to come off first, and each activation is read once and written once.
+// Blocks stay on the GPU and go from row to row; while a row's sums go around its warps, the next
+// row's inputs come into shared memory by asynchronous copies, each thread its own items, so that
+// no barrier waits for them. One row to a block keeps every row's address in uniform registers.
 #pragma once
 
 #include <algorithm>
@@ -49,8 +49,8 @@ struct Ckpt {
   uint8_t *hc, *hs, *gc, *gs;
 };
 
-// The sums of K values over the threads of a block. buf holds two sets of kSums floats for each of 32
-// warps, used in turn (`turn`), so that one barrier a call is enough.
+// The sums of K values over the threads of a block. buf holds two sets of kSums floats for each of
+// 32 warps, used in turn (`turn`), so that one barrier a call is enough.
 constexpr int kSums = 2;
 template <int K>
 __device__ __forceinline__ void row_sum(float (&s)[K], float* buf, int& turn) {
@@ -84,8 +84,12 @@ struct Items {
   __device__ __forceinline__ bool on(int j) const { return channel(j) < H; }
   __device__ __forceinline__ bool all() const { return on(NV - 1); }  // no item past the end
   // the items of pair p's halves
-  static __device__ __forceinline__ constexpr int first(int p) { return VEC > 1 ? p * 2 / VEC : 2 * p; }
-  static __device__ __forceinline__ constexpr int second(int p) { return VEC > 1 ? p * 2 / VEC : 2 * p + 1; }
+  static __device__ __forceinline__ constexpr int first(int p) {
+    return VEC > 1 ? p * 2 / VEC : 2 * p;
+  }
+  static __device__ __forceinline__ constexpr int second(int p) {
+    return VEC > 1 ? p * 2 / VEC : 2 * p + 1;
+  }
   // float32 parameters of the channels; 0 past the end
   __device__ __forceinline__ void params(const float* w, float2 (&out)[P]) const {
     if (all()) {
@@ -120,7 +124,10 @@ struct Items {
   static __device__ __forceinline__ void pick(int j, const float2 (&in)[P], float* t) {
     if constexpr (VEC > 1) {
 #pragma unroll
-      for (int v = 0; v < VEC; v += 2) t[v] = in[(j * VEC + v) / 2].x, t[v + 1] = in[(j * VEC + v) / 2].y;
+      for (int v = 0; v < VEC; v += 2) {
+        t[v] = in[(j * VEC + v) / 2].x;
+        t[v + 1] = in[(j * VEC + v) / 2].y;
+      }
     } else {
       t[0] = j & 1 ? in[j / 2].y : in[j / 2].x;
     }
@@ -154,9 +161,10 @@ struct Items {
   }
 };
 
-// The shared memory of one array of a block's rows: item j of thread t. Copies of one stage go to it
-// asynchronously (16, 8 or 4 bytes an item; single 16-bit elements and bytes by a load and a store).
-// kDirect: rows too long for that; nothing is staged and the items are read from memory (again by the L2).
+// The shared memory of one array of a block's rows: item j of thread t. Copies of one stage go to
+// it asynchronously (16, 8 or 4 bytes an item; single 16-bit elements and bytes by a load and a
+// store). kDirect: rows too long for that; nothing is staged and the items are read from memory
+// (again by the L2).
 template <typename T, int VEC, int NV, bool kDirect>
 struct Staged {
   static constexpr int kBytes = VEC * (int)sizeof(T);
@@ -164,10 +172,13 @@ struct Staged {
   struct alignas(kBytes) item {
     uint8_t bytes[kBytes];
   };
-  static __device__ __forceinline__ int slot(int j) { return j * (int)blockDim.x + (int)threadIdx.x; }
+  static __device__ __forceinline__ int slot(int j) {
+    return j * (int)blockDim.x + (int)threadIdx.x;
+  }
   static __device__ __forceinline__ int items() { return NV * (int)blockDim.x; }
   // zeros for an item that is not there
-  static __device__ __forceinline__ void fetch(item* s, int j, const T* src, const T* any, bool on) {
+  static __device__ __forceinline__ void fetch(item* s, int j, const T* src, const T* any,
+                                               bool on) {
     if constexpr (kDirect) return;
     if constexpr (kAsync) {
       const uint32_t d = (uint32_t)__cvta_generic_to_shared(s + slot(j));
@@ -206,8 +217,8 @@ struct Staged {
       k.get(src);
     return k;
   }
-  static __device__ __forceinline__ void get(const item* s, const Items<VEC, NV>& it, const Rows<const T>& r,
-                                             int64_t row,
+  static __device__ __forceinline__ void get(const item* s, const Items<VEC, NV>& it,
+                                             const Rows<const T>& r, int64_t row,
                                              float2 (&out)[Items<VEC, NV>::P]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -225,8 +236,8 @@ __device__ __forceinline__ void stage_wait() {
 
 // z -> z less its mean (layer) and 1 / its deviation. Channels past H hold 0 and are left at 0.
 template <int VEC, int NV>
-__device__ __forceinline__ float centre(const Items<VEC, NV>& it, float2 (&z)[VEC * NV / 2], bool layer,
-                                        float inv_h, float eps, float* buf, int& turn) {
+__device__ __forceinline__ float centre(const Items<VEC, NV>& it, float2 (&z)[VEC * NV / 2],
+                                        bool layer, float inv_h, float eps, float* buf, int& turn) {
   constexpr int P = VEC * NV / 2;
   if (layer) {
     float2 t = two(0.0f);
@@ -247,7 +258,8 @@ __device__ __forceinline__ float centre(const Items<VEC, NV>& it, float2 (&z)[VE
   return 1.0f / sqrtf(q[0] * inv_h + eps);
 }
 
-// act(g) = g s or s, s = sigmoid(g); g sigmoid(g) is 0 at -inf (where g is taken as a finite number)
+// act(g) = g s or s, s = sigmoid(g); g sigmoid(g) is 0 at -inf (where g is taken as a finite
+// number)
 __device__ __forceinline__ float2 silu(float2 g, float2 s) {
   return mul2(make_float2(max_nan(g.x, -1e30f), max_nan(g.y, -1e30f)), s);
 }
@@ -274,7 +286,9 @@ Rows<T> rows(P* p, int64_t st) {
 }
 
 // Threads of a row, for `each` channels of a thread.
-inline int row_threads(int64_t H, int each) { return (int)(((H + each - 1) / each + 31) / 32 * 32); }
+inline int row_threads(int64_t H, int each) {
+  return (int)(((H + each - 1) / each + 31) / 32 * 32);
+}
 
 constexpr size_t kMostSmem = 220 * 1024;  // of an SM for the staged rows
 

@@ -14,8 +14,18 @@
 // to the nearest one whose end value is there, and publishes its own end value. End values are
 // always formed in the same order (each from the one before it), so the results do not depend on
 // which of them a tile found. A tile that begins a sequence knows its end from its own steps.
+//
+// What bounds it: four arrays go through memory forwards and seven backwards, but in 16 bits the 5
+// and 7 special functions and some 40 and 73 instructions an element weigh as much. B4 L16384 H2048
+// bfloat16 takes 233 us forwards (4.6 TB/s, 68% of a plain copy's bandwidth) and 415 us backwards
+// (4.5 TB/s); at L2048 the counters show 49% and 52% of the issue slots used, the special-function
+// pipe at 36% and 30%, and the rest of the time waits between a tile's two phases, which all warps
+// of the one block on an SM go through together. Two smaller blocks on an SM (6 computing warps
+// each: 297 and 612 us), 12 warps (248 and 415 us) or one reciprocal for both gates (241 and 425
+// us) were slower. In float32 memory bounds it: B1 L4096 H4096 52 and 81 us (75% and 85%). Where a
+// row of tiles is long and there are few, a tile's turn on its chain does: B1 L65536 H256 float32
+// 89 us (44%).
 #include <algorithm>
-#include <type_traits>
 
 #include "glr_common.cuh"
 #include "tc_ptx.cuh"
@@ -29,12 +39,13 @@ int* device_status_word();
 namespace glr {
 namespace {
 
-constexpr int kHead = 64;  // words of the chain's workspace before the maps; the first counts tickets
+// Words of the chain's workspace before the maps; the first counts tickets.
+constexpr int kHead = 64;
 
-// Every word of the chain's workspace begins with these bits, a NaN that no arithmetic makes: a float
-// that reads otherwise has been published. One 32-bit store publishes one float, so readers need
-// neither flags nor fences; with flags, the two fences of a tile (to the L2 and back each)
-// and the flag's own way made a tile's turn on the chain 4 us long instead of some 1.2 us.
+// Every word of the chain's workspace begins with these bits, a NaN that no arithmetic makes: a
+// float that reads otherwise has been published. One 32-bit store publishes one float, so readers
+// need neither flags nor fences. With flags, a tile's two fences and the flag's own way made B4
+// L2048 H2048 bfloat16 take 56 us where it took 48 us so.
 constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;  // a longer wait is a fault
 
@@ -133,9 +144,11 @@ __device__ __forceinline__ Tile tile_of(const J& q, uint32_t k, bool backwards) 
 
 // s through a map (A, e): A s + e
 template <int VEC>
-__device__ __forceinline__ void through(const float (&A)[VEC], const float (&e)[VEC], float (&s)[VEC]) {
+__device__ __forceinline__ void through(const float (&A)[VEC], const float (&e)[VEC],
+                                        float (&s)[VEC]) {
   if constexpr (VEC == 2) {
-    const float2 t = fma2(make_float2(A[0], A[1]), make_float2(s[0], s[1]), make_float2(e[0], e[1]));
+    const float2 t = fma2(make_float2(A[0], A[1]), make_float2(s[0], s[1]),
+                          make_float2(e[0], e[1]));
     s[0] = t.x, s[1] = t.y;
   } else {
     s[0] = fmaf(A[0], s[0], e[0]);
@@ -161,20 +174,22 @@ struct Patience {
   }
 };
 
-// Called by one warp: the value s that enters the tile, and `end`, the one that leaves it, from
-// the tile's map (A, e); `cut`: the map does not depend on what enters. row: the lane's first
-// element of `in`; dir = 1 forwards, -1 backwards. The first tile of the chain has its s.
+// Called by one warp: the value s that enters the tile, and `end`, the one that leaves it, from the
+// tile's map (A, e); `cut`: the map does not depend on what enters. row: the lane's first element
+// of `in`; dir = 1 forwards, -1 backwards. The first tile of the chain has its s.
 //
 // Each lane looks at one of the 32 tiles before this one, at the group's first channel, for the
-// nearest whose end value is there with all maps between there too; the first tile of a chain always
-// comes to its end value by itself. With the same loads comes the end value of the tile just before
-// for the lane's own channels, which many chains side by side mostly find; else that end value
-// and the maps are read then.
+// nearest whose end value is there with all maps between there too; the first tile of a chain
+// always comes to its end value by itself. With the same loads comes the end value of the tile just
+// before for the lane's own channels, which many chains side by side mostly find; else that end
+// value and the maps are read then.
 template <int VEC, typename J>
 __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, int dir,
                                       const float (&A)[VEC], const float (&e)[VEC], bool cut,
                                       float (&s)[VEC], float (&end)[VEC]) {
-  constexpr int U = VEC == 1 ? 8 : 4;  // 90 against 94 us at B1 L65536 H256 f32; 8 pairs cost registers
+  // maps read at a time: 8 against 4 is 90 against 94 us at B1 L65536 H256 f32; 8 pairs of
+  // channels want too many registers (B8 L4096 H256 bf16: 24.3 against 23.6 us)
+  constexpr int U = VEC == 1 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const int done = dir > 0 ? at.tile : q.tiles - 1 - at.tile;  // tiles of the chain before this
   const bool last = done == q.tiles - 1;
@@ -186,7 +201,7 @@ __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, i
     const int64_t all = q.B * q.tiles * q.HP;
     if (!last && cut && DLR_IN(row + step + VEC - 1, all)) post(q.in + row + step, e);
     if (!last && !cut && DLR_IN(row + VEC - 1, all)) post(q.maps + 2 * row, m);
-    const float* in = q.in + row;                   // what enters this tile: the end of the one before
+    const float* in = q.in + row;                   // the end of the tile before
     const float* maps = q.maps + 2 * (row - step);  // of the one before
     Patience wait;
     int far = 0;           // maps between the nearest end and this tile
@@ -255,8 +270,8 @@ __device__ __forceinline__ void chain(const J& q, const Tile& at, int64_t row, i
     post(q.in + row + step, end);
 }
 
-// The warps' maps of a tile, (A, e) of all its channels each, folded in shared memory's order by the
-// chain's warp: the tile's map, and the value that enters each warp's steps.
+// The warps' maps of a tile, (A, e) of all its channels each, folded in shared memory's order by
+// the chain's warp: the tile's map, and the value that enters each warp's steps.
 template <int W, int VEC>
 struct Fold {
   float A[W][VEC], e[W][VEC];
@@ -296,10 +311,10 @@ struct Fold {
   }
 };
 
-// As chain(), for few chains, of which many tiles are at work at a time, in runs of kRun tiles: the last tile of a
-// run publishes the map of the whole run, and later the value that enters the next run. A tile takes the value
-// that enters its own run, looking back over runs, through the maps of its run's tiles before it. A map that does
-// not depend on what enters has kCut for its A.
+// As chain(), for few chains, of which many tiles are at work at a time, in runs of kRun tiles: the
+// last tile of a run publishes the map of the whole run, and later the value that enters the next
+// run. A tile takes the value that enters its own run, looking back over runs, through the maps of
+// its run's tiles before it. A map that does not depend on what enters has kCut for its A.
 constexpr uint32_t kCut = 0xfffffffeu;
 constexpr int kRun = 8;
 template <int VEC>
@@ -454,8 +469,8 @@ __device__ __forceinline__ float2 sign_ones(float2 k) {
 }
 __device__ __forceinline__ float2 kept_decay(float2 k) { return add2(k, sign_ones(k)); }
 
-// A warp's S steps of VEC channels a lane are S VEC / 2 pairs: the two channels of a step, or, with one
-// channel to a lane, two steps. half(): step j of channel v.
+// A warp's S steps of VEC channels a lane are S VEC / 2 pairs: the two channels of a step, or, with
+// one channel to a lane, two steps. half(): step j of channel v.
 template <int VEC, int N>
 __device__ __forceinline__ float& half(float2 (&p)[N], int j, int v) {
   if constexpr (VEC == 2) return v ? p[j].y : p[j].x;
@@ -480,11 +495,11 @@ __device__ __forceinline__ void advance(float (&s)[VEC], float2 (&a)[N], float2 
 }
 
 // How a tile's inputs come into shared memory and its outputs leave it. Where every row begins on a
-// 16-byte boundary and H is a whole number of 16 bytes, one thread has a whole tile moved by a tensor
-// copy (kTma), which also fills what a tile has past the ends with zeros and leaves it out on the way
-// back; describing an array to it costs the host some 0.1 us. Else the computing warps copy 4 bytes at a
-// time, or single elements where not even 4-byte boundaries hold (16-bit types with odd strides), and
-// store for themselves.
+// 16-byte boundary and H is a whole number of 16 bytes, one thread has a whole tile moved by a
+// tensor copy (kTma), which also fills what a tile has past the ends with zeros and leaves it out
+// on the way back; describing an array to it costs the host some 0.1 us. Else the computing warps
+// copy 4 bytes at a time, or single elements where not even 4-byte boundaries hold (16-bit types
+// with odd strides), and store for themselves.
 constexpr int kTma = 16;
 
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
@@ -500,13 +515,13 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// kSteps rows of C channels of v into dst [kSteps][C], by kThreads threads; rows past the end and channels
-// past H are zero
+// kSteps rows of C channels of v into dst [kSteps][C], by kThreads threads; rows past the end and
+// channels past H are zero
 template <typename T, int C, int kSteps, int kBytes, int kThreads>
 __device__ __forceinline__ void stage(T* dst, const view<const T>& v, int64_t b, int64_t t0,
                                       int64_t h0, int64_t L, int64_t H) {
   constexpr int per = kBytes / (int)sizeof(T), cols = C / per, rows = kThreads / cols;
-  static_assert(kSteps % rows == 0, "whole rounds");
+  static_assert(kSteps % rows == 0, "whole turns");
   const int col = threadIdx.x % cols * per, first = threadIdx.x / cols;
   const T* p = v.row(b, t0 + first) + h0 + col;
   const int64_t dp = rows * v.st;
@@ -549,7 +564,7 @@ __device__ __forceinline__ void put(T* p, const float (&f)[VEC], bool (&on)[VEC]
   }
 }
 
-// channels of a lane: a warp's row of a tile is 128 bytes
+// Channels of a lane: a warp's row of a tile is 128 bytes.
 template <typename T>
 constexpr int kVec = 4 / (int)sizeof(T);
 
@@ -559,8 +574,8 @@ constexpr int kScanTile = kScanSteps * kScanWarps;   // steps
 constexpr int kScanThreads = 32 * (kScanWarps + 2);
 constexpr int kRing = 8;                             // tiles whose places a block remembers
 
-// Named barriers of a block, two of each kind for even and odd tiles: the maps of a tile are in shared
-// memory (the computing warps arrive, the chain's warp waits); the values that enter its
+// Named barriers of a block, two of each kind for even and odd tiles: the maps of a tile are in
+// shared memory (the computing warps arrive, the chain's warp waits); the values that enter its
 // warps are there (the chain's warp arrives, all others wait); and two for the beginning.
 constexpr int kMapsBar = 1, kEnterBar = 3, kWarpsBar = 5;
 
@@ -579,7 +594,9 @@ struct ScanShared {
 
 // One warp keeps the chain and one supplies the tiles; the others compute, one tile ahead of the
 // chain: they have the gates of tile k + 1 done before they need the state that enters tile k, so a
-// tile's way along the chain (stores and loads through L2) passes while they work.
+// tile's way along the chain (stores and loads through L2) passes while they work. A tile is 14
+// warps of 8 steps: with the gates of two tiles in registers (64 of them) 16 warps fill the
+// register file.
 template <typename T, int kBytes, bool kRuns>
 __global__ void __launch_bounds__(kScanThreads, 1)
 scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant__ Maps<1> out,
@@ -614,8 +631,8 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       tc::mbar_arrive_expect_tx(&sh.here[k & 1], sizeof(sh.buf[0]));
 #pragma unroll
       for (int a = 0; a < 3; ++a)
-        tc::tma_load_3d(&sh.buf[k & 1][a][0][0], &in.map[a], at.group * C, at.tile * kScanTile, at.b,
-                        &sh.here[k & 1]);
+        tc::tma_load_3d(&sh.buf[k & 1][a][0][0], &in.map[a], at.group * C, at.tile * kScanTile,
+                        at.b, &sh.here[k & 1]);
     };
     if (lane == 0) {
       tc::mbar_init(&sh.here[0], 1);
@@ -702,7 +719,8 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
     const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
     z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
-    const float2 kz = make_float2(sh.kz[k % kRing][lane * VEC], sh.kz[k % kRing][lane * VEC + VEC - 1]);
+    const float* own = &sh.kz[k % kRing][lane * VEC];
+    const float2 kz = make_float2(own[0], own[VEC - 1]);
     const T* r = &sh.buf[k & 1][0][warp * S][lane * VEC];
     if (kBulk && !tc::mbar_wait_sleep(&sh.here[k & 1], (k >> 1) & 1) && lane == 0)
       report_status(q.status, DLR_ERR_TIMEOUT);
@@ -891,8 +909,8 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       tc::mbar_arrive_expect_tx(here, 2 * kBackTile * 128);
 #pragma unroll
       for (int a = 0; a < 2; ++a)
-        tc::tma_load_3d(dst + a * kBackTile * C, &in.map[first + a], at.group * C, at.tile * kBackTile, at.b,
-                        here);
+        tc::tma_load_3d(dst + a * kBackTile * C, &in.map[first + a], at.group * C,
+                        at.tile * kBackTile, at.b, here);
     };
     auto copy_rd = [&](int k) { copy(&sh.rd[k & 3][0][0][0], &sh.rd_here[k & 3], 0, k); };
     auto copy_ix = [&](int k) { copy(&sh.ix[k & 1][0][0][0], &sh.ix_here[k & 1], 2, k); };
@@ -1001,8 +1019,8 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
     z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
-    const float2 kz = mul2(make_float2(sh.k[k % kRing][lane * VEC], sh.k[k % kRing][lane * VEC + VEC - 1]),
-                           two(-kLog2e));
+    const float* own = &sh.k[k % kRing][lane * VEC];
+    const float2 kz = mul2(make_float2(own[0], own[VEC - 1]), two(-kLog2e));
     const T* r = &sh.rd[k & 3][0][warp * S][lane * VEC];
     wait(&sh.rd_here[k & 3], (k >> 2) & 1);
     float2 a[NP];
@@ -1079,7 +1097,8 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       G[v] = sh.enter[k & 1][warp][lane * VEC + v];
       sum[v] = 0.0f;
     }
-    const float2 k2 = make_float2(sh.k[k % kRing][lane * VEC], sh.k[k % kRing][lane * VEC + VEC - 1]);
+    const float* own = &sh.k[k % kRing][lane * VEC];
+    const float2 k2 = make_float2(own[0], own[VEC - 1]);
     T* r = &sh.rd[k & 3][0][warp * S][lane * VEC];
     T* i = &sh.ix[k & 1][0][warp * S][lane * VEC];
     T* x = i + kBackTile * C;
@@ -1240,9 +1259,10 @@ back_sum(const float* __restrict__ part, int64_t n, int64_t H, const float* __re
 constexpr int kThreads = 128;
 constexpr int kStepRows = 4;
 
-// One token. A thread has VEC channels (two neighbouring 16-bit or 32-bit ones where the rows allow an access
-// of both) of kStepRows batch entries, whose loads go out together and share the decay parameter. Two
-// channels and four entries to a thread: 256 x 4096 bf16 in 3.8 us, against 6.9 us with one element.
+// One token. A thread has VEC channels (two neighbouring 16-bit or 32-bit ones where the rows allow
+// an access of both) of kStepRows batch entries, whose loads go out together and share the decay
+// parameter. Two channels and four entries to a thread: 256 x 4096 bf16 in 3.8 us, against 6.9 us
+// with one element.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
 step_kernel(view<const T> x, view<const T> r, view<const T> i, const float* __restrict__ p,
@@ -1277,7 +1297,8 @@ step_kernel(view<const T> x, view<const T> r, view<const T> i, const float* __re
   for (int j = 0; j < kStepRows; ++j) {
     if (j >= n) break;
     const gate2 g = make_gate2(make_float2(rv[j][0], rv[j][VEC - 1]),
-                               make_float2(iv[j][0], iv[j][VEC - 1]), make_float2(kz[0], kz[VEC - 1]));
+                               make_float2(iv[j][0], iv[j][VEC - 1]),
+                               make_float2(kz[0], kz[VEC - 1]));
     const float2 b = mul2(g.m, mul2(g.si, make_float2(xv[j][0], xv[j][VEC - 1])));
     float2 s = fma2(g.a, make_float2(hv[j][0], hv[j][VEC - 1]), b);
     if (cut[j]) s = b;
@@ -1321,15 +1342,15 @@ bool describe(CUtensorMap* m, const V& v, int64_t B, int64_t L, int64_t H, int r
   auto fn = tc::tensor_map_encoder();
   if (!fn) return false;
   const CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+                                   : is_half<T>   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const cuuint64_t dims[3] = {(cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
   // the stride of a dimension of one is never used
   const cuuint64_t st = (cuuint64_t)(L > 1 ? v.stride_t : H) * sizeof(T);
   const cuuint64_t strides[2] = {st, B > 1 ? (cuuint64_t)v.stride_b * sizeof(T) : st};
   const cuuint32_t box[3] = {128 / sizeof(T), (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
-  return fn(m, type, 3, const_cast<void*>(static_cast<const void*>(v.data)), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+  return fn(m, type, 3, const_cast<void*>(static_cast<const void*>(v.data)), dims, strides, box,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // whether it can be: strides that are positive, a multiple of 16 bytes and below 2^40 of them
@@ -1353,12 +1374,13 @@ Job<T> make_job(const A& a, const Space& sp) {
   const int64_t groups = (a.H + 32 * kVec<T> - 1) / (32 * kVec<T>);
   return {in_view<T>(a.x), in_view<T>(a.r), in_view<T>(a.i), a.p, a.reset,
           reinterpret_cast<float*>(ws + sp.head + sp.maps), reinterpret_cast<float*>(ws + sp.head),
-          nullptr, nullptr, reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H, sp.HP, a.B * groups,
+          nullptr, nullptr, reinterpret_cast<uint32_t*>(ws), device_status_word(), a.B, a.L, a.H,
+          sp.HP, a.B * groups,
           (int)groups, (int)sp.tiles, 0, 1, (float)a.c};
 }
 
-// Blocks for all tiles, one to an SM at most; the chain's workspace becomes empty. A chain of one tile
-// needs neither that nor the counter: each has a block.
+// Blocks for all tiles, one to an SM at most; the chain's workspace becomes empty. A chain of one
+// tile needs neither that nor the counter: each has a block.
 template <typename T>
 cudaError_t prepare_chain(Job<T>& q, const Space& sp, unsigned* blocks, cudaStream_t s) {
   const int64_t all = q.chains * q.tiles;
@@ -1370,9 +1392,9 @@ cudaError_t prepare_chain(Job<T>& q, const Space& sp, unsigned* blocks, cudaStre
   if (e != cudaSuccess) return e;
   *blocks = (unsigned)std::min<int64_t>(all, sms);
   q.most = (int)((all - 1) / *blocks + 1);  // all blocks get as many, however early they come
-  // Runs, where many tiles of a chain are at work at a time. B1 L65536, us with and without runs: float32
-  // H64 (2 chains) 28 and 41, H128 (4) 63 and 57, H256 (8) 115 and 89; bfloat16 H64 (1) 21 and 65, H256
-  // (4) 68 and 89, but B2 H256 (8) 128 and 112.
+  // Runs, where many tiles of a chain are at work at a time. B1 L65536, us with and without runs:
+  // float32 H64 (2 chains) 28 and 41, H128 (4) 63 and 57, H256 (8) 115 and 89; bfloat16 H64 (1) 21
+  // and 65, H256 (4) 68 and 89, but B2 H256 (8) 128 and 112.
   if (*blocks / q.chains * kVec<T> >= 64) q.runs = (q.tiles - 1) / kRun + 1;
   q.run_in = q.in + sp.in / sizeof(float);
   q.run_maps = q.run_in + q.B * q.runs * q.HP;
@@ -1450,7 +1472,8 @@ cudaError_t scan_t(const glr_scan_args& a, cudaStream_t s) {
     return a.H * z % n == 0 && wide(a.x, z, n) && wide(a.r, z, n) && wide(a.i, z, n) &&
            wide(a.y, z, n);
   };
-  if (a.H * z % 16 == 0 && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.y)) return scan_w<T, kTma>(a, s);
+  if (a.H * z % 16 == 0 && tma(a.x) && tma(a.r) && tma(a.i) && tma(a.y))
+    return scan_w<T, kTma>(a, s);
   if (all(4)) return scan_w<T, 4>(a, s);
   if constexpr (sizeof(T) == 2) return scan_w<T, 2>(a, s);
   return cudaErrorInvalidValue;  // not reached: float rows begin on 4-byte boundaries

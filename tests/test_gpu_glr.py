@@ -74,7 +74,8 @@ SCAN_CASES = [
     (1, 5000, 8, "apart", True, 3), (1, 70001, 3, "apart", False, 0),
     (4, 4000, 640, "columns", True, 9),  # more tiles to a block than it remembers places for
     # few chains with many tiles at work: runs of tiles, ended by resets and by the row's end
-    (1, 40000, 32, "apart", True, 0), (1, 9000, 64, "columns", True, 40), (2, 21000, 20, "apart", False, 3),
+    (1, 40000, 32, "apart", True, 0), (1, 9000, 64, "columns", True, 40),
+    (2, 21000, 20, "apart", False, 3),
 ]
 
 
@@ -570,7 +571,8 @@ def test_refusals():
         glr.glr_scan(x, r, i, p, out=torch.empty(1, L, H, dtype=x.dtype,
                                                  device="cuda").expand(B, L, H))
     with pytest.raises(dlr.DLRError):
-        glr.glr_scan(*(t.repeat(1, 20, 1) for t in (x, r, i)), p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        glr.glr_scan(*(t.repeat(1, 20, 1) for t in (x, r, i)), p,
+                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     w, al = torch.ones(H, device="cuda"), torch.ones(1, device="cuda")
     a = [t.reshape(B * L, H) for t in (x, r, i)]
     with pytest.raises(KeyError):
