@@ -180,24 +180,26 @@ __device__ __forceinline__ void decay2(float2 z, float2& rest, float2& a) {
   a = mul2(s, fma2(q, two(-1.0f), two(1.0f)));
 }
 
-// Two elements' gates. kz = -c softplus(p) log2(e).
-struct gate2 {
-  float2 sr, si;    // sigmoid(r), sigmoid(i)
-  float2 rest, a;   // the decay from 1, and the decay
-  float2 m;         // sqrt(1 - a^2)
-};
 // 1 / sqrt(u), a finite number where u is 0
 __device__ __forceinline__ float2 rsqrt2(float2 u) {
   return make_float2(rsqrt_approx(max_nan(u.x, 1e-36f)), rsqrt_approx(max_nan(u.y, 1e-36f)));
 }
-__device__ __forceinline__ gate2 make_gate2(float2 r, float2 i, float2 kz) {
-  gate2 g;
-  g.sr = sigmoid2(r);
-  g.si = sigmoid2(i);
-  decay2(mul2(kz, g.sr), g.rest, g.a);
-  const float2 u = mul2(g.rest, add2(g.a, two(1.0f)));
-  g.m = mul2(u, rsqrt2(u));
-  return g;
+__device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays a NaN
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Two elements' decays and inputs: a, and b = sqrt(1 - a^2) sigmoid(i) x. kz = -c softplus(p) log2(e).
+// With u = 1 - a^2 and d = 1 + e^-i, b = x u / sqrt(u d^2), which takes one special function less than
+// sqrt(u) and 1 / d by themselves. e^-i is held at 2^60, so that d^2 stays finite.
+__device__ __forceinline__ void gates2(float2 r, float2 i, float2 x, float2 kz, float2& a, float2& b) {
+  float2 rest;
+  decay2(mul2(kz, sigmoid2(r)), rest, a);
+  const float2 u = mul2(rest, add2(a, two(1.0f)));
+  const float2 t = mul2(i, two(-kLog2e));
+  const float2 d = add2(make_float2(min_nan(ex2(t.x), 0x1p60f), min_nan(ex2(t.y), 0x1p60f)), two(1.0f));
+  b = mul2(mul2(u, rsqrt2(mul2(mul2(u, d), d))), x);
 }
 
 }  // namespace glr

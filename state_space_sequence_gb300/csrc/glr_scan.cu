@@ -15,16 +15,17 @@
 // always formed in the same order (each from the one before it), so the results do not depend on
 // which of them a tile found. A tile that begins a sequence knows its end from its own steps.
 //
-// What bounds it: four arrays go through memory forwards and seven backwards, but in 16 bits the 5
+// What bounds it: four arrays go through memory forwards and seven backwards, but in 16 bits the 4
 // and 7 special functions and some 40 and 73 instructions an element weigh as much. B4 L16384 H2048
-// bfloat16 takes 233 us forwards (4.6 TB/s, 68% of a plain copy's bandwidth) and 415 us backwards
-// (4.5 TB/s); at L2048 the counters show 49% and 52% of the issue slots used, the special-function
-// pipe at 36% and 30%, and the rest of the time waits between a tile's two phases, which all warps
-// of the one block on an SM go through together. Two smaller blocks on an SM (6 computing warps
-// each: 297 and 612 us), 12 warps (248 and 415 us) or one reciprocal for both gates (241 and 425
-// us) were slower. In float32 memory bounds it: B1 L4096 H4096 52 and 81 us (75% and 85%). Where a
-// row of tiles is long and there are few, a tile's turn on its chain does: B1 L65536 H256 float32
-// 89 us (44%).
+// bfloat16 takes 227 us forwards (4.7 TB/s, 70% of a plain copy's bandwidth) and 415 us backwards
+// (4.5 TB/s), and 3 and 1 us less with the chain left out; at L2048 the counters show half of the
+// issue slots used, the special-function pipe at 30 to 36%, and the rest of the time waits between
+// a tile's two phases, which all warps of the one block on an SM go through together. Two smaller
+// blocks on an SM (6 computing warps each: 297 and 612 us), 12 warps (248 and 415 us) or one
+// reciprocal for both gates (241 and 425 us) were slower than the 233 and 415 us of their time. In
+// float32 memory bounds it: B1 L4096 H4096 52 and 81 us (75% and 85%). Where a row of tiles is long
+// and there are few, a tile's turn on its chain does: B1 L65536 H256 float32 88 us (45%; 46 us with
+// the chain left out).
 #include <algorithm>
 
 #include "glr_common.cuh"
@@ -452,6 +453,16 @@ __device__ __forceinline__ void chain_runs(const J& q, const Tile& at, int64_t r
   through_cut<VEC>(m, end);
 }
 
+// How many of S steps there are when `left` are left of the row. The empty statement pins the value: formed
+// in 32 bits and left to the compiler, it came out as S in the stores of a warp whose steps the row's
+// end cuts short (seen with float32 and rows of 4-byte alignment), which then wrote past the row.
+template <int S>
+__device__ __forceinline__ int steps_left(int64_t left) {
+  int n = (int)max((int64_t)0, min((int64_t)S, left));
+  asm volatile("" : "+r"(n));
+  return n;
+}
+
 // bits of the n steps from t on that begin a sequence
 __device__ __forceinline__ uint32_t cuts(const uint8_t* reset, int64_t first, int n) {
   if (!reset) return 0u;
@@ -717,7 +728,7 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       return;
     }
     const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
-    z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
+    z.n = steps_left<S>(q.L - t0);
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
     const float* own = &sh.kz[k % kRing][lane * VEC];
     const float2 kz = make_float2(own[0], own[VEC - 1]);
@@ -726,9 +737,8 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       report_status(q.status, DLR_ERR_TIMEOUT);
 #pragma unroll
     for (int m = 0; m < NP; ++m) {
-      const gate2 g = make_gate2(get2<T, VEC, C>(r, m), get2<T, VEC, C>(r + kScanTile * C, m), kz);
-      z.a[m] = g.a;
-      z.b[m] = mul2(g.m, mul2(g.si, get2<T, VEC, C>(r + 2 * kScanTile * C, m)));
+      gates2(get2<T, VEC, C>(r, m), get2<T, VEC, C>(r + kScanTile * C, m),
+             get2<T, VEC, C>(r + 2 * kScanTile * C, m), kz, z.a[m], z.b[m]);
     }
     if (z.n < S) {
 #pragma unroll
@@ -1017,7 +1027,7 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       return;
     }
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
-    z.n = (int)max((int64_t)0, min((int64_t)S, q.L - t0));
+    z.n = steps_left<S>(q.L - t0);
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
     const float* own = &sh.k[k % kRing][lane * VEC];
     const float2 kz = mul2(make_float2(own[0], own[VEC - 1]), two(-kLog2e));
@@ -1296,11 +1306,10 @@ step_kernel(view<const T> x, view<const T> r, view<const T> i, const float* __re
 #pragma unroll
   for (int j = 0; j < kStepRows; ++j) {
     if (j >= n) break;
-    const gate2 g = make_gate2(make_float2(rv[j][0], rv[j][VEC - 1]),
-                               make_float2(iv[j][0], iv[j][VEC - 1]),
-                               make_float2(kz[0], kz[VEC - 1]));
-    const float2 b = mul2(g.m, mul2(g.si, make_float2(xv[j][0], xv[j][VEC - 1])));
-    float2 s = fma2(g.a, make_float2(hv[j][0], hv[j][VEC - 1]), b);
+    float2 a, b;
+    gates2(make_float2(rv[j][0], rv[j][VEC - 1]), make_float2(iv[j][0], iv[j][VEC - 1]),
+           make_float2(xv[j][0], xv[j][VEC - 1]), make_float2(kz[0], kz[VEC - 1]), a, b);
+    float2 s = fma2(a, make_float2(hv[j][0], hv[j][VEC - 1]), b);
     if (cut[j]) s = b;
     if (!DLR_IN((b0 + j) * H + ch + VEC - 1, B * H)) continue;
     const float out[2] = {s.x, s.y};

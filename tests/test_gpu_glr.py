@@ -112,6 +112,24 @@ def test_scan_and_its_gradients(B, L, H, layout, start, cuts, dtype):
     assert dlr.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [33, 65, 66, 128, 258])
+def test_nothing_is_written_outside_the_rows(H, dtype):
+    """y, dx, dr and di as the middle rows of larger buffers: what stands around them stays, for
+    rows that end anywhere in a warp's steps, with one and with several tiles to a block."""
+    B, room = 2, 128
+    p = decay_param(H)
+    for L in (1, 7, 8, 9, 112, 113, 250, 905, 1017, 1025, 1030, 1032, 2025):
+        x, r, i, dy = arrays("apart", 4, L, B, L, H, dtype)
+        bufs = [torch.full((B, L + 2 * room, H), 7.0, dtype=dtype, device="cuda") for _ in range(4)]
+        y, dx, dr, di = (b[:, room:room + L] for b in bufs)
+        _, _, st = glr.glr_scan(x, r, i, p, out=y, save_states=True)
+        glr.glr_scan_backward(x, r, i, p, dy, st, out=(dx, dr, di))
+        for b in bufs:
+            assert (b[:, :room] == 7).all() and (b[:, room + L:] == 7).all(), L
+            assert torch.isfinite(b).all()
+
+
 def test_scan_of_no_steps():
     x = torch.empty(2, 0, 5, device="cuda")
     p, h0, dhl = decay_param(5), normal(1, 2, 5), normal(2, 2, 5)
