@@ -2,8 +2,8 @@
 // (include/glr.h, glr_join): u = h act(g), y = x + alpha w norm(u), n = v norm(y), with h and g
 // kept in 8 bits on the way where the caller wants them for the gradients.
 //
-// Bound by memory: three rows in and two out. 32768 x 2048 bfloat16 takes 107 us (6.3 TB/s, 92% of
-// a plain copy's bandwidth); with both checkpoints 65536 x 1024 takes 137 us (87%); 8191 x 515
+// Bound by memory: three rows in and two out. 32768 x 2048 bfloat16 takes 105 us (6.4 TB/s, 94% of
+// a plain copy's bandwidth); with both checkpoints 65536 x 1024 takes 136 us (88%); 8191 x 515
 // float32, single channels to an access, 26 us (47%: 6 channels to a thread do not hide its row's
 // sums). glr_join.cuh has the layout.
 #include "glr_join.cuh"

@@ -51,7 +51,7 @@ struct Ckpt {
 
 // The sums of K values over the threads of a block. buf holds two sets of kSums floats for each of
 // 32 warps, used in turn (`turn`), so that one barrier a call is enough.
-constexpr int kSums = 2;
+constexpr int kSums = 3;
 template <int K>
 __device__ __forceinline__ void row_sum(float (&s)[K], float* buf, int& turn) {
   static_assert(K <= kSums, "the sets do not meet");
@@ -234,28 +234,42 @@ __device__ __forceinline__ void stage_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// z -> z less its mean (layer) and 1 / its deviation. Channels past H hold 0 and are left at 0.
+template <int P>
+__device__ __forceinline__ float dot(const float2 (&a)[P], const float2 (&b)[P]) {
+  float2 t = two(0.0f);
+#pragma unroll
+  for (int p = 0; p < P; ++p) t = fma2(a[p], b[p], t);
+  return sum2(t);
+}
+template <int P>
+__device__ __forceinline__ float total(const float2 (&a)[P]) {
+  float2 t = two(0.0f);
+#pragma unroll
+  for (int p = 0; p < P; ++p) t = add2(t, a[p]);
+  return sum2(t);
+}
+// z -> z less its mean. Channels past H hold 0 and are left at 0.
+template <int VEC, int NV>
+__device__ __forceinline__ void less_mean(const Items<VEC, NV>& it, float2 (&z)[VEC * NV / 2],
+                                          float inv_h, float* buf, int& turn) {
+  constexpr int P = VEC * NV / 2;
+  float m[1] = {total(z)};
+  row_sum<1>(m, buf, turn);
+#pragma unroll
+  for (int p = 0; p < P; ++p) z[p] = add2(z[p], two(-m[0] * inv_h));
+  it.clear(z);
+}
+__device__ __forceinline__ float inverse_deviation(float squares, float inv_h, float eps) {
+  return 1.0f / sqrtf(squares * inv_h + eps);
+}
+// z -> z less its mean (layer) and 1 / its deviation
 template <int VEC, int NV>
 __device__ __forceinline__ float centre(const Items<VEC, NV>& it, float2 (&z)[VEC * NV / 2],
                                         bool layer, float inv_h, float eps, float* buf, int& turn) {
-  constexpr int P = VEC * NV / 2;
-  if (layer) {
-    float2 t = two(0.0f);
-#pragma unroll
-    for (int p = 0; p < P; ++p) t = add2(t, z[p]);
-    float m[1] = {sum2(t)};
-    row_sum<1>(m, buf, turn);
-    const float mean = m[0] * inv_h;
-#pragma unroll
-    for (int p = 0; p < P; ++p) z[p] = add2(z[p], two(-mean));
-    it.clear(z);
-  }
-  float2 t = two(0.0f);
-#pragma unroll
-  for (int p = 0; p < P; ++p) t = fma2(z[p], z[p], t);
-  float q[1] = {sum2(t)};
+  if (layer) less_mean<VEC, NV>(it, z, inv_h, buf, turn);
+  float q[1] = {dot(z, z)};
   row_sum<1>(q, buf, turn);
-  return 1.0f / sqrtf(q[0] * inv_h + eps);
+  return inverse_deviation(q[0], inv_h, eps);
 }
 
 // act(g) = g s or s, s = sigmoid(g); g sigmoid(g) is 0 at -inf (where g is taken as a finite

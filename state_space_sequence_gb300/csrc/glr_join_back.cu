@@ -3,12 +3,12 @@
 // each block's registers to the end, go to the workspace once a block, and are added up in a fixed
 // order.
 //
-// Five rows in and three out. 32768 x 2048 bfloat16 takes 229 us with the sums (4.7 TB/s, 69% of a
-// plain copy's bandwidth): 74 instructions an element fill 57% of the issue slots, and with 16
+// Five rows in and three out. 32768 x 2048 bfloat16 takes 215 us with the sums (5.0 TB/s, 73% of a
+// plain copy's bandwidth): 71 instructions an element fill 58% of the issue slots, and with 16
 // warps on an SM the rest goes on waiting between a row's sums; more warps with fewer registers
 // spill (96 of them: 286 us; 8 channels to a thread: 385 us). From 8-bit checkpoints 65536 x 1024
-// takes 243 us (57%), bound the same way with a quarter fewer bytes. 8191 x 515 float32 takes 66 us
-// (30%). glr_join.cuh has the layout.
+// takes 234 us (59%), bound the same way with a quarter fewer bytes. 8191 x 515 float32 takes 63 us
+// (32%). glr_join.cuh has the layout.
 #include "glr_join.cuh"
 
 namespace dlr {
@@ -17,23 +17,6 @@ namespace dlr {
 
 namespace glr {
 namespace {
-
-// s[0] over the row and, for a layer norm, s[1] the sum of q
-template <int P>
-__device__ __forceinline__ void both_sums(bool layer, const float2 (&q)[P], float (&s)[2],
-                                          float* buf, int& turn) {
-  if (layer) {
-    float2 t = two(0.0f);
-#pragma unroll
-    for (int p = 0; p < P; ++p) t = add2(t, q[p]);
-    s[1] = sum2(t);
-    row_sum<2>(s, buf, turn);
-  } else {
-    float one[1] = {s[0]};
-    row_sum<1>(one, buf, turn);
-    s[0] = one[0];
-  }
-}
 
 // part: [parts, 2, H] sums of D uhat and of dn yhat, then [parts] sums of w D uhat
 template <typename T, int VEC, int NV, bool kKept, bool kDirect, int kThreads, int kResident>
@@ -122,21 +105,32 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
     }
     float2 d[P];
     if (dn.p) {
-      const float ry = centre<VEC, NV>(it, z, layer, inv_h, a.eps, buf, turn);
-      float2 q[P], v[P], s0 = two(0.0f);
-      St::get(at(k, 2), it, dn, row, q);
-      it.params(a.v, v);
+      // the squares and the products with q = v dn go around together; yhat = ry z
+      float2 q[P], v[P];
+      if (layer) less_mean<VEC, NV>(it, z, inv_h, buf, turn);
+      St::get(at(k, 2), it, dn, row, v);
+      it.params(a.v, q);
+#pragma unroll
+      for (int p = 0; p < P; ++p) q[p] = mul2(q[p], v[p]);
+      float sq = 0.0f, sz = dot(z, z), sqz = dot(q, z);
+      if (layer) {
+        float s[3] = {sz, sqz, total(q)};
+        row_sum<3>(s, buf, turn);
+        sz = s[0], sqz = s[1], sq = s[2];
+      } else {
+        float s[2] = {sz, sqz};
+        row_sum<2>(s, buf, turn);
+        sz = s[0], sqz = s[1];
+      }
+      const float ry = inverse_deviation(sz, inv_h, a.eps);
+      St::get(at(k, 2), it, dn, row, v);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        z[p] = mul2(z[p], two(ry));  // yhat
-        sv[p] = fma2(q[p], z[p], sv[p]);
-        q[p] = mul2(q[p], v[p]);
-        s0 = fma2(q[p], z[p], s0);
+        z[p] = mul2(z[p], two(ry));
+        sv[p] = fma2(v[p], z[p], sv[p]);
       }
-      float s[2] = {sum2(s0), 0.0f};
-      both_sums(layer, q, s, buf, turn);
       // what cancels does so before it is scaled
-      const float2 m = two(-s[0] * inv_h), mean = two(layer ? -s[1] * inv_h : 0.0f);
+      const float2 m = two(-ry * sqz * inv_h), mean = two(-sq * inv_h);
 #pragma unroll
       for (int p = 0; p < P; ++p) z[p] = mul2(fma2(z[p], m, add2(q[p], mean)), two(ry));
     }
@@ -154,20 +148,25 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
     if (!block) continue;
     it.params(a.w, w);
     if (layer) it.clear(d);
-    float2 s0 = two(0.0f);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       u[p] = mul2(u[p], two(ru));  // uhat
       sw[p] = fma2(d[p], u[p], sw[p]);
       d[p] = mul2(d[p], w[p]);
-      s0 = fma2(d[p], u[p], s0);
     }
-    float s[2] = {sum2(s0), 0.0f};
-    both_sums(layer, d, s, buf, turn);
+    float s[2] = {dot(d, u), 0.0f};
+    if (layer) {
+      s[1] = total(d);
+      row_sum<2>(s, buf, turn);
+    } else {
+      float one[1] = {s[0]};
+      row_sum<1>(one, buf, turn);
+      s[0] = one[0];
+    }
     if (threadIdx.x == 0) sa += (double)s[0];
     // alpha stands outside, so that dalpha's sum needs no division
     const float ar = alpha * ru;
-    const float2 m = two(-s[0] * inv_h), mean = two(layer ? -s[1] * inv_h : 0.0f);
+    const float2 m = two(-s[0] * inv_h), mean = two(-s[1] * inv_h);
 #pragma unroll
     for (int p = 0; p < P; ++p) d[p] = mul2(fma2(u[p], m, add2(d[p], mean)), two(ar));
     if (gated) {

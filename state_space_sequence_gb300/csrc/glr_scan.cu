@@ -453,9 +453,10 @@ __device__ __forceinline__ void chain_runs(const J& q, const Tile& at, int64_t r
   through_cut<VEC>(m, end);
 }
 
-// How many of S steps there are when `left` are left of the row. The empty statement pins the value: formed
-// in 32 bits and left to the compiler, it came out as S in the stores of a warp whose steps the row's
-// end cuts short (seen with float32 and rows of 4-byte alignment), which then wrote past the row.
+// How many of S steps there are when `left` are left of the row. The empty statement pins the
+// value: formed in 32 bits and left to the compiler, it came out as S in the stores of a warp whose
+// steps the row's end cuts short (seen with float32 and rows of 4-byte alignment), which then wrote
+// past the row.
 template <int S>
 __device__ __forceinline__ int steps_left(int64_t left) {
   int n = (int)max((int64_t)0, min((int64_t)S, left));
