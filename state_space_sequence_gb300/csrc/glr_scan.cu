@@ -784,6 +784,8 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
     const Tile at = sh.tile[k % kRing];
     const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
     const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
+    // stores to the rows themselves are held by a count formed beside their address
+    const int n = kBulk ? z.n : steps_left<S>(q.L - t0);
     bool on[VEC];
     float s[VEC];
 #pragma unroll
@@ -791,7 +793,7 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       on[v] = h + v < q.H && DLR_IN(at.b, q.B);
       s[v] = sh.enter[k & 1][warp][lane * VEC + v];
     }
-    if (states && z.n > 0) {
+    if (states && n > 0) {
       const int64_t runs = (q.L - 1) / S + 1;
       float* to = states + (at.b * runs + t0 / S) * q.H + h;
 #pragma unroll
@@ -806,7 +808,7 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
 #pragma unroll
       for (int v = 0; v < VEC; ++v) on[v] = true;
     }
-    if (z.cut == 0 && (kBulk || z.n == S)) {
+    if (z.cut == 0 && (kBulk || n == S)) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
         advance<VEC>(s, z.a, z.b, j);
@@ -819,10 +821,10 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           if ((z.cut >> j) & 1u) s[v] = half<VEC>(z.b, j, v);
-        if (j < z.n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp + j * st, s, on);
+        if (j < n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp + j * st, s, on);
       }
     }
-    if (kBulk && z.n > 0) {
+    if (kBulk && n > 0) {
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -1100,6 +1102,8 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
     const Tile at = sh.tile[k % kRing];
     const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
+    // stores to the rows themselves are held by a count formed beside their address
+    const int n = kBulk ? z.n : steps_left<S>(q.L - t0);
     bool on[VEC];
     float G[VEC], sum[VEC];
 #pragma unroll
@@ -1187,7 +1191,7 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
           put<T, VEC, kOne>(x + (j + d) * C, px, on);
           put<T, VEC, kOne>(r + (j + d) * C, pr, on);
           put<T, VEC, kOne>(i + (j + d) * C, pi, on);
-        } else if (j + d < z.n && DLR_IN(t0 + j + d, q.L)) {
+        } else if (j + d < n && DLR_IN(t0 + j + d, q.L)) {
           put<T, VEC, kOne>(dx.row(at.b, t0 + j + d) + h, px, on);
           put<T, VEC, kOne>(dr.row(at.b, t0 + j + d) + h, pr, on);
           put<T, VEC, kOne>(di.row(at.b, t0 + j + d) + h, pi, on);
