@@ -18,7 +18,10 @@ namespace dlr {
 namespace glr {
 namespace {
 
-// part: [parts, 2, H] sums of D uhat and of dn yhat, then [parts] sums of w D uhat
+// part: [parts, 2, H] sums of D uhat and of dn yhat, then [parts] sums of w D uhat in 64 bits.
+// dalpha is one sum over all rows and channels, of terms of either sign, and may come out far below
+// the root of their squares' sum: a thread adds up its channels of a row in 32 bits, everything
+// beyond them in 64.
 template <typename T, int VEC, int NV, bool kKept, bool kDirect, int kThreads, int kResident>
 __global__ void __launch_bounds__(kThreads, kResident / kThreads)
 join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<const T> h,
@@ -28,6 +31,7 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
   using Sc = Staged<uint8_t, VEC, NV, kDirect>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[64 * kSums];
+  __shared__ double own[32];
   const Items<VEC, NV> it{a.H, (int)blockDim.x};
   const int per = St::items();
   const bool layer = a.norm == GLR_NORM_LAYER, block = a.w != nullptr;
@@ -65,7 +69,7 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
     stage_end();
   };
   float2 sw[P] = {}, sv[P] = {};
-  double sa = 0.0;  // one term a row, of either sign: its sum may cancel
+  double sa = 0.0;  // of this thread's channels
   int turn = 0;
   fetch(row, 0);
   for (int k = 0; row < a.M; row += gridDim.x, k ^= 1) {
@@ -155,6 +159,7 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
       d[p] = mul2(d[p], w[p]);
     }
     float s[2] = {dot(d, u), 0.0f};
+    sa += (double)s[0];
     if (layer) {
       s[1] = total(d);
       row_sum<2>(s, buf, turn);
@@ -163,7 +168,6 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
       row_sum<1>(one, buf, turn);
       s[0] = one[0];
     }
-    if (threadIdx.x == 0) sa += (double)s[0];
     // alpha stands outside, so that dalpha's sum needs no division
     const float ar = alpha * ru;
     const float2 m = two(-s[0] * inv_h), mean = two(-s[1] * inv_h);
@@ -209,7 +213,14 @@ join_back(JoinArgs a, Rows<const T> dy, Rows<const T> dn, Rows<const T> x, Rows<
     store<float, VEC == 8 ? 4 : VEC>(part + (me * 2 + 1) * a.H + it.channel(j), t);
     if constexpr (VEC == 8) store<float, 4>(part + (me * 2 + 1) * a.H + it.channel(j) + 4, t + 4);
   }
-  if (threadIdx.x == 0) part[parts * 2 * a.H + me] = (float)sa;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sa += __shfl_xor_sync(0xffffffffu, sa, o);
+  if ((threadIdx.x & 31) == 0) own[threadIdx.x >> 5] = sa;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int j = 1; j < (int)blockDim.x >> 5; ++j) sa += own[j];
+    reinterpret_cast<double*>(part + parts * 2 * a.H)[me] = sa;
+  }
 }
 
 // dw, dv and dalpha from the partial sums, in a fixed order: 32 channels of one of the two sums to
@@ -223,7 +234,8 @@ join_sums(const float* __restrict__ part, int parts, int H, const float* __restr
   if ((int)blockIdx.x == 2 * per) {
     if (!dalpha || row) return;
     double s = 0.0;
-    for (int k = lane; k < parts; k += 32) s += (double)part[(int64_t)parts * 2 * H + k];
+    const double* each = reinterpret_cast<const double*>(part + (int64_t)parts * 2 * H);
+    for (int k = lane; k < parts; k += 32) s += each[k];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) *dalpha = (float)s;
@@ -305,7 +317,7 @@ cudaError_t back_k(const glr_join_backward_args& a, cudaStream_t s) {
 
 size_t join_backward_workspace_bytes(int64_t H) {
   // the fewest threads that any layout above gives a row make the most parts
-  return sizeof(float) * (size_t)most_parts(row_threads(H, 16)) * (2 * (size_t)H + 1);
+  return sizeof(float) * (size_t)most_parts(row_threads(H, 16)) * (2 * (size_t)H + 2);
 }
 
 cudaError_t launch_join_backward(const glr_join_backward_args& a, cudaStream_t s) {
