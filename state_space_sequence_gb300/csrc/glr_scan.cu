@@ -453,15 +453,18 @@ __device__ __forceinline__ void chain_runs(const J& q, const Tile& at, int64_t r
   through_cut<VEC>(m, end);
 }
 
-// How many of S steps there are when `left` are left of the row. The empty statement pins the
-// value: formed in 32 bits and left to the compiler, it came out as S in the stores of a warp whose
-// steps the row's end cuts short (seen with float32 and rows of 4-byte alignment), which then wrote
-// past the row.
-template <int S>
-__device__ __forceinline__ int steps_left(int64_t left) {
-  int n = (int)max((int64_t)0, min((int64_t)S, left));
-  asm volatile("" : "+r"(n));
-  return n;
+// How many steps each of a tile's W warps has: S, or what the row's end leaves of them. The
+// supplying warp writes the counts beside the tile's place and the computing warps read them there.
+// A warp's padding, its maps, its sums and its stores all go by that one number, which a compiler
+// cannot form again from the tile's place at one of them. In a draft each warp formed its own in
+// 32-bit arithmetic; its padding went by the right count and its stores by S, past the row's end.
+// Reading the source did not show why.
+template <int W, int S, typename J>
+__device__ __forceinline__ void write_steps(const J& q, const Tile& at, int (&steps)[W]) {
+  const int lane = threadIdx.x & 31;
+  if (lane >= W) return;
+  const int64_t left = q.L - ((int64_t)at.tile * W + lane) * S;
+  steps[lane] = at.tile < 0 ? 0 : (int)max((int64_t)0, min((int64_t)S, left));
 }
 
 // bits of the n steps from t on that begin a sequence
@@ -599,6 +602,7 @@ struct ScanShared {
   float map[3][kScanWarps][2][C];   // A and e of each warp's steps
   float enter[2][kScanWarps][C];    // the state that enters them
   float kz[kRing][C];
+  int steps[kRing][kScanWarps];     // that there are of each warp's
   uint32_t cut[3][kScanWarps];
   Tile tile[kRing];
   uint64_t here[2];                 // barriers of the buffers' copies
@@ -628,8 +632,9 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       if (lane == 0) sh.tile[k % kRing] = at;
       __syncwarp();
     };
-    auto params = [&](int k) {  // and its decay parameters
+    auto params = [&](int k) {  // its steps and decay parameters
       const Tile at = sh.tile[k % kRing];
+      write_steps<W, S>(q, at, sh.steps[k % kRing]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
@@ -718,18 +723,19 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
     }
   };
   struct Part {  // what a warp has of a tile: its steps, how many there are, which begin a sequence
-    float2 a[NP], b[NP];
-    int n;
-    uint32_t cut;
+    float2 a[NP] = {}, b[NP] = {};
+    int n = 0;
+    uint32_t cut = 0;
   };
   auto gates = [&](int k, Part& z) {
     const Tile at = sh.tile[k % kRing];
+    z.n = sh.steps[k % kRing][warp];
+    z.cut = 0;
     if (at.tile < 0) {
       bar_arrive(kMapsBar + (k & 1), kWork + 32);
       return;
     }
     const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
-    z.n = steps_left<S>(q.L - t0);
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
     const float* own = &sh.kz[k % kRing][lane * VEC];
     const float2 kz = make_float2(own[0], own[VEC - 1]);
@@ -784,8 +790,6 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
     const Tile at = sh.tile[k % kRing];
     const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
     const int64_t t0 = (int64_t)at.tile * kScanTile + warp * S;
-    // stores to the rows themselves are held by a count formed beside their address
-    const int n = kBulk ? z.n : steps_left<S>(q.L - t0);
     bool on[VEC];
     float s[VEC];
 #pragma unroll
@@ -793,7 +797,7 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
       on[v] = h + v < q.H && DLR_IN(at.b, q.B);
       s[v] = sh.enter[k & 1][warp][lane * VEC + v];
     }
-    if (states && n > 0) {
+    if (states && z.n > 0) {
       const int64_t runs = (q.L - 1) / S + 1;
       float* to = states + (at.b * runs + t0 / S) * q.H + h;
 #pragma unroll
@@ -808,7 +812,7 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
 #pragma unroll
       for (int v = 0; v < VEC; ++v) on[v] = true;
     }
-    if (z.cut == 0 && (kBulk || n == S)) {
+    if (z.cut == 0 && (kBulk || z.n == S)) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
         advance<VEC>(s, z.a, z.b, j);
@@ -821,10 +825,10 @@ scan_kernel(Job<T> q, const __grid_constant__ Maps<3> in, const __grid_constant_
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
           if ((z.cut >> j) & 1u) s[v] = half<VEC>(z.b, j, v);
-        if (j < n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp + j * st, s, on);
+        if (j < z.n && DLR_IN(t0 + j, q.L)) put<T, VEC, kOne>(yp + j * st, s, on);
       }
     }
-    if (kBulk && n > 0) {
+    if (kBulk && z.n > 0) {
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -879,6 +883,7 @@ struct BackShared {
   float enter[2][kBackWarps][C];    // the gradient that enters behind them
   float sum[2][kBackWarps][C];      // their parts of dp
   float k[kRing][C];                // c softplus(p)
+  int steps[kRing][kBackWarps];     // that there are of each warp's
   uint32_t cut[3][kBackWarps];
   Tile tile[kRing];
   uint64_t rd_here[4], ix_here[2];  // barriers of the buffers' copies
@@ -908,8 +913,9 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       if (lane == 0) sh.tile[k % kRing] = at;
       __syncwarp();
     };
-    auto params = [&](int k) {  // and its decay parameters
+    auto params = [&](int k) {  // its steps and decay parameters
       const Tile at = sh.tile[k % kRing];
+      write_steps<W, S>(q, at, sh.steps[k % kRing]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const int64_t h = ((int64_t)at.group * 32 + lane) * VEC + v;
@@ -1019,18 +1025,19 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
       report_status(q.status, DLR_ERR_TIMEOUT);
   };
   struct Part {  // what a warp has of a tile: its decays, its steps, which begin a sequence
-    float2 ka[NP];
-    int n;
-    uint32_t cut;
+    float2 ka[NP] = {};
+    int n = 0;
+    uint32_t cut = 0;
   };
   auto decays = [&](int k, Part& z) {
     const Tile at = sh.tile[k % kRing];
+    z.n = sh.steps[k % kRing][warp];
+    z.cut = 0;
     if (at.tile < 0) {
       bar_arrive(kMapsBar + (k & 1), kWork + 32);
       return;
     }
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
-    z.n = steps_left<S>(q.L - t0);
     z.cut = cuts(q.reset, at.b * q.L + t0, z.n);
     const float* own = &sh.k[k % kRing][lane * VEC];
     const float2 kz = mul2(make_float2(own[0], own[VEC - 1]), two(-kLog2e));
@@ -1087,14 +1094,14 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
     bar_arrive(kMapsBar + (k & 1), kWork + 32);
   };
   // the state that enters the warp's steps of a tile
-  auto kept = [&](int k, float (&s)[VEC]) {
+  auto kept = [&](int k, const Part& z, float (&s)[VEC]) {
     const Tile at = sh.tile[k % kRing];
     const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       const int64_t runs = (q.L - 1) / S + 1, from = (at.b * runs + t0 / S) * q.H + h + v;
-      s[v] = t0 < q.L && h + v < q.H && DLR_IN(from, q.B * runs * q.H) ? states[from] : 0.0f;
+      s[v] = z.n > 0 && h + v < q.H && DLR_IN(from, q.B * runs * q.H) ? states[from] : 0.0f;
     }
   };
   // plain (a constant in each call): all S steps are there and none begins a sequence
@@ -1102,8 +1109,6 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
     const Tile at = sh.tile[k % kRing];
     const int64_t h = ((int64_t)at.group * 32 + lane) * VEC;
     const int64_t t0 = (int64_t)at.tile * kBackTile + warp * S;
-    // stores to the rows themselves are held by a count formed beside their address
-    const int n = kBulk ? z.n : steps_left<S>(q.L - t0);
     bool on[VEC];
     float G[VEC], sum[VEC];
 #pragma unroll
@@ -1191,7 +1196,7 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
           put<T, VEC, kOne>(x + (j + d) * C, px, on);
           put<T, VEC, kOne>(r + (j + d) * C, pr, on);
           put<T, VEC, kOne>(i + (j + d) * C, pi, on);
-        } else if (j + d < n && DLR_IN(t0 + j + d, q.L)) {
+        } else if (j + d < z.n && DLR_IN(t0 + j + d, q.L)) {
           put<T, VEC, kOne>(dx.row(at.b, t0 + j + d) + h, px, on);
           put<T, VEC, kOne>(dr.row(at.b, t0 + j + d) + h, pr, on);
           put<T, VEC, kOne>(di.row(at.b, t0 + j + d) + h, pi, on);
@@ -1214,7 +1219,7 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
   // tile k's decays are in `now`; true when it was the last
   auto turn = [&](int k, Part& now, Part& next) {
     float s[VEC];
-    kept(k, s);
+    kept(k, now, s);
     decays(k + 1, next);
     if (kBulk) {
       if (lane == 0) tc::bulk_wait_group_read0();  // the outputs of tile k - 1 have left
