@@ -204,7 +204,7 @@ dlr_status glr_join_backward(const glr_join_backward_args* args, dlr_stream_t st
  * e4m3 (4 exponent and 3 mantissa bits), rounded to nearest even. The maximum runs over the
  * finite values; an infinity or a NaN becomes a NaN code and disturbs no other value. Unpacking
  * gives code * 2^s, rounded to `type` (exact in float32 and bfloat16 for normal values). M >= 0,
- * H >= 1.
+ * 1 <= H <= 2^31 - 32, and M * ceil(H / GLR_CKPT_GROUP) <= 2^34 - 8.
  */
 #define GLR_CKPT_GROUP 32
 dlr_status glr_ckpt_pack(int64_t type, int64_t M, int64_t H, const void* t, int64_t stride_t,

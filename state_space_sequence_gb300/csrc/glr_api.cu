@@ -32,7 +32,6 @@ constexpr int64_t kMaxGrid = 2147483647;
 constexpr int64_t kMaxH = int64_t(1) << 24;   // channels of the recurrence
 constexpr int64_t kMaxRowH = 16384;           // channels of a joined row (held in registers)
 constexpr int64_t kMaxStride = int64_t(1) << 40;
-constexpr int64_t kMaxRows = int64_t(1) << 40;
 
 bool bad_type(int64_t t) { return t != GLR_F32 && t != GLR_BF16 && t != GLR_F16; }
 int64_t type_bytes(int64_t t) { return t == GLR_F32 ? 4 : 2; }
@@ -323,8 +322,11 @@ dlr_status glr_join_backward(const glr_join_backward_args* args, dlr_stream_t st
 static dlr_status ckpt_args(int64_t type, int64_t M, int64_t H, const void* t, int64_t st,
                             const uint8_t* codes, const uint8_t* scales) {
   if (bad_type(type) || M < 0 || H < 1) return DLR_ERR_INVALID_ARG;
-  if (H > kMaxGrid || M > kMaxRows || (M > 0 && H > (int64_t(1) << 38) / M))
-    return DLR_ERR_UNSUPPORTED;  // a thread for each channel at most
+  // A thread for each channel at most, rows in whole groups and groups in blocks of 256 threads: as
+  // many blocks as a launch may have, and channels that a kernel counts in 32 bits.
+  if (H > kMaxGrid - GLR_CKPT_GROUP + 1) return DLR_ERR_UNSUPPORTED;
+  const int64_t groups = (H + GLR_CKPT_GROUP - 1) / GLR_CKPT_GROUP;
+  if (M > kMaxGrid * (256 / GLR_CKPT_GROUP) / groups) return DLR_ERR_UNSUPPORTED;
   if (M == 0) return DLR_OK;
   if (!t || !codes || !scales || !aligned(t, type_bytes(type)) || bad_strides(0, st))
     return DLR_ERR_INVALID_ARG;
