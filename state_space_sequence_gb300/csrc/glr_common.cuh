@@ -191,18 +191,19 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays a N
 }
 
 // Two elements' decays and inputs: a, and b = sqrt(1 - a^2) sigmoid(i) x. kz = -c softplus(p)
-// log2(e). With u = 1 - a^2 and d = 1 + e^-i, b = x u / sqrt(u d^2), which takes one special
-// function less than sqrt(u) and 1 / d by themselves. e^-i is held at 2^60, so that d^2 stays
-// finite.
+// log2(e). With u = 1 - a^2 and E = e^i, b = x E u / sqrt(u (1 + E)^2), which takes one special
+// function less than sqrt(u) and 1 / (1 + E) by themselves. E is held at 2^40, where the gate is 1
+// to float precision, so that the square stays finite; a gate that shuts keeps its value while
+// sqrt(u) E is a normal float, and is 0 at i = -inf.
 __device__ __forceinline__ void gates2(float2 r, float2 i, float2 x, float2 kz, float2& a,
                                        float2& b) {
   float2 rest;
   decay2(mul2(kz, sigmoid2(r)), rest, a);
   const float2 u = mul2(rest, add2(a, two(1.0f)));
-  const float2 t = mul2(i, two(-kLog2e));
-  const float2 e = make_float2(min_nan(ex2(t.x), 0x1p60f), min_nan(ex2(t.y), 0x1p60f));
+  const float2 t = mul2(i, two(kLog2e));
+  const float2 e = make_float2(min_nan(ex2(t.x), 0x1p40f), min_nan(ex2(t.y), 0x1p40f));
   const float2 d = add2(e, two(1.0f));
-  b = mul2(mul2(u, rsqrt2(mul2(mul2(u, d), d))), x);
+  b = mul2(mul2(mul2(u, rsqrt2(mul2(mul2(u, d), d))), e), x);
 }
 
 }  // namespace glr
