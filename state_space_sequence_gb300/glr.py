@@ -10,8 +10,9 @@
 Like ``dlr.py`` this module passes pointers, sizes and the current torch CUDA stream, and turns
 non-zero status codes into exceptions; there is no CPU fallback. Activations are float32,
 bfloat16 or float16 with contiguous channels and otherwise any strides (so ``x``, ``r`` and ``i``
-may be columns of one projection's output); parameters and states are contiguous float32. Memory
-allocated here for a call on ``stream`` belongs to that stream.
+may be columns of one projection's output); parameters and states are contiguous float32. All are
+on the current device. Memory allocated here for a call on ``stream`` belongs to that stream.
+Gradients are calls of their own: nothing here is recorded for autograd.
 """
 from __future__ import annotations
 
@@ -68,10 +69,21 @@ def _ok(fn: str, status: int):
         raise _dlr.DLRError(fn, status)
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _stream(stream, dev: int):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(dev)
+    """The stream of a call whose tensors are on device ``dev``. The library launches on the current
+    device, so that has to be the tensors' and the stream's: another device's pointers, or its
+    stream's handle, would mean nothing there."""
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, but the current device is "
+                         f"cuda:{_current_device()}: call within torch.cuda.device({dev})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _on(stream):
