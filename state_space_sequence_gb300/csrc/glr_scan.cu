@@ -400,7 +400,8 @@ __device__ __forceinline__ void chain_runs(const J& q, const Tile& at, int64_t r
       }
       if (far == 0) look(in, s);
       const uint32_t ins = __ballot_sync(0xffffffffu, k < run && !empty(has_in[0]));
-      const uint32_t there = __ballot_sync(0xffffffffu, k < run && !empty(has_map[0]));
+      // what leaves the first run is waited for, not its map, so that the look stops there
+      const uint32_t there = __ballot_sync(0xffffffffu, k < run - 1 && !empty(has_map[0]));
       const int l = ins ? __ffs(ins) - 1 : 32;
       const uint32_t before = l == 32 ? 0xffffffffu : (1u << l) - 1u;
       if ((there & before) != before) {
