@@ -59,7 +59,10 @@ typedef struct {
  *   h_t = abar_t h_{t-1} + b_t,   abar_t = 0 where reset[b, t] != 0, else a_t
  * per channel, h_{-1} = h0 (float32 [B, H]; NULL: zero). y = h; h_last (float32 [B, H], may be
  * NULL) = h_{L-1}. reset: bytes [B, L], contiguous, NULL for none; a step that it marks begins a
- * new sequence: nothing before it, not even an infinity or a NaN, reaches it.
+ * new sequence: nothing before it, not even an infinity or a NaN, reaches it. Its input keeps the
+ * factor sqrt(1 - a_t^2), as that of a sequence begun from a zero state (a model that was trained
+ * with a factor of 1 at its documents' first steps gives other values there). A step whose i is
+ * -inf adds nothing, whatever finite x it has.
  * states (NULL: not kept): float32 [B, glr_states(L), H], the state before each run of
  * GLR_STATE_STEPS steps, for glr_scan_backward.
  * workspace: glr_scan_workspace_size(B, L, H) bytes, 16-byte aligned (0 for short rows: none).

@@ -1,14 +1,16 @@
 // glr_join_back.cu -- the gradients of glr_join (include/glr.h). A row's statistics are computed
 // again from x, h and g, which are read anyway; the sums over the rows (dw, dv, dalpha) stay in
 // each block's registers to the end, go to the workspace once a block, and are added up in a fixed
-// order.
+// order (dalpha in 64 bits, at no cost in time).
 //
 // Five rows in and three out. 32768 x 2048 bfloat16 takes 215 us with the sums (5.0 TB/s, 73% of a
 // plain copy's bandwidth): 71 instructions an element fill 58% of the issue slots, and with 16
 // warps on an SM the rest goes on waiting between a row's sums; more warps with fewer registers
 // spill (96 of them: 286 us; 8 channels to a thread: 385 us). From 8-bit checkpoints 65536 x 1024
-// takes 234 us (59%), bound the same way with a quarter fewer bytes. 8191 x 515 float32 takes 63 us
-// (32%). glr_join.cuh has the layout.
+// takes 233 us (60%), bound the same way with a quarter fewer bytes. 8191 x 515 float32 takes 64 us
+// (31%). Rows of single channels from 769 on and all rows above 8192 channels spill (100 to 1640
+// bytes a thread): 33520 x 1001 float32 884 us (18%), bfloat16 977 us (8%), 2730 x 12288 bfloat16
+// 272 us (29%). glr_join.cuh has the layout.
 #include "glr_join.cuh"
 
 namespace dlr {

@@ -6,8 +6,9 @@
 // run backwards in time with G_t = dy_t + abar_{t+1} G_{t+1}: a stretch maps the gradient that
 // enters behind it to the one that leaves before it by G -> A G + C with the same A.
 //
-// Each direction is one launch that reads every input once from memory. Blocks stay on the GPU and
-// take tiles (some steps of a group of channels) in turn; while a block works on one tile, the next
+// Each direction is one kernel that reads every input once from memory; before it goes a clearing
+// of the chains' workspace, where a row is more than one tile, and after the gradients' a small
+// kernel that adds up the parts of dp. Blocks stay on the GPU and take tiles (some steps of a group of channels) in turn; while a block works on one tile, the next
 // one's inputs come into shared memory by asynchronous copies. Each warp takes S of a tile's steps,
 // its gates in registers; the warps' maps meet in shared memory, the tiles of a row in a chain
 // through global memory: a tile publishes its map, looks back over the maps of the tiles before it
@@ -16,15 +17,15 @@
 // which of them a tile found. A tile that begins a sequence knows its end from its own steps.
 //
 // What bounds it: four arrays go through memory forwards and seven backwards, but in 16 bits the 4
-// and 7 special functions and some 40 and 73 instructions an element weigh as much. B4 L16384 H2048
-// bfloat16 takes 227 us forwards (4.7 TB/s, 70% of a plain copy's bandwidth) and 415 us backwards
-// (4.5 TB/s), and 3 and 1 us less with the chain left out; at L2048 the counters show half of the
-// issue slots used, the special-function pipe at 30 to 36%, and the rest of the time waits between
-// a tile's two phases, which all warps of the one block on an SM go through together. Two smaller
+// and 7 special functions and some 41 and 72 instructions an element weigh as much. B4 L16384 H2048
+// bfloat16 takes 231 us forwards (4.6 TB/s, 69% of a plain copy's bandwidth) and 412 us backwards
+// (4.6 TB/s), and 3 and 1 us less with the chain left out; at L2048 the counters show half of the
+// issue slots used, the special-function pipe at 21%, and the rest of the time waits between a
+// tile's two phases, which all warps of the one block on an SM go through together. Two smaller
 // blocks on an SM (6 computing warps each: 297 and 612 us), 12 warps (248 and 415 us) or one
 // reciprocal for both gates (241 and 425 us) were slower than the 233 and 415 us of their time. In
 // float32 memory bounds it: B1 L4096 H4096 52 and 81 us (75% and 85%). Where a row of tiles is long
-// and there are few, a tile's turn on its chain does: B1 L65536 H256 float32 88 us (45%; 46 us with
+// and there are few, a tile's turn on its chain does: B1 L65536 H256 float32 92 us (43%; 46 us with
 // the chain left out).
 #include <algorithm>
 
@@ -1258,7 +1259,9 @@ back_kernel(Job<T> q, const __grid_constant__ Maps<4> in, const __grid_constant_
 }
 
 // dp = -c sigmoid(p) times the sum of a channel's parts, in a fixed order: a warp for each 32
-// channels and 8 rows of warps that share the parts
+// channels and 8 rows of warps that share the parts. Bound by latency: a warp adds its parts one
+// after another, and few channels make few blocks. B8 L4096 H256 (296 parts, 8 blocks): 11 us by
+// itself with cold caches, beside back_kernel's 39.
 __global__ void __launch_bounds__(256)
 back_sum(const float* __restrict__ part, int64_t n, int64_t H, const float* __restrict__ p, float c,
          float* __restrict__ dp) {
