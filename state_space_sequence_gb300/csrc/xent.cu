@@ -1,0 +1,655 @@
+// xent.cu -- the softmax cross entropy of include/xent.h: a projection onto the vocabulary whose
+// logits live in tensor memory, and its gradients.
+//
+// Four products on the 5th-generation tensor cores, one kernel (xgemm) with four ends:
+//   the loss        z = h W^T, a tile's rows reduced to their maximum and sum of exponentials;
+//   the gradients   z again for a piece of the vocabulary, d = (softmax - onehot) dloss rounded to
+//                   the inputs' type and stored; then dh += d W and dW = d^T h over that piece.
+// The gradients form the logits a second time, a third of their work, for never holding more of d
+// than a piece (at most 256 MB). W and h are read as they lie: the operands of the last two products
+// have their rows along the sum, which the tensor core takes as they are (MN-major).
+//
+// float32 goes through the same kernel: x = x0 + x1 + x2 with bfloat16 parts, exact to 2^-24, and
+// the six products of parts whose orders of magnitude add up to no less than 2^-16, the small ones
+// first. Products of parts are exact and accumulated in float32, as those of 16-bit inputs.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "dlr_common.cuh"
+#include "glr_common.cuh"
+#include "tc_ptx.cuh"
+#include "xent.h"
+
+namespace dlr {
+// source file number of the bounds-checked build's failing sites
+[[maybe_unused]] constexpr int kSiteFile = 26;
+
+int* device_status_word();
+
+namespace xent {
+namespace {
+
+using glr::ex2;
+using glr::from_f;
+using glr::kLog2e;
+using glr::to_f;
+
+constexpr int kBM = 128, kBN = 256, kBK = 64;  // a tile, and the sum's extent of a stage
+constexpr uint32_t kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
+constexpr uint32_t kStage = kABytes + kBBytes;
+constexpr int kStages = 4;
+constexpr uint32_t kBox = 32 * 128;                // a warp's staging: 32 rows x 128 bytes
+constexpr uint32_t kBoxes = 2;
+constexpr uint32_t kEpiOff = kStages * kStage;
+constexpr uint32_t kBarOff = kEpiOff + 4 * kBoxes * kBox;
+constexpr size_t kSmem = 1024 + kBarOff + 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kThreads = 256;
+constexpr int kGroup = 16;  // rows of tiles that go through the columns together
+static_assert(kSmem <= 232448, "shared memory");
+
+enum Mode { kLoss, kGrad, kRows, kColumns };
+
+// The parts whose products are formed, the small ones first.
+__device__ __constant__ const int8_t kPartA[6] = {0, 2, 1, 0, 1, 0};
+__device__ __constant__ const int8_t kPartB[6] = {2, 0, 1, 1, 0, 0};
+
+struct gemm_args {
+  int M, N, K;
+  int products;        // 1, or 6 for float32
+  int b_row;           // where the piece begins among W's rows
+  int v0;              // first column's place in the vocabulary (kLoss, kGrad)
+  const int64_t* target;
+  int V;
+  const float* lse;    // kGrad
+  const float* dloss;
+  const float* scale;  // {2^k, 2^-k} of float16's d, or null
+  float2* stats;       // kLoss: [column of tiles, M] maximum and sum
+  float* hit;          // kLoss: [M] the target's logit
+  float* acc;          // kRows: float32 [M, N], the sum over the pieces so far
+  int has_acc, keep;   // read acc; write acc instead of out
+  void* out;
+  int64_t out_stride;
+  int* status;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, tc::mbar_wait_sleep(bar, parity)) != 0;
+}
+
+// Tile t in an order that keeps kGroup rows of tiles on one column's operand at a time.
+__device__ __forceinline__ void tile_at(int64_t t, int mt, int nt, int& mi, int& ni) {
+  const int64_t per = (int64_t)kGroup * nt;
+  const int g = (int)(t / per), first = g * kGroup, rows = min(kGroup, mt - first);
+  const int64_t r = t - g * per;
+  mi = first + (int)(r % rows);
+  ni = (int)(r / rows);
+}
+
+// bf16 parts of a float32: x = b[0] + b[1] + b[2] to 2^-24 of x.
+__device__ __forceinline__ void split3(float x, __nv_bfloat16 (&b)[3]) {
+  b[0] = __float2bfloat16_rn(x);
+  float r = x - __bfloat162float(b[0]);
+  if (!isfinite(r)) {  // x is not finite, or rounds to an infinity: its parts are cut off instead
+    b[0] = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x) >> 16));
+    if (x != x) b[0] = __float2bfloat16_rn(x);
+    r = isfinite(x) ? x - __bfloat162float(b[0]) : 0.0f;
+  }
+  b[1] = __float2bfloat16_rn(r);
+  b[2] = __float2bfloat16_rn(r - __bfloat162float(b[1]));
+}
+
+// T: the operands' type (bfloat16 also for float32's parts); O: the type of out, kGrad: float means
+// that d is stored in three parts. Warp 0 loads, warp 1 issues the products, warp 2 has the tensor
+// memory, warps 4-7 read the accumulators; two accumulators take turns.
+template <Mode MODE, typename T, typename O>
+__global__ void __launch_bounds__(kThreads, 1)
+xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+      const __grid_constant__ CUtensorMap tmC, const gemm_args g) {
+  constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kBarOff);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kStages;
+  uint64_t* acc_full = bars + 2 * kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mt = (g.M + kBM - 1) / kBM, nt = (g.N + kBN - 1) / kBN;
+  const int64_t tiles = (int64_t)mt * nt;
+  const int nk = (g.K + kBK - 1) / kBK, steps = nk * g.products;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(&acc_full[a], 1);
+      tc::mbar_init(&acc_empty[a], 4);
+    }
+    tc::mbar_fence_init();
+  }
+  if (warp == 2) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      int mi, ni;
+      tile_at(t, mt, nt, mi, ni);
+      const int m0 = mi * kBM, n0 = ni * kBN;
+      for (int k = 0; k < steps; ++k, ++it) {
+        const int s = it % kStages;
+        if (it >= kStages && !(ok = tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1))) break;
+        const int product = g.products == 1 ? 5 : k / nk, k0 = (k % nk) * kBK;
+        const int pa = kPartA[product], pb = kPartB[product];
+        uint8_t* a = base + s * kStage;
+        uint8_t* b = a + kABytes;
+        tc::mbar_arrive_expect_tx(&full[s], kStage);
+        if constexpr (kAmn) {
+#pragma unroll
+          for (int i = 0; i < kBM / 64; ++i)
+            tc::tma_load_3d(a + i * 8192, &tmA, m0 + 64 * i, k0, pa, &full[s]);
+        } else {
+          tc::tma_load_3d(a, &tmA, k0, m0, pa, &full[s]);
+        }
+        if constexpr (kBmn) {
+#pragma unroll
+          for (int i = 0; i < kBN / 64; ++i)
+            tc::tma_load_3d(b + i * 8192, &tmB, n0 + 64 * i, g.b_row + k0, pb, &full[s]);
+        } else {
+          tc::tma_load_3d(b, &tmB, k0, g.b_row + n0, pb, &full[s]);
+        }
+      }
+    }
+    // before the CTA may exit, every copy it issued has landed (normally long since consumed)
+    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+      ok &= tc::mbar_wait(&full[j % kStages], (j / kStages) & 1);
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc =
+        (sizeof(T) == 2 && glr::is_half<T> ? tc::idesc_f16_f32(kBM, kBN)
+                                           : tc::idesc_bf16_f32(kBM, kBN)) |
+        (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
+    uint32_t it = 0, local = 0;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++local) {
+      const uint32_t acc = local & 1;
+      if (local >= 2 && !(ok = tc::mbar_wait(&acc_empty[acc], ((local >> 1) - 1) & 1))) break;
+      tc::fence_after_sync();
+      const uint32_t d = tmem + acc * kBN;
+      for (int k = 0; k < steps; ++k, ++it) {
+        const int s = it % kStages;
+        if (!(ok = tc::mbar_wait(&full[s], (it / kStages) & 1))) break;
+        tc::fence_after_sync();
+        const uint8_t* a = base + s * kStage;
+        const uint8_t* b = a + kABytes;
+        const uint64_t ad = kAmn ? tc::smem_desc_mn_sw128(a, 8192, 1024) : tc::smem_desc_k_sw128(a);
+        const uint64_t bd = kBmn ? tc::smem_desc_mn_sw128(b, 8192, 1024) : tc::smem_desc_k_sw128(b);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)  // 16 of the sum: 32 bytes of a row, or 16 rows
+          tc::mma_kind_f16(d, ad + (kAmn ? 128 : 2) * kk, bd + (kBmn ? 128 : 2) * kk, idesc,
+                           (k | kk) != 0);
+        tc::mma_commit(&empty[s]);
+      }
+      tc::mma_commit(&acc_full[acc]);
+    }
+  } else if (warp >= 4) {
+    const int q = warp - 4;
+    uint8_t* boxes = base + kEpiOff + q * kBoxes * kBox;
+    uint32_t local = 0, boxed = 0;
+    float scale = 1.0f, unscale = 1.0f;
+    if (g.scale) scale = g.scale[0], unscale = g.scale[1];
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++local) {
+      int mi, ni;
+      tile_at(t, mt, nt, mi, ni);
+      const uint32_t acc = local & 1;
+      const int m0 = mi * kBM + q * 32, n0 = ni * kBN, row = m0 + lane;
+      const int cols = min(kBN, g.N - n0);
+      const uint32_t tcol = tmem + acc * kBN + (uint32_t(q * 32) << 16);
+      // what a row brings, fetched before the accumulator is waited for
+      int64_t target = -1;
+      float lse = 0.0f, weight = 0.0f;
+      if constexpr (MODE == kLoss || MODE == kGrad) {
+        if (row < g.M) {
+          target = g.target[row];
+          if constexpr (MODE == kGrad) {
+            lse = g.lse[row] * kLog2e;
+            weight = g.dloss[row] * scale;
+          }
+        }
+      }
+      const bool counts = target >= 0 && target < g.V;
+      const int64_t at = counts ? target - g.v0 - n0 : -1;  // its column within the tile
+      if (!(ok = warp_wait(&acc_full[acc], (local >> 1) & 1))) break;
+      tc::fence_after_sync();
+      if constexpr (MODE == kLoss) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int c = 0; c < kBN; c += 32) {
+          if (c >= cols) break;
+          float v[32];
+          tc::tmem_ld32(tcol + c, v);
+          if (cols - c < 32)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = i < cols - c ? v[i] : -INFINITY;
+          if (at >= c && at < c + 32)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (at == c + i) g.hit[row] = v[i];
+          float most = v[0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
+          const float next = fmaxf(top, most), from = next == -INFINITY ? 0.0f : next * kLog2e;
+          float part = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part += ex2(fmaf(v[i], kLog2e, -from));
+          sum = fmaf(sum, ex2(fmaf(top, kLog2e, -from)), part);
+          top = next;
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
+        if (row < g.M) g.stats[(int64_t)ni * g.M + row] = make_float2(top, sum);
+      } else if constexpr (MODE == kGrad) {
+        constexpr int kParts = sizeof(O) == 4 ? 3 : 1;
+        const uint32_t sw = uint32_t(lane & 7);
+        const int n_slices = (cols + 63) / 64;
+        for (int c = 0; c < n_slices; ++c) {
+          float v[64];
+          {
+            float lo[32], hi[32];
+            tc::tmem_ld32(tcol + c * 64, lo);
+            tc::tmem_ld32(tcol + c * 64 + 32, hi);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = lo[i], v[32 + i] = hi[i];
+          }
+          if (c == n_slices - 1) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
+          }
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const float p = ex2(fmaf(v[i], kLog2e, -lse)) - (at == c * 64 + i ? 1.0f : 0.0f);
+            v[i] = counts ? p * weight : 0.0f;
+          }
+#pragma unroll
+          for (int part = 0; part < kParts; ++part, ++boxed) {
+            uint8_t* box = boxes + (boxed % kBoxes) * kBox;
+            if (lane == 0) tc::bulk_wait_group_read<kBoxes - 1>();  // its last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float a = v[8 * k + 2 * i], b = v[8 * k + 2 * i + 1];
+                w[i] = glr::pack2<T>(make_float2(a, b));
+                if constexpr (kParts == 3) {  // what this part leaves
+                  const float2 f = glr::unpack2<T>(w[i]);
+                  v[8 * k + 2 * i] = a - f.x;
+                  v[8 * k + 2 * i + 1] = b - f.y;
+                }
+              }
+              *reinterpret_cast<uint4*>(box + lane * 128 + ((uint32_t(k) ^ sw) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (m0 < g.M) tc::tma_store_3d(&tmC, box, n0 + c * 64, m0, part);
+              tc::bulk_commit_group();
+            }
+          }
+        }
+      } else {
+        // float32 sums to rows of out, through shared memory so that a row's 32 go together
+        float* box = reinterpret_cast<float*>(boxes);
+        for (int c = 0; c < cols; c += 32) {
+          float v[32];
+          tc::tmem_ld32(tcol + c, v);
+          if (c + 32 >= cols) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) box[lane * 33 + i] = v[i];
+          __syncwarp();
+          const int col = n0 + c + lane;
+          if (col < g.N) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+              if (m0 + r >= g.M) break;
+              const int64_t m = m0 + r;
+              float o = box[r * 33 + lane];
+              if (g.has_acc) o += g.acc[m * g.N + col];
+              if (g.keep)
+                g.acc[m * g.N + col] = o;
+              else
+                static_cast<O*>(g.out)[m * g.out_stride + col] = from_f<O>(o * unscale);
+            }
+          }
+        }
+      }
+    }
+    if (MODE == kGrad && lane == 0) tc::bulk_wait_group0();
+  }
+  if (!ok) report_status(g.status, DLR_ERR_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// lse and loss of 32 rows to a block from the tiles' maxima and sums; 8 warps share the tiles of a
+// row and meet in order.
+__global__ void __launch_bounds__(256)
+finish_loss(const float2* stats, const float* hit, const int64_t* target, float* loss, float* lse,
+            int64_t M, int nt, int64_t V) {
+  __shared__ float2 part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
+  float top = -INFINITY, sum = 0.0f;
+  auto add = [&](float2 s) {
+    const float next = fmaxf(top, s.x), from = next == -INFINITY ? 0.0f : next;
+    sum = sum * expf(top - from) + s.y * expf(s.x - from);
+    top = next;
+  };
+  if (m < M)
+#pragma unroll 4
+    for (int k = warp; k < nt; k += 8) add(stats[(int64_t)k * M + m]);
+  part[warp][lane] = make_float2(top, sum);
+  __syncthreads();
+  if (warp || m >= M) return;
+  for (int u = 1; u < 8; ++u) add(part[u][lane]);
+  const float total = top + logf(sum);
+  const int64_t t = target[m];
+  lse[m] = total;
+  loss[m] = t >= 0 && t < V ? total - hit[m] : 0.0f;
+}
+
+// The power of two by which float16's d is scaled, from the largest |dloss| of a row that counts.
+__global__ void __launch_bounds__(1024)
+find_scale(const float* dloss, const int64_t* target, int64_t M, int64_t V, float* scale) {
+  __shared__ float part[32];
+  float top = 0.0f;
+  for (int64_t m = threadIdx.x; m < M; m += 1024)
+    if (target[m] >= 0 && target[m] < V) top = fmaxf(top, fabsf(dloss[m]));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  top = part[threadIdx.x];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (threadIdx.x) return;
+  int e = 14;
+  if (top > 0.0f && top <= 3.4e38f) frexpf(top, &e);  // top < 2^e
+  const int k = max(-100, min(100, 14 - e));
+  scale[0] = ldexpf(1.0f, k);
+  scale[1] = ldexpf(1.0f, -k);
+}
+
+// Rows as the products take them: [parts, rows, pitch] with zeros between `cols` and the pitch. Rows
+// whose target does not count are zeros (target NULL: all count).
+template <typename T, typename S>
+__global__ void __launch_bounds__(256)
+stage_rows(const S* src, int64_t stride, T* dst, int64_t rows, int64_t cols, int64_t pitch,
+           const int64_t* target, int64_t V) {
+  const int64_t per = pitch / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = i / per, c = (i - r * per) * 8;
+  if (r >= rows) return;
+  const bool counts = !target || (target[r] >= 0 && target[r] < V);
+  const S* p = src + r * stride + c;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = counts && c + k < cols ? to_f(p[k]) : 0.0f;
+  if constexpr (sizeof(S) == 4) {
+    __nv_bfloat16 b[8][3];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) split3(v[k], b[k]);
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = __bfloat16_as_ushort(b[2 * k][part]) |
+               (uint32_t)__bfloat16_as_ushort(b[2 * k + 1][part]) << 16;
+      *reinterpret_cast<uint4*>(dst + (part * rows + r) * pitch + c) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = glr::pack2<T>(make_float2(v[2 * k], v[2 * k + 1]));
+    *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+__global__ void clear_rows(void* dst, int64_t rows, int64_t bytes, int64_t stride) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / bytes;
+  if (r < rows) static_cast<uint8_t*>(dst)[r * stride + (i - r * bytes)] = 0;
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+// [parts, rows, cols] of 16-bit values, rows `pitch` elements apart, in boxes of box_rows x 64
+// (128 bytes, swizzled).
+bool make_map(CUtensorMap* m, const void* p, bool half, uint64_t parts, uint64_t rows, uint64_t cols,
+              uint64_t pitch, uint32_t box_rows) {
+  auto fn = tc::tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, rows, parts};
+  cuuint64_t strides[2] = {pitch * 2, rows * pitch * 2};
+  cuuint32_t box[3] = {64, box_rows, 1}, one[3] = {1, 1, 1};
+  return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 1;
+  return n;
+}
+
+// Rows that the products read: the caller's own, or staged ones.
+struct operand {
+  const void* p;
+  uint64_t parts, rows, cols, pitch;
+};
+
+template <Mode MODE, typename T, typename O>
+cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_args g,
+                    cudaStream_t s) {
+  constexpr bool kHalf = glr::is_half<T>;
+  constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
+  CUtensorMap ma, mb, mc;
+  if (!make_map(&ma, a.p, kHalf, a.parts, a.rows, a.cols, a.pitch, kAmn ? kBK : kBM) ||
+      !make_map(&mb, b.p, kHalf, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : kBN))
+    return cudaErrorInvalidValue;
+  if (!c)
+    mc = ma;  // not used
+  else if (!make_map(&mc, c->p, kHalf, c->parts, c->rows, c->cols, c->pitch, 32))
+    return cudaErrorInvalidValue;
+  g.status = device_status_word();
+  const cudaError_t e = max_smem_once<xgemm<MODE, T, O>>(kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
+  xgemm<MODE, T, O><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, kSmem, s>>>(
+      ma, mb, mc, g);
+  return cudaGetLastError();
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Whether the products read a caller's rows as they lie: 16-bit values whose rows begin on multiples
+// of 16 bytes, one after the other.
+bool direct(int64_t type, const glr_view& v, int64_t rows, int64_t cols) {
+  return type != GLR_F32 && (reinterpret_cast<uintptr_t>(v.data) & 15) == 0 &&
+         (rows <= 1 || (v.stride_t % 8 == 0 && v.stride_t >= cols));
+}
+
+// Bytes of staged rows.
+int64_t staged(int64_t type, int64_t rows, int64_t cols) {
+  return up((type == GLR_F32 ? 3 : 1) * rows * up(cols, 8) * 2, 256);
+}
+
+template <typename T, typename S>
+cudaError_t stage(const glr_view& v, void* to, int64_t rows, int64_t cols, const int64_t* target,
+                  int64_t V, operand* out, cudaStream_t s) {
+  const int64_t pitch = up(cols, 8), n = rows * (pitch / 8);
+  stage_rows<T, S><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
+      static_cast<const S*>(v.data), v.stride_t, static_cast<T*>(to), rows, cols, pitch, target, V);
+  *out = operand{to, sizeof(S) == 4 ? 3u : 1u, (uint64_t)rows, (uint64_t)cols, (uint64_t)pitch};
+  return cudaGetLastError();
+}
+
+// The rows of h or W for the products: as they lie, or staged at `to`.
+template <typename T, typename S>
+cudaError_t rows_of(int64_t type, const glr_view& v, void* to, int64_t rows, int64_t cols,
+                    operand* out, cudaStream_t s) {
+  if (direct(type, v, rows, cols)) {
+    *out = operand{v.data, 1, (uint64_t)rows, (uint64_t)cols,
+                   (uint64_t)(rows > 1 ? v.stride_t : up(cols, 8))};
+    return cudaSuccess;
+  }
+  return stage<T, S>(v, to, rows, cols, nullptr, 0, out, s);
+}
+
+// How the gradients' vocabulary is cut, and where things lie in their workspace.
+struct back_plan {
+  int64_t piece, pieces;         // columns of a piece
+  int64_t d, h, w, acc, scale;   // offsets
+  int64_t bytes;
+};
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
+  const int64_t parts = type == GLR_F32 ? 3 : 1;
+  back_plan p;
+  const int64_t most = std::max<int64_t>(kBN, kPieceBytes / (M * 2 * parts) / kBN * kBN);
+  p.pieces = (V + most - 1) / most;
+  p.piece = up((V + p.pieces - 1) / p.pieces, kBN);
+  p.pieces = (V + p.piece - 1) / p.piece;
+  p.d = 0;
+  p.h = p.d + up(parts * M * std::min(p.piece, up(V, 8)) * 2, 256);
+  p.w = p.h + staged(type, M, D);
+  p.acc = p.w + staged(type, V, D);
+  p.scale = p.acc + (p.pieces > 1 ? up(M * D * 4, 256) : 0);
+  p.bytes = p.scale + 256;
+  return p;
+}
+
+template <typename T, typename S>
+cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const int nt = (int)((a.V + kBN - 1) / kBN);
+  gemm_args g{};
+  g.M = (int)a.M, g.N = (int)a.V, g.K = (int)a.D, g.V = (int)a.V;
+  g.products = sizeof(S) == 4 ? 6 : 1;
+  g.target = a.target;
+  g.stats = reinterpret_cast<float2*>(ws), ws += up((int64_t)nt * a.M * 8, 256);
+  g.hit = reinterpret_cast<float*>(ws), ws += up(a.M * 4, 256);
+  operand h, w;
+  cudaError_t e = rows_of<T, S>(a.type, a.h, ws, a.M, a.D, &h, s);
+  if (e != cudaSuccess) return e;
+  e = rows_of<T, S>(a.type, a.W, ws + staged(a.type, a.M, a.D), a.V, a.D, &w, s);
+  if (e != cudaSuccess) return e;
+  if ((e = product<kLoss, T, T>(h, w, nullptr, g, s)) != cudaSuccess) return e;
+  finish_loss<<<(unsigned)((a.M + 31) / 32), 256, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse,
+                                                          a.M, nt, a.V);
+  return cudaGetLastError();
+}
+
+template <typename T, typename S>
+cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const back_plan p = plan(a.type, a.M, a.V, a.D);
+  const uint64_t parts = sizeof(S) == 4 ? 3 : 1;
+  float* scale = nullptr;
+  cudaError_t e;
+  if (glr::is_half<S>) {
+    scale = reinterpret_cast<float*>(ws + p.scale);
+    find_scale<<<1, 1024, 0, s>>>(a.dloss, a.target, a.M, a.V, scale);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  operand h, hz, w;
+  // the rows of h that count, for dW; the logits take them too
+  if ((e = stage<T, S>(a.h, ws + p.h, a.M, a.D, a.target, a.V, &hz, s)) != cudaSuccess) return e;
+  h = hz;
+  if ((e = rows_of<T, S>(a.type, a.W, ws + p.w, a.V, a.D, &w, s)) != cudaSuccess) return e;
+  for (int64_t k = 0; k < p.pieces; ++k) {
+    const int64_t v0 = k * p.piece, cols = std::min(p.piece, a.V - v0);
+    const operand d{ws + p.d, parts, (uint64_t)a.M, (uint64_t)cols, (uint64_t)up(cols, 8)};
+    gemm_args g{};
+    g.M = (int)a.M, g.N = (int)cols, g.K = (int)a.D, g.V = (int)a.V;
+    g.products = sizeof(S) == 4 ? 6 : 1;
+    g.b_row = g.v0 = (int)v0;
+    g.target = a.target, g.lse = a.lse, g.dloss = a.dloss, g.scale = scale;
+    if ((e = product<kGrad, T, S>(h, w, &d, g, s)) != cudaSuccess) return e;
+    if (a.dh.data) {
+      gemm_args r{};
+      r.M = (int)a.M, r.N = (int)a.D, r.K = (int)cols, r.products = g.products, r.b_row = (int)v0;
+      r.scale = scale;
+      r.acc = reinterpret_cast<float*>(ws + p.acc);
+      r.has_acc = k > 0, r.keep = k + 1 < p.pieces;
+      r.out = a.dh.data, r.out_stride = a.dh.stride_t;
+      if ((e = product<kRows, T, S>(d, w, nullptr, r, s)) != cudaSuccess) return e;
+    }
+    if (a.dW.data) {
+      gemm_args c{};
+      c.M = (int)cols, c.N = (int)a.D, c.K = (int)a.M, c.products = g.products;
+      c.scale = scale;
+      c.out = static_cast<S*>(a.dW.data) + v0 * a.dW.stride_t, c.out_stride = a.dW.stride_t;
+      if ((e = product<kColumns, T, S>(d, hz, nullptr, c, s)) != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t loss_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D) {
+  const int64_t nt = (V + kBN - 1) / kBN;
+  return (size_t)(up(nt * M * 8, 256) + up(M * 4, 256) + staged(type, M, D) + staged(type, V, D));
+}
+
+size_t loss_backward_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D) {
+  return (size_t)plan(type, M, V, D).bytes;
+}
+
+cudaError_t launch_loss(const xent_loss_args& a, cudaStream_t s) {
+  if (a.type == GLR_F32) return loss_of<__nv_bfloat16, float>(a, s);
+  return a.type == GLR_BF16 ? loss_of<__nv_bfloat16, __nv_bfloat16>(a, s)
+                            : loss_of<__half, __half>(a, s);
+}
+
+cudaError_t launch_loss_backward(const xent_loss_backward_args& a, cudaStream_t s) {
+  if (a.type == GLR_F32) return back_of<__nv_bfloat16, float>(a, s);
+  return a.type == GLR_BF16 ? back_of<__nv_bfloat16, __nv_bfloat16>(a, s)
+                            : back_of<__half, __half>(a, s);
+}
+
+cudaError_t clear_gradient(const glr_out& dW, int64_t type, int64_t V, int64_t D, cudaStream_t s) {
+  const int64_t size = type == GLR_F32 ? 4 : 2;
+  clear_rows<<<(unsigned)((V * D * size + 255) / 256), 256, 0, s>>>(dW.data, V, D * size,
+                                                                    dW.stride_t * size);
+  return cudaGetLastError();
+}
+
+}  // namespace xent
+}  // namespace dlr
