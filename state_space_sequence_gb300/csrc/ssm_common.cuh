@@ -1,13 +1,18 @@
 // ssm_common.cuh -- device helpers shared by the kernels behind include/ssm.h: the token's step, the
 // decays of a pair of states, pieces of activation rows, and sums over the lanes of a warp.
 //
-// The scan's layout, the same in all its kernels. A warp has 128 / LN channels of one batch entry,
-// LN lanes to a channel: a lane has kStates = 4 states of each of kChannels = 4 neighbouring
-// channels, sixteen numbers in registers. N <= 4 LN; missing states and channels are zeros. So a
-// word of Bm or Cm that a lane reads from shared memory serves four channels, and one of the step
-// four states: with one channel and sixteen states to a lane the scan would read twice as much of
-// shared memory, whose bandwidth it is near. Steps go in tiles of kT, staged by the warp for itself:
-// no warp waits for another.
+// The scan's layout, the same in all its kernels. A warp has 64 / LN channels of one batch entry, LN
+// lanes to a channel: a lane has kStates = 8 states of each of kChannels = 2 neighbouring channels,
+// sixteen numbers in registers, in pairs of neighbouring states. N <= 8 LN; missing states and
+// channels are zeros. A lane reads per step four 16-byte words of Bm and Cm, which the lanes beside
+// it share, and two 8-byte ones of its channels' steps and inputs, and a sum over the states takes
+// one exchange at N = 16: shared memory is then as busy as the multiply-adds and the exponentials
+// are, each about 20 cycles an SM for a warp's step. With 4 x 4 it takes three exchanges for four
+// sums, with one channel and sixteen states twice the words.
+//
+// Two warps work on a unit of channels: one runs the recurrence, its helper stages what it reads and
+// finishes what it leaves, a tile of kT steps ahead and behind, so that neither the latency of memory
+// nor the elementwise work stands in the recurrence's way. Pairs meet once a tile.
 #pragma once
 
 #include "glr_common.cuh"
@@ -31,43 +36,50 @@ using glr::view;
 using glr::words;
 
 constexpr int kT = SSM_STATE_STEPS;  // steps of a tile
-constexpr int kStates = 4, kChannels = 4;
+constexpr int kStates = 8, kChannels = 2, kPairs = kStates / 2;
+constexpr int kUnits = 4;  // of a block: warps 0-3 run, warps 4-7 help
 
-// softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], and sigmoid(v). log1p(e) =
-// 2 atanh(r), r = e / (2 + e) <= 1/3, by its odd series to r^15: the next term is 2e-9 of the
-// first. The logarithm of the rounded 1 + e would lose 6e-5 of a step of 0.001. 0 at -inf, inf at
-// +inf, a NaN stays one.
-__device__ __forceinline__ float softplus(float v, float& sig) {
-  const float e = ex2(-kLog2e * fabsf(v));
-  const float r = e * rcp(2.0f + e), s = r * r;
-  float q = 1.0f / 15.0f;
-  q = fmaf(q, s, 1.0f / 13.0f);
-  q = fmaf(q, s, 1.0f / 11.0f);
-  q = fmaf(q, s, 1.0f / 9.0f);
-  q = fmaf(q, s, 1.0f / 7.0f);
-  q = fmaf(q, s, 1.0f / 5.0f);
-  q = fmaf(q, s, 1.0f / 3.0f);
-  q = fmaf(q, s, 1.0f);
-  const float w = rcp(1.0f + e);
-  sig = v >= 0.0f ? w : e * w;
-  return fmaf(2.0f * r, q, max_nan(v, 0.0f));
+// log1p(e) for e in [0, 1]: e P(e), P of degree 8 by a least-maximum fit of the relative error
+// (3e-8; 1.7e-7 with its roundings). The logarithm of the rounded 1 + e would lose 6e-5 of a step of
+// 0.001, and this needs neither a logarithm nor a reciprocal.
+__device__ __forceinline__ float2 log1p2(float2 e) {
+  float2 q = two(0.0052326940931379795f);
+  q = fma2(q, e, two(-0.029505237936973572f));
+  q = fma2(q, e, two(0.07822595536708832f));
+  q = fma2(q, e, two(-0.13663245737552643f));
+  q = fma2(q, e, two(0.19106006622314453f));
+  q = fma2(q, e, two(-0.2484298199415207f));
+  q = fma2(q, e, two(0.3331909775733948f));
+  q = fma2(q, e, two(-0.4999949336051941f));
+  q = fma2(q, e, two(0.9999999403953552f));
+  return mul2(q, e);
 }
-
-// What a pair of states keeps of `v` over a step whose exponents (in powers of two) are z: v 2^z.
-// For 16-bit activations 2^z comes from the special-function unit. For float32 1 - 2^z comes first
-// (glr::decay2: its digits hold next to a decay of 1) and v - (1 - 2^z) v keeps them, so that a
-// memory of thousands of steps does not add up the rounding of its decay. z is held at +-126.
+// softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|): 0 at -inf, inf at +inf, a NaN stays one.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const float2 z = mul2(make_float2(fabsf(v.x), fabsf(v.y)), two(-kLog2e));
+  return add2(log1p2(make_float2(ex2(z.x), ex2(z.y))),
+              make_float2(max_nan(v.x, 0.0f), max_nan(v.y, 0.0f)));
+}
+// What a pair of states keeps of `v` over a step whose exponents (in powers of two) are rate * s.
+// For 16-bit activations the decay comes from the special-function unit, whose results lie 1.9e-8 of
+// themselves low on average next to 1 (measured; as cutting off would make them): over a memory of a
+// thousand steps that adds up, so the exponent gets kNudge, which is still no step where s is 0. For
+// float32 1 - decay comes first (glr::decay2: its digits hold next to a decay of 1) and v - (1 -
+// decay) v keeps them; the exponent is held at +-126.
+constexpr float kNudge = 2.7e-8f;
 template <bool PRECISE>
 struct decay {
   float2 a;  // the decay, or (PRECISE) one less it, negative
-  __device__ __forceinline__ explicit decay(float2 z) {
+  __device__ __forceinline__ decay(float2 rate, float2 s) {
     if constexpr (PRECISE) {
+      float2 z = mul2(rate, s);
       z = make_float2(min_nan(z.x, 126.0f), min_nan(z.y, 126.0f));
       float2 rest, unused;
       glr::decay2(z, rest, unused);
       a = mul2(rest, two(-1.0f));
     } else {
-      a = make_float2(ex2(min_nan(z.x, 126.0f)), ex2(min_nan(z.y, 126.0f)));
+      const float2 z = fma2(rate, s, two(kNudge));
+      a = make_float2(ex2(z.x), ex2(z.y));
     }
   }
   __device__ __forceinline__ float2 of(float2 v) const {
@@ -126,46 +138,52 @@ __device__ __forceinline__ void load_floats(float* v, const float* p) {
   }
 }
 
-// Sums of four values over LANES lanes that stand STRIDE apart; `at` is a lane's place among them.
-// Each exchange halves what a lane still has to add, so that four sums over four lanes take three
-// exchanges. Afterwards a lane has value at & 3 (LANES >= 4; the same in every fourth lane), values
-// 2 at and 2 at + 1 (2 lanes) or all four (1 lane). The order of the additions is fixed.
-template <int STRIDE, int LANES>
-__device__ __forceinline__ void sum4(float (&v)[4], int at) {
+// Sums of COUNT values over LANES lanes that stand STRIDE apart; `at` is a lane's place among them.
+// Each exchange halves what a lane still has to add, so that eight sums over eight lanes take seven
+// exchanges, and what is left of the lanes is added up whole. The order of the additions is fixed.
+template <int STRIDE, int COUNT, int LANES>
+__device__ __forceinline__ void sum_lanes(float* v, int at) {
   constexpr uint32_t kAll = 0xffffffffu;
-  if constexpr (LANES >= 4) {
-    const bool hi = at & 2, odd = at & 1;
-    const float s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
-    const float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
-    const float t0 = k0 + __shfl_xor_sync(kAll, s0, 2 * STRIDE);
-    const float t1 = k1 + __shfl_xor_sync(kAll, s1, 2 * STRIDE);
-    v[0] = (odd ? t1 : t0) + __shfl_xor_sync(kAll, odd ? t0 : t1, STRIDE);
+  if constexpr (LANES > 1) {
+    if constexpr (COUNT > 1) {
+      const bool upper = at & (LANES / 2);
 #pragma unroll
-    for (int d = 4; d < LANES; d *= 2) v[0] += __shfl_xor_sync(kAll, v[0], d * STRIDE);
-  } else if constexpr (LANES == 2) {
-    const bool odd = at & 1;
-    const float s0 = odd ? v[0] : v[2], s1 = odd ? v[1] : v[3];
-    const float k0 = odd ? v[2] : v[0], k1 = odd ? v[3] : v[1];
-    v[0] = k0 + __shfl_xor_sync(kAll, s0, STRIDE);
-    v[1] = k1 + __shfl_xor_sync(kAll, s1, STRIDE);
+      for (int i = 0; i < COUNT / 2; ++i) {
+        const float send = upper ? v[i] : v[i + COUNT / 2];
+        const float keep = upper ? v[i + COUNT / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(kAll, send, STRIDE * (LANES / 2));
+      }
+    } else {
+      v[0] += __shfl_xor_sync(kAll, v[0], STRIDE * (LANES / 2));
+    }
+    sum_lanes<STRIDE, (COUNT > 1 ? COUNT / 2 : 1), LANES / 2>(v, at);
   }
 }
-// Writes them: p is the place of the first of the four, 16-byte aligned.
-template <int LANES>
-__device__ __forceinline__ void put4(float* p, const float (&v)[4], int at) {
-  if constexpr (LANES >= 4) {
-    if (at < 4) p[at] = v[0];
-  } else if constexpr (LANES == 2) {
+// Writes them to p[0 .. COUNT), by the lanes that have them.
+template <int COUNT, int LANES>
+__device__ __forceinline__ void put_lanes(float* p, const float* v, int at) {
+  if constexpr (COUNT <= LANES) {
+    if (at % (LANES / COUNT) == 0) p[at / (LANES / COUNT)] = v[0];
+  } else if constexpr (COUNT == 2 * LANES) {
     *reinterpret_cast<float2*>(p + 2 * at) = make_float2(v[0], v[1]);
   } else {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    static_assert(COUNT == 4 * LANES, "");
+    *reinterpret_cast<float4*>(p + 4 * at) = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
-// How a warp's tile is cut into pieces of VE channels (and VB states) for its lanes.
+// A pair's two warps meet (barriers 1 .. kUnits), and the helpers of a block (barrier kUnits + 1).
+__device__ __forceinline__ void meet_pair(int pair) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+}
+__device__ __forceinline__ void meet_helpers() {
+  asm volatile("bar.sync %0, %1;" ::"n"(1 + kUnits), "n"(32 * kUnits) : "memory");
+}
+
+// How a unit's tile is cut into pieces of VE channels (and VB states) for a warp's lanes.
 template <typename T, int LN>
 struct shape {
-  static constexpr int kCW = 32 / LN * kChannels;  // channels of a warp
+  static constexpr int kCW = 32 / LN * kChannels;  // channels of a unit
   static constexpr int kNP = LN * kStates;         // states of a channel, with the missing ones
   static constexpr int VE = 16 / (int)sizeof(T) < kCW ? 16 / (int)sizeof(T) : kCW;
   static constexpr int VB = 16 / (int)sizeof(T) < kNP ? 16 / (int)sizeof(T) : kNP;
@@ -174,13 +192,8 @@ struct shape {
   static_assert(kRow <= 32 && kRowB <= 32 && 32 % kRow == 0 && 32 % kRowB == 0, "");
 };
 
-// Where a warp works.
-struct place {
-  int64_t b;
-  int split, group, c0, n_ch;  // c0: first channel; n_ch: channels of the warp that exist (<= kCW)
-};
-
-inline int lanes_for(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+// Lanes of a channel.
+inline int lanes_for(int64_t N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
 
 }  // namespace ssm
 }  // namespace dlr

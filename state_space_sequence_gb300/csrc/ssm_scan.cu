@@ -6,6 +6,8 @@
 // the layout), which issues for two states a product for the exponent, two exponentials, one
 // multiply-add for the state, one for the output and one product for the input. Everything else is
 // done once a tile of 16 steps, by pieces of rows: the step's softplus, the skip and the gate.
+#include <type_traits>
+
 #include "ssm_scan.cuh"
 
 namespace dlr {
@@ -15,8 +17,6 @@ namespace dlr {
 namespace ssm {
 namespace {
 
-constexpr int kWarps = 4;  // of a block; each works by itself
-
 template <typename T>
 struct scan_params {
   inputs<T> in;
@@ -24,192 +24,190 @@ struct scan_params {
   float *h_last, *states;
 };
 
-// A warp's part of shared memory: the tile's steps s, inputs s x, outputs, Bm and Cm.
-template <typename T, int LN>
+// A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
+// tiles in turn.
+template <typename T, int LN, bool MAP>
 struct scan_tile {
   using S = shape<T, LN>;
-  float s[kT][S::kCW], u[kT][S::kCW], o[kT][S::kCW];
-  float Bm[kT][S::kNP], Cm[kT][S::kNP];
+  float s[2][kT][S::kCW], u[2][kT][S::kCW];
+  float Bm[2][kT][S::kNP];
+  float Cm[MAP ? 1 : 2][MAP ? 1 : kT][S::kNP];
+  float o[MAP ? 1 : 2][MAP ? 1 : kT][S::kCW];
   float bias[S::kCW], D[S::kCW];
 };
 
 // MAP: only the state that each split but the last adds, and the sum of its steps.
 template <typename T, int LN, bool MAP>
-__global__ void __launch_bounds__(32 * kWarps) scan_kernel(scan_params<T> q) {
+__global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
   using S = shape<T, LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
-  constexpr int VE = S::VE, VB = S::VB;
+  constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  scan_tile<T, LN>& m = reinterpret_cast<scan_tile<T, LN>*>(smem)[warp];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp % kUnits;
+  scan_tile<T, LN, MAP>& m = reinterpret_cast<scan_tile<T, LN, MAP>*>(smem)[pair];
+  unit<T, LN> u;
+  if (!u.find(in, (int64_t)blockIdx.x * kUnits + pair, MAP ? in.splits - 1 : in.splits)) return;
+  const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
+  const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  const int64_t id = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-  const int per_row = in.blocks * in.G, n_split = MAP ? in.splits - 1 : in.splits;
-  if (id >= (int64_t)per_row * n_split * in.B) return;
-  const int cb = (int)(id % per_row);
-  const int split = (int)(id / per_row % n_split);
-  const int64_t b = id / per_row / n_split;
-  const int group = cb / in.blocks, first = (cb % in.blocks) * S::kCW;
-  const int c0 = group * in.Hg + first, n_ch = min(S::kCW, in.Hg - first);
-  // this lane's channels and states
-  const int at = lane % LN, cl = lane / LN * kChannels, n0 = at * kStates;
-  const int my_ch = n_ch - cl;
-
-  const bool whole = n_ch == S::kCW && pieces(in.x, c0, VE * sizeof(T)) &&
-                     pieces(in.dt, c0, VE * sizeof(T));
-  const bool whole_z = in.z.p && n_ch == S::kCW && pieces(in.z, c0, VE * sizeof(T));
-  const bool whole_y = n_ch == S::kCW && pieces(q.y, c0, VE * sizeof(T));
-  const bool whole_b = in.N % VB == 0 && pieces(in.Bm, (int64_t)group * in.N, VB * sizeof(T)) &&
-                       pieces(in.Cm, (int64_t)group * in.N, VB * sizeof(T));
-
-  for (int c = lane; c < S::kCW; c += 32) {
-    m.bias[c] = in.bias && c < n_ch ? in.bias[c0 + c] : 0.0f;
-    m.D[c] = in.D && c < n_ch ? in.D[c0 + c] : 0.0f;
+  if (warp >= kUnits) {
+    const bool ok_z = u.n_ch == S::kCW && u.pieces(in.z), ok_y = u.n_ch == S::kCW && u.pieces(q.y);
+    for (int c = lane; c < S::kCW; c += 32) {
+      m.bias[c] = in.bias && c < u.n_ch ? in.bias[u.c0 + c] : 0.0f;
+      m.D[c] = in.D && c < u.n_ch ? in.D[u.c0 + c] : 0.0f;
+    }
+    __syncwarp();
+    // what is staged next, and what is finished next: each read a tile before its use
+    words<T, VE> wx[S::NV], wd[S::NV], fx[S::NV], fz[S::NV];
+    words<T, VB> wb[S::NB], wc[S::NB];
+    auto fetch = [&](int tile) {
+      const int64_t t0 = (int64_t)tile * kT;
+      u.fetch(wx, in.x, t0, in.L, lane, u.whole);
+      u.fetch(wd, in.dt, t0, in.L, lane, u.whole);
+      u.fetch_b(wb, in.Bm, t0, in.L, in.N, lane);
+      if (!MAP) u.fetch_b(wc, in.Cm, t0, in.L, in.N, lane);
+    };
+    auto stage = [&](int tile) {
+      stage_steps<T, LN>(u, in.softplus, (int64_t)tile * kT, in.L, lane, m.bias, wx, wd,
+                         m.s[tile & 1], m.u[tile & 1]);
+      u.put_b(m.Bm[tile & 1], wb, lane);
+      if constexpr (!MAP) u.put_b(m.Cm[tile & 1], wc, lane);
+    };
+    auto fetch_rest = [&](int tile) {
+      if (in.D) u.fetch(fx, in.x, (int64_t)tile * kT, in.L, lane, u.whole);
+      if (in.z.p) u.fetch(fz, in.z, (int64_t)tile * kT, in.L, lane, ok_z);
+    };
+    auto finish = [&](int tile) {  // the skip, the gate, and out
+      const int64_t t0 = (int64_t)tile * kT;
+#pragma unroll
+      for (int k = 0; k < S::NV; ++k) {
+        int t, c;
+        if (!u.piece(k, lane, t, c)) break;
+        if (t0 + t >= in.L || c >= u.n_ch) continue;
+        float o[VE], v[VE], d[VE];
+        load_floats<VE>(o, &m.o[tile & 1][t][c]);
+        if (in.D) {
+          fx[k].to(v);
+          load_floats<VE>(d, m.D + c);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) o[i] = fmaf(d[i], v[i], o[i]);
+        }
+        if (in.z.p) {
+          fz[k].to(v);
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) {
+            const float2 z = make_float2(v[i], v[i + 1]), g = mul2(z, glr::sigmoid2(z));
+            o[i] *= g.x, o[i + 1] *= g.y;
+          }
+        }
+        put_piece<T, VE>(q.y.row(u.b, t0 + t) + u.c0 + c, o, u.n_ch - c, ok_y);
+      }
+    };
+    fetch(t_first);
+    stage(t_first);
+    if (t_first + 1 < t_end) fetch(t_first + 1);
+    meet_pair(pair);
+    for (int tile = t_first; tile < t_end; ++tile) {
+      if (tile + 1 < t_end) stage(tile + 1);
+      if (tile + 2 < t_end) fetch(tile + 2);
+      if constexpr (!MAP) {
+        if (tile > t_first) finish(tile - 1);
+        fetch_rest(tile);
+      }
+      meet_pair(pair);
+    }
+    if constexpr (!MAP) finish(t_end - 1);
+    return;
   }
-  float2 rate[kChannels][2], h[kChannels][2];
-  load_rates(rate, in.A, in.N, c0 + cl, my_ch, n0);
-  const int64_t HN = (int64_t)in.H * in.N, ch = (int64_t)(c0 + cl) * in.N;
-  if (MAP || (split == 0 && !in.h0))
-    load_states(h, nullptr, in.N, 0, 0);
-  else if (split == 0)
-    load_states(h, in.h0 + b * HN + ch, in.N, my_ch, n0);
+
+  // the recurrence: this lane's channels and states
+  const int at = lane / CL, cg = lane % CL, cl = cg * kChannels, n0 = at * kStates;
+  const int my_ch = u.n_ch - cl;
+  const int64_t ch = (int64_t)(u.c0 + cl) * in.N;
+  float2 rate[kChannels][kPairs], h[kChannels][kPairs];
+  load_rates(rate, in.A, in.N, u.c0 + cl, my_ch, n0);
+  if (MAP || (u.split == 0 && !in.h0))
+    clear(h);
+  else if (u.split == 0)
+    load_states(h, in.h0 + u.b * HN + ch, in.N, my_ch, n0);
   else
-    load_states(h, in.ends + (b * in.splits + split - 1) * HN + ch, in.N, my_ch, n0);
+    load_states(h, in.ends + (row_map - 1) * HN + ch, in.N, my_ch, n0);
   float sum[kChannels] = {};
   bool cut = false;
-  __syncwarp();
-
-  const int t_first = split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
+  meet_pair(pair);
   for (int tile = t_first; tile < t_end; ++tile) {
     const int64_t t0 = (int64_t)tile * kT;
-    const uint32_t mark = marks(in.reset, b, t0, in.L, lane);
-    // the steps and what they bring in
-#pragma unroll
-    for (int k = 0; k < S::NV; ++k) {
-      const int p = k * 32 + lane, t = p / S::kRow, c = p % S::kRow * VE;
-      if (t >= kT) break;
-      float xv[VE], dv[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) xv[i] = dv[i] = 0.0f;
-      const bool there = t0 + t < in.L && c < n_ch;
-      if (there) {
-        words<T, VE> wx, wd;
-        get_piece<T, VE>(wx, in.x.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-        get_piece<T, VE>(wd, in.dt.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-        wx.to(xv);
-        wd.to(dv);
-      }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        float sig, s = dv[i] + m.bias[c + i];
-        if (in.softplus) s = softplus(s, sig);
-        // steps and channels that do not exist leave the state as it is
-        s = there && c + i < n_ch ? s : 0.0f;
-        dv[i] = s;
-        xv[i] = there && c + i < n_ch ? s * xv[i] : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        m.s[t][c + i] = dv[i];
-        m.u[t][c + i] = xv[i];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < S::NB; ++k) {
-      const int p = k * 32 + lane, t = p / S::kRowB, n = p % S::kRowB * VB;
-      if (t >= kT) break;
-      float bv[VB], cv[VB];
-#pragma unroll
-      for (int i = 0; i < VB; ++i) bv[i] = cv[i] = 0.0f;
-      if (t0 + t < in.L && n < in.N) {
-        words<T, VB> wb, wc;
-        const int64_t o = (int64_t)group * in.N + n;
-        get_piece<T, VB>(wb, in.Bm.row(b, t0 + t) + o, in.N - n, whole_b);
-        wb.to(bv);
-        if (!MAP) {
-          get_piece<T, VB>(wc, in.Cm.row(b, t0 + t) + o, in.N - n, whole_b);
-          wc.to(cv);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VB; ++i) {
-        m.Bm[t][n + i] = bv[i];
-        if (!MAP) m.Cm[t][n + i] = cv[i];
-      }
-    }
-    __syncwarp();
+    const uint32_t mark = marks(in.reset, u.b, t0, in.L, lane);
+    const float (*ms)[S::kCW] = m.s[tile & 1];
+    const float (*mu)[S::kCW] = m.u[tile & 1];
+    const float (*mb)[S::kNP] = m.Bm[tile & 1];
+    const float (*mc)[S::kNP] = m.Cm[MAP ? 0 : tile & 1];
+    float (*mo)[S::kCW] = m.o[MAP ? 0 : tile & 1];
     if (!MAP && q.states)
-      store_states(q.states + (b * in.tiles + tile) * HN + ch, h, in.N, my_ch, n0);
-
+      store_states(q.states + (u.b * in.tiles + tile) * HN + ch, h, in.N, my_ch, n0);
+    // A tile without marks goes without looking for them: a branch would keep the steps apart that
+    // are to overlap.
+    auto steps = [&](auto marks_here) {
+      constexpr bool MARKS = decltype(marks_here)::value;
+      // a step's words are read a step ahead
+      float s_next[kChannels], x_next[kChannels];
+      float2 b_next[kPairs], c_next[kPairs];
+      auto read = [&](int t) {
+        get_channels(s_next, &ms[t][cl]);
+        get_channels(x_next, &mu[t][cl]);
+        get_map(b_next, &mb[t][n0]);
+        if (!MAP) get_map(c_next, &mc[t][n0]);
+      };
+      read(0);
 #pragma unroll 4
-    for (int t = 0; t < kT; ++t) {
-      const float4 s4 = *reinterpret_cast<const float4*>(&m.s[t][cl]);
-      const float4 u4 = *reinterpret_cast<const float4*>(&m.u[t][cl]);
-      const float4 b4 = *reinterpret_cast<const float4*>(&m.Bm[t][n0]);
-      const float4 c4 = *reinterpret_cast<const float4*>(&m.Cm[t][n0]);
-      const float s[4] = {s4.x, s4.y, s4.z, s4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-      const float2 bp[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-      const float2 cp[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
-      if (mark >> t & 1) {
-        load_states(h, nullptr, in.N, 0, 0);
-        cut = true;
-      }
-      float o[kChannels];
+      for (int t = 0; t < kT; ++t) {
+        float s[kChannels], x[kChannels], o[kChannels];
+        float2 bp[kPairs], cp[kPairs];
 #pragma unroll
-      for (int i = 0; i < kChannels; ++i) {
-        float2 acc = two(0.0f);
+        for (int i = 0; i < kChannels; ++i) s[i] = s_next[i], x[i] = x_next[i];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const decay<kPrecise> a(mul2(rate[i][p], two(s[i])));
-          h[i][p] = a.of_plus(h[i][p], mul2(bp[p], two(u[i])));
-          if (!MAP) acc = fma2(h[i][p], cp[p], acc);
+        for (int p = 0; p < kPairs; ++p) {
+          bp[p] = b_next[p];
+          if (!MAP) cp[p] = c_next[p];
         }
-        o[i] = acc.x + acc.y;
-        if (MAP) sum[i] += s[i];
+        read((t + 1) % kT);  // the last one for nothing
+        if (MARKS && (mark >> t & 1)) clear(h);
+#pragma unroll
+        for (int i = 0; i < kChannels; ++i) {
+          float2 acc;
+#pragma unroll
+          for (int p = 0; p < kPairs; ++p) {
+            const decay<kPrecise> a(rate[i][p], two(s[i]));
+            h[i][p] = a.of_plus(h[i][p], mul2(bp[p], two(x[i])));
+            if (!MAP) acc = p ? fma2(h[i][p], cp[p], acc) : mul2(h[i][p], cp[p]);
+          }
+          if (!MAP) o[i] = acc.x + acc.y;
+          if (MAP) sum[i] += s[i];
+        }
+        if (!MAP) {
+          sum_lanes<CL, kChannels, LN>(o, at);
+          put_lanes<kChannels, LN>(&mo[t][cl], o, at);
+        }
       }
-      if (!MAP) {
-        sum4<1, LN>(o, at);
-        put4<LN>(&m.o[t][cl], o, at);
-      }
+    };
+    if (mark) {
+      steps(std::true_type{});
+      cut = true;
+    } else {
+      steps(std::false_type{});
     }
-    __syncwarp();
-    // the skip, the gate, and out
-#pragma unroll
-    for (int k = 0; k < (MAP ? 0 : S::NV); ++k) {
-      const int p = k * 32 + lane, t = p / S::kRow, c = p % S::kRow * VE;
-      if (t >= kT) break;
-      if (t0 + t >= in.L || c >= n_ch) continue;
-      float o[VE], v[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) o[i] = m.o[t][c + i];
-      words<T, VE> w;
-      if (in.D) {
-        get_piece<T, VE>(w, in.x.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-        w.to(v);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) o[i] = fmaf(m.D[c + i], v[i], o[i]);
-      }
-      if (in.z.p) {
-        get_piece<T, VE>(w, in.z.row(b, t0 + t) + c0 + c, n_ch - c, whole_z);
-        w.to(v);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) o[i] *= v[i] * glr::sigmoid(v[i]);
-      }
-      put_piece<T, VE>(q.y.row(b, t0 + t) + c0 + c, o, n_ch - c, whole_y);
-    }
-    __syncwarp();
+    meet_pair(pair);
   }
   if (MAP) {
-    store_states(in.ends + (b * in.splits + split) * HN + ch, h, in.N, my_ch, n0);
+    store_states(in.ends + row_map * HN + ch, h, in.N, my_ch, n0);
     if (at == 0)
 #pragma unroll
       for (int i = 0; i < kChannels; ++i)
         if (i < my_ch)
-          in.sums[(b * in.splits + split) * in.H + c0 + cl + i] =
-              cut ? __int_as_float(0x7fffffff) : sum[i];
-  } else if (split == in.splits - 1 && q.h_last) {
-    store_states(q.h_last + b * HN + ch, h, in.N, my_ch, n0);
+          in.sums[row_map * in.H + u.c0 + cl + i] = cut ? __int_as_float(0x7fffffff) : sum[i];
+  } else if (u.split == in.splits - 1 && q.h_last) {
+    store_states(q.h_last + u.b * HN + ch, h, in.N, my_ch, n0);
   }
 }
 
@@ -218,20 +216,21 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
   using S = shape<T, LN>;
   q.in.blocks = (q.in.Hg + S::kCW - 1) / S::kCW;
   const int64_t units = (int64_t)q.in.blocks * q.in.G * q.in.B;
-  constexpr size_t bytes = sizeof(scan_tile<T, LN>) * kWarps;
-  auto grid = [](int64_t warps) { return (unsigned)((warps + kWarps - 1) / kWarps); };
+  auto grid = [](int64_t n) { return (unsigned)((n + kUnits - 1) / kUnits); };
   cudaError_t e;
   if (q.in.splits > 1) {
+    constexpr size_t bytes = sizeof(scan_tile<T, LN, true>) * kUnits;
     if ((e = max_smem_once<scan_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
-    scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 32 * kWarps, bytes, s>>>(q);
+    scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 64 * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t HN = (int64_t)q.in.H * q.in.N;
     join_splits<false><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
         q.in.A, q.in.h0, q.in.ends, q.in.sums, q.in.B, q.in.splits, HN, q.in.N);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  constexpr size_t bytes = sizeof(scan_tile<T, LN, false>) * kUnits;
   if ((e = max_smem_once<scan_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
-  scan_kernel<T, LN, false><<<grid(units * q.in.splits), 32 * kWarps, bytes, s>>>(q);
+  scan_kernel<T, LN, false><<<grid(units * q.in.splits), 64 * kUnits, bytes, s>>>(q);
   return cudaGetLastError();
 }
 
@@ -244,8 +243,7 @@ cudaError_t scan_of(const ssm_scan_args& a, cudaStream_t s) {
     case 1: return run_scan<T, 1>(q, s);
     case 2: return run_scan<T, 2>(q, s);
     case 4: return run_scan<T, 4>(q, s);
-    case 8: return run_scan<T, 8>(q, s);
-    default: return run_scan<T, 16>(q, s);
+    default: return run_scan<T, 8>(q, s);
   }
 }
 
@@ -262,17 +260,17 @@ struct step_params {
   float* h_out;
 };
 
-// LN lanes to a channel, 4 states to a lane; LN a power of two. The states go through memory once
+// LN lanes to a channel, 4 states to a lane. The states go through memory once
 // each way and are all there is to it: 134 MB at 256 x 4096 x 16.
 template <typename T, int LN, bool QUADS>
 __global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
-  const int lane = threadIdx.x & 31, at = lane % LN, n0 = at * kStates;
+  const int lane = threadIdx.x & 31, at = lane % LN, n0 = 4 * at;
   const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LN;
   const bool there = unit < (int64_t)q.B * q.H;
   const int64_t b = there ? unit / q.H : 0;
   const int c = there ? (int)(unit - b * q.H) : 0, group = c / q.Hg;
-  float sig, s = to_f(q.dt.row(b, 0)[c]) + (q.bias ? q.bias[c] : 0.0f);
-  if (q.softplus) s = softplus(s, sig);
+  float s = to_f(q.dt.row(b, 0)[c]) + (q.bias ? q.bias[c] : 0.0f);
+  if (q.softplus) s = softplus2(two(s)).x;
   const float x = to_f(q.x.row(b, 0)[c]), u = s * x;
   const bool fresh = q.reset && q.reset[b];
   float A[4], h[4], Bm[4], Cm[4];
@@ -294,7 +292,7 @@ __global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
   for (int j = 0; j < 4; ++j) {
     Bm[j] = QUADS || n0 + j < q.N ? to_f(pb[j]) : 0.0f;
     Cm[j] = QUADS || n0 + j < q.N ? to_f(pc[j]) : 0.0f;
-    const float a = expf(min_nan(s * A[j], 87.0f));
+    const float a = expf(s * A[j]);
     h[j] = fresh ? u * Bm[j] : fmaf(a, h[j], u * Bm[j]);
     acc = fmaf(h[j], Cm[j], acc);
   }
@@ -337,7 +335,7 @@ cudaError_t step_of(const ssm_step_args& a, cudaStream_t s) {
   const step_params<T> q{a.B, (int)a.H, (int)(a.H / a.G), (int)a.N, (int)a.G, (int)a.softplus,
                          in(a.x), in(a.dt), in(a.z), in(a.Bm), in(a.Cm), a.A, a.D, a.dt_bias,
                          a.h, a.reset, out_view<T>(a.y), a.h_out};
-  switch (lanes_for(a.N)) {
+  switch (a.N <= 4 ? 1 : 2 * lanes_for(a.N)) {
     case 1: return run_step<T, 1>(q, s);
     case 2: return run_step<T, 2>(q, s);
     case 4: return run_step<T, 4>(q, s);

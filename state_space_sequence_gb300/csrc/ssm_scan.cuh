@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "ssm_common.cuh"
 
@@ -69,71 +70,224 @@ __device__ __forceinline__ uint32_t marks(const uint8_t* reset, int64_t row, int
 
 // The rates of a lane's states times log2(e), in pairs of neighbouring states; zero for states and
 // channels that do not exist.
-__device__ __forceinline__ void load_rates(float2 (&a)[kChannels][2], const float* A, int N,
+__device__ __forceinline__ void load_rates(float2 (&a)[kChannels][kPairs], const float* A, int N,
                                            int64_t c, int n_ch, int n0) {
 #pragma unroll
-  for (int i = 0; i < kChannels; ++i) {
-    float v[4];
+  for (int i = 0; i < kChannels; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = i < n_ch && n0 + j < N ? A[(c + i) * N + n0 + j] * kLog2e : 0.0f;
-    a[i][0] = make_float2(v[0], v[1]);
-    a[i][1] = make_float2(v[2], v[3]);
-  }
+    for (int p = 0; p < kPairs; ++p) {
+      const int n = n0 + 2 * p;
+      const float* q = A + (c + i) * N + n;
+      a[i][p] = make_float2(i < n_ch && n < N ? q[0] * kLog2e : 0.0f,
+                            i < n_ch && n + 1 < N ? q[1] * kLog2e : 0.0f);
+    }
 }
-// A lane's states from an array [.., H, N] whose row of channel c begins at p (or zeros), and back.
-__device__ __forceinline__ void load_states(float2 (&h)[kChannels][2], const float* p, int N,
+__device__ __forceinline__ void clear(float2 (&h)[kChannels][kPairs]) {
+#pragma unroll
+  for (int i = 0; i < kChannels; ++i)
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) h[i][p] = two(0.0f);
+}
+// A lane's states from an array [.., H, N] whose row of the lane's first channel begins at p, and
+// back.
+__device__ __forceinline__ void load_states(float2 (&h)[kChannels][kPairs], const float* p, int N,
                                             int n_ch, int n0) {
 #pragma unroll
   for (int i = 0; i < kChannels; ++i) {
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (p && i < n_ch) {
-      const float* q = p + (int64_t)i * N + n0;
-      if ((N & 3) == 0 && n0 < N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-        const float4 t = *reinterpret_cast<const float4*>(q);
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-      } else {
+    const float* q = p + (int64_t)i * N + n0;
+    const bool quads = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n0 + j < N) v[j] = q[j];
+    for (int k = 0; k < kStates; k += 4) {
+      float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < n_ch && n0 + k < N) {
+        if (quads) {
+          t = *reinterpret_cast<const float4*>(q + k);
+        } else {
+          t.x = q[k];
+          if (n0 + k + 1 < N) t.y = q[k + 1];
+          if (n0 + k + 2 < N) t.z = q[k + 2];
+          if (n0 + k + 3 < N) t.w = q[k + 3];
+        }
       }
+      h[i][k / 2] = make_float2(t.x, t.y);
+      h[i][k / 2 + 1] = make_float2(t.z, t.w);
     }
-    h[i][0] = make_float2(v[0], v[1]);
-    h[i][1] = make_float2(v[2], v[3]);
   }
 }
-__device__ __forceinline__ void store_states(float* p, const float2 (&h)[kChannels][2], int N,
+__device__ __forceinline__ void store_states(float* p, const float2 (&h)[kChannels][kPairs], int N,
                                              int n_ch, int n0) {
 #pragma unroll
   for (int i = 0; i < kChannels; ++i) {
-    if (i >= n_ch) break;
     float* q = p + (int64_t)i * N + n0;
-    const float v[4] = {h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y};
-    if ((N & 3) == 0 && n0 < N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-      *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+    const bool quads = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n0 + j < N) q[j] = v[j];
+    for (int k = 0; k < kStates; k += 4) {
+      if (i >= n_ch || n0 + k >= N) continue;
+      const float2 a = h[i][k / 2], b = h[i][k / 2 + 1];
+      if (quads) {
+        *reinterpret_cast<float4*>(q + k) = make_float4(a.x, a.y, b.x, b.y);
+      } else {
+        q[k] = a.x;
+        if (n0 + k + 1 < N) q[k + 1] = a.y;
+        if (n0 + k + 2 < N) q[k + 2] = b.x;
+        if (n0 + k + 3 < N) q[k + 3] = b.y;
+      }
     }
   }
 }
-
-// Whether a view's pieces of `bytes` from element `first` of each row on stand on multiples of them.
-template <typename T>
-__host__ __device__ inline bool pieces(const view<T>& v, int64_t first, int64_t bytes) {
-  return ((reinterpret_cast<uintptr_t>(v.p + first) | (uintptr_t)(v.sb * (int64_t)sizeof(T)) |
-           (uintptr_t)(v.st * (int64_t)sizeof(T))) & (uintptr_t)(bytes - 1)) == 0;
+// A lane's words of a step: its states' (of Bm or Cm), and its channels'.
+__device__ __forceinline__ void get_map(float2 (&v)[kPairs], const float* p) {
+#pragma unroll
+  for (int k = 0; k < kPairs; k += 2) {
+    const float4 t = *reinterpret_cast<const float4*>(p + 2 * k);
+    v[k] = make_float2(t.x, t.y);
+    v[k + 1] = make_float2(t.z, t.w);
+  }
+}
+__device__ __forceinline__ void get_channels(float (&v)[kChannels], const float* p) {
+  const float2 t = *reinterpret_cast<const float2*>(p);
+  v[0] = t.x, v[1] = t.y;
 }
 
-// How many splits a sequence is cut into. The warps of a call, B * H / (128 / LN), each go through
-// their rows step by step; with fewer warps than the GPU has room for the rows are cut, and the
-// states at the cuts come from a pass over the steps alone.
+// Where a unit works, and how its rows lie.
+template <typename T, int LN>
+struct unit {
+  using S = shape<T, LN>;
+  int64_t b;
+  int split, group, c0, n_ch;  // c0: first channel; n_ch: how many of the unit's exist
+  bool whole, whole_b;         // pieces of rows go by whole accesses
+
+  // units of a batch entry and split: `blocks` of each group
+  __device__ __forceinline__ bool find(const inputs<T>& in, int64_t id, int n_split) {
+    const int per_row = in.blocks * in.G;
+    if (id >= (int64_t)per_row * n_split * in.B) return false;
+    const int cb = (int)(id % per_row);
+    split = (int)(id / per_row % n_split);
+    b = id / per_row / n_split;
+    place(in, cb / in.blocks, cb % in.blocks * S::kCW);
+    return true;
+  }
+  __device__ __forceinline__ void place(const inputs<T>& in, int g, int first) {
+    group = g;
+    c0 = g * in.Hg + first;
+    n_ch = max(0, min(S::kCW, in.Hg - first));
+    whole = n_ch == S::kCW && pieces(in.x) && pieces(in.dt);
+    whole_b = in.N % S::VB == 0 && maps(in.Bm, in.N) && maps(in.Cm, in.N);
+  }
+  template <typename V>
+  __device__ __forceinline__ bool pieces(const view<V>& v) const {
+    return !v.p || ((reinterpret_cast<uintptr_t>(v.p + c0) | (uintptr_t)(v.sb * (int64_t)sizeof(T)) |
+                     (uintptr_t)(v.st * (int64_t)sizeof(T))) &
+                    (uintptr_t)(S::VE * sizeof(T) - 1)) == 0;
+  }
+  __device__ __forceinline__ bool maps(const view<const T>& v, int N) const {
+    return ((reinterpret_cast<uintptr_t>(v.p + (int64_t)group * N) |
+             (uintptr_t)(v.sb * (int64_t)sizeof(T)) | (uintptr_t)(v.st * (int64_t)sizeof(T))) &
+            (uintptr_t)(S::VB * sizeof(T) - 1)) == 0;
+  }
+  // piece k of a tile for this lane: its step and first channel; false where there is none
+  static __device__ __forceinline__ bool piece(int k, int lane, int& t, int& c) {
+    const int p = k * 32 + lane;
+    t = p / S::kRow;
+    c = p % S::kRow * S::VE;
+    return t < kT;
+  }
+  static __device__ __forceinline__ bool piece_b(int k, int lane, int& t, int& n) {
+    const int p = k * 32 + lane;
+    t = p / S::kRowB;
+    n = p % S::kRowB * S::VB;
+    return t < kT;
+  }
+  // A tile's pieces of a row, zeros where the row or the sequence ends.
+  template <typename V>
+  __device__ __forceinline__ void fetch(words<T, S::VE> (&w)[S::NV], const view<V>& v, int64_t t0,
+                                        int64_t L, int lane, bool ok) const {
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+      int t, c;
+      w[k] = words<T, S::VE>();
+      if (piece(k, lane, t, c) && t0 + t < L && c < n_ch)
+        get_piece<T, S::VE>(w[k], v.row(b, t0 + t) + c0 + c, n_ch - c, ok);
+    }
+  }
+  __device__ __forceinline__ void fetch_b(words<T, S::VB> (&w)[S::NB], const view<const T>& v,
+                                          int64_t t0, int64_t L, int N, int lane) const {
+#pragma unroll
+    for (int k = 0; k < S::NB; ++k) {
+      int t, n;
+      w[k] = words<T, S::VB>();
+      if (piece_b(k, lane, t, n) && t0 + t < L && n < N)
+        get_piece<T, S::VB>(w[k], v.row(b, t0 + t) + (int64_t)group * N + n, N - n, whole_b);
+    }
+  }
+  static __device__ __forceinline__ void put_b(float (*m)[S::kNP], const words<T, S::VB> (&w)[S::NB],
+                                               int lane) {
+#pragma unroll
+    for (int k = 0; k < S::NB; ++k) {
+      int t, n;
+      float v[S::VB];
+      w[k].to(v);
+      if (piece_b(k, lane, t, n)) store_floats<S::VB>(&m[t][n], v);
+    }
+  }
+};
+
+// The steps s and the inputs s x of a tile's pieces: softplus, and zeros where there is no channel
+// or step (which leave the state as it is).
+template <typename T, int LN>
+__device__ __forceinline__ void stage_steps(const unit<T, LN>& u, int softplus, int64_t t0, int64_t L,
+                                            int lane, const float* bias,
+                                            const words<T, shape<T, LN>::VE> (&wx)[shape<T, LN>::NV],
+                                            const words<T, shape<T, LN>::VE> (&wd)[shape<T, LN>::NV],
+                                            float (*s)[shape<T, LN>::kCW],
+                                            float (*in)[shape<T, LN>::kCW]) {
+  using S = shape<T, LN>;
+#pragma unroll
+  for (int k = 0; k < S::NV; ++k) {
+    int t, c;
+    if (!unit<T, LN>::piece(k, lane, t, c)) break;
+    float xv[S::VE], dv[S::VE], bv[S::VE];
+    wx[k].to(xv);
+    wd[k].to(dv);
+    load_floats<S::VE>(bv, bias + c);
+#pragma unroll
+    for (int i = 0; i < S::VE; i += 2) {
+      float2 d = add2(make_float2(dv[i], dv[i + 1]), make_float2(bv[i], bv[i + 1]));
+      if (softplus) d = softplus2(d);
+      dv[i] = d.x, dv[i + 1] = d.y;
+    }
+    if (t0 + t >= L || c + S::VE > u.n_ch) {
+#pragma unroll
+      for (int i = 0; i < S::VE; ++i) {
+        const bool there = t0 + t < L && c + i < u.n_ch;
+        dv[i] = there ? dv[i] : 0.0f;
+        xv[i] = there ? xv[i] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S::VE; ++i) xv[i] *= dv[i];
+    store_floats<S::VE>(&s[t][c], dv);
+    store_floats<S::VE>(&in[t][c], xv);
+  }
+}
+
+// How many splits a sequence is cut into. A unit goes through its rows step by step, so few channels
+// leave the GPU idle; rows are then cut, and the states at the cuts come from a pass over the steps
+// alone (about a third of the scan's time). Blocks of kUnits units go one to an SM; a split takes
+// two tiles more, to fill and to drain.
 inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
-  const int64_t cw = 128 / lanes_for(N);
-  const int64_t warps = B * G * ((H / G + cw - 1) / cw), tiles = (L + kT - 1) / kT;
-  if (warps >= 608 || tiles < 4) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles / 2, (1824 + warps - 1) / warps));
+  constexpr int64_t kSMs = 152;
+  const int64_t cw = 64 / lanes_for(N), units = (H / G + cw - 1) / cw;
+  const int64_t blocks = B * G * ((units + kUnits - 1) / kUnits), tiles = (L + kT - 1) / kT;
+  if (const char* e = getenv("SSM_SPLITS")) return std::max(1, std::min<int>(atoi(e), tiles));
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= std::min<int64_t>(64, tiles); ++s) {
+    const double cost = double((blocks * s + kSMs - 1) / kSMs) * ((tiles + s - 1) / s + 2) *
+                        (s == 1 ? 1.0 : 1.35);
+    if (s == 1 || cost < least) best = s, least = cost;
+  }
+  return best;
 }
 
 template <typename T, typename ARGS>

@@ -2,14 +2,16 @@
 //
 // Backwards in time with the gradient of the state carried along: G_t = g_t Cm_t + a_{t+1} G_{t+1}.
 // Sums over the states (q, e, o) go over a channel's lanes, sums over the channels (dBm, dCm) over a
-// warp's channels, then the block's warps, then the blocks of a group (through the workspace, added
-// up by a second kernel); sums over time (dA, dD, ddt_bias) stay with the warp, one partial sum for
-// each batch entry and split.
+// unit's lanes, then the block's units, then the blocks of a group (through the workspace, added up
+// by a second kernel); sums over time stay with the unit's two warps, one partial sum for each batch
+// entry and split.
 //
 // The states are not kept but every 16 steps. A tile's second half needs them first: a run over the
 // first half finds where it begins; then each half is run forwards, its states held in registers
 // (8 steps x 16 numbers a lane), dCm and o formed on the way, and backwards. In all 2.5 exponentials
 // a state and step instead of one, for an eighth of the memory that all states would take.
+#include <type_traits>
+
 #include "ssm_scan.cuh"
 
 namespace dlr {
@@ -19,7 +21,6 @@ namespace dlr {
 namespace ssm {
 namespace {
 
-constexpr int kWarps = 4;   // of a block at most; they meet once a tile
 constexpr int kHalf = kT / 2;
 
 template <typename T>
@@ -29,359 +30,416 @@ struct back_params {
   view<T> dx, ddt, dz, dBm, dCm;
   const float *states, *dh_last;
   float *dA, *dD, *ddt_bias, *dh0;
-  // parts: dBm and dCm [G, blocks, B, L, 2, NP] (NP = 4 LN), dA [B splits, H, N], dD and ddt_bias
+  // parts: dBm and dCm [G, blocks, B, L, 2, NP] (NP = 8 LN), dA [B splits, H, N], ddt_bias and dD
   // [2, B splits, H]
   float *part_bc, *part_A, *part_c;
 };
 
-template <typename T, int LN>
+// A unit's part of shared memory: what a tile's steps read and what they leave, two tiles in turn
+// (dBC three: the helpers of other units read it). MAP needs s, g and Cm alone.
+template <typename T, int LN, bool MAP>
 struct back_tile {
   using S = shape<T, LN>;
-  float s[kT][S::kCW], u[kT][S::kCW], g[kT][S::kCW];
-  float q[kT][S::kCW], e[kT][S::kCW], o[kT][S::kCW];
-  float Bm[kT][S::kNP], Cm[kT][S::kNP];
-  float dBC[2][kT][2][S::kNP];  // two tiles in turn
+  static constexpr int kN = MAP ? 1 : 2, kSteps = MAP ? 1 : kT;
+  float s[2][kT][S::kCW], g[2][kT][S::kCW];
+  float u[2][kT][S::kCW];  // the inputs; q takes a step's place once it is gone through
+  float Bm[kN][kSteps][S::kNP], Cm[2][kT][S::kNP];
+  float h[kN][MAP ? 1 : S::kCW][S::kNP];
+  float e[kN][kSteps][S::kCW], o[kN][kSteps][S::kCW];
+  float dBC[MAP ? 1 : 3][kSteps][2][S::kNP];
   float bias[S::kCW], D[S::kCW];
 };
 
 template <bool PRECISE>
-__device__ __forceinline__ void advance(float2 (&h)[kChannels][2],
-                                        const float2 (&rate)[kChannels][2], const float (&s)[4],
-                                        const float (&u)[4], const float2 (&bp)[2]) {
+__device__ __forceinline__ void advance(float2 (&h)[kChannels][kPairs],
+                                        const float2 (&rate)[kChannels][kPairs],
+                                        const float (&s)[kChannels], const float (&u)[kChannels],
+                                        const float2 (&bp)[kPairs]) {
 #pragma unroll
   for (int i = 0; i < kChannels; ++i)
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const decay<PRECISE> a(mul2(rate[i][p], two(s[i])));
+    for (int p = 0; p < kPairs; ++p) {
+      const decay<PRECISE> a(rate[i][p], two(s[i]));
       h[i][p] = a.of_plus(h[i][p], mul2(bp[p], two(u[i])));
     }
 }
 
-__device__ __forceinline__ void clear(float2 (&h)[kChannels][2]) {
-#pragma unroll
-  for (int i = 0; i < kChannels; ++i) h[i][0] = h[i][1] = two(0.0f);
-}
-
-__device__ __forceinline__ void get4(float (&v)[4], const float* p) { load_floats<4>(v, p); }
-__device__ __forceinline__ void get4(float2 (&v)[2], const float* p) {
-  const float4 t = *reinterpret_cast<const float4*>(p);
-  v[0] = make_float2(t.x, t.y);
-  v[1] = make_float2(t.z, t.w);
-}
-
 // MAP: only the gradient that each split but the first sends on, and the sum of its steps.
 template <typename T, int LN, bool MAP>
-__global__ void __launch_bounds__(32 * kWarps) back_kernel(back_params<T> q) {
+__global__ void __launch_bounds__(64 * kUnits, 1) back_kernel(back_params<T> q) {
   using S = shape<T, LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
   constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  back_tile<T, LN>* all = reinterpret_cast<back_tile<T, LN>*>(smem);
-  back_tile<T, LN>& m = all[warp];
+  using tile_t = back_tile<T, LN, MAP>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp % kUnits;
+  tile_t* all = reinterpret_cast<tile_t*>(smem);
+  tile_t& m = all[pair];
 
-  // a block: `warps` neighbouring warps of one group, split and batch entry
+  // a block: kUnits neighbouring units of one group, split and batch entry (all of them run, also
+  // those without channels, for the helpers' meetings)
   const int per_row = in.blocks * in.G, n_split = MAP ? in.splits - 1 : in.splits;
-  const int cb = (int)(blockIdx.x % per_row);
-  const int split = (int)(blockIdx.x / per_row % n_split) + (MAP ? 1 : 0);
-  const int64_t b = blockIdx.x / per_row / n_split;
-  const int group = cb / in.blocks, block = cb % in.blocks;
-  const int first = (block * warps + warp) * S::kCW;
-  const int c0 = group * in.Hg + first, n_ch = max(0, min(S::kCW, in.Hg - first));
-  const int at = lane % LN, cg = lane / LN, cl = cg * kChannels, n0 = at * kStates;
-  const int my_ch = n_ch - cl;
+  const int cb = (int)(blockIdx.x % per_row), block = cb % in.blocks;
+  unit<T, LN> u;
+  u.split = (int)(blockIdx.x / per_row % n_split) + (MAP ? 1 : 0);
+  u.b = blockIdx.x / per_row / n_split;
+  u.place(in, cb / in.blocks, (block * kUnits + pair) * S::kCW);
+  u.whole = u.whole && u.pieces(q.dy);
+  const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
+  const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  const bool full = n_ch == S::kCW;
-  const bool whole = full && pieces(in.x, c0, VE * sizeof(T)) &&
-                     pieces(in.dt, c0, VE * sizeof(T)) && pieces(q.dy, c0, VE * sizeof(T));
-  const bool whole_z = in.z.p && full && pieces(in.z, c0, VE * sizeof(T));
-  const bool whole_o = full && pieces(q.dx, c0, VE * sizeof(T)) &&
-                       pieces(q.ddt, c0, VE * sizeof(T)) &&
-                       (!in.z.p || pieces(q.dz, c0, VE * sizeof(T)));
-  const bool whole_b = in.N % VB == 0 && pieces(in.Bm, (int64_t)group * in.N, VB * sizeof(T)) &&
-                       pieces(in.Cm, (int64_t)group * in.N, VB * sizeof(T));
-
-  for (int c = lane; c < S::kCW; c += 32) {
-    m.bias[c] = in.bias && c < n_ch ? in.bias[c0 + c] : 0.0f;
-    m.D[c] = in.D && c < n_ch ? in.D[c0 + c] : 0.0f;
-  }
-  float2 rate[kChannels][2], carry[kChannels][2], dA[kChannels][2];
-  load_rates(rate, in.A, in.N, c0 + cl, my_ch, n0);
-  clear(dA);
-  const int64_t HN = (int64_t)in.H * in.N, ch = (int64_t)(c0 + cl) * in.N;
-  const int64_t row_map = b * in.splits + split;
-  if (MAP)
-    clear(carry);
-  else if (split == in.splits - 1)
-    load_states(carry, q.dh_last ? q.dh_last + b * HN + ch : nullptr, in.N, my_ch, n0);
-  else
-    load_states(carry, in.ends + (row_map + 1) * HN + ch, in.N, my_ch, n0);
-  float sum[kChannels] = {};
-  float sum_c[(S::kCW + 31) / 32][2] = {};  // of channel lane + 32 k: ddt and g x
-  bool cut = false;
-  __syncwarp();
-
-  const int t_first = split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
-  for (int tile = t_end - 1; tile >= t_first; --tile) {
-    const int64_t t0 = (int64_t)tile * kT;
-    const uint32_t mark = marks(in.reset, b, t0, in.L, lane);
-#pragma unroll
-    for (int k = 0; k < S::NV; ++k) {
-      const int p = k * 32 + lane, t = p / S::kRow, c = p % S::kRow * VE;
-      if (t >= kT) break;
-      float xv[VE], dv[VE], gv[VE], zv[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) xv[i] = dv[i] = gv[i] = zv[i] = 0.0f;
-      const bool there = t0 + t < in.L && c < n_ch;
-      if (there) {
-        words<T, VE> w;
-        get_piece<T, VE>(w, in.x.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-        w.to(xv);
-        get_piece<T, VE>(w, in.dt.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-        w.to(dv);
-        get_piece<T, VE>(w, q.dy.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-        w.to(gv);
-        if (in.z.p) {
-          get_piece<T, VE>(w, in.z.row(b, t0 + t) + c0 + c, n_ch - c, whole_z);
-          w.to(zv);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const bool ok = there && c + i < n_ch;
-        float sig, s = dv[i] + m.bias[c + i];
-        if (in.softplus) s = softplus(s, sig);
-        m.s[t][c + i] = ok ? s : 0.0f;
-        m.u[t][c + i] = ok ? s * xv[i] : 0.0f;
-        const float gate = in.z.p ? zv[i] * glr::sigmoid(zv[i]) : 1.0f;
-        m.g[t][c + i] = ok ? gv[i] * gate : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < S::NB; ++k) {
-      const int p = k * 32 + lane, t = p / S::kRowB, n = p % S::kRowB * VB;
-      if (t >= kT) break;
-      float bv[VB], cv[VB];
-#pragma unroll
-      for (int i = 0; i < VB; ++i) bv[i] = cv[i] = 0.0f;
-      if (t0 + t < in.L && n < in.N) {
-        words<T, VB> w;
-        const int64_t o = (int64_t)group * in.N + n;
-        get_piece<T, VB>(w, in.Bm.row(b, t0 + t) + o, in.N - n, whole_b);
-        w.to(bv);
-        get_piece<T, VB>(w, in.Cm.row(b, t0 + t) + o, in.N - n, whole_b);
-        w.to(cv);
-      }
-#pragma unroll
-      for (int i = 0; i < VB; ++i) {
-        m.Bm[t][n + i] = bv[i];
-        m.Cm[t][n + i] = cv[i];
-      }
+  if (warp >= kUnits) {
+    const bool full = u.n_ch == S::kCW;
+    const bool ok_z = full && u.pieces(in.z);
+    const bool ok_o = full && u.pieces(q.dx) && u.pieces(q.ddt) && u.pieces(q.dz);
+    for (int c = lane; c < S::kCW; c += 32) {
+      m.bias[c] = in.bias && c < u.n_ch ? in.bias[u.c0 + c] : 0.0f;
+      m.D[c] = in.D && c < u.n_ch ? in.D[u.c0 + c] : 0.0f;
     }
     __syncwarp();
-
-    if constexpr (MAP) {
-#pragma unroll 4
-      for (int t = kT - 1; t >= 0; --t) {
-        float s[4], g[4];
-        float2 cp[2];
-        get4(s, &m.s[t][cl]);
-        get4(g, &m.g[t][cl]);
-        get4(cp, &m.Cm[t][n0]);
+    // what is staged next, and what is finished next: each read a tile before its use
+    words<T, VE> wx[S::NV], wd[S::NV], wy[S::NV], wz[S::NV];
+    words<T, VE> fx[S::NV], fd[S::NV], fy[S::NV], fz[S::NV];
+    words<T, VB> wb[S::NB], wc[S::NB];
+    // a tile's first states: quads of the unit's kCW x NP, 4 to a lane
+    float4 first[4];
+    const bool quads = in.N % 4 == 0 && (reinterpret_cast<uintptr_t>(q.states) & 15) == 0;
+    auto fetch = [&](int tile) {
+      const int64_t t0 = (int64_t)tile * kT;
+      if (!MAP) u.fetch(wx, in.x, t0, in.L, lane, u.whole);
+      u.fetch(wd, in.dt, t0, in.L, lane, u.whole);
+      u.fetch(wy, q.dy, t0, in.L, lane, u.whole);
+      if (in.z.p) u.fetch(wz, in.z, t0, in.L, lane, ok_z);
+      u.fetch_b(wc, in.Cm, t0, in.L, in.N, lane);
+      if constexpr (!MAP) {
+        u.fetch_b(wb, in.Bm, t0, in.L, in.N, lane);
+        const float* src = q.states + (u.b * in.tiles + tile) * HN + (int64_t)u.c0 * in.N;
 #pragma unroll
-        for (int i = 0; i < kChannels; ++i) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const decay<kPrecise> a(mul2(rate[i][p], two(s[i])));
-            carry[i][p] = a.of(fma2(cp[p], two(g[i]), carry[i][p]));
+        for (int k = 0; k < 4; ++k) {
+          const int i = (k * 32 + lane) * 4, c = i / S::kNP, n = i % S::kNP;
+          first[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (c >= u.n_ch || n >= in.N) continue;
+          const float* p = src + (int64_t)c * in.N + n;
+          if (quads) {
+            first[k] = *reinterpret_cast<const float4*>(p);
+          } else {
+            first[k].x = p[0];
+            if (n + 1 < in.N) first[k].y = p[1];
+            if (n + 2 < in.N) first[k].z = p[2];
+            if (n + 3 < in.N) first[k].w = p[3];
           }
-          sum[i] += s[i];
-        }
-        if (mark >> t & 1) {
-          clear(carry);
-          cut = true;
         }
       }
-      __syncwarp();
-    } else {
-      const float* start = q.states + (b * in.tiles + tile) * HN + ch;
-      float (*dBC)[2][S::kNP] = m.dBC[tile & 1];
-#pragma unroll 1
-      for (int half = 1; half >= 0; --half) {
-        float2 h[kChannels][2], hist[kHalf][kChannels][2];
-        load_states(h, start, in.N, my_ch, n0);
-        if (half)
-#pragma unroll 2
-          for (int t = 0; t < kHalf; ++t) {
-            float s[4], u[4];
-            float2 bp[2];
-            get4(s, &m.s[t][cl]);
-            get4(u, &m.u[t][cl]);
-            get4(bp, &m.Bm[t][n0]);
-            if (mark >> t & 1) clear(h);
-            advance<kPrecise>(h, rate, s, u, bp);
-          }
-        const int first_t = half * kHalf;
-#pragma unroll
-        for (int k = 0; k < kHalf; ++k) {
-          const int t = first_t + k;
-          float s[4], u[4], g[4];
-          float2 bp[2], cp[2];
-          get4(s, &m.s[t][cl]);
-          get4(u, &m.u[t][cl]);
-          get4(g, &m.g[t][cl]);
-          get4(bp, &m.Bm[t][n0]);
-          get4(cp, &m.Cm[t][n0]);
-          if (mark >> t & 1) clear(h);
-#pragma unroll
-          for (int i = 0; i < kChannels; ++i) hist[k][i][0] = h[i][0], hist[k][i][1] = h[i][1];
-          advance<kPrecise>(h, rate, s, u, bp);
-          float2 dc[2] = {two(0.0f), two(0.0f)};
-#pragma unroll
-          for (int i = 0; i < kChannels; ++i)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) dc[p] = fma2(h[i][p], two(g[i]), dc[p]);
-          float v[4] = {dc[0].x, dc[0].y, dc[1].x, dc[1].y};
-          sum4<LN, CL>(v, cg);
-          put4<CL>(&dBC[t][1][n0], v, cg);
-          if (in.z.p) {
-            float o[4];
-#pragma unroll
-            for (int i = 0; i < kChannels; ++i) {
-              const float2 acc = fma2(h[i][1], cp[1], mul2(h[i][0], cp[0]));
-              o[i] = acc.x + acc.y;
-            }
-            sum4<1, LN>(o, at);
-            put4<LN>(&m.o[t][cl], o, at);
-          }
-        }
-#pragma unroll
-        for (int k = kHalf - 1; k >= 0; --k) {
-          const int t = first_t + k;
-          float s[4], u[4], g[4], qv[4], ev[4];
-          float2 bp[2], cp[2], db[2] = {two(0.0f), two(0.0f)};
-          get4(s, &m.s[t][cl]);
-          get4(u, &m.u[t][cl]);
-          get4(g, &m.g[t][cl]);
-          get4(bp, &m.Bm[t][n0]);
-          get4(cp, &m.Cm[t][n0]);
-          const bool stop = mark >> t & 1;
-#pragma unroll
-          for (int i = 0; i < kChannels; ++i) {
-            float2 qs = two(0.0f), es = two(0.0f);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const float2 G = fma2(cp[p], two(g[i]), carry[i][p]);
-              qs = fma2(G, bp[p], qs);
-              db[p] = fma2(G, two(u[i]), db[p]);
-              const decay<kPrecise> a(mul2(rate[i][p], two(s[i])));
-              float2 c = a.of(G);
-              if (stop) c = two(0.0f);
-              carry[i][p] = c;
-              const float2 r = mul2(c, hist[k][i][p]);
-              es = fma2(r, rate[i][p], es);
-              dA[i][p] = fma2(r, two(s[i]), dA[i][p]);
-            }
-            qv[i] = qs.x + qs.y;
-            ev[i] = es.x + es.y;
-          }
-          sum4<1, LN>(qv, at);
-          put4<LN>(&m.q[t][cl], qv, at);
-          sum4<1, LN>(ev, at);
-          put4<LN>(&m.e[t][cl], ev, at);
-          float v[4] = {db[0].x, db[0].y, db[1].x, db[1].y};
-          sum4<LN, CL>(v, cg);
-          put4<CL>(&dBC[t][0][n0], v, cg);
-        }
-      }
-      __syncwarp();
-      // what the channels' gradients take besides, by pieces of rows
+    };
+    auto stage = [&](int tile) {
+      const int64_t t0 = (int64_t)tile * kT;
+      const int j = tile & 1;
+      stage_steps<T, LN>(u, in.softplus, t0, in.L, lane, m.bias, MAP ? wd : wx, wd, m.s[j], m.u[j]);
+      u.put_b(m.Cm[j], wc, lane);
 #pragma unroll
       for (int k = 0; k < S::NV; ++k) {
-        const int p = k * 32 + lane, t = p / S::kRow, c = p % S::kRow * VE;
-        if (t >= kT) break;
-        const bool there = t0 + t < in.L && c < n_ch;
-        if (there) {
-          float xv[VE], dv[VE], dxv[VE];
-          words<T, VE> w;
-          get_piece<T, VE>(w, in.x.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-          w.to(xv);
-          get_piece<T, VE>(w, in.dt.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-          w.to(dv);
+        int t, c;
+        if (!u.piece(k, lane, t, c)) break;
+        float yv[VE], zv[VE];
+        wy[k].to(yv);  // zeros where there is no channel or step
+        if (in.z.p) {
+          wz[k].to(zv);
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) {
+            const float2 z = make_float2(zv[i], zv[i + 1]), g = mul2(z, glr::sigmoid2(z));
+            yv[i] *= g.x, yv[i + 1] *= g.y;
+          }
+        }
+        store_floats<VE>(&m.g[j][t][c], yv);
+      }
+      if constexpr (!MAP) {
+        u.put_b(m.Bm[j], wb, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float4*>(&m.h[j][0][0] + (k * 32 + lane) * 4) = first[k];
+      }
+    };
+    auto fetch_rest = [&](int tile) {
+      const int64_t t0 = (int64_t)tile * kT;
+      u.fetch(fx, in.x, t0, in.L, lane, u.whole);
+      u.fetch(fd, in.dt, t0, in.L, lane, u.whole);
+      if (in.z.p) {
+        u.fetch(fy, q.dy, t0, in.L, lane, u.whole);
+        u.fetch(fz, in.z, t0, in.L, lane, ok_z);
+      }
+    };
+    // of this lane's channels (the same in all its pieces): ddt and g x summed over time
+    float sum_t[VE], sum_x[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) sum_t[i] = sum_x[i] = 0.0f;
+    // what the channels' gradients take besides, by pieces of rows, and the units' dBm and dCm
+    auto finish = [&](int tile) {
+      const int64_t t0 = (int64_t)tile * kT;
+      const int j = tile & 1;
+      meet_helpers();
+      if constexpr (!MAP) {
+        constexpr int pitch = 2 * S::kNP, quarter = kT * pitch / kUnits;
+        float* part = q.part_bc +
+                      ((((int64_t)u.group * in.blocks + block) * in.B + u.b) * in.L + t0) * pitch;
+#pragma unroll
+        for (int k = 0; k < (quarter + 127) / 128; ++k) {
+          const int i = pair * quarter + (k * 32 + lane) * 4;
+          if (quarter % 128 && (k * 32 + lane) * 4 >= quarter) break;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < kUnits; ++w) {
+            const float4 p =
+                *reinterpret_cast<const float4*>(&all[w].dBC[tile % 3][0][0][0] + i);
+            v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+          }
+          if (t0 + i / pitch < in.L) *reinterpret_cast<float4*>(part + i) = v;
+        }
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+          int t, c;
+          if (!u.piece(k, lane, t, c)) break;
+          if (t0 + t >= in.L || c >= u.n_ch) continue;
+          float xv[VE], dv[VE], dxv[VE], bv[VE], Dv[VE], qv[VE], ev[VE], gv[VE], sv[VE];
+          fx[k].to(xv);
+          fd[k].to(dv);
+          load_floats<VE>(bv, m.bias + c);
+          load_floats<VE>(Dv, m.D + c);
+          load_floats<VE>(qv, &m.u[j][t][c]);
+          load_floats<VE>(ev, &m.e[j][t][c]);
+          load_floats<VE>(gv, &m.g[j][t][c]);
+          load_floats<VE>(sv, &m.s[j][t][c]);
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
-            const float qv = m.q[t][c + i], g = m.g[t][c + i];
-            float sig = 1.0f, s = dv[i] + m.bias[c + i];
-            if (in.softplus) s = softplus(s, sig);
+            const bool ok = c + i < u.n_ch;
+            dxv[i] = fmaf(sv[i], qv[i], Dv[i] * gv[i]);
             // e was summed with the rates in powers of two
-            const float slope = m.e[t][c + i] * (1.0f / kLog2e);
-            dxv[i] = fmaf(s, qv, m.D[c + i] * g);
-            dv[i] = fmaf(xv[i], qv, slope) * sig;
-            m.q[t][c + i] = c + i < n_ch ? dv[i] : 0.0f;
-            m.e[t][c + i] = c + i < n_ch ? g * xv[i] : 0.0f;
+            float d = fmaf(xv[i], qv[i], ev[i] * (1.0f / kLog2e));
+            if (in.softplus) d *= glr::sigmoid(dv[i] + bv[i]);
+            dv[i] = d;
+            sum_t[i] += ok ? d : 0.0f;
+            sum_x[i] += ok ? gv[i] * xv[i] : 0.0f;
           }
-          put_piece<T, VE>(q.dx.row(b, t0 + t) + c0 + c, dxv, n_ch - c, whole_o);
-          put_piece<T, VE>(q.ddt.row(b, t0 + t) + c0 + c, dv, n_ch - c, whole_o);
+          put_piece<T, VE>(q.dx.row(u.b, t0 + t) + u.c0 + c, dxv, u.n_ch - c, ok_o);
+          put_piece<T, VE>(q.ddt.row(u.b, t0 + t) + u.c0 + c, dv, u.n_ch - c, ok_o);
           if (in.z.p) {
             float zv[VE], yv[VE];
-            get_piece<T, VE>(w, in.z.row(b, t0 + t) + c0 + c, n_ch - c, whole_z);
-            w.to(zv);
-            get_piece<T, VE>(w, q.dy.row(b, t0 + t) + c0 + c, n_ch - c, whole);
-            w.to(yv);
+            fz[k].to(zv);
+            fy[k].to(yv);
+            load_floats<VE>(ev, &m.o[j][t][c]);
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
               const float sig = glr::sigmoid(zv[i]);
-              const float o = fmaf(m.D[c + i], xv[i], m.o[t][c + i]);
-              yv[i] *= o * fmaf(zv[i] * sig, 1.0f - sig, sig);
+              yv[i] *= fmaf(Dv[i], xv[i], ev[i]) * fmaf(zv[i] * sig, 1.0f - sig, sig);
             }
-            put_piece<T, VE>(q.dz.row(b, t0 + t) + c0 + c, yv, n_ch - c, whole_o);
+            put_piece<T, VE>(q.dz.row(u.b, t0 + t) + u.c0 + c, yv, u.n_ch - c, ok_o);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < VE; ++i) m.q[t][c + i] = m.e[t][c + i] = 0.0f;
         }
       }
-      __syncwarp();
+    };
+    fetch(t_end - 1);
+    stage(t_end - 1);
+    if (t_end - 2 >= t_first) fetch(t_end - 2);
+    meet_pair(pair);
+    for (int tile = t_end - 1; tile >= t_first; --tile) {
+      if (!MAP && tile < t_end - 1) finish(tile + 1);  // reads the stage that the next one takes
+      if (tile - 1 >= t_first) stage(tile - 1);
+      if (tile - 2 >= t_first) fetch(tile - 2);
+      if constexpr (!MAP) fetch_rest(tile);
+      meet_pair(pair);
+    }
+    if constexpr (!MAP) {
+      finish(t_first);
 #pragma unroll
-      for (int k = 0; k < (S::kCW + 31) / 32; ++k) {
-        const int c = lane + 32 * k;
-        if (c < S::kCW)
-          for (int t = 0; t < kT; ++t) {
-            sum_c[k][0] += m.q[t][c];
-            sum_c[k][1] += m.e[t][c];
+      for (int i = 0; i < VE; ++i)
+#pragma unroll
+        for (int d = S::kRow; d < 32; d *= 2) {
+          sum_t[i] += __shfl_xor_sync(0xffffffffu, sum_t[i], d);
+          sum_x[i] += __shfl_xor_sync(0xffffffffu, sum_x[i], d);
+        }
+      const int c = lane * VE;
+      if (lane < S::kRow) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (c + i < u.n_ch) {
+            float* p = q.part_c + row_map * in.H + u.c0 + c + i;
+            p[0] = sum_t[i];
+            p[in.B * in.splits * in.H] = sum_x[i];
           }
       }
-      // the warps' sums over their channels
-      __syncthreads();
-      const int64_t pitch = 2 * S::kNP;
-      float* part = q.part_bc + (((int64_t)group * in.blocks + block) * in.B + b) * in.L * pitch;
-      for (int i = threadIdx.x; i < kT * pitch; i += blockDim.x) {
-        const int t = i / pitch;
-        float v = 0.0f;
-        for (int w = 0; w < warps; ++w) v += (&all[w].dBC[tile & 1][0][0][0])[i];
-        if (t0 + t < in.L) part[t0 * pitch + i] = v;
-      }
     }
+    return;
   }
+
+  // the recurrence: this lane's channels and states
+  const int at = lane / CL, cg = lane % CL, cl = cg * kChannels, n0 = at * kStates;
+  const int my_ch = u.n_ch - cl;
+  const int64_t ch = (int64_t)(u.c0 + cl) * in.N;
+  float2 rate[kChannels][kPairs], carry[kChannels][kPairs];
+  load_rates(rate, in.A, in.N, u.c0 + cl, my_ch, n0);
+  if (MAP || (u.split == in.splits - 1 && !q.dh_last))
+    clear(carry);
+  else if (u.split == in.splits - 1)
+    load_states(carry, q.dh_last + u.b * HN + ch, in.N, my_ch, n0);
+  else
+    load_states(carry, in.ends + (row_map + 1) * HN + ch, in.N, my_ch, n0);
+  meet_pair(pair);
+
   if constexpr (MAP) {
+    float sum[kChannels] = {};
+    bool cut = false;
+    for (int tile = t_end - 1; tile >= t_first; --tile) {
+      const uint32_t mark = marks(in.reset, u.b, (int64_t)tile * kT, in.L, lane);
+      const int j = tile & 1;
+      auto steps = [&](auto marks_here) {
+        constexpr bool MARKS = decltype(marks_here)::value;
+#pragma unroll 4
+        for (int t = kT - 1; t >= 0; --t) {
+          float s[kChannels], g[kChannels];
+          float2 cp[kPairs];
+          get_channels(s, &m.s[j][t][cl]);
+          get_channels(g, &m.g[j][t][cl]);
+          get_map(cp, &m.Cm[j][t][n0]);
+#pragma unroll
+          for (int i = 0; i < kChannels; ++i) {
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+              const decay<kPrecise> a(rate[i][p], two(s[i]));
+              carry[i][p] = a.of(fma2(cp[p], two(g[i]), carry[i][p]));
+            }
+            sum[i] += s[i];
+          }
+          if (MARKS && (mark >> t & 1)) clear(carry);
+        }
+      };
+      if (mark) {
+        steps(std::true_type{});
+        cut = true;
+      } else {
+        steps(std::false_type{});
+      }
+      meet_pair(pair);
+    }
     store_states(in.ends + row_map * HN + ch, carry, in.N, my_ch, n0);
     if (at == 0)
 #pragma unroll
       for (int i = 0; i < kChannels; ++i)
         if (i < my_ch)
-          in.sums[row_map * in.H + c0 + cl + i] = cut ? __int_as_float(0x7fffffff) : sum[i];
+          in.sums[row_map * in.H + u.c0 + cl + i] = cut ? __int_as_float(0x7fffffff) : sum[i];
   } else {
-    store_states(q.part_A + row_map * HN + ch, dA, in.N, my_ch, n0);
+    float2 dA[kChannels][kPairs];
+    clear(dA);
+    for (int tile = t_end - 1; tile >= t_first; --tile) {
+      const uint32_t mark = marks(in.reset, u.b, (int64_t)tile * kT, in.L, lane);
+      const int j = tile & 1;
+      float (*dBC)[2][S::kNP] = m.dBC[tile % 3];
+      // A tile without marks goes without looking for them: a branch would keep the steps apart that
+      // are to overlap.
+      auto steps = [&](auto marks_here) {
+        constexpr bool MARKS = decltype(marks_here)::value;
+#pragma unroll 1
+        for (int half = 1; half >= 0; --half) {
+          float2 h[kChannels][kPairs], hist[kHalf][kChannels][kPairs];
 #pragma unroll
-    for (int k = 0; k < (S::kCW + 31) / 32; ++k) {
-      const int c = lane + 32 * k;
-      if (c < n_ch) {
-        q.part_c[row_map * in.H + c0 + c] = sum_c[k][0];
-        q.part_c[((int64_t)in.B * in.splits + row_map) * in.H + c0 + c] = sum_c[k][1];
-      }
+          for (int i = 0; i < kChannels; ++i) get_map(h[i], &m.h[j][cl + i][n0]);
+          if (half)
+#pragma unroll 2
+            for (int t = 0; t < kHalf; ++t) {
+              float s[kChannels], x[kChannels];
+              float2 bp[kPairs];
+              get_channels(s, &m.s[j][t][cl]);
+              get_channels(x, &m.u[j][t][cl]);
+              get_map(bp, &m.Bm[j][t][n0]);
+              if (MARKS && (mark >> t & 1)) clear(h);
+              advance<kPrecise>(h, rate, s, x, bp);
+            }
+          const int t_half = half * kHalf;
+#pragma unroll
+          for (int k = 0; k < kHalf; ++k) {
+            const int t = t_half + k;
+            asm volatile("" ::: "memory");  // words read too far ahead cost registers
+            float s[kChannels], x[kChannels], g[kChannels];
+            float2 bp[kPairs];
+            get_channels(s, &m.s[j][t][cl]);
+            get_channels(x, &m.u[j][t][cl]);
+            get_channels(g, &m.g[j][t][cl]);
+            get_map(bp, &m.Bm[j][t][n0]);
+            if (MARKS && (mark >> t & 1)) clear(h);
+#pragma unroll
+            for (int i = 0; i < kChannels; ++i)
+#pragma unroll
+              for (int p = 0; p < kPairs; ++p) hist[k][i][p] = h[i][p];
+            advance<kPrecise>(h, rate, s, x, bp);
+            float v[kStates];
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+              const float2 d = fma2(h[1][p], two(g[1]), mul2(h[0][p], two(g[0])));
+              v[2 * p] = d.x, v[2 * p + 1] = d.y;
+            }
+            sum_lanes<1, kStates, CL>(v, cg);
+            put_lanes<kStates, CL>(&dBC[t][1][n0], v, cg);
+            float2 cp[kPairs];
+            get_map(cp, &m.Cm[j][t][n0]);
+            float o[kChannels];
+#pragma unroll
+            for (int i = 0; i < kChannels; ++i) {
+              float2 acc = mul2(h[i][0], cp[0]);
+#pragma unroll
+              for (int p = 1; p < kPairs; ++p) acc = fma2(h[i][p], cp[p], acc);
+              o[i] = acc.x + acc.y;
+            }
+            sum_lanes<CL, kChannels, LN>(o, at);
+            put_lanes<kChannels, LN>(&m.o[j][t][cl], o, at);
+          }
+#pragma unroll
+          for (int k = kHalf - 1; k >= 0; --k) {
+            const int t = t_half + k;
+            asm volatile("" ::: "memory");  // words read too far ahead cost registers
+            float s[kChannels], x[kChannels], g[kChannels], qv[kChannels], ev[kChannels];
+            float2 bp[kPairs], cp[kPairs], db[kPairs];
+            get_channels(s, &m.s[j][t][cl]);
+            get_channels(x, &m.u[j][t][cl]);
+            get_channels(g, &m.g[j][t][cl]);
+            get_map(bp, &m.Bm[j][t][n0]);
+            get_map(cp, &m.Cm[j][t][n0]);
+#pragma unroll
+            for (int i = 0; i < kChannels; ++i) {
+              float2 qs, es;
+#pragma unroll
+              for (int p = 0; p < kPairs; ++p) {
+                const float2 G = fma2(cp[p], two(g[i]), carry[i][p]);
+                qs = p ? fma2(G, bp[p], qs) : mul2(G, bp[p]);
+                db[p] = i ? fma2(G, two(x[i]), db[p]) : mul2(G, two(x[i]));
+                const decay<kPrecise> a(rate[i][p], two(s[i]));
+                const float2 c = a.of(G), r = mul2(c, hist[k][i][p]);
+                carry[i][p] = c;
+                es = p ? fma2(r, rate[i][p], es) : mul2(r, rate[i][p]);
+                dA[i][p] = fma2(r, two(s[i]), dA[i][p]);
+              }
+              qv[i] = qs.x + qs.y;
+              ev[i] = es.x + es.y;
+            }
+            if (MARKS && (mark >> t & 1)) clear(carry);
+            sum_lanes<CL, kChannels, LN>(qv, at);
+            put_lanes<kChannels, LN>(&m.u[j][t][cl], qv, at);
+            sum_lanes<CL, kChannels, LN>(ev, at);
+            put_lanes<kChannels, LN>(&m.e[j][t][cl], ev, at);
+            float v[kStates];
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) v[2 * p] = db[p].x, v[2 * p + 1] = db[p].y;
+            sum_lanes<1, kStates, CL>(v, cg);
+            put_lanes<kStates, CL>(&dBC[t][0][n0], v, cg);
+          }
+        }
+      };
+      if (mark)
+        steps(std::true_type{});
+      else
+        steps(std::false_type{});
+      meet_pair(pair);
     }
-    if (split == 0 && q.dh0) store_states(q.dh0 + b * HN + ch, carry, in.N, my_ch, n0);
+    store_states(q.part_A + row_map * HN + ch, dA, in.N, my_ch, n0);
+    if (u.split == 0 && q.dh0) store_states(q.dh0 + u.b * HN + ch, carry, in.N, my_ch, n0);
   }
 }
 
@@ -425,21 +483,20 @@ __global__ void sum_params(const float* part_A, const float* part_c, float* dA, 
 }
 
 struct back_plan {
-  int64_t warps, blocks, NP, splits;  // warps of a block, blocks of a group
-  int64_t bc, A, c, map;              // floats of the parts and the splits' maps
+  int64_t blocks, NP, splits;  // blocks of a group
+  int64_t bc, A, c, map;       // floats of the parts and the splits' maps
 };
 back_plan plan(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
   back_plan p;
-  const int64_t ln = lanes_for(N), cw = 128 / ln, units = (H / G + cw - 1) / cw;
-  p.warps = std::min<int64_t>(kWarps, units);
-  p.blocks = (units + p.warps - 1) / p.warps;
-  p.NP = 4 * ln;
+  const int64_t ln = lanes_for(N), cw = 64 / ln, units = (H / G + cw - 1) / cw;
+  p.blocks = (units + kUnits - 1) / kUnits;
+  p.NP = kStates * ln;
   const int64_t want = splits_for(B, L, H, N, G), tiles = (L + kT - 1) / kT;
   const int64_t per = (tiles + want - 1) / want;
   p.splits = (tiles + per - 1) / per;
   p.bc = G * p.blocks * B * L * 2 * p.NP;
-  p.A = B * p.splits * H * N;
-  p.c = 2 * B * p.splits * H;
+  p.A = (B * p.splits * H * N + 3) / 4 * 4;
+  p.c = (2 * B * p.splits * H + 3) / 4 * 4;
   p.map = map_floats(B, H, N, p.splits);
   return p;
 }
@@ -447,25 +504,22 @@ back_plan plan(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
 template <typename T, int LN>
 cudaError_t run_back(back_params<T> q, const back_plan& p, cudaStream_t s) {
   q.in.blocks = (int)p.blocks;
-  const int threads = 32 * (int)p.warps;
-  const size_t bytes = sizeof(back_tile<T, LN>) * (size_t)p.warps;
   const int64_t units = p.blocks * q.in.G * q.in.B;
   const int64_t HN = (int64_t)q.in.H * q.in.N;
   cudaError_t e;
   if (q.in.splits > 1) {
-    if ((e = max_smem_once<back_kernel<T, LN, true>>(sizeof(back_tile<T, LN>) * kWarps)) !=
-        cudaSuccess)
-      return e;
-    back_kernel<T, LN, true><<<(unsigned)(units * (q.in.splits - 1)), threads, bytes, s>>>(q);
+    constexpr size_t bytes = sizeof(back_tile<T, LN, true>) * kUnits;
+    if ((e = max_smem_once<back_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
+    back_kernel<T, LN, true><<<(unsigned)(units * (q.in.splits - 1)), 64 * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     join_splits<true><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
         q.in.A, q.dh_last, q.in.ends, q.in.sums, q.in.B, q.in.splits, HN, q.in.N);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = max_smem_once<back_kernel<T, LN, false>>(sizeof(back_tile<T, LN>) * kWarps)) !=
-      cudaSuccess)
-    return e;
-  back_kernel<T, LN, false><<<(unsigned)(units * q.in.splits), threads, bytes, s>>>(q);
+  constexpr size_t bytes = sizeof(back_tile<T, LN, false>) * kUnits;
+  static_assert(bytes <= 232448, "shared memory");
+  if ((e = max_smem_once<back_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
+  back_kernel<T, LN, false><<<(unsigned)(units * q.in.splits), 64 * kUnits, bytes, s>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t n = q.in.B * q.in.L * q.in.G * 2 * p.NP;
   sum_maps<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(q.part_bc, q.dBm, q.dCm, q.in.B, q.in.L,
@@ -496,8 +550,7 @@ cudaError_t back_of(const ssm_scan_backward_args& a, cudaStream_t s) {
     case 1: return run_back<T, 1>(q, p, s);
     case 2: return run_back<T, 2>(q, p, s);
     case 4: return run_back<T, 4>(q, p, s);
-    case 8: return run_back<T, 8>(q, p, s);
-    default: return run_back<T, 16>(q, p, s);
+    default: return run_back<T, 8>(q, p, s);
   }
 }
 
