@@ -10,9 +10,10 @@
 // are, each about 20 cycles an SM for a warp's step. With 4 x 4 it takes three exchanges for four
 // sums, with one channel and sixteen states twice the words.
 //
-// Two warps work on a unit of channels: one runs the recurrence, its helper stages what it reads and
-// finishes what it leaves, a tile of kT steps ahead and behind, so that neither the latency of memory
-// nor the elementwise work stands in the recurrence's way. Pairs meet once a tile.
+// Three warps work on a unit of channels: one runs the recurrence, one stages what it reads, a tile of
+// kT steps ahead, and one finishes what it leaves, a tile behind, so that neither the latency of
+// memory nor the elementwise work stands in the recurrence's way. They meet once a tile. With a
+// single helper for both B4 L4096 H4096 N16 bfloat16 took 574 us forwards: the helper was the slower.
 #pragma once
 
 #include "glr_common.cuh"
@@ -37,7 +38,6 @@ using glr::words;
 
 constexpr int kT = SSM_STATE_STEPS;  // steps of a tile
 constexpr int kStates = 8, kChannels = 2, kPairs = kStates / 2;
-constexpr int kUnits = 4;  // of a block: warps 0-3 run, warps 4-7 help
 
 // log1p(e) for e in [0, 1]: e P(e), P of degree 8 by a least-maximum fit of the relative error
 // (3e-8; 1.7e-7 with its roundings). The logarithm of the rounded 1 + e would lose 6e-5 of a step of
@@ -167,17 +167,21 @@ __device__ __forceinline__ void put_lanes(float* p, const float* v, int at) {
   } else if constexpr (COUNT == 2 * LANES) {
     *reinterpret_cast<float2*>(p + 2 * at) = make_float2(v[0], v[1]);
   } else {
-    static_assert(COUNT == 4 * LANES, "");
-    *reinterpret_cast<float4*>(p + 4 * at) = make_float4(v[0], v[1], v[2], v[3]);
+    static_assert(COUNT % (4 * LANES) == 0, "");
+#pragma unroll
+    for (int i = 0; i < COUNT / LANES; i += 4)
+      *reinterpret_cast<float4*>(p + COUNT / LANES * at + i) =
+          make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
   }
 }
 
-// A pair's two warps meet (barriers 1 .. kUnits), and the helpers of a block (barrier kUnits + 1).
-__device__ __forceinline__ void meet_pair(int pair) {
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+// The three warps of a unit meet (barriers 1 .. units), and the UNITS finishing warps of a block.
+__device__ __forceinline__ void meet_unit(int k) {
+  asm volatile("bar.sync %0, 96;" ::"r"(1 + k) : "memory");
 }
-__device__ __forceinline__ void meet_helpers() {
-  asm volatile("bar.sync %0, %1;" ::"n"(1 + kUnits), "n"(32 * kUnits) : "memory");
+template <int UNITS>
+__device__ __forceinline__ void meet_finishing() {
+  asm volatile("bar.sync %0, %1;" ::"n"(1 + UNITS), "n"(32 * UNITS) : "memory");
 }
 
 // How a unit's tile is cut into pieces of VE channels (and VB states) for a warp's lanes.

@@ -24,6 +24,8 @@ struct scan_params {
   float *h_last, *states;
 };
 
+constexpr int kUnits = 4;  // of a block: a warp of each kind on each quarter of an SM
+
 // A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
 // tiles in turn.
 template <typename T, int LN, bool MAP>
@@ -32,34 +34,89 @@ struct scan_tile {
   float s[2][kT][S::kCW], u[2][kT][S::kCW];
   float Bm[2][kT][S::kNP];
   float Cm[MAP ? 1 : 2][MAP ? 1 : kT][S::kNP];
-  float o[MAP ? 1 : 2][MAP ? 1 : kT][S::kCW];
-  float bias[S::kCW], D[S::kCW];
+  float o[MAP ? 1 : 2][MAP ? 1 : kT][LN][S::kCW];  // a channel's sum, in the parts of its lanes
+  float D[S::kCW];
 };
 
 // MAP: only the state that each split but the last adds, and the sum of its steps.
 template <typename T, int LN, bool MAP>
-__global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
+__global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) {
   using S = shape<T, LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
   constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp % kUnits;
-  scan_tile<T, LN, MAP>& m = reinterpret_cast<scan_tile<T, LN, MAP>*>(smem)[pair];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kUnits;
+  scan_tile<T, LN, MAP>& m = reinterpret_cast<scan_tile<T, LN, MAP>*>(smem)[mine];
   unit<T, LN> u;
-  if (!u.find(in, (int64_t)blockIdx.x * kUnits + pair, MAP ? in.splits - 1 : in.splits)) return;
+  if (!u.find(in, (int64_t)blockIdx.x * kUnits + mine, MAP ? in.splits - 1 : in.splits)) return;
   const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
   const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  if (warp >= kUnits) {
-    const bool ok_z = u.n_ch == S::kCW && u.pieces(in.z), ok_y = u.n_ch == S::kCW && u.pieces(q.y);
-    for (int c = lane; c < S::kCW; c += 32) {
-      m.bias[c] = in.bias && c < u.n_ch ? in.bias[u.c0 + c] : 0.0f;
-      m.D[c] = in.D && c < u.n_ch ? in.D[u.c0 + c] : 0.0f;
+  if (warp >= 2 * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate, and out
+    if constexpr (MAP) {
+      for (int tile = t_first; tile <= t_end; ++tile) meet_unit(mine);
+    } else {
+      const bool ok_z = u.n_ch == S::kCW && u.pieces(in.z);
+      const bool ok_y = u.n_ch == S::kCW && u.pieces(q.y);
+      for (int c = lane; c < S::kCW; c += 32)
+        m.D[c] = in.D && c < u.n_ch ? in.D[u.c0 + c] : 0.0f;
+      __syncwarp();
+      words<T, VE> wx[S::NV], wz[S::NV];  // read a tile before their use
+      auto fetch = [&](int tile) {
+        if (in.D) u.fetch(wx, in.x, (int64_t)tile * kT, in.L, lane, u.whole);
+        if (in.z.p) u.fetch(wz, in.z, (int64_t)tile * kT, in.L, lane, ok_z);
+      };
+      auto finish = [&](int tile) {
+        const int64_t t0 = (int64_t)tile * kT;
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+          int t, c;
+          if (!u.piece(k, lane, t, c)) break;
+          if (t0 + t >= in.L || c >= u.n_ch) continue;
+          float o[VE], v[VE];
+          load_floats<VE>(o, &m.o[tile & 1][t][0][c]);
+#pragma unroll
+          for (int l = 1; l < LN; ++l) {
+            load_floats<VE>(v, &m.o[tile & 1][t][l][c]);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) o[i] += v[i];
+          }
+          if (in.D) {
+            float d[VE];
+            wx[k].to(v);
+            load_floats<VE>(d, m.D + c);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) o[i] = fmaf(d[i], v[i], o[i]);
+          }
+          if (in.z.p) {
+            wz[k].to(v);
+#pragma unroll
+            for (int i = 0; i < VE; i += 2) {
+              const float2 z = make_float2(v[i], v[i + 1]), g = mul2(z, glr::sigmoid2(z));
+              o[i] *= g.x, o[i + 1] *= g.y;
+            }
+          }
+          put_piece<T, VE>(q.y.row(u.b, t0 + t) + u.c0 + c, o, u.n_ch - c, ok_y);
+        }
+      };
+      meet_unit(mine);
+      for (int tile = t_first; tile < t_end; ++tile) {
+        if (tile > t_first) finish(tile - 1);
+        fetch(tile);
+        meet_unit(mine);
+      }
+      finish(t_end - 1);
     }
-    __syncwarp();
-    // what is staged next, and what is finished next: each read a tile before its use
-    words<T, VE> wx[S::NV], wd[S::NV], fx[S::NV], fz[S::NV];
+    return;
+  }
+  if (warp >= kUnits) {  // stages
+    float bias[VE];
+    const int c_mine = lane % S::kRow * VE;
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      bias[i] = in.bias && c_mine + i < u.n_ch ? in.bias[u.c0 + c_mine + i] : 0.0f;
+    words<T, VE> wx[S::NV], wd[S::NV];  // read a tile before their use
     words<T, VB> wb[S::NB], wc[S::NB];
     auto fetch = [&](int tile) {
       const int64_t t0 = (int64_t)tile * kT;
@@ -69,55 +126,20 @@ __global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
       if (!MAP) u.fetch_b(wc, in.Cm, t0, in.L, in.N, lane);
     };
     auto stage = [&](int tile) {
-      stage_steps<T, LN>(u, in.softplus, (int64_t)tile * kT, in.L, lane, m.bias, wx, wd,
+      stage_steps<T, LN>(u, in.softplus, (int64_t)tile * kT, in.L, lane, bias, wx, wd,
                          m.s[tile & 1], m.u[tile & 1]);
       u.put_b(m.Bm[tile & 1], wb, lane);
       if constexpr (!MAP) u.put_b(m.Cm[tile & 1], wc, lane);
     };
-    auto fetch_rest = [&](int tile) {
-      if (in.D) u.fetch(fx, in.x, (int64_t)tile * kT, in.L, lane, u.whole);
-      if (in.z.p) u.fetch(fz, in.z, (int64_t)tile * kT, in.L, lane, ok_z);
-    };
-    auto finish = [&](int tile) {  // the skip, the gate, and out
-      const int64_t t0 = (int64_t)tile * kT;
-#pragma unroll
-      for (int k = 0; k < S::NV; ++k) {
-        int t, c;
-        if (!u.piece(k, lane, t, c)) break;
-        if (t0 + t >= in.L || c >= u.n_ch) continue;
-        float o[VE], v[VE], d[VE];
-        load_floats<VE>(o, &m.o[tile & 1][t][c]);
-        if (in.D) {
-          fx[k].to(v);
-          load_floats<VE>(d, m.D + c);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) o[i] = fmaf(d[i], v[i], o[i]);
-        }
-        if (in.z.p) {
-          fz[k].to(v);
-#pragma unroll
-          for (int i = 0; i < VE; i += 2) {
-            const float2 z = make_float2(v[i], v[i + 1]), g = mul2(z, glr::sigmoid2(z));
-            o[i] *= g.x, o[i + 1] *= g.y;
-          }
-        }
-        put_piece<T, VE>(q.y.row(u.b, t0 + t) + u.c0 + c, o, u.n_ch - c, ok_y);
-      }
-    };
     fetch(t_first);
     stage(t_first);
     if (t_first + 1 < t_end) fetch(t_first + 1);
-    meet_pair(pair);
+    meet_unit(mine);
     for (int tile = t_first; tile < t_end; ++tile) {
       if (tile + 1 < t_end) stage(tile + 1);
       if (tile + 2 < t_end) fetch(tile + 2);
-      if constexpr (!MAP) {
-        if (tile > t_first) finish(tile - 1);
-        fetch_rest(tile);
-      }
-      meet_pair(pair);
+      meet_unit(mine);
     }
-    if constexpr (!MAP) finish(t_end - 1);
     return;
   }
 
@@ -135,7 +157,7 @@ __global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
     load_states(h, in.ends + (row_map - 1) * HN + ch, in.N, my_ch, n0);
   float sum[kChannels] = {};
   bool cut = false;
-  meet_pair(pair);
+  meet_unit(mine);
   for (int tile = t_first; tile < t_end; ++tile) {
     const int64_t t0 = (int64_t)tile * kT;
     const uint32_t mark = marks(in.reset, u.b, t0, in.L, lane);
@@ -143,7 +165,7 @@ __global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
     const float (*mu)[S::kCW] = m.u[tile & 1];
     const float (*mb)[S::kNP] = m.Bm[tile & 1];
     const float (*mc)[S::kNP] = m.Cm[MAP ? 0 : tile & 1];
-    float (*mo)[S::kCW] = m.o[MAP ? 0 : tile & 1];
+    float (*mo)[LN][S::kCW] = m.o[MAP ? 0 : tile & 1];
     if (!MAP && q.states)
       store_states(q.states + (u.b * in.tiles + tile) * HN + ch, h, in.N, my_ch, n0);
     // A tile without marks goes without looking for them: a branch would keep the steps apart that
@@ -185,10 +207,7 @@ __global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
           if (!MAP) o[i] = acc.x + acc.y;
           if (MAP) sum[i] += s[i];
         }
-        if (!MAP) {
-          sum_lanes<CL, kChannels, LN>(o, at);
-          put_lanes<kChannels, LN>(&mo[t][cl], o, at);
-        }
+        if (!MAP) *reinterpret_cast<float2*>(&mo[t][at][cl]) = make_float2(o[0], o[1]);
       }
     };
     if (mark) {
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(64 * kUnits) scan_kernel(scan_params<T> q) {
     } else {
       steps(std::false_type{});
     }
-    meet_pair(pair);
+    meet_unit(mine);
   }
   if (MAP) {
     store_states(in.ends + row_map * HN + ch, h, in.N, my_ch, n0);
@@ -221,7 +240,7 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
   if (q.in.splits > 1) {
     constexpr size_t bytes = sizeof(scan_tile<T, LN, true>) * kUnits;
     if ((e = max_smem_once<scan_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
-    scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 64 * kUnits, bytes, s>>>(q);
+    scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 96 * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t HN = (int64_t)q.in.H * q.in.N;
     join_splits<false><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
@@ -230,7 +249,7 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
   }
   constexpr size_t bytes = sizeof(scan_tile<T, LN, false>) * kUnits;
   if ((e = max_smem_once<scan_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
-  scan_kernel<T, LN, false><<<grid(units * q.in.splits), 64 * kUnits, bytes, s>>>(q);
+  scan_kernel<T, LN, false><<<grid(units * q.in.splits), 96 * kUnits, bytes, s>>>(q);
   return cudaGetLastError();
 }
 

@@ -232,11 +232,12 @@ struct unit {
   }
 };
 
-// The steps s and the inputs s x of a tile's pieces: softplus, and zeros where there is no channel
+// The steps s and the inputs s x of a tile's pieces (`bias`: of the channels of this lane's pieces,
+// which are the same in all of them): softplus, and zeros where there is no channel
 // or step (which leave the state as it is).
 template <typename T, int LN>
 __device__ __forceinline__ void stage_steps(const unit<T, LN>& u, int softplus, int64_t t0, int64_t L,
-                                            int lane, const float* bias,
+                                            int lane, const float (&bias)[shape<T, LN>::VE],
                                             const words<T, shape<T, LN>::VE> (&wx)[shape<T, LN>::NV],
                                             const words<T, shape<T, LN>::VE> (&wd)[shape<T, LN>::NV],
                                             float (*s)[shape<T, LN>::kCW],
@@ -249,7 +250,8 @@ __device__ __forceinline__ void stage_steps(const unit<T, LN>& u, int softplus, 
     float xv[S::VE], dv[S::VE], bv[S::VE];
     wx[k].to(xv);
     wd[k].to(dv);
-    load_floats<S::VE>(bv, bias + c);
+#pragma unroll
+    for (int i = 0; i < S::VE; ++i) bv[i] = bias[i];
 #pragma unroll
     for (int i = 0; i < S::VE; i += 2) {
       float2 d = add2(make_float2(dv[i], dv[i + 1]), make_float2(bv[i], bv[i + 1]));
@@ -273,10 +275,10 @@ __device__ __forceinline__ void stage_steps(const unit<T, LN>& u, int softplus, 
 
 // How many splits a sequence is cut into. A unit goes through its rows step by step, so few channels
 // leave the GPU idle; rows are then cut, and the states at the cuts come from a pass over the steps
-// alone (about a third of the scan's time). Blocks of kUnits units go one to an SM; a split takes
-// two tiles more, to fill and to drain.
+// alone (about a third of the scan's time). Blocks of four units go one to an SM; a split takes two
+// tiles more, to fill and to drain.
 inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
-  constexpr int64_t kSMs = 152;
+  constexpr int64_t kSMs = 152, kUnits = 4;
   const int64_t cw = 64 / lanes_for(N), units = (H / G + cw - 1) / cw;
   const int64_t blocks = B * G * ((units + kUnits - 1) / kUnits), tiles = (L + kT - 1) / kT;
   if (const char* e = getenv("SSM_SPLITS")) return std::max(1, std::min<int>(atoi(e), tiles));
