@@ -1,19 +1,17 @@
 // ssm_common.cuh -- device helpers shared by the kernels behind include/ssm.h: the token's step, the
 // decays of a pair of states, pieces of activation rows, and sums over the lanes of a warp.
 //
-// The scan's layout, the same in all its kernels. A warp has 64 / LN channels of one batch entry, LN
-// lanes to a channel: a lane has kStates = 8 states of each of kChannels = 2 neighbouring channels,
-// sixteen numbers in registers, in pairs of neighbouring states. N <= 8 LN; missing states and
-// channels are zeros. A lane reads per step four 16-byte words of Bm and Cm, which the lanes beside
-// it share, and two 8-byte ones of its channels' steps and inputs, and a sum over the states takes
-// one exchange at N = 16: shared memory is then as busy as the multiply-adds and the exponentials
-// are, each about 20 cycles an SM for a warp's step. With 4 x 4 it takes three exchanges for four
-// sums, with one channel and sixteen states twice the words.
+// The scan's layout, the same in all its kernels. A unit is 64 / LN channels of one batch entry with
+// their N <= 8 LN states (missing states and channels are zeros): 512 numbers. Two warps run it, each
+// with one half of the states: LN lanes to a channel, a lane has kStates = 4 states of each of
+// kChannels = 2 neighbouring channels, eight numbers in registers, in pairs of neighbouring states. A
+// lane reads per step one 16-byte word of Bm and of Cm, which the lanes beside it share, and 8-byte
+// words of its channels' steps and inputs. One warp with sixteen numbers a lane reads a third less but
+// waits for itself: with it B4 L4096 H4096 N16 bfloat16 took 457 us forwards.
 //
-// Three warps work on a unit of channels: one runs the recurrence, one stages what it reads, a tile of
-// kT steps ahead, and one finishes what it leaves, a tile behind, so that neither the latency of
-// memory nor the elementwise work stands in the recurrence's way. They meet once a tile. With a
-// single helper for both B4 L4096 H4096 N16 bfloat16 took 574 us forwards: the helper was the slower.
+// Helpers stage what a unit reads, a tile of kT steps ahead, and finish what it leaves, a tile behind,
+// so that neither the latency of memory nor the elementwise work stands in the recurrence's way.
+// A unit's warps meet once a tile.
 #pragma once
 
 #include "glr_common.cuh"
@@ -37,7 +35,8 @@ using glr::view;
 using glr::words;
 
 constexpr int kT = SSM_STATE_STEPS;  // steps of a tile
-constexpr int kStates = 8, kChannels = 2, kPairs = kStates / 2;
+constexpr int kStates = 4, kChannels = 2, kPairs = kStates / 2;  // of a lane
+constexpr int kHalves = 2;  // warps that share a unit's states
 
 // log1p(e) for e in [0, 1]: e P(e), P of degree 8 by a least-maximum fit of the relative error
 // (3e-8; 1.7e-7 with its roundings). The logarithm of the rounded 1 + e would lose 6e-5 of a step of
@@ -175,9 +174,10 @@ __device__ __forceinline__ void put_lanes(float* p, const float* v, int at) {
   }
 }
 
-// The three warps of a unit meet (barriers 1 .. units), and the UNITS finishing warps of a block.
+// The WARPS warps of a unit meet (barriers 1 .. units), and the UNITS finishing warps of a block.
+template <int WARPS>
 __device__ __forceinline__ void meet_unit(int k) {
-  asm volatile("bar.sync %0, 96;" ::"r"(1 + k) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + k), "n"(32 * WARPS) : "memory");
 }
 template <int UNITS>
 __device__ __forceinline__ void meet_finishing() {
@@ -188,7 +188,7 @@ __device__ __forceinline__ void meet_finishing() {
 template <typename T, int LN>
 struct shape {
   static constexpr int kCW = 32 / LN * kChannels;  // channels of a unit
-  static constexpr int kNP = LN * kStates;         // states of a channel, with the missing ones
+  static constexpr int kNP = kHalves * LN * kStates;  // states of a channel, with the missing ones
   static constexpr int VE = 16 / (int)sizeof(T) < kCW ? 16 / (int)sizeof(T) : kCW;
   static constexpr int VB = 16 / (int)sizeof(T) < kNP ? 16 / (int)sizeof(T) : kNP;
   static constexpr int kRow = kCW / VE, kRowB = kNP / VB;  // pieces of a step

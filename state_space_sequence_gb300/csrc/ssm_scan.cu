@@ -24,7 +24,8 @@ struct scan_params {
   float *h_last, *states;
 };
 
-constexpr int kUnits = 4;  // of a block: a warp of each kind on each quarter of an SM
+constexpr int kUnits = 4;             // of a block: on each quarter of an SM two warps that run a unit,
+constexpr int kUnitWarps = kHalves + 2;  // one that stages and one that finishes
 
 // A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
 // tiles in turn.
@@ -34,13 +35,13 @@ struct scan_tile {
   float s[2][kT][S::kCW], u[2][kT][S::kCW];
   float Bm[2][kT][S::kNP];
   float Cm[MAP ? 1 : 2][MAP ? 1 : kT][S::kNP];
-  float o[MAP ? 1 : 2][MAP ? 1 : kT][LN][S::kCW];  // a channel's sum, in the parts of its lanes
+  float o[MAP ? 1 : 2][MAP ? 1 : kT][kHalves * LN][S::kCW];  // sums, in the parts of the lanes
   float D[S::kCW];
 };
 
 // MAP: only the state that each split but the last adds, and the sum of its steps.
 template <typename T, int LN, bool MAP>
-__global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) {
+__global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_params<T> q) {
   using S = shape<T, LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
   constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN;
@@ -53,9 +54,9 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
   const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
   const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  if (warp >= 2 * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate, and out
+  if (warp >= (kHalves + 1) * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate, and out
     if constexpr (MAP) {
-      for (int tile = t_first; tile <= t_end; ++tile) meet_unit(mine);
+      for (int tile = t_first; tile <= t_end; ++tile) meet_unit<kUnitWarps>(mine);
     } else {
       const bool ok_z = u.n_ch == S::kCW && u.pieces(in.z);
       const bool ok_y = u.n_ch == S::kCW && u.pieces(q.y);
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
           float o[VE], v[VE];
           load_floats<VE>(o, &m.o[tile & 1][t][0][c]);
 #pragma unroll
-          for (int l = 1; l < LN; ++l) {
+          for (int l = 1; l < kHalves * LN; ++l) {
             load_floats<VE>(v, &m.o[tile & 1][t][l][c]);
 #pragma unroll
             for (int i = 0; i < VE; ++i) o[i] += v[i];
@@ -100,17 +101,17 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
           put_piece<T, VE>(q.y.row(u.b, t0 + t) + u.c0 + c, o, u.n_ch - c, ok_y);
         }
       };
-      meet_unit(mine);
+      meet_unit<kUnitWarps>(mine);
       for (int tile = t_first; tile < t_end; ++tile) {
         if (tile > t_first) finish(tile - 1);
         fetch(tile);
-        meet_unit(mine);
+        meet_unit<kUnitWarps>(mine);
       }
       finish(t_end - 1);
     }
     return;
   }
-  if (warp >= kUnits) {  // stages
+  if (warp >= kHalves * kUnits) {  // stages
     float bias[VE];
     const int c_mine = lane % S::kRow * VE;
 #pragma unroll
@@ -134,17 +135,17 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
     fetch(t_first);
     stage(t_first);
     if (t_first + 1 < t_end) fetch(t_first + 1);
-    meet_unit(mine);
+    meet_unit<kUnitWarps>(mine);
     for (int tile = t_first; tile < t_end; ++tile) {
       if (tile + 1 < t_end) stage(tile + 1);
       if (tile + 2 < t_end) fetch(tile + 2);
-      meet_unit(mine);
+      meet_unit<kUnitWarps>(mine);
     }
     return;
   }
 
   // the recurrence: this lane's channels and states
-  const int at = lane / CL, cg = lane % CL, cl = cg * kChannels, n0 = at * kStates;
+  const int at = warp / kUnits * LN + lane / CL, cl = lane % CL * kChannels, n0 = at * kStates;
   const int my_ch = u.n_ch - cl;
   const int64_t ch = (int64_t)(u.c0 + cl) * in.N;
   float2 rate[kChannels][kPairs], h[kChannels][kPairs];
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
     load_states(h, in.ends + (row_map - 1) * HN + ch, in.N, my_ch, n0);
   float sum[kChannels] = {};
   bool cut = false;
-  meet_unit(mine);
+  meet_unit<kUnitWarps>(mine);
   for (int tile = t_first; tile < t_end; ++tile) {
     const int64_t t0 = (int64_t)tile * kT;
     const uint32_t mark = marks(in.reset, u.b, t0, in.L, lane);
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
     const float (*mu)[S::kCW] = m.u[tile & 1];
     const float (*mb)[S::kNP] = m.Bm[tile & 1];
     const float (*mc)[S::kNP] = m.Cm[MAP ? 0 : tile & 1];
-    float (*mo)[LN][S::kCW] = m.o[MAP ? 0 : tile & 1];
+    float (*mo)[kHalves * LN][S::kCW] = m.o[MAP ? 0 : tile & 1];
     if (!MAP && q.states)
       store_states(q.states + (u.b * in.tiles + tile) * HN + ch, h, in.N, my_ch, n0);
     // A tile without marks goes without looking for them: a branch would keep the steps apart that
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(96 * kUnits, 1) scan_kernel(scan_params<T> q) 
     } else {
       steps(std::false_type{});
     }
-    meet_unit(mine);
+    meet_unit<kUnitWarps>(mine);
   }
   if (MAP) {
     store_states(in.ends + row_map * HN + ch, h, in.N, my_ch, n0);
@@ -240,7 +241,7 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
   if (q.in.splits > 1) {
     constexpr size_t bytes = sizeof(scan_tile<T, LN, true>) * kUnits;
     if ((e = max_smem_once<scan_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
-    scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 96 * kUnits, bytes, s>>>(q);
+    scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t HN = (int64_t)q.in.H * q.in.N;
     join_splits<false><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
@@ -249,7 +250,7 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
   }
   constexpr size_t bytes = sizeof(scan_tile<T, LN, false>) * kUnits;
   if ((e = max_smem_once<scan_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
-  scan_kernel<T, LN, false><<<grid(units * q.in.splits), 96 * kUnits, bytes, s>>>(q);
+  scan_kernel<T, LN, false><<<grid(units * q.in.splits), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
   return cudaGetLastError();
 }
 

@@ -90,59 +90,52 @@ __device__ __forceinline__ void clear(float2 (&h)[kChannels][kPairs]) {
 }
 // A lane's states from an array [.., H, N] whose row of the lane's first channel begins at p, and
 // back.
+__device__ __forceinline__ float4 get_quad(const float* p, int n, int N, bool whole) {
+  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (n >= N) return t;
+  if (whole) return *reinterpret_cast<const float4*>(p + n);
+  t.x = p[n];
+  if (n + 1 < N) t.y = p[n + 1];
+  if (n + 2 < N) t.z = p[n + 2];
+  if (n + 3 < N) t.w = p[n + 3];
+  return t;
+}
+__device__ __forceinline__ bool quads(const float* p, int N) {
+  return (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
 __device__ __forceinline__ void load_states(float2 (&h)[kChannels][kPairs], const float* p, int N,
                                             int n_ch, int n0) {
+  const bool whole = quads(p, N);
 #pragma unroll
   for (int i = 0; i < kChannels; ++i) {
-    const float* q = p + (int64_t)i * N + n0;
-    const bool quads = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-#pragma unroll
-    for (int k = 0; k < kStates; k += 4) {
-      float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i < n_ch && n0 + k < N) {
-        if (quads) {
-          t = *reinterpret_cast<const float4*>(q + k);
-        } else {
-          t.x = q[k];
-          if (n0 + k + 1 < N) t.y = q[k + 1];
-          if (n0 + k + 2 < N) t.z = q[k + 2];
-          if (n0 + k + 3 < N) t.w = q[k + 3];
-        }
-      }
-      h[i][k / 2] = make_float2(t.x, t.y);
-      h[i][k / 2 + 1] = make_float2(t.z, t.w);
-    }
+    const float4 t = i < n_ch ? get_quad(p + (int64_t)i * N, n0, N, whole)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    h[i][0] = make_float2(t.x, t.y);
+    h[i][1] = make_float2(t.z, t.w);
   }
 }
 __device__ __forceinline__ void store_states(float* p, const float2 (&h)[kChannels][kPairs], int N,
                                              int n_ch, int n0) {
+  const bool whole = quads(p, N);
 #pragma unroll
   for (int i = 0; i < kChannels; ++i) {
+    if (i >= n_ch || n0 >= N) continue;
     float* q = p + (int64_t)i * N + n0;
-    const bool quads = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-#pragma unroll
-    for (int k = 0; k < kStates; k += 4) {
-      if (i >= n_ch || n0 + k >= N) continue;
-      const float2 a = h[i][k / 2], b = h[i][k / 2 + 1];
-      if (quads) {
-        *reinterpret_cast<float4*>(q + k) = make_float4(a.x, a.y, b.x, b.y);
-      } else {
-        q[k] = a.x;
-        if (n0 + k + 1 < N) q[k + 1] = a.y;
-        if (n0 + k + 2 < N) q[k + 2] = b.x;
-        if (n0 + k + 3 < N) q[k + 3] = b.y;
-      }
+    if (whole) {
+      *reinterpret_cast<float4*>(q) = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
+    } else {
+      q[0] = h[i][0].x;
+      if (n0 + 1 < N) q[1] = h[i][0].y;
+      if (n0 + 2 < N) q[2] = h[i][1].x;
+      if (n0 + 3 < N) q[3] = h[i][1].y;
     }
   }
 }
 // A lane's words of a step: its states' (of Bm or Cm), and its channels'.
 __device__ __forceinline__ void get_map(float2 (&v)[kPairs], const float* p) {
-#pragma unroll
-  for (int k = 0; k < kPairs; k += 2) {
-    const float4 t = *reinterpret_cast<const float4*>(p + 2 * k);
-    v[k] = make_float2(t.x, t.y);
-    v[k + 1] = make_float2(t.z, t.w);
-  }
+  const float4 t = *reinterpret_cast<const float4*>(p);
+  v[0] = make_float2(t.x, t.y);
+  v[1] = make_float2(t.z, t.w);
 }
 __device__ __forceinline__ void get_channels(float (&v)[kChannels], const float* p) {
   const float2 t = *reinterpret_cast<const float2*>(p);

@@ -6,18 +6,15 @@
 // by a second kernel); sums over time stay with the unit's two warps, one partial sum for each batch
 // entry and split.
 //
-// The states are not kept but every 16 steps. A run over the tile's first twelve finds where its
-// quarters begin; then each quarter, the last first, is run forwards, its states held in registers (4
-// steps x 16 numbers a lane), dCm and o formed on the way, and backwards. In all 2.75 exponentials a
-// state and step instead of one, for a sixteenth of the memory that all states would take. With halves
-// of 8 steps it is 2.5, but the code of a half did not fit the instruction caches, nor its registers
-// beside a step's words read ahead.
+// The states are not kept but every 16 steps. A tile's second half needs them first: a run over the
+// first half finds where it begins; then each half is run forwards, its states held in registers (8
+// steps x 8 numbers a lane), dCm and o formed on the way, and backwards. In all 2.5 exponentials a
+// state and step instead of one, for a sixteenth of the memory that all states would take.
 //
-// The sums over a unit's channels for dBm and dCm, 16 values over 16 lanes a step at N = 16, go
+// The sums over a unit's channels for dBm and dCm, 8 values over 16 lanes a step at N = 16, go
 // through the tensor cores (mma.sync, the only form that takes registers): a product with a matrix
-// of ones adds up four lanes, and four steps share one accumulator, so that the rest takes six
-// exchanges for four steps instead of eight for one. The operands have 11 bits, so each value goes
-// in two parts, which keep 21.
+// of ones adds up four lanes, and four steps share one accumulator, so that the rest takes three
+// exchanges for four steps. The operands have 11 bits, so each value goes in two parts, which keep 21.
 #include <type_traits>
 
 #include "ssm_scan.cuh"
@@ -29,9 +26,10 @@ namespace dlr {
 namespace ssm {
 namespace {
 
-constexpr int kQuarter = 4;  // steps whose states are in registers at a time
+constexpr int kHalf = kT / 2;  // steps whose states are in registers at a time
+constexpr int kUnitWarps = kHalves + 1;  // two run a unit, one stages and finishes
 
-// Units of a block: four, one warp of each kind on each quarter of an SM; two where their channels
+// Units of a block: four, each on a quarter of an SM; two where their channels
 // (64 each, N <= 8) take more of shared memory than a quarter.
 template <int LN>
 constexpr int kUnitsOf = LN == 1 ? 2 : 4;
@@ -48,33 +46,26 @@ struct back_params {
   float *part_bc, *part_A, *part_c;
 };
 
-// A unit's part of shared memory: what a tile's steps read and what they leave, two tiles in turn,
-// three where the finishing warp reads it while the next but one is staged (s, g, and u with q in its
-// place) or where those of other units read it (dBC). MAP needs s, g and Cm alone.
+// A unit's part of shared memory: what a tile's steps read and what they leave, two tiles in turn.
+// MAP needs s, g and Cm alone.
 template <typename T, int LN, bool MAP>
 struct back_tile {
   using S = shape<T, LN>;
   static constexpr int kN = MAP ? 1 : 2, kSteps = MAP ? 1 : kT;
-  float s[3][kT][S::kCW], g[3][kT][S::kCW];
-  float u[3][kT][S::kCW];  // the inputs; q takes a step's place once it is gone through
+  float s[2][kT][S::kCW], g[2][kT][S::kCW], u[2][kT][S::kCW];
   float Bm[kN][kSteps][S::kNP], Cm[2][kT][S::kNP];
-  float h[kN][MAP ? 1 : S::kCW][S::kNP];            // the tile's first states
-  float mid[MAP ? 1 : 3][MAP ? 1 : S::kCW][S::kNP];  // and those of its other quarters
-  float e[kN][kSteps][S::kCW], o[kN][kSteps][S::kCW];
-  float dBC[MAP ? 1 : 3][kSteps][2][S::kNP];
-  float bias[S::kCW], D[S::kCW];
+  float h[kN][MAP ? 1 : S::kCW][S::kNP];  // the tile's first states
+  float q[kN][kSteps][kHalves][S::kCW], e[kN][kSteps][kHalves][S::kCW];
+  float o[kN][kSteps][kHalves][S::kCW];
+  float dBC[kN][kSteps][2][S::kNP];
 };
 
-// Sums over the unit's channels of a lane's 8 values for each of 4 steps: take() for step k of them,
-// then finish() writes them to p[k * pitch + 0 .. 8) (p the place of the lane's first state).
+// Sums over the unit's channels of a lane's 4 values for each of 4 steps: take() for step k of them,
+// then finish() writes them to p[k * pitch + 0 .. 4) (p the place of the lane's first state).
 struct channel_sums {
-  float c[8];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 0.0f;
-  }
-  static __device__ __forceinline__ void mma(float* c, const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
+  float c[4];
+  __device__ __forceinline__ void clear() { c[0] = c[1] = c[2] = c[3] = 0.0f; }
+  __device__ __forceinline__ void mma(const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -86,27 +77,24 @@ struct channel_sums {
     const uint32_t one = __float_as_uint(1.0f);
     const uint32_t b0 = lane >> 2 == 2 * k ? one : 0u, b1 = lane >> 2 == 2 * k + 1 ? one : 0u;
     constexpr uint32_t kTop = 0xffffe000u;  // sign, exponent and the 10 leading bits
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 x = v[2 * j], y = v[2 * j + 1];
-      const uint32_t hi[4] = {__float_as_uint(x.x) & kTop, __float_as_uint(y.x) & kTop,
-                              __float_as_uint(x.y) & kTop, __float_as_uint(y.y) & kTop};
-      const float2 lx = fma2(make_float2(__uint_as_float(hi[0]), __uint_as_float(hi[2])),
-                             two(-1.0f), x);
-      const float2 ly = fma2(make_float2(__uint_as_float(hi[1]), __uint_as_float(hi[3])),
-                             two(-1.0f), y);
-      const uint32_t lo[4] = {__float_as_uint(lx.x), __float_as_uint(ly.x), __float_as_uint(lx.y),
-                              __float_as_uint(ly.y)};
-      mma(c + 4 * j, lo, b0, b1);
-      mma(c + 4 * j, hi, b0, b1);
-    }
+    const float2 x = v[0], y = v[1];
+    const uint32_t hi[4] = {__float_as_uint(x.x) & kTop, __float_as_uint(y.x) & kTop,
+                            __float_as_uint(x.y) & kTop, __float_as_uint(y.y) & kTop};
+    const float2 lx =
+        fma2(make_float2(__uint_as_float(hi[0]), __uint_as_float(hi[2])), two(-1.0f), x);
+    const float2 ly =
+        fma2(make_float2(__uint_as_float(hi[1]), __uint_as_float(hi[3])), two(-1.0f), y);
+    const uint32_t lo[4] = {__float_as_uint(lx.x), __float_as_uint(ly.x), __float_as_uint(lx.y),
+                            __float_as_uint(ly.y)};
+    mma(lo, b0, b1);
+    mma(hi, b0, b1);
   }
-  // Lane's quad: channels 4 (quad % (CL / 4)) on of states `at`; its place in the quad: the step.
+  // The other quads of the lane's states are added up; its place in the quad is the step.
   template <int CL>
   __device__ __forceinline__ void finish(float* p, int pitch, int lane) {
     const int quad = (lane >> 2) % (CL / 4);
-    sum_lanes<4, 8, CL / 4>(c, quad);
-    put_lanes<8, CL / 4>(p + (lane & 3) * pitch, c, quad);
+    sum_lanes<4, 4, CL / 4>(c, quad);
+    put_lanes<4, CL / 4>(p + (lane & 3) * pitch, c, quad);
   }
 };
 
@@ -126,12 +114,10 @@ __device__ __forceinline__ void advance(float2 (&h)[kChannels][kPairs],
 
 // MAP: only the gradient that each split but the first sends on, and the sum of its steps.
 template <typename T, int LN, bool MAP>
-__global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<T> q) {
+__global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel(back_params<T> q) {
   using S = shape<T, LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
   constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN, kUnits = kUnitsOf<LN>;
-  // 12 warps of 168 registers at launch: a recurrence takes 248, its helpers leave it theirs
-  constexpr bool kShare = !MAP && kUnits == 4;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
   using tile_t = back_tile<T, LN, MAP>;
@@ -140,7 +126,7 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
   tile_t& m = all[mine];
 
   // a block: kUnits neighbouring units of one group, split and batch entry (all of them run, also
-  // those without channels, for the finishing warps' meetings)
+  // those without channels, for the helpers' meetings)
   const int per_row = in.blocks * in.G, n_split = MAP ? in.splits - 1 : in.splits;
   const int cb = (int)(blockIdx.x % per_row), block = cb % in.blocks;
   unit<T, LN> u;
@@ -148,141 +134,27 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
   u.b = blockIdx.x / per_row / n_split;
   u.place(in, cb / in.blocks, (block * kUnits + mine) * S::kCW);
   u.whole = u.whole && u.pieces(q.dy);
-  const bool full = u.n_ch == S::kCW, ok_z = full && u.pieces(in.z);
   const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
   const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  if (warp >= 2 * kUnits) {  // finishes
-    if constexpr (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
-    if constexpr (MAP) {
-      for (int tile = t_first; tile <= t_end; ++tile) meet_unit(mine);
-    } else {
-      const bool ok_o = full && u.pieces(q.dx) && u.pieces(q.ddt) && u.pieces(q.dz);
-      for (int c = lane; c < S::kCW; c += 32) {
-        m.bias[c] = in.bias && c < u.n_ch ? in.bias[u.c0 + c] : 0.0f;
-        m.D[c] = in.D && c < u.n_ch ? in.D[u.c0 + c] : 0.0f;
-      }
-      __syncwarp();
-      // read a tile before their use, as many as registers hold
-      constexpr bool kAhead = S::NV <= 2;
-      words<T, VE> wx[S::NV], wd[S::NV], wy[S::NV], wz[S::NV];
-      auto fetch = [&](int tile) {
-        const int64_t t0 = (int64_t)tile * kT;
-        u.fetch(wx, in.x, t0, in.L, lane, u.whole);
-        u.fetch(wd, in.dt, t0, in.L, lane, u.whole);
-        if (in.z.p) {
-          u.fetch(wy, q.dy, t0, in.L, lane, u.whole);
-          u.fetch(wz, in.z, t0, in.L, lane, ok_z);
-        }
-      };
-      // of this lane's channels (the same in all its pieces): ddt and g x summed over time
-      float sum_t[VE], sum_x[VE];
+  if (warp >= kHalves * kUnits) {
+    const bool full = u.n_ch == S::kCW, ok_z = full && u.pieces(in.z);
+    const bool ok_o = full && u.pieces(q.dx) && u.pieces(q.ddt) && u.pieces(q.dz);
+    // of the channels of this lane's pieces (the same in all of them)
+    float bias[VE], D[VE];
+    const int c_mine = lane % S::kRow * VE;
 #pragma unroll
-      for (int i = 0; i < VE; ++i) sum_t[i] = sum_x[i] = 0.0f;
-      // the units' dBm and dCm, and what the channels' gradients take besides, by pieces of rows
-      auto finish = [&](int tile) {
-        const int64_t t0 = (int64_t)tile * kT;
-        const int j = tile & 1, j3 = tile % 3;
-        meet_finishing<kUnits>();
-        constexpr int pitch = 2 * S::kNP, share = kT * pitch / kUnits;
-        float* part = q.part_bc +
-                      ((((int64_t)u.group * in.blocks + block) * in.B + u.b) * in.L + t0) * pitch;
-#pragma unroll
-        for (int k = 0; k < (share + 127) / 128; ++k) {
-          const int i = mine * share + (k * 32 + lane) * 4;
-          if (share % 128 && (k * 32 + lane) * 4 >= share) break;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int w = 0; w < kUnits; ++w) {
-            const float4 p = *reinterpret_cast<const float4*>(&all[w].dBC[j3][0][0][0] + i);
-            v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
-          }
-          if (t0 + i / pitch < in.L) *reinterpret_cast<float4*>(part + i) = v;
-        }
-        if (!kAhead) fetch(tile);
-#pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-          int t, c;
-          if (!u.piece(k, lane, t, c)) break;
-          if (t0 + t >= in.L || c >= u.n_ch) continue;
-          float xv[VE], dv[VE], gv[VE], qv[VE], ev[VE];
-          wx[k].to(xv);
-          wd[k].to(dv);
-          load_floats<VE>(qv, &m.u[j3][t][c]);
-          load_floats<VE>(ev, &m.e[j][t][c]);
-          load_floats<VE>(gv, &m.bias[c]);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            // e was summed with the rates in powers of two
-            float d = fmaf(xv[i], qv[i], ev[i] * (1.0f / kLog2e));
-            if (in.softplus) d *= glr::sigmoid(dv[i] + gv[i]);
-            dv[i] = d;
-            sum_t[i] += c + i < u.n_ch ? d : 0.0f;
-          }
-          put_piece<T, VE>(q.ddt.row(u.b, t0 + t) + u.c0 + c, dv, u.n_ch - c, ok_o);
-          load_floats<VE>(gv, &m.g[j3][t][c]);
-          load_floats<VE>(dv, &m.s[j3][t][c]);
-          load_floats<VE>(ev, &m.D[c]);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            qv[i] = fmaf(dv[i], qv[i], ev[i] * gv[i]);
-            sum_x[i] += c + i < u.n_ch ? gv[i] * xv[i] : 0.0f;
-          }
-          put_piece<T, VE>(q.dx.row(u.b, t0 + t) + u.c0 + c, qv, u.n_ch - c, ok_o);
-          if (in.z.p) {
-            wz[k].to(dv);
-            wy[k].to(gv);
-            load_floats<VE>(qv, &m.o[j][t][c]);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-              const float sig = glr::sigmoid(dv[i]);
-              gv[i] *= fmaf(ev[i], xv[i], qv[i]) * fmaf(dv[i] * sig, 1.0f - sig, sig);
-            }
-            put_piece<T, VE>(q.dz.row(u.b, t0 + t) + u.c0 + c, gv, u.n_ch - c, ok_o);
-          }
-        }
-      };
-      meet_unit(mine);
-      for (int tile = t_end - 1; tile >= t_first; --tile) {
-        if (tile < t_end - 1) finish(tile + 1);
-        if (kAhead) fetch(tile);
-        meet_unit(mine);
-      }
-      finish(t_first);
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-#pragma unroll
-        for (int d = S::kRow; d < 32; d *= 2) {
-          sum_t[i] += __shfl_xor_sync(0xffffffffu, sum_t[i], d);
-          sum_x[i] += __shfl_xor_sync(0xffffffffu, sum_x[i], d);
-        }
-      const int c = lane * VE;
-      if (lane < S::kRow) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (c + i < u.n_ch) {
-            float* p = q.part_c + row_map * in.H + u.c0 + c + i;
-            p[0] = sum_t[i];
-            p[in.B * in.splits * in.H] = sum_x[i];
-          }
-      }
+    for (int i = 0; i < VE; ++i) {
+      const bool there = c_mine + i < u.n_ch;
+      bias[i] = in.bias && there ? in.bias[u.c0 + c_mine + i] : 0.0f;
+      D[i] = in.D && there ? in.D[u.c0 + c_mine + i] : 0.0f;
     }
-    return;
-  }
-  if (warp >= kUnits) {  // stages
-    if constexpr (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
-    // (its own copy of the bias: the finishing warp writes the shared one)
+    // what is staged is read a tile before, where registers hold it
     constexpr bool kAhead = S::NV <= 2;
-    float bias[VE];
-    const int c_mine = lane % S::kRow * VE;  // the channels of all this lane's pieces
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      bias[i] = in.bias && c_mine + i < u.n_ch ? in.bias[u.c0 + c_mine + i] : 0.0f;
     words<T, VE> wx[S::NV], wd[S::NV], wy[S::NV], wz[S::NV];
     words<T, VB> wb[S::NB], wc[S::NB];
-    // a tile's first states: quads of the unit's kCW x NP, 4 to a lane
-    float4 first[4];
-    const bool quads = in.N % 4 == 0 && (reinterpret_cast<uintptr_t>(q.states) & 15) == 0;
+    float4 first[4];  // a tile's first states: quads of the unit's kCW x NP
+    const bool whole_h = quads(q.states, in.N);
     auto fetch = [&](int tile) {
       const int64_t t0 = (int64_t)tile * kT;
       if (!MAP) u.fetch(wx, in.x, t0, in.L, lane, u.whole);
@@ -295,25 +167,16 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
         const float* src = q.states + (u.b * in.tiles + tile) * HN + (int64_t)u.c0 * in.N;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int i = (k * 32 + lane) * 4, c = i / S::kNP, n = i % S::kNP;
-          first[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (c >= u.n_ch || n >= in.N) continue;
-          const float* p = src + (int64_t)c * in.N + n;
-          if (quads) {
-            first[k] = *reinterpret_cast<const float4*>(p);
-          } else {
-            first[k].x = p[0];
-            if (n + 1 < in.N) first[k].y = p[1];
-            if (n + 2 < in.N) first[k].z = p[2];
-            if (n + 3 < in.N) first[k].w = p[3];
-          }
+          const int i = (k * 32 + lane) * 4, c = i / S::kNP;
+          first[k] = c < u.n_ch ? get_quad(src + (int64_t)c * in.N, i % S::kNP, in.N, whole_h)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
       }
     };
     auto stage = [&](int tile) {
-      const int j = tile & 1, j3 = tile % 3;
+      const int j = tile & 1;
       stage_steps<T, LN>(u, in.softplus, (int64_t)tile * kT, in.L, lane, bias, MAP ? wd : wx, wd,
-                         m.s[j3], m.u[j3]);
+                         m.s[j], m.u[j]);
       u.put_b(m.Cm[j], wc, lane);
 #pragma unroll
       for (int k = 0; k < S::NV; ++k) {
@@ -329,7 +192,7 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
             yv[i] *= g.x, yv[i + 1] *= g.y;
           }
         }
-        store_floats<VE>(&m.g[j3][t][c], yv);
+        store_floats<VE>(&m.g[j][t][c], yv);
       }
       if constexpr (!MAP) {
         u.put_b(m.Bm[j], wb, lane);
@@ -338,24 +201,125 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
           *reinterpret_cast<float4*>(&m.h[j][0][0] + (k * 32 + lane) * 4) = first[k];
       }
     };
+    // of this lane's channels: ddt and g x summed over time
+    float sum_t[VE], sum_x[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) sum_t[i] = sum_x[i] = 0.0f;
+    auto both = [&](float (&v)[VE], const float (*p)[S::kCW], int c) {  // the two halves' sum
+      float w[VE];
+      load_floats<VE>(v, &p[0][c]);
+      load_floats<VE>(w, &p[1][c]);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) v[i] += w[i];
+    };
+    // the units' dBm and dCm, and what the channels' gradients take besides, by pieces of rows
+    auto finish = [&](int tile) {
+      const int64_t t0 = (int64_t)tile * kT;
+      const int j = tile & 1;
+      words<T, VE> fx[S::NV], fd[S::NV], fy[S::NV], fz[S::NV];
+      u.fetch(fx, in.x, t0, in.L, lane, u.whole);
+      u.fetch(fd, in.dt, t0, in.L, lane, u.whole);
+      if (in.z.p) {
+        u.fetch(fy, q.dy, t0, in.L, lane, u.whole);
+        u.fetch(fz, in.z, t0, in.L, lane, ok_z);
+      }
+      meet_finishing<kUnits>();
+      constexpr int pitch = 2 * S::kNP, share = kT * pitch / kUnits;
+      float* part = q.part_bc +
+                    ((((int64_t)u.group * in.blocks + block) * in.B + u.b) * in.L + t0) * pitch;
+#pragma unroll
+      for (int k = 0; k < (share + 127) / 128; ++k) {
+        const int i = mine * share + (k * 32 + lane) * 4;
+        if (share % 128 && (k * 32 + lane) * 4 >= share) break;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kUnits; ++w) {
+          const float4 p = *reinterpret_cast<const float4*>(&all[w].dBC[j][0][0][0] + i);
+          v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+        }
+        if (t0 + i / pitch < in.L) *reinterpret_cast<float4*>(part + i) = v;
+      }
+#pragma unroll
+      for (int k = 0; k < S::NV; ++k) {
+        int t, c;
+        if (!u.piece(k, lane, t, c)) break;
+        if (t0 + t >= in.L || c >= u.n_ch) continue;
+        float xv[VE], dv[VE], gv[VE], qv[VE], ev[VE];
+        fx[k].to(xv);
+        fd[k].to(dv);
+        both(qv, m.q[j][t], c);
+        both(ev, m.e[j][t], c);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          // e was summed with the rates in powers of two
+          float d = fmaf(xv[i], qv[i], ev[i] * (1.0f / kLog2e));
+          if (in.softplus) d *= glr::sigmoid(dv[i] + bias[i]);
+          dv[i] = d;
+          sum_t[i] += c + i < u.n_ch ? d : 0.0f;
+        }
+        put_piece<T, VE>(q.ddt.row(u.b, t0 + t) + u.c0 + c, dv, u.n_ch - c, ok_o);
+        load_floats<VE>(gv, &m.g[j][t][c]);
+        load_floats<VE>(dv, &m.s[j][t][c]);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          qv[i] = fmaf(dv[i], qv[i], D[i] * gv[i]);
+          sum_x[i] += c + i < u.n_ch ? gv[i] * xv[i] : 0.0f;
+        }
+        put_piece<T, VE>(q.dx.row(u.b, t0 + t) + u.c0 + c, qv, u.n_ch - c, ok_o);
+        if (in.z.p) {
+          fz[k].to(dv);
+          fy[k].to(gv);
+          both(qv, m.o[j][t], c);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            const float sig = glr::sigmoid(dv[i]);
+            gv[i] *= fmaf(D[i], xv[i], qv[i]) * fmaf(dv[i] * sig, 1.0f - sig, sig);
+          }
+          put_piece<T, VE>(q.dz.row(u.b, t0 + t) + u.c0 + c, gv, u.n_ch - c, ok_o);
+        }
+      }
+    };
     fetch(t_end - 1);
     stage(t_end - 1);
     if (kAhead && t_end - 2 >= t_first) fetch(t_end - 2);
-    meet_unit(mine);
+    meet_unit<kUnitWarps>(mine);
     for (int tile = t_end - 1; tile >= t_first; --tile) {
+      if constexpr (!MAP)
+        if (tile < t_end - 1) finish(tile + 1);  // reads s and g, whose place the next stage takes
       if (tile - 1 >= t_first) {
         if (!kAhead) fetch(tile - 1);
         stage(tile - 1);
         if (kAhead && tile - 2 >= t_first) fetch(tile - 2);
       }
-      meet_unit(mine);
+      // no unit goes on, and over its dBC, before all helpers have read it
+      if (!MAP) meet_finishing<kUnits>();
+      meet_unit<kUnitWarps>(mine);
+    }
+    if constexpr (!MAP) {
+      finish(t_first);
+#pragma unroll
+      for (int i = 0; i < VE; ++i)
+#pragma unroll
+        for (int d = S::kRow; d < 32; d *= 2) {
+          sum_t[i] += __shfl_xor_sync(0xffffffffu, sum_t[i], d);
+          sum_x[i] += __shfl_xor_sync(0xffffffffu, sum_x[i], d);
+        }
+      if (lane < S::kRow) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (c_mine + i < u.n_ch) {
+            float* p = q.part_c + row_map * in.H + u.c0 + c_mine + i;
+            p[0] = sum_t[i];
+            p[in.B * in.splits * in.H] = sum_x[i];
+          }
+      }
     }
     return;
   }
 
   // the recurrence: this lane's channels and states
-  if constexpr (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 248;");
-  const int at = lane / CL, cg = lane % CL, cl = cg * kChannels, n0 = at * kStates;
+  const int half_of = warp / kUnits, at = lane / CL, cl = lane % CL * kChannels;
+  const int n0 = (half_of * LN + at) * kStates;
   const int my_ch = u.n_ch - cl;
   const int64_t ch = (int64_t)(u.c0 + cl) * in.N;
   float2 rate[kChannels][kPairs], carry[kChannels][kPairs];
@@ -366,7 +330,7 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
     load_states(carry, q.dh_last + u.b * HN + ch, in.N, my_ch, n0);
   else
     load_states(carry, in.ends + (row_map + 1) * HN + ch, in.N, my_ch, n0);
-  meet_unit(mine);
+  meet_unit<kUnitWarps>(mine);
 
   // A tile without marks goes without looking for them: a branch would keep the steps apart that are
   // to overlap. A step's words are read a step ahead (the last ones for nothing).
@@ -375,14 +339,14 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
     bool cut = false;
     for (int tile = t_end - 1; tile >= t_first; --tile) {
       const uint32_t mark = marks(in.reset, u.b, (int64_t)tile * kT, in.L, lane);
-      const int j = tile & 1, j3 = tile % 3;
+      const int j = tile & 1;
       auto steps = [&](auto marks_here) {
         constexpr bool MARKS = decltype(marks_here)::value;
         float s_next[kChannels], g_next[kChannels];
         float2 c_next[kPairs];
         auto read = [&](int t) {
-          get_channels(s_next, &m.s[j3][t][cl]);
-          get_channels(g_next, &m.g[j3][t][cl]);
+          get_channels(s_next, &m.s[j][t][cl]);
+          get_channels(g_next, &m.g[j][t][cl]);
           get_map(c_next, &m.Cm[j][t][n0]);
         };
         read(kT - 1);
@@ -413,10 +377,10 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
       } else {
         steps(std::false_type{});
       }
-      meet_unit(mine);
+      meet_unit<kUnitWarps>(mine);
     }
     store_states(in.ends + row_map * HN + ch, carry, in.N, my_ch, n0);
-    if (at == 0)
+    if (n0 == 0)
 #pragma unroll
       for (int i = 0; i < kChannels; ++i)
         if (i < my_ch)
@@ -426,64 +390,51 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
     clear(dA);
     for (int tile = t_end - 1; tile >= t_first; --tile) {
       const uint32_t mark = marks(in.reset, u.b, (int64_t)tile * kT, in.L, lane);
-      const int j = tile & 1, j3 = tile % 3;
-      float (*dBC)[2][S::kNP] = m.dBC[j3];
+      const int j = tile & 1;
+      float (*dBC)[2][S::kNP] = m.dBC[j];
       auto steps = [&](auto marks_here) {
         constexpr bool MARKS = decltype(marks_here)::value;
         float2 h[kChannels][kPairs];
         float s_next[kChannels], x_next[kChannels], g_next[kChannels];
         float2 b_next[kPairs], c_next[kPairs];
         auto read = [&](int t) {
-          get_channels(s_next, &m.s[j3][t][cl]);
-          get_channels(x_next, &m.u[j3][t][cl]);
+          get_channels(s_next, &m.s[j][t][cl]);
+          get_channels(x_next, &m.u[j][t][cl]);
           get_map(b_next, &m.Bm[j][t][n0]);
         };
         auto read_all = [&](int t) {
           read(t);
-          get_channels(g_next, &m.g[j3][t][cl]);
+          get_channels(g_next, &m.g[j][t][cl]);
           get_map(c_next, &m.Cm[j][t][n0]);
         };
+        // where the second half begins
 #pragma unroll
         for (int i = 0; i < kChannels; ++i) get_map(h[i], &m.h[j][cl + i][n0]);
-        // where the quarters begin
         read(0);
-#pragma unroll 1
-        for (int k = 0; k < 3; ++k) {
+#pragma unroll 4
+        for (int t = 0; t < kHalf; ++t) {
+          float s[kChannels], x[kChannels];
+          float2 bp[kPairs];
 #pragma unroll
-          for (int i = 0; i < kQuarter; ++i) {
-            const int t = k * kQuarter + i;
-            float s[kChannels], x[kChannels];
-            float2 bp[kPairs];
+          for (int i = 0; i < kChannels; ++i) s[i] = s_next[i], x[i] = x_next[i];
 #pragma unroll
-            for (int c = 0; c < kChannels; ++c) s[c] = s_next[c], x[c] = x_next[c];
-#pragma unroll
-            for (int p = 0; p < kPairs; ++p) bp[p] = b_next[p];
-            read(t + 1);
-            if (MARKS && (mark >> t & 1)) clear(h);
-            advance<kPrecise>(h, rate, s, x, bp);
-          }
-#pragma unroll
-          for (int i = 0; i < kChannels; ++i)
-#pragma unroll
-            for (int p = 0; p < kPairs; p += 2)
-              *reinterpret_cast<float4*>(&m.mid[k][cl + i][n0 + 2 * p]) =
-                  make_float4(h[i][p].x, h[i][p].y, h[i][p + 1].x, h[i][p + 1].y);
+          for (int p = 0; p < kPairs; ++p) bp[p] = b_next[p];
+          read(t + 1);
+          if (MARKS && (mark >> t & 1)) clear(h);
+          advance<kPrecise>(h, rate, s, x, bp);
         }
 #pragma unroll 1
-        for (int quarter = 3; quarter >= 0; --quarter) {
-          const int t_first_q = quarter * kQuarter;
-          float2 hist[kQuarter][kChannels][kPairs];
-          read_all(t_first_q);
-          if (quarter < 3) {
-            const float* p0 = quarter ? &m.mid[quarter - 1][0][0] : &m.h[j][0][0];
-#pragma unroll
-            for (int i = 0; i < kChannels; ++i) get_map(h[i], p0 + (cl + i) * S::kNP + n0);
-          }
+        for (int half = 1; half >= 0; --half) {
+          const int t_half = half * kHalf;
+          float2 hist[kHalf][kChannels][kPairs];
           channel_sums sums;
-          sums.clear();
+          read_all(t_half);
+          if (half == 0)
 #pragma unroll
-          for (int k = 0; k < kQuarter; ++k) {
-            const int t = t_first_q + k;
+            for (int i = 0; i < kChannels; ++i) get_map(h[i], &m.h[j][cl + i][n0]);
+#pragma unroll
+          for (int k = 0; k < kHalf; ++k) {
+            const int t = t_half + k;
             asm volatile("" ::: "memory");  // words read further ahead would cost registers
             float s[kChannels], x[kChannels], g[kChannels], o[kChannels];
             float2 bp[kPairs], cp[kPairs], d[kPairs];
@@ -492,34 +443,31 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
               s[i] = s_next[i], x[i] = x_next[i], g[i] = g_next[i];
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) bp[p] = b_next[p], cp[p] = c_next[p];
-            if (k + 1 < kQuarter) read_all(t + 1);
+            read_all(k + 1 < kHalf ? t + 1 : t);
             if (MARKS && (mark >> t & 1)) clear(h);
 #pragma unroll
             for (int i = 0; i < kChannels; ++i)
 #pragma unroll
               for (int p = 0; p < kPairs; ++p) hist[k][i][p] = h[i][p];
             advance<kPrecise>(h, rate, s, x, bp);
+            if (k % 4 == 0) sums.clear();
 #pragma unroll
             for (int p = 0; p < kPairs; ++p)
               d[p] = fma2(h[1][p], two(g[1]), mul2(h[0][p], two(g[0])));
-            sums.take(d, k, lane);
+            sums.take(d, k % 4, lane);
 #pragma unroll
             for (int i = 0; i < kChannels; ++i) {
-              float2 acc = mul2(h[i][0], cp[0]);
-#pragma unroll
-              for (int p = 1; p < kPairs; ++p) acc = fma2(h[i][p], cp[p], acc);
+              const float2 acc = fma2(h[i][1], cp[1], mul2(h[i][0], cp[0]));
               o[i] = acc.x + acc.y;
             }
             sum_lanes<CL, kChannels, LN>(o, at);
-            put_lanes<kChannels, LN>(&m.o[j][t][cl], o, at);
+            put_lanes<kChannels, LN>(&m.o[j][t][half_of][cl], o, at);
+            if (k % 4 == 3) sums.finish<CL>(&dBC[t - 3][1][n0], 2 * S::kNP, lane);
           }
-          read_all(t_first_q + kQuarter - 1);
-          sums.finish<CL>(&dBC[t_first_q][1][n0], 2 * S::kNP, lane);
-          sums.clear();
 #pragma unroll
-          for (int k = kQuarter - 1; k >= 0; --k) {
-            const int t = t_first_q + k;
-            asm volatile("" ::: "memory");  // words read further ahead would cost registers
+          for (int k = kHalf - 1; k >= 0; --k) {
+            const int t = t_half + k;
+            asm volatile("" ::: "memory");
             float s[kChannels], x[kChannels], g[kChannels], qv[kChannels], ev[kChannels];
             float2 bp[kPairs], cp[kPairs], db[kPairs];
 #pragma unroll
@@ -528,6 +476,7 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) bp[p] = b_next[p], cp[p] = c_next[p];
             if (k) read_all(t - 1);
+            if (k % 4 == 3) sums.clear();
 #pragma unroll
             for (int i = 0; i < kChannels; ++i) {
               float2 qs, es;
@@ -546,20 +495,20 @@ __global__ void __launch_bounds__(96 * kUnitsOf<LN>, 1) back_kernel(back_params<
               ev[i] = es.x + es.y;
             }
             if (MARKS && (mark >> t & 1)) clear(carry);
-            sums.take(db, k, lane);
+            sums.take(db, k % 4, lane);
             sum_lanes<CL, kChannels, LN>(qv, at);
-            put_lanes<kChannels, LN>(&m.u[j3][t][cl], qv, at);
+            put_lanes<kChannels, LN>(&m.q[j][t][half_of][cl], qv, at);
             sum_lanes<CL, kChannels, LN>(ev, at);
-            put_lanes<kChannels, LN>(&m.e[j][t][cl], ev, at);
+            put_lanes<kChannels, LN>(&m.e[j][t][half_of][cl], ev, at);
+            if (k % 4 == 0) sums.finish<CL>(&dBC[t][0][n0], 2 * S::kNP, lane);
           }
-          sums.finish<CL>(&dBC[t_first_q][0][n0], 2 * S::kNP, lane);
         }
       };
       if (mark)
         steps(std::true_type{});
       else
         steps(std::false_type{});
-      meet_unit(mine);
+      meet_unit<kUnitWarps>(mine);
     }
     store_states(q.part_A + row_map * HN + ch, dA, in.N, my_ch, n0);
     if (u.split == 0 && q.dh0) store_states(q.dh0 + u.b * HN + ch, carry, in.N, my_ch, n0);
@@ -614,7 +563,7 @@ back_plan plan(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
   const int64_t ln = lanes_for(N), cw = 64 / ln, units = (H / G + cw - 1) / cw;
   const int64_t per_block = ln == 1 ? kUnitsOf<1> : kUnitsOf<2>;
   p.blocks = (units + per_block - 1) / per_block;
-  p.NP = kStates * ln;
+  p.NP = kHalves * kStates * ln;
   const int64_t want = splits_for(B, L, H, N, G), tiles = (L + kT - 1) / kT;
   const int64_t per = (tiles + want - 1) / want;
   p.splits = (tiles + per - 1) / per;
@@ -635,7 +584,7 @@ cudaError_t run_back(back_params<T> q, const back_plan& p, cudaStream_t s) {
   if (q.in.splits > 1) {
     constexpr size_t bytes = sizeof(back_tile<T, LN, true>) * kUnits;
     if ((e = max_smem_once<back_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
-    back_kernel<T, LN, true><<<(unsigned)(units * (q.in.splits - 1)), 96 * kUnits, bytes, s>>>(q);
+    back_kernel<T, LN, true><<<(unsigned)(units * (q.in.splits - 1)), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     join_splits<true><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
         q.in.A, q.dh_last, q.in.ends, q.in.sums, q.in.B, q.in.splits, HN, q.in.N);
@@ -644,7 +593,7 @@ cudaError_t run_back(back_params<T> q, const back_plan& p, cudaStream_t s) {
   constexpr size_t bytes = sizeof(back_tile<T, LN, false>) * kUnits;
   static_assert(bytes <= 232448, "shared memory");
   if ((e = max_smem_once<back_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
-  back_kernel<T, LN, false><<<(unsigned)(units * q.in.splits), 96 * kUnits, bytes, s>>>(q);
+  back_kernel<T, LN, false><<<(unsigned)(units * q.in.splits), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t n = q.in.B * q.in.L * q.in.G * 2 * p.NP;
   sum_maps<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(q.part_bc, q.dBm, q.dCm, q.in.B, q.in.L,
