@@ -2,10 +2,12 @@
 // one token.
 //
 // Memory bounds all three: two arrays go through it forwards and three backwards, and a tap is one
-// multiply-add. A thread takes VE neighbouring channels over a run of steps, the last K inputs in a
-// window of registers: each input is read once by its run and, of the K - 1 before the run, once
-// more (from the cache: the run before is the neighbouring warp's). A marked step empties the window.
+// multiply-add. A thread takes VE neighbouring channels over a run of steps, a few steps at a time with
+// the K - 1 inputs before them in registers, and reads the next few meanwhile: each input is read once
+// by its run and, of the K - 1 before the run, once more (from the cache: the run before is the
+// neighbouring warp's).
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_common.cuh"
 
@@ -16,9 +18,7 @@ namespace dlr {
 namespace ssm {
 namespace {
 
-constexpr int kWarps = 8;      // of a block: neighbouring runs of the same channels
-constexpr int kRun = 16;       // steps of a run, forwards
-constexpr int kRunBack = 32;   // and backwards, where a run's sums are written out at its end
+constexpr int kWarps = 8;  // of a block: neighbouring runs of the same channels
 
 template <typename T>
 struct conv_params {
@@ -32,229 +32,330 @@ struct conv_params {
   T *last, *dstate;
   float* part;  // [K + 1, parts, H]: a block's sums for the taps and the bias
   int64_t parts;
-  int64_t runs;  // of a row
+  int64_t runs;      // of a row
+  int run;           // steps of a run
   unsigned columns;  // blocks beside one another over the channels
+};
+
+// Steps of a run: long ones repeat less (the inputs before a run, backwards the steps behind it and
+// the writing of its sums), short ones where there are few threads.
+int run_for(int64_t B, int64_t L, int64_t columns, int lo, int hi) {
+  int run = hi;
+  while (run > lo && B * ((L + run - 1) / run) * columns < 152 * 32) run /= 2;
+  return run;
+}
+int forward_run(int64_t B, int64_t L, int64_t H) { return run_for(B, L, (H + 127) / 128, 8, 64); }
+int back_run(int64_t B, int64_t L, int64_t H) { return run_for(B, L, (H + 63) / 64, 16, 128); }
+
+// VE channels as pairs, on which one instruction works at a time (a single channel pairs with zero).
+template <int VE>
+struct piece {
+  static constexpr int kP = (VE + 1) / 2;
+  float2 p[kP];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = two(0.0f);
+  }
+  __device__ __forceinline__ void fma(const piece& a, const piece& b) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = fma2(a.p[i], b.p[i], p[i]);
+  }
+  __device__ __forceinline__ void add(const piece& a) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = add2(p[i], a.p[i]);
+  }
+  __device__ __forceinline__ void mul(const piece& a) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = mul2(p[i], a.p[i]);
+  }
+  template <typename T>
+  __device__ __forceinline__ void from(const words<T, VE>& w) {
+    float v[VE];
+    w.to(v);
+    set(v);
+  }
+  __device__ __forceinline__ void set(const float* v) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = make_float2(v[2 * i], 2 * i + 1 < VE ? v[2 * i + 1] : 0.0f);
+  }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[i] = i & 1 ? p[i / 2].y : p[i / 2].x;
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(T* to) const {
+    float v[VE];
+    get(v);
+    words<T, VE> w;
+    w.from(v);
+    w.put(to);
+  }
+  __device__ __forceinline__ void silu() {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = mul2(p[i], glr::sigmoid2(p[i]));
+  }
+  __device__ __forceinline__ void silu_slope() {  // s + p s (1 - s)
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const float2 s = glr::sigmoid2(p[i]);
+      p[i] = fma2(mul2(p[i], s), fma2(s, two(-1.0f), two(1.0f)), s);
+    }
+  }
 };
 
 // The input of step t (which may lie before the first): x, the carried state or zero.
 template <typename T, int VE>
-__device__ __forceinline__ void input(float (&v)[VE], const conv_params<T>& q, int64_t b, int64_t t,
+__device__ __forceinline__ void input(piece<VE>& v, const conv_params<T>& q, int64_t b, int64_t t,
                                       int64_t c) {
   words<T, VE> w;
-#pragma unroll
-  for (int i = 0; i < VE; ++i) v[i] = 0.0f;
-  const T* p = nullptr;
   if (t >= 0)
-    p = q.x.row(b, t) + c;
+    w.get(q.x.row(b, t) + c);
   else if (q.state)
-    p = q.state + (b * (q.K - 1) + t + q.K - 1) * q.H + c;
-  if (!p) return;
-  get_piece<T, VE>(w, p, VE, true);
-  w.to(v);
+    w.get(q.state + (b * (q.K - 1) + t + q.K - 1) * q.H + c);
+  v.from(w);
 }
 
 // Taps of a thread's channels: w[j] of x_{t-j}.
 template <typename T, int VE, int KM>
-__device__ __forceinline__ void taps(float (&w)[KM][VE], float (&bias)[VE], const conv_params<T>& q,
+__device__ __forceinline__ void taps(piece<VE> (&w)[KM], piece<VE>& bias, const conv_params<T>& q,
                                      int64_t c) {
+  float v[VE];
 #pragma unroll
-  for (int i = 0; i < VE; ++i) bias[i] = q.bias ? q.bias[c + i] : 0.0f;
+  for (int i = 0; i < VE; ++i) v[i] = q.bias ? q.bias[c + i] : 0.0f;
+  bias.set(v);
 #pragma unroll
-  for (int j = 0; j < KM; ++j)
+  for (int j = 0; j < KM; ++j) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-      w[j][i] = j < q.K ? q.w[(c + i) * q.K + q.K - 1 - j] : 0.0f;
+    for (int i = 0; i < VE; ++i) v[i] = j < q.K ? q.w[(c + i) * q.K + q.K - 1 - j] : 0.0f;
+    w[j].set(v);
+  }
 }
 
+// The marks around step t, the same in all lanes: bit l is step t - 16 + l.
 template <typename T>
-__device__ __forceinline__ bool marked(const conv_params<T>& q, int64_t b, int64_t t) {
-  return q.reset && t >= 0 && q.reset[b * q.L + t] != 0;
+__device__ __forceinline__ uint32_t marks_around(const conv_params<T>& q, int64_t b, int64_t t,
+                                                 int lane) {
+  if (!q.reset) return 0;
+  const int64_t s = t - 16 + lane;
+  return __ballot_sync(0xffffffffu, s >= 0 && s < q.L && q.reset[b * q.L + s] != 0);
+}
+// Whether step t + i sees the input j steps before it: no mark on the way.
+__device__ __forceinline__ bool sees(uint32_t bits, int i, int j) {
+  return (bits >> (17 + i - j) & ((1u << j) - 1)) == 0;
 }
 
-// EXACT: K = KM. Otherwise the window ends at K: what a tap of zero meets may be infinite.
+// CH steps at a time: v[KM - 1 + i] is the input of step t + i. EXACT: K = KM. Otherwise taps end at
+// K: what a tap of zero meets may be infinite.
 template <typename T, int VE, int KM, bool EXACT>
 __global__ void __launch_bounds__(32 * kWarps) conv_kernel(conv_params<T> q) {
-  const int64_t c = ((int64_t)(blockIdx.x % q.columns) * 32 + (threadIdx.x & 31)) * VE;
+  constexpr int CH = 8, HALO = KM - 1;
+  const int lane = threadIdx.x & 31;
+  const int64_t c0 = ((int64_t)(blockIdx.x % q.columns) * 32 + lane) * VE;
   const int64_t run = (int64_t)(blockIdx.x / q.columns) * kWarps + (threadIdx.x >> 5);
-  const int64_t b = run / q.runs, t0 = (run - b * q.runs) * kRun;
-  if (b >= q.B || c >= q.H) return;
-  float w[KM][VE], bias[VE], win[KM][VE];  // win[j]: the input j steps before
+  const int64_t b = run / q.runs, t0 = (run - b * q.runs) * q.run;
+  if (b >= q.B) return;
+  const bool there = c0 < q.H;  // the other lanes vote for the marks
+  const int64_t c = there ? c0 : 0;
+  piece<VE> w[KM], bias, v[HALO + CH];
   taps<T, VE, KM>(w, bias, q, c);
 #pragma unroll
-  for (int j = 0; j < KM; ++j)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) win[j][i] = 0.0f;
-  const int64_t end = min(q.L, t0 + kRun);
-#pragma unroll
-  for (int j = KM - 1; j >= 1; --j) {
-    if (j >= q.K) continue;
-    const int64_t t = t0 - j;
-    if (marked(q, b, t))
-#pragma unroll
-      for (int k = j + 1; k < KM; ++k)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) win[k][i] = 0.0f;
-    input<T, VE>(win[j], q, b, t, c);
+  for (int j = 1; j <= HALO; ++j) {
+    v[HALO - j].clear();
+    if (EXACT || j < q.K) input<T, VE>(v[HALO - j], q, b, t0 - j, c);
   }
-  // win[j] for j >= 1 is now the input of t0 - j; the loop moves it on before each step
+  const int64_t end = min(q.L, t0 + q.run);
+  words<T, VE> next[CH];
+  const T* px = q.x.row(b, t0) + c;
+  T* py = q.y.row(b, t0) + c;
+  auto fetch = [&](int64_t t) {
 #pragma unroll
-  for (int j = 0; j < KM - 1; ++j)
+    for (int i = 0; i < CH; ++i)
+      if (t + i < end) next[i].get(px + i * q.x.st);
+    px += CH * q.x.st;
+  };
+  fetch(t0);
+  for (int64_t t = t0; t < end; t += CH) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) win[j][i] = win[j + 1][i];
-#pragma unroll 4
-  for (int64_t t = t0; t < end; ++t) {
-    float v[VE];
-    input<T, VE>(v, q, b, t, c);
-    if (marked(q, b, t))
+    for (int i = 0; i < CH; ++i) v[HALO + i].from(next[i]);
+    if (t + CH < end) fetch(t + CH);
+    const uint32_t bits = marks_around(q, b, t, lane);
+    auto steps = [&](auto marks_here) {
+      constexpr bool MARKS = decltype(marks_here)::value;
 #pragma unroll
-      for (int j = 0; j < KM; ++j)
+      for (int i = 0; i < CH; ++i) {
+        if (t + i >= end) break;
+        piece<VE> o = bias;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) win[j][i] = 0.0f;
+        for (int j = HALO; j >= 0; --j) {
+          if (!EXACT && j >= q.K) continue;
+          if (MARKS && !sees(bits, i, j)) continue;
+          o.fma(w[j], v[HALO + i - j]);
+        }
+        if (q.act == SSM_ACT_SILU) o.silu();
+        if (there) o.put(py + i * q.y.st);
+      }
+    };
+    if (bits)
+      steps(std::true_type{});
+    else
+      steps(std::false_type{});
+    py += CH * q.y.st;
 #pragma unroll
-    for (int j = KM - 1; j >= 1; --j)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) win[j][i] = EXACT || j < q.K ? win[j - 1][i] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) win[0][i] = v[i];
-    float o[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      o[i] = bias[i];
-#pragma unroll
-      for (int j = 0; j < KM; ++j) o[i] = fmaf(w[j][i], win[j][i], o[i]);
-      if (q.act == SSM_ACT_SILU) o[i] *= glr::sigmoid(o[i]);
-    }
-    put_piece<T, VE>(q.y.row(b, t) + c, o, VE, true);
+    for (int j = 0; j < HALO; ++j) v[j] = v[CH + j];
   }
   if (end == q.L && q.last) {
-#pragma unroll
-    for (int j = 0; j < KM - 1; ++j)
-      if (j < q.K - 1)
-        put_piece<T, VE>(q.last + (b * (q.K - 1) + q.K - 2 - j) * q.H + c, win[j], VE, true);
+    const uint32_t bits = marks_around(q, b, q.L - 1, lane);
+    for (int j = 0; j < q.K - 1; ++j) {
+      piece<VE> o;
+      o.clear();
+      if (sees(bits, 0, j)) input<T, VE>(o, q, b, q.L - 1 - j, c);
+      if (there) o.put(q.last + (b * (q.K - 1) + q.K - 2 - j) * q.H + c);
+    }
   }
 }
 
-// A run's steps t0 .. t0 + kRunBack - 1: dx of those, from the g of those and of the K - 1 behind
-// them. dx of step t is complete K - 1 steps later: `open[j]` is dx of the step j before, so far.
+// The same backwards in what it forms, not in time: g of a run's steps and of the K - 1 behind it;
+// dx of a step is complete K - 1 steps later. g[HALO + i] is that of step t + i.
 template <typename T, int VE, int KM, bool EXACT>
-__global__ void __launch_bounds__(32 * kWarps) conv_back(conv_params<T> q) {
+__global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 2 : 1) conv_back(conv_params<T> q) {
+  constexpr int CH = 4, HALO = KM - 1;
   __shared__ float sums[kWarps][32 * VE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned column = blockIdx.x % q.columns, part = blockIdx.x / q.columns;
-  const int64_t c = ((int64_t)column * 32 + lane) * VE;
+  const int64_t c0 = ((int64_t)column * 32 + lane) * VE;
   const int64_t run = (int64_t)part * kWarps + warp;
-  const int64_t b = run / q.runs, t0 = (run - b * q.runs) * kRunBack;
-  const bool there = b < q.B && c < q.H;
-  const int halo = EXACT ? KM - 1 : q.K - 1;
-  float w[KM][VE], bias[VE], win[KM][VE], open[KM][VE], dw[KM][VE], db[VE];
+  const int64_t b = run / q.runs, t0 = (run - b * q.runs) * q.run;
+  const bool there = c0 < q.H;
+  const int64_t c = there ? c0 : 0;
+  const int halo = EXACT ? HALO : q.K - 1;
+  piece<VE> dw[KM], db;
+  db.clear();
 #pragma unroll
-  for (int i = 0; i < VE; ++i) {
-    db[i] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < KM; ++j) win[j][i] = open[j][i] = dw[j][i] = 0.0f;
-  }
-  if (there) {
+  for (int j = 0; j < KM; ++j) dw[j].clear();
+  if (b < q.B) {
+    piece<VE> w[KM], bias, v[HALO + CH], g[HALO + CH];
     taps<T, VE, KM>(w, bias, q, c);
-    int seen = halo;  // inputs before the current one that it sees
 #pragma unroll
-    for (int j = KM - 1; j >= 1; --j) {
-      if (j >= q.K) continue;
-      const int64_t t = t0 - j;
-      seen = marked(q, b, t) ? 0 : min(seen + 1, halo);
-      input<T, VE>(win[j], q, b, t, c);
+    for (int j = 1; j <= HALO; ++j) {
+      v[HALO - j].clear();
+      g[HALO - j].clear();
+      if (EXACT || j < q.K) input<T, VE>(v[HALO - j], q, b, t0 - j, c);
     }
-#pragma unroll
-    for (int j = 0; j < KM - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) win[j][i] = win[j + 1][i];
-    const int64_t end = min(q.L, t0 + kRunBack);
+    const int64_t end = min(q.L, t0 + q.run), stop = min(q.L, end + halo);
     // the first run also closes the steps of the carried state
     const int64_t from = t0 == 0 ? -halo : t0;
-#pragma unroll 2
-    for (int64_t t = t0; t < end + halo; ++t) {
-      float v[VE], g[VE];
+    words<T, VE> nx[CH], ng[CH];
+    const T* px = q.x.row(b, t0) + c;
+    const T* pg = q.dy.row(b, t0) + c;
+    T* py = q.y.p + b * q.y.sb + (t0 - halo) * q.y.st + c;  // of step t - halo
+    auto fetch = [&](int64_t t) {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) v[i] = g[i] = 0.0f;
-      const bool real = t < q.L;
-      if (real) {
-        words<T, VE> wg;
-        input<T, VE>(v, q, b, t, c);
-        get_piece<T, VE>(wg, q.dy.row(b, t) + c, VE, true);
-        wg.to(g);
-      }
-      seen = real && marked(q, b, t) ? 0 : min(seen + 1, halo);
-#pragma unroll
-      for (int j = KM - 1; j >= 1; --j)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          win[j][i] = j > seen ? 0.0f : win[j - 1][i];
-          open[j][i] = open[j - 1][i];
-        }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        win[0][i] = v[i];
-        open[0][i] = 0.0f;
-      }
-      if (q.act == SSM_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          float p = bias[i];
-#pragma unroll
-          for (int j = 0; j < KM; ++j) p = fmaf(w[j][i], win[j][i], p);
-          const float s = glr::sigmoid(p);
-          g[i] *= fmaf(p * s, 1.0f - s, s);
+      for (int i = 0; i < CH; ++i) {
+        nx[i] = ng[i] = words<T, VE>();
+        if (t + i < stop) {
+          nx[i].get(px + i * q.x.st);
+          ng[i].get(pg + i * q.dy.st);
         }
       }
-      if (real)
+      px += CH * q.x.st;
+      pg += CH * q.dy.st;
+    };
+    fetch(t0);
+    for (int64_t t = t0; t < end + halo; t += CH) {
 #pragma unroll
-        for (int j = 0; j < KM; ++j)
-          if (j <= seen)
+      for (int i = 0; i < CH; ++i) {
+        v[HALO + i].from(nx[i]);
+        g[HALO + i].from(ng[i]);
+      }
+      fetch(t + CH);
+      const uint32_t bits = marks_around(q, b, t, lane);
+      // PLAIN: all CH steps are the run's own, the steps that they complete too, and no mark is near
+      auto steps = [&](auto plain) {
+        constexpr bool PLAIN = decltype(plain)::value;
+        if (q.act == SSM_ACT_SILU) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) open[j][i] = fmaf(w[j][i], g[i], open[j][i]);
-      if (t < end) {
+          for (int i = 0; i < CH; ++i) {
+            piece<VE> p = bias;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          db[i] += g[i];
-#pragma unroll
-          for (int j = 0; j < KM; ++j) dw[j][i] = fmaf(g[i], win[j][i], dw[j][i]);
+            for (int j = HALO; j >= 0; --j) {
+              if (!EXACT && j > halo) continue;
+              if (!PLAIN && !sees(bits, i, j)) continue;
+              p.fma(w[j], v[HALO + i - j]);
+            }
+            p.silu_slope();
+            g[HALO + i].mul(p);
+            // what is behind the row may have been formed of anything
+            if (!PLAIN && t + i >= q.L) g[HALO + i].clear();
+          }
         }
-      }
-      // step t - halo is complete
-      const int64_t done = t - halo;
-      if (done < from || done >= end) continue;
-      float o[VE];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        o[i] = open[0][i];
+        for (int i = 0; i < CH; ++i) {
+          if (!PLAIN && t + i >= end) continue;
+          db.add(g[HALO + i]);
 #pragma unroll
-        for (int j = 1; j < KM; ++j)
-          if (j == halo) o[i] = open[j][i];
-      }
-      if (q.dlast && done >= q.L - halo) {
-        bool cut = false;
-        for (int64_t s = max(done + 1, (int64_t)0); s < q.L; ++s) cut |= marked(q, b, s);
-        if (!cut) {
-          words<T, VE> wl;
-          float d[VE];
-          get_piece<T, VE>(wl, q.dlast + (b * halo + done - (q.L - halo)) * q.H + c, VE, true);
-          wl.to(d);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) o[i] += d[i];
+          for (int j = 0; j <= HALO; ++j) {
+            if (!EXACT && j > halo) continue;
+            if (!PLAIN && !sees(bits, i, j)) continue;
+            dw[j].fma(g[HALO + i], v[HALO + i - j]);
+          }
         }
+        // steps t + i - halo are complete
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int64_t done = t + i - halo;
+          if (!PLAIN && (done < from || done >= end)) continue;
+          piece<VE> o;
+          o.clear();
+#pragma unroll
+          for (int j = 0; j <= HALO; ++j) {  // what step done + j gives it
+            if (!EXACT && j > halo) continue;
+            if (!PLAIN && !sees(bits, i - halo + j, j)) continue;
+            if constexpr (EXACT) {
+              o.fma(w[j], g[i + j]);
+            } else {  // indexed without an address
+#pragma unroll
+              for (int m = 0; m < HALO + CH; ++m)
+                if (m == HALO - halo + i + j) o.fma(w[j], g[m]);
+            }
+          }
+          if (!PLAIN && q.dlast && done >= q.L - halo) {
+            const int j = (int)(q.L - 1 - done);
+            if (sees(marks_around(q, b, q.L - 1, lane), 0, j)) {
+              words<T, VE> wl;
+              piece<VE> d;
+              wl.get(q.dlast + (b * halo + done - (q.L - halo)) * q.H + c);
+              d.from(wl);
+              o.add(d);
+            }
+          }
+          if (!there) continue;
+          if (PLAIN || done >= 0)
+            o.put(py + i * q.y.st);
+          else if (q.dstate)
+            o.put(q.dstate + (b * halo + done + halo) * q.H + c);
+        }
+      };
+      if (bits || t + CH > end || t - halo < t0 || (q.dlast && t + CH > q.L - halo))
+        steps(std::false_type{});
+      else
+        steps(std::true_type{});
+      py += CH * q.y.st;
+#pragma unroll
+      for (int j = 0; j < HALO; ++j) {
+        v[j] = v[CH + j];
+        g[j] = g[CH + j];
       }
-      if (done >= 0)
-        put_piece<T, VE>(q.y.row(b, done) + c, o, VE, true);
-      else if (q.dstate)
-        put_piece<T, VE>(q.dstate + (b * halo + done + halo) * q.H + c, o, VE, true);
     }
   }
   // the block's sums for its channels, tap by tap, the warps in order
 #pragma unroll
   for (int j = 0; j <= KM; ++j) {
     if (j < KM && j >= q.K) continue;
+    float mine[VE];
+    (j < KM ? dw[j < KM ? j : 0] : db).get(mine);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < VE; ++i) sums[warp][lane * VE + i] = j < KM ? dw[j < KM ? j : 0][i] : db[i];
+    for (int i = 0; i < VE; ++i) sums[warp][lane * VE + i] = mine[i];
     __syncthreads();
     for (int k = threadIdx.x; k < 32 * VE; k += 32 * kWarps) {
       const int64_t ch = (int64_t)column * 32 * VE + k;
@@ -287,34 +388,28 @@ __global__ void __launch_bounds__(256) conv_sums(const float* part, float* dw, f
     dbias[c] = v;
 }
 
+// A block goes over a run of channels of several batch entries.
 template <typename T, int VE, int KM>
 __global__ void __launch_bounds__(128) conv_step(conv_params<T> q) {
-  const int64_t per = (q.H + VE - 1) / VE;
-  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  const int64_t b = i / per, c = (i - b * per) * VE;
-  if (b >= q.B) return;
-  float w[KM][VE], bias[VE], win[KM][VE];
-  taps<T, VE, KM>(w, bias, q, c);
+  const int64_t c = ((int64_t)(blockIdx.x % q.columns) * 32 + (threadIdx.x & 31)) * VE;
+  const int64_t b = (int64_t)(blockIdx.x / q.columns) * 4 + (threadIdx.x >> 5);
+  if (b >= q.B || c >= q.H) return;
+  piece<VE> w[KM], bias, win[KM];
   const bool fresh = q.reset && q.reset[b] != 0;
 #pragma unroll
   for (int j = 0; j < KM; ++j) {
-#pragma unroll
-    for (int k = 0; k < VE; ++k) win[j][k] = 0.0f;
+    win[j].clear();
     if (j == 0 || (j < q.K && !fresh)) input<T, VE>(win[j], q, b, -j, c);
   }
-  float o[VE];
+  taps<T, VE, KM>(w, bias, q, c);
+  piece<VE> o = bias;
 #pragma unroll
-  for (int k = 0; k < VE; ++k) {
-    o[k] = bias[k];
-#pragma unroll
-    for (int j = 0; j < KM; ++j) o[k] = fmaf(w[j][k], win[j][k], o[k]);
-    if (q.act == SSM_ACT_SILU) o[k] *= glr::sigmoid(o[k]);
-  }
-  put_piece<T, VE>(q.y.row(b, 0) + c, o, VE, true);
+  for (int j = 0; j < KM; ++j) o.fma(w[j], win[j]);
+  if (q.act == SSM_ACT_SILU) o.silu();
+  o.put(q.y.row(b, 0) + c);
 #pragma unroll
   for (int j = 0; j < KM - 1; ++j)
-    if (j < q.K - 1)
-      put_piece<T, VE>(q.last + (b * (q.K - 1) + q.K - 2 - j) * q.H + c, win[j], VE, true);
+    if (j < q.K - 1) win[j].put(q.last + (b * (q.K - 1) + q.K - 2 - j) * q.H + c);
 }
 
 // Whether rows of H channels go in pieces of `bytes`: every row begins on a multiple of it.
@@ -336,8 +431,7 @@ template <typename T, int VE, int KM, bool EXACT, Dir DIR>
 void go(conv_params<T> q, cudaStream_t s) {
   q.columns = (unsigned)((q.H + 32 * VE - 1) / (32 * VE));
   if constexpr (DIR == kStep) {
-    const int64_t n = q.B * ((q.H + VE - 1) / VE);
-    conv_step<T, VE, KM><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(q);
+    conv_step<T, VE, KM><<<q.columns * (unsigned)((q.B + 3) / 4), 128, 0, s>>>(q);
   } else {
     const unsigned grid = q.columns * (unsigned)((q.B * q.runs + kWarps - 1) / kWarps);
     if constexpr (DIR == kForward)
@@ -347,11 +441,11 @@ void go(conv_params<T> q, cudaStream_t s) {
   }
 }
 
-// Pieces of 16 bytes forwards, 8 backwards (its windows and sums take three times the registers);
-// single channels where rows do not stand on multiples of them.
+// Pieces of 8 bytes forwards, two channels backwards (with wider ones the registers would leave too
+// few warps on an SM); single channels where rows do not stand on multiples of them.
 template <typename T, int KM, bool EXACT, Dir DIR>
 void by_piece(const conv_params<T>& q, cudaStream_t s) {
-  constexpr int kBytes = DIR == kBack ? 8 : 16, VE = kBytes / (int)sizeof(T);
+  constexpr int VE = DIR == kBack ? 2 : 8 / (int)sizeof(T), kBytes = VE * (int)sizeof(T);
   if (whole_rows(q, kBytes))
     go<T, VE, KM, EXACT, DIR>(q, s);
   else
@@ -376,19 +470,20 @@ cudaError_t by_type(int64_t type, F fill, cudaStream_t s) {
   return by_taps<__half, DIR>(fill(__half{}), s);
 }
 
-int64_t back_parts(int64_t B, int64_t L) {
-  return (B * ((L + kRunBack - 1) / kRunBack) + kWarps - 1) / kWarps;
+int64_t back_parts(int64_t B, int64_t L, int64_t H) {
+  const int64_t run = back_run(B, L, H);
+  return (B * ((L + run - 1) / run) + kWarps - 1) / kWarps;
 }
 
 }  // namespace
 
 // No more blocks than this to a launch.
 int64_t conv_blocks(int64_t B, int64_t L, int64_t H) {
-  return ((B * ((L + kRun - 1) / kRun) + kWarps - 1) / kWarps) * ((H + 31) / 32);
+  return ((B * ((L + 7) / 8) + kWarps - 1) / kWarps) * ((H + 31) / 32);
 }
 
 size_t conv_backward_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t K) {
-  return (size_t)((K + 1) * back_parts(B, L) * H) * 4;
+  return (size_t)((K + 1) * back_parts(B, L, H) * H) * 4;
 }
 
 cudaError_t launch_conv(const ssm_conv_args& a, cudaStream_t s) {
@@ -400,13 +495,13 @@ cudaError_t launch_conv(const ssm_conv_args& a, cudaStream_t s) {
     q.y = view<T>{static_cast<T*>(a.y.data), a.y.stride_b, a.y.stride_t};
     q.w = a.w, q.bias = a.bias, q.reset = a.reset;
     q.state = static_cast<const T*>(a.state), q.last = static_cast<T*>(a.last);
-    q.runs = (a.L + kRun - 1) / kRun;
+    q.run = forward_run(a.B, a.L, a.H), q.runs = (a.L + q.run - 1) / q.run;
     return q;
   }, s);
 }
 
 cudaError_t launch_conv_backward(const ssm_conv_backward_args& a, cudaStream_t s) {
-  const int64_t parts = back_parts(a.B, a.L);
+  const int64_t parts = back_parts(a.B, a.L, a.H);
   const cudaError_t e = by_type<kBack>(a.type, [&](auto t) {
     using T = decltype(t);
     conv_params<T> q{};
@@ -418,7 +513,7 @@ cudaError_t launch_conv_backward(const ssm_conv_backward_args& a, cudaStream_t s
     q.state = static_cast<const T*>(a.state), q.dlast = static_cast<const T*>(a.dlast);
     q.dstate = static_cast<T*>(a.dstate);
     q.part = static_cast<float*>(a.workspace), q.parts = parts;
-    q.runs = (a.L + kRunBack - 1) / kRunBack;
+    q.run = back_run(a.B, a.L, a.H), q.runs = (a.L + q.run - 1) / q.run;
     return q;
   }, s);
   if (e != cudaSuccess) return e;
