@@ -123,6 +123,18 @@ __device__ __forceinline__ void taps(piece<VE> (&w)[KM], piece<VE>& bias, const 
 #pragma unroll
   for (int i = 0; i < VE; ++i) v[i] = q.bias ? q.bias[c + i] : 0.0f;
   bias.set(v);
+  if (KM == 4 && q.K == 4 && (reinterpret_cast<uintptr_t>(q.w) & 15) == 0) {
+    float4 t[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) t[i] = *reinterpret_cast<const float4*>(q.w + (c + i) * 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) v[i] = j == 0 ? t[i].w : j == 1 ? t[i].z : j == 2 ? t[i].y : t[i].x;
+      w[j < KM ? j : 0].set(v);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < KM; ++j) {
 #pragma unroll
@@ -388,28 +400,38 @@ __global__ void __launch_bounds__(256) conv_sums(const float* part, float* dw, f
     dbias[c] = v;
 }
 
-// A block goes over a run of channels of several batch entries.
-template <typename T, int VE, int KM>
+// A thread has its channels of R batch entries, so that the taps, 16 bytes a channel where an entry's
+// inputs and output are 10 (K = 4 in 16 bits), are read once for all of them.
+template <typename T, int VE, int KM, int R>
 __global__ void __launch_bounds__(128) conv_step(conv_params<T> q) {
   const int64_t c = ((int64_t)(blockIdx.x % q.columns) * 32 + (threadIdx.x & 31)) * VE;
-  const int64_t b = (int64_t)(blockIdx.x / q.columns) * 4 + (threadIdx.x >> 5);
-  if (b >= q.B || c >= q.H) return;
-  piece<VE> w[KM], bias, win[KM];
-  const bool fresh = q.reset && q.reset[b] != 0;
+  const int64_t b0 = ((int64_t)(blockIdx.x / q.columns) * 4 + (threadIdx.x >> 5)) * R;
+  if (b0 >= q.B || c >= q.H) return;
+  piece<VE> w[KM], bias, win[R][KM];
 #pragma unroll
-  for (int j = 0; j < KM; ++j) {
-    win[j].clear();
-    if (j == 0 || (j < q.K && !fresh)) input<T, VE>(win[j], q, b, -j, c);
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = min(b0 + r, q.B - 1);
+    const bool fresh = q.reset && q.reset[b] != 0;
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+      win[r][j].clear();
+      if (j == 0 || (j < q.K && !fresh)) input<T, VE>(win[r][j], q, b, -j, c);
+    }
   }
   taps<T, VE, KM>(w, bias, q, c);
-  piece<VE> o = bias;
 #pragma unroll
-  for (int j = 0; j < KM; ++j) o.fma(w[j], win[j]);
-  if (q.act == SSM_ACT_SILU) o.silu();
-  o.put(q.y.row(b, 0) + c);
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = b0 + r;
+    if (b >= q.B) return;
+    piece<VE> o = bias;
 #pragma unroll
-  for (int j = 0; j < KM - 1; ++j)
-    if (j < q.K - 1) win[j].put(q.last + (b * (q.K - 1) + q.K - 2 - j) * q.H + c);
+    for (int j = 0; j < KM; ++j) o.fma(w[j], win[r][j]);
+    if (q.act == SSM_ACT_SILU) o.silu();
+    o.put(q.y.row(b, 0) + c);
+#pragma unroll
+    for (int j = 0; j < KM - 1; ++j)
+      if (j < q.K - 1) win[r][j].put(q.last + (b * (q.K - 1) + q.K - 2 - j) * q.H + c);
+  }
 }
 
 // Whether rows of H channels go in pieces of `bytes`: every row begins on a multiple of it.
@@ -431,7 +453,11 @@ template <typename T, int VE, int KM, bool EXACT, Dir DIR>
 void go(conv_params<T> q, cudaStream_t s) {
   q.columns = (unsigned)((q.H + 32 * VE - 1) / (32 * VE));
   if constexpr (DIR == kStep) {
-    conv_step<T, VE, KM><<<q.columns * (unsigned)((q.B + 3) / 4), 128, 0, s>>>(q);
+    // four entries to a thread where that leaves every SM its warps
+    if (KM == 4 && (int64_t)q.columns * q.B >= 4 * 152 * 8)
+      conv_step<T, VE, KM, 4><<<q.columns * (unsigned)((q.B + 15) / 16), 128, 0, s>>>(q);
+    else
+      conv_step<T, VE, KM, 1><<<q.columns * (unsigned)((q.B + 3) / 4), 128, 0, s>>>(q);
   } else {
     const unsigned grid = q.columns * (unsigned)((q.B * q.runs + kWarps - 1) / kWarps);
     if constexpr (DIR == kForward)

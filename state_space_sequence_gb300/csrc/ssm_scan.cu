@@ -280,70 +280,97 @@ struct step_params {
   float* h_out;
 };
 
-// LN lanes to a channel, 4 states to a lane. The states go through memory once
-// each way and are all there is to it: 134 MB at 256 x 4096 x 16.
-template <typename T, int LN, bool QUADS>
+// LN lanes to a channel, 4 states to a lane, of R batch entries (the rates are then read once for all
+// of them). The states go through memory once each way and are all there is to it: 134 MB at 256 x
+// 4096 x 16.
+template <typename T, int LN, bool QUADS, int R>
 __global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
-  const int lane = threadIdx.x & 31, at = lane % LN, n0 = 4 * at;
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LN;
-  const bool there = unit < (int64_t)q.B * q.H;
-  const int64_t b = there ? unit / q.H : 0;
-  const int c = there ? (int)(unit - b * q.H) : 0, group = c / q.Hg;
-  float s = to_f(q.dt.row(b, 0)[c]) + (q.bias ? q.bias[c] : 0.0f);
-  if (q.softplus) s = softplus2(two(s)).x;
-  const float x = to_f(q.x.row(b, 0)[c]), u = s * x;
-  const bool fresh = q.reset && q.reset[b];
-  float A[4], h[4], Bm[4], Cm[4];
-  const int64_t o = (b * q.H + c) * q.N + n0;
-  const T* pb = q.Bm.row(b, 0) + (int64_t)group * q.N + n0;
-  const T* pc = q.Cm.row(b, 0) + (int64_t)group * q.N + n0;
-  if (QUADS) {
-    load_floats<4>(A, q.A + (int64_t)c * q.N + n0);
-    load_floats<4>(h, q.h + o);
-  } else {
+  const unsigned columns = (unsigned)(q.H + 256 / LN - 1) / (256 / LN);
+  const int at = threadIdx.x % LN, n0 = 4 * at;
+  const int c0 = (int)(blockIdx.x % columns) * (256 / LN) + threadIdx.x / LN, c = min(c0, q.H - 1);
+  const int64_t b0 = (int64_t)(blockIdx.x / columns) * R;
+  const int group = c / q.Hg;
+  float2 rate[2], h[R][2], bm[R][2], cm[R][2];
+  float s[R], x[R], z[R];
+  auto quad = [&](float2 (&v)[2], const float* p) {
+    const float4 t = get_quad(p, n0, q.N, QUADS);
+    v[0] = make_float2(t.x, t.y);
+    v[1] = make_float2(t.z, t.w);
+  };
+  auto map = [&](float2 (&v)[2], const T* p) {
+    float t[4];
+    if constexpr (QUADS) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      A[j] = n0 + j < q.N ? q.A[(int64_t)c * q.N + n0 + j] : 0.0f;
-      h[j] = n0 + j < q.N ? q.h[o + j] : 0.0f;
+      for (int j = 0; j < 4; ++j) t[j] = to_f(p[n0 + j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] = n0 + j < q.N ? to_f(p[n0 + j]) : 0.0f;
     }
-  }
-  float acc = 0.0f;
+    v[0] = make_float2(t[0], t[1]);
+    v[1] = make_float2(t[2], t[3]);
+  };
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    Bm[j] = QUADS || n0 + j < q.N ? to_f(pb[j]) : 0.0f;
-    Cm[j] = QUADS || n0 + j < q.N ? to_f(pc[j]) : 0.0f;
-    const float a = expf(s * A[j]);
-    h[j] = fresh ? u * Bm[j] : fmaf(a, h[j], u * Bm[j]);
-    acc = fmaf(h[j], Cm[j], acc);
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = min(b0 + r, q.B - 1);
+    quad(h[r], q.h + (b * q.H + c) * q.N);
+    if (q.reset && q.reset[b]) h[r][0] = h[r][1] = two(0.0f);
+    s[r] = to_f(q.dt.row(b, 0)[c]);
+    x[r] = to_f(q.x.row(b, 0)[c]);
+    z[r] = q.z.p ? to_f(q.z.row(b, 0)[c]) : 0.0f;
+    map(bm[r], q.Bm.row(b, 0) + (int64_t)group * q.N);
+    map(cm[r], q.Cm.row(b, 0) + (int64_t)group * q.N);
   }
+  quad(rate, q.A + (int64_t)c * q.N);
+  rate[0] = mul2(rate[0], two(kLog2e));
+  rate[1] = mul2(rate[1], two(kLog2e));
+  const float bias = q.bias ? q.bias[c] : 0.0f, D = q.D ? q.D[c] : 0.0f;
 #pragma unroll
-  for (int d = 1; d < LN; d *= 2) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-  if (!there) return;
-  if (QUADS) {
-    store_floats<4>(q.h_out + o, h);
-  } else {
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = b0 + r;
+    s[r] += bias;
+    if (q.softplus) s[r] = softplus2(two(s[r])).x;
+    float2 acc;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n0 + j < q.N) q.h_out[o + j] = h[j];
+    for (int p = 0; p < 2; ++p) {
+      const decay<sizeof(T) == 4> a(rate[p], two(s[r]));
+      h[r][p] = a.of_plus(h[r][p], mul2(bm[r][p], two(s[r] * x[r])));
+      acc = p ? fma2(h[r][p], cm[r][p], acc) : mul2(h[r][p], cm[r][p]);
+    }
+    float o = acc.x + acc.y;
+#pragma unroll
+    for (int d = 1; d < LN; d *= 2) o += __shfl_xor_sync(0xffffffffu, o, d);
+    if (b >= q.B || c0 >= q.H) continue;
+    float* to = q.h_out + (b * q.H + c) * q.N + n0;
+    if constexpr (QUADS) {
+      *reinterpret_cast<float4*>(to) =
+          make_float4(h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y);
+    } else {
+      const float v[4] = {h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n0 + j < q.N) to[j] = v[j];
+    }
+    if (at) continue;
+    if (q.D) o = fmaf(D, x[r], o);
+    if (q.z.p) o *= z[r] * glr::sigmoid(z[r]);
+    q.y.row(b, 0)[c] = from_f<T>(o);
   }
-  if (at) return;
-  if (q.D) acc = fmaf(q.D[c], x, acc);
-  if (q.z.p) {
-    const float z = to_f(q.z.row(b, 0)[c]);
-    acc *= z * glr::sigmoid(z);
-  }
-  q.y.row(b, 0)[c] = from_f<T>(acc);
 }
 
 template <typename T, int LN>
 cudaError_t run_step(const step_params<T>& q, cudaStream_t s) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(q.A) | reinterpret_cast<uintptr_t>(q.h) |
                         reinterpret_cast<uintptr_t>(q.h_out);
-  const unsigned grid = (unsigned)((q.B * q.H * LN + 255) / 256);
-  if (q.N == 4 * LN && (all & 15) == 0)
-    step_kernel<T, LN, true><<<grid, 256, 0, s>>>(q);
-  else
-    step_kernel<T, LN, false><<<grid, 256, 0, s>>>(q);
+  const unsigned columns = (unsigned)((q.H + 256 / LN - 1) / (256 / LN));
+  if (q.N == 4 * LN && (all & 15) == 0) {
+    // two entries to a thread where that leaves every SM some blocks
+    if (columns * q.B >= 2 * 152 * 4)
+      step_kernel<T, LN, true, 2><<<columns * (unsigned)((q.B + 1) / 2), 256, 0, s>>>(q);
+    else
+      step_kernel<T, LN, true, 1><<<columns * (unsigned)q.B, 256, 0, s>>>(q);
+  } else {
+    step_kernel<T, LN, false, 1><<<columns * (unsigned)q.B, 256, 0, s>>>(q);
+  }
   return cudaGetLastError();
 }
 
