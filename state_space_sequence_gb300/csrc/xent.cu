@@ -11,7 +11,9 @@
 //
 // float32 goes through the same kernel: x = x0 + x1 + x2 with bfloat16 parts, exact to 2^-24, and
 // the six products of parts whose orders of magnitude add up to no less than 2^-16, the small ones
-// first. Products of parts are exact and accumulated in float32, as those of 16-bit inputs.
+// first. Products of parts are exact and accumulated in float32, as those of 16-bit inputs; but the
+// tensor core cuts off where it adds, a step of 16 of the sum at a time, and what that leaves out adds
+// up (5e-6 of dh at V = 4099), so for float32 every 64 steps the accumulator is added to a second one.
 #include <cuda.h>
 
 #include <algorithm>
@@ -47,6 +49,7 @@ constexpr size_t kSmem = 1024 + kBarOff + 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kThreads = 256;
 constexpr int kGroup = 16;  // rows of tiles that go through the columns together
+constexpr int kChunk = 16;  // float32: stages between additions to the second accumulator
 static_assert(kSmem <= 232448, "shared memory");
 
 enum Mode { kLoss, kGrad, kRows, kColumns };
@@ -67,8 +70,7 @@ struct gemm_args {
   const float* scale;  // {2^k, 2^-k} of float16's d, or null
   float2* stats;       // kLoss: [column of tiles, M] maximum and sum
   float* hit;          // kLoss: [M] the target's logit
-  float* acc;          // kRows: float32 [M, N], the sum over the pieces so far
-  int has_acc, keep;   // read acc; write acc instead of out
+  int keep;            // kRows: 1 store the sums (float32, at tmC), 2 add them to those there
   void* out;
   int64_t out_stride;
   int* status;
@@ -100,14 +102,16 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&b)[3]) {
   b[2] = __float2bfloat16_rn(r - __bfloat162float(b[1]));
 }
 
-// T: the operands' type (bfloat16 also for float32's parts); O: the type of out, kGrad: float means
-// that d is stored in three parts. Warp 0 loads, warp 1 issues the products, warp 2 has the tensor
+// T: the operands' type (bfloat16 also for float32's parts); O: the inputs' own, float for parts, in
+// three of which kGrad then stores d. Warp 0 loads, warp 1 issues the products, warp 2 has the tensor
 // memory, warps 4-7 read the accumulators; two accumulators take turns.
 template <Mode MODE, typename T, typename O>
 __global__ void __launch_bounds__(kThreads, 1)
 xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
       const __grid_constant__ CUtensorMap tmC, const gemm_args g) {
   constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
+  // float32: accumulator 0 works, 1 keeps; otherwise they take turns
+  constexpr bool kKeeps = sizeof(O) == 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -181,27 +185,34 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         (sizeof(T) == 2 && glr::is_half<T> ? tc::idesc_f16_f32(kBM, kBN)
                                            : tc::idesc_bf16_f32(kBM, kBN)) |
         (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
-    uint32_t it = 0, local = 0;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++local) {
-      const uint32_t acc = local & 1;
-      if (local >= 2 && !(ok = tc::mbar_wait(&acc_empty[acc], ((local >> 1) - 1) & 1))) break;
-      tc::fence_after_sync();
-      const uint32_t d = tmem + acc * kBN;
-      for (int k = 0; k < steps; ++k, ++it) {
-        const int s = it % kStages;
-        if (!(ok = tc::mbar_wait(&full[s], (it / kStages) & 1))) break;
+    uint32_t it = 0, local = 0;  // stages, accumulators handed over
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int k = 0; k < steps && ok;) {
+        const uint32_t acc = kKeeps ? 0 : local & 1, turns = kKeeps ? 1 : 2;
+        if (local >= turns && !(ok = tc::mbar_wait(&acc_empty[acc], (local / turns - 1) & 1))) break;
         tc::fence_after_sync();
-        const uint8_t* a = base + s * kStage;
-        const uint8_t* b = a + kABytes;
-        const uint64_t ad = kAmn ? tc::smem_desc_mn_sw128(a, 8192, 1024) : tc::smem_desc_k_sw128(a);
-        const uint64_t bd = kBmn ? tc::smem_desc_mn_sw128(b, 8192, 1024) : tc::smem_desc_k_sw128(b);
+        const uint32_t d = tmem + acc * kBN;
+        const int stop = kKeeps ? min(steps, k + kChunk) : steps;
+        for (int first = k; k < stop; ++k, ++it) {
+          const int s = it % kStages;
+          if (!(ok = tc::mbar_wait(&full[s], (it / kStages) & 1))) break;
+          tc::fence_after_sync();
+          const uint8_t* a = base + s * kStage;
+          const uint8_t* b = a + kABytes;
+          const uint64_t ad =
+              kAmn ? tc::smem_desc_mn_sw128(a, 8192, 1024) : tc::smem_desc_k_sw128(a);
+          const uint64_t bd =
+              kBmn ? tc::smem_desc_mn_sw128(b, 8192, 1024) : tc::smem_desc_k_sw128(b);
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk)  // 16 of the sum: 32 bytes of a row, or 16 rows
-          tc::mma_kind_f16(d, ad + (kAmn ? 128 : 2) * kk, bd + (kBmn ? 128 : 2) * kk, idesc,
-                           (k | kk) != 0);
-        tc::mma_commit(&empty[s]);
+          for (int kk = 0; kk < kBK / 16; ++kk)  // 16 of the sum: 32 bytes of a row, or 16 rows
+            tc::mma_kind_f16(d, ad + (kAmn ? 128 : 2) * kk, bd + (kBmn ? 128 : 2) * kk, idesc,
+                             k != first || kk != 0);
+          tc::mma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&acc_full[acc]);
+        ++local;
       }
-      tc::mma_commit(&acc_full[acc]);
     }
   } else if (warp >= 4) {
     const int q = warp - 4;
@@ -209,13 +220,11 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
     uint32_t local = 0, boxed = 0;
     float scale = 1.0f, unscale = 1.0f;
     if (g.scale) scale = g.scale[0], unscale = g.scale[1];
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++local) {
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       int mi, ni;
       tile_at(t, mt, nt, mi, ni);
-      const uint32_t acc = local & 1;
       const int m0 = mi * kBM + q * 32, n0 = ni * kBN, row = m0 + lane;
       const int cols = min(kBN, g.N - n0);
-      const uint32_t tcol = tmem + acc * kBN + (uint32_t(q * 32) << 16);
       // what a row brings, fetched before the accumulator is waited for
       int64_t target = -1;
       float lse = 0.0f, weight = 0.0f;
@@ -230,14 +239,55 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
       }
       const bool counts = target >= 0 && target < g.V;
       const int64_t at = counts ? target - g.v0 - n0 : -1;  // its column within the tile
-      if (!(ok = warp_wait(&acc_full[acc], (local >> 1) & 1))) break;
+      const uint32_t lanes = uint32_t(q * 32) << 16;
+      // float32: all but the last chunk to the second accumulator
+      const int chunks = kKeeps ? (steps + kChunk - 1) / kChunk : 1;
+      if constexpr (kKeeps) {
+        for (int c = 0; c + 1 < chunks && ok; ++c, ++local) {
+          if (!(ok = warp_wait(&acc_full[0], local & 1))) break;
+          tc::fence_after_sync();
+          for (int i = 0; i < kBN; i += 16) {
+            uint32_t v[16], w[16];
+            tc::tmem_ld16_issue(tmem + lanes + i, v);
+            if (c) tc::tmem_ld16_issue(tmem + lanes + kBN + i, w);
+            tc::tmem_wait_ld16(v);
+            if (c) {
+              tc::tmem_wait_ld16(w);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
+            }
+            tc::tmem_st16(tmem + lanes + kBN + i, v);
+          }
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&acc_empty[0]);
+        }
+        if (!ok) break;
+      }
+      const uint32_t acc = kKeeps ? 0 : local & 1;
+      const uint32_t tcol = tmem + acc * kBN + lanes;
+      auto load = [&](int c, float (&v)[32]) {
+        tc::tmem_ld32(tcol + c, v);
+        if constexpr (kKeeps) {
+          if (chunks > 1) {
+            float w[32];
+            tc::tmem_ld32(tcol + kBN + c, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += w[i];
+          }
+        }
+      };
+      if (!(ok = warp_wait(&acc_full[acc], kKeeps ? local & 1 : (local >> 1) & 1))) break;
+      ++local;
       tc::fence_after_sync();
       if constexpr (MODE == kLoss) {
         float top = -INFINITY, sum = 0.0f;
         for (int c = 0; c < kBN; c += 32) {
           if (c >= cols) break;
           float v[32];
-          tc::tmem_ld32(tcol + c, v);
+          load(c, v);
           if (cols - c < 32)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = i < cols - c ? v[i] : -INFINITY;
@@ -267,8 +317,8 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
           float v[64];
           {
             float lo[32], hi[32];
-            tc::tmem_ld32(tcol + c * 64, lo);
-            tc::tmem_ld32(tcol + c * 64 + 32, hi);
+            load(c * 64, lo);
+            load(c * 64 + 32, hi);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = lo[i], v[32 + i] = hi[i];
           }
@@ -312,38 +362,55 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
           }
         }
       } else {
-        // float32 sums to rows of out, through shared memory so that a row's 32 go together
-        float* box = reinterpret_cast<float*>(boxes);
-        for (int c = 0; c < cols; c += 32) {
+        const uint32_t sw = uint32_t(lane & 7);
+        for (int c = 0; c < cols; c += 32, ++boxed) {
           float v[32];
-          tc::tmem_ld32(tcol + c, v);
+          load(c, v);
           if (c + 32 >= cols) {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
           }
+          if (MODE == kRows && g.keep) {  // float32 sums, to be added up over the pieces
+            uint8_t* box = boxes + (boxed % kBoxes) * kBox;
+            if (lane == 0) tc::bulk_wait_group_read<kBoxes - 1>();  // its last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(box + lane * 128 + ((uint32_t(k) ^ sw) << 4)) =
+                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (m0 < g.M) {
+                if (g.keep == 1)
+                  tc::tma_store_3d(&tmC, box, n0 + c, m0, 0);
+                else
+                  tc::tma_reduce_add_3d(&tmC, box, n0 + c, m0, 0);
+              }
+              tc::bulk_commit_group();
+            }
+            continue;
+          }
+          // to rows of out, through shared memory so that a row's 32 go together
+          float* box = reinterpret_cast<float*>(boxes);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; ++i) box[lane * 33 + i] = v[i];
           __syncwarp();
           const int col = n0 + c + lane;
           if (col < g.N) {
+            O* to = static_cast<O*>(g.out) + (int64_t)m0 * g.out_stride + col;
 #pragma unroll 8
             for (int r = 0; r < 32; ++r) {
               if (m0 + r >= g.M) break;
-              const int64_t m = m0 + r;
-              float o = box[r * 33 + lane];
-              if (g.has_acc) o += g.acc[m * g.N + col];
-              if (g.keep)
-                g.acc[m * g.N + col] = o;
-              else
-                static_cast<O*>(g.out)[m * g.out_stride + col] = from_f<O>(o * unscale);
+              to[r * g.out_stride] = from_f<O>(box[r * 33 + lane] * unscale);
             }
           }
         }
       }
     }
-    if (MODE == kGrad && lane == 0) tc::bulk_wait_group0();
+    if ((MODE == kGrad || MODE == kRows) && lane == 0) tc::bulk_wait_group0();
   }
   if (!ok) report_status(g.status, DLR_ERR_TIMEOUT);
   tc::fence_before_sync();
@@ -376,6 +443,22 @@ finish_loss(const float2* stats, const float* hit, const int64_t* target, float*
   const int64_t t = target[m];
   lse[m] = total;
   loss[m] = t >= 0 && t < V ? total - hit[m] : 0.0f;
+}
+
+// The sums over the pieces in the inputs' type.
+template <typename O>
+__global__ void __launch_bounds__(256)
+finish_rows(const float* acc, int64_t pitch, O* out, int64_t stride, int64_t M, int64_t D,
+            const float* scale) {
+  const int64_t per = (D + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = i / per, c = (i - m * per) * 4;
+  if (m >= M) return;
+  const float k = scale ? scale[1] : 1.0f;
+  const float4 v = *reinterpret_cast<const float4*>(acc + m * pitch + c);
+  const float o[4] = {v.x * k, v.y * k, v.z * k, v.w * k};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c + j < D) out[m * stride + c + j] = from_f<O>(o[j]);
 }
 
 // The power of two by which float16's d is scaled, from the largest |dloss| of a row that counts.
@@ -444,16 +527,16 @@ __global__ void clear_rows(void* dst, int64_t rows, int64_t bytes, int64_t strid
 
 // ---- host ---------------------------------------------------------------------------------
 
-// [parts, rows, cols] of 16-bit values, rows `pitch` elements apart, in boxes of box_rows x 64
-// (128 bytes, swizzled).
-bool make_map(CUtensorMap* m, const void* p, bool half, uint64_t parts, uint64_t rows, uint64_t cols,
-              uint64_t pitch, uint32_t box_rows) {
+// [parts, rows, cols], rows `pitch` elements apart, in boxes of box_rows x 128 bytes (swizzled).
+bool make_map(CUtensorMap* m, const void* p, CUtensorMapDataType type, uint64_t parts, uint64_t rows,
+              uint64_t cols, uint64_t pitch, uint32_t box_rows) {
   auto fn = tc::tensor_map_encoder();
   if (!fn) return false;
+  const uint64_t size = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   cuuint64_t dims[3] = {cols, rows, parts};
-  cuuint64_t strides[2] = {pitch * 2, rows * pitch * 2};
-  cuuint32_t box[3] = {64, box_rows, 1}, one[3] = {1, 1, 1};
-  return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  cuuint64_t strides[2] = {pitch * size, rows * pitch * size};
+  cuuint32_t box[3] = {uint32_t(128 / size), box_rows, 1}, one[3] = {1, 1, 1};
+  return fn(m, type, 3,
             const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -476,15 +559,17 @@ struct operand {
 template <Mode MODE, typename T, typename O>
 cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_args g,
                     cudaStream_t s) {
-  constexpr bool kHalf = glr::is_half<T>;
+  constexpr auto kType = glr::is_half<T> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
   CUtensorMap ma, mb, mc;
-  if (!make_map(&ma, a.p, kHalf, a.parts, a.rows, a.cols, a.pitch, kAmn ? kBK : kBM) ||
-      !make_map(&mb, b.p, kHalf, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : kBN))
+  if (!make_map(&ma, a.p, kType, a.parts, a.rows, a.cols, a.pitch, kAmn ? kBK : kBM) ||
+      !make_map(&mb, b.p, kType, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : kBN))
     return cudaErrorInvalidValue;
   if (!c)
     mc = ma;  // not used
-  else if (!make_map(&mc, c->p, kHalf, c->parts, c->rows, c->cols, c->pitch, 32))
+  else if (!make_map(&mc, c->p, MODE == kRows ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kType, c->parts,
+                     c->rows, c->cols, c->pitch, 32))
     return cudaErrorInvalidValue;
   g.status = device_status_word();
   const cudaError_t e = max_smem_once<xgemm<MODE, T, O>>(kSmem);
@@ -541,15 +626,27 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
   const int64_t parts = type == GLR_F32 ? 3 : 1;
   back_plan p;
+  // A piece's d takes at most kPieceBytes. Of the piece counts from the least to twice as many, the
+  // one whose three products leave the fewest SMs without a tile (in stages; a launch costs some
+  // forty).
+  auto tiles = [](int64_t rows, int64_t cols) {
+    return up(((rows + kBM - 1) / kBM) * ((cols + kBN - 1) / kBN), 152) / 152;
+  };
   const int64_t most = std::max<int64_t>(kBN, kPieceBytes / (M * 2 * parts) / kBN * kBN);
-  p.pieces = (V + most - 1) / most;
-  p.piece = up((V + p.pieces - 1) / p.pieces, kBN);
-  p.pieces = (V + p.piece - 1) / p.piece;
+  const int64_t least = (V + most - 1) / most;
+  int64_t best = -1;
+  for (int64_t n = least; n <= 2 * least; ++n) {
+    const int64_t piece = up((V + n - 1) / n, kBN), pieces = (V + piece - 1) / piece;
+    const int64_t cost = pieces * (tiles(M, piece) * (D + kBK - 1) / kBK +
+                                   tiles(M, D) * (piece + kBK - 1) / kBK +
+                                   tiles(piece, D) * (M + kBK - 1) / kBK + 3 * 40);
+    if (best < 0 || cost < best) best = cost, p.piece = piece, p.pieces = pieces;
+  }
   p.d = 0;
   p.h = p.d + up(parts * M * std::min(p.piece, up(V, 8)) * 2, 256);
   p.w = p.h + staged(type, M, D);
   p.acc = p.w + staged(type, V, D);
-  p.scale = p.acc + (p.pieces > 1 ? up(M * D * 4, 256) : 0);
+  p.scale = p.acc + (p.pieces > 1 ? up(M * up(D, 4) * 4, 256) : 0);
   p.bytes = p.scale + 256;
   return p;
 }
@@ -569,7 +666,7 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = rows_of<T, S>(a.type, a.W, ws + staged(a.type, a.M, a.D), a.V, a.D, &w, s);
   if (e != cudaSuccess) return e;
-  if ((e = product<kLoss, T, T>(h, w, nullptr, g, s)) != cudaSuccess) return e;
+  if ((e = product<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
   finish_loss<<<(unsigned)((a.M + 31) / 32), 256, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse,
                                                           a.M, nt, a.V);
   return cudaGetLastError();
@@ -605,10 +702,10 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
       gemm_args r{};
       r.M = (int)a.M, r.N = (int)a.D, r.K = (int)cols, r.products = g.products, r.b_row = (int)v0;
       r.scale = scale;
-      r.acc = reinterpret_cast<float*>(ws + p.acc);
-      r.has_acc = k > 0, r.keep = k + 1 < p.pieces;
       r.out = a.dh.data, r.out_stride = a.dh.stride_t;
-      if ((e = product<kRows, T, S>(d, w, nullptr, r, s)) != cudaSuccess) return e;
+      r.keep = p.pieces == 1 ? 0 : k == 0 ? 1 : 2;
+      const operand acc{ws + p.acc, 1, (uint64_t)a.M, (uint64_t)a.D, (uint64_t)up(a.D, 4)};
+      if ((e = product<kRows, T, S>(d, w, r.keep ? &acc : nullptr, r, s)) != cudaSuccess) return e;
     }
     if (a.dW.data) {
       gemm_args c{};
@@ -617,6 +714,13 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
       c.out = static_cast<S*>(a.dW.data) + v0 * a.dW.stride_t, c.out_stride = a.dW.stride_t;
       if ((e = product<kColumns, T, S>(d, hz, nullptr, c, s)) != cudaSuccess) return e;
     }
+  }
+  if (a.dh.data && p.pieces > 1) {
+    const int64_t n = a.M * ((a.D + 3) / 4);
+    finish_rows<S><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
+        reinterpret_cast<const float*>(ws + p.acc), up(a.D, 4), static_cast<S*>(a.dh.data),
+        a.dh.stride_t, a.M, a.D, scale);
+    return cudaGetLastError();
   }
   return cudaSuccess;
 }
