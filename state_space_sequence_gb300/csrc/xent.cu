@@ -60,6 +60,8 @@ __device__ __constant__ const int8_t kPartB[6] = {2, 0, 1, 1, 0, 0};
 
 struct gemm_args {
   int M, N, K;
+  int bn;              // columns of a tile, at most kBN (kLoss, kGrad)
+  int splits, k_split; // kRows: parts of the sum, each of k_split, that go to float32 sums of their own
   int products;        // 1, or 6 for float32
   int b_row;           // where the piece begins among W's rows
   int v0;              // first column's place in the vocabulary (kLoss, kGrad)
@@ -122,9 +124,16 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
   uint64_t* acc_empty = acc_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt = (g.M + kBM - 1) / kBM, nt = (g.N + kBN - 1) / kBN;
-  const int64_t tiles = (int64_t)mt * nt;
-  const int nk = (g.K + kBK - 1) / kBK, steps = nk * g.products;
+  // all tiles have kBN columns and the whole sum, but where a few would leave SMs without one
+  const int bn = MODE == kLoss || MODE == kGrad ? g.bn : kBN;
+  const int mt = (g.M + kBM - 1) / kBM, nt = (g.N + bn - 1) / bn;
+  const int64_t tiles = (int64_t)mt * nt, work = MODE == kRows ? tiles * g.splits : tiles;
+  // stages of a tile's sum: nk(t) for each product, from k_from(t) on
+  auto k_from = [&](int64_t t) { return MODE == kRows ? (int)(t / tiles) * g.k_split : 0; };
+  auto stages = [&](int64_t t) {
+    const int k = MODE == kRows ? min(g.k_split, g.K - k_from(t)) : g.K;
+    return (k + kBK - 1) / kBK;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -149,18 +158,19 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
 
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int64_t t = blockIdx.x; t < work && ok; t += gridDim.x) {
       int mi, ni;
-      tile_at(t, mt, nt, mi, ni);
-      const int m0 = mi * kBM, n0 = ni * kBN;
+      tile_at(t % tiles, mt, nt, mi, ni);
+      const int m0 = mi * kBM, n0 = ni * bn, nk = stages(t), steps = nk * g.products;
+      const int from = k_from(t);
       for (int k = 0; k < steps; ++k, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !(ok = tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1))) break;
-        const int product = g.products == 1 ? 5 : k / nk, k0 = (k % nk) * kBK;
+        const int product = g.products == 1 ? 5 : k / nk, k0 = from + (k % nk) * kBK;
         const int pa = kPartA[product], pb = kPartB[product];
         uint8_t* a = base + s * kStage;
         uint8_t* b = a + kABytes;
-        tc::mbar_arrive_expect_tx(&full[s], kStage);
+        tc::mbar_arrive_expect_tx(&full[s], kABytes + bn * kBK * 2);
         if constexpr (kAmn) {
 #pragma unroll
           for (int i = 0; i < kBM / 64; ++i)
@@ -181,12 +191,12 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
     for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
       ok &= tc::mbar_wait(&full[j % kStages], (j / kStages) & 1);
   } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t idesc =
-        (sizeof(T) == 2 && glr::is_half<T> ? tc::idesc_f16_f32(kBM, kBN)
-                                           : tc::idesc_bf16_f32(kBM, kBN)) |
+    const uint32_t idesc =
+        (glr::is_half<T> ? tc::idesc_f16_f32(kBM, bn) : tc::idesc_bf16_f32(kBM, bn)) |
         (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
     uint32_t it = 0, local = 0;  // stages, accumulators handed over
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int64_t t = blockIdx.x; t < work && ok; t += gridDim.x) {
+      const int steps = stages(t) * g.products;
       for (int k = 0; k < steps && ok;) {
         const uint32_t acc = kKeeps ? 0 : local & 1, turns = kKeeps ? 1 : 2;
         if (local >= turns && !(ok = tc::mbar_wait(&acc_empty[acc], (local / turns - 1) & 1))) break;
@@ -220,11 +230,11 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
     uint32_t local = 0, boxed = 0;
     float scale = 1.0f, unscale = 1.0f;
     if (g.scale) scale = g.scale[0], unscale = g.scale[1];
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int64_t t = blockIdx.x; t < work && ok; t += gridDim.x) {
       int mi, ni;
-      tile_at(t, mt, nt, mi, ni);
-      const int m0 = mi * kBM + q * 32, n0 = ni * kBN, row = m0 + lane;
-      const int cols = min(kBN, g.N - n0);
+      tile_at(t % tiles, mt, nt, mi, ni);
+      const int m0 = mi * kBM + q * 32, n0 = ni * bn, row = m0 + lane;
+      const int cols = min(bn, g.N - n0);
       // what a row brings, fetched before the accumulator is waited for
       int64_t target = -1;
       float lse = 0.0f, weight = 0.0f;
@@ -241,7 +251,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
       const int64_t at = counts ? target - g.v0 - n0 : -1;  // its column within the tile
       const uint32_t lanes = uint32_t(q * 32) << 16;
       // float32: all but the last chunk to the second accumulator
-      const int chunks = kKeeps ? (steps + kChunk - 1) / kChunk : 1;
+      const int chunks = kKeeps ? (stages(t) * g.products + kChunk - 1) / kChunk : 1;
       if constexpr (kKeeps) {
         for (int c = 0; c + 1 < chunks && ok; ++c, ++local) {
           if (!(ok = warp_wait(&acc_full[0], local & 1))) break;
@@ -284,8 +294,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
       tc::fence_after_sync();
       if constexpr (MODE == kLoss) {
         float top = -INFINITY, sum = 0.0f;
-        for (int c = 0; c < kBN; c += 32) {
-          if (c >= cols) break;
+        for (int c = 0; c < cols; c += 32) {
           float v[32];
           load(c, v);
           if (cols - c < 32)
@@ -383,10 +392,11 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
             __syncwarp();
             if (lane == 0) {
               if (m0 < g.M) {
+                const int split = (int)(t / tiles);
                 if (g.keep == 1)
-                  tc::tma_store_3d(&tmC, box, n0 + c, m0, 0);
+                  tc::tma_store_3d(&tmC, box, n0 + c, m0, split);
                 else
-                  tc::tma_reduce_add_3d(&tmC, box, n0 + c, m0, 0);
+                  tc::tma_reduce_add_3d(&tmC, box, n0 + c, m0, split);
               }
               tc::bulk_commit_group();
             }
@@ -445,16 +455,21 @@ finish_loss(const float2* stats, const float* hit, const int64_t* target, float*
   loss[m] = t >= 0 && t < V ? total - hit[m] : 0.0f;
 }
 
-// The sums over the pieces in the inputs' type.
+// The sums over the pieces, and over the parts of each, in the inputs' type.
 template <typename O>
 __global__ void __launch_bounds__(256)
-finish_rows(const float* acc, int64_t pitch, O* out, int64_t stride, int64_t M, int64_t D,
+finish_rows(const float* acc, int64_t pitch, int splits, O* out, int64_t stride, int64_t M, int64_t D,
             const float* scale) {
   const int64_t per = (D + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = i / per, c = (i - m * per) * 4;
   if (m >= M) return;
   const float k = scale ? scale[1] : 1.0f;
-  const float4 v = *reinterpret_cast<const float4*>(acc + m * pitch + c);
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < splits; ++k) {
+    const float4 p = *reinterpret_cast<const float4*>(acc + (k * M + m) * pitch + c);
+    v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+  }
   const float o[4] = {v.x * k, v.y * k, v.z * k, v.w * k};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -564,7 +579,7 @@ cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_a
   constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
   CUtensorMap ma, mb, mc;
   if (!make_map(&ma, a.p, kType, a.parts, a.rows, a.cols, a.pitch, kAmn ? kBK : kBM) ||
-      !make_map(&mb, b.p, kType, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : kBN))
+      !make_map(&mb, b.p, kType, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : g.bn))
     return cudaErrorInvalidValue;
   if (!c)
     mc = ma;  // not used
@@ -574,13 +589,37 @@ cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_a
   g.status = device_status_word();
   const cudaError_t e = max_smem_once<xgemm<MODE, T, O>>(kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
+  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + g.bn - 1) / g.bn) * g.splits;
   xgemm<MODE, T, O><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, kSmem, s>>>(
       ma, mb, mc, g);
   return cudaGetLastError();
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+constexpr int64_t kSMs = 152;
+// Rounds of tiles of bn columns over the SMs.
+int64_t rounds(int64_t rows, int64_t cols, int64_t bn, int64_t splits = 1) {
+  return (((rows + kBM - 1) / kBM) * ((cols + bn - 1) / bn) * splits + kSMs - 1) / kSMs;
+}
+// Columns of a tile, a multiple of `step`: kBN, unless a last round would leave many SMs without one.
+// A narrow tile reads its rows of A as often as a wide one.
+int columns_of(int64_t rows, int64_t cols, int step) {
+  int best = kBN;
+  for (int bn = kBN; bn >= 128; bn -= step)
+    if (rounds(rows, cols, bn) * (bn + 32) < rounds(rows, cols, best) * (best + 32)) best = bn;
+  return best;
+}
+// Parts of the sum over K of the product for dh, where its tiles are few or would leave many SMs
+// without one in the last round. Each part ends with the sums' way out, some eight stages.
+int splits_of(int64_t rows, int64_t cols, int64_t K) {
+  const int64_t nk = (K + kBK - 1) / kBK;
+  int best = 1;
+  auto cost = [&](int64_t s) { return rounds(rows, cols, kBN, s) * ((nk + s - 1) / s + 8); };
+  for (int s = 2; s <= std::min<int64_t>(kSMs, nk); ++s)
+    if (cost(s) < cost(best)) best = s;
+  return (int)((nk + (nk + best - 1) / best - 1) / ((nk + best - 1) / best));  // none is empty
+}
 
 // Whether the products read a caller's rows as they lie: 16-bit values whose rows begin on multiples
 // of 16 bytes, one after the other.
@@ -619,34 +658,33 @@ cudaError_t rows_of(int64_t type, const glr_view& v, void* to, int64_t rows, int
 // How the gradients' vocabulary is cut, and where things lie in their workspace.
 struct back_plan {
   int64_t piece, pieces;         // columns of a piece
+  int64_t splits;                // parts of its sum for dh
   int64_t d, h, w, acc, scale;   // offsets
   int64_t bytes;
+  bool sums() const { return pieces > 1 || splits > 1; }  // dh goes through float32 sums
 };
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
   const int64_t parts = type == GLR_F32 ? 3 : 1;
   back_plan p;
   // A piece's d takes at most kPieceBytes. Of the piece counts from the least to twice as many, the
-  // one whose three products leave the fewest SMs without a tile (in stages; a launch costs some
-  // forty).
-  auto tiles = [](int64_t rows, int64_t cols) {
-    return up(((rows + kBM - 1) / kBM) * ((cols + kBN - 1) / kBN), 152) / 152;
-  };
+  // one whose three products take the fewest stages (a launch costs some forty).
   const int64_t most = std::max<int64_t>(kBN, kPieceBytes / (M * 2 * parts) / kBN * kBN);
   const int64_t least = (V + most - 1) / most;
   int64_t best = -1;
   for (int64_t n = least; n <= 2 * least; ++n) {
     const int64_t piece = up((V + n - 1) / n, kBN), pieces = (V + piece - 1) / piece;
-    const int64_t cost = pieces * (tiles(M, piece) * (D + kBK - 1) / kBK +
-                                   tiles(M, D) * (piece + kBK - 1) / kBK +
-                                   tiles(piece, D) * (M + kBK - 1) / kBK + 3 * 40);
-    if (best < 0 || cost < best) best = cost, p.piece = piece, p.pieces = pieces;
+    const int64_t s = splits_of(M, D, std::min(piece, V));
+    const int64_t cost = pieces * (rounds(M, piece, kBN) * (D + kBK - 1) / kBK +
+                                   rounds(M, D, kBN, s) * ((piece + kBK - 1) / kBK + s - 1) / s +
+                                   rounds(piece, D, kBN) * (M + kBK - 1) / kBK + 3 * 40);
+    if (best < 0 || cost < best) best = cost, p.piece = piece, p.pieces = pieces, p.splits = s;
   }
   p.d = 0;
   p.h = p.d + up(parts * M * std::min(p.piece, up(V, 8)) * 2, 256);
   p.w = p.h + staged(type, M, D);
   p.acc = p.w + staged(type, V, D);
-  p.scale = p.acc + (p.pieces > 1 ? up(M * up(D, 4) * 4, 256) : 0);
+  p.scale = p.acc + (p.sums() ? up(p.splits * M * up(D, 4) * 4, 256) : 0);
   p.bytes = p.scale + 256;
   return p;
 }
@@ -654,8 +692,9 @@ back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
 template <typename T, typename S>
 cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const int nt = (int)((a.V + kBN - 1) / kBN);
+  const int bn = columns_of(a.M, a.V, 16), nt = (int)((a.V + bn - 1) / bn);
   gemm_args g{};
+  g.bn = bn, g.splits = 1;
   g.M = (int)a.M, g.N = (int)a.V, g.K = (int)a.D, g.V = (int)a.V;
   g.products = sizeof(S) == 4 ? 6 : 1;
   g.target = a.target;
@@ -693,6 +732,7 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
     const int64_t v0 = k * p.piece, cols = std::min(p.piece, a.V - v0);
     const operand d{ws + p.d, parts, (uint64_t)a.M, (uint64_t)cols, (uint64_t)up(cols, 8)};
     gemm_args g{};
+    g.bn = columns_of(a.M, cols, 64), g.splits = 1;
     g.M = (int)a.M, g.N = (int)cols, g.K = (int)a.D, g.V = (int)a.V;
     g.products = sizeof(S) == 4 ? 6 : 1;
     g.b_row = g.v0 = (int)v0;
@@ -703,23 +743,27 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
       r.M = (int)a.M, r.N = (int)a.D, r.K = (int)cols, r.products = g.products, r.b_row = (int)v0;
       r.scale = scale;
       r.out = a.dh.data, r.out_stride = a.dh.stride_t;
-      r.keep = p.pieces == 1 ? 0 : k == 0 ? 1 : 2;
-      const operand acc{ws + p.acc, 1, (uint64_t)a.M, (uint64_t)a.D, (uint64_t)up(a.D, 4)};
+      // a short last piece may have fewer parts, and leaves the sums of the others as they are
+      r.bn = kBN, r.k_split = (int)up((cols + p.splits - 1) / p.splits, kBK);
+      r.splits = (int)((cols + r.k_split - 1) / r.k_split);
+      r.keep = !p.sums() ? 0 : k == 0 ? 1 : 2;
+      const operand acc{ws + p.acc, (uint64_t)p.splits, (uint64_t)a.M, (uint64_t)a.D, (uint64_t)up(a.D, 4)};
       if ((e = product<kRows, T, S>(d, w, r.keep ? &acc : nullptr, r, s)) != cudaSuccess) return e;
     }
     if (a.dW.data) {
       gemm_args c{};
+      c.bn = kBN, c.splits = 1;
       c.M = (int)cols, c.N = (int)a.D, c.K = (int)a.M, c.products = g.products;
       c.scale = scale;
       c.out = static_cast<S*>(a.dW.data) + v0 * a.dW.stride_t, c.out_stride = a.dW.stride_t;
       if ((e = product<kColumns, T, S>(d, hz, nullptr, c, s)) != cudaSuccess) return e;
     }
   }
-  if (a.dh.data && p.pieces > 1) {
+  if (a.dh.data && p.sums()) {
     const int64_t n = a.M * ((a.D + 3) / 4);
     finish_rows<S><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
-        reinterpret_cast<const float*>(ws + p.acc), up(a.D, 4), static_cast<S*>(a.dh.data),
-        a.dh.stride_t, a.M, a.D, scale);
+        reinterpret_cast<const float*>(ws + p.acc), up(a.D, 4), (int)p.splits,
+        static_cast<S*>(a.dh.data), a.dh.stride_t, a.M, a.D, scale);
     return cudaGetLastError();
   }
   return cudaSuccess;
@@ -728,7 +772,7 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
 }  // namespace
 
 size_t loss_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D) {
-  const int64_t nt = (V + kBN - 1) / kBN;
+  const int64_t bn = columns_of(M, V, 16), nt = (V + bn - 1) / bn;
   return (size_t)(up(nt * M * 8, 256) + up(M * 4, 256) + staged(type, M, D) + staged(type, V, D));
 }
 
