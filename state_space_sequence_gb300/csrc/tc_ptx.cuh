@@ -130,6 +130,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// The same tile to the L2 alone, not tracked.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // 2D tile store from shared memory to global (x innermost; x * element size a multiple of 16
 // bytes; both coordinates non-negative; the part of the box outside the tensor is not written),
 // tracked by the issuing thread's bulk group.

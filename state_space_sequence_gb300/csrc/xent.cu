@@ -137,7 +137,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&full[s], 2);
       tc::mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -156,34 +156,41 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
-  if (warp == 0 && lane == 0) {
+  if ((warp == 0 || warp == 3) && lane == 0) {
+    // warp 0 loads A's rows, warp 3 B's: with one thread for both the six copies of a stage took
+    // longer to issue than its products
+    const bool is_a = warp == 0;
+    const uint32_t bytes = is_a ? kABytes : bn * kBK * 2;
     uint32_t it = 0;
     for (int64_t t = blockIdx.x; t < work && ok; t += gridDim.x) {
       int mi, ni;
       tile_at(t % tiles, mt, nt, mi, ni);
-      const int m0 = mi * kBM, n0 = ni * bn, nk = stages(t), steps = nk * g.products;
-      const int from = k_from(t);
-      for (int k = 0; k < steps; ++k, ++it) {
-        const int s = it % kStages;
-        if (it >= kStages && !(ok = tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1))) break;
-        const int product = g.products == 1 ? 5 : k / nk, k0 = from + (k % nk) * kBK;
-        const int pa = kPartA[product], pb = kPartB[product];
-        uint8_t* a = base + s * kStage;
-        uint8_t* b = a + kABytes;
-        tc::mbar_arrive_expect_tx(&full[s], kABytes + bn * kBK * 2);
-        if constexpr (kAmn) {
+      const int m0 = mi * kBM, n0 = ni * bn, nk = stages(t), from = k_from(t);
+      for (int p = 0; p < g.products && ok; ++p) {
+        const int product = g.products == 1 ? 5 : p;
+        const int part = is_a ? kPartA[product] : kPartB[product];
+        for (int k = 0, k0 = from; k < nk; ++k, k0 += kBK, ++it) {
+          const uint32_t s = it % kStages;
+          if (it >= kStages && !(ok = tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1))) break;
+          uint8_t* to = base + s * kStage + (is_a ? 0 : kABytes);
+          tc::mbar_arrive_expect_tx(&full[s], bytes);
+          if (is_a) {
+            if constexpr (kAmn) {
 #pragma unroll
-          for (int i = 0; i < kBM / 64; ++i)
-            tc::tma_load_3d(a + i * 8192, &tmA, m0 + 64 * i, k0, pa, &full[s]);
-        } else {
-          tc::tma_load_3d(a, &tmA, k0, m0, pa, &full[s]);
-        }
-        if constexpr (kBmn) {
+              for (int i = 0; i < kBM / 64; ++i)
+                tc::tma_load_3d(to + i * 8192, &tmA, m0 + 64 * i, k0, part, &full[s]);
+            } else {
+              tc::tma_load_3d(to, &tmA, k0, m0, part, &full[s]);
+            }
+          } else {
+            if constexpr (kBmn) {
 #pragma unroll
-          for (int i = 0; i < kBN / 64; ++i)
-            tc::tma_load_3d(b + i * 8192, &tmB, n0 + 64 * i, g.b_row + k0, pb, &full[s]);
-        } else {
-          tc::tma_load_3d(b, &tmB, k0, g.b_row + n0, pb, &full[s]);
+              for (int i = 0; i < kBN / 64; ++i)
+                tc::tma_load_3d(to + i * 8192, &tmB, n0 + 64 * i, g.b_row + k0, part, &full[s]);
+            } else {
+              tc::tma_load_3d(to, &tmB, k0, g.b_row + n0, part, &full[s]);
+            }
+          }
         }
       }
     }
