@@ -63,6 +63,7 @@ struct gemm_args {
   int bn;              // columns of a tile, at most kBN (kLoss, kGrad)
   int splits, k_split; // kRows: parts of the sum, each of k_split, that go to float32 sums of their own
   int products;        // 1, or 6 for float32
+  int a_along, b_along;  // rows along the sum have their 64s as a dimension of the map
   int b_row;           // where the piece begins among W's rows
   int v0;              // first column's place in the vocabulary (kLoss, kGrad)
   const int64_t* target;
@@ -161,11 +162,16 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
     // longer to issue than its products
     const bool is_a = warp == 0;
     const uint32_t bytes = is_a ? kABytes : bn * kBK * 2;
+    const CUtensorMap* map = is_a ? &tmA : &tmB;
+    // rows along the sum: a box of 64 x 64 for each 64 of them, by one copy where the map has them as
+    // a dimension
+    const bool mn = is_a ? kAmn : kBmn, along = mn && (is_a ? g.a_along : g.b_along);
+    const int shift = is_a ? 0 : g.b_row;
     uint32_t it = 0;
     for (int64_t t = blockIdx.x; t < work && ok; t += gridDim.x) {
       int mi, ni;
       tile_at(t % tiles, mt, nt, mi, ni);
-      const int m0 = mi * kBM, n0 = ni * bn, nk = stages(t), from = k_from(t);
+      const int row = is_a ? mi * kBM : ni * bn, nk = stages(t), from = k_from(t);
       for (int p = 0; p < g.products && ok; ++p) {
         const int product = g.products == 1 ? 5 : p;
         const int part = is_a ? kPartA[product] : kPartB[product];
@@ -174,22 +180,13 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
           if (it >= kStages && !(ok = tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1))) break;
           uint8_t* to = base + s * kStage + (is_a ? 0 : kABytes);
           tc::mbar_arrive_expect_tx(&full[s], bytes);
-          if (is_a) {
-            if constexpr (kAmn) {
-#pragma unroll
-              for (int i = 0; i < kBM / 64; ++i)
-                tc::tma_load_3d(to + i * 8192, &tmA, m0 + 64 * i, k0, part, &full[s]);
-            } else {
-              tc::tma_load_3d(to, &tmA, k0, m0, part, &full[s]);
-            }
+          if (along) {
+            tc::tma_load_4d(to, map, 0, shift + k0, row / 64, part, &full[s]);
+          } else if (mn) {
+            for (uint32_t i = 0; i < bytes / 8192; ++i)
+              tc::tma_load_3d(to + i * 8192, map, row + 64 * i, shift + k0, part, &full[s]);
           } else {
-            if constexpr (kBmn) {
-#pragma unroll
-              for (int i = 0; i < kBN / 64; ++i)
-                tc::tma_load_3d(to + i * 8192, &tmB, n0 + 64 * i, g.b_row + k0, part, &full[s]);
-            } else {
-              tc::tma_load_3d(to, &tmB, k0, g.b_row + n0, part, &full[s]);
-            }
+            tc::tma_load_3d(to, map, k0, shift + row, part, &full[s]);
           }
         }
       }
@@ -255,7 +252,9 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         }
       }
       const bool counts = target >= 0 && target < g.V;
-      const int64_t at = counts ? target - g.v0 - n0 : -1;  // its column within the tile
+      // its column, if it is one of the tile's (slices of columns may reach past a narrow tile)
+      const int64_t in_tile = target - g.v0 - n0;
+      const int64_t at = counts && in_tile < bn ? in_tile : -1;
       const uint32_t lanes = uint32_t(q * 32) << 16;
       // float32: all but the last chunk to the second accumulator
       const int chunks = kKeeps ? (stages(t) * g.products + kChunk - 1) / kChunk : 1;
@@ -550,11 +549,22 @@ __global__ void clear_rows(void* dst, int64_t rows, int64_t bytes, int64_t strid
 // ---- host ---------------------------------------------------------------------------------
 
 // [parts, rows, cols], rows `pitch` elements apart, in boxes of box_rows x 128 bytes (swizzled).
+// `blocks` > 0: columns in 64s as a dimension of their own, `blocks` of them to a box of box_rows rows
+// each; then cols is a multiple of 64 or the rows are followed by as many elements as are missing.
 bool make_map(CUtensorMap* m, const void* p, CUtensorMapDataType type, uint64_t parts, uint64_t rows,
-              uint64_t cols, uint64_t pitch, uint32_t box_rows) {
+              uint64_t cols, uint64_t pitch, uint32_t box_rows, uint32_t blocks = 0) {
   auto fn = tc::tensor_map_encoder();
   if (!fn) return false;
   const uint64_t size = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+  if (blocks) {
+    cuuint64_t dims[4] = {64, rows, (cols + 63) / 64, parts};
+    cuuint64_t strides[3] = {pitch * 2, 128, rows * pitch * 2};
+    cuuint32_t box[4] = {64, box_rows, blocks, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, type, 4, const_cast<void*>(p), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   cuuint64_t dims[3] = {cols, rows, parts};
   cuuint64_t strides[2] = {pitch * size, rows * pitch * size};
   cuuint32_t box[3] = {uint32_t(128 / size), box_rows, 1}, one[3] = {1, 1, 1};
@@ -576,6 +586,8 @@ int sm_count() {
 struct operand {
   const void* p;
   uint64_t parts, rows, cols, pitch;
+  bool ours = false;  // rows are a multiple of 64 elements apart, in the workspace
+  bool blocks() const { return cols % 64 == 0 || ours; }
 };
 
 template <Mode MODE, typename T, typename O>
@@ -585,8 +597,11 @@ cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_a
                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
   CUtensorMap ma, mb, mc;
-  if (!make_map(&ma, a.p, kType, a.parts, a.rows, a.cols, a.pitch, kAmn ? kBK : kBM) ||
-      !make_map(&mb, b.p, kType, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : g.bn))
+  g.a_along = kAmn && a.blocks(), g.b_along = kBmn && b.blocks();
+  if (!make_map(&ma, a.p, kType, a.parts, a.rows, a.cols, a.pitch, kAmn ? kBK : kBM,
+                g.a_along ? kBM / 64 : 0) ||
+      !make_map(&mb, b.p, kType, b.parts, b.rows, b.cols, b.pitch, kBmn ? kBK : g.bn,
+                g.b_along ? kBN / 64 : 0))
     return cudaErrorInvalidValue;
   if (!c)
     mc = ma;  // not used
@@ -637,16 +652,16 @@ bool direct(int64_t type, const glr_view& v, int64_t rows, int64_t cols) {
 
 // Bytes of staged rows.
 int64_t staged(int64_t type, int64_t rows, int64_t cols) {
-  return up((type == GLR_F32 ? 3 : 1) * rows * up(cols, 8) * 2, 256);
+  return up((type == GLR_F32 ? 3 : 1) * rows * up(cols, 64) * 2, 256);
 }
 
 template <typename T, typename S>
 cudaError_t stage(const glr_view& v, void* to, int64_t rows, int64_t cols, const int64_t* target,
                   int64_t V, operand* out, cudaStream_t s) {
-  const int64_t pitch = up(cols, 8), n = rows * (pitch / 8);
+  const int64_t pitch = up(cols, 64), n = rows * (pitch / 8);
   stage_rows<T, S><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
       static_cast<const S*>(v.data), v.stride_t, static_cast<T*>(to), rows, cols, pitch, target, V);
-  *out = operand{to, sizeof(S) == 4 ? 3u : 1u, (uint64_t)rows, (uint64_t)cols, (uint64_t)pitch};
+  *out = operand{to, sizeof(S) == 4 ? 3u : 1u, (uint64_t)rows, (uint64_t)cols, (uint64_t)pitch, true};
   return cudaGetLastError();
 }
 
@@ -688,7 +703,7 @@ back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
     if (best < 0 || cost < best) best = cost, p.piece = piece, p.pieces = pieces, p.splits = s;
   }
   p.d = 0;
-  p.h = p.d + up(parts * M * std::min(p.piece, up(V, 8)) * 2, 256);
+  p.h = p.d + up(parts * M * std::min(p.piece, up(V, 64)) * 2, 256);
   p.w = p.h + staged(type, M, D);
   p.acc = p.w + staged(type, V, D);
   p.scale = p.acc + (p.sums() ? up(p.splits * M * up(D, 4) * 4, 256) : 0);
@@ -737,7 +752,7 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
   if ((e = rows_of<T, S>(a.type, a.W, ws + p.w, a.V, a.D, &w, s)) != cudaSuccess) return e;
   for (int64_t k = 0; k < p.pieces; ++k) {
     const int64_t v0 = k * p.piece, cols = std::min(p.piece, a.V - v0);
-    const operand d{ws + p.d, parts, (uint64_t)a.M, (uint64_t)cols, (uint64_t)up(cols, 8)};
+    const operand d{ws + p.d, parts, (uint64_t)a.M, (uint64_t)cols, (uint64_t)up(cols, 64), true};
     gemm_args g{};
     g.bn = columns_of(a.M, cols, 64), g.splits = 1;
     g.M = (int)a.M, g.N = (int)cols, g.K = (int)a.D, g.V = (int)a.V;
