@@ -144,7 +144,8 @@ dlr_status ssm_scan(const ssm_scan_args* args, dlr_stream_t stream);
  *   dx = s q + D g,   ddt = (x q + e) sigmoid(dt + dt_bias)  (softplus = 0: x q + e)
  *   dz = dy o silu'(z),   dBm = sum_h G s x,   dCm = sum_h g h_t   (over a group's channels)
  *   dA = sum s G a h_{t-1},   dD = sum g x,   ddt_bias = sum ddt,   dh0 = a_0 G_0
- * dBm, dCm: views [B, L, G N]. dA [H, N], dD, ddt_bias [H] and dh0 [B, H, N] are float32; dD is
+ * Where an input is not finite and no step near it is marked, the dBm and dCm of the steps of its run
+ * of four may be NaN too. dBm, dCm: views [B, L, G N]. dA [H, N], dD, ddt_bias [H] and dh0 [B, H, N] are float32; dD is
  * given exactly when D is, dz when z is; ddt_bias and dh0 may be NULL. The states between the kept
  * ones are computed again. workspace: ssm_scan_backward_workspace_size(B, L, H, N, G) bytes,
  * 16-byte aligned. L = 0 writes zero to the parameters' gradients and dh_last (or 0) to dh0.

@@ -15,6 +15,8 @@
 // through the tensor cores (mma.sync, the only form that takes registers): a product with a matrix
 // of ones adds up four lanes, and four steps share one accumulator, so that the rest takes three
 // exchanges for four steps. The operands have 11 bits, so each value goes in two parts, which keep 21.
+// A value that is not finite spreads over its four steps that way (zero times it is no zero); tiles
+// with marks, past which nothing may come, add up by exchanges alone.
 #include <type_traits>
 
 #include "ssm_scan.cuh"
@@ -454,7 +456,13 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
 #pragma unroll
             for (int p = 0; p < kPairs; ++p)
               d[p] = fma2(h[1][p], two(g[1]), mul2(h[0][p], two(g[0])));
-            sums.take(d, k % 4, lane);
+            if constexpr (MARKS) {
+              float v[4] = {d[0].x, d[0].y, d[1].x, d[1].y};
+              sum_lanes<1, 4, CL>(v, lane % CL);
+              put_lanes<4, CL>(&dBC[t][1][n0], v, lane % CL);
+            } else {
+              sums.take(d, k % 4, lane);
+            }
 #pragma unroll
             for (int i = 0; i < kChannels; ++i) {
               const float2 acc = fma2(h[i][1], cp[1], mul2(h[i][0], cp[0]));
@@ -462,7 +470,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
             }
             sum_lanes<CL, kChannels, LN>(o, at);
             put_lanes<kChannels, LN>(&m.o[j][t][half_of][cl], o, at);
-            if (k % 4 == 3) sums.finish<CL>(&dBC[t - 3][1][n0], 2 * S::kNP, lane);
+            if (!MARKS && k % 4 == 3) sums.finish<CL>(&dBC[t - 3][1][n0], 2 * S::kNP, lane);
           }
 #pragma unroll
           for (int k = kHalf - 1; k >= 0; --k) {
@@ -495,12 +503,18 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
               ev[i] = es.x + es.y;
             }
             if (MARKS && (mark >> t & 1)) clear(carry);
-            sums.take(db, k % 4, lane);
+            if constexpr (MARKS) {
+              float v[4] = {db[0].x, db[0].y, db[1].x, db[1].y};
+              sum_lanes<1, 4, CL>(v, lane % CL);
+              put_lanes<4, CL>(&dBC[t][0][n0], v, lane % CL);
+            } else {
+              sums.take(db, k % 4, lane);
+            }
             sum_lanes<CL, kChannels, LN>(qv, at);
             put_lanes<kChannels, LN>(&m.q[j][t][half_of][cl], qv, at);
             sum_lanes<CL, kChannels, LN>(ev, at);
             put_lanes<kChannels, LN>(&m.e[j][t][half_of][cl], ev, at);
-            if (k % 4 == 0) sums.finish<CL>(&dBC[t][0][n0], 2 * S::kNP, lane);
+            if (!MARKS && k % 4 == 0) sums.finish<CL>(&dBC[t][0][n0], 2 * S::kNP, lane);
           }
         }
       };

@@ -12,7 +12,8 @@ checkpoints or as they are. ``step`` takes one token through the block from a ca
     python -m state_space_sequence_gb300.gated_block
 
 trains a stack of two such blocks for a few steps to repeat the last marked token of its sequence,
-several documents to a row, and then decodes token by token from the states of a prompt.
+several documents to a row, and then decodes token by token from the states of a prompt. The loss is
+:mod:`xent`'s, over the embedding's rows.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import glr
+from . import glr, xent
 
 
 class Params(NamedTuple):
@@ -97,7 +98,7 @@ def step(par: Params, y, n, h, reset=None):
     return glr.glr_join(y, o, n @ par.Wg, par.w, par.alpha, par.v)
 
 
-def main() -> None:
+def main(steps: int = 241) -> None:
     torch.manual_seed(0)
     B, L, H, V, lr = 16, 192, 128, 32, 3e-3
     dtype = torch.bfloat16
@@ -139,20 +140,16 @@ def main() -> None:
             saved.append(s)
         return n, saved
 
-    for k in range(241):
+    for k in range(steps):
         tok, reset, want = batch()
         n, saved = run(tok, reset)
-        logits = n.float() @ embed.t()
-        prob = torch.softmax(logits, -1)
-        count = B * L
-        loss = -torch.log(prob.gather(-1, want[..., None]) + 1e-9).mean()
+        rows, target = _rows(n).float(), want.reshape(-1)
+        losses, lse = xent.xent_loss(rows, embed, target)
         if k % 60 == 0:
-            print(f"step {k:3d}  loss {loss.item():.4f}")
-        d = prob
-        d.scatter_add_(-1, want[..., None], torch.full_like(d[..., :1], -1.0))
-        d = d / count
-        de = _rows(d).t() @ _rows(n).float()
-        dn, dy = (d @ embed).to(dtype), torch.zeros_like(n)
+            print(f"step {k:3d}  loss {losses.mean().item():.4f}")
+        dn, de = xent.xent_loss_backward(rows, embed, target, lse,
+                                         torch.full_like(losses, 1.0 / (B * L)))
+        dn, dy = dn.view_as(n).to(dtype), torch.zeros_like(n)
         for j in (1, 0):
             dy, dn, grads = backward(blocks[j], saved[j], dy, dn)
             adam(k, weights[j], moments[j], grads)
