@@ -112,9 +112,8 @@ dlr_status ssm_conv_step(const ssm_conv_step_args* args, dlr_stream_t stream);
  * h0, h_last: float32 [B, H, N] (either may be NULL). A marked step has no h_{t-1}; its input keeps
  * the factor s_t. A step whose dt is -inf leaves the state as it is (with softplus, for finite x).
  * states (NULL: not kept): float32 [B, ssm_states(L), H, N], the state before each run of
- * SSM_STATE_STEPS steps, for ssm_scan_backward. A state that grows by more than 2^126 in a step
- * (rates above zero) grows by 2^126. workspace: ssm_scan_workspace_size(B, L, H, N, G) bytes,
- * 16-byte aligned (0: none needed). L = 0 copies h0 (or zero) to h_last.
+ * SSM_STATE_STEPS steps, for ssm_scan_backward. workspace:
+ * ssm_scan_workspace_size(B, L, H, N, G) bytes, 16-byte aligned (0: none needed). L = 0 copies h0 (or zero) to h_last.
  * G >= 1 divides H; 1 <= N <= SSM_MAX_STATES; B and L < 2^31, H < 2^24.
  */
 typedef struct {

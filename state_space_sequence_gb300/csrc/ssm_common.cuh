@@ -26,7 +26,6 @@ using glr::from_f;
 using glr::fma2;
 using glr::kLog2e;
 using glr::max_nan;
-using glr::min_nan;
 using glr::mul2;
 using glr::rcp;
 using glr::to_f;
@@ -62,20 +61,25 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
 // What a pair of states keeps of `v` over a step whose exponents (in powers of two) are rate * s.
 // For 16-bit activations the decay comes from the special-function unit, whose results lie 1.9e-8 of
 // themselves low on average next to 1 (measured; as cutting off would make them): over a memory of a
-// thousand steps that adds up, so the exponent gets kNudge, which is still no step where s is 0. For
-// float32 1 - decay comes first (glr::decay2: its digits hold next to a decay of 1) and v - (1 -
-// decay) v keeps them; the exponent is held at +-126.
+// thousand steps that adds up, so the exponent gets kNudge, which is still no step where s is 0.
+// For float32 the decay less 1 comes first and v + (decay - 1) v keeps its digits, so that a memory of
+// thousands of steps does not add up the rounding of its decay: below 1/4 as z P(z), a least-maximum
+// fit of (2^z - 1) / z (1.4e-8), above from the unit, where the subtraction loses less than two bits.
 constexpr float kNudge = 2.7e-8f;
 template <bool PRECISE>
 struct decay {
-  float2 a;  // the decay, or (PRECISE) one less it, negative
+  float2 a;  // the decay, or (PRECISE) the decay less 1
   __device__ __forceinline__ decay(float2 rate, float2 s) {
     if constexpr (PRECISE) {
-      float2 z = mul2(rate, s);
-      z = make_float2(min_nan(z.x, 126.0f), min_nan(z.y, 126.0f));
-      float2 rest, unused;
-      glr::decay2(z, rest, unused);
-      a = mul2(rest, two(-1.0f));
+      const float2 z = mul2(rate, s);
+      float2 p = two(0.0013333556708f);
+      p = fma2(p, z, two(0.0096301622689f));
+      p = fma2(p, z, two(0.0555041655898f));
+      p = fma2(p, z, two(0.2402263134718f));
+      p = fma2(p, z, two(0.6931471824646f));
+      p = mul2(p, z);
+      const float2 e = add2(make_float2(ex2(z.x), ex2(z.y)), two(-1.0f));
+      a = make_float2(fabsf(z.x) < 0.25f ? p.x : e.x, fabsf(z.y) < 0.25f ? p.y : e.y);
     } else {
       const float2 z = fma2(rate, s, two(kNudge));
       a = make_float2(ex2(z.x), ex2(z.y));
@@ -109,7 +113,7 @@ __device__ __forceinline__ void get_piece(words<T, VE>& w, const T* p, int n, bo
   w.from(v);
 }
 template <typename T, int VE>
-__device__ __forceinline__ void put_piece(T* p, const float* v, int n, bool whole) {
+__device__ __forceinline__ void put_piece(T* p, const float (&v)[VE], int n, bool whole) {
   if (whole) {
     words<T, VE> w;
     w.from(v);
@@ -121,20 +125,12 @@ __device__ __forceinline__ void put_piece(T* p, const float* v, int n, bool whol
     if (i < n) p[i] = from_f<T>(v[i]);
 }
 
-template <int VE>
-__device__ __forceinline__ void store_floats(float* p, const float* v) {
-  static_assert(VE % 4 == 0, "");
-#pragma unroll
-  for (int i = 0; i < VE; i += 4)
-    *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
-template <int VE>
-__device__ __forceinline__ void load_floats(float* v, const float* p) {
-#pragma unroll
-  for (int i = 0; i < VE; i += 4) {
-    const float4 t = *reinterpret_cast<const float4*>(p + i);
-    v[i] = t.x, v[i + 1] = t.y, v[i + 2] = t.z, v[i + 3] = t.w;
-  }
+__device__ __forceinline__ void load4(float (&v)[4], const float* p) {
+  const float4 t = *reinterpret_cast<const float4*>(p);
+  v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
 }
 
 // Sums of COUNT values over LANES lanes that stand STRIDE apart; `at` is a lane's place among them.
@@ -184,16 +180,16 @@ __device__ __forceinline__ void meet_finishing() {
   asm volatile("bar.sync %0, %1;" ::"n"(1 + UNITS), "n"(32 * UNITS) : "memory");
 }
 
-// How a unit's tile is cut into pieces of VE channels (and VB states) for a warp's lanes.
-template <typename T, int LN>
+// How a unit's tile is cut into pieces of 4 channels (or 4 states) for a warp's lanes: a lane has the
+// same channels in all its pieces, and words that lie beside those of its neighbours in shared memory.
+constexpr int kPiece = 4;
+template <int LN>
 struct shape {
-  static constexpr int kCW = 32 / LN * kChannels;  // channels of a unit
+  static constexpr int kCW = 32 / LN * kChannels;     // channels of a unit
   static constexpr int kNP = kHalves * LN * kStates;  // states of a channel, with the missing ones
-  static constexpr int VE = 16 / (int)sizeof(T) < kCW ? 16 / (int)sizeof(T) : kCW;
-  static constexpr int VB = 16 / (int)sizeof(T) < kNP ? 16 / (int)sizeof(T) : kNP;
-  static constexpr int kRow = kCW / VE, kRowB = kNP / VB;  // pieces of a step
-  static constexpr int NV = (kT * kRow + 31) / 32, NB = (kT * kRowB + 31) / 32;
-  static_assert(kRow <= 32 && kRowB <= 32 && 32 % kRow == 0 && 32 % kRowB == 0, "");
+  static constexpr int kRow = kCW / kPiece, kRowB = kNP / kPiece;  // pieces of a step
+  static constexpr int NV = kT * kRow / 32, NB = kT * kRowB / 32;  // and of a lane
+  static_assert(kT * kRow % 32 == 0 && kT * kRowB % 32 == 0 && 32 % kRow == 0 && 32 % kRowB == 0, "");
 };
 
 // Lanes of a channel.

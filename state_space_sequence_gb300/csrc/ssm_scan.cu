@@ -29,76 +29,78 @@ constexpr int kUnitWarps = kHalves + 2;  // one that stages and one that finishe
 
 // A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
 // tiles in turn.
-template <typename T, int LN, bool MAP>
+template <int LN, bool MAP>
 struct scan_tile {
-  using S = shape<T, LN>;
+  using S = shape<LN>;
   float s[2][kT][S::kCW], u[2][kT][S::kCW];
   float Bm[2][kT][S::kNP];
   float Cm[MAP ? 1 : 2][MAP ? 1 : kT][S::kNP];
   float o[MAP ? 1 : 2][MAP ? 1 : kT][kHalves * LN][S::kCW];  // sums, in the parts of the lanes
-  float D[S::kCW];
 };
 
 // MAP: only the state that each split but the last adds, and the sum of its steps.
 template <typename T, int LN, bool MAP>
 __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_params<T> q) {
-  using S = shape<T, LN>;
+  using S = shape<LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
-  constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN;
+  constexpr int CL = 32 / LN;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kUnits;
-  scan_tile<T, LN, MAP>& m = reinterpret_cast<scan_tile<T, LN, MAP>*>(smem)[mine];
+  scan_tile<LN, MAP>& m = reinterpret_cast<scan_tile<LN, MAP>*>(smem)[mine];
   unit<T, LN> u;
   if (!u.find(in, (int64_t)blockIdx.x * kUnits + mine, MAP ? in.splits - 1 : in.splits)) return;
   const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
   const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  if (warp >= (kHalves + 1) * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate, and out
+  if (warp >= (kHalves + 1) * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate
     if constexpr (MAP) {
       for (int tile = t_first; tile <= t_end; ++tile) meet_unit<kUnitWarps>(mine);
     } else {
-      const bool ok_z = u.n_ch == S::kCW && u.pieces(in.z);
-      const bool ok_y = u.n_ch == S::kCW && u.pieces(q.y);
-      for (int c = lane; c < S::kCW; c += 32)
-        m.D[c] = in.D && c < u.n_ch ? in.D[u.c0 + c] : 0.0f;
-      __syncwarp();
-      words<T, VE> wx[S::NV], wz[S::NV];  // read a tile before their use
+      const bool full = u.n_ch == S::kCW, ok_z = full && u.pieces(in.z), ok_y = full && u.pieces(q.y);
+      const int c = u.channel(lane);
+      float D[kPiece];
+      load_channels(D, in.D, u, lane);
+      words<T, kPiece> wx[S::NV], wz[S::NV];  // read a tile before their use
       auto fetch = [&](int tile) {
         if (in.D) u.fetch(wx, in.x, (int64_t)tile * kT, in.L, lane, u.whole);
         if (in.z.p) u.fetch(wz, in.z, (int64_t)tile * kT, in.L, lane, ok_z);
       };
       auto finish = [&](int tile) {
         const int64_t t0 = (int64_t)tile * kT;
+        T* py = q.y.p + (u.b * q.y.sb + (t0 + u.step(0, lane)) * q.y.st + u.c0 + c);
+        const bool all = ok_y && t0 + kT <= in.L;
 #pragma unroll
         for (int k = 0; k < S::NV; ++k) {
-          int t, c;
-          if (!u.piece(k, lane, t, c)) break;
-          if (t0 + t >= in.L || c >= u.n_ch) continue;
-          float o[VE], v[VE];
-          load_floats<VE>(o, &m.o[tile & 1][t][0][c]);
+          const int t = u.step(k, lane);
+          float2 o[2] = {two(0.0f), two(0.0f)};
 #pragma unroll
-          for (int l = 1; l < kHalves * LN; ++l) {
-            load_floats<VE>(v, &m.o[tile & 1][t][l][c]);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) o[i] += v[i];
+          for (int l = 0; l < kHalves * LN; ++l) {
+            float v[kPiece];
+            load4(v, &m.o[tile & 1][t][l][c]);
+            o[0] = l ? add2(o[0], make_float2(v[0], v[1])) : make_float2(v[0], v[1]);
+            o[1] = l ? add2(o[1], make_float2(v[2], v[3])) : make_float2(v[2], v[3]);
           }
           if (in.D) {
-            float d[VE];
+            float v[kPiece];
             wx[k].to(v);
-            load_floats<VE>(d, m.D + c);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) o[i] = fmaf(d[i], v[i], o[i]);
+            o[0] = fma2(make_float2(D[0], D[1]), make_float2(v[0], v[1]), o[0]);
+            o[1] = fma2(make_float2(D[2], D[3]), make_float2(v[2], v[3]), o[1]);
           }
           if (in.z.p) {
+            float v[kPiece];
             wz[k].to(v);
 #pragma unroll
-            for (int i = 0; i < VE; i += 2) {
-              const float2 z = make_float2(v[i], v[i + 1]), g = mul2(z, glr::sigmoid2(z));
-              o[i] *= g.x, o[i + 1] *= g.y;
+            for (int i = 0; i < 2; ++i) {
+              const float2 z = make_float2(v[2 * i], v[2 * i + 1]);
+              o[i] = mul2(o[i], mul2(z, glr::sigmoid2(z)));
             }
           }
-          put_piece<T, VE>(q.y.row(u.b, t0 + t) + u.c0 + c, o, u.n_ch - c, ok_y);
+          const float y[kPiece] = {o[0].x, o[0].y, o[1].x, o[1].y};
+          if (all)
+            put_piece<T, kPiece>(py + k * (32 / S::kRow) * q.y.st, y, kPiece, true);
+          else if (t0 + t < in.L && c < u.n_ch)
+            put_piece<T, kPiece>(py + k * (32 / S::kRow) * q.y.st, y, u.n_ch - c, ok_y);
         }
       };
       meet_unit<kUnitWarps>(mine);
@@ -112,13 +114,9 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
     return;
   }
   if (warp >= kHalves * kUnits) {  // stages
-    float bias[VE];
-    const int c_mine = lane % S::kRow * VE;
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      bias[i] = in.bias && c_mine + i < u.n_ch ? in.bias[u.c0 + c_mine + i] : 0.0f;
-    words<T, VE> wx[S::NV], wd[S::NV];  // read a tile before their use
-    words<T, VB> wb[S::NB], wc[S::NB];
+    float bias[kPiece];
+    load_channels(bias, in.bias, u, lane);
+    words<T, kPiece> wx[S::NV], wd[S::NV], wb[S::NB], wc[S::NB];  // read a tile before their use
     auto fetch = [&](int tile) {
       const int64_t t0 = (int64_t)tile * kT;
       u.fetch(wx, in.x, t0, in.L, lane, u.whole);
@@ -150,12 +148,11 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
   const int64_t ch = (int64_t)(u.c0 + cl) * in.N;
   float2 rate[kChannels][kPairs], h[kChannels][kPairs];
   load_rates(rate, in.A, in.N, u.c0 + cl, my_ch, n0);
-  if (MAP || (u.split == 0 && !in.h0))
-    clear(h);
-  else if (u.split == 0)
-    load_states(h, in.h0 + u.b * HN + ch, in.N, my_ch, n0);
-  else
-    load_states(h, in.ends + (row_map - 1) * HN + ch, in.N, my_ch, n0);
+  clear(h);
+  if (!MAP) {
+    if (in.h0) load_states(h, in.h0 + u.b * HN + ch, in.N, my_ch, n0);
+    enter<false>(h, in, u.b, u.split, u.c0 + cl, my_ch, n0, rate);
+  }
   float sum[kChannels] = {};
   bool cut = false;
   meet_unit<kUnitWarps>(mine);
@@ -233,22 +230,18 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
 
 template <typename T, int LN>
 cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
-  using S = shape<T, LN>;
+  using S = shape<LN>;
   q.in.blocks = (q.in.Hg + S::kCW - 1) / S::kCW;
   const int64_t units = (int64_t)q.in.blocks * q.in.G * q.in.B;
   auto grid = [](int64_t n) { return (unsigned)((n + kUnits - 1) / kUnits); };
   cudaError_t e;
   if (q.in.splits > 1) {
-    constexpr size_t bytes = sizeof(scan_tile<T, LN, true>) * kUnits;
+    constexpr size_t bytes = sizeof(scan_tile<LN, true>) * kUnits;
     if ((e = max_smem_once<scan_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
     scan_kernel<T, LN, true><<<grid(units * (q.in.splits - 1)), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t HN = (int64_t)q.in.H * q.in.N;
-    join_splits<false><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
-        q.in.A, q.in.h0, q.in.ends, q.in.sums, q.in.B, q.in.splits, HN, q.in.N);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  constexpr size_t bytes = sizeof(scan_tile<T, LN, false>) * kUnits;
+  constexpr size_t bytes = sizeof(scan_tile<LN, false>) * kUnits;
   if ((e = max_smem_once<scan_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
   scan_kernel<T, LN, false><<<grid(units * q.in.splits), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
   return cudaGetLastError();

@@ -20,45 +20,10 @@ struct inputs {
   view<const T> x, dt, z, Bm, Cm;
   const float *A, *D, *bias, *h0;
   const uint8_t* reset;
-  // the splits' maps: what a split adds to the state that enters it, later what enters the next
-  // one, [B, splits, H, N]; and the sum of its steps, [B, splits, H], a NaN where a mark stops all
+  // the splits' maps: what a split adds to the state that enters it, [B, splits, H, N], and the sum
+  // of its steps, [B, splits, H], a NaN where a mark stops all
   float *ends, *sums;
 };
-
-// A split of a sequence takes the state that enters it to P h + e: e is its end from zero, and P =
-// exp(A sum of its steps). One split (the common case) has no maps. Forwards the states are joined
-// from the first split on, backwards the gradients from the last one on; `ends` then holds what
-// enters: the split behind (forwards), the one before (backwards).
-template <bool BACK>
-__global__ void join_splits(const float* A, const float* first, float* ends, const float* sums,
-                            int64_t B, int splits, int64_t HN, int N) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= B * HN) return;
-  const int64_t b = i / HN, k = i - b * HN, c = k / N;
-  const float rate = A[k] * kLog2e;
-  float h = first ? first[i] : 0.0f;
-  const int64_t H = HN / N;
-  // forwards splits 0 .. splits-2 pass something on, backwards splits-1 .. 1
-  constexpr int kAhead = 8;
-  for (int j0 = 0; j0 < splits - 1; j0 += kAhead) {
-    float e[kAhead], s[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int j = min(j0 + u, splits - 2);
-      const int64_t row = b * splits + (BACK ? splits - 1 - j : j);
-      e[u] = ends[row * HN + k];
-      s[u] = sums[row * H + c];
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (j0 + u >= splits - 1) break;
-      const int j = j0 + u;
-      const int64_t row = b * splits + (BACK ? splits - 1 - j : j);
-      h = s[u] != s[u] ? e[u] : fmaf(ex2(min_nan(rate * s[u], 126.0f)), h, e[u]);
-      ends[row * HN + k] = h;
-    }
-  }
-}
 
 // The bits of a tile's marked steps (bit t: step t0 + t), the same in all lanes.
 __device__ __forceinline__ uint32_t marks(const uint8_t* reset, int64_t row, int64_t t0, int64_t L,
@@ -142,10 +107,39 @@ __device__ __forceinline__ void get_channels(float (&v)[kChannels], const float*
   v[0] = t.x, v[1] = t.y;
 }
 
+// A split of a sequence takes the state that enters it to P h + e: e is its end from zero, and P =
+// exp(A sum of its steps). What enters a split, from what enters the sequence (`h`): forwards through
+// the splits before it, backwards (the gradients) through those behind it, the same for every split in
+// the same order. One split, the common case, has no maps.
+template <bool BACK, typename T>
+__device__ __forceinline__ void enter(float2 (&h)[kChannels][kPairs], const inputs<T>& in, int64_t b,
+                                      int split, int64_t c, int n_ch, int n0,
+                                      const float2 (&rate)[kChannels][kPairs]) {
+  const int64_t HN = (int64_t)in.H * in.N;
+  const int count = BACK ? in.splits - 1 - split : split;
+#pragma unroll 4
+  for (int j = 0; j < count; ++j) {
+    const int64_t row = b * in.splits + (BACK ? in.splits - 1 - j : j);
+    float2 e[kChannels][kPairs];
+    load_states(e, in.ends + row * HN + c * in.N, in.N, n_ch, n0);
+#pragma unroll
+    for (int i = 0; i < kChannels; ++i) {
+      if (i >= n_ch) continue;
+      const float s = in.sums[row * in.H + c + i];
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        const float2 z = mul2(rate[i][p], two(s));
+        h[i][p] = s != s ? e[i][p] : fma2(make_float2(ex2(z.x), ex2(z.y)), h[i][p], e[i][p]);
+      }
+    }
+  }
+}
+
 // Where a unit works, and how its rows lie.
 template <typename T, int LN>
 struct unit {
-  using S = shape<T, LN>;
+  using S = shape<LN>;
+  using piece = words<T, kPiece>;
   int64_t b;
   int split, group, c0, n_ch;  // c0: first channel; n_ch: how many of the unit's exist
   bool whole, whole_b;         // pieces of rows go by whole accesses
@@ -165,105 +159,120 @@ struct unit {
     c0 = g * in.Hg + first;
     n_ch = max(0, min(S::kCW, in.Hg - first));
     whole = n_ch == S::kCW && pieces(in.x) && pieces(in.dt);
-    whole_b = in.N % S::VB == 0 && maps(in.Bm, in.N) && maps(in.Cm, in.N);
+    whole_b = in.N == S::kNP && maps(in.Bm, in.N) && maps(in.Cm, in.N);
   }
   template <typename V>
   __device__ __forceinline__ bool pieces(const view<V>& v) const {
     return !v.p || ((reinterpret_cast<uintptr_t>(v.p + c0) | (uintptr_t)(v.sb * (int64_t)sizeof(T)) |
                      (uintptr_t)(v.st * (int64_t)sizeof(T))) &
-                    (uintptr_t)(S::VE * sizeof(T) - 1)) == 0;
+                    (uintptr_t)(kPiece * sizeof(T) - 1)) == 0;
   }
   __device__ __forceinline__ bool maps(const view<const T>& v, int N) const {
     return ((reinterpret_cast<uintptr_t>(v.p + (int64_t)group * N) |
              (uintptr_t)(v.sb * (int64_t)sizeof(T)) | (uintptr_t)(v.st * (int64_t)sizeof(T))) &
-            (uintptr_t)(S::VB * sizeof(T) - 1)) == 0;
+            (uintptr_t)(kPiece * sizeof(T) - 1)) == 0;
   }
-  // piece k of a tile for this lane: its step and first channel; false where there is none
-  static __device__ __forceinline__ bool piece(int k, int lane, int& t, int& c) {
-    const int p = k * 32 + lane;
-    t = p / S::kRow;
-    c = p % S::kRow * S::VE;
-    return t < kT;
+  // a lane's channels of the unit, and the step of its piece k
+  static __device__ __forceinline__ int channel(int lane) { return lane % S::kRow * kPiece; }
+  static __device__ __forceinline__ int step(int k, int lane) {
+    return lane / S::kRow + k * (32 / S::kRow);
   }
-  static __device__ __forceinline__ bool piece_b(int k, int lane, int& t, int& n) {
-    const int p = k * 32 + lane;
-    t = p / S::kRowB;
-    n = p % S::kRowB * S::VB;
-    return t < kT;
+  static __device__ __forceinline__ int state(int lane) { return lane % S::kRowB * kPiece; }
+  static __device__ __forceinline__ int step_b(int k, int lane) {
+    return lane / S::kRowB + k * (32 / S::kRowB);
   }
   // A tile's pieces of a row, zeros where the row or the sequence ends.
   template <typename V>
-  __device__ __forceinline__ void fetch(words<T, S::VE> (&w)[S::NV], const view<V>& v, int64_t t0,
-                                        int64_t L, int lane, bool ok) const {
+  __device__ __forceinline__ void fetch(piece (&w)[S::NV], const view<V>& v, int64_t t0, int64_t L,
+                                        int lane, bool ok) const {
+    const int c = channel(lane);
+    const V* p = v.p + (b * v.sb + (t0 + step(0, lane)) * v.st + c0 + c);
+    if (ok && t0 + kT <= L) {
 #pragma unroll
-    for (int k = 0; k < S::NV; ++k) {
-      int t, c;
-      w[k] = words<T, S::VE>();
-      if (piece(k, lane, t, c) && t0 + t < L && c < n_ch)
-        get_piece<T, S::VE>(w[k], v.row(b, t0 + t) + c0 + c, n_ch - c, ok);
+      for (int k = 0; k < S::NV; ++k) w[k].get(p + k * (32 / S::kRow) * v.st);
+    } else {
+#pragma unroll
+      for (int k = 0; k < S::NV; ++k) {
+        w[k] = piece();
+        if (t0 + step(k, lane) < L && c < n_ch)
+          get_piece<T, kPiece>(w[k], p + k * (32 / S::kRow) * v.st, n_ch - c, ok);
+      }
     }
   }
-  __device__ __forceinline__ void fetch_b(words<T, S::VB> (&w)[S::NB], const view<const T>& v,
-                                          int64_t t0, int64_t L, int N, int lane) const {
+  __device__ __forceinline__ void fetch_b(piece (&w)[S::NB], const view<const T>& v, int64_t t0,
+                                          int64_t L, int N, int lane) const {
+    const int n = state(lane);
+    const T* p = v.p + (b * v.sb + (t0 + step_b(0, lane)) * v.st + (int64_t)group * N + n);
+    if (whole_b && t0 + kT <= L) {
 #pragma unroll
-    for (int k = 0; k < S::NB; ++k) {
-      int t, n;
-      w[k] = words<T, S::VB>();
-      if (piece_b(k, lane, t, n) && t0 + t < L && n < N)
-        get_piece<T, S::VB>(w[k], v.row(b, t0 + t) + (int64_t)group * N + n, N - n, whole_b);
+      for (int k = 0; k < S::NB; ++k) w[k].get(p + k * (32 / S::kRowB) * v.st);
+    } else {
+#pragma unroll
+      for (int k = 0; k < S::NB; ++k) {
+        w[k] = piece();
+        if (t0 + step_b(k, lane) < L && n < N)
+          get_piece<T, kPiece>(w[k], p + k * (32 / S::kRowB) * v.st, N - n, false);
+      }
     }
   }
-  static __device__ __forceinline__ void put_b(float (*m)[S::kNP], const words<T, S::VB> (&w)[S::NB],
+  static __device__ __forceinline__ void put_b(float (*m)[S::kNP], const piece (&w)[S::NB],
                                                int lane) {
 #pragma unroll
     for (int k = 0; k < S::NB; ++k) {
-      int t, n;
-      float v[S::VB];
+      float v[kPiece];
       w[k].to(v);
-      if (piece_b(k, lane, t, n)) store_floats<S::VB>(&m[t][n], v);
+      store4(&m[step_b(k, lane)][state(lane)], v);
     }
   }
 };
 
-// The steps s and the inputs s x of a tile's pieces (`bias`: of the channels of this lane's pieces,
-// which are the same in all of them): softplus, and zeros where there is no channel
-// or step (which leave the state as it is).
+// The steps s and the inputs s x of a tile's pieces (`bias`: of this lane's channels): softplus, and
+// zeros where there is no channel or step (which leave the state as it is).
 template <typename T, int LN>
 __device__ __forceinline__ void stage_steps(const unit<T, LN>& u, int softplus, int64_t t0, int64_t L,
-                                            int lane, const float (&bias)[shape<T, LN>::VE],
-                                            const words<T, shape<T, LN>::VE> (&wx)[shape<T, LN>::NV],
-                                            const words<T, shape<T, LN>::VE> (&wd)[shape<T, LN>::NV],
-                                            float (*s)[shape<T, LN>::kCW],
-                                            float (*in)[shape<T, LN>::kCW]) {
-  using S = shape<T, LN>;
+                                            int lane, const float (&bias)[kPiece],
+                                            const words<T, kPiece> (&wx)[shape<LN>::NV],
+                                            const words<T, kPiece> (&wd)[shape<LN>::NV],
+                                            float (*s)[shape<LN>::kCW], float (*in)[shape<LN>::kCW]) {
+  using S = shape<LN>;
+  const int c = u.channel(lane);
+  const bool all = u.n_ch == S::kCW && t0 + kT <= L;
 #pragma unroll
   for (int k = 0; k < S::NV; ++k) {
-    int t, c;
-    if (!unit<T, LN>::piece(k, lane, t, c)) break;
-    float xv[S::VE], dv[S::VE], bv[S::VE];
+    const int t = u.step(k, lane);
+    float xv[kPiece], dv[kPiece];
     wx[k].to(xv);
     wd[k].to(dv);
 #pragma unroll
-    for (int i = 0; i < S::VE; ++i) bv[i] = bias[i];
-#pragma unroll
-    for (int i = 0; i < S::VE; i += 2) {
-      float2 d = add2(make_float2(dv[i], dv[i + 1]), make_float2(bv[i], bv[i + 1]));
+    for (int i = 0; i < kPiece; i += 2) {
+      float2 d = add2(make_float2(dv[i], dv[i + 1]), make_float2(bias[i], bias[i + 1]));
       if (softplus) d = softplus2(d);
       dv[i] = d.x, dv[i + 1] = d.y;
     }
-    if (t0 + t >= L || c + S::VE > u.n_ch) {
+    if (!all) {
 #pragma unroll
-      for (int i = 0; i < S::VE; ++i) {
+      for (int i = 0; i < kPiece; ++i) {
         const bool there = t0 + t < L && c + i < u.n_ch;
         dv[i] = there ? dv[i] : 0.0f;
         xv[i] = there ? xv[i] : 0.0f;
       }
     }
 #pragma unroll
-    for (int i = 0; i < S::VE; ++i) xv[i] *= dv[i];
-    store_floats<S::VE>(&s[t][c], dv);
-    store_floats<S::VE>(&in[t][c], xv);
+    for (int i = 0; i < kPiece; i += 2) {
+      const float2 p = mul2(make_float2(xv[i], xv[i + 1]), make_float2(dv[i], dv[i + 1]));
+      xv[i] = p.x, xv[i + 1] = p.y;
+    }
+    store4(&s[t][c], dv);
+    store4(&in[t][c], xv);
   }
+}
+// A lane's channels of a parameter (zeros for none).
+template <typename T, int LN>
+__device__ __forceinline__ void load_channels(float (&v)[kPiece], const float* p,
+                                              const unit<T, LN>& u, int lane) {
+  const int c = u.channel(lane);
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) v[i] = p && c + i < u.n_ch ? p[u.c0 + c + i] : 0.0f;
 }
 
 // How many splits a sequence is cut into. A unit goes through its rows step by step, so few channels

@@ -50,9 +50,9 @@ struct back_params {
 
 // A unit's part of shared memory: what a tile's steps read and what they leave, two tiles in turn.
 // MAP needs s, g and Cm alone.
-template <typename T, int LN, bool MAP>
+template <int LN, bool MAP>
 struct back_tile {
-  using S = shape<T, LN>;
+  using S = shape<LN>;
   static constexpr int kN = MAP ? 1 : 2, kSteps = MAP ? 1 : kT;
   float s[2][kT][S::kCW], g[2][kT][S::kCW], u[2][kT][S::kCW];
   float Bm[kN][kSteps][S::kNP], Cm[2][kT][S::kNP];
@@ -117,12 +117,12 @@ __device__ __forceinline__ void advance(float2 (&h)[kChannels][kPairs],
 // MAP: only the gradient that each split but the first sends on, and the sum of its steps.
 template <typename T, int LN, bool MAP>
 __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel(back_params<T> q) {
-  using S = shape<T, LN>;
+  using S = shape<LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
-  constexpr int VE = S::VE, VB = S::VB, CL = 32 / LN, kUnits = kUnitsOf<LN>;
+  constexpr int CL = 32 / LN, kUnits = kUnitsOf<LN>;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
-  using tile_t = back_tile<T, LN, MAP>;
+  using tile_t = back_tile<LN, MAP>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kUnits;
   tile_t* all = reinterpret_cast<tile_t*>(smem);
   tile_t& m = all[mine];
@@ -142,19 +142,14 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
   if (warp >= kHalves * kUnits) {
     const bool full = u.n_ch == S::kCW, ok_z = full && u.pieces(in.z);
     const bool ok_o = full && u.pieces(q.dx) && u.pieces(q.ddt) && u.pieces(q.dz);
-    // of the channels of this lane's pieces (the same in all of them)
-    float bias[VE], D[VE];
-    const int c_mine = lane % S::kRow * VE;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const bool there = c_mine + i < u.n_ch;
-      bias[i] = in.bias && there ? in.bias[u.c0 + c_mine + i] : 0.0f;
-      D[i] = in.D && there ? in.D[u.c0 + c_mine + i] : 0.0f;
-    }
+    const int c = u.channel(lane);
+    float bias[kPiece], D[kPiece];
+    load_channels(bias, in.bias, u, lane);
+    load_channels(D, in.D, u, lane);
     // what is staged is read a tile before, where registers hold it
-    constexpr bool kAhead = S::NV <= 2;
-    words<T, VE> wx[S::NV], wd[S::NV], wy[S::NV], wz[S::NV];
-    words<T, VB> wb[S::NB], wc[S::NB];
+    constexpr bool kAhead = S::NV * sizeof(T) <= 8;
+    using piece = words<T, kPiece>;
+    piece wx[S::NV], wd[S::NV], wy[S::NV], wz[S::NV], wb[S::NB], wc[S::NB];
     float4 first[4];  // a tile's first states: quads of the unit's kCW x NP
     const bool whole_h = quads(q.states, in.N);
     auto fetch = [&](int tile) {
@@ -169,9 +164,9 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
         const float* src = q.states + (u.b * in.tiles + tile) * HN + (int64_t)u.c0 * in.N;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int i = (k * 32 + lane) * 4, c = i / S::kNP;
-          first[k] = c < u.n_ch ? get_quad(src + (int64_t)c * in.N, i % S::kNP, in.N, whole_h)
-                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const int i = (k * 32 + lane) * 4, ci = i / S::kNP;
+          first[k] = ci < u.n_ch ? get_quad(src + (int64_t)ci * in.N, i % S::kNP, in.N, whole_h)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
       }
     };
@@ -182,19 +177,17 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
       u.put_b(m.Cm[j], wc, lane);
 #pragma unroll
       for (int k = 0; k < S::NV; ++k) {
-        int t, c;
-        if (!u.piece(k, lane, t, c)) break;
-        float yv[VE], zv[VE];
+        float yv[kPiece], zv[kPiece];
         wy[k].to(yv);  // zeros where there is no channel or step
         if (in.z.p) {
           wz[k].to(zv);
 #pragma unroll
-          for (int i = 0; i < VE; i += 2) {
+          for (int i = 0; i < kPiece; i += 2) {
             const float2 z = make_float2(zv[i], zv[i + 1]), g = mul2(z, glr::sigmoid2(z));
             yv[i] *= g.x, yv[i + 1] *= g.y;
           }
         }
-        store_floats<VE>(&m.g[j][t][c], yv);
+        store4(&m.g[j][u.step(k, lane)][c], yv);
       }
       if constexpr (!MAP) {
         u.put_b(m.Bm[j], wb, lane);
@@ -204,21 +197,30 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
       }
     };
     // of this lane's channels: ddt and g x summed over time
-    float sum_t[VE], sum_x[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i) sum_t[i] = sum_x[i] = 0.0f;
-    auto both = [&](float (&v)[VE], const float (*p)[S::kCW], int c) {  // the two halves' sum
-      float w[VE];
-      load_floats<VE>(v, &p[0][c]);
-      load_floats<VE>(w, &p[1][c]);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) v[i] += w[i];
+    float2 sum_t[2] = {two(0.0f), two(0.0f)}, sum_x[2] = {two(0.0f), two(0.0f)};
+    auto pair4 = [&](float2 (&v)[2], const float* p) {
+      const float4 t = *reinterpret_cast<const float4*>(p);
+      v[0] = make_float2(t.x, t.y);
+      v[1] = make_float2(t.z, t.w);
+    };
+    auto both = [&](float2 (&v)[2], const float (*p)[S::kCW]) {  // the two halves' sum
+      float2 w[2];
+      pair4(v, &p[0][c]);
+      pair4(w, &p[1][c]);
+      v[0] = add2(v[0], w[0]);
+      v[1] = add2(v[1], w[1]);
+    };
+    auto pairs_of = [](float2 (&v)[2], const piece& w) {
+      float t[kPiece];
+      w.to(t);
+      v[0] = make_float2(t[0], t[1]);
+      v[1] = make_float2(t[2], t[3]);
     };
     // the units' dBm and dCm, and what the channels' gradients take besides, by pieces of rows
     auto finish = [&](int tile) {
       const int64_t t0 = (int64_t)tile * kT;
       const int j = tile & 1;
-      words<T, VE> fx[S::NV], fd[S::NV], fy[S::NV], fz[S::NV];
+      piece fx[S::NV], fd[S::NV], fy[S::NV], fz[S::NV];
       u.fetch(fx, in.x, t0, in.L, lane, u.whole);
       u.fetch(fd, in.dt, t0, in.L, lane, u.whole);
       if (in.z.p) {
@@ -241,43 +243,60 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
         }
         if (t0 + i / pitch < in.L) *reinterpret_cast<float4*>(part + i) = v;
       }
+      const bool all_there = ok_o && t0 + kT <= in.L;
+      auto out = [&](const view<T>& v, int k, const float2 (&o)[2]) {
+        const int64_t t = t0 + u.step(k, lane);
+        T* p = v.p + (u.b * v.sb + t * v.st + u.c0 + c);
+        const float y[kPiece] = {o[0].x, o[0].y, o[1].x, o[1].y};
+        if (all_there)
+          put_piece<T, kPiece>(p, y, kPiece, true);
+        else if (t < in.L && c < u.n_ch)
+          put_piece<T, kPiece>(p, y, u.n_ch - c, ok_o);
+      };
+      // steps and channels that do not exist add nothing to the sums
 #pragma unroll
       for (int k = 0; k < S::NV; ++k) {
-        int t, c;
-        if (!u.piece(k, lane, t, c)) break;
-        if (t0 + t >= in.L || c >= u.n_ch) continue;
-        float xv[VE], dv[VE], gv[VE], qv[VE], ev[VE];
-        fx[k].to(xv);
-        fd[k].to(dv);
-        both(qv, m.q[j][t], c);
-        both(ev, m.e[j][t], c);
+        const int t = u.step(k, lane);
+        const bool there = full ? t0 + t < in.L : t0 + t < in.L && c < u.n_ch;
+        float2 xv[2], dv[2], gv[2], qv[2], ev[2], sv[2];
+        pairs_of(xv, fx[k]);
+        pairs_of(dv, fd[k]);
+        both(qv, m.q[j][t]);
+        both(ev, m.e[j][t]);
+        pair4(gv, &m.g[j][t][c]);
+        pair4(sv, &m.s[j][t][c]);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
+        for (int i = 0; i < 2; ++i) {
           // e was summed with the rates in powers of two
-          float d = fmaf(xv[i], qv[i], ev[i] * (1.0f / kLog2e));
-          if (in.softplus) d *= glr::sigmoid(dv[i] + bias[i]);
+          float2 d = fma2(xv[i], qv[i], mul2(ev[i], two(1.0f / kLog2e)));
+          if (in.softplus)
+            d = mul2(d, glr::sigmoid2(add2(dv[i], make_float2(bias[2 * i], bias[2 * i + 1]))));
           dv[i] = d;
-          sum_t[i] += c + i < u.n_ch ? d : 0.0f;
-        }
-        put_piece<T, VE>(q.ddt.row(u.b, t0 + t) + u.c0 + c, dv, u.n_ch - c, ok_o);
-        load_floats<VE>(gv, &m.g[j][t][c]);
-        load_floats<VE>(dv, &m.s[j][t][c]);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          qv[i] = fmaf(dv[i], qv[i], D[i] * gv[i]);
-          sum_x[i] += c + i < u.n_ch ? gv[i] * xv[i] : 0.0f;
-        }
-        put_piece<T, VE>(q.dx.row(u.b, t0 + t) + u.c0 + c, qv, u.n_ch - c, ok_o);
-        if (in.z.p) {
-          fz[k].to(dv);
-          fy[k].to(gv);
-          both(qv, m.o[j][t], c);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const float sig = glr::sigmoid(dv[i]);
-            gv[i] *= fmaf(D[i], xv[i], qv[i]) * fmaf(dv[i] * sig, 1.0f - sig, sig);
+          if (!full) {
+            if (c + 2 * i >= u.n_ch) d.x = 0.0f;
+            if (c + 2 * i + 1 >= u.n_ch) d.y = 0.0f;
           }
-          put_piece<T, VE>(q.dz.row(u.b, t0 + t) + u.c0 + c, gv, u.n_ch - c, ok_o);
+          if (there) {
+            sum_t[i] = add2(sum_t[i], d);
+            sum_x[i] = fma2(gv[i], xv[i], sum_x[i]);
+          }
+          qv[i] = fma2(sv[i], qv[i], mul2(make_float2(D[2 * i], D[2 * i + 1]), gv[i]));
+        }
+        out(q.ddt, k, dv);
+        out(q.dx, k, qv);
+        if (in.z.p) {
+          float2 zv[2];
+          pairs_of(zv, fz[k]);
+          pairs_of(gv, fy[k]);
+          both(qv, m.o[j][t]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 s = glr::sigmoid2(zv[i]);
+            const float2 slope = fma2(mul2(zv[i], s), fma2(s, two(-1.0f), two(1.0f)), s);
+            const float2 o = fma2(make_float2(D[2 * i], D[2 * i + 1]), xv[i], qv[i]);
+            gv[i] = mul2(gv[i], mul2(o, slope));
+          }
+          out(q.dz, k, gv);
         }
       }
     };
@@ -299,20 +318,22 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
     }
     if constexpr (!MAP) {
       finish(t_first);
+      float sum[2][kPiece] = {{sum_t[0].x, sum_t[0].y, sum_t[1].x, sum_t[1].y},
+                              {sum_x[0].x, sum_x[0].y, sum_x[1].x, sum_x[1].y}};
 #pragma unroll
-      for (int i = 0; i < VE; ++i)
+      for (int i = 0; i < kPiece; ++i)
 #pragma unroll
         for (int d = S::kRow; d < 32; d *= 2) {
-          sum_t[i] += __shfl_xor_sync(0xffffffffu, sum_t[i], d);
-          sum_x[i] += __shfl_xor_sync(0xffffffffu, sum_x[i], d);
+          sum[0][i] += __shfl_xor_sync(0xffffffffu, sum[0][i], d);
+          sum[1][i] += __shfl_xor_sync(0xffffffffu, sum[1][i], d);
         }
       if (lane < S::kRow) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (c_mine + i < u.n_ch) {
-            float* p = q.part_c + row_map * in.H + u.c0 + c_mine + i;
-            p[0] = sum_t[i];
-            p[in.B * in.splits * in.H] = sum_x[i];
+        for (int i = 0; i < kPiece; ++i)
+          if (c + i < u.n_ch) {
+            float* p = q.part_c + row_map * in.H + u.c0 + c + i;
+            p[0] = sum[0][i];
+            p[in.B * in.splits * in.H] = sum[1][i];
           }
       }
     }
@@ -326,12 +347,11 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
   const int64_t ch = (int64_t)(u.c0 + cl) * in.N;
   float2 rate[kChannels][kPairs], carry[kChannels][kPairs];
   load_rates(rate, in.A, in.N, u.c0 + cl, my_ch, n0);
-  if (MAP || (u.split == in.splits - 1 && !q.dh_last))
-    clear(carry);
-  else if (u.split == in.splits - 1)
-    load_states(carry, q.dh_last + u.b * HN + ch, in.N, my_ch, n0);
-  else
-    load_states(carry, in.ends + (row_map + 1) * HN + ch, in.N, my_ch, n0);
+  clear(carry);
+  if (!MAP) {
+    if (q.dh_last) load_states(carry, q.dh_last + u.b * HN + ch, in.N, my_ch, n0);
+    enter<true>(carry, in, u.b, u.split, u.c0 + cl, my_ch, n0, rate);
+  }
   meet_unit<kUnitWarps>(mine);
 
   // A tile without marks goes without looking for them: a branch would keep the steps apart that are
@@ -596,15 +616,12 @@ cudaError_t run_back(back_params<T> q, const back_plan& p, cudaStream_t s) {
   const int64_t HN = (int64_t)q.in.H * q.in.N;
   cudaError_t e;
   if (q.in.splits > 1) {
-    constexpr size_t bytes = sizeof(back_tile<T, LN, true>) * kUnits;
+    constexpr size_t bytes = sizeof(back_tile<LN, true>) * kUnits;
     if ((e = max_smem_once<back_kernel<T, LN, true>>(bytes)) != cudaSuccess) return e;
     back_kernel<T, LN, true><<<(unsigned)(units * (q.in.splits - 1)), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    join_splits<true><<<(unsigned)((q.in.B * HN + 127) / 128), 128, 0, s>>>(
-        q.in.A, q.dh_last, q.in.ends, q.in.sums, q.in.B, q.in.splits, HN, q.in.N);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  constexpr size_t bytes = sizeof(back_tile<T, LN, false>) * kUnits;
+  constexpr size_t bytes = sizeof(back_tile<LN, false>) * kUnits;
   static_assert(bytes <= 232448, "shared memory");
   if ((e = max_smem_once<back_kernel<T, LN, false>>(bytes)) != cudaSuccess) return e;
   back_kernel<T, LN, false><<<(unsigned)(units * q.in.splits), 32 * kUnitWarps * kUnits, bytes, s>>>(q);
