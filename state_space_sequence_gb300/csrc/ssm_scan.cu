@@ -24,8 +24,10 @@ struct scan_params {
   float *h_last, *states;
 };
 
-constexpr int kUnits = 4;             // of a block: on each quarter of an SM two warps that run a unit,
-constexpr int kUnitWarps = kHalves + 2;  // one that stages and one that finishes
+// Of a block: on each quarter of an SM two warps that run a unit, two that stage, each every other
+// piece of a tile, and two that finish. With one of each B4 L4096 H4096 N16 bfloat16 took 437 us: a
+// helper alone, mostly waiting for itself, took as long for a tile as the running warps.
+constexpr int kUnits = 4, kHelpers = 2, kUnitWarps = kHalves + 2 * kHelpers;
 
 // A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
 // tiles in turn.
@@ -53,7 +55,13 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
   const int t_first = u.split * in.per_split, t_end = min(in.tiles, t_first + in.per_split);
   const int64_t HN = (int64_t)in.H * in.N, row_map = u.b * in.splits + u.split;
 
-  if (warp >= (kHalves + 1) * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate
+  // a helper's part of the pieces of a tile: every second one, or all of one piece
+  constexpr int kMany = S::NV > 1 ? S::NV / kHelpers : 1, kStep = S::NV > 1 ? kHelpers : 1;
+  const int part = (warp - kHalves * kUnits) / kUnits % kHelpers;
+  const int from = S::NV > 1 ? part : 0;
+  const bool busy = S::NV > 1 || part == 0;
+
+  if (warp >= (kHalves + kHelpers) * kUnits) {  // finishes: the sum of the lanes' parts, the skip, the gate
     if constexpr (MAP) {
       for (int tile = t_first; tile <= t_end; ++tile) meet_unit<kUnitWarps>(mine);
     } else {
@@ -61,18 +69,22 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
       const int c = u.channel(lane);
       float D[kPiece];
       load_channels(D, in.D, u, lane);
-      words<T, kPiece> wx[S::NV], wz[S::NV];  // read a tile before their use
+      words<T, kPiece> wx[kMany], wz[kMany];  // read a tile before their use
       auto fetch = [&](int tile) {
-        if (in.D) u.fetch(wx, in.x, (int64_t)tile * kT, in.L, lane, u.whole);
-        if (in.z.p) u.fetch(wz, in.z, (int64_t)tile * kT, in.L, lane, ok_z);
+        const int64_t t0 = (int64_t)tile * kT;
+        if (!busy) return;
+        if (in.D) u.fetch<kMany, kStep>(wx, in.x, t0, in.L, lane, u.whole, from);
+        if (!in.z.p) return;
+        u.fetch<kMany, kStep>(wz, in.z, t0, in.L, lane, ok_z, from);
       };
       auto finish = [&](int tile) {
         const int64_t t0 = (int64_t)tile * kT;
-        T* py = q.y.p + (u.b * q.y.sb + (t0 + u.step(0, lane)) * q.y.st + u.c0 + c);
+        if (!busy) return;
+        T* py = q.y.p + (u.b * q.y.sb + (t0 + u.step(from, lane)) * q.y.st + u.c0 + c);
         const bool all = ok_y && t0 + kT <= in.L;
 #pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-          const int t = u.step(k, lane);
+        for (int k = 0; k < kMany; ++k) {
+          const int t = u.step(from + k * kStep, lane);
           float2 o[2] = {two(0.0f), two(0.0f)};
 #pragma unroll
           for (int l = 0; l < kHalves * LN; ++l) {
@@ -98,9 +110,9 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
           }
           const float y[kPiece] = {o[0].x, o[0].y, o[1].x, o[1].y};
           if (all)
-            put_piece<T, kPiece>(py + k * (32 / S::kRow) * q.y.st, y, kPiece, true);
+            put_piece<T, kPiece>(py + k * kStep * (32 / S::kRow) * q.y.st, y, kPiece, true);
           else if (t0 + t < in.L && c < u.n_ch)
-            put_piece<T, kPiece>(py + k * (32 / S::kRow) * q.y.st, y, u.n_ch - c, ok_y);
+            put_piece<T, kPiece>(py + k * kStep * (32 / S::kRow) * q.y.st, y, u.n_ch - c, ok_y);
         }
       };
       meet_unit<kUnitWarps>(mine);
@@ -113,22 +125,28 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
     }
     return;
   }
-  if (warp >= kHalves * kUnits) {  // stages
+  if (warp >= kHalves * kUnits) {  // stages: its pieces of s and s x, and one of the maps
     float bias[kPiece];
     load_channels(bias, in.bias, u, lane);
-    words<T, kPiece> wx[S::NV], wd[S::NV], wb[S::NB], wc[S::NB];  // read a tile before their use
+    words<T, kPiece> wx[kMany], wd[kMany], wm[S::NB];  // read a tile before their use
+    const view<const T>& map = part ? in.Cm : in.Bm;
     auto fetch = [&](int tile) {
       const int64_t t0 = (int64_t)tile * kT;
-      u.fetch(wx, in.x, t0, in.L, lane, u.whole);
-      u.fetch(wd, in.dt, t0, in.L, lane, u.whole);
-      u.fetch_b(wb, in.Bm, t0, in.L, in.N, lane);
-      if (!MAP) u.fetch_b(wc, in.Cm, t0, in.L, in.N, lane);
+      if (busy) {
+        u.fetch<kMany, kStep>(wx, in.x, t0, in.L, lane, u.whole, from);
+        u.fetch<kMany, kStep>(wd, in.dt, t0, in.L, lane, u.whole, from);
+      }
+      if (!MAP || part == 0) u.fetch_b(wm, map, t0, in.L, in.N, lane);
     };
     auto stage = [&](int tile) {
-      stage_steps<T, LN>(u, in.softplus, (int64_t)tile * kT, in.L, lane, bias, wx, wd,
-                         m.s[tile & 1], m.u[tile & 1]);
-      u.put_b(m.Bm[tile & 1], wb, lane);
-      if constexpr (!MAP) u.put_b(m.Cm[tile & 1], wc, lane);
+      if (busy)
+        stage_steps<kMany, kStep>(u, in.softplus, (int64_t)tile * kT, in.L, lane, bias, wx, wd,
+                                  m.s[tile & 1], m.u[tile & 1], from);
+      if constexpr (MAP) {
+        if (part == 0) u.put_b(m.Bm[tile & 1], wm, lane);
+      } else {
+        u.put_b(part ? m.Cm[tile & 1] : m.Bm[tile & 1], wm, lane);
+      }
     };
     fetch(t_first);
     stage(t_first);
@@ -155,6 +173,8 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
   }
   float sum[kChannels] = {};
   bool cut = false;
+  float* keep = q.states + (u.b * in.tiles + t_first) * HN + ch + n0;
+  const bool keep_whole = my_ch >= kChannels && n0 < in.N && quads(q.states, in.N);
   meet_unit<kUnitWarps>(mine);
   for (int tile = t_first; tile < t_end; ++tile) {
     const int64_t t0 = (int64_t)tile * kT;
@@ -164,8 +184,17 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
     const float (*mb)[S::kNP] = m.Bm[tile & 1];
     const float (*mc)[S::kNP] = m.Cm[MAP ? 0 : tile & 1];
     float (*mo)[kHalves * LN][S::kCW] = m.o[MAP ? 0 : tile & 1];
-    if (!MAP && q.states)
-      store_states(q.states + (u.b * in.tiles + tile) * HN + ch, h, in.N, my_ch, n0);
+    if (!MAP && q.states) {
+      if (keep_whole) {
+#pragma unroll
+        for (int i = 0; i < kChannels; ++i)
+          *reinterpret_cast<float4*>(keep + i * in.N) =
+              make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
+      } else {
+        store_states(keep - n0, h, in.N, my_ch, n0);
+      }
+      keep += HN;
+    }
     // A tile without marks goes without looking for them: a branch would keep the steps apart that
     // are to overlap.
     auto steps = [&](auto marks_here) {
@@ -180,7 +209,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
         if (!MAP) get_map(c_next, &mc[t][n0]);
       };
       read(0);
-#pragma unroll 4
+#pragma unroll 8
       for (int t = 0; t < kT; ++t) {
         float s[kChannels], x[kChannels], o[kChannels];
         float2 bp[kPairs], cp[kPairs];

@@ -181,23 +181,29 @@ struct unit {
   static __device__ __forceinline__ int step_b(int k, int lane) {
     return lane / S::kRowB + k * (32 / S::kRowB);
   }
-  // A tile's pieces of a row, zeros where the row or the sequence ends.
+  // A tile's pieces of a row, zeros where the row or the sequence ends: COUNT of them, every STRIDE
+  // one from `from` on.
+  template <int COUNT, int STRIDE, typename V>
+  __device__ __forceinline__ void fetch(piece (&w)[COUNT], const view<V>& v, int64_t t0, int64_t L,
+                                        int lane, bool ok, int from = 0) const {
+    const int c = channel(lane);
+    const V* p = v.p + (b * v.sb + (t0 + step(from, lane)) * v.st + c0 + c);
+    if (ok && t0 + kT <= L) {
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k) w[k].get(p + k * STRIDE * (32 / S::kRow) * v.st);
+    } else {
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k) {
+        w[k] = piece();
+        if (t0 + step(from + k * STRIDE, lane) < L && c < n_ch)
+          get_piece<T, kPiece>(w[k], p + k * STRIDE * (32 / S::kRow) * v.st, n_ch - c, ok);
+      }
+    }
+  }
   template <typename V>
   __device__ __forceinline__ void fetch(piece (&w)[S::NV], const view<V>& v, int64_t t0, int64_t L,
                                         int lane, bool ok) const {
-    const int c = channel(lane);
-    const V* p = v.p + (b * v.sb + (t0 + step(0, lane)) * v.st + c0 + c);
-    if (ok && t0 + kT <= L) {
-#pragma unroll
-      for (int k = 0; k < S::NV; ++k) w[k].get(p + k * (32 / S::kRow) * v.st);
-    } else {
-#pragma unroll
-      for (int k = 0; k < S::NV; ++k) {
-        w[k] = piece();
-        if (t0 + step(k, lane) < L && c < n_ch)
-          get_piece<T, kPiece>(w[k], p + k * (32 / S::kRow) * v.st, n_ch - c, ok);
-      }
-    }
+    fetch<S::NV, 1>(w, v, t0, L, lane, ok);
   }
   __device__ __forceinline__ void fetch_b(piece (&w)[S::NB], const view<const T>& v, int64_t t0,
                                           int64_t L, int N, int lane) const {
@@ -228,18 +234,19 @@ struct unit {
 
 // The steps s and the inputs s x of a tile's pieces (`bias`: of this lane's channels): softplus, and
 // zeros where there is no channel or step (which leave the state as it is).
-template <typename T, int LN>
+template <int COUNT, int STRIDE, typename T, int LN>
 __device__ __forceinline__ void stage_steps(const unit<T, LN>& u, int softplus, int64_t t0, int64_t L,
                                             int lane, const float (&bias)[kPiece],
-                                            const words<T, kPiece> (&wx)[shape<LN>::NV],
-                                            const words<T, kPiece> (&wd)[shape<LN>::NV],
-                                            float (*s)[shape<LN>::kCW], float (*in)[shape<LN>::kCW]) {
+                                            const words<T, kPiece> (&wx)[COUNT],
+                                            const words<T, kPiece> (&wd)[COUNT],
+                                            float (*s)[shape<LN>::kCW], float (*in)[shape<LN>::kCW],
+                                            int from = 0) {
   using S = shape<LN>;
   const int c = u.channel(lane);
   const bool all = u.n_ch == S::kCW && t0 + kT <= L;
 #pragma unroll
-  for (int k = 0; k < S::NV; ++k) {
-    const int t = u.step(k, lane);
+  for (int k = 0; k < COUNT; ++k) {
+    const int t = u.step(from + k * STRIDE, lane);
     float xv[kPiece], dv[kPiece];
     wx[k].to(xv);
     wd[k].to(dv);

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
     };
     auto stage = [&](int tile) {
       const int j = tile & 1;
-      stage_steps<T, LN>(u, in.softplus, (int64_t)tile * kT, in.L, lane, bias, MAP ? wd : wx, wd,
+      stage_steps<S::NV, 1>(u, in.softplus, (int64_t)tile * kT, in.L, lane, bias, MAP ? wd : wx, wd,
                          m.s[j], m.u[j]);
       u.put_b(m.Cm[j], wc, lane);
 #pragma unroll

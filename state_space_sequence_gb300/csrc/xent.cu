@@ -434,12 +434,13 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
   if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// lse and loss of 32 rows to a block from the tiles' maxima and sums; 8 warps share the tiles of a
-// row and meet in order.
-__global__ void __launch_bounds__(256)
+// lse and loss of 32 rows to a block from the tiles' maxima and sums; the block's WARPS warps share the
+// tiles of a row and meet in order (many of them where there are few rows).
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
 finish_loss(const float2* stats, const float* hit, const int64_t* target, float* loss, float* lse,
             int64_t M, int nt, int64_t V) {
-  __shared__ float2 part[8][32];
+  __shared__ float2 part[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t m = (int64_t)blockIdx.x * 32 + lane;
   float top = -INFINITY, sum = 0.0f;
@@ -450,11 +451,11 @@ finish_loss(const float2* stats, const float* hit, const int64_t* target, float*
   };
   if (m < M)
 #pragma unroll 4
-    for (int k = warp; k < nt; k += 8) add(stats[(int64_t)k * M + m]);
+    for (int k = warp; k < nt; k += WARPS) add(stats[(int64_t)k * M + m]);
   part[warp][lane] = make_float2(top, sum);
   __syncthreads();
   if (warp || m >= M) return;
-  for (int u = 1; u < 8; ++u) add(part[u][lane]);
+  for (int u = 1; u < WARPS; ++u) add(part[u][lane]);
   const float total = top + logf(sum);
   const int64_t t = target[m];
   lse[m] = total;
@@ -728,8 +729,11 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   e = rows_of<T, S>(a.type, a.W, ws + staged(a.type, a.M, a.D), a.V, a.D, &w, s);
   if (e != cudaSuccess) return e;
   if ((e = product<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
-  finish_loss<<<(unsigned)((a.M + 31) / 32), 256, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse,
-                                                          a.M, nt, a.V);
+  const unsigned blocks = (unsigned)((a.M + 31) / 32);
+  if (blocks < 152)
+    finish_loss<32><<<blocks, 1024, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V);
+  else
+    finish_loss<8><<<blocks, 256, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V);
   return cudaGetLastError();
 }
 

@@ -146,7 +146,7 @@ def main(steps: int = 241) -> None:
         rows, target = _rows(n).float(), want.reshape(-1)
         losses, lse = xent.xent_loss(rows, embed, target)
         if k % 60 == 0:
-            print(f"step {k:3d}  loss {losses.mean().item():.4f}")
+            print(f"step {k:3d}  loss {-torch.log(torch.exp(-losses) + 1e-9).mean().item():.4f}")
         dn, de = xent.xent_loss_backward(rows, embed, target, lse,
                                          torch.full_like(losses, 1.0 / (B * L)))
         dn, dy = dn.view_as(n).to(dtype), torch.zeros_like(n)

@@ -204,10 +204,22 @@ def _maps(ts, like, B, L, H, dev, what):
 
 def _maps_step(ts, like, B, H, dev, what):
     """The same for one token: [B, N] or [B, G, N]."""
-    if ts[0].dim() not in (2, 3):
-        raise ValueError(f"{what[0]}: expected [{B}, N] or [{B}, G, N], got {tuple(ts[0].shape)}")
-    G, N, out = _maps([t.unsqueeze(1) for t in ts], like, B, 1, H, dev, what)
-    return G, N, (out[0], out[1], 0, out[3], out[4], 0)
+    shape, dtype, out = ts[0].shape, like.dtype, []
+    if len(shape) == 2:
+        G, N = 1, shape[1]
+    elif len(shape) == 3:
+        G, N = shape[1], shape[2]
+    else:
+        raise ValueError(f"{what[0]}: expected [{B}, N] or [{B}, G, N], got {tuple(shape)}")
+    if shape[0] != B or G < 1 or N < 1 or H % G:
+        raise ValueError(f"{what[0]}: {tuple(shape)} for {B} entries of {H} channels")
+    for t in ts:
+        s = t.stride()
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
+                (s[-1] != 1 and N > 1) or (G > 1 and s[1] != N):
+            _wrong(t, like, shape, what[len(out) // 3])
+        out += (t.data_ptr(), s[0], 0)
+    return G, N, out
 
 
 def ssm_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, h0=None,
