@@ -18,7 +18,7 @@ namespace dlr {
 namespace ssm {
 namespace {
 
-constexpr int kWarps = 8;  // of a block: neighbouring runs of the same channels
+constexpr int kWarps = 4;  // of a block: neighbouring runs of the same channels
 
 template <typename T>
 struct conv_params {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(conv_params<T> q) {
 // The same backwards in what it forms, not in time: g of a run's steps and of the K - 1 behind it;
 // dx of a step is complete K - 1 steps later. g[HALO + i] is that of step t + i.
 template <typename T, int VE, int KM, bool EXACT>
-__global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 2 : 1) conv_back(conv_params<T> q) {
+__global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_params<T> q) {
   constexpr int CH = 4, HALO = KM - 1;
   __shared__ float sums[kWarps][32 * VE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

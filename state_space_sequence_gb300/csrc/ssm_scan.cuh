@@ -3,7 +3,6 @@
 #pragma once
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "ssm_common.cuh"
 
@@ -290,7 +289,6 @@ inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
   constexpr int64_t kSMs = 152, kUnits = 4;
   const int64_t cw = 64 / lanes_for(N), units = (H / G + cw - 1) / cw;
   const int64_t blocks = B * G * ((units + kUnits - 1) / kUnits), tiles = (L + kT - 1) / kT;
-  if (const char* e = getenv("SSM_SPLITS")) return std::max(1, std::min<int>(atoi(e), tiles));
   int best = 1;
   double least = 0.0;
   for (int s = 1; s <= std::min<int64_t>(64, tiles); ++s) {
