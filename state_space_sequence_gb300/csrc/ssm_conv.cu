@@ -151,6 +151,31 @@ __device__ __forceinline__ uint32_t marks_around(const conv_params<T>& q, int64_
   const int64_t s = t - 16 + lane;
   return __ballot_sync(0xffffffffu, s >= 0 && s < q.L && q.reset[b * q.L + s] != 0);
 }
+// The marks of 16 steps at a time, as a warp walks over them (t = 0, CH, .. from t0 on): the next
+// ones are read meanwhile, so that no step waits for them.
+template <typename T>
+struct marks_ahead {
+  const conv_params<T>& q;
+  const uint8_t* row;
+  int64_t at;  // the step whose mark this lane has in `next`
+  uint8_t next = 0;
+  uint32_t bits = 0;
+  __device__ __forceinline__ marks_ahead(const conv_params<T>& q, int64_t b, int64_t t0, int lane)
+      : q(q), row(q.reset ? q.reset + b * q.L : nullptr), at(t0 - 16 + lane) {
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() { next = row && at >= 0 && at < q.L ? row[at] : 0; }
+  // those around step t0 + t: bit l is step t0 + t - 16 + l, as far as the 16 steps go
+  __device__ __forceinline__ uint32_t around(int t) {
+    if (!row) return 0;
+    if ((t & 15) == 0) {
+      bits = __ballot_sync(0xffffffffu, next != 0);
+      at += 16;
+      fetch();
+    }
+    return bits >> (t & 15);
+  }
+};
 // Whether step t + i sees the input j steps before it: no mark on the way.
 __device__ __forceinline__ bool sees(uint32_t bits, int i, int j) {
   return (bits >> (17 + i - j) & ((1u << j) - 1)) == 0;
@@ -175,47 +200,54 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(conv_params<T> q) {
     v[HALO - j].clear();
     if (EXACT || j < q.K) input<T, VE>(v[HALO - j], q, b, t0 - j, c);
   }
-  const int64_t end = min(q.L, t0 + q.run);
+  const int steps_here = (int)min(q.L - t0, (int64_t)q.run);
+  marks_ahead<T> ahead(q, b, t0, lane);
   words<T, VE> next[CH];
   const T* px = q.x.row(b, t0) + c;
   T* py = q.y.row(b, t0) + c;
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](int t) {
+    if (t + CH <= steps_here) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
-      if (t + i < end) next[i].get(px + i * q.x.st);
+      for (int i = 0; i < CH; ++i) next[i].get(px + i * q.x.st);
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (t + i < steps_here) next[i].get(px + i * q.x.st);
+    }
     px += CH * q.x.st;
   };
-  fetch(t0);
-  for (int64_t t = t0; t < end; t += CH) {
+  fetch(0);
+  for (int t = 0; t < steps_here; t += CH) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) v[HALO + i].from(next[i]);
-    if (t + CH < end) fetch(t + CH);
-    const uint32_t bits = marks_around(q, b, t, lane);
-    auto steps = [&](auto marks_here) {
-      constexpr bool MARKS = decltype(marks_here)::value;
+    if (t + CH < steps_here) fetch(t + CH);
+    const uint32_t bits = ahead.around(t);
+    // PLAIN: all CH steps are there and no mark is near
+    auto steps = [&](auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        if (t + i >= end) break;
+        if (!PLAIN && t + i >= steps_here) break;
         piece<VE> o = bias;
 #pragma unroll
         for (int j = HALO; j >= 0; --j) {
           if (!EXACT && j >= q.K) continue;
-          if (MARKS && !sees(bits, i, j)) continue;
+          if (!PLAIN && !sees(bits, i, j)) continue;
           o.fma(w[j], v[HALO + i - j]);
         }
         if (q.act == SSM_ACT_SILU) o.silu();
         if (there) o.put(py + i * q.y.st);
       }
     };
-    if (bits)
-      steps(std::true_type{});
-    else
+    if (bits || t + CH > steps_here)
       steps(std::false_type{});
+    else
+      steps(std::true_type{});
     py += CH * q.y.st;
 #pragma unroll
     for (int j = 0; j < HALO; ++j) v[j] = v[CH + j];
   }
-  if (end == q.L && q.last) {
+  if (t0 + steps_here == q.L && q.last) {
     const uint32_t bits = marks_around(q, b, q.L - 1, lane);
     for (int j = 0; j < q.K - 1; ++j) {
       piece<VE> o;
@@ -229,7 +261,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(conv_params<T> q) {
 // The same backwards in what it forms, not in time: g of a run's steps and of the K - 1 behind it;
 // dx of a step is complete K - 1 steps later. g[HALO + i] is that of step t + i.
 template <typename T, int VE, int KM, bool EXACT>
-__global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_params<T> q) {
+__global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 3 : 1) conv_back(conv_params<T> q) {
   constexpr int CH = 4, HALO = KM - 1;
   __shared__ float sums[kWarps][32 * VE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -253,34 +285,45 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_p
       g[HALO - j].clear();
       if (EXACT || j < q.K) input<T, VE>(v[HALO - j], q, b, t0 - j, c);
     }
-    const int64_t end = min(q.L, t0 + q.run), stop = min(q.L, end + halo);
+    // counted from t0: the run's end, the row's, and where what is read ends
+    const int left = (int)min(q.L - t0, (int64_t)(q.run + SSM_MAX_TAPS + CH)), end = min(left, q.run);
+    const int stop = min(left, end + halo);
     // the first run also closes the steps of the carried state
-    const int64_t from = t0 == 0 ? -halo : t0;
+    const int from = t0 == 0 ? -halo : 0;
+    marks_ahead<T> ahead(q, b, t0, lane);
     words<T, VE> nx[CH], ng[CH];
     const T* px = q.x.row(b, t0) + c;
     const T* pg = q.dy.row(b, t0) + c;
     T* py = q.y.p + b * q.y.sb + (t0 - halo) * q.y.st + c;  // of step t - halo
-    auto fetch = [&](int64_t t) {
+    auto fetch = [&](int t) {
+      if (t + CH <= stop) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        nx[i] = ng[i] = words<T, VE>();
-        if (t + i < stop) {
+        for (int i = 0; i < CH; ++i) {
           nx[i].get(px + i * q.x.st);
           ng[i].get(pg + i * q.dy.st);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          nx[i] = ng[i] = words<T, VE>();
+          if (t + i < stop) {
+            nx[i].get(px + i * q.x.st);
+            ng[i].get(pg + i * q.dy.st);
+          }
         }
       }
       px += CH * q.x.st;
       pg += CH * q.dy.st;
     };
-    fetch(t0);
-    for (int64_t t = t0; t < end + halo; t += CH) {
+    fetch(0);
+    for (int t = 0; t < end + halo; t += CH) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         v[HALO + i].from(nx[i]);
         g[HALO + i].from(ng[i]);
       }
       fetch(t + CH);
-      const uint32_t bits = marks_around(q, b, t, lane);
+      const uint32_t bits = ahead.around(t);
       // PLAIN: all CH steps are the run's own, the steps that they complete too, and no mark is near
       auto steps = [&](auto plain) {
         constexpr bool PLAIN = decltype(plain)::value;
@@ -297,7 +340,7 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_p
             p.silu_slope();
             g[HALO + i].mul(p);
             // what is behind the row may have been formed of anything
-            if (!PLAIN && t + i >= q.L) g[HALO + i].clear();
+            if (!PLAIN && t + i >= left) g[HALO + i].clear();
           }
         }
 #pragma unroll
@@ -314,7 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_p
         // steps t + i - halo are complete
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const int64_t done = t + i - halo;
+          const int done = t + i - halo;
           if (!PLAIN && (done < from || done >= end)) continue;
           piece<VE> o;
           o.clear();
@@ -330,12 +373,12 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_p
                 if (m == HALO - halo + i + j) o.fma(w[j], g[m]);
             }
           }
-          if (!PLAIN && q.dlast && done >= q.L - halo) {
-            const int j = (int)(q.L - 1 - done);
+          if (!PLAIN && q.dlast && done >= left - halo) {
+            const int j = left - 1 - done;
             if (sees(marks_around(q, b, q.L - 1, lane), 0, j)) {
               words<T, VE> wl;
               piece<VE> d;
-              wl.get(q.dlast + (b * halo + done - (q.L - halo)) * q.H + c);
+              wl.get(q.dlast + (b * halo + done - (left - halo)) * q.H + c);
               d.from(wl);
               o.add(d);
             }
@@ -347,7 +390,7 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 4 : 1) conv_back(conv_p
             o.put(q.dstate + (b * halo + done + halo) * q.H + c);
         }
       };
-      if (bits || t + CH > end || t - halo < t0 || (q.dlast && t + CH > q.L - halo))
+      if (bits || t + CH > end || t < halo || (q.dlast && t + CH > left - halo))
         steps(std::false_type{});
       else
         steps(std::true_type{});
@@ -467,11 +510,12 @@ void go(conv_params<T> q, cudaStream_t s) {
   }
 }
 
-// Pieces of 8 bytes forwards, two channels backwards (with wider ones the registers would leave too
-// few warps on an SM); single channels where rows do not stand on multiples of them.
+// Pieces of 8 bytes; single channels where rows do not stand on multiples of them. Backwards four
+// channels in 16 bits leave an SM 12 warps and take 190 us at B4 L16384 H2048, two leave it 16 and take
+// 215: what a step costs besides its channels is then shared by fewer.
 template <typename T, int KM, bool EXACT, Dir DIR>
 void by_piece(const conv_params<T>& q, cudaStream_t s) {
-  constexpr int VE = DIR == kBack ? 2 : 8 / (int)sizeof(T), kBytes = VE * (int)sizeof(T);
+  constexpr int VE = 8 / (int)sizeof(T), kBytes = 8;
   if (whole_rows(q, kBytes))
     go<T, VE, KM, EXACT, DIR>(q, s);
   else
