@@ -91,11 +91,11 @@ struct decay {
     else
       return mul2(a, v);
   }
-  __device__ __forceinline__ float2 of_plus(float2 v, float2 b) const {
+  __device__ __forceinline__ float2 of_plus(float2 v, float2 b, float2 x) const {  // and b x
     if constexpr (PRECISE)
-      return add2(fma2(a, v, v), b);
+      return fma2(b, x, fma2(a, v, v));
     else
-      return fma2(a, v, b);
+      return fma2(a, v, mul2(b, x));
   }
 };
 

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
 #pragma unroll
           for (int p = 0; p < kPairs; ++p) {
             const decay<kPrecise> a(rate[i][p], two(s[i]));
-            h[i][p] = a.of_plus(h[i][p], mul2(bp[p], two(x[i])));
+            h[i][p] = a.of_plus(h[i][p], bp[p], two(x[i]));
             if (!MAP) acc = p ? fma2(h[i][p], cp[p], acc) : mul2(h[i][p], cp[p]);
           }
           if (!MAP) o[i] = acc.x + acc.y;
@@ -302,40 +302,48 @@ struct step_params {
   float* h_out;
 };
 
-// LN lanes to a channel, 4 states to a lane, of R batch entries (the rates are then read once for all
-// of them). The states go through memory once each way and are all there is to it: 134 MB at 256 x
-// 4096 x 16.
-template <typename T, int LN, bool QUADS, int R>
-__global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
-  const unsigned columns = (unsigned)(q.H + 256 / LN - 1) / (256 / LN);
+// LN lanes to a channel, Q quads of states to a lane (the lanes' quads in turn, so that a channel's lie
+// beside one another), of R batch entries (the rates are then read once for all of them). The states
+// go through memory once each way and are all there is to it: 134 MB at 256 x 4096 x 16, which took
+// 36 us with one quad to a lane and its maps read one by one (the steps and gates, formed by every
+// lane of a channel, bound it then), 35 with two quads, 30 with them in blocks of 128 threads.
+constexpr int kStepThreads = 128;
+template <typename T, int LN, int Q, bool QUADS, int R>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(step_params<T> q) {
+  constexpr int P = 2 * Q;  // pairs of states
+  const unsigned columns = (unsigned)(q.H + kStepThreads / LN - 1) / (kStepThreads / LN);
   const int at = threadIdx.x % LN, n0 = 4 * at;
-  const int c0 = (int)(blockIdx.x % columns) * (256 / LN) + threadIdx.x / LN, c = min(c0, q.H - 1);
+  const int c0 = (int)(blockIdx.x % columns) * (kStepThreads / LN) + threadIdx.x / LN, c = min(c0, q.H - 1);
   const int64_t b0 = (int64_t)(blockIdx.x / columns) * R;
   const int group = c / q.Hg;
-  float2 rate[2], h[R][2], bm[R][2], cm[R][2];
+  float2 rate[P], h[R][P], bm[R][P], cm[R][P];
   float s[R], x[R], z[R];
-  auto quad = [&](float2 (&v)[2], const float* p) {
-    const float4 t = get_quad(p, n0, q.N, QUADS);
-    v[0] = make_float2(t.x, t.y);
-    v[1] = make_float2(t.z, t.w);
-  };
-  auto map = [&](float2 (&v)[2], const T* p) {
-    float t[4];
-    if constexpr (QUADS) {
+  auto quad = [&](float2 (&v)[P], const float* p) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = to_f(p[n0 + j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = n0 + j < q.N ? to_f(p[n0 + j]) : 0.0f;
+    for (int k = 0; k < Q; ++k) {
+      const float4 t = get_quad(p, n0 + 4 * LN * k, q.N, QUADS);
+      v[2 * k] = make_float2(t.x, t.y);
+      v[2 * k + 1] = make_float2(t.z, t.w);
     }
-    v[0] = make_float2(t[0], t[1]);
-    v[1] = make_float2(t[2], t[3]);
+  };
+  auto map = [&](float2 (&v)[P], const T* p) {
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      words<T, 4> w;
+      float t[4];
+      get_piece<T, 4>(w, p + n0 + 4 * LN * k, q.N - n0 - 4 * LN * k, QUADS);
+      w.to(t);
+      v[2 * k] = make_float2(t[0], t[1]);
+      v[2 * k + 1] = make_float2(t[2], t[3]);
+    }
   };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t b = min(b0 + r, q.B - 1);
     quad(h[r], q.h + (b * q.H + c) * q.N);
-    if (q.reset && q.reset[b]) h[r][0] = h[r][1] = two(0.0f);
+    if (q.reset && q.reset[b])
+#pragma unroll
+      for (int p = 0; p < P; ++p) h[r][p] = two(0.0f);
     s[r] = to_f(q.dt.row(b, 0)[c]);
     x[r] = to_f(q.x.row(b, 0)[c]);
     z[r] = q.z.p ? to_f(q.z.row(b, 0)[c]) : 0.0f;
@@ -343,8 +351,8 @@ __global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
     map(cm[r], q.Cm.row(b, 0) + (int64_t)group * q.N);
   }
   quad(rate, q.A + (int64_t)c * q.N);
-  rate[0] = mul2(rate[0], two(kLog2e));
-  rate[1] = mul2(rate[1], two(kLog2e));
+#pragma unroll
+  for (int p = 0; p < P; ++p) rate[p] = mul2(rate[p], two(kLog2e));
   const float bias = q.bias ? q.bias[c] : 0.0f, D = q.D ? q.D[c] : 0.0f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -353,24 +361,28 @@ __global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
     if (q.softplus) s[r] = softplus2(two(s[r])).x;
     float2 acc;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < P; ++p) {
       const decay<sizeof(T) == 4> a(rate[p], two(s[r]));
-      h[r][p] = a.of_plus(h[r][p], mul2(bm[r][p], two(s[r] * x[r])));
+      h[r][p] = a.of_plus(h[r][p], bm[r][p], two(s[r] * x[r]));
       acc = p ? fma2(h[r][p], cm[r][p], acc) : mul2(h[r][p], cm[r][p]);
     }
     float o = acc.x + acc.y;
 #pragma unroll
     for (int d = 1; d < LN; d *= 2) o += __shfl_xor_sync(0xffffffffu, o, d);
     if (b >= q.B || c0 >= q.H) continue;
-    float* to = q.h_out + (b * q.H + c) * q.N + n0;
-    if constexpr (QUADS) {
-      *reinterpret_cast<float4*>(to) =
-          make_float4(h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y);
-    } else {
-      const float v[4] = {h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y};
+    float* to = q.h_out + (b * q.H + c) * q.N;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n0 + j < q.N) to[j] = v[j];
+    for (int k = 0; k < Q; ++k) {
+      const int n = n0 + 4 * LN * k;
+      const float2 lo = h[r][2 * k], hi = h[r][2 * k + 1];
+      if constexpr (QUADS) {
+        *reinterpret_cast<float4*>(to + n) = make_float4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < q.N) to[n + j] = v[j];
+      }
     }
     if (at) continue;
     if (q.D) o = fmaf(D, x[r], o);
@@ -379,19 +391,21 @@ __global__ void __launch_bounds__(256) step_kernel(step_params<T> q) {
   }
 }
 
-template <typename T, int LN>
+template <typename T, int LN, int Q>
 cudaError_t run_step(const step_params<T>& q, cudaStream_t s) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(q.A) | reinterpret_cast<uintptr_t>(q.h) |
                         reinterpret_cast<uintptr_t>(q.h_out);
-  const unsigned columns = (unsigned)((q.H + 256 / LN - 1) / (256 / LN));
-  if (q.N == 4 * LN && (all & 15) == 0) {
+  const uintptr_t maps = reinterpret_cast<uintptr_t>(q.Bm.p) | reinterpret_cast<uintptr_t>(q.Cm.p) |
+                         (uintptr_t)((q.Bm.sb | q.Cm.sb) * (int64_t)sizeof(T));
+  const unsigned columns = (unsigned)((q.H + kStepThreads / LN - 1) / (kStepThreads / LN));
+  if (q.N == 4 * LN * Q && (all & 15) == 0 && (maps & (4 * sizeof(T) - 1)) == 0) {
     // two entries to a thread where that leaves every SM some blocks
     if (columns * q.B >= 2 * 152 * 4)
-      step_kernel<T, LN, true, 2><<<columns * (unsigned)((q.B + 1) / 2), 256, 0, s>>>(q);
+      step_kernel<T, LN, Q, true, 2><<<columns * (unsigned)((q.B + 1) / 2), kStepThreads, 0, s>>>(q);
     else
-      step_kernel<T, LN, true, 1><<<columns * (unsigned)q.B, 256, 0, s>>>(q);
+      step_kernel<T, LN, Q, true, 1><<<columns * (unsigned)q.B, kStepThreads, 0, s>>>(q);
   } else {
-    step_kernel<T, LN, false, 1><<<columns * (unsigned)q.B, 256, 0, s>>>(q);
+    step_kernel<T, LN, Q, false, 1><<<columns * (unsigned)q.B, kStepThreads, 0, s>>>(q);
   }
   return cudaGetLastError();
 }
@@ -404,12 +418,12 @@ cudaError_t step_of(const ssm_step_args& a, cudaStream_t s) {
   const step_params<T> q{a.B, (int)a.H, (int)(a.H / a.G), (int)a.N, (int)a.G, (int)a.softplus,
                          in(a.x), in(a.dt), in(a.z), in(a.Bm), in(a.Cm), a.A, a.D, a.dt_bias,
                          a.h, a.reset, out_view<T>(a.y), a.h_out};
-  switch (a.N <= 4 ? 1 : 2 * lanes_for(a.N)) {
-    case 1: return run_step<T, 1>(q, s);
-    case 2: return run_step<T, 2>(q, s);
-    case 4: return run_step<T, 4>(q, s);
-    case 8: return run_step<T, 8>(q, s);
-    default: return run_step<T, 16>(q, s);
+  if (a.N <= 4) return run_step<T, 1, 1>(q, s);
+  switch (lanes_for(a.N)) {
+    case 1: return run_step<T, 1, 2>(q, s);
+    case 2: return run_step<T, 2, 2>(q, s);
+    case 4: return run_step<T, 4, 2>(q, s);
+    default: return run_step<T, 8, 2>(q, s);
   }
 }
 

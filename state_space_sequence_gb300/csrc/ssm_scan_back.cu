@@ -110,7 +110,7 @@ __device__ __forceinline__ void advance(float2 (&h)[kChannels][kPairs],
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
       const decay<PRECISE> a(rate[i][p], two(s[i]));
-      h[i][p] = a.of_plus(h[i][p], mul2(bp[p], two(u[i])));
+      h[i][p] = a.of_plus(h[i][p], bp[p], two(u[i]));
     }
 }
 
