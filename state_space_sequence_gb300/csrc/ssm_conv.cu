@@ -108,6 +108,7 @@ template <typename T, int VE>
 __device__ __forceinline__ void input(piece<VE>& v, const conv_params<T>& q, int64_t b, int64_t t,
                                       int64_t c) {
   words<T, VE> w;
+  if (!DLR_IN(c + VE - 1, q.H) || !DLR_IN(t + q.K - 1, q.L + q.K - 1)) t = 0, c = 0;
   if (t >= 0)
     w.get(q.x.row(b, t) + c);
   else if (q.state)
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(conv_params<T> q) {
   auto fetch = [&](int t) {
     if (t + CH <= steps_here) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) next[i].get(px + i * q.x.st);
+      for (int i = 0; i < CH; ++i)
+        if (DLR_IN(t0 + t + i, q.L)) next[i].get(px + i * q.x.st);
     } else {
 #pragma unroll
       for (int i = 0; i < CH; ++i)
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(conv_params<T> q) {
           o.fma(w[j], v[HALO + i - j]);
         }
         if (q.act == SSM_ACT_SILU) o.silu();
-        if (there) o.put(py + i * q.y.st);
+        if (there && DLR_IN(t0 + t + i, q.L) && DLR_IN(c + VE - 1, q.H)) o.put(py + i * q.y.st);
       }
     };
     if (bits || t + CH > steps_here)
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 3 : 1) conv_back(conv_p
       if (t + CH <= stop) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+          if (!DLR_IN(t0 + t + i, q.L)) continue;
           nx[i].get(px + i * q.x.st);
           ng[i].get(pg + i * q.dy.st);
         }
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 3 : 1) conv_back(conv_p
               o.add(d);
             }
           }
-          if (!there) continue;
+          if (!there || !DLR_IN(t0 + done + halo, q.L + halo) || !DLR_IN(c + VE - 1, q.H)) continue;
           if (PLAIN || done >= 0)
             o.put(py + i * q.y.st);
           else if (q.dstate)
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(32 * kWarps, KM == 4 ? 3 : 1) conv_back(conv_p
       float v = 0.0f;
       for (int u = 0; u < kWarps; ++u) v += sums[u][k];
       const int row = j < KM ? q.K - 1 - j : q.K;
-      if (ch < q.H) q.part[((int64_t)row * q.parts + part) * q.H + ch] = v;
+      if (ch < q.H && DLR_IN(part, q.parts)) q.part[((int64_t)row * q.parts + part) * q.H + ch] = v;
     }
   }
 }
@@ -469,6 +472,7 @@ __global__ void __launch_bounds__(128) conv_step(conv_params<T> q) {
     piece<VE> o = bias;
 #pragma unroll
     for (int j = 0; j < KM; ++j) o.fma(w[j], win[r][j]);
+    if (!DLR_IN(c + VE - 1, q.H)) return;
     if (q.act == SSM_ACT_SILU) o.silu();
     o.put(q.y.row(b, 0) + c);
 #pragma unroll

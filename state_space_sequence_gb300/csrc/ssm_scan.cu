@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
             }
           }
           const float y[kPiece] = {o[0].x, o[0].y, o[1].x, o[1].y};
+          if (!DLR_IN(c, S::kCW) || !DLR_IN(all ? t0 + t : 0, in.L)) continue;
           if (all)
             put_piece<T, kPiece>(py + k * kStep * (32 / S::kRow) * q.y.st, y, kPiece, true);
           else if (t0 + t < in.L && c < u.n_ch)
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
     const float (*mb)[S::kNP] = m.Bm[tile & 1];
     const float (*mc)[S::kNP] = m.Cm[MAP ? 0 : tile & 1];
     float (*mo)[kHalves * LN][S::kCW] = m.o[MAP ? 0 : tile & 1];
-    if (!MAP && q.states) {
+    if (!MAP && q.states && DLR_IN(tile, in.tiles)) {
       if (keep_whole) {
 #pragma unroll
         for (int i = 0; i < kChannels; ++i)
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(step_params<T> q) {
     float o = acc.x + acc.y;
 #pragma unroll
     for (int d = 1; d < LN; d *= 2) o += __shfl_xor_sync(0xffffffffu, o, d);
-    if (b >= q.B || c0 >= q.H) continue;
+    if (b >= q.B || c0 >= q.H || !DLR_IN(QUADS ? n0 + 4 * LN * (Q - 1) + 3 : 0, q.N)) continue;
     float* to = q.h_out + (b * q.H + c) * q.N;
 #pragma unroll
     for (int k = 0; k < Q; ++k) {

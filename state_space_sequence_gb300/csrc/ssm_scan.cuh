@@ -9,6 +9,8 @@
 namespace dlr {
 namespace ssm {
 
+constexpr int kSiteFileScan = 27;  // bounds-checked build: this header's site number
+
 template <typename T>
 struct inputs {
   int64_t B, L;
@@ -57,7 +59,7 @@ __device__ __forceinline__ void clear(float2 (&h)[kChannels][kPairs]) {
 __device__ __forceinline__ float4 get_quad(const float* p, int n, int N, bool whole) {
   float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (n >= N) return t;
-  if (whole) return *reinterpret_cast<const float4*>(p + n);
+  if (whole && DLR_IN_FILE(n + 3, N, kSiteFileScan)) return *reinterpret_cast<const float4*>(p + n);
   t.x = p[n];
   if (n + 1 < N) t.y = p[n + 1];
   if (n + 2 < N) t.z = p[n + 2];
@@ -85,7 +87,7 @@ __device__ __forceinline__ void store_states(float* p, const float2 (&h)[kChanne
   for (int i = 0; i < kChannels; ++i) {
     if (i >= n_ch || n0 >= N) continue;
     float* q = p + (int64_t)i * N + n0;
-    if (whole) {
+    if (whole && DLR_IN_FILE(n0 + 3, N, kSiteFileScan)) {
       *reinterpret_cast<float4*>(q) = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
     } else {
       q[0] = h[i][0].x;
@@ -124,7 +126,10 @@ __device__ __forceinline__ void enter(float2 (&h)[kChannels][kPairs], const inpu
 #pragma unroll
     for (int i = 0; i < kChannels; ++i) {
       if (i >= n_ch) continue;
-      const float s = in.sums[row * in.H + c + i];
+      const float s = DLR_IN_FILE(row, in.B * in.splits, kSiteFileScan) &&
+                              DLR_IN_FILE(c + i, in.H, kSiteFileScan)
+                          ? in.sums[row * in.H + c + i]
+                          : 0.0f;
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         const float2 z = mul2(rate[i][p], two(s));
@@ -189,7 +194,10 @@ struct unit {
     const V* p = v.p + (b * v.sb + (t0 + step(from, lane)) * v.st + c0 + c);
     if (ok && t0 + kT <= L) {
 #pragma unroll
-      for (int k = 0; k < COUNT; ++k) w[k].get(p + k * STRIDE * (32 / S::kRow) * v.st);
+      for (int k = 0; k < COUNT; ++k)
+        if (DLR_IN_FILE(t0 + step(from + k * STRIDE, lane), L, kSiteFileScan) &&
+            DLR_IN_FILE(c + kPiece - 1, n_ch, kSiteFileScan))
+          w[k].get(p + k * STRIDE * (32 / S::kRow) * v.st);
     } else {
 #pragma unroll
       for (int k = 0; k < COUNT; ++k) {
@@ -210,7 +218,10 @@ struct unit {
     const T* p = v.p + (b * v.sb + (t0 + step_b(0, lane)) * v.st + (int64_t)group * N + n);
     if (whole_b && t0 + kT <= L) {
 #pragma unroll
-      for (int k = 0; k < S::NB; ++k) w[k].get(p + k * (32 / S::kRowB) * v.st);
+      for (int k = 0; k < S::NB; ++k)
+        if (DLR_IN_FILE(t0 + step_b(k, lane), L, kSiteFileScan) &&
+            DLR_IN_FILE(n + kPiece - 1, N, kSiteFileScan))
+          w[k].get(p + k * (32 / S::kRowB) * v.st);
     } else {
 #pragma unroll
       for (int k = 0; k < S::NB; ++k) {

@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
       u.fetch_b(wc, in.Cm, t0, in.L, in.N, lane);
       if constexpr (!MAP) {
         u.fetch_b(wb, in.Bm, t0, in.L, in.N, lane);
-        const float* src = q.states + (u.b * in.tiles + tile) * HN + (int64_t)u.c0 * in.N;
+        const float* src = q.states + (u.b * in.tiles + (DLR_IN(tile, in.tiles) ? tile : 0)) * HN +
+                           (int64_t)u.c0 * in.N;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int i = (k * 32 + lane) * 4, ci = i / S::kNP;
@@ -241,13 +242,16 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<LN>, 1) back_kernel
           const float4 p = *reinterpret_cast<const float4*>(&all[w].dBC[j][0][0][0] + i);
           v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
         }
-        if (t0 + i / pitch < in.L) *reinterpret_cast<float4*>(part + i) = v;
+        if (t0 + i / pitch < in.L &&
+            DLR_IN(part + i + 3 - q.part_bc, (int64_t)in.G * in.blocks * in.B * in.L * pitch))
+          *reinterpret_cast<float4*>(part + i) = v;
       }
       const bool all_there = ok_o && t0 + kT <= in.L;
       auto out = [&](const view<T>& v, int k, const float2 (&o)[2]) {
         const int64_t t = t0 + u.step(k, lane);
         T* p = v.p + (u.b * v.sb + t * v.st + u.c0 + c);
         const float y[kPiece] = {o[0].x, o[0].y, o[1].x, o[1].y};
+        if (!DLR_IN(all_there ? t : 0, in.L) || !DLR_IN(all_there ? c + kPiece - 1 : 0, S::kCW)) return;
         if (all_there)
           put_piece<T, kPiece>(p, y, kPiece, true);
         else if (t < in.L && c < u.n_ch)

@@ -179,7 +179,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         for (int k = 0, k0 = from; k < nk; ++k, k0 += kBK, ++it) {
           const uint32_t s = it % kStages;
           if (it >= kStages && !(ok = tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1))) break;
-          uint8_t* to = base + s * kStage + (is_a ? 0 : kABytes);
+          uint8_t* to = base + (DLR_IN(s, kStages) ? s : 0) * kStage + (is_a ? 0 : kABytes);
           tc::mbar_arrive_expect_tx(&full[s], bytes);
           if (along) {
             tc::tma_load_4d(to, map, 0, shift + k0, row / 64, part, &full[s]);
@@ -310,7 +310,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
           if (at >= c && at < c + 32)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (at == c + i) g.hit[row] = v[i];
+              if (at == c + i && DLR_IN(row, g.M)) g.hit[row] = v[i];
           float most = v[0];
 #pragma unroll
           for (int i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
@@ -324,7 +324,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
-        if (row < g.M) g.stats[(int64_t)ni * g.M + row] = make_float2(top, sum);
+        if (row < g.M && DLR_IN(ni, nt)) g.stats[(int64_t)ni * g.M + row] = make_float2(top, sum);
       } else if constexpr (MODE == kGrad) {
         constexpr int kParts = sizeof(O) == 4 ? 3 : 1;
         const uint32_t sw = uint32_t(lane & 7);
@@ -366,7 +366,8 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
                   v[8 * k + 2 * i + 1] = b - f.y;
                 }
               }
-              *reinterpret_cast<uint4*>(box + lane * 128 + ((uint32_t(k) ^ sw) << 4)) =
+              if (DLR_IN(box - base + lane * 128 + 127, kBarOff))
+                *reinterpret_cast<uint4*>(box + lane * 128 + ((uint32_t(k) ^ sw) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
             tc::fence_proxy_async_smem();
@@ -393,7 +394,8 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
             __syncwarp();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(box + lane * 128 + ((uint32_t(k) ^ sw) << 4)) =
+              if (DLR_IN(box - base + lane * 128 + 127, kBarOff))
+                *reinterpret_cast<float4*>(box + lane * 128 + ((uint32_t(k) ^ sw) << 4)) =
                   make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             tc::fence_proxy_async_smem();
             __syncwarp();
