@@ -5,7 +5,8 @@
 // multiply-add. A thread takes VE neighbouring channels over a run of steps, a few steps at a time with
 // the K - 1 inputs before them in registers, and reads the next few meanwhile: each input is read once
 // by its run and, of the K - 1 before the run, once more (from the cache: the run before is the
-// neighbouring warp's).
+// neighbouring warp's). B4 L16384 H2048 K4 bfloat16 with marks: 92 us forwards (5.8 TB/s), 186 backwards
+// (4.3 TB/s; fixed latencies at 12 warps an SM), one token of 256 x 4096 5 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -14,6 +14,9 @@
 // first. Products of parts are exact and accumulated in float32, as those of 16-bit inputs; but the
 // tensor core cuts off where it adds, a step of 16 of the sum at a time, and what that leaves out adds
 // up (5e-6 of dh at V = 4099), so for float32 every 64 steps the accumulator is added to a second one.
+//
+// 8192 x 50257 x 2048 bfloat16, tensor products at the rate of the power limit: z with the loss 949 us
+// (1.78 PFLOP/s), d 1100, dh 1114, dW 1152 (1.46). 16 rows of it: 37 us, W read at 5.6 TB/s.
 #include <cuda.h>
 
 #include <algorithm>
