@@ -7,8 +7,8 @@
 // multiply-add for the state, one for the output and one product for the input. Everything else is
 // done once a tile of 16 steps, by pieces of rows: the step's softplus, the skip and the gate.
 //
-// B4 L4096 H4096 N16 bfloat16 with its states kept takes 423 us (1.9 TB/s): issue slots (60%, 71% on the
-// 128 SMs that have units) and shared memory (66%, 79%) bound it; its exponentials alone are 115 us.
+// B4 L4096 H4096 N16 bfloat16 with its states kept takes 421 us (1.9 TB/s): issue slots (60%, 71% where an
+// SM has four units) and shared memory (66%, 79%) bound it; its exponentials alone are 115 us.
 // Float32 at B1 L65536 H256 N64 takes 500 us, and 402 for the maps of its 19 splits: its decays bound it.
 #include <type_traits>
 
@@ -28,10 +28,17 @@ struct scan_params {
   float *h_last, *states;
 };
 
-// Of a block: on each quarter of an SM two warps that run a unit, two that stage, each every other
-// piece of a tile, and two that finish. With one of each the case above took 437 us: a
-// helper alone, mostly waiting for itself, took as long for a tile as the running warps.
-constexpr int kUnits = 4, kHelpers = 2, kUnitWarps = kHalves + 2 * kHelpers;
+// Of a unit: two warps that run it, two that stage, each every other piece of a tile, and two that
+// finish. With one of each the case above took 437 us: a helper alone, mostly waiting for itself, took
+// as long for a tile as the running warps.
+constexpr int kHelpers = 2, kUnitWarps = kHalves + 2 * kHelpers;
+// Units of a block, of which an SM has four units' worth. In 16 bits one: where there are few they then
+// spread over the SMs (B1 L333 H1024 N16 16 -> 13 us, the case above 423 -> 421). Four for float32, each
+// on a quarter of an SM, whose multiply-adds then are not left to chance (B1 L16384 H1024 N16 246 us,
+// with one 289), and above 32 states, whose maps are most of what is read and stay in the L1 for all
+// four (B4 L4096 H1024 N64 bfloat16 463 us, with one 487).
+template <typename T, int LN>
+constexpr int kUnitsOf = sizeof(T) == 2 && LN <= 4 ? 1 : 4;
 
 // A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
 // tiles in turn.
@@ -46,10 +53,11 @@ struct scan_tile {
 
 // MAP: only the state that each split but the last adds, and the sum of its steps.
 template <typename T, int LN, bool MAP>
-__global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_params<T> q) {
+__global__ void __launch_bounds__(32 * kUnitWarps * kUnitsOf<T, LN>, 4 / kUnitsOf<T, LN>)
+scan_kernel(scan_params<T> q) {
   using S = shape<LN>;
   constexpr bool kPrecise = sizeof(T) == 4;
-  constexpr int CL = 32 / LN;
+  constexpr int CL = 32 / LN, kUnits = kUnitsOf<T, LN>;
   extern __shared__ float4 smem[];
   const inputs<T>& in = q.in;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kUnits;
@@ -265,6 +273,7 @@ __global__ void __launch_bounds__(32 * kUnitWarps * kUnits, 1) scan_kernel(scan_
 template <typename T, int LN>
 cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
   using S = shape<LN>;
+  constexpr int kUnits = kUnitsOf<T, LN>;
   q.in.blocks = (q.in.Hg + S::kCW - 1) / S::kCW;
   const int64_t units = (int64_t)q.in.blocks * q.in.G * q.in.B;
   auto grid = [](int64_t n) { return (unsigned)((n + kUnits - 1) / kUnits); };
