@@ -292,7 +292,7 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
 
 template <typename T>
 cudaError_t scan_of(const ssm_scan_args& a, cudaStream_t s) {
-  scan_params<T> q{make_inputs<T>(a), out_view<T>(a.y), a.h_last, a.states};
+  scan_params<T> q{make_inputs<T>(a, lanes_for(a.N)), out_view<T>(a.y), a.h_last, a.states};
   q.in.ends = static_cast<float*>(a.workspace);
   q.in.sums = q.in.ends + a.B * q.in.splits * a.H * a.N;
   switch (lanes_for(a.N)) {
@@ -444,7 +444,7 @@ cudaError_t step_of(const ssm_step_args& a, cudaStream_t s) {
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
-  return (size_t)map_floats(B, H, N, splits_for(B, L, H, N, G)) * 4;
+  return (size_t)map_floats(B, H, N, splits_for(B, L, H, G, lanes_for(N))) * 4;
 }
 
 cudaError_t launch_scan(const ssm_scan_args& a, cudaStream_t s) {

@@ -163,7 +163,7 @@ struct unit {
     c0 = g * in.Hg + first;
     n_ch = max(0, min(S::kCW, in.Hg - first));
     whole = n_ch == S::kCW && pieces(in.x) && pieces(in.dt);
-    whole_b = in.N == S::kNP && maps(in.Bm, in.N) && maps(in.Cm, in.N);
+    whole_b = in.N % kPiece == 0 && maps(in.Bm, in.N) && maps(in.Cm, in.N);
   }
   template <typename V>
   __device__ __forceinline__ bool pieces(const view<V>& v) const {
@@ -216,7 +216,7 @@ struct unit {
                                           int64_t L, int N, int lane) const {
     const int n = state(lane);
     const T* p = v.p + (b * v.sb + (t0 + step_b(0, lane)) * v.st + (int64_t)group * N + n);
-    if (whole_b && t0 + kT <= L) {
+    if (whole_b && N == S::kNP && t0 + kT <= L) {
 #pragma unroll
       for (int k = 0; k < S::NB; ++k)
         if (DLR_IN_FILE(t0 + step_b(k, lane), L, kSiteFileScan) &&
@@ -227,7 +227,7 @@ struct unit {
       for (int k = 0; k < S::NB; ++k) {
         w[k] = piece();
         if (t0 + step_b(k, lane) < L && n < N)
-          get_piece<T, kPiece>(w[k], p + k * (32 / S::kRowB) * v.st, N - n, false);
+          get_piece<T, kPiece>(w[k], p + k * (32 / S::kRowB) * v.st, N - n, whole_b);
       }
     }
   }
@@ -296,9 +296,9 @@ __device__ __forceinline__ void load_channels(float (&v)[kPiece], const float* p
 // leave the GPU idle; rows are then cut, and the states at the cuts come from a pass over the steps
 // alone (about a third of the scan's time). Blocks of four units go one to an SM; a split takes two
 // tiles more, to fill and to drain.
-inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
+inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t G, int lanes) {
   constexpr int64_t kSMs = 152, kUnits = 4;
-  const int64_t cw = 64 / lanes_for(N), units = (H / G + cw - 1) / cw;
+  const int64_t cw = 64 / lanes, units = (H / G + cw - 1) / cw;
   const int64_t blocks = B * G * ((units + kUnits - 1) / kUnits), tiles = (L + kT - 1) / kT;
   int best = 1;
   double least = 0.0;
@@ -311,7 +311,7 @@ inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
 }
 
 template <typename T, typename ARGS>
-inputs<T> make_inputs(const ARGS& a) {
+inputs<T> make_inputs(const ARGS& a, int lanes) {
   inputs<T> q{};
   q.B = a.B, q.L = a.L, q.H = (int)a.H, q.N = (int)a.N, q.G = (int)a.G;
   q.Hg = q.H / q.G;
@@ -322,7 +322,7 @@ inputs<T> make_inputs(const ARGS& a) {
   q.x = in(a.x), q.dt = in(a.dt), q.z = in(a.z), q.Bm = in(a.Bm), q.Cm = in(a.Cm);
   q.A = a.A, q.D = a.D, q.bias = a.dt_bias, q.h0 = a.h0, q.reset = a.reset;
   q.tiles = (int)((a.L + kT - 1) / kT);
-  const int want = splits_for(a.B, a.L, a.H, a.N, a.G);
+  const int want = splits_for(a.B, a.L, a.H, a.G, lanes);
   q.per_split = (q.tiles + want - 1) / want;
   q.splits = (q.tiles + q.per_split - 1) / q.per_split;  // each has at least one tile
   return q;
