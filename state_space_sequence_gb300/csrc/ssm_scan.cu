@@ -37,8 +37,14 @@ constexpr int kHelpers = 2, kUnitWarps = kHalves + 2 * kHelpers;
 // on a quarter of an SM, whose multiply-adds then are not left to chance (B1 L16384 H1024 N16 246 us,
 // with one 289), and above 32 states, whose maps are most of what is read and stay in the L1 for all
 // four (B4 L4096 H1024 N64 bfloat16 463 us, with one 487).
+constexpr int units_of(size_t element, int lanes) { return element == 2 && lanes <= 4 ? 1 : 4; }
 template <typename T, int LN>
-constexpr int kUnitsOf = sizeof(T) == 2 && LN <= 4 ? 1 : 4;
+constexpr int kUnitsOf = units_of(sizeof(T), LN);
+// The maps take 0.70 of the scan's time in 16 bits, 0.80 in float32.
+int splits_of(size_t element, int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
+  const int lanes = lanes_for(N);
+  return splits_for(B, L, H, G, lanes, units_of(element, lanes), element == 2 ? 0.7 : 0.8);
+}
 
 // A unit's part of shared memory: what a tile's steps read (s, s x, Bm, Cm), and the outputs, for two
 // tiles in turn.
@@ -292,7 +298,7 @@ cudaError_t run_scan(scan_params<T> q, cudaStream_t s) {
 
 template <typename T>
 cudaError_t scan_of(const ssm_scan_args& a, cudaStream_t s) {
-  scan_params<T> q{make_inputs<T>(a, lanes_for(a.N)), out_view<T>(a.y), a.h_last, a.states};
+  scan_params<T> q{make_inputs<T>(a, splits_of(sizeof(T), a.B, a.L, a.H, a.N, a.G)), out_view<T>(a.y), a.h_last, a.states};
   q.in.ends = static_cast<float*>(a.workspace);
   q.in.sums = q.in.ends + a.B * q.in.splits * a.H * a.N;
   switch (lanes_for(a.N)) {
@@ -444,7 +450,9 @@ cudaError_t step_of(const ssm_step_args& a, cudaStream_t s) {
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
-  return (size_t)map_floats(B, H, N, splits_for(B, L, H, G, lanes_for(N))) * 4;
+  // enough for either type
+  return (size_t)map_floats(B, H, N, std::max(splits_of(2, B, L, H, N, G),
+                                              splits_of(4, B, L, H, N, G))) * 4;
 }
 
 cudaError_t launch_scan(const ssm_scan_args& a, cudaStream_t s) {

@@ -294,24 +294,28 @@ __device__ __forceinline__ void load_channels(float (&v)[kPiece], const float* p
 
 // How many splits a sequence is cut into. A unit goes through its rows step by step, so few channels
 // leave the GPU idle; rows are then cut, and the states at the cuts come from a pass over the steps
-// alone (about a third of the scan's time). Blocks of four units go one to an SM; a split takes two
-// tiles more, to fill and to drain.
-inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t G, int lanes) {
+// alone, which takes `maps` of the time of the pass itself and, to be launched, that of two tiles. A
+// split takes two tiles more, to fill and to drain. Blocks have `per_block` units, an SM has four:
+// with one, two and three of them a tile takes 0.58, 0.64 and 0.84 of its time with four (measured).
+inline int splits_for(int64_t B, int64_t L, int64_t H, int64_t G, int lanes, int per_block,
+                      double maps) {
   constexpr int64_t kSMs = 152, kUnits = 4;
-  const int64_t cw = 64 / lanes, units = (H / G + cw - 1) / cw;
-  const int64_t blocks = B * G * ((units + kUnits - 1) / kUnits), tiles = (L + kT - 1) / kT;
+  constexpr double kTime[kUnits + 1] = {0.0, 0.58, 0.64, 0.84, 1.0};
+  const int64_t cw = 64 / lanes, units = (H / G + cw - 1) / cw, tiles = (L + kT - 1) / kT;
+  const int64_t blocks = B * G * ((units + per_block - 1) / per_block);
   int best = 1;
   double least = 0.0;
   for (int s = 1; s <= std::min<int64_t>(64, tiles); ++s) {
-    const double cost = double((blocks * s + kSMs - 1) / kSMs) * ((tiles + s - 1) / s + 2) *
-                        (s == 1 ? 1.0 : 1.35);
+    const int64_t all = (blocks * s + kSMs - 1) / kSMs * per_block;  // units that an SM goes through
+    const double cost = (double(all / kUnits) + kTime[all % kUnits]) * ((tiles + s - 1) / s + 2) *
+                            (s == 1 ? 1.0 : 1.0 + maps) + (s == 1 ? 0.0 : 2.0);
     if (s == 1 || cost < least) best = s, least = cost;
   }
   return best;
 }
 
 template <typename T, typename ARGS>
-inputs<T> make_inputs(const ARGS& a, int lanes) {
+inputs<T> make_inputs(const ARGS& a, int want) {
   inputs<T> q{};
   q.B = a.B, q.L = a.L, q.H = (int)a.H, q.N = (int)a.N, q.G = (int)a.G;
   q.Hg = q.H / q.G;
@@ -322,7 +326,6 @@ inputs<T> make_inputs(const ARGS& a, int lanes) {
   q.x = in(a.x), q.dt = in(a.dt), q.z = in(a.z), q.Bm = in(a.Bm), q.Cm = in(a.Cm);
   q.A = a.A, q.D = a.D, q.bias = a.dt_bias, q.h0 = a.h0, q.reset = a.reset;
   q.tiles = (int)((a.L + kT - 1) / kT);
-  const int want = splits_for(a.B, a.L, a.H, a.G, lanes);
   q.per_split = (q.tiles + want - 1) / want;
   q.splits = (q.tiles + q.per_split - 1) / q.per_split;  // each has at least one tile
   return q;

@@ -607,7 +607,7 @@ back_plan plan(int64_t B, int64_t L, int64_t H, int64_t N, int64_t G) {
   const int64_t ln = back_lanes(N), cw = 64 / ln, units = (H / G + cw - 1) / cw;
   p.blocks = (units + kUnits - 1) / kUnits;
   p.NP = kHalves * kStates * ln;
-  const int64_t want = splits_for(B, L, H, G, (int)ln), tiles = (L + kT - 1) / kT;
+  const int64_t want = splits_for(B, L, H, G, (int)ln, kUnits, 0.25), tiles = (L + kT - 1) / kT;
   const int64_t per = (tiles + want - 1) / want;
   p.splits = (tiles + per - 1) / per;
   p.bc = G * p.blocks * B * L * 2 * p.NP;
@@ -646,7 +646,7 @@ cudaError_t run_back(back_params<T> q, const back_plan& p, cudaStream_t s) {
 template <typename T>
 cudaError_t back_of(const ssm_scan_backward_args& a, cudaStream_t s) {
   back_params<T> q{};
-  q.in = make_inputs<T>(a, back_lanes(a.N));
+  q.in = make_inputs<T>(a, (int)plan(a.B, a.L, a.H, a.N, a.G).splits);
   q.dy = view<const T>{static_cast<const T*>(a.dy.data), a.dy.stride_b, a.dy.stride_t};
   q.dx = out_view<T>(a.dx), q.ddt = out_view<T>(a.ddt), q.dz = out_view<T>(a.dz);
   q.dBm = out_view<T>(a.dBm), q.dCm = out_view<T>(a.dCm);
