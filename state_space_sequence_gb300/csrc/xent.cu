@@ -13,7 +13,8 @@
 // the six products of parts whose orders of magnitude add up to no less than 2^-16, the small ones
 // first. Products of parts are exact and accumulated in float32, as those of 16-bit inputs; but the
 // tensor core cuts off where it adds, a step of 16 of the sum at a time, and what that leaves out adds
-// up (5e-6 of dh at V = 4099), so for float32 every 64 steps the accumulator is added to a second one.
+// up (5e-6 of dh at V = 4099), so for float32 every 64 steps the accumulator is added to a second one,
+// and for few rows, whose time is W's memory, every 16.
 //
 // 8192 x 50257 x 2048 bfloat16, tensor products at the rate of the power limit: z with the loss 949 us
 // (1.78 PFLOP/s), d 1100, dh 1114, dW 1152 (1.46). 16 rows of it: 37 us, W read at 5.6 TB/s.
@@ -52,7 +53,6 @@ constexpr size_t kSmem = 1024 + kBarOff + 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kThreads = 256;
 constexpr int kGroup = 16;  // rows of tiles that go through the columns together
-constexpr int kChunk = 16;  // float32: stages between additions to the second accumulator
 static_assert(kSmem <= 232448, "shared memory");
 
 enum Mode { kLoss, kGrad, kRows, kColumns };
@@ -66,6 +66,7 @@ struct gemm_args {
   int bn;              // columns of a tile, at most kBN (kLoss, kGrad)
   int splits, k_split; // kRows: parts of the sum, each of k_split, that go to float32 sums of their own
   int products;        // 1, or 6 for float32
+  int chunk;           // KEEPS: stages between additions to the second accumulator
   int a_rows;          // of A's box: all kBM, or those of the only tile (not kColumns)
   int a_along, b_along;  // rows along the sum have their 64s as a dimension of the map
   int b_row;           // where the piece begins among W's rows
@@ -112,13 +113,12 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&b)[3]) {
 // T: the operands' type (bfloat16 also for float32's parts); O: the inputs' own, float for parts, in
 // three of which kGrad then stores d. Warp 0 loads, warp 1 issues the products, warp 2 has the tensor
 // memory, warps 4-7 read the accumulators; two accumulators take turns.
-template <Mode MODE, typename T, typename O>
+template <Mode MODE, typename T, typename O, bool KEEPS>
 __global__ void __launch_bounds__(kThreads, 1)
 xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
       const __grid_constant__ CUtensorMap tmC, const gemm_args g) {
   constexpr bool kAmn = MODE == kColumns, kBmn = MODE == kRows || MODE == kColumns;
-  // float32: accumulator 0 works, 1 keeps; otherwise they take turns
-  constexpr bool kKeeps = sizeof(O) == 4;
+  // KEEPS: accumulator 0 works, 1 keeps; otherwise they take turns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -206,11 +206,11 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
     for (int64_t t = blockIdx.x; t < work && ok; t += gridDim.x) {
       const int steps = stages(t) * g.products;
       for (int k = 0; k < steps && ok;) {
-        const uint32_t acc = kKeeps ? 0 : local & 1, turns = kKeeps ? 1 : 2;
+        const uint32_t acc = KEEPS ? 0 : local & 1, turns = KEEPS ? 1 : 2;
         if (local >= turns && !(ok = tc::mbar_wait(&acc_empty[acc], (local / turns - 1) & 1))) break;
         tc::fence_after_sync();
         const uint32_t d = tmem + acc * kBN;
-        const int stop = kKeeps ? min(steps, k + kChunk) : steps;
+        const int stop = KEEPS ? min(steps, k + g.chunk) : steps;
         for (int first = k; k < stop; ++k, ++it) {
           const int s = it % kStages;
           if (!(ok = tc::mbar_wait(&full[s], (it / kStages) & 1))) break;
@@ -260,13 +260,13 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
       const int64_t in_tile = target - g.v0 - n0;
       const int64_t at = counts && in_tile < bn ? in_tile : -1;
       const uint32_t lanes = uint32_t(q * 32) << 16;
-      // float32: all but the last chunk to the second accumulator
-      const int chunks = kKeeps ? (stages(t) * g.products + kChunk - 1) / kChunk : 1;
-      if constexpr (kKeeps) {
+      // all but the last chunk to the second accumulator
+      const int chunks = KEEPS ? (stages(t) * g.products + g.chunk - 1) / g.chunk : 1;
+      if constexpr (KEEPS) {
         for (int c = 0; c + 1 < chunks && ok; ++c, ++local) {
           if (!(ok = warp_wait(&acc_full[0], local & 1))) break;
           tc::fence_after_sync();
-          for (int i = 0; i < kBN; i += 16) {
+          for (int i = 0; i < bn; i += 16) {
             uint32_t v[16], w[16];
             tc::tmem_ld16_issue(tmem + lanes + i, v);
             if (c) tc::tmem_ld16_issue(tmem + lanes + kBN + i, w);
@@ -286,11 +286,11 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         }
         if (!ok) break;
       }
-      const uint32_t acc = kKeeps ? 0 : local & 1;
+      const uint32_t acc = KEEPS ? 0 : local & 1;
       const uint32_t tcol = tmem + acc * kBN + lanes;
       auto load = [&](int c, float (&v)[32]) {
         tc::tmem_ld32(tcol + c, v);
-        if constexpr (kKeeps) {
+        if constexpr (KEEPS) {
           if (chunks > 1) {
             float w[32];
             tc::tmem_ld32(tcol + kBN + c, w);
@@ -299,7 +299,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
           }
         }
       };
-      if (!(ok = warp_wait(&acc_full[acc], kKeeps ? local & 1 : (local >> 1) & 1))) break;
+      if (!(ok = warp_wait(&acc_full[acc], KEEPS ? local & 1 : (local >> 1) & 1))) break;
       ++local;
       tc::fence_after_sync();
       if constexpr (MODE == kLoss) {
@@ -462,10 +462,11 @@ finish_loss(const float2* stats, const float* hit, const int64_t* target, float*
   __syncthreads();
   if (warp || m >= M) return;
   for (int u = 1; u < WARPS; ++u) add(part[u][lane]);
-  const float total = top + logf(sum);
+  const float rest = logf(sum), total = top + rest;
   const int64_t t = target[m];
   lse[m] = total;
-  loss[m] = t >= 0 && t < V ? total - hit[m] : 0.0f;
+  // not total - hit: the loss of a sure row is small beside both
+  loss[m] = t >= 0 && t < V ? (top - hit[m]) + rest : 0.0f;
 }
 
 // The sums over the pieces, and over the parts of each, in the inputs' type.
@@ -599,7 +600,7 @@ struct operand {
   bool blocks() const { return cols % 64 == 0 || ours; }
 };
 
-template <Mode MODE, typename T, typename O>
+template <Mode MODE, typename T, typename O, bool KEEPS = sizeof(O) == 4>
 cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_args g,
                     cudaStream_t s) {
   constexpr auto kType = glr::is_half<T> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -620,11 +621,12 @@ cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_a
   else if (!make_map(&mc, c->p, MODE == kRows ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kType, c->parts,
                      c->rows, c->cols, c->pitch, 32))
     return cudaErrorInvalidValue;
+  g.chunk = sizeof(O) == 4 ? 16 : 4;
   g.status = device_status_word();
-  const cudaError_t e = max_smem_once<xgemm<MODE, T, O>>(kSmem);
+  const cudaError_t e = max_smem_once<xgemm<MODE, T, O, KEEPS>>(kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + g.bn - 1) / g.bn) * g.splits;
-  xgemm<MODE, T, O><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, kSmem, s>>>(
+  xgemm<MODE, T, O, KEEPS><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, kSmem, s>>>(
       ma, mb, mc, g);
   return cudaGetLastError();
 }
@@ -721,6 +723,17 @@ back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
   return p;
 }
 
+// The logits, for the loss or for d. Few rows wait for W's memory anyway: theirs are added up as
+// float32's are, every 4 stages, so that 16-bit inputs' z has 4e-7 of itself left out instead of 3e-6 (at
+// 1690 terms). Both directions by one rule: d of a sure row is a small difference of z and lse.
+template <Mode MODE, typename T, typename S>
+cudaError_t logits(const operand& h, const operand& w, const operand* d, const gemm_args& g,
+                   cudaStream_t s) {
+  if constexpr (sizeof(S) == 2)
+    if (g.M <= kBM) return product<MODE, T, S, true>(h, w, d, g, s);
+  return product<MODE, T, S>(h, w, d, g, s);
+}
+
 template <typename T, typename S>
 cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -737,7 +750,7 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = rows_of<T, S>(a.type, a.W, ws + staged(a.type, a.M, a.D), a.V, a.D, &w, s);
   if (e != cudaSuccess) return e;
-  if ((e = product<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
+  if ((e = logits<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((a.M + 31) / 32);
   if (blocks < 152)
     finish_loss<32><<<blocks, 1024, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V);
@@ -772,7 +785,7 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
     g.products = sizeof(S) == 4 ? 6 : 1;
     g.b_row = g.v0 = (int)v0;
     g.target = a.target, g.lse = a.lse, g.dloss = a.dloss, g.scale = scale;
-    if ((e = product<kGrad, T, S>(h, w, &d, g, s)) != cudaSuccess) return e;
+    if ((e = logits<kGrad, T, S>(h, w, &d, g, s)) != cudaSuccess) return e;
     if (a.dh.data) {
       gemm_args r{};
       r.M = (int)a.M, r.N = (int)a.D, r.K = (int)cols, r.products = g.products, r.b_row = (int)v0;
