@@ -63,38 +63,42 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
 // For 16-bit activations the decay comes from the special-function unit, whose results lie 1.9e-8 of
 // themselves low on average next to 1 (measured; as cutting off would make them): over a memory of a
 // thousand steps that adds up, so the exponent gets kNudge, which is still no step where s is 0.
-// For float32 the decay less 1 comes first and v + (decay - 1) v keeps its digits, so that a memory of
-// thousands of steps does not add up the rounding of its decay: below 1/4 as z P(z), a least-maximum
-// fit of (2^z - 1) / z (1.4e-8), above from the unit, where the subtraction loses less than two bits.
+// For float32 a decay next to 1 goes by the decay less 1: v + (a - 1) v keeps its digits, so that a memory
+// of thousands of steps does not add up the rounding of its decay. Below |z| = 1/4 that is z P(z), a
+// least-maximum fit of (2^z - 1) / z (2.0e-8); from there on v is multiplied by 2^z itself, which has its
+// digits however small it is (a - 1 would round it to a multiple of 2^-24). The choice is made on z + v
+// 2^-126, which is z for all but enormous states: those, and infinite ones, of which v + (a - 1) v would
+// make a NaN, are multiplied.
 constexpr float kNudge = 2.7e-8f;
 template <bool PRECISE>
 struct decay {
-  float2 a;  // the decay, or (PRECISE) the decay less 1
+  float2 z, a, less;  // (PRECISE: the exponents,) the decay (and the decay less 1)
   __device__ __forceinline__ decay(float2 rate, float2 s) {
     if constexpr (PRECISE) {
-      const float2 z = mul2(rate, s);
+      z = mul2(rate, s);
       float2 p = two(0.0013333556708f);
       p = fma2(p, z, two(0.0096301622689f));
       p = fma2(p, z, two(0.0555041655898f));
       p = fma2(p, z, two(0.2402263134718f));
       p = fma2(p, z, two(0.6931471824646f));
-      p = mul2(p, z);
-      const float2 e = add2(make_float2(ex2(z.x), ex2(z.y)), two(-1.0f));
-      a = make_float2(fabsf(z.x) < 0.25f ? p.x : e.x, fabsf(z.y) < 0.25f ? p.y : e.y);
+      less = mul2(p, z);
+      a = make_float2(ex2(z.x), ex2(z.y));
     } else {
-      const float2 z = fma2(rate, s, two(kNudge));
+      z = fma2(rate, s, two(kNudge));
       a = make_float2(ex2(z.x), ex2(z.y));
     }
   }
   __device__ __forceinline__ float2 of(float2 v) const {
-    if constexpr (PRECISE)
-      return fma2(a, v, v);
-    else
+    if constexpr (PRECISE) {
+      const float2 near = fma2(less, v, v), far = mul2(a, v), t = fma2(v, two(0x1p-126f), z);
+      return make_float2(fabsf(t.x) < 0.25f ? near.x : far.x, fabsf(t.y) < 0.25f ? near.y : far.y);
+    } else {
       return mul2(a, v);
+    }
   }
   __device__ __forceinline__ float2 of_plus(float2 v, float2 b, float2 x) const {  // and b x
     if constexpr (PRECISE)
-      return fma2(b, x, fma2(a, v, v));
+      return fma2(b, x, of(v));
     else
       return fma2(a, v, mul2(b, x));
   }
