@@ -250,7 +250,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         if (row < g.M) {
           target = g.target[row];
           if constexpr (MODE == kGrad) {
-            lse = g.lse[row] * kLog2e;
+            lse = g.lse[row];
             weight = g.dloss[row] * scale;
           }
         }
@@ -347,10 +347,16 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
           }
+          // z - lse first, which is exact next to the top: lse log2(e) has a rounding that grows with lse
+          // and would be the whole row's
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float p = ex2(fmaf(v[i], kLog2e, -lse)) - (at == c * 64 + i ? 1.0f : 0.0f);
-            v[i] = counts ? p * weight : 0.0f;
+          for (int i = 0; i < 64; i += 2) {
+            const float2 t = glr::mul2(
+                glr::add2(make_float2(v[i], v[i + 1]), glr::two(-lse)), glr::two(kLog2e));
+            const float p0 = ex2(t.x) - (at == c * 64 + i ? 1.0f : 0.0f);
+            const float p1 = ex2(t.y) - (at == c * 64 + i + 1 ? 1.0f : 0.0f);
+            v[i] = counts ? p0 * weight : 0.0f;
+            v[i + 1] = counts ? p1 * weight : 0.0f;
           }
 #pragma unroll
           for (int part = 0; part < kParts; ++part, ++boxed) {
