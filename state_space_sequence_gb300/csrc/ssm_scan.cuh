@@ -108,6 +108,14 @@ __device__ __forceinline__ void get_channels(float (&v)[kChannels], const float*
   v[0] = t.x, v[1] = t.y;
 }
 
+// 2^z v + e, over a split. Over many steps 2^z may underflow or overflow where no step's does: an infinite v
+// then still passes, and zero stays zero.
+__device__ __forceinline__ float pass(float z, float v, float e) {
+  const float a = ex2(z);
+  const bool all = (a == 0.0f && fabsf(v) == INFINITY && z > -INFINITY) || (a == INFINITY && v == 0.0f);
+  return all ? v + e : fmaf(a, v, e);
+}
+
 // A split of a sequence takes the state that enters it to P h + e: e is its end from zero, and P =
 // exp(A sum of its steps). What enters a split, from what enters the sequence (`h`): forwards through
 // the splits before it, backwards (the gradients) through those behind it, the same for every split in
@@ -133,7 +141,8 @@ __device__ __forceinline__ void enter(float2 (&h)[kChannels][kPairs], const inpu
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         const float2 z = mul2(rate[i][p], two(s));
-        h[i][p] = s != s ? e[i][p] : fma2(make_float2(ex2(z.x), ex2(z.y)), h[i][p], e[i][p]);
+        h[i][p] = s != s ? e[i][p]
+                         : make_float2(pass(z.x, h[i][p].x, e[i][p].x), pass(z.y, h[i][p].y, e[i][p].y));
       }
     }
   }

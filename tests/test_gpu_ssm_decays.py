@@ -92,9 +92,10 @@ def test_a_cut_sequence_decays_as_a_whole_one(H):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("L", [1, 5, 40])
+@pytest.mark.parametrize("L", [1, 5, 40, 700])
 def test_an_infinite_state_stays_infinite(L, dtype):
-    """As exp(s A) times infinity is, whether the decay is 1, next to it or far from it."""
+    """As exp(s A) times infinity is, whether the decay is 1, next to it or far from it, and in a cut
+    sequence, over whose parts the decays underflow."""
     steps = torch.tensor([0.0, 1e-4, 0.01, 0.2, 1.0, 1.5])
     H, N = len(steps), 4
     A = torch.tensor([-1.0, -2.0, -16.0, -0.5]).repeat(H, 1).cuda()
@@ -115,3 +116,19 @@ def test_an_infinite_state_stays_infinite(L, dtype):
     assert torch.equal(g.dh0, first)
     y = ssm.ssm_step(x[:, 0], dt[:, 0], A, B[:, 0], C[:, 0], h, softplus=False)
     assert torch.equal(h, first) and (y == float("inf")).all()
+
+
+def test_a_cut_sequence_that_grows_from_nothing():
+    """Steps below zero (without softplus) let a state grow; over a part of a cut sequence its factor
+    overflows, but what is zero stays zero, and what begins behind it is what it is."""
+    L, H, N = 700, 6, 4
+    A = -torch.ones(H, N, device="cuda")
+    dt = torch.full((1, L, H), -8.0, device="cuda")
+    x, maps = torch.zeros(1, L, H, device="cuda"), torch.ones(1, L, N, device="cuda")
+    x[:, -5] = 1.0
+    assert ssm.ssm_scan_workspace_size(1, L, H, N) > 0
+    _, last, st = ssm.ssm_scan(x, dt, A, maps, maps, softplus=False, save_states=True)
+    assert (np.abs(host(last) / (-8 * np.exp(32.0)) - 1) <= 1e-5).all() and not st[:, :-1].any()
+    g = ssm.ssm_scan_backward(x, dt, A, maps, maps, torch.zeros_like(x), st, softplus=False,
+                              h0=torch.zeros(1, H, N, device="cuda"))
+    assert not g.dh0.any() and not g.dx.any()
