@@ -38,9 +38,9 @@ constexpr int kT = SSM_STATE_STEPS;  // steps of a tile
 constexpr int kStates = 4, kChannels = 2, kPairs = kStates / 2;  // of a lane
 constexpr int kHalves = 2;  // warps that share a unit's states
 
-// log1p(e) for e in [0, 1]: e P(e), P of degree 8 by a least-maximum fit of the relative error
-// (3e-8; 1.7e-7 with its roundings). The logarithm of the rounded 1 + e would lose 6e-5 of a step of
-// 0.001, and this needs neither a logarithm nor a reciprocal.
+// log1p(e) for e in [0, 1]: e P(e), P of degree 8 by a fit of the relative error (at most 6.4e-8, 6e-8 low
+// where e is small, for P(0) = 1 - 2^-24; 1.7e-7 with its roundings). The logarithm of the rounded 1 + e
+// would lose 6e-5 of a step of 0.001, and this needs neither a logarithm nor a reciprocal.
 __device__ __forceinline__ float2 log1p2(float2 e) {
   float2 q = two(0.0052326940931379795f);
   q = fma2(q, e, two(-0.029505237936973572f));
