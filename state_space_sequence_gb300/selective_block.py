@@ -152,6 +152,36 @@ def step(par: Params, y, n, state: State, reset=None):
     return glr.glr_join(y, o @ par.Wo, None, par.w, par.alpha, par.v, act="none")
 
 
+def stack(blocks, embed, first, tok, reset=None):
+    """Tokens [B, L] looked up in embed [V, H] and normed (weights first [H]), then through the blocks:
+    (n, each block's Saved)."""
+    y = embed[tok].to(blocks[0].Wxz.dtype)
+    n = glr.glr_join(_rows(y), None, None, None, None, first)[1].view_as(y)
+    saved = []
+    for b in blocks:
+        y, n, _, s = forward(b, y, n, reset=reset)
+        saved.append(s)
+    return n, saved
+
+
+def gradients(blocks, embed, first, tok, target, reset=None):
+    """(losses [B L], each block's Params of gradients, embed's) of the mean loss over the tokens that have a
+    target. The rows of embed [V, H] (float32) are looked up and are the vocabulary's: both count."""
+    n, saved = stack(blocks, embed, first, tok, reset)
+    rows, table = _rows(n), embed.to(n.dtype)
+    losses, lse = xent.xent_loss(rows, table, target)
+    weight = (1.0 / (target >= 0).sum()).expand(losses.shape).contiguous()
+    dn, dtable = xent.xent_loss_backward(rows, table, target, lse, weight)
+    dn, dy, grads = dn.view_as(n), torch.zeros_like(n), []
+    for b, s in zip(blocks[::-1], saved[::-1]):
+        dy, dn, g = backward(b, s, dy, dn)
+        grads.insert(0, g)
+    dx = glr.glr_join_backward(None, _rows(dn), _rows(saved[0].y), None, None, None, None, first)[0]
+    dx = dx.float() + _rows(dy)  # the stack's first y is read by the norm and by the first block
+    # a token's rows are added up in a fixed order
+    return losses, grads, dtable.float().index_put_((tok.reshape(-1),), dx, accumulate=True)
+
+
 def main(steps: int = 241) -> None:
     torch.manual_seed(0)
     B, L, H, V, lr = 16, 192, 128, 32, 3e-3
@@ -186,35 +216,19 @@ def main(steps: int = 241) -> None:
             want[:, t] = keep
         return tok, reset, want.reshape(-1)
 
-    def run(tok, reset):
-        y = embed[tok].to(dtype)
-        n = glr.glr_join(_rows(y), None, None, None, None, first)[1].view_as(y)
-        saved = []
-        for b in blocks:
-            y, n, _, s = forward(b, y, n, reset=reset)
-            saved.append(s)
-        return n, saved
-
     for k in range(steps):
         tok, reset, want = batch()
-        n, saved = run(tok, reset)
-        table = embed.to(dtype)
-        losses, lse = xent.xent_loss(_rows(n), table, want)
-        count = (want >= 0).sum()
+        losses, grads, de = gradients(blocks, embed, first, tok, want, reset)
         if k % 60 == 0:
-            print(f"step {k:3d}  loss {(losses.sum() / count).item():.4f}")
-        dn, de = xent.xent_loss_backward(_rows(n), table, want, lse,
-                                         (1.0 / count).expand(losses.shape).contiguous())
-        dn, dy = dn.view_as(n), torch.zeros_like(n)
+            print(f"step {k:3d}  loss {(losses.sum() / (want >= 0).sum()).item():.4f}")
         for j in (1, 0):
-            dy, dn, grads = backward(blocks[j], saved[j], dy, dn)
-            adam(k, weights[j], moments[j], grads)
+            adam(k, weights[j], moments[j], grads[j])
             blocks[j] = Params(*(w.to(t.dtype) for w, t in zip(weights[j], blocks[j])))
         adam(k, weights[2], moments[2], [de])
 
     # the same rows token by token: a state a block, begun anew where a document begins
     tok, reset, _ = batch()
-    n, _ = run(tok, reset)
+    n = stack(blocks, embed, first, tok, reset)[0]
     states = [start(b, B) for b in blocks]
     worst = 0.0
     for t in range(L):
