@@ -98,6 +98,36 @@ def step(par: Params, y, n, h, reset=None):
     return glr.glr_join(y, o, n @ par.Wg, par.w, par.alpha, par.v)
 
 
+def stack(blocks, embed, first, tok, reset=None, ckpt: bool = True):
+    """Tokens [B, L] looked up in embed [V, H] and normed (weights first [H]), then through the blocks:
+    (n, each block's Saved)."""
+    y = embed[tok].to(blocks[0].Wxri.dtype)
+    n = glr.glr_join(_rows(y), None, None, None, None, first)[1].view_as(y)
+    saved = []
+    for b in blocks:
+        y, n, _, s = forward(b, y, n, reset=reset, ckpt=ckpt)
+        saved.append(s)
+    return n, saved
+
+
+def gradients(blocks, embed, first, tok, target, reset=None, ckpt: bool = True):
+    """(losses [B L], each block's Params of gradients, embed's) of the mean loss over all tokens. The rows of
+    embed [V, H] (float32) are looked up and are the vocabulary's: both count."""
+    n, saved = stack(blocks, embed, first, tok, reset, ckpt)
+    rows = _rows(n).float()
+    losses, lse = xent.xent_loss(rows, embed, target)
+    dn, de = xent.xent_loss_backward(rows, embed, target, lse,
+                                     torch.full_like(losses, 1.0 / len(losses)))
+    dn, dy, grads = dn.view_as(n).to(n.dtype), torch.zeros_like(n), []
+    for b, s in zip(blocks[::-1], saved[::-1]):
+        dy, dn, g = backward(b, s, dy, dn)
+        grads.insert(0, g)
+    dx = glr.glr_join_backward(None, _rows(dn), _rows(saved[0].y), None, None, None, None, first)[0]
+    dx = dx.float() + _rows(dy)  # the stack's first y is read by the norm and by the first block
+    # a token's rows are added up in a fixed order
+    return losses, grads, de.index_put_((tok.reshape(-1),), dx, accumulate=True)
+
+
 def main(steps: int = 241) -> None:
     torch.manual_seed(0)
     B, L, H, V, lr = 16, 192, 128, 32, 3e-3
@@ -131,34 +161,19 @@ def main(steps: int = 241) -> None:
             want[:, t] = keep
         return tok, reset, want
 
-    def run(tok, reset, ckpt=True):
-        y = embed[tok].to(dtype)
-        n = glr.glr_join(_rows(y), None, None, None, None, first)[1].view_as(y)
-        saved = []
-        for b in blocks:
-            y, n, _, s = forward(b, y, n, reset=reset, ckpt=ckpt)
-            saved.append(s)
-        return n, saved
-
     for k in range(steps):
         tok, reset, want = batch()
-        n, saved = run(tok, reset)
-        rows, target = _rows(n).float(), want.reshape(-1)
-        losses, lse = xent.xent_loss(rows, embed, target)
+        losses, grads, de = gradients(blocks, embed, first, tok, want.reshape(-1), reset)
         if k % 60 == 0:
             print(f"step {k:3d}  loss {-torch.log(torch.exp(-losses) + 1e-9).mean().item():.4f}")
-        dn, de = xent.xent_loss_backward(rows, embed, target, lse,
-                                         torch.full_like(losses, 1.0 / (B * L)))
-        dn, dy = dn.view_as(n).to(dtype), torch.zeros_like(n)
         for j in (1, 0):
-            dy, dn, grads = backward(blocks[j], saved[j], dy, dn)
-            adam(k, weights[j], moments[j], grads)
+            adam(k, weights[j], moments[j], grads[j])
             blocks[j] = Params(*(w.to(t.dtype) for w, t in zip(weights[j], blocks[j])))
         adam(k, weights[2], moments[2], [de])
 
     # the same rows token by token: a state a block, reset where a document begins
     tok, reset, _ = batch()
-    n, _ = run(tok, reset)
+    n = stack(blocks, embed, first, tok, reset)[0]
     h = [torch.zeros(B, H, device="cuda") for _ in blocks]
     worst = 0.0
     for t in range(L):

@@ -4,8 +4,9 @@ torch's autograd in float64, as the blocks' own tests: within 1e-4 of each gradi
 import pytest
 import torch
 
-from state_space_sequence_gb300 import dlr, selective_block as sb
+from state_space_sequence_gb300 import dlr, gated_block as gb, selective_block as sb
 
+from test_gpu_gated_block import plain as plain_gated
 from test_gpu_selective_block import plain
 
 pytestmark = pytest.mark.gpu
@@ -51,5 +52,28 @@ def test_the_selective_stack():
     for a, q in zip((*grads[0], *grads[1], de), want):
         assert (a.double() - q).norm() <= 1e-4 * q.norm()
     again = sb.gradients(pars, embed, first, tok, target, reset)
+    assert torch.equal(again[2], de) and torch.equal(again[0], losses)
+    assert dlr.device_status() == 0
+
+
+def test_the_gated_stack():
+    torch.backends.cuda.matmul.allow_tf32 = False
+    B, L, H, V = 2, 24, 16, 20
+    tok, target, reset, embed = batch(B, L, V)
+    target = target.clamp(min=0)
+    first = (1 + 0.1 * torch.randn(H, generator=torch.Generator().manual_seed(2))).cuda()
+    pars = [gb.make_params(H, torch.float32, seed=s) for s in (6, 7)]
+    losses, grads, de = gb.gradients(pars, embed, first, tok, target, reset, ckpt=False)
+    leaves = [t.double().requires_grad_(True) for t in (*pars[0], *pars[1], embed)]
+    y = leaves[12][tok]
+    n = first.double() * norm(y)
+    for k in range(2):
+        y, n = plain_gated(leaves[6 * k:6 * k + 6], y, n, reset)
+    ref = mean_loss(n, leaves[12], target)
+    want = torch.autograd.grad(ref, leaves)
+    assert abs(losses.double().mean() - ref) <= 1e-4 * ref
+    for a, q in zip((*grads[0], *grads[1], de), want):
+        assert (a.double() - q).norm() <= 1e-4 * q.norm()
+    again = gb.gradients(pars, embed, first, tok, target, reset, ckpt=False)
     assert torch.equal(again[2], de) and torch.equal(again[0], losses)
     assert dlr.device_status() == 0
