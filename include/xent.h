@@ -17,6 +17,16 @@ extern "C" {
 #endif
 
 /*
+ * Rows h and W are read as they lie where they have 16 bits, begin on multiples of 16 bytes and are a
+ * multiple of 8 elements and no less than D apart (M = 1 or V = 1: at any distance); other rows, and
+ * float32's, are laid out anew in the workspace. The size queries count on that for both. Their answer
+ * is without it for the rows that a flag added to the (16-bit) type names, and is then what calls with
+ * such rows need.
+ */
+#define XENT_H_IN_PLACE 16 /* of xent_loss; xent_loss_backward always lays h out */
+#define XENT_W_IN_PLACE 32
+
+/*
  * xent_loss -- for rows h [M, D] and the vocabulary's rows W [V, D] (contiguous channels, rows
  * `stride_t` elements apart, stride_b unused, one type), with z = h W^T:
  *   lse[m] = log sum_v exp z[m, v],   loss[m] = lse[m] - z[m, target[m]]

@@ -669,6 +669,12 @@ bool direct(int64_t type, const glr_view& v, int64_t rows, int64_t cols) {
          (rows <= 1 || (v.stride_t % 8 == 0 && v.stride_t >= cols));
 }
 
+bool direct_h(const xent_loss_args& a) { return direct(a.type, a.h, a.M, a.D); }
+template <typename ARGS>
+bool direct_w(const ARGS& a) {
+  return direct(a.type, a.W, a.V, a.D);
+}
+
 // Bytes of staged rows.
 int64_t staged(int64_t type, int64_t rows, int64_t cols) {
   return up((type == GLR_F32 ? 3 : 1) * rows * up(cols, 64) * 2, 256);
@@ -705,7 +711,7 @@ struct back_plan {
   bool sums() const { return pieces > 1 || splits > 1; }  // dh goes through float32 sums
 };
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
-back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
+back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D, bool w_there) {
   const int64_t parts = type == GLR_F32 ? 3 : 1;
   back_plan p;
   // A piece's d takes at most kPieceBytes. Of the piece counts from the least to twice as many, the
@@ -724,7 +730,7 @@ back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D) {
   p.d = 0;
   p.h = p.d + up(parts * M * std::min(p.piece, up(V, 64)) * 2, 256);
   p.w = p.h + staged(type, M, D);
-  p.acc = p.w + staged(type, V, D);
+  p.acc = p.w + (w_there ? 0 : staged(type, V, D));
   p.scale = p.acc + (p.sums() ? up(p.splits * M * up(D, 4) * 4, 256) : 0);
   p.bytes = p.scale + 256;
   return p;
@@ -755,7 +761,8 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   operand h, w;
   cudaError_t e = rows_of<T, S>(a.type, a.h, ws, a.M, a.D, &h, s);
   if (e != cudaSuccess) return e;
-  e = rows_of<T, S>(a.type, a.W, ws + staged(a.type, a.M, a.D), a.V, a.D, &w, s);
+  if (!direct_h(a)) ws += staged(a.type, a.M, a.D);
+  e = rows_of<T, S>(a.type, a.W, ws, a.V, a.D, &w, s);
   if (e != cudaSuccess) return e;
   if ((e = logits<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((a.M + 31) / 32);
@@ -769,7 +776,7 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
 template <typename T, typename S>
 cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const back_plan p = plan(a.type, a.M, a.V, a.D);
+  const back_plan p = plan(a.type, a.M, a.V, a.D, direct_w(a));
   const uint64_t parts = sizeof(S) == 4 ? 3 : 1;
   float* scale = nullptr;
   cudaError_t e;
@@ -826,13 +833,22 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t loss_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D) {
+// h_there, w_there: the products read those rows as they lie.
+size_t loss_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D, bool h_there,
+                            bool w_there) {
   const int64_t bn = columns_of(M, V, 16), nt = (V + bn - 1) / bn;
-  return (size_t)(up(nt * M * 8, 256) + up(M * 4, 256) + staged(type, M, D) + staged(type, V, D));
+  return (size_t)(up(nt * M * 8, 256) + up(M * 4, 256) + (h_there ? 0 : staged(type, M, D)) +
+                  (w_there ? 0 : staged(type, V, D)));
+}
+size_t loss_workspace_bytes(const xent_loss_args& a) {
+  return loss_workspace_bytes(a.type, a.M, a.V, a.D, direct_h(a), direct_w(a));
 }
 
-size_t loss_backward_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D) {
-  return (size_t)plan(type, M, V, D).bytes;
+size_t loss_backward_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D, bool w_there) {
+  return (size_t)plan(type, M, V, D, w_there).bytes;
+}
+size_t loss_backward_workspace_bytes(const xent_loss_backward_args& a) {
+  return loss_backward_workspace_bytes(a.type, a.M, a.V, a.D, direct_w(a));
 }
 
 cudaError_t launch_loss(const xent_loss_args& a, cudaStream_t s) {

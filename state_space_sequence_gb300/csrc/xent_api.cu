@@ -9,8 +9,11 @@ namespace dlr {
 dlr_status status_from_cuda(cudaError_t e);
 
 namespace xent {
-size_t loss_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D);
-size_t loss_backward_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D);
+size_t loss_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D, bool h_there,
+                            bool w_there);
+size_t loss_workspace_bytes(const xent_loss_args& a);
+size_t loss_backward_workspace_bytes(int64_t type, int64_t M, int64_t V, int64_t D, bool w_there);
+size_t loss_backward_workspace_bytes(const xent_loss_backward_args& a);
 cudaError_t launch_loss(const xent_loss_args& a, cudaStream_t s);
 cudaError_t launch_loss_backward(const xent_loss_backward_args& a, cudaStream_t s);
 cudaError_t clear_gradient(const glr_out& dW, int64_t type, int64_t V, int64_t D, cudaStream_t s);
@@ -32,6 +35,14 @@ dlr_status sizes(int64_t type, int64_t M, int64_t V, int64_t D) {
   return DLR_OK;
 }
 
+// The flags of a size query's type, which is left without them; those of float32 are not flags.
+int64_t take_flags(int64_t& type) {
+  const int64_t all = XENT_H_IN_PLACE | XENT_W_IN_PLACE, flags = type & all;
+  if (type < 0 || (type & ~all) == GLR_F32) return 0;
+  type &= ~all;
+  return flags;
+}
+
 dlr_status bad_space(const void* ws, uint64_t bytes, size_t need) {
   return !ws || !aligned(ws, 256) || bytes < need ? DLR_ERR_WORKSPACE : DLR_OK;
 }
@@ -44,8 +55,10 @@ extern "C" {
 int xent_abi_version(void) { return 1; }
 
 size_t xent_loss_workspace_size(int64_t type, int64_t M, int64_t V, int64_t D) {
+  const int64_t there = take_flags(type);
   if (M < 1 || sizes(type, M, V, D) != DLR_OK) return 0;
-  return dlr::xent::loss_workspace_bytes(type, M, V, D);
+  return dlr::xent::loss_workspace_bytes(type, M, V, D, there & XENT_H_IN_PLACE,
+                                         there & XENT_W_IN_PLACE);
 }
 
 dlr_status xent_loss(const xent_loss_args* args, dlr_stream_t stream) {
@@ -56,7 +69,7 @@ dlr_status xent_loss(const xent_loss_args* args, dlr_stream_t stream) {
   if (bad_view(a.h, a.type, 1, a.M) || bad_view(a.W, a.type, 1, a.V) || bad_i64(a.target) ||
       bad_f32(a.loss) || bad_f32(a.lse))
     return DLR_ERR_INVALID_ARG;
-  const size_t need = dlr::xent::loss_workspace_bytes(a.type, a.M, a.V, a.D);
+  const size_t need = dlr::xent::loss_workspace_bytes(a);
   if ((st = bad_space(a.workspace, a.workspace_bytes, need)) != DLR_OK) return st;
   const Area in[] = {strided(a.h, a.type, 1, a.M, a.D), strided(a.W, a.type, 1, a.V, a.D),
                      flat(a.target, 8 * a.M)};
@@ -67,8 +80,9 @@ dlr_status xent_loss(const xent_loss_args* args, dlr_stream_t stream) {
 }
 
 size_t xent_loss_backward_workspace_size(int64_t type, int64_t M, int64_t V, int64_t D) {
+  const int64_t there = take_flags(type);
   if (M < 1 || sizes(type, M, V, D) != DLR_OK) return 0;
-  return dlr::xent::loss_backward_workspace_bytes(type, M, V, D);
+  return dlr::xent::loss_backward_workspace_bytes(type, M, V, D, there & XENT_W_IN_PLACE);
 }
 
 dlr_status xent_loss_backward(const xent_loss_backward_args* args, dlr_stream_t stream) {
@@ -87,7 +101,7 @@ dlr_status xent_loss_backward(const xent_loss_backward_args* args, dlr_stream_t 
   if (bad_view(a.h, a.type, 1, a.M) || bad_view(a.W, a.type, 1, a.V) || bad_i64(a.target) ||
       bad_f32(a.lse) || bad_f32(a.dloss) || (a.dh.data && bad_view(a.dh, a.type, 1, a.M)))
     return DLR_ERR_INVALID_ARG;
-  const size_t need = dlr::xent::loss_backward_workspace_bytes(a.type, a.M, a.V, a.D);
+  const size_t need = dlr::xent::loss_backward_workspace_bytes(a);
   if ((st = bad_space(a.workspace, a.workspace_bytes, need)) != DLR_OK) return st;
   const Area in[] = {strided(a.h, a.type, 1, a.M, a.D), strided(a.W, a.type, 1, a.V, a.D),
                      flat(a.target, 8 * a.M), flat(a.lse, 4 * a.M), flat(a.dloss, 4 * a.M)};

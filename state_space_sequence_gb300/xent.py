@@ -23,6 +23,7 @@ _lib = None
 # the argument structs of xent.h, every field 8 bytes wide
 _LOSS = struct.Struct("15q").pack
 _BACK = struct.Struct("21q").pack
+_IN_PLACE_H, _IN_PLACE_W = 16, 32  # XENT_H_IN_PLACE, XENT_W_IN_PLACE
 
 
 def _load():
@@ -50,14 +51,19 @@ def _back_space(kind: int, M: int, V: int, D: int) -> int:
     return int(_load().xent_loss_backward_workspace_size(kind, M, V, D))
 
 
-def xent_loss_workspace_size(dtype, M: int, V: int, D: int) -> int:
-    """Bytes of device workspace xent_loss needs (0: none, or sizes out of range)."""
-    return _loss_space(_act_kind(dtype), M, V, D)
+def xent_loss_workspace_size(dtype, M: int, V: int, D: int, h=None, W=None) -> int:
+    """Bytes of device workspace xent_loss needs (0: none, or sizes out of range), wherever its rows lie, or,
+    with ``h`` or ``W``, for those rows: 16-bit ones that begin on 16 bytes and are a multiple of 8
+    elements apart are read as they lie and need no room of their own."""
+    there = (_IN_PLACE_H if h is not None and _in_place(h) else 0) | \
+        (_IN_PLACE_W if W is not None and _in_place(W) else 0)
+    return _loss_space(_act_kind(dtype) + there, M, V, D)
 
 
-def xent_loss_backward_workspace_size(dtype, M: int, V: int, D: int) -> int:
-    """Bytes of device workspace xent_loss_backward needs (0: none, or sizes out of range)."""
-    return _back_space(_act_kind(dtype), M, V, D)
+def xent_loss_backward_workspace_size(dtype, M: int, V: int, D: int, W=None) -> int:
+    """The same for xent_loss_backward, which always lays ``h`` out anew."""
+    there = _IN_PLACE_W if W is not None and _in_place(W) else 0
+    return _back_space(_act_kind(dtype) + there, M, V, D)
 
 
 def _act_kind(dtype) -> int:
@@ -78,6 +84,14 @@ def _rows(h, W):
     return kind, M, V, D, dev, hv, wv
 
 
+def _in_place(t) -> bool:
+    """Whether rows are read as they lie."""
+    rows, D = t.shape
+    step = t.stride(0)
+    return t.dtype is not torch.float32 and t.data_ptr() % 16 == 0 and \
+        (rows <= 1 or (step % 8 == 0 and step >= D))
+
+
 def _target(t, M: int, dev: int) -> int:
     if t.dtype is not torch.int64 or t.get_device() != dev or not t.is_contiguous():
         raise TypeError(f"target: expected a contiguous int64 tensor on cuda:{dev}")
@@ -95,7 +109,8 @@ def xent_loss(h, W, target, workspace=None, stream=None):
     with _on(stream):
         loss = torch.empty((M,), dtype=torch.float32, device=h.device)
         lse = torch.empty((M,), dtype=torch.float32, device=h.device)
-        ws = _workspace(workspace, _loss_space(kind, M, V, D), h)
+        there = (_IN_PLACE_H if _in_place(h) else 0) + (_IN_PLACE_W if _in_place(W) else 0)
+        ws = _workspace(workspace, _loss_space(kind + there, M, V, D), h)
     args = _LOSS(kind, M, V, D, *hv, *wv, _target(target, M, dev), loss.data_ptr(),
                  lse.data_ptr(), ws.data_ptr(), ws.numel())
     _ok("xent_loss", lib.xent_loss(args, _stream(stream, dev)))
@@ -116,7 +131,7 @@ def xent_loss_backward(h, W, target, lse, dloss, wanted=(True, True), out=None, 
             dW = torch.empty((V, D), dtype=h.dtype, device=h.device) if wanted[1] else None
         else:
             dh, dW = out
-        ws = _workspace(workspace, _back_space(kind, M, V, D), h)
+        ws = _workspace(workspace, _back_space(kind + (_IN_PLACE_W if _in_place(W) else 0), M, V, D), h)
     dhv = _NONE3 if dh is None else _views2((dh,), h, h.dtype, dev, (M, D), ("dh",))
     dWv = _NONE3 if dW is None else _views2((dW,), h, h.dtype, dev, (V, D), ("dW",))
     args = _BACK(kind, M, V, D, *hv, *wv, _target(target, M, dev), _f32(lse, (M,), dev, "lse"),
