@@ -32,7 +32,11 @@ extern "C" {
  *   lse[m] = log sum_v exp z[m, v],   loss[m] = lse[m] - z[m, target[m]]
  * target: int64 [M]. A row whose target is outside 0 .. V-1 (-1, -100: the end of a sequence,
  * padding) has the loss 0, whatever h holds there. loss and lse are float32 [M]. Products are exact
- * and summed in float32 (float32 inputs: as three bfloat16 parts of each value, six products).
+ * and summed in float32 (float32 inputs: as three bfloat16 parts of each value, six products of the nine).
+ * The tensor core adds 16 of them at a time and cuts off where it adds, up to 2^-23 of the sum so far; so
+ * sums are formed in pieces that are added up with rounding: of 256 terms for up to 128 rows of 16 bits, of
+ * the whole sum for more rows as far as D = 4096 and of 2048 terms beyond, of 1024 for float32. A row's loss
+ * may therefore differ in its last digits with the number of rows in the call.
  * M >= 0; V, D >= 1; M, V < 2^31 - 256; D <= 2^20. workspace: xent_loss_workspace_size(type, M, V,
  * D) bytes, 256-byte aligned.
  */
@@ -56,7 +60,9 @@ dlr_status xent_loss(const xent_loss_args* args, dlr_stream_t stream);
  *   dh = d W [M, D],   dW = d^T h [V, D]
  * dh or dW may have data NULL: not wanted. Rows without a target add nothing to dW, whatever h
  * holds there, and their dh is 0 where W is finite. The logits are formed again, piece by piece of
- * the vocabulary; d is rounded to the inputs' type before its two products (float16: scaled by a
+ * the vocabulary (of columns whose d takes 256 MB, or of 256 columns where they take more); d is rounded
+ * to the inputs' type before its two products (float32: kept in three parts), whose sums are formed whole
+ * as far as 16384 terms and in pieces of 4096 beyond (float32: of 1024; float16: d is scaled by a
  * power of two first, so that the largest |dloss| is below 2^15). workspace:
  * xent_loss_backward_workspace_size(type, M, V, D) bytes, 256-byte aligned. M = 0 writes dW = 0.
  */

@@ -13,8 +13,8 @@
 // the six products of parts whose orders of magnitude add up to no less than 2^-16, the small ones
 // first. Products of parts are exact and accumulated in float32, as those of 16-bit inputs; but the
 // tensor core cuts off where it adds, a step of 16 of the sum at a time, and what that leaves out adds
-// up (5e-6 of dh at V = 4099), so for float32 every 64 steps the accumulator is added to a second one,
-// and for few rows, whose time is W's memory, every 16.
+// up (5e-6 of dh at V = 4099), so float32's, few rows' and long sums are added to a second accumulator
+// piece by piece (`product`).
 //
 // 8192 x 50257 x 2048 bfloat16, tensor products at the rate of the power limit: z with the loss 950 us
 // (1.78 PFLOP/s), d 1100, dh 1114, dW 1152 (1.46). 16 rows of it: 39 us, W read at 5.3 TB/s.
@@ -607,8 +607,8 @@ struct operand {
   bool blocks() const { return cols % 64 == 0 || ours; }
 };
 
-template <Mode MODE, typename T, typename O, bool KEEPS = sizeof(O) == 4>
-cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_args g,
+template <Mode MODE, typename T, typename O, bool KEEPS>
+cudaError_t launch(const operand& a, const operand& b, const operand* c, gemm_args g,
                     cudaStream_t s) {
   constexpr auto kType = glr::is_half<T> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -628,7 +628,6 @@ cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_a
   else if (!make_map(&mc, c->p, MODE == kRows ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kType, c->parts,
                      c->rows, c->cols, c->pitch, 32))
     return cudaErrorInvalidValue;
-  g.chunk = sizeof(O) == 4 ? 16 : 4;
   g.status = device_status_word();
   const cudaError_t e = max_smem_once<xgemm<MODE, T, O, KEEPS>>(kSmem);
   if (e != cudaSuccess) return e;
@@ -636,6 +635,29 @@ cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_a
   xgemm<MODE, T, O, KEEPS><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, kSmem, s>>>(
       ma, mb, mc, g);
   return cudaGetLastError();
+}
+
+// A product, and how often its sums go to the second accumulator. The tensor core cuts off some 2^-24 of what
+// it has at each step of 16 terms, always towards zero, so that a sum of one sign loses 6e-8 of itself a step
+// (measured: 3e-3 of 524288 terms, 5e-4 of 131072). float32's add up every 16 stages of 64 terms. In 16 bits:
+// logits of few rows, which wait for W's memory anyway, every 4 (4e-7 of z left out instead of 3e-6 at 1690
+// terms); logits of more than 64 stages every 32, dh and dW of more than 256 every 64, so that no more than
+// 2e-5 is lost; shorter sums stay in one accumulator, and the two take turns. Both directions' logits go by
+// one rule: d of a sure row is a small difference of z and lse.
+template <Mode MODE, typename T, typename S>
+cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_args g,
+                    cudaStream_t s) {
+  if constexpr (sizeof(S) == 4) {
+    g.chunk = 16;
+    return launch<MODE, T, S, true>(a, b, c, g, s);
+  } else {
+    constexpr bool kLogits = MODE == kLoss || MODE == kGrad;
+    const int stages = ((MODE == kRows ? g.k_split : g.K) + kBK - 1) / kBK;
+    g.chunk = !kLogits ? 64 : g.M <= kBM ? 4 : 32;
+    if ((kLogits && g.M <= kBM) || stages > (kLogits ? 64 : 256))
+      return launch<MODE, T, S, true>(a, b, c, g, s);
+    return launch<MODE, T, S, false>(a, b, c, g, s);
+  }
 }
 
 constexpr int64_t kSMs = 152;
@@ -736,17 +758,6 @@ back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D, bool w_there) {
   return p;
 }
 
-// The logits, for the loss or for d. Few rows wait for W's memory anyway: theirs are added up as
-// float32's are, every 4 stages, so that 16-bit inputs' z has 4e-7 of itself left out instead of 3e-6 (at
-// 1690 terms). Both directions by one rule: d of a sure row is a small difference of z and lse.
-template <Mode MODE, typename T, typename S>
-cudaError_t logits(const operand& h, const operand& w, const operand* d, const gemm_args& g,
-                   cudaStream_t s) {
-  if constexpr (sizeof(S) == 2)
-    if (g.M <= kBM) return product<MODE, T, S, true>(h, w, d, g, s);
-  return product<MODE, T, S>(h, w, d, g, s);
-}
-
 template <typename T, typename S>
 cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -764,7 +775,7 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   if (!direct_h(a)) ws += staged(a.type, a.M, a.D);
   e = rows_of<T, S>(a.type, a.W, ws, a.V, a.D, &w, s);
   if (e != cudaSuccess) return e;
-  if ((e = logits<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
+  if ((e = product<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((a.M + 31) / 32);
   if (blocks < 152)
     finish_loss<32><<<blocks, 1024, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V);
@@ -799,7 +810,7 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
     g.products = sizeof(S) == 4 ? 6 : 1;
     g.b_row = g.v0 = (int)v0;
     g.target = a.target, g.lse = a.lse, g.dloss = a.dloss, g.scale = scale;
-    if ((e = logits<kGrad, T, S>(h, w, &d, g, s)) != cudaSuccess) return e;
+    if ((e = product<kGrad, T, S>(h, w, &d, g, s)) != cudaSuccess) return e;
     if (a.dh.data) {
       gemm_args r{};
       r.M = (int)a.M, r.N = (int)a.D, r.K = (int)cols, r.products = g.products, r.b_row = (int)v0;

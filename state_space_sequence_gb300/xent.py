@@ -55,15 +55,18 @@ def xent_loss_workspace_size(dtype, M: int, V: int, D: int, h=None, W=None) -> i
     """Bytes of device workspace xent_loss needs (0: none, or sizes out of range), wherever its rows lie, or,
     with ``h`` or ``W``, for those rows: 16-bit ones that begin on 16 bytes and are a multiple of 8
     elements apart are read as they lie and need no room of their own."""
-    there = (_IN_PLACE_H if h is not None and _in_place(h) else 0) | \
-        (_IN_PLACE_W if W is not None and _in_place(W) else 0)
-    return _loss_space(_act_kind(dtype) + there, M, V, D)
+    return _loss_space(_act_kind(dtype) + _given(dtype, h, D) * _IN_PLACE_H +
+                       _given(dtype, W, D) * _IN_PLACE_W, M, V, D)
 
 
 def xent_loss_backward_workspace_size(dtype, M: int, V: int, D: int, W=None) -> int:
     """The same for xent_loss_backward, which always lays ``h`` out anew."""
-    there = _IN_PLACE_W if W is not None and _in_place(W) else 0
-    return _back_space(_act_kind(dtype) + there, M, V, D)
+    return _back_space(_act_kind(dtype) + _given(dtype, W, D) * _IN_PLACE_W, M, V, D)
+
+
+def _given(dtype, t, D: int) -> bool:
+    return t is not None and t.dtype == dtype and \
+        _in_place(_act_kind(dtype), (t.data_ptr(), 0, t.stride(0)), t.shape[0], D)
 
 
 def _act_kind(dtype) -> int:
@@ -84,12 +87,9 @@ def _rows(h, W):
     return kind, M, V, D, dev, hv, wv
 
 
-def _in_place(t) -> bool:
-    """Whether rows are read as they lie."""
-    rows, D = t.shape
-    step = t.stride(0)
-    return t.dtype is not torch.float32 and t.data_ptr() % 16 == 0 and \
-        (rows <= 1 or (step % 8 == 0 and step >= D))
+def _in_place(kind: int, view, rows: int, D: int) -> bool:
+    """Whether rows at a view (pointer, 0, stride) are read as they lie."""
+    return kind != 0 and view[0] % 16 == 0 and (rows <= 1 or (view[2] % 8 == 0 and view[2] >= D))
 
 
 def _target(t, M: int, dev: int) -> int:
@@ -109,8 +109,8 @@ def xent_loss(h, W, target, workspace=None, stream=None):
     with _on(stream):
         loss = torch.empty((M,), dtype=torch.float32, device=h.device)
         lse = torch.empty((M,), dtype=torch.float32, device=h.device)
-        there = (_IN_PLACE_H if _in_place(h) else 0) + (_IN_PLACE_W if _in_place(W) else 0)
-        ws = _workspace(workspace, _loss_space(kind + there, M, V, D), h)
+        space = kind + _in_place(kind, hv, M, D) * _IN_PLACE_H + _in_place(kind, wv, V, D) * _IN_PLACE_W
+        ws = _workspace(workspace, _loss_space(space, M, V, D), h)
     args = _LOSS(kind, M, V, D, *hv, *wv, _target(target, M, dev), loss.data_ptr(),
                  lse.data_ptr(), ws.data_ptr(), ws.numel())
     _ok("xent_loss", lib.xent_loss(args, _stream(stream, dev)))
@@ -131,7 +131,8 @@ def xent_loss_backward(h, W, target, lse, dloss, wanted=(True, True), out=None, 
             dW = torch.empty((V, D), dtype=h.dtype, device=h.device) if wanted[1] else None
         else:
             dh, dW = out
-        ws = _workspace(workspace, _back_space(kind + (_IN_PLACE_W if _in_place(W) else 0), M, V, D), h)
+        space = kind + _in_place(kind, wv, V, D) * _IN_PLACE_W
+        ws = _workspace(workspace, _back_space(space, M, V, D), h)
     dhv = _NONE3 if dh is None else _views2((dh,), h, h.dtype, dev, (M, D), ("dh",))
     dWv = _NONE3 if dW is None else _views2((dW,), h, h.dtype, dev, (V, D), ("dW",))
     args = _BACK(kind, M, V, D, *hv, *wv, _target(target, M, dev), _f32(lse, (M,), dev, "lse"),

@@ -1,0 +1,69 @@
+"""Long sums of 16-bit inputs with terms of one sign, where what the tensor core cuts off at each step of 16
+terms adds up. A step cuts off at most 2^-23 of what has been added so far; a piece of a sum, T terms long, so
+T / 16 * 2^-23 at most, and the pieces are added up with 2^-24 each."""
+import numpy as np
+import pytest
+import torch
+
+from state_space_sequence_gb300 import dlr, xent
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+def cut_off(terms, piece):
+    return piece / 16 * 2.0 ** -23 + -(-terms // piece) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M", [16384, 16385, 131072, 600001])
+def test_weights_gradients_over_many_rows(M, dtype):
+    """W = 0: every probability is 1 / 256, and d, with dloss a power of two, of eight digits: dW is the sum
+    of h's rows."""
+    V, D = 256, 24
+    g = torch.Generator(device="cuda").manual_seed(M)
+    h = (0.5 + 0.5 * torch.rand(M, D, generator=g, device="cuda")).to(dtype)
+    W = torch.zeros(V, D, dtype=dtype, device="cuda")
+    target = torch.full((M,), 7, device="cuda")
+    dloss = torch.full((M,), 2.0 ** -11, device="cuda")
+    _, lse = xent.xent_loss(h, W, target)
+    _, dW = xent.xent_loss_backward(h, W, target, lse, dloss, wanted=(False, True))
+    d = torch.full((V, 1), 2.0 ** -19, dtype=torch.float64, device="cuda")
+    d[7] = -255 * 2.0 ** -19
+    ref = d * h.double().sum(0)
+    tol = HALF[dtype] + (cut_off(M, 4096) if M > 16384 else cut_off(M, M))
+    least = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    off = (dW.double() - ref).abs() / (tol * ref.abs() + least)
+    assert off.max() <= 1, off.max()
+    assert dlr.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,D", [(200, 4096), (200, 4104), (200, 65536), (20, 65536)])
+def test_logits_of_wide_rows(M, D, dtype):
+    """Logits of about 20, all terms positive: losses and the logarithms of sums are as far off as they are,
+    the gradients' exponentials likewise."""
+    V = 70
+    g = torch.Generator(device="cuda").manual_seed(D + M)
+    h = (0.5 + 0.5 * torch.rand(M, D, generator=g, device="cuda")).to(dtype)
+    W = ((0.5 + 0.5 * torch.rand(V, D, generator=g, device="cuda")) * (36.0 / D)).to(dtype)
+    target = torch.randint(0, V, (M,), generator=g, device="cuda")
+    dloss = torch.full((M,), 1.0, device="cuda")
+    loss, lse = xent.xent_loss(h, W, target)
+    z = h.double() @ W.double().t()
+    ref = torch.logsumexp(z, 1)
+    # few rows' sums by pieces of 256, wide ones' of 2048
+    piece = 256 if M <= 128 else 2048 if D > 4096 else D
+    off = cut_off(D, piece) * float(z.abs().max()) + 8 * 2.0 ** -24 * float(ref.max())
+    assert float((lse.double() - ref).abs().max()) <= off
+    hit = z.gather(1, target[:, None])[:, 0]
+    assert float((loss.double() - (ref - hit)).abs().max()) <= 2 * off
+    dh, _ = xent.xent_loss_backward(h, W, target, lse, dloss, wanted=(True, False))
+    d = torch.exp(z - ref[:, None])
+    d[torch.arange(M), target] -= 1.0
+    size = d.abs() @ W.double()
+    tol = 2 * HALF[dtype] + 2 * off
+    least = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    assert ((dh.double() - d @ W.double()).abs() <= tol * size + least).all()
+    assert dlr.device_status() == 0
