@@ -11,8 +11,13 @@
  * elements must be distinct, and no output may share an element with an input or another output
  * unless a call says so. Arguments come in one struct per call (all fields 8 bytes wide; unused
  * pointers NULL). Parameters, scan states and their gradients are float32 and contiguous. All
- * arithmetic is float32; results are rounded once, to nearest even, where they are stored in 16
- * bits. Sums over rows and channels run in a fixed order: results repeat bit for bit.
+ * arithmetic is float32 (what ssm_scan_backward sums over channels for dBm and dCm is cut to 21 bits
+ * first); results are rounded once, to nearest even, where they are stored in 16 bits. Sums over rows
+ * and channels run in a fixed order: results repeat bit for bit.
+ *
+ * A decay exp(s A) of float32 activations keeps its digits at every size: next to 1 it is 1 - a that is
+ * rounded. That of 16-bit activations is one number, off by up to 1.5 * 2^-24 of itself: over a memory
+ * of 8192 steps a state, and h_last with it, may be 7.4e-4 off.
  *
  * reset: bytes [B, L], contiguous, NULL for none; a step that it marks begins a new sequence:
  * nothing before it, not even an infinity or a NaN, reaches it.

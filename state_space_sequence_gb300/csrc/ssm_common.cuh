@@ -8,7 +8,7 @@
 // lane reads per step one 16-byte word of Bm and of Cm, which the lanes beside it share, and 8-byte
 // words of its channels' steps and inputs. One warp with sixteen numbers a lane reads a third less but
 // waits for itself: forwards B4 L4096 H4096 N16 bfloat16 takes 406 to 422 us with it and 423 with two,
-// B1 L65536 H256 N64 float32 979 beside 909, and the gradients have no registers for it.
+// B1 L65536 H256 N64 float32 8% longer, and the gradients have no registers for it.
 //
 // Helpers stage what a unit reads, a tile of kT steps ahead, and finish what it leaves, a tile behind,
 // so that neither the latency of memory nor the elementwise work stands in the recurrence's way.

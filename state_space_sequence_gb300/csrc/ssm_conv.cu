@@ -6,7 +6,7 @@
 // the K - 1 inputs before them in registers, and reads the next few meanwhile: each input is read once
 // by its run and, of the K - 1 before the run, once more (from the cache: the run before is the
 // neighbouring warp's). B4 L16384 H2048 K4 bfloat16 with marks: 92 us forwards (5.8 TB/s), 186 backwards
-// (4.3 TB/s; fixed latencies at 12 warps an SM), one token of 256 x 4096 5 us.
+// and 6 for its sums (4.2 TB/s; fixed latencies at 12 warps an SM), one token of 256 x 4096 5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -516,7 +516,7 @@ void go(conv_params<T> q, cudaStream_t s) {
 }
 
 // Pieces of 8 bytes; single channels where rows do not stand on multiples of them. Backwards four
-// channels in 16 bits leave an SM 12 warps and take 190 us at B4 L16384 H2048, two leave it 16 and take
+// channels in 16 bits leave an SM 12 warps and take 186 us at B4 L16384 H2048, two leave it 16 and take
 // 215: what a step costs besides its channels is then shared by fewer.
 template <typename T, int KM, bool EXACT, Dir DIR>
 void by_piece(const conv_params<T>& q, cudaStream_t s) {

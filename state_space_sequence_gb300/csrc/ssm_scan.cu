@@ -7,9 +7,10 @@
 // multiply-add for the state, one for the output and one product for the input. Everything else is
 // done once a tile of 16 steps, by pieces of rows: the step's softplus, the skip and the gate.
 //
-// B4 L4096 H4096 N16 bfloat16 with its states kept takes 421 us (1.9 TB/s): issue slots (60%, 71% where an
-// SM has four units) and shared memory (66%, 79%) bound it; its exponentials alone are 115 us.
-// Float32 at B1 L65536 H256 N64 takes 500 us, and 402 for the maps of its 19 splits: its decays bound it.
+// B4 L4096 H4096 N16 bfloat16 with its states kept takes 424 us (1.9 TB/s): issue slots (52%, 61% where an
+// SM has four units; the others have three) and shared memory (67%) bound it; its exponentials alone are
+// 115 us. Float32 at B1 L65536 H256 N64 takes 531 us, and 431 for the maps of its 19 splits: its decays
+// bound it (the multiply-adds' pipe is busy for 64 and 68% of the time).
 #include <type_traits>
 
 #include "ssm_scan.cuh"

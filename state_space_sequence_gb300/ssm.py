@@ -230,7 +230,8 @@ def ssm_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True
     groups of H / G channels; z [batch, L, H] (None: no gate); h0 [batch, H, N] the state before the
     first step (None: zero); reset [batch, L] (bool or uint8, None: none) marks steps that begin a new
     sequence. Returns (y, h_last [batch, H, N]) and, with ``save_states``, the float32 states
-    [batch, ceil(L / 16), H, N] that ssm_scan_backward takes."""
+    [batch, ceil(L / 16), H, N] that ssm_scan_backward takes. The decays of 16-bit activations are off by up
+    to 1.5 * 2^-24: states with a memory of thousands of steps by 1e-7 for each of them."""
     lib, kind = _load(), _act_type(x)
     if x.dim() != 3:
         raise ValueError("x: expected [batch, L, H]")
