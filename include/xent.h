@@ -62,8 +62,8 @@ dlr_status xent_loss(const xent_loss_args* args, dlr_stream_t stream);
  * holds there, and their dh is 0 where W is finite. The logits are formed again, piece by piece of
  * the vocabulary (of columns whose d takes 256 MB, or of 256 columns where they take more); d is rounded
  * to the inputs' type before its two products (float32: kept in three parts), whose sums are formed whole
- * as far as 16384 terms and in pieces of 4096 beyond (float32: of 1024; float16: d is scaled by a
- * power of two first, so that the largest |dloss| is below 2^15). workspace:
+ * as far as 16384 terms and in pieces of 4096 beyond (float32: of 1024). In 16 bits d is first
+ * divided by the largest |dloss| (float16: over 2^14): under a mean the weights are then 1. workspace:
  * xent_loss_backward_workspace_size(type, M, V, D) bytes, 256-byte aligned. M = 0 writes dW = 0.
  */
 typedef struct {
