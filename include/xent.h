@@ -35,7 +35,7 @@ extern "C" {
  * and summed in float32 (float32 inputs: as three bfloat16 parts of each value, six products of the nine).
  * The tensor core adds 16 of them at a time and cuts off where it adds, up to 2^-23 of the sum so far; so
  * sums are formed in pieces that are added up with rounding: of 256 terms for up to 128 rows of 16 bits, of
- * the whole sum for more rows as far as D = 4096 and of 2048 terms beyond, of 1024 for float32. A row's loss
+ * the whole sum for more rows as far as D = 4096 and of 2048 terms beyond, of 512 for float32. A row's loss
  * may therefore differ in its last digits with the number of rows in the call.
  * M >= 0; V, D >= 1; M, V < 2^31 - 256; D <= 2^20. workspace: xent_loss_workspace_size(type, M, V,
  * D) bytes, 256-byte aligned.
@@ -62,7 +62,7 @@ dlr_status xent_loss(const xent_loss_args* args, dlr_stream_t stream);
  * holds there, and their dh is 0 where W is finite. The logits are formed again, piece by piece of
  * the vocabulary (of columns whose d takes 256 MB, or of 256 columns where they take more); d is rounded
  * to the inputs' type before its two products (float32: kept in three parts), whose sums are formed whole
- * as far as 16384 terms and in pieces of 4096 beyond (float32: of 1024). In 16 bits d is first
+ * as far as 16384 terms and in pieces of 4096 beyond (float32: of 512). In 16 bits d is first
  * divided by the largest |dloss| (float16: over 2^14): under a mean the weights are then 1. workspace:
  * xent_loss_backward_workspace_size(type, M, V, D) bytes, 256-byte aligned. M = 0 writes dW = 0.
  */

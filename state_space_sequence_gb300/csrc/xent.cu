@@ -67,7 +67,8 @@ struct gemm_args {
   int bn;              // columns of a tile, at most kBN (kLoss, kGrad)
   int splits, k_split; // kRows: parts of the sum, each of k_split, that go to float32 sums of their own
   int products;        // 1, or 6 for float32
-  int chunk;           // KEEPS: stages between additions to the second accumulator
+  int chunk;           // KEEPS: stages between additions to the second accumulator (kSmall times as many of the
+                       // small products' stages)
   int a_rows;          // of A's box: all kBM, or those of the only tile (not kColumns)
   int a_along, b_along;  // rows along the sum have their 64s as a dimension of the map
   int b_row;           // where the piece begins among W's rows
@@ -87,6 +88,21 @@ struct gemm_args {
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, tc::mbar_wait_sleep(bar, parity)) != 0;
+}
+
+constexpr int kSmall = 8;
+// KEEPS: where the piece of a sum ends that begins at stage k of `steps`, and how many pieces there are. Of
+// float32's six products all but the last are 2^-8 of the sum or less, and so is what they lose.
+__device__ __forceinline__ int small_stages(const gemm_args& g, int steps) {
+  return g.products == 1 ? 0 : steps / g.products * (g.products - 1);
+}
+__device__ __forceinline__ int piece_end(const gemm_args& g, int k, int steps) {
+  const int small = small_stages(g, steps);
+  return k < small ? min(small, k + kSmall * g.chunk) : min(steps, k + g.chunk);
+}
+__device__ __forceinline__ int pieces(const gemm_args& g, int steps) {
+  const int small = small_stages(g, steps), most = kSmall * g.chunk;
+  return (small + most - 1) / most + (steps - small + g.chunk - 1) / g.chunk;
 }
 
 // Tile t in an order that keeps kGroup rows of tiles on one column's operand at a time.
@@ -211,7 +227,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
         if (local >= turns && !(ok = tc::mbar_wait(&acc_empty[acc], (local / turns - 1) & 1))) break;
         tc::fence_after_sync();
         const uint32_t d = tmem + acc * kBN;
-        const int stop = KEEPS ? min(steps, k + g.chunk) : steps;
+        const int stop = KEEPS ? piece_end(g, k, steps) : steps;
         for (int first = k; k < stop; ++k, ++it) {
           const int s = it % kStages;
           if (!(ok = tc::mbar_wait(&full[s], (it / kStages) & 1))) break;
@@ -262,7 +278,7 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
       const int64_t at = counts && in_tile < bn ? in_tile : -1;
       const uint32_t lanes = uint32_t(q * 32) << 16;
       // all but the last chunk to the second accumulator
-      const int chunks = KEEPS ? (stages(t) * g.products + g.chunk - 1) / g.chunk : 1;
+      const int chunks = KEEPS ? pieces(g, stages(t) * g.products) : 1;
       if constexpr (KEEPS) {
         for (int c = 0; c + 1 < chunks && ok; ++c, ++local) {
           if (!(ok = warp_wait(&acc_full[0], local & 1))) break;
@@ -642,7 +658,7 @@ cudaError_t launch(const operand& a, const operand& b, const operand* c, gemm_ar
 
 // A product, and how often its sums go to the second accumulator. The tensor core cuts off some 2^-24 of what
 // it has at each step of 16 terms, always towards zero, so that a sum of one sign loses 6e-8 of itself a step
-// (measured: 3e-3 of 524288 terms, 5e-4 of 131072). float32's add up every 16 stages of 64 terms. In 16 bits:
+// (measured: 3e-3 of 524288 terms, 5e-4 of 131072). float32's add up every 8 stages of 64 terms. In 16 bits:
 // logits of few rows, which wait for W's memory anyway, every 4 (4e-7 of z left out instead of 3e-6 at 1690
 // terms); logits of more than 64 stages every 32, dh and dW of more than 256 every 64, so that no more than
 // 2e-5 is lost; shorter sums stay in one accumulator, and the two take turns. Both directions' logits go by
@@ -651,7 +667,7 @@ template <Mode MODE, typename T, typename S>
 cudaError_t product(const operand& a, const operand& b, const operand* c, gemm_args g,
                     cudaStream_t s) {
   if constexpr (sizeof(S) == 4) {
-    g.chunk = 16;
+    g.chunk = 8;
     return launch<MODE, T, S, true>(a, b, c, g, s);
   } else {
     constexpr bool kLogits = MODE == kLoss || MODE == kGrad;
