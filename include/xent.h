@@ -35,8 +35,9 @@ extern "C" {
  * and summed in float32 (float32 inputs: as three bfloat16 parts of each value, six products of the nine).
  * The tensor core adds 16 of them at a time and cuts off where it adds, up to 2^-23 of the sum so far; so
  * sums are formed in pieces that are added up with rounding: of 256 terms for up to 128 rows of 16 bits, of
- * the whole sum for more rows as far as D = 4096 and of 2048 terms beyond, of 512 for float32. A row's loss
- * may therefore differ in its last digits with the number of rows in the call.
+ * the whole sum for more rows as far as D = 4096 and of 2048 terms beyond, of 512 for float32. The
+ * target's logit of more than 128 rows of 16 bits is formed once more by itself, rounded to nearest. A
+ * row's loss may therefore differ in its last digits with the number of rows in the call.
  * M >= 0; V, D >= 1; M, V < 2^31 - 256; D <= 2^20. workspace: xent_loss_workspace_size(type, M, V,
  * D) bytes, 256-byte aligned.
  */

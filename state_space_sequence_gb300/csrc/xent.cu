@@ -2,7 +2,8 @@
 // logits live in tensor memory, and its gradients.
 //
 // Four products on the 5th-generation tensor cores, one kernel (xgemm) with four ends:
-//   the loss        z = h W^T, a tile's rows reduced to their maximum and sum of exponentials;
+//   the loss        z = h W^T, a tile's rows reduced to their maximum and sum of exponentials (the target's
+//                   logit apart);
 //   the gradients   z again for a piece of the vocabulary, d = (softmax - onehot) dloss rounded to
 //                   the inputs' type and stored; then dh += d W and dW = d^T h over that piece.
 // The gradients form the logits a second time, a third of their work, for never holding more of d
@@ -22,6 +23,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dlr_common.cuh"
 #include "glr_common.cuh"
@@ -79,7 +81,7 @@ struct gemm_args {
   const float* dloss;
   const float* scale;  // of d in 16 bits and its inverse, or null
   float2* stats;       // kLoss: [column of tiles, M] maximum and sum
-  float* hit;          // kLoss: [M] the target's logit
+  float* hit;          // [M] the target's logit: kLoss writes it, kGrad takes it (null: its own)
   int keep;            // kRows: 1 store the sums (float32, at tmC), 2 add them to those there
   void* out;
   int64_t out_stride;
@@ -262,13 +264,14 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
       const int cols = min(bn, g.N - n0);
       // what a row brings, fetched before the accumulator is waited for
       int64_t target = -1;
-      float lse = 0.0f, weight = 0.0f;
+      float lse = 0.0f, weight = 0.0f, exact = 0.0f;
       if constexpr (MODE == kLoss || MODE == kGrad) {
         if (row < g.M) {
           target = g.target[row];
           if constexpr (MODE == kGrad) {
             lse = g.lse[row];
             weight = g.dloss[row] * scale;
+            if (g.hit) exact = g.hit[row];
           }
         }
       }
@@ -327,15 +330,17 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
           if (cols - c < 32)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = i < cols - c ? v[i] : -INFINITY;
-          if (at >= c && at < c + 32)
+          if (at >= c && at < c + 32)  // the target's stays by itself: a sure row's loss hangs on the others
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (at == c + i && DLR_IN(row, g.M)) g.hit[row] = v[i];
+              if (at == c + i) {
+                if (DLR_IN(row, g.M)) g.hit[row] = v[i];
+                v[i] = -INFINITY;
+              }
           float most = v[0];
 #pragma unroll
           for (int i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
           const float next = fmaxf(top, most), from = next == -INFINITY ? 0.0f : next;
-          // the largest counts as exactly 1, which a sure row's loss, log(1 + little), hangs on
           float part = 0.0f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) part += ex2((v[i] - from) * kLog2e);
@@ -359,6 +364,10 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = lo[i], v[32 + i] = hi[i];
           }
+          if (g.hit && at >> 6 == c)
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (at == c * 64 + i) v[i] = exact;
           if (c == n_slices - 1) {
             tc::fence_before_sync();
             __syncwarp();
@@ -464,13 +473,52 @@ xgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
   if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// lse and loss of 32 rows to a block from the tiles' maxima and sums; the block's WARPS warps share the
-// tiles of a row and meet in order (many of them where there are few rows).
-template <int WARPS>
+// The logit of one row and one of the vocabulary's, by a warp: 16 terms one after the other for 4096, rounded
+// to nearest.
+template <typename T>
+__device__ __forceinline__ float row_logit(const T* h, const T* w, int64_t D, int lane) {
+  float2 sum[4] = {};
+  for (int64_t d = lane * 8; d < D; d += 256) {
+    glr::words<T, 8> a, b;
+    if (d + 8 <= D) {
+      a.get(h + d);
+      b.get(w + d);
+    } else {
+      float u[8], v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        u[i] = d + i < D ? to_f(h[d + i]) : 0.0f;
+        v[i] = d + i < D ? to_f(w[d + i]) : 0.0f;
+      }
+      a.from(u);
+      b.from(v);
+    }
+    float x[8], y[8];
+    a.to(x);
+    b.to(y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sum[i] = glr::fma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(y[2 * i], y[2 * i + 1]), sum[i]);
+  }
+  const float2 s = glr::add2(glr::add2(sum[0], sum[1]), glr::add2(sum[2], sum[3]));
+  float z = s.x + s.y;
+#pragma unroll
+  for (int k = 16; k; k >>= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
+  return z;
+}
+
+// lse and loss of 32 rows to a block from the tiles' maxima and sums, which are those of the other logits
+// than the target's; the block's WARPS warps share the tiles of a row and meet in order (many of them where
+// there are few rows). EXACT: the targets' logits are formed here again: a sure row's is a long sum of one
+// sign, of which a single accumulator cuts off 3e-6, and its loss is small beside it. (8192 x 50257 x 2048:
+// losses 1.7e-6 -> 2.8e-7 off, 10 -> 21 of 960 us, in the gradients 9 more; with eight warps 29.)
+template <int WARPS, typename T, bool EXACT>
 __global__ void __launch_bounds__(32 * WARPS)
 finish_loss(const float2* stats, const float* hit, const int64_t* target, float* loss, float* lse,
-            int64_t M, int nt, int64_t V) {
+            int64_t M, int nt, int64_t V, const T* h, int64_t h_pitch, const T* W, int64_t w_pitch,
+            int64_t D) {
   __shared__ float2 part[WARPS][32];
+  __shared__ float exact[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t m = (int64_t)blockIdx.x * 32 + lane;
   float top = -INFINITY, sum = 0.0f;
@@ -479,6 +527,13 @@ finish_loss(const float2* stats, const float* hit, const int64_t* target, float*
     sum = sum * expf(top - from) + s.y * expf(s.x - from);
     top = next;
   };
+  if constexpr (EXACT)
+    for (int r = warp; r < 32; r += WARPS) {
+      const int64_t row = (int64_t)blockIdx.x * 32 + r, t = row < M ? target[row] : -1;
+      if (t < 0 || t >= V) continue;
+      const float z = row_logit(h + row * h_pitch, W + t * w_pitch, D, lane);
+      if (lane == 0) exact[r] = z;
+    }
   if (m < M)
 #pragma unroll 4
     for (int k = warp; k < nt; k += WARPS) add(stats[(int64_t)k * M + m]);
@@ -486,11 +541,17 @@ finish_loss(const float2* stats, const float* hit, const int64_t* target, float*
   __syncthreads();
   if (warp || m >= M) return;
   for (int u = 1; u < WARPS; ++u) add(part[u][lane]);
-  const float rest = logf(sum), total = top + rest;
+  const float rest = logf(sum), others = top + rest;
   const int64_t t = target[m];
-  lse[m] = total;
-  // not total - hit: the loss of a sure row is small beside both
-  loss[m] = t >= 0 && t < V ? (top - hit[m]) + rest : 0.0f;
+  if (t < 0 || t >= V) {
+    lse[m] = others;
+    loss[m] = 0.0f;
+    return;
+  }
+  // log(1 + e^x) for what the others are beyond the target: neither is a difference of large numbers
+  const float z = EXACT ? exact[lane] : hit[m], x = (top - z) + rest, little = log1pf(expf(-fabsf(x)));
+  loss[m] = fmaxf(x, 0.0f) + little;
+  lse[m] = z == -INFINITY && others == -INFINITY ? z : fmaxf(z, others) + little;
 }
 
 // The sums over the pieces, and over the parts of each, in the inputs' type.
@@ -518,9 +579,21 @@ finish_rows(const float* acc, int64_t pitch, int splits, O* out, int64_t stride,
 // counts. Under a mean all weights are then 1, and d of the many targets that are hardly expected, next to -1,
 // is exact; by dloss itself all of them had the same rounding, up to 2^-8 (dh 2.5e-3 off at 8192 x 50257 x
 // 2048, now 1.8e-3, of which the result's own rounding is 1.7e-3). float16 adds a factor 2^14 for its range.
+//
+// The first block does that. The others form the targets' logits of 32 rows each again, which kGrad then takes:
+// lse is that of these.
+template <typename T>
 __global__ void __launch_bounds__(1024)
-find_scale(const float* dloss, const int64_t* target, int64_t M, int64_t V, float most, float* scale) {
+before_back(const float* dloss, const int64_t* target, int64_t M, int64_t V, float most, float* scale,
+            const T* h, int64_t h_pitch, const T* W, int64_t w_pitch, int64_t D, float* hit) {
   __shared__ float part[32];
+  if (blockIdx.x) {
+    const int64_t row = (int64_t)(blockIdx.x - 1) * 32 + (threadIdx.x >> 5), t = row < M ? target[row] : -1;
+    if (t < 0 || t >= V) return;
+    const float z = row_logit(h + row * h_pitch, W + t * w_pitch, D, threadIdx.x & 31);
+    if ((threadIdx.x & 31) == 0) hit[row] = z;
+    return;
+  }
   float top = 0.0f;
   for (int64_t m = threadIdx.x; m < M; m += 1024)
     if (target[m] >= 0 && target[m] < V) top = fmaxf(top, fabsf(dloss[m]));
@@ -743,11 +816,14 @@ cudaError_t rows_of(int64_t type, const glr_view& v, void* to, int64_t rows, int
   return stage<T, S>(v, to, rows, cols, nullptr, 0, out, s);
 }
 
+// Whether the targets' logits are formed again: where all of a logit goes through one accumulator.
+bool exact_targets(int64_t type, int64_t M) { return type != GLR_F32 && M > kBM; }
+
 // How the gradients' vocabulary is cut, and where things lie in their workspace.
 struct back_plan {
   int64_t piece, pieces;         // columns of a piece
   int64_t splits;                // parts of its sum for dh
-  int64_t d, h, w, acc, scale;   // offsets
+  int64_t d, h, w, acc, scale, hit;  // offsets
   int64_t bytes;
   bool sums() const { return pieces > 1 || splits > 1; }  // dh goes through float32 sums
 };
@@ -773,7 +849,8 @@ back_plan plan(int64_t type, int64_t M, int64_t V, int64_t D, bool w_there) {
   p.w = p.h + staged(type, M, D);
   p.acc = p.w + (w_there ? 0 : staged(type, V, D));
   p.scale = p.acc + (p.sums() ? up(p.splits * M * up(D, 4) * 4, 256) : 0);
-  p.bytes = p.scale + 256;
+  p.hit = p.scale + 256;
+  p.bytes = p.hit + (exact_targets(type, M) ? up(M * 4, 256) : 0);
   return p;
 }
 
@@ -796,10 +873,23 @@ cudaError_t loss_of(const xent_loss_args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((e = product<kLoss, T, S>(h, w, nullptr, g, s)) != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((a.M + 31) / 32);
-  if (blocks < 152)
-    finish_loss<32><<<blocks, 1024, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V);
-  else
-    finish_loss<8><<<blocks, 256, 0, s>>>(g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V);
+  auto finish = [&](auto warps, auto exact) {
+    finish_loss<warps.value, T, exact.value><<<blocks, 32 * warps.value, 0, s>>>(
+        g.stats, g.hit, a.target, a.loss, a.lse, a.M, nt, a.V, static_cast<const T*>(h.p), (int64_t)h.pitch,
+        static_cast<const T*>(w.p), (int64_t)w.pitch, a.D);
+  };
+  auto by_rows = [&](auto exact) {
+    if (blocks < 152 || exact.value)
+      finish(std::integral_constant<int, 32>{}, exact);
+    else
+      finish(std::integral_constant<int, 8>{}, exact);
+  };
+  if constexpr (sizeof(S) == 2)
+    if (exact_targets(a.type, a.M)) {
+      by_rows(std::true_type{});
+      return cudaGetLastError();
+    }
+  by_rows(std::false_type{});
   return cudaGetLastError();
 }
 
@@ -808,18 +898,22 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const back_plan p = plan(a.type, a.M, a.V, a.D, direct_w(a));
   const uint64_t parts = sizeof(S) == 4 ? 3 : 1;
-  float* scale = nullptr;
   cudaError_t e;
-  if (sizeof(S) == 2) {
-    scale = reinterpret_cast<float*>(ws + p.scale);
-    find_scale<<<1, 1024, 0, s>>>(a.dloss, a.target, a.M, a.V, glr::is_half<S> ? 0x1p14f : 1.0f, scale);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   operand h, hz, w;
   // the rows of h that count, for dW; the logits take them too
   if ((e = stage<T, S>(a.h, ws + p.h, a.M, a.D, a.target, a.V, &hz, s)) != cudaSuccess) return e;
   h = hz;
   if ((e = rows_of<T, S>(a.type, a.W, ws + p.w, a.V, a.D, &w, s)) != cudaSuccess) return e;
+  float *scale = nullptr, *hit = nullptr;
+  if constexpr (sizeof(S) == 2) {
+    const bool exact = exact_targets(a.type, a.M);
+    scale = reinterpret_cast<float*>(ws + p.scale);
+    if (exact) hit = reinterpret_cast<float*>(ws + p.hit);
+    before_back<T><<<1 + (exact ? (unsigned)((a.M + 31) / 32) : 0), 1024, 0, s>>>(
+        a.dloss, a.target, a.M, a.V, glr::is_half<S> ? 0x1p14f : 1.0f, scale, static_cast<const T*>(hz.p),
+        (int64_t)hz.pitch, static_cast<const T*>(w.p), (int64_t)w.pitch, a.D, hit);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   for (int64_t k = 0; k < p.pieces; ++k) {
     const int64_t v0 = k * p.piece, cols = std::min(p.piece, a.V - v0);
     const operand d{ws + p.d, parts, (uint64_t)a.M, (uint64_t)cols, (uint64_t)up(cols, 64), true};
@@ -828,7 +922,7 @@ cudaError_t back_of(const xent_loss_backward_args& a, cudaStream_t s) {
     g.M = (int)a.M, g.N = (int)cols, g.K = (int)a.D, g.V = (int)a.V;
     g.products = sizeof(S) == 4 ? 6 : 1;
     g.b_row = g.v0 = (int)v0;
-    g.target = a.target, g.lse = a.lse, g.dloss = a.dloss, g.scale = scale;
+    g.target = a.target, g.lse = a.lse, g.dloss = a.dloss, g.scale = scale, g.hit = hit;
     if ((e = product<kGrad, T, S>(h, w, &d, g, s)) != cudaSuccess) return e;
     if (a.dh.data) {
       gemm_args r{};
