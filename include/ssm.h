@@ -15,9 +15,9 @@
  * first); results are rounded once, to nearest even, where they are stored in 16 bits. Sums over rows
  * and channels run in a fixed order: results repeat bit for bit.
  *
- * A decay exp(s A) of float32 activations keeps its digits at every size: next to 1 it is 1 - a that is
- * rounded. That of 16-bit activations is one number, off by up to 1.5 * 2^-24 of itself: over a memory
- * of 8192 steps a state, and h_last with it, may be 7.4e-4 off.
+ * A decay exp(s A) of float32 activations keeps its digits down to 2^-126 (below it is 0): next to 1 it
+ * is 1 - a that is rounded. That of 16-bit activations is one number, off by up to 1.5 * 2^-24 of
+ * itself: over a memory of 8192 steps a state, and h_last with it, may be 7.4e-4 off.
  *
  * reset: bytes [B, L], contiguous, NULL for none; a step that it marks begins a new sequence:
  * nothing before it, not even an infinity or a NaN, reaches it.

@@ -595,8 +595,11 @@ before_back(const float* dloss, const int64_t* target, int64_t M, int64_t V, flo
     return;
   }
   float top = 0.0f;
-  for (int64_t m = threadIdx.x; m < M; m += 1024)
-    if (target[m] >= 0 && target[m] < V) top = fmaxf(top, fabsf(dloss[m]));
+#pragma unroll 8
+  for (int64_t m = threadIdx.x; m < M; m += 1024) {
+    const float w = fabsf(dloss[m]);
+    top = fmaxf(top, target[m] >= 0 && target[m] < V ? w : 0.0f);
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
