@@ -111,9 +111,10 @@ __device__ __forceinline__ void get_channels(float (&v)[kChannels], const float*
 // 2^z v + e, over a split. Over many steps 2^z may underflow or overflow where no step's does: an infinite v
 // then still passes, and zero stays zero.
 __device__ __forceinline__ float pass(float z, float v, float e) {
-  const float a = ex2(z);
+  const float a = ex2(z), r = fmaf(a, v, e);
+  if (r == r) return r;
   const bool all = (a == 0.0f && fabsf(v) == INFINITY && z > -INFINITY) || (a == INFINITY && v == 0.0f);
-  return all ? v + e : fmaf(a, v, e);
+  return all ? v + e : r;
 }
 
 // A split of a sequence takes the state that enters it to P h + e: e is its end from zero, and P =
